@@ -25,7 +25,7 @@ BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libdiffattn_debug.so")
 SOURCES = ["api.cu", "fwd_bf16_sm103.cu", "fwd_f32.cu", "headnorm.cu", "splitkv.cu",
            "noalloc.cu", "bwd_bf16_sm103.cu", "fwd_d128_sm103.cu", "bwd_d128_sm103.cu",
-           "selftest.cu"]
+           "selftest.cu", "paged_api.cu", "paged_append.cu", "paged_fwd.cu", "paged_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -60,7 +60,7 @@ def _stale(lib: str = LIB) -> bool:
         return True
     t = os.path.getmtime(lib)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(HERE, "..", "include", "diffattn.h"))
+    deps += [os.path.join(HERE, "..", "include", f) for f in ("diffattn.h", "diffattn_paged.h")]
     return any(os.path.getmtime(p) > t for p in deps if os.path.exists(p))
 
 

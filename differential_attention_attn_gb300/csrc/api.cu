@@ -117,6 +117,12 @@ diffattn_status plan_kv(const diffattn_desc *desc, int64_t n_kv, int splits, int
 
 }  // namespace
 
+namespace diffattn {
+diffattn_status check_common_desc(const diffattn_desc *desc) { return check_desc(desc); }
+diffattn_status require_sm103() { return check_sm103(); }
+int device_sm_count() { return sm_count(); }
+}  // namespace diffattn
+
 extern "C" {
 
 namespace {
@@ -461,6 +467,7 @@ const char *diffattn_strerror(diffattn_status status) {
     case DIFFATTN_ERR_UNSUPPORTED: return "unsupported configuration";
     case DIFFATTN_ERR_CUDA: return "CUDA error";
     case DIFFATTN_ERR_TIMEOUT: return "kernel pipeline wait timed out";
+    case DIFFATTN_ERR_PAGE: return "page number or sequence length outside the paged cache";
     case DIFFATTN_ERR_BOUNDS: return "kernel bounds check failed (debug build)";
   }
   return "unknown status";

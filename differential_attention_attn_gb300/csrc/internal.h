@@ -125,6 +125,12 @@ diffattn_status launch_fwd_f32(const diffattn_desc &desc, const float *q1, const
 diffattn_status launch_headnorm(const diffattn_desc &desc, const float *x, const float *norm_w,
                                 void *out, cudaStream_t stream);
 
+// Checks shared by the C-ABI files (api.cu): the descriptor's own fields, the
+// current device (DIFFATTN_OK on sm_103) and its SM count (0 on failure).
+diffattn_status check_common_desc(const diffattn_desc *desc);
+diffattn_status require_sm103();
+int device_sm_count();
+
 constexpr int kF32MaxN = 4096;
 constexpr int kF32MaxD = 128;
 

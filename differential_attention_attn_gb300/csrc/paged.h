@@ -1,0 +1,55 @@
+// Launchers of the paged key/value-cache operators (include/diffattn_paged.h).
+// Each takes validated arguments and enqueues its kernels on `stream`.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "../../include/diffattn_paged.h"
+#include "internal.h"
+
+namespace diffattn {
+
+constexpr int kPageGrain = 16;  // page sizes are multiples of this many rows
+
+// Forward: keys are taken in tiles of kPagedTile; the rows (new token, query
+// head) of one key/value head in blocks of 8 * query_tiles(rows).
+constexpr int kPagedTile = 64;
+constexpr int kPagedMaxTokens = 16;
+constexpr int kPagedMaxGroup = 64;
+
+struct PagedFwdPlan {
+  int ctas;        // CTAs of the main kernel
+  bool whole;      // one CTA per item (nothing to join); else equal shares of all tiles
+  int row_tiles;   // query tiles of 8 rows per block (1 or 2)
+  int row_blocks;  // row blocks per key/value head
+  int64_t items;   // B * kv_heads * row_blocks
+  int64_t padded;  // keys per sequence in the logit buffer, a multiple of kPagedTile
+  size_t part, stats, records, items_rec, item_stats, logits;  // workspace offsets, bytes
+  size_t bytes;
+};
+
+// False when a size does not fit.
+bool plan_paged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache, bool accumulate,
+                    int sm_count, PagedFwdPlan *plan);
+
+diffattn_status launch_paged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache,
+                                 const PagedFwdPlan &plan, const void *q1, const void *q2,
+                                 const float *lambda, const float *norm_w, void *out,
+                                 const diffattn_strides *strides, bool accumulate,
+                                 void *workspace, cudaStream_t stream);
+
+diffattn_status launch_paged_append(const diffattn_desc &desc, const diffpaged_cache &cache,
+                                    const void *k1, const void *k2, const void *v,
+                                    const diffattn_strides *strides, cudaStream_t stream);
+
+size_t paged_evict_bytes(const diffattn_desc &desc, const diffpaged_cache &cache, int64_t keep);
+diffattn_status launch_paged_evict(const diffattn_desc &desc, const diffpaged_cache &cache,
+                                   int64_t keep, int64_t recent, void *workspace,
+                                   cudaStream_t stream);
+
+// Stores DIFFATTN_ERR_PAGE in the call's status word unless another code is there.
+__device__ __forceinline__ void report_bad_page(int32_t *status) {
+  if (status != nullptr) atomicCAS(status, 0, static_cast<int32_t>(DIFFATTN_ERR_PAGE));
+}
+
+}  // namespace diffattn

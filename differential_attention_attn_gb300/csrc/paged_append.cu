@@ -1,0 +1,195 @@
+// diffpaged_append: the newest tokens' k1, k2 and v rows into the pages of a
+// cache.
+//
+// Token i of sequence b goes to position t = kv_len[b] - N + i (t < 0 is
+// padding and is skipped): row t % page_size of page table[b][t / page_size].
+// With an e4m3 key cache k1 and k2 are rounded on the way: to nearest, ties to
+// even, saturating at +-448 (one conversion from the exact bf16 value; the
+// attention then uses the stored values exactly).
+//
+// Bound: a copy, so HBM bandwidth for prompts (B Hkv N rows of 8 d bytes read
+// and written) and the chain length -> page number -> store for a few tokens.
+// One warp takes whole rows: a row of k1 | k2 | v is 32 (d = 64) or 64 sixteen-
+// byte units, so each lane moves one or two units a row and every access is
+// a full 128-byte line.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "debug_check.cuh"
+#include "paged.h"
+
+namespace diffattn {
+namespace {
+
+constexpr int kWarps = 8;
+
+struct AppendParams {
+  const uint8_t *src[3];  // k1, k2, v (bf16)
+  uint8_t *dst[3];        // the pools
+  int64_t src_b[3], src_h[3], src_n[3];  // strides in bytes
+  int64_t dst_p[3], dst_h[3], dst_n[3];
+  float *weights;
+  const int32_t *page_table;
+  const int32_t *kv_len;
+  int32_t *status;
+  uint32_t rows;  // B * kv_heads * N
+  uint32_t N, kv_heads, page_size, max_pages, num_pages;
+};
+
+// Eight bf16 values of each of two 16-byte units as sixteen e4m3 values.
+__device__ __forceinline__ uint4 to_e4m3(const uint4 &a, const uint4 &b) {
+  uint32_t out[4];
+  const uint32_t in[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint16_t half[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t w = in[2 * i + j];
+      const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xFFFF0000u);
+      half[j] = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+    }
+    out[i] = static_cast<uint32_t>(half[0]) | (static_cast<uint32_t>(half[1]) << 16);
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// kRows rows per warp, whose loads are all in flight before the first store.
+template <int kD, bool kFp8, int kRows>
+__global__ void __launch_bounds__(kWarps * 32) diffpaged_append_kernel(const AppendParams p) {
+  constexpr int kKeyUnits = kFp8 ? kD / 16 : kD / 8;  // 16-byte units stored per key row
+  constexpr int kUnits = 2 * kKeyUnits + kD / 4;
+  constexpr int kPerLane = (kUnits + 31) / 32;
+  const int lane = threadIdx.x % 32;
+  const uint32_t row0 = (blockIdx.x * kWarps + threadIdx.x / 32) * kRows;
+  if (row0 >= p.rows) return;
+
+  uint32_t bs[kRows], hs[kRows], is[kRows];
+  int32_t at[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const uint32_t row = row0 + r < p.rows ? row0 + r : p.rows - 1;
+    const uint32_t bh = row / p.N;
+    is[r] = row - bh * p.N;
+    bs[r] = bh / p.kv_heads;
+    hs[r] = bh - bs[r] * p.kv_heads;
+    at[r] = __ldg(p.kv_len + bs[r]);
+  }
+  // The rows' data does not depend on the places: load it meanwhile.
+  uint4 x[kRows][kPerLane], y[kRows][kPerLane];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r)
+#pragma unroll
+    for (int u = 0; u < kPerLane; ++u) {
+      const int unit = lane + 32 * u;
+      if (unit < kUnits) {
+        const int t = unit < kKeyUnits ? 0 : unit < 2 * kKeyUnits ? 1 : 2;
+        const int off = unit - t * kKeyUnits;
+        const bool wide = kFp8 && t < 2;  // sixteen bf16 in, sixteen bytes out
+        const uint8_t *s = p.src[t] + bs[r] * p.src_b[t] + hs[r] * p.src_h[t] +
+                           is[r] * p.src_n[t] + off * (wide ? 32 : 16);
+        x[r][u] = __ldg(reinterpret_cast<const uint4 *>(s));
+        if (wide) y[r][u] = __ldg(reinterpret_cast<const uint4 *>(s) + 1);
+      }
+    }
+  int32_t page[kRows];
+  uint32_t slot[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const uint32_t most = p.max_pages * p.page_size;
+    const bool fits = at[r] >= 0 && static_cast<uint32_t>(at[r]) <= most;
+    const int32_t t = at[r] - static_cast<int32_t>(p.N) + static_cast<int32_t>(is[r]);
+    page[r] = -1;
+    slot[r] = 0;
+    if (!fits) report_bad_page(p.status);
+    if (fits && t >= 0 && row0 + r < p.rows) {
+      const uint32_t n = static_cast<uint32_t>(t) / p.page_size;
+      slot[r] = static_cast<uint32_t>(t) - n * p.page_size;
+      page[r] = __ldg(p.page_table + static_cast<int64_t>(bs[r]) * p.max_pages + n);
+      if (static_cast<uint32_t>(page[r]) >= p.num_pages) {
+        page[r] = -1;
+        report_bad_page(p.status);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    if (page[r] < 0) continue;
+    if (!dbg_ok(static_cast<uint32_t>(page[r]) < p.num_pages && slot[r] < p.page_size, p.status,
+                40))
+      continue;
+#pragma unroll
+    for (int u = 0; u < kPerLane; ++u) {
+      const int unit = lane + 32 * u;
+      if (unit < kUnits) {
+        const int t = unit < kKeyUnits ? 0 : unit < 2 * kKeyUnits ? 1 : 2;
+        const int off = unit - t * kKeyUnits;
+        uint8_t *d = p.dst[t] + page[r] * p.dst_p[t] + hs[r] * p.dst_h[t] +
+                     static_cast<int64_t>(slot[r]) * p.dst_n[t] + off * 16;
+        *reinterpret_cast<uint4 *>(d) = (kFp8 && t < 2) ? to_e4m3(x[r][u], y[r][u]) : x[r][u];
+      }
+    }
+    if (lane == 0 && p.weights != nullptr)
+      p.weights[(static_cast<int64_t>(page[r]) * p.kv_heads + hs[r]) * p.page_size + slot[r]] = 0.f;
+  }
+}
+
+template <int kD, bool kFp8>
+cudaError_t launch(const AppendParams &p, cudaStream_t stream) {
+  // Few rows: one per warp, for the shortest chain.  Many: four, for more loads in flight.
+  const uint32_t per_block = kWarps * (p.rows <= 16384 ? 1 : 4);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((p.rows + per_block - 1) / per_block);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = stream;
+  return p.rows <= 16384 ? cudaLaunchKernelEx(&cfg, diffpaged_append_kernel<kD, kFp8, 1>, p)
+                         : cudaLaunchKernelEx(&cfg, diffpaged_append_kernel<kD, kFp8, 4>, p);
+}
+
+}  // namespace
+
+diffattn_status launch_paged_append(const diffattn_desc &desc, const diffpaged_cache &cache,
+                                    const void *k1, const void *k2, const void *v,
+                                    const diffattn_strides *strides, cudaStream_t stream) {
+  const double rows = static_cast<double>(desc.B) * static_cast<double>(cache.kv_heads) *
+                      static_cast<double>(desc.N);
+  if (rows >= 2147483648.0) return DIFFATTN_ERR_UNSUPPORTED;  // a terabyte of rows
+  const bool fp8 = desc.dtype == DIFFATTN_E4M3_QK;
+  AppendParams p = {};
+  const void *src[3] = {k1, k2, v};
+  void *dst[3] = {cache.k1, cache.k2, cache.v};
+  const diffattn_strides *ds[3] = {&cache.k1_strides, &cache.k2_strides, &cache.v_strides};
+  for (int t = 0; t < 3; ++t) {
+    const int64_t width = t == 2 ? 2 * desc.d : desc.d;
+    const diffattn_strides s =
+        strides ? strides[t]
+                : diffattn_strides{cache.kv_heads * desc.N * width, desc.N * width, width};
+    const int64_t es = (fp8 && t < 2) ? 1 : 2;
+    p.src[t] = static_cast<const uint8_t *>(src[t]);
+    p.dst[t] = static_cast<uint8_t *>(dst[t]);
+    p.src_b[t] = 2 * s.b;
+    p.src_h[t] = 2 * s.h;
+    p.src_n[t] = 2 * s.n;
+    p.dst_p[t] = es * ds[t]->b;
+    p.dst_h[t] = es * ds[t]->h;
+    p.dst_n[t] = es * ds[t]->n;
+  }
+  p.weights = cache.weights;
+  p.page_table = cache.page_table;
+  p.kv_len = cache.kv_len;
+  p.status = desc.status_dev;
+  p.rows = static_cast<uint32_t>(rows);
+  p.N = static_cast<uint32_t>(desc.N);
+  p.kv_heads = static_cast<uint32_t>(cache.kv_heads);
+  p.page_size = static_cast<uint32_t>(cache.page_size);
+  p.max_pages = static_cast<uint32_t>(cache.max_pages);
+  p.num_pages = static_cast<uint32_t>(cache.num_pages);
+  const cudaError_t e = desc.d == 64 ? (fp8 ? launch<64, true>(p, stream) : launch<64, false>(p, stream))
+                                     : (fp8 ? launch<128, true>(p, stream) : launch<128, false>(p, stream));
+  return e == cudaSuccess ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
+}
+
+}  // namespace diffattn

@@ -18,8 +18,10 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdiffattn.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "diffattn.h")
+PAGED_HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "diffattn_paged.h")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_BOUNDS = 0, 1, 2, 3, 4, 5
+ERR_PAGE = 6
 BF16, F32, E4M3_QK = 0, 1, 2
 _DTYPE_CODE = {torch.bfloat16: BF16, torch.float32: F32}
 
@@ -43,6 +45,19 @@ class Desc(ctypes.Structure):
 class Strides(ctypes.Structure):
     """Mirror of `diffattn_strides` (element strides of batch, head, row)."""
     _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("n", ctypes.c_int64)]
+
+
+class PagedCacheStruct(ctypes.Structure):
+    """Mirror of `diffpaged_cache` in include/diffattn_paged.h."""
+    _fields_ = [
+        ("k1", ctypes.c_void_p), ("k2", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+        ("kv_len", ctypes.c_void_p),
+        ("k1_strides", Strides), ("k2_strides", Strides), ("v_strides", Strides),
+        ("num_pages", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
+        ("max_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
 
 
 _lock = threading.Lock()
@@ -120,6 +135,16 @@ def bind(lib):
     lib.diffattn_fwd_kv_strided.argtypes = [dp, ctypes.c_int64, vp, vp, vp, vp, vp, fp, fp,
                                             vp, ctypes.c_int, vp, ctypes.c_size_t,
                                             ctypes.POINTER(Strides), vp]
+    cp, szp, i64 = ctypes.POINTER(PagedCacheStruct), ctypes.POINTER(ctypes.c_size_t), ctypes.c_int64
+    for name, args in (
+            ("append", [dp, cp, vp, vp, vp, ctypes.POINTER(Strides), vp]),
+            ("fwd_plan", [dp, cp, ctypes.c_int, szp]),
+            ("fwd", [dp, cp, vp, vp, fp, fp, vp, ctypes.POINTER(Strides), ctypes.c_int, vp,
+                     ctypes.c_size_t, vp]),
+            ("evict_plan", [dp, cp, i64, szp]),
+            ("evict", [dp, cp, i64, i64, vp, ctypes.c_size_t, vp])):
+        fn = getattr(lib, "diffpaged_" + name)
+        fn.restype, fn.argtypes = ctypes.c_int, args
     lib.diffattn_selftest_wait.restype = ctypes.c_int
     lib.diffattn_selftest_wait.argtypes = [vp, ctypes.c_int64, vp]
     lib.diffattn_headnorm.restype = ctypes.c_int
@@ -616,6 +641,229 @@ def fwd_kv_noalloc(q1, k1, q2, k2, v, lam, *, causal: bool, headnorm: bool = Tru
         return st
     _check(st)
     return out
+
+
+class PagedCache:
+    """A paged key/value cache (`diffpaged_cache` of include/diffattn_paged.h).
+
+    k1, k2: [pages, kv_heads, page_size, d], bf16 or both float8_e4m3fn; v: bf16 [pages,
+    kv_heads, page_size, 2d]; CUDA tensors or views of any layout with contiguous rows
+    (e.g. x.permute(0, 2, 1, 3) of [pages, page_size, kv_heads, d] storage).  page_table:
+    int32 [B, max_pages]; kv_len: int32 [B], the lengths with the newest tokens counted;
+    weights: float32 [pages, kv_heads, page_size] or None.  All on one device.
+
+    The tensors are checked here, once; the calls then use their addresses, so they are
+    changed in place (kv_len.add_(1), page_table[b, n] = page), not replaced.
+    """
+
+    def __init__(self, k1, k2, v, page_table, kv_len, weights=None):
+        if k1.dim() != 4:
+            raise ValueError("k1 must be [pages, kv_heads, page_size, d]")
+        pages, heads, page, d = k1.shape
+        if k1.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError(f"unsupported key dtype {k1.dtype}")
+        if page_table.dim() != 2 or kv_len.dim() != 1:
+            raise ValueError("page_table must be [B, max_pages] and kv_len [B]")
+        B, max_pages = page_table.shape
+        for name, t, shape, dtype in (
+                ("k1", k1, (pages, heads, page, d), k1.dtype),
+                ("k2", k2, (pages, heads, page, d), k1.dtype),
+                ("v", v, (pages, heads, page, 2 * d), torch.bfloat16),
+                ("page_table", page_table, (B, max_pages), torch.int32),
+                ("kv_len", kv_len, (B,), torch.int32),
+                ("weights", weights, (pages, heads, page), torch.float32)):
+            if t is None:
+                continue
+            if tuple(t.shape) != shape or t.dtype != dtype:
+                raise ValueError(f"{name} must be {shape} {dtype}")
+            if name in ("k1", "k2", "v"):
+                if d and t.stride(-1) != 1:
+                    raise ValueError("rows must be contiguous (last stride 1)")
+            elif not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        for t in (k1, k2, v, page_table, kv_len, weights):
+            if t is not None and (not t.is_cuda or t.device != k1.device):
+                raise ValueError("all tensors must be CUDA tensors of one device")
+        self.k1, self.k2, self.v = k1, k2, v
+        self.page_table, self.kv_len, self.weights = page_table, kv_len, weights
+        self.B, self.kv_heads, self.d, self.page_size = B, heads, d, page
+        self.device, self.dtype = k1.device, k1.dtype
+        self.code = E4M3_QK if k1.dtype == torch.float8_e4m3fn else BF16
+        self._struct = PagedCacheStruct(
+            k1.data_ptr(), k2.data_ptr(), v.data_ptr(),
+            0 if weights is None else weights.data_ptr(), page_table.data_ptr(),
+            kv_len.data_ptr(), *(_strides4(t) for t in (k1, k2, v)), pages, heads, max_pages,
+            page, 0)
+        self._ref = ctypes.byref(self._struct)
+
+
+def _strides4(t):
+    """(outer, head, row) element strides of a 4-D tensor with contiguous rows.  An axis of one
+    element is never stepped along: it gets the stride it would have in contiguous storage."""
+    s, n = t.stride(), t.shape
+    row = s[2] if n[2] > 1 else n[3]
+    head = s[1] if n[1] > 1 else row * n[2]
+    return Strides(s[0] if n[0] > 1 else head * n[1], head, row)
+
+
+def _on_device(dev, stream):
+    """The stream of a call on tensors of device `dev`; refuses one of another device, and the
+    current device being another (its context would run the kernels)."""
+    index = torch.cuda.current_device()
+    if dev.index != index:
+        raise ValueError(f"the cache is on cuda:{dev.index}, the current device is cuda:{index}")
+    if stream is None:
+        return torch.cuda.current_stream()
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the cache on {dev}")
+    return stream
+
+
+def _scratch(nbytes, dev, stream):
+    """A torch buffer that belongs to `stream`, so that its memory is reused only in its order."""
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
+def _workspace(workspace, need, dev, stream):
+    """(pointer, bytes, buffer to keep) of a call's workspace: the caller's, or one of its own."""
+    if workspace is None:
+        if not need:
+            return None, 0, None
+        workspace = _scratch(need, dev, stream)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def paged_append(cache, k1, k2, v, *, status=None, stream=None, raw_status: bool = False):
+    """`diffpaged_append`: the N newest tokens' rows into the cache, at positions kv_len - N + i
+    (negative ones are padding).
+
+    k1, k2: bf16 [B, kv_heads, N, d] (rounded to e4m3 where the cache holds that); v: bf16
+    [B, kv_heads, N, 2d]; views of any layout with contiguous rows.
+    """
+    if k1.dim() != 4:
+        raise ValueError("k1 must be [B, kv_heads, N, d]")
+    B, H, N, d = cache.B, cache.kv_heads, k1.shape[2], cache.d
+    for name, t, width in (("k1", k1, d), ("k2", k2, d), ("v", v, 2 * d)):
+        if t.shape != (B, H, N, width) or t.dtype != torch.bfloat16:
+            raise ValueError(f"{name} must be {(B, H, N, width)} bfloat16")
+        if t.device != cache.device or t.stride(3) != 1:
+            raise ValueError(f"{name} must be on the cache's device with contiguous rows")
+    stream = _on_device(cache.device, stream)
+    desc = make_desc(B, H, N, d, cache.code, True, 0, 0.0, 0.0, status)
+    strides = (Strides * 3)(_strides4(k1), _strides4(k2), _strides4(v))
+    st = load().diffpaged_append(ctypes.byref(desc), cache._ref, k1.data_ptr(), k2.data_ptr(),
+                                 v.data_ptr(), strides, stream.cuda_stream)
+    if raw_status:
+        return st
+    _check(st)
+
+
+def paged_fwd_plan(cache, H: int, N: int = 1, *, accumulate: bool = False,
+                   raw_status: bool = False):
+    """`diffpaged_fwd_plan`: workspace bytes of paged_fwd with H query heads and N new tokens."""
+    desc = make_desc(cache.B, H, N, cache.d, cache.code, True, 1, 1e-5, 0.0)
+    n = ctypes.c_size_t(0)
+    st = load().diffpaged_fwd_plan(ctypes.byref(desc), cache._ref, int(accumulate),
+                                   ctypes.byref(n))
+    if raw_status:
+        return st, n.value
+    _check(st)
+    return n.value
+
+
+def paged_fwd(cache, q1, q2, lam, *, causal: bool = True, headnorm: int = 1, norm_w=None,
+              eps: float = 1e-5, lambda_init: float = 0.0, accumulate: bool = False,
+              workspace=None, out=None, status=None, stream=None, raw_status: bool = False):
+    """`diffpaged_fwd`: the N newest tokens of every sequence against the paged cache.
+
+    q1, q2: [B, H, N, d] of the cache's key dtype, H a multiple of its kv_heads, N <= 16;
+    lam: float32 [H]; norm_w: float32 [H, 2d] or None.  Views of any layout with contiguous
+    rows (`out` too).  accumulate adds each key's sum |map1 - lam map2| to cache.weights.
+    workspace: a CUDA tensor of at least paged_fwd_plan bytes (a torch buffer when None).
+    Returns bf16 out [B, H, N, 2d] (of `stream`'s memory when allocated here).
+    """
+    if q1.dim() != 4:
+        raise ValueError("q1 must be [B, H, N, d]")
+    B, H, N, d = q1.shape
+    dev = cache.device
+    if B != cache.B or d != cache.d or q2.shape != q1.shape:
+        raise ValueError(f"q1 and q2 must be [{cache.B}, H, N, {cache.d}]")
+    if q1.dtype != cache.dtype or q2.dtype != cache.dtype:
+        raise ValueError(f"q1 and q2 must be {cache.dtype}, as the cache's keys")
+    if q1.stride(3) != 1 or q2.stride(3) != 1:
+        raise ValueError("rows must be contiguous (last stride 1)")
+    if lam.dtype != torch.float32 or lam.numel() != H or not lam.is_contiguous():
+        raise ValueError("lam must be contiguous float32 [H]")
+    if norm_w is not None and (norm_w.dtype != torch.float32 or norm_w.numel() != H * 2 * d or
+                               not norm_w.is_contiguous() or norm_w.device != dev):
+        raise ValueError("norm_w must be contiguous float32 [H, 2d]")
+    if q1.device != dev or q2.device != dev or lam.device != dev:
+        raise ValueError("all tensors must be on the cache's device")
+    stream = _on_device(dev, stream)
+    if out is None:
+        if stream == torch.cuda.current_stream():
+            out = torch.empty((B, H, N, 2 * d), dtype=torch.bfloat16, device=dev)
+        else:
+            with torch.cuda.stream(stream):
+                out = torch.empty((B, H, N, 2 * d), dtype=torch.bfloat16, device=dev)
+    elif out.shape != (B, H, N, 2 * d) or out.dtype != torch.bfloat16 or out.device != dev or \
+            out.stride(3) != 1:
+        raise ValueError("out must be bfloat16 [B, H, N, 2d] with contiguous rows")
+    desc = make_desc(B, H, N, d, cache.code, causal, headnorm, eps, lambda_init, status)
+    ref, lib = ctypes.byref(desc), load()
+    need = 0
+    if workspace is None:
+        n = ctypes.c_size_t(0)
+        st = lib.diffpaged_fwd_plan(ref, cache._ref, int(accumulate), ctypes.byref(n))
+        if st != OK:
+            if raw_status:
+                return st
+            _check(st)
+        need = n.value
+    ws, ws_bytes, _keep = _workspace(workspace, need, dev, stream)
+    strides = (Strides * 3)(_strides4(q1), _strides4(q2), _strides4(out))
+    st = lib.diffpaged_fwd(ref, cache._ref, q1.data_ptr(), q2.data_ptr(), lam.data_ptr(),
+                           None if norm_w is None else norm_w.data_ptr(), out.data_ptr(),
+                           strides, int(accumulate), ws, ws_bytes, stream.cuda_stream)
+    if raw_status:
+        return st
+    _check(st)
+    return out
+
+
+def paged_evict_plan(cache, *, keep: int, raw_status: bool = False):
+    """`diffpaged_evict_plan`: workspace bytes of paged_evict."""
+    desc = make_desc(cache.B, cache.kv_heads, 0, cache.d, cache.code, True, 0, 0.0, 0.0)
+    n = ctypes.c_size_t(0)
+    st = load().diffpaged_evict_plan(ctypes.byref(desc), cache._ref, int(keep), ctypes.byref(n))
+    if raw_status:
+        return st, n.value
+    _check(st)
+    return n.value
+
+
+def paged_evict(cache, *, keep: int, recent: int = 0, workspace=None, status=None, stream=None,
+                raw_status: bool = False):
+    """`diffpaged_evict`: cut every sequence longer than `keep` to its last `recent` keys and
+    the keep - recent of the largest weights, in place; updates cache.kv_len."""
+    stream = _on_device(cache.device, stream)
+    need = 0
+    if workspace is None:
+        st, need = paged_evict_plan(cache, keep=keep, raw_status=True)
+        if st != OK:
+            if raw_status:
+                return st
+            _check(st)
+    ws, ws_bytes, _keep = _workspace(workspace, need, cache.device, stream)
+    desc = make_desc(cache.B, cache.kv_heads, 0, cache.d, cache.code, True, 0, 0.0, 0.0, status)
+    st = load().diffpaged_evict(ctypes.byref(desc), cache._ref, int(keep), int(recent), ws,
+                                ws_bytes, stream.cuda_stream)
+    if raw_status:
+        return st
+    _check(st)
 
 
 def headnorm(x, *, H: int, norm_w=None, eps: float = 1e-5, lambda_init: float = 0.0,

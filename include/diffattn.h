@@ -56,10 +56,13 @@ typedef enum diffattn_status {
     DIFFATTN_ERR_UNSUPPORTED = 2, /* valid request outside the implemented domain */
     DIFFATTN_ERR_CUDA = 3,        /* a CUDA runtime or driver call failed */
     DIFFATTN_ERR_TIMEOUT = 4,     /* written to status_dev by a kernel whose wait ran out */
-    DIFFATTN_ERR_BOUNDS = 5       /* debug build only (compiled with DIFFATTN_DEBUG): a
+    DIFFATTN_ERR_BOUNDS = 5,      /* debug build only (compiled with DIFFATTN_DEBUG): a
                                      kernel's bounds check failed; status_dev holds
                                      5 | (site << 8) of the first failing check, and the
                                      checked access was skipped */
+    DIFFATTN_ERR_PAGE = 6         /* written to status_dev by a paged-cache kernel
+                                     (diffattn_paged.h) that met a page number outside the
+                                     pool or a sequence length outside the table */
 } diffattn_status;
 
 typedef enum diffattn_dtype {

@@ -1,0 +1,502 @@
+"""The paged key/value-cache operators on the GPU against float64 references."""
+import pytest
+import torch
+
+from differential_attention_attn_gb300 import ops
+from tests import paged_ref as R
+
+pytestmark = pytest.mark.gpu
+E4M3 = torch.float8_e4m3fn
+LI = 0.5
+
+
+def _fwd(c, q1, q2, lam, w, **kw):
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = ops.paged_fwd(c.ops_cache(), q1, q2, lam, norm_w=w, lambda_init=LI, status=status, **kw)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    return out
+
+
+def _parity(c, H, N, seed=3, causal=True, headnorm=1, scale=1.5, **kw):
+    q1, q2, lam, w = R.queries(seed, c.B, H, N, c.d, c.dtype, scale)
+    out = _fwd(c, q1, q2, lam, w, causal=causal, headnorm=headnorm, **kw)
+    ref, tol, _, _ = R.attend(c, q1, q2, lam, causal=causal, headnorm=headnorm, norm_w=w,
+                              lambda_init=LI)
+    R.check(out, ref, tol, "out")
+    return out
+
+
+# ---- append ---------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, E4M3])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("layout", ["head", "token"])
+@pytest.mark.parametrize("N", [1, 3, 70])
+def test_append_writes_the_newest_positions_and_nothing_else(dtype, d, layout, N):
+    lens = [1, 70, 0, 33, 129, 2]
+    c = R.Cache(1, lens=lens, kv=3, d=d, page=32, dtype=dtype, layout=layout, weights=True,
+                fill=7.0)
+    want = {t: R.f64(getattr(c, t)).clone() for t in ("k1", "k2", "v", "weights")}
+    g = torch.Generator().manual_seed(5)
+    new = {t: (torch.randn(6, N, 3, w, generator=g) * 20).to(torch.bfloat16).cuda()
+           .permute(0, 2, 1, 3) for t, w in (("k1", d), ("k2", d), ("v", 2 * d))}
+    for b, n in enumerate(lens):
+        for i in range(N):
+            t = n - N + i
+            if t < 0:
+                continue
+            page, slot = int(c.table[b, t // 32]), t % 32
+            for name in ("k1", "k2", "v"):
+                row = R.f64(new[name][b, :, i])
+                want[name][page, :, slot] = R.to_e4m3(row) if dtype == E4M3 and name != "v" else row
+            want["weights"][page, :, slot] = 0
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ops.paged_append(c.ops_cache(), new["k1"], new["k2"], new["v"], status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    for t in want:
+        assert torch.equal(R.f64(getattr(c, t)), want[t]), t
+
+
+def test_append_many_rows():
+    """More rows than the one-row-per-warp variant takes."""
+    c = R.Cache(2, lens=[4100, 4033], kv=4, d=64, page=64, fill=0.0)
+    g = torch.Generator().manual_seed(6)
+    new = [torch.randn(2, 4, 4099, w, generator=g).to(torch.bfloat16).cuda() for w in (64, 64, 128)]
+    before = [c.rows(t, 0, 1).clone() for t in ("k1", "k2", "v")]
+    ops.paged_append(c.ops_cache(), *new)
+    for t, x, old in zip(("k1", "k2", "v"), new, before):
+        assert torch.equal(c.rows(t, 0)[:, 1:], x[0])
+        assert torch.equal(c.rows(t, 0)[:, :1], old)
+        assert torch.equal(c.rows(t, 1), x[1, :, 4099 - 4033:])
+
+
+def test_append_rounds_to_e4m3():
+    """Ties, subnormals, values at and past the largest, infinities and NaN."""
+    c = R.Cache(3, lens=[1], kv=1, d=64, page=16, dtype=E4M3)
+    x = torch.zeros(64)
+    vals = [0.0, -0.0, 1.0625, 1.1875, 447.0, 448.0, 464.0, 466.0, -1e4, float("inf"),
+            float("-inf"), float("nan"), 2.0 ** -9, 2.0 ** -10, 3 * 2.0 ** -10, 2.0 ** -11,
+            -5 * 2.0 ** -10, 0.0146484375, 17.0, 19.0, 240.0, 248.0]
+    x[:len(vals)] = torch.tensor(vals)
+    x = x.to(torch.bfloat16)
+    k = x.reshape(1, 1, 1, 64).cuda()
+    ops.paged_append(c.ops_cache(), k, k, torch.zeros(1, 1, 1, 128, dtype=torch.bfloat16,
+                                                      device="cuda"))
+    got, want = R.f64(c.rows("k1", 0))[0, 0].cpu(), R.to_e4m3(x.double())
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got[~torch.isnan(want)], want[~torch.isnan(want)])
+
+
+# ---- attention ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("d,dtype", [(64, torch.bfloat16), (128, torch.bfloat16), (64, E4M3),
+                                     (128, E4M3)])
+@pytest.mark.parametrize("H,kv,N", [(2, 2, 1), (4, 1, 1), (6, 2, 3), (7, 1, 1), (9, 1, 1),
+                                    (8, 2, 5), (3, 3, 16)])
+def test_short_ragged_batch(d, dtype, H, kv, N):
+    """Up to four tiles a sequence: one CTA per item."""
+    c = R.Cache(11, lens=[1, 0, 16, 17, 63, 64, 65, 128, 200, 5], kv=kv, d=d, page=16,
+                dtype=dtype)
+    _parity(c, H, N)
+
+
+@pytest.mark.parametrize("d,dtype", [(64, torch.bfloat16), (128, torch.bfloat16), (64, E4M3),
+                                     (128, E4M3)])
+@pytest.mark.parametrize("page,layout", [(16, "token"), (48, "head"), (64, "head"),
+                                         (128, "token")])
+def test_long_ragged_batch(d, dtype, page, layout):
+    """Shares of all tiles: items cut by CTA boundaries and joined."""
+    c = R.Cache(12, lens=[1500, 1, 0, 700, 65, 2049], kv=2, d=d, page=page, dtype=dtype,
+                layout=layout)
+    _parity(c, 4, 2)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("headnorm", [0, 1, 2])
+@pytest.mark.parametrize("N", [1, 4])
+def test_norms_and_masks(causal, headnorm, N):
+    c = R.Cache(13, lens=[3, 400, 0, 61, 1, 66], kv=2, d=64, page=16)
+    _parity(c, 2, N, causal=causal, headnorm=headnorm)
+    c = R.Cache(14, lens=[2, 3, 1, 0, 130], kv=2, d=128, page=16)
+    _parity(c, 4, N, causal=causal, headnorm=headnorm)
+
+
+@pytest.mark.parametrize("kv,H,n", [(1, 1, 20001), (1, 8, 30000), (1, 20, 9000), (2, 2, 16384)])
+def test_one_long_sequence(kv, H, n):
+    """One item cut over many CTAs; with 20 query heads three row blocks of it."""
+    c = R.Cache(15, lens=[n], kv=kv, d=64, page=64)
+    _parity(c, H, 1)
+
+
+def test_group_of_64_and_16_tokens():
+    c = R.Cache(16, lens=[90, 10], kv=1, d=64, page=16)
+    _parity(c, 64, 16)
+
+
+def test_large_and_climbing_logits():
+    """Logits of +-100s that grow along the keys move the reference maximum at every tile."""
+    c = R.Cache(17, lens=[900, 130], kv=2, d=64, page=16, fill=0.0)
+    for b in range(2):
+        n = c.lens[b]
+        for t in range(n):
+            page, slot = int(c.table[b, t // 16]), t % 16
+            c.k1[page, :, slot] *= 0.02 * t
+            c.k2[page, :, slot] *= 6.0
+    _parity(c, 4, 2, scale=3.0)
+
+
+def test_garbage_in_unused_places_has_no_influence():
+    lens = [70, 0, 200, 1, 129]
+    a = R.Cache(18, lens=lens, kv=2, d=64, page=32, fill=float("nan"))
+    b = R.Cache(18, lens=lens, kv=2, d=64, page=32, fill=float("inf"))
+    z = R.Cache(18, lens=lens, kv=2, d=64, page=32, fill=0.0)
+    outs = [_parity(c, 4, 3) for c in (a, b, z)]
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[2])
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("where", ["v", "k1", "k2"])
+def test_non_finite_newest_token_reaches_only_rows_that_see_it(bad, where):
+    """A masked key is left out, not multiplied by zero: earlier tokens stay finite."""
+    for lens in ([66, 300], [64, 1], [3, 40]):
+        c = R.Cache(19, lens=lens, kv=1, d=64, page=16)
+        for b, n in enumerate(lens):
+            pool = getattr(c, where)
+            pool[int(c.table[b, (n - 1) // 16]), 0, (n - 1) % 16, 5] = bad
+        q1, q2, lam, w = R.queries(4, 2, 2, 4, 64)
+        out = _fwd(c, q1, q2, lam, w, headnorm=0).double()
+        ref, tol, _, _ = R.attend(c, q1, q2, lam, headnorm=0)
+        for b, n in enumerate(lens):
+            R.check(out[b, :, :3], ref[b, :, :3], tol[b, :, :3], "rows before it")
+            if where == "v":
+                last = out[b, :, 3]
+                assert bool(torch.isfinite(last[:, [4, 6]]).all())
+                assert not bool(torch.isfinite(last[:, 5]).any())
+            else:  # a logit of +inf or NaN makes the row NaN, one of -inf drops the key
+                R.check(out[b, :, 3], ref[b, :, 3], tol[b, :, 3], "the newest row")
+
+
+def test_strided_queries_and_output():
+    c = R.Cache(20, lens=[300, 40], kv=2, d=64, page=16)
+    q1, q2, lam, w = R.queries(7, 2, 6, 3, 64)
+    v1, v2 = (q.permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3) for q in (q1, q2))
+    big = torch.full((2, 3, 6, 160), 9.0, dtype=torch.bfloat16, device="cuda")
+    out = big[..., 16:144].permute(0, 2, 1, 3)
+    want = _fwd(c, q1, q2, lam, w)
+    got = _fwd(c, v1, v2, lam, w, out=out)
+    assert got is out and torch.equal(got, want)
+    assert bool((big[..., :16] == 9).all()) and bool((big[..., 144:] == 9).all())
+
+
+def test_offsets_past_32_bits():
+    """Pages whose byte and element offsets do not fit 32 bits."""
+    page, d, P = 64, 64, 1 << 19  # v: 2^32 elements
+    k1, k2 = (torch.empty(P, 1, page, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    v = torch.empty(P, 1, page, 2 * d, dtype=torch.bfloat16, device="cuda")
+    small = R.Cache(21, lens=[150], kv=1, d=d, page=page, weights=True)
+    far = [P - 1, P - 7, P // 2 + 3]
+    weights = torch.zeros(P, 1, page, device="cuda")
+    for k, f in enumerate(far):
+        s = int(small.table[0, k])
+        for big, t in ((k1, small.k1), (k2, small.k2), (v, small.v)):
+            big[f] = t[s]
+    table = torch.tensor([far], dtype=torch.int32, device="cuda")
+    cache = ops.PagedCache(k1, k2, v, table, small.kv_len, weights=weights)
+    q1, q2, lam, w = R.queries(8, 1, 2, 1, d)
+    out = ops.paged_fwd(cache, q1, q2, lam, norm_w=w, lambda_init=LI, accumulate=True)
+    ref, tol, add, add_tol = R.attend(small, q1, q2, lam, norm_w=w, lambda_init=LI)
+    R.check(out, ref, tol, "out")
+    got = torch.cat([weights[f, 0] for f in far])[:150]
+    R.check(got, add[0][0], add_tol[0][0] + 2.0 ** -23, "weights")
+    new = [torch.ones(1, 1, 1, x, dtype=torch.bfloat16, device="cuda") for x in (d, d, 2 * d)]
+    ops.paged_append(cache, *new)
+    assert bool((v[far[2], 0, 149 - 128] == 1).all()) and float(weights[far[2], 0, 21]) == 0
+    weights[far[0], 0, :10] = 5.0
+    rows = v[far[0], 0, 0:10].clone()
+    last = v[far[2], 0, 21].clone()
+    ops.paged_evict(cache, keep=11, recent=1)
+    assert torch.equal(v[far[0], 0, :10], rows) and torch.equal(v[far[0], 0, 10], last)
+    assert small.kv_len.tolist() == [11]
+
+
+# ---- weights --------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("lens,H,kv,N,d,page,dtype", [
+    ([100, 0, 1, 64, 130], 4, 2, 1, 64, 16, torch.bfloat16),
+    ([3, 700, 1100], 6, 2, 3, 64, 48, torch.bfloat16),
+    ([2300], 12, 1, 2, 128, 32, torch.bfloat16),
+    ([1030, 33], 2, 2, 1, 64, 64, E4M3),
+])
+def test_accumulated_weights(lens, H, kv, N, d, page, dtype):
+    c = R.Cache(31, lens=lens, kv=kv, d=d, page=page, dtype=dtype, weights=True)
+    before = c.weights.clone()
+    q1, q2, lam, w = R.queries(9, c.B, H, N, d, dtype)
+    out = _fwd(c, q1, q2, lam, w, accumulate=True)
+    ref, tol, add, add_tol = R.attend(c, q1, q2, lam, norm_w=w, lambda_init=LI)
+    R.check(out, ref, tol, "out")
+    after = c.weights.clone()
+    touched = torch.zeros_like(before, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        if not n:
+            continue
+        c.weights = before
+        old = c.rows("weights", b).double()
+        c.weights = after
+        want = old + add[b]
+        # R N fp32 additions and one to the old value
+        tol_w = add_tol[b] + want.abs() * (H // kv * N + 2) * 2.0 ** -23
+        R.check(c.rows("weights", b), want, tol_w, f"weights of sequence {b}")
+        for t in range(n):
+            touched[int(c.table[b, t // page]), :, t % page] = True
+    assert torch.equal(after[~touched], before[~touched])
+    # a fixed order of addition: the same bits again
+    c.weights = before.clone()
+    assert torch.equal(_fwd(c, q1, q2, lam, w, accumulate=True), out)
+    assert torch.equal(c.weights, after)
+
+
+# ---- bad pages and lengths ------------------------------------------------------------------
+
+@pytest.mark.parametrize("lens", [[100, 90, 33], [1000, 900, 33]])
+@pytest.mark.parametrize("bad", [-1, 1 << 20])
+def test_bad_page_is_reported_and_kept_apart(lens, bad):
+    c = R.Cache(41, lens=lens, kv=2, d=64, page=16, weights=True)
+    q1, q2, lam, w = R.queries(10, 3, 4, 1, 64)
+    want = _fwd(c, q1, q2, lam, w)
+    c.table[1, 2] = bad
+    pools = {t: getattr(c, t).clone() for t in ("k1", "k2", "v", "weights")}
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = ops.paged_fwd(c.ops_cache(), q1, q2, lam, norm_w=w, lambda_init=LI, status=status,
+                        accumulate=True)
+    assert int(status) == ops.ERR_PAGE
+    assert bool(torch.isnan(out[1]).all())
+    assert torch.equal(out[0], want[0]) and torch.equal(out[2], want[2])
+    for t in range(lens[1]):
+        if t // 16 != 2:
+            page, slot = int(c.table[1, t // 16]), t % 16
+            assert torch.equal(c.weights[page, :, slot], pools["weights"][page, :, slot])
+    status.zero_()
+    lens_before = c.kv_len.clone()
+    kept = {t: c.rows(t, 0).clone() for t in ("k1", "v")}
+    ops.paged_evict(c.ops_cache(), keep=60, recent=4, status=status)
+    assert int(status) == ops.ERR_PAGE
+    assert c.kv_len.tolist() == [min(60, lens[0]), lens[1], min(60, lens[2])]
+    assert lens_before.tolist() == lens
+    status.zero_()
+    c.kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+    c.kv_len[1] = 48
+    new = [torch.ones(3, 2, 20, x, dtype=torch.bfloat16, device="cuda") for x in (64, 64, 128)]
+    ops.paged_append(c.ops_cache(), *new, status=status)
+    assert int(status) == ops.ERR_PAGE
+    assert bool((c.v[int(c.table[1, 1]), :, 12:] == 1).all())
+    del kept
+
+
+@pytest.mark.parametrize("bad", [-1, 161, 2 ** 31 - 1, -2 ** 31])
+def test_bad_length_is_reported_and_kept_apart(bad):
+    c = R.Cache(42, lens=[100, 90, 33], kv=2, d=64, page=16, weights=True, extra_pages=3)
+    q1, q2, lam, w = R.queries(10, 3, 4, 2, 64)
+    want = _fwd(c, q1, q2, lam, w)
+    c.kv_len[1] = bad
+    pools = {t: getattr(c, t).clone() for t in ("k1", "k2", "v", "weights")}
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = ops.paged_fwd(c.ops_cache(), q1, q2, lam, norm_w=w, lambda_init=LI, status=status)
+    assert int(status) == ops.ERR_PAGE
+    assert bool(torch.isnan(out[1]).all())
+    assert torch.equal(out[0], want[0]) and torch.equal(out[2], want[2])
+    status.zero_()
+    ops.paged_evict(c.ops_cache(), keep=120, recent=4, status=status)
+    assert int(status) == ops.ERR_PAGE
+    new = [torch.ones(3, 2, 1, x, dtype=torch.bfloat16, device="cuda") for x in (64, 64, 128)]
+    status.zero_()
+    ops.paged_append(c.ops_cache(), *new, status=status)
+    assert int(status) == ops.ERR_PAGE
+    mine = [int(x) for x in c.table[1] if x >= 0]
+    for t in pools:
+        raw = getattr(c, t).view(torch.int16 if t != "weights" else torch.int32)
+        old = pools[t].view(raw.dtype)
+        assert torch.equal(raw[mine], old[mine]), t
+    assert c.kv_len.tolist() == [100, bad, 33]
+
+
+# ---- eviction -------------------------------------------------------------------------------
+
+def _check_evict(c, keep, recent, **kw):
+    before = {t: getattr(c, t).clone() for t in ("k1", "k2", "v", "weights")}
+    kept = [R.evict(c, b, keep, recent) for b in range(c.B)]
+    want = {t: x.view(torch.uint8).clone() if x.dtype == E4M3 else
+            x.view(torch.int16).clone() if x.dtype == torch.bfloat16 else
+            x.view(torch.int32).clone() for t, x in before.items()}
+    for b, rows in enumerate(kept):
+        if rows is None:
+            continue
+        for h, src in enumerate(rows):
+            s = torch.tensor(src, dtype=torch.long, device="cuda")
+            dst = torch.arange(len(src), device="cuda")
+            tab = c.table[b].long()
+            for t in want:
+                want[t][tab[dst // c.page], h, dst % c.page] = \
+                    want[t][tab[s // c.page], h, s % c.page].clone()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ops.paged_evict(c.ops_cache(), keep=keep, recent=recent, status=status, **kw)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    assert c.kv_len.tolist() == [min(n, keep) for n in c.lens]
+    for t in want:
+        got = getattr(c, t)
+        assert torch.equal(got.view(want[t].dtype), want[t]), t
+    c.lens = c.kv_len.tolist()
+
+
+@pytest.mark.parametrize("keep,recent", [(0, 0), (1, 0), (1, 1), (64, 0), (64, 64), (100, 17),
+                                         (1024, 100), (2999, 5), (3000, 0)])
+def test_evict_keeps_the_largest_weights(keep, recent):
+    c = R.Cache(51, lens=[3000, 100, 0, 65, 1025, 2048], kv=2, d=64, page=16, weights=True)
+    _check_evict(c, keep, recent)
+
+
+@pytest.mark.parametrize("d,dtype,layout,page", [(128, torch.bfloat16, "token", 48),
+                                                 (64, E4M3, "head", 64),
+                                                 (128, E4M3, "token", 16)])
+def test_evict_layouts(d, dtype, layout, page):
+    c = R.Cache(52, lens=[777, 300, 12], kv=3, d=d, page=page, dtype=dtype, layout=layout,
+                weights=True)
+    _check_evict(c, 256, 32)
+    _check_evict(c, 255, 0)
+
+
+def test_evict_ties_and_special_values():
+    """Equal weights: the lower position stays; NaN as +infinity; -0 equals 0; negatives last."""
+    c = R.Cache(53, lens=[1500, 1500, 40, 1500], kv=1, d=64, page=16, weights=True)
+
+    def put(b, values):
+        for t, x in enumerate(values):
+            c.weights[int(c.table[b, t // 16]), 0, t % 16] = x
+
+    put(0, [1.0] * 1500)
+    put(1, [0.0 if t % 3 else -0.0 for t in range(1500)])
+    special = [float("nan"), float("inf"), -1.0, 0.0, -0.0, 1e-45, -float("inf"), 3.0, 3.0, 3.0]
+    put(2, special * 4)
+    put(3, [float((t * 7919) % 13) for t in range(1500)])
+    _check_evict(c, 37, 5)
+    _check_evict(c, 20, 3)
+
+
+def test_evict_large_cache():
+    c = R.Cache(54, lens=[40000], kv=1, d=64, page=64, weights=True)
+    _check_evict(c, 20000, 1000)
+
+
+# ---- a run of them --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, E4M3])
+def test_prompt_decode_and_evict_together(dtype):
+    """Prompts of different lengths, then decoding steps with eviction whenever a sequence passes
+    its budget, the whole state followed by the float64 operators on the stored values."""
+    B, H, kv, d, page, budget, recent = 3, 4, 2, 64, 16, 96, 24
+    c = R.Cache(61, lens=[160, 160, 160], kv=kv, d=d, page=page, dtype=dtype, weights=True,
+                fill=0.0)
+    prompt = [70, 95, 1]
+    c.kv_len.copy_(torch.tensor(prompt, dtype=torch.int32))
+    cache = c.ops_cache()
+    g = torch.Generator().manual_seed(62)
+
+    def new(N):
+        return [torch.randn(B, kv, N, w, generator=g).to(torch.bfloat16).cuda()
+                for w in (d, d, 2 * d)]
+
+    ops.paged_append(cache, *new(95))
+    for step in range(40):
+        N = 1 if step % 4 else 3
+        c.kv_len.add_(N)
+        c.lens = c.kv_len.tolist()
+        ops.paged_append(cache, *new(N))
+        q1, q2, lam, w = R.queries(100 + step, B, H, N, d, dtype)
+        old = [c.rows("weights", b).double() for b in range(B)]
+        ref, tol, add, add_tol = R.attend(c, q1, q2, lam, norm_w=w, lambda_init=LI)
+        out = ops.paged_fwd(cache, q1, q2, lam, norm_w=w, lambda_init=LI, accumulate=True)
+        R.check(out, ref, tol, f"step {step}")
+        for b in range(B):
+            want = old[b] + add[b]
+            R.check(c.rows("weights", b), want,
+                    add_tol[b] + want * (H // kv * N + 2) * 2.0 ** -23, f"weights, step {step}")
+        if max(c.lens) > budget:
+            _check_evict(c, budget - 8, recent)
+    assert c.kv_len.tolist() != prompt
+
+
+def test_captured_step_replays_with_new_lengths():
+    """append, fwd with weights and evict in one CUDA graph, replayed while kv_len moves on."""
+    B, H, kv, d, page = 2, 4, 2, 64, 16
+    make = lambda: R.Cache(71, lens=[400, 400], kv=kv, d=d, page=page, weights=True, fill=0.0)
+    a, b = make(), make()
+    for c in (a, b):
+        c.kv_len.copy_(torch.tensor([100, 260], dtype=torch.int32))
+    q1, q2, lam, w = R.queries(72, B, H, 1, d)
+    g = torch.Generator().manual_seed(73)
+    steps = [[torch.randn(B, kv, 1, x, generator=g).to(torch.bfloat16).cuda() for x in (d, d, 2 * d)]
+             for _ in range(6)]
+    buf = [t.clone() for t in steps[0]]
+
+    def step(cache, kv_len, new):
+        kv_len.add_(1)
+        ops.paged_append(cache, *new)
+        out = ops.paged_fwd(cache, q1, q2, lam, norm_w=w, lambda_init=LI, accumulate=True)
+        ops.paged_evict(cache, keep=262, recent=10)
+        return out
+
+    ca, cb = a.ops_cache(), b.ops_cache()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    saved = {t: getattr(a, t).clone() for t in ("k1", "k2", "v", "weights", "kv_len")}
+    with torch.cuda.stream(side):
+        step(ca, a.kv_len, buf)  # warm-up on the capture stream
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(ca, a.kv_len, buf)
+    for t, x in saved.items():
+        getattr(a, t).copy_(x)
+    for new in steps:
+        for dst, src in zip(buf, new):
+            dst.copy_(src)
+        graph.replay()
+        want = step(cb, b.kv_len, new)
+        assert torch.equal(out, want)
+    for t in saved:
+        assert torch.equal(getattr(a, t), getattr(b, t)), t
+    assert b.kv_len.tolist() == [106, 262]
+
+
+def test_other_stream_and_two_at_once():
+    """Calls on a stream of their own, and two at once with a workspace each."""
+    c = R.Cache(81, lens=[3000, 500], kv=2, d=64, page=16)
+    cache = c.ops_cache()
+    q1, q2, lam, w = R.queries(82, 2, 4, 1, 64)
+    want = _fwd(c, q1, q2, lam, w)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    need = ops.paged_fwd_plan(cache, 4, 1)
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for k in range(20):
+        s = streams[k % 2]
+        outs.append(ops.paged_fwd(cache, q1, q2, lam, norm_w=w, lambda_init=LI, stream=s,
+                                  workspace=ws[k % 2] if k < 10 else None))
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, want)
+
+
+def test_empty_calls():
+    c = R.Cache(91, lens=[5], kv=2, d=64, page=16, weights=True)
+    cache = c.ops_cache()
+    q = torch.empty(1, 4, 0, 64, dtype=torch.bfloat16, device="cuda")
+    lam = torch.ones(4, device="cuda")
+    assert ops.paged_fwd(cache, q, q, lam).shape == (1, 4, 0, 128)
+    k = torch.empty(1, 2, 0, 64, dtype=torch.bfloat16, device="cuda")
+    ops.paged_append(cache, k, k, torch.empty(1, 2, 0, 128, dtype=torch.bfloat16, device="cuda"))
+    ops.paged_evict(cache, keep=16)
+    assert c.kv_len.tolist() == [5]
