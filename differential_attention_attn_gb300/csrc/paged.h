@@ -12,15 +12,15 @@ namespace diffattn {
 constexpr int kPageGrain = 16;  // page sizes are multiples of this many rows
 
 // Forward: keys are taken in tiles of kPagedTile; the rows (new token, query
-// head) of one key/value head in blocks of 8 * query_tiles(rows).
-constexpr int kPagedTile = 64;
+// head) of one key/value head in blocks of 8, 16 or 32.
+constexpr int kPagedTile = 128;
 constexpr int kPagedMaxTokens = 16;
 constexpr int kPagedMaxGroup = 64;
 
 struct PagedFwdPlan {
   int ctas;        // CTAs of the main kernel
   bool whole;      // one CTA per item (nothing to join); else equal shares of all tiles
-  int row_tiles;   // query tiles of 8 rows per block (1 or 2)
+  int row_tile;    // rows of a block
   int row_blocks;  // row blocks per key/value head
   int64_t items;   // B * kv_heads * row_blocks
   int64_t padded;  // keys per sequence in the logit buffer, a multiple of kPagedTile

@@ -11,32 +11,31 @@
 //   O = sum_s 2^(m_s - M) O_s,  l = sum_s 2^(m_s - M) l_s,  o = O / l.
 //
 // What bounds it: each key is read once (8 d bytes in bf16) for 12 d R
-// multiply-adds, so up to R = 16 and more this is HBM-bound; everything here
-// serves to keep loads in flight.
+// multiply-adds, so for the R <= 32 rows of a block this is HBM-bound, and
+// everything here serves to keep loads in flight.
 //
-//   - Work is counted in tiles of 64 keys over all sequences and heads, and
+//   - Work is counted in tiles of 128 keys over all sequences and heads, and
 //     every CTA (one per SM) takes the same number of consecutive tiles,
 //     found from kv_len on the device; a ragged batch is balanced and a graph
 //     replays with new lengths.  Items cut by a CTA boundary leave partial
 //     states, which a second kernel (launched dependent on the first) joins.
 //     With few tiles in all, one CTA takes each item and nothing is joined.
-//   - One warp issues TMA copies of page pieces (16, 32 or 64 rows, by the
-//     page size) into a ring of tile buffers of about 192 KB.
-//   - Eight warps compute: four per map.  S^T = K Q^T by mma.sync (m16n8k16)
-//     with the keys as the 16-row operand and 8 rows r as the 8-column one:
-//     tcgen05 needs 128 rows per product of which R would be used, while here
-//     nothing but the padding to 8 is lost and the tensor pipe stays far from
-//     its limit.  The four warps of a map take 16 keys each, exchange P
-//     through shared memory and then accumulate a quarter of O^T = V^T P^T.
-//   - The reference maximum moves only when some logit passes it by 2^8: one
-//     barrier with a vote per tile instead of a reduction.
-//   - P enters the second product as bf16 hi + lo (two products, relative
+//   - One warp issues TMA copies of page pieces (16 to 64 rows, by the page
+//     size) into a ring of 32 KB buffers: the keys of both maps (d = 64), one
+//     map's keys or half the value columns (d = 128).
+//   - One warp issues the products, keys and value columns on the 128-row side
+//     of tcgen05.mma, where the tile fills it, and the few rows r on the other:
+//       S_m^T = K_m Q_m^T            (128 keys x rows)
+//       O^T  += V^T [P1 | P2]^T      (128 value columns x rows of both maps)
+//     so V is read once for both maps and O stays in tensor memory.
+//   - Eight warps do the softmax, a thread per key and map.  The reference
+//     maximum moves only when some logit passes it by 2^8: one barrier with a
+//     vote per tile instead of a reduction over the keys.
+//   - P enters the second product as bf16 hi + lo side by side (relative
 //     error 2^-17): o1 - lambda o2 cancels and the head norm scales the
-//     difference back up, so a plain bf16 P would show; the second product is
+//     difference back up, so a plain bf16 P would show; the wider product is
 //     hidden behind the loads.
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -51,27 +50,18 @@ namespace diffattn {
 namespace {
 
 constexpr int kTile = kPagedTile;
-constexpr int kConsumers = 256;
-constexpr int kThreads = kConsumers + 32;
+constexpr int kConsumers = 256;  // softmax and epilogue threads
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = kConsumers + 64;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kGrowth = 8.f;  // log2 units a logit may pass the reference maximum by
-constexpr int kPStride = kTile + 8;  // bf16 elements of a row of P: 16-byte steps, no bank conflicts
-constexpr int kMinShare = 2;  // tiles
+constexpr int kMinShare = 1;    // tiles
+constexpr int kMaxBad = 16;     // new tokens of a call, so more than keys that only some of them see
+constexpr int kRing = 8;        // tile descriptors; at most 5 tiles are between load and epilogue
+constexpr int kBoxBytes = kTile * 128;   // 64 bf16 columns of a tile
+constexpr int kSlotBytes = 2 * kBoxBytes;
 constexpr float kLog2e = 1.4426950408889634f;
-
-template <int kD, bool kFp8>
-struct Geo {
-  static constexpr int kKeyRow = kFp8 ? kD : 2 * kD;               // bytes
-  static constexpr int kKeyBox = kKeyRow < 128 ? kKeyRow : 128;    // bytes of a TMA box row
-  static constexpr int kKeyBoxes = kKeyRow / kKeyBox;
-  static constexpr int kValBoxes = 4 * kD / 128;
-  static constexpr int kKeyBytes = kTile * kKeyRow;                // one map's keys of a tile
-  static constexpr int kValBytes = kTile * 4 * kD;
-  static constexpr int kStageBytes = 2 * kKeyBytes + kValBytes;
-  static constexpr int kStages = 196608 / kStageBytes;
-  static constexpr int kBoxesPerPiece = 2 * kKeyBoxes + kValBoxes;
-};
 
 enum : int32_t { kFirst = 1, kLast = 2, kStop = 4, kBad = 8, kDirect = 16 };
 
@@ -92,7 +82,7 @@ struct FwdParams {
   int32_t num_pages, max_pages, page_size, piece_rows;
   int32_t row_blocks, causal, headnorm, whole;
   float eps, out_scale, scale_log2;
-  // Workspace (see PagedFwdPlan): partial O [2 C][2][RPB][2 d], their (m, l), one join record per
+  // Workspace (see PagedFwdPlan): partial O [2 C][2][NQ][2 d], their (m, l), one join record per
   // CTA, and for accumulate one record per item, whole items' (m, l) and all logits.
   float *part;
   float2 *part_ml;
@@ -104,54 +94,55 @@ struct FwdParams {
   float *weights;
 };
 
-template <int kD, bool kFp8, int kNT>
-struct Smem {
-  using G = Geo<kD, kFp8>;
-  static constexpr int kRows = 8 * kNT;
-  __nv_bfloat16 p[2][2][kRows][kPStride];  // [map][hi, lo]
-  float obuf[kRows][2 * kD + 4];
-  float wmax[2][4][kRows];
-  float lsum[2][4][kRows];
-  float rsum[2][4][kRows];
-  uint64_t full[G::kStages], empty[G::kStages];
-  TileDesc ring[G::kStages];
-  unsigned long long bad_rows[3];
+// kNQ: rows of a block (8, 16 or 32).
+template <int kD, bool kFp8, int kNQ>
+struct Geo {
+  static constexpr int kKeyRow = kFp8 ? kD : 2 * kD;                // bytes
+  static constexpr int kKeyBox = kKeyRow < 128 ? kKeyRow : 128;     // bytes of a key box row
+  static constexpr int kKeySlots = kKeyRow <= 128 ? 1 : 2;          // both maps in one, or each its own
+  static constexpr int kValSlots = kD / 64;                         // 128 value columns each
+  static constexpr int kTileSlots = kKeySlots + kValSlots;
+  static constexpr int kNS = kNQ < 16 ? 16 : kNQ;                   // columns of S (N is at least 16)
+  static constexpr int kQBytes = kNS * kKeyRow;                     // one map's rows
+  static constexpr int kPRows = 4 * kNQ;                            // map 1 hi, lo, map 2 hi, lo
+  static constexpr int kPBytes = kPRows * 2 * kTile;
+  static constexpr int kPBufs = kNQ == 32 ? 1 : 2;
+  static constexpr int kOCols = kValSlots * kPRows;
+  static constexpr int kOBufs = kNQ == 32 && kD == 128 ? 1 : 2;
+  static constexpr int kTmemO = 4 * kNS;                            // after two buffers of two S
+  static constexpr int kTmemUsed = kTmemO + kOBufs * kOCols;
+  static constexpr int kTmemCols = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
+  static_assert(kTmemUsed <= 512, "tensor memory");
+};
+
+template <int kNQ>
+struct Ctrl {
+  float wmax[2][4][kNQ];
+  float lsum[2][4][kNQ];
+  float rsum[2][4][kNQ];
+  float late[2][kMaxBad][kNQ];  // logits of keys kept out of the product
+  TileDesc ring[kRing];
+  uint64_t full[6], empty[6];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_empty[2], drain;
+  uint32_t bad_rows[3];
+  uint32_t tmem;
   int abort, failed;
 };
 
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-// D += A B, A 16 x 16, B 16 x 8, fp32 accumulators.
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                        uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// Two e4m3 values (low half of x, or the high one) as f16x2; exact.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t x) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(x)));
-  return r;
-}
+template <int kD, bool kFp8, int kNQ>
+struct Layout {
+  using G = Geo<kD, kFp8, kNQ>;
+  static constexpr int kP = 0;
+  static constexpr int kQ = kP + G::kPBufs * G::kPBytes;
+  static constexpr int kFixed = kQ + 4 * G::kQBytes;  // then the ring, then Ctrl
+  static constexpr int kRoom =
+      227 * 1024 - 1024 - static_cast<int>(sizeof(Ctrl<kNQ>)) - kFixed;
+  static constexpr int kSlots = kRoom / kSlotBytes < 6 ? kRoom / kSlotBytes : 6;
+  static_assert(kSlots >= G::kTileSlots, "one tile must fit");
+  static constexpr int kRingAt = kFixed;
+  static constexpr int kCtrl = kRingAt + kSlots * kSlotBytes;
+  static constexpr int kBytes = 1024 + kCtrl + static_cast<int>(sizeof(Ctrl<kNQ>));
+};
 
 __device__ __forceinline__ int32_t units_of(int32_t len, int32_t most) {
   if (len <= 0 || len > most) return 1;  // an idle or invalid sequence still has rows to write
@@ -163,109 +154,185 @@ __device__ __forceinline__ int64_t warp_sum64(int64_t x) {
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
-
-__device__ __forceinline__ float group_sum(float x) {  // over the 8 lanes with the same lane % 4
-  x += __shfl_xor_sync(0xffffffffu, x, 4);
-  x += __shfl_xor_sync(0xffffffffu, x, 8);
-  x += __shfl_xor_sync(0xffffffffu, x, 16);
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
   return x;
 }
 
-// ---------------------------------------------------------------------------
-// The load warp: finds this CTA's tiles, describes them and issues their copies.
-// ---------------------------------------------------------------------------
-template <int kD, bool kFp8, int kNT>
-__device__ void load_warp(const FwdParams &p, const CUtensorMap *mk1, const CUtensorMap *mk2,
-                          const CUtensorMap *mv, uint8_t *stages, Smem<kD, kFp8, kNT> *sm) {
-  using G = Geo<kD, kFp8>;
+// Sixteen bytes from global to shared memory, asynchronously.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// One arrival on the barrier when this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void fence_async_proxy() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// tcgen05.mma of a converged warp (one elected lane issues).
+__device__ __forceinline__ void umma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Descriptor of K-major rows of 64 bytes with 64-byte swizzle (8-row groups 512 bytes apart).
+__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (1ull << 16) |
+         (static_cast<uint64_t>(512 >> 4) << 32) | (1ull << 46) | (4ull << 61);
+}
+
+template <int kN>
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[kN]) {
+  if constexpr (kN == 8)
+    tmem_ld_x8(addr, r);
+  else if constexpr (kN == 16)
+    tmem_ld_x16(addr, r);
+  else
+    tmem_ld_x32(addr, r);
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
+// Phase parity of the n-th use (from 0) of buffer n % kBufs.
+template <int kBufs>
+__device__ __forceinline__ uint32_t phase(uint32_t n) {
+  return (n / kBufs) & 1;
+}
+
+// The CTA's share of the tiles.
+struct Share {
+  int64_t todo, total, begin, ctas;
+  int32_t b, hk, rb, tile, len, units;
+};
+
+// Where this CTA's share begins: item (b, hk, rb) and tile within it (one warp, uniform).
+__device__ Share find_share(const FwdParams &p) {
   const int lane = threadIdx.x % 32;
   const int32_t most = p.max_pages * p.page_size;
-  const int64_t per_unit = static_cast<int64_t>(p.kv_heads) * p.row_blocks;  // items a sequence
-
-  // Where this CTA's share begins: item (b, hk, rb) and tile within it.
-  int64_t todo = 0, total = 0, begin = 0, ctas = 1;
-  int32_t b = 0, hk = 0, rb = 0, tile = 0, len = 0, units = 1;
+  Share s = {0, 0, 0, 1, 0, 0, 0, 0, 0, 1};
   if (p.whole) {
     const uint32_t item = blockIdx.x;
-    rb = static_cast<int32_t>(item % p.row_blocks);
-    hk = static_cast<int32_t>(item / p.row_blocks % p.kv_heads);
-    b = static_cast<int32_t>(item / p.row_blocks / p.kv_heads);
-    len = __ldg(p.kv_len + b);
-    units = units_of(len, most);
-    todo = units;
-  } else {
-    for (int32_t b0 = 0; b0 < p.B; b0 += 128) {
-      int32_t n[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int32_t x = b0 + 32 * k + lane;
-        n[k] = x < p.B ? units_of(__ldg(p.kv_len + x), most) : 0;
-      }
-      total += warp_sum64(static_cast<int64_t>(n[0]) + n[1] + n[2] + n[3]);
-    }
-    total *= per_unit;
-    // Every share has at least kMinShare tiles (the last CTAs may have none).
-    ctas = min(static_cast<int64_t>(gridDim.x), max(int64_t{1}, total / kMinShare));
-    if (blockIdx.x < ctas) {
-      begin = total * blockIdx.x / ctas;
-      todo = total * (blockIdx.x + 1) / ctas - begin;
-      int64_t left = begin;  // tiles before the share, counted down sequence by sequence
-      for (int32_t b0 = 0; b0 < p.B; b0 += 32) {
-        const int32_t x = b0 + lane;
-        const int64_t u = x < p.B ? units_of(__ldg(p.kv_len + x), most) * per_unit : 0;
-        int64_t incl = u;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += y;
-        }
-        const int64_t all = __shfl_sync(0xffffffffu, incl, 31);
-        if (left < all) {
-          const int at = __ffs(__ballot_sync(0xffffffffu, left < incl)) - 1;
-          b = b0 + at;
-          left -= __shfl_sync(0xffffffffu, incl - u, at);
-          break;
-        }
-        left -= all;
-      }
-      len = __ldg(p.kv_len + b);
-      units = units_of(len, most);
-      const int32_t item = static_cast<int32_t>(left / units);
-      tile = static_cast<int32_t>(left - static_cast<int64_t>(item) * units);
-      rb = item % p.row_blocks;
-      hk = item / p.row_blocks;
-    }
-    // The join record of an item that is cut: written by the CTA whose share
-    // begins where that of the CTA with the item's first tile ends.
-    if (lane == 0) {
-      int4 rec = make_int4(-1, 0, 0, 0);
-      if (tile > 0) {
-        const int64_t start = begin - tile;
-        const int64_t c0 = ((start + 1) * ctas - 1) / total;
-        if (begin == total * (c0 + 1) / ctas)
-          rec = make_int4((b * p.kv_heads + hk) * p.row_blocks + rb,
-                          static_cast<int>(2 * c0 + (total * c0 / ctas < start ? 1 : 0)),
-                          static_cast<int>(((start + units) * ctas - 1) / total - c0 + 1), 0);
-      }
-      p.records[blockIdx.x] = rec;
-    }
+    s.rb = static_cast<int32_t>(item % p.row_blocks);
+    s.hk = static_cast<int32_t>(item / p.row_blocks % p.kv_heads);
+    s.b = static_cast<int32_t>(item / p.row_blocks / p.kv_heads);
+    s.len = __ldg(p.kv_len + s.b);
+    s.units = units_of(s.len, most);
+    s.todo = s.units;
+    return s;
   }
+  const int64_t per_unit = static_cast<int64_t>(p.kv_heads) * p.row_blocks;  // items a sequence
+  for (int32_t b0 = 0; b0 < p.B; b0 += 128) {
+    int32_t n[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int32_t x = b0 + 32 * k + lane;
+      n[k] = x < p.B ? units_of(__ldg(p.kv_len + x), most) : 0;
+    }
+    s.total += warp_sum64(static_cast<int64_t>(n[0]) + n[1] + n[2] + n[3]);
+  }
+  s.total *= per_unit;
+  // Every share has at least kMinShare tiles (the last CTAs may have none).
+  s.ctas = min(static_cast<int64_t>(gridDim.x), max(int64_t{1}, s.total / kMinShare));
+  if (blockIdx.x < s.ctas) {
+    s.begin = s.total * blockIdx.x / s.ctas;
+    s.todo = s.total * (blockIdx.x + 1) / s.ctas - s.begin;
+    int64_t left = s.begin;  // tiles before the share, counted down sequence by sequence
+    for (int32_t b0 = 0; b0 < p.B; b0 += 32) {
+      const int32_t x = b0 + lane;
+      const int64_t u = x < p.B ? units_of(__ldg(p.kv_len + x), most) * per_unit : 0;
+      int64_t incl = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const int64_t all = __shfl_sync(0xffffffffu, incl, 31);
+      if (left < all) {
+        const int at = __ffs(__ballot_sync(0xffffffffu, left < incl)) - 1;
+        s.b = b0 + at;
+        left -= __shfl_sync(0xffffffffu, incl - u, at);
+        break;
+      }
+      left -= all;
+    }
+    s.len = __ldg(p.kv_len + s.b);
+    s.units = units_of(s.len, most);
+    const int32_t item = static_cast<int32_t>(left / s.units);
+    s.tile = static_cast<int32_t>(left - static_cast<int64_t>(item) * s.units);
+    s.rb = item % p.row_blocks;
+    s.hk = item / p.row_blocks;
+  }
+  // The join record of an item that is cut: written by the CTA whose share
+  // begins where that of the CTA with the item's first tile ends.
+  if (lane == 0) {
+    int4 rec = make_int4(-1, 0, 0, 0);
+    if (s.tile > 0) {
+      const int64_t start = s.begin - s.tile;
+      const int64_t c0 = ((start + 1) * s.ctas - 1) / s.total;
+      if (s.begin == s.total * (c0 + 1) / s.ctas)
+        rec = make_int4((s.b * p.kv_heads + s.hk) * p.row_blocks + s.rb,
+                        static_cast<int>(2 * c0 + (s.total * c0 / s.ctas < start ? 1 : 0)),
+                        static_cast<int>(((start + s.units) * s.ctas - 1) / s.total - c0 + 1), 0);
+    }
+    p.records[blockIdx.x] = rec;
+  }
+  return s;
+}
 
-  const int piece = lane / G::kBoxesPerPiece, box = lane % G::kBoxesPerPiece;
-  const int pieces = kTile / p.piece_rows;
+// ---------------------------------------------------------------------------
+// The load warp: describes the share's tiles and issues their copies.
+// ---------------------------------------------------------------------------
+template <int kD, bool kFp8, int kNQ>
+__device__ void load_warp(const FwdParams &p, const CUtensorMap *mk1, const CUtensorMap *mk2,
+                          const CUtensorMap *mv, uint8_t *smem, Ctrl<kNQ> *sm, const Share &share) {
+  using G = Geo<kD, kFp8, kNQ>;
+  using L = Layout<kD, kFp8, kNQ>;
+  const int lane = threadIdx.x % 32;
+  const int32_t most = p.max_pages * p.page_size;
+  int32_t b = share.b, hk = share.hk, rb = share.rb, tile = share.tile, len = share.len,
+          units = share.units;
+  // Each slot is two boxes wide and up to eight page pieces high: a lane each.
+  const int piece = lane / 2, box = lane % 2;
+  const bool piece_ok = piece < kTile / p.piece_rows;
+  const int first_row = piece * p.piece_rows;
   const auto page_of = [&](int32_t t) {  // this lane's page of tile t of the current sequence
-    const int32_t key = t * kTile + piece * p.piece_rows;
-    return piece < pieces && key < len && len <= most
+    const int32_t key = t * kTile + first_row;
+    return piece_ok && key < len && len <= most
                ? __ldg(p.page_table + static_cast<int64_t>(b) * p.max_pages + key / p.page_size)
                : 0;
   };
   bool ok = true;
-  uint32_t it = 0;
-  int32_t seg_start = tile;  // first tile of the current segment (the share's part of one item)
+  uint32_t c = 0;      // slots used
+  uint32_t it = 0;     // tiles
+  uint32_t seg = 0;    // segments (the share's parts of items)
+  int32_t seg_start = tile;
   int32_t slot = 2 * blockIdx.x;
-  int32_t id = todo > 0 ? page_of(tile) : 0;
-  for (int64_t left = todo; left > 0; --left, ++it) {
-    const int s = it % G::kStages;
+  int32_t id = share.todo > 0 ? page_of(tile) : 0;
+  for (int64_t left = share.todo; ok && left > 0; --left, ++it) {
     const bool valid_len = len >= 0 && len <= most;
     const bool seg_last = tile + 1 == units || left == 1;
     const int32_t page = id;
@@ -280,19 +347,22 @@ __device__ void load_warp(const FwdParams &p, const CUtensorMap *mk1, const CUte
               (seg_start == 0 && tile + 1 == units ? kDirect : 0);
     d.item = (b * p.kv_heads + hk) * p.row_blocks + rb;
     const int32_t keys = max(0, min(kTile, d.len - d.key0));  // 0 for an idle sequence
-    const bool have = piece < pieces && piece * p.piece_rows < keys;
+    const bool have = piece_ok && first_row < keys;
     const bool bad_id = have && static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages);
     const bool bad = __any_sync(0xffffffffu, bad_id) || !valid_len;
     if (bad) d.flags |= kBad;
     if (p.item_records != nullptr && lane == 0 && tile == 0) {
       int32_t n = 1;
       if (!p.whole) {
-        const int64_t start = begin + (todo - left);
-        n = static_cast<int32_t>(((start + units) * ctas - 1) / total - blockIdx.x + 1);
+        const int64_t start = share.begin + (share.todo - left);
+        n = static_cast<int32_t>(((start + units) * share.ctas - 1) / share.total - blockIdx.x + 1);
       }
       p.item_records[d.item] = make_int2(slot, n);
     }
-    // Move on; the next tile's page numbers are fetched while a buffer is awaited.
+    const int32_t row = (d.key0 + first_row) % p.page_size;
+    const int32_t z = bad_id ? 0 : page;
+    const int32_t rows = (keys + p.piece_rows - 1) / p.piece_rows * p.piece_rows;
+    // Move on; the next tile's page numbers are fetched while buffers are awaited.
     if (seg_last) {
       seg_start = 0;
       slot = 2 * blockIdx.x + 1;
@@ -312,538 +382,603 @@ __device__ void load_warp(const FwdParams &p, const CUtensorMap *mk1, const CUte
       }
     }
     if (left > 1) id = page_of(tile);
-    if (it >= G::kStages && !mbar_wait_warp(&sm->empty[s], (it / G::kStages - 1) & 1, &sm->abort,
-                                            kWaitNs)) {
-      ok = false;
-      break;
-    }
-    uint8_t *buf = stages + s * G::kStageBytes;
-    if (lane == 0) {
-      if (bad) report_bad_page(p.status);
-      sm->ring[s] = d;
-      const int32_t rows = (keys + p.piece_rows - 1) / p.piece_rows * p.piece_rows;
-      if (rows > 0)
-        mbar_arrive_expect_tx(&sm->full[s],
-                              static_cast<uint32_t>(rows) * (2 * G::kKeyRow + 4 * kD));
-      else
-        mbar_arrive(&sm->full[s]);
-    }
-    __syncwarp();
-    if (have) {
-      const int32_t row = (d.key0 + piece * p.piece_rows) % p.page_size;
-      const int32_t z = bad_id ? 0 : page;
-      constexpr int kKeyX = kFp8 ? G::kKeyBox : 64;  // elements of a key box
-      const int first_row = piece * p.piece_rows;
-      if (box < G::kKeyBoxes) {
-        tma_load_4d(buf + (box * kTile + first_row) * G::kKeyBox, mk1, &sm->full[s], box * kKeyX,
-                    row, d.hk, z);
-      } else if (box < 2 * G::kKeyBoxes) {
-        const int x = box - G::kKeyBoxes;
-        tma_load_4d(buf + G::kKeyBytes + (x * kTile + first_row) * G::kKeyBox, mk2, &sm->full[s],
-                    x * kKeyX, row, d.hk, z);
-      } else {
-        const int x = box - 2 * G::kKeyBoxes;
-        tma_load_4d(buf + 2 * G::kKeyBytes + (x * kTile + first_row) * 128, mv, &sm->full[s],
-                    x * 64, row, d.hk, z);
+#pragma unroll
+    for (int k = 0; k < G::kTileSlots; ++k, ++c) {
+      // The segment's q rows, between its first keys and values (the products may wait for them
+      // before they free a slot for the values): 16-byte units into the swizzled operand layout.
+      if (k == G::kKeySlots && (d.flags & kFirst)) {
+        const uint32_t qb = seg & 1;
+        if (seg >= 2 &&
+            !(ok = mbar_wait_warp(&sm->q_empty[qb], phase<2>(seg - 2), &sm->abort, kWaitNs)))
+          break;
+        constexpr int kUnits = G::kKeyRow / 16;
+        const int real = min(kNQ, p.rows - d.rb * kNQ);
+        for (int x = lane; x < 2 * real * kUnits; x += 32) {
+          const int map = x >= real * kUnits, y = x - map * real * kUnits;
+          const int q = y / kUnits, u = y % kUnits;
+          const int r = d.rb * kNQ + q;
+          const int i = r / p.group, h = d.hk * p.group + r - i * p.group;
+          const diffattn_strides &qs = map ? p.q2s : p.q1s;
+          const int64_t at = d.b * qs.b + h * qs.h + i * qs.n;
+          const uint8_t *src =
+              static_cast<const uint8_t *>(map ? p.q2 : p.q1) + at * (kFp8 ? 1 : 2) + 16 * u;
+          uint32_t off;
+          if (G::kKeyRow == 64)
+            off = q * 64 + ((u ^ ((q >> 1) & 3)) << 4);
+          else
+            off = (u / 8) * (G::kNS * 128) + q * 128 + (((u % 8) ^ (q & 7)) << 4);
+          cp_async16(smem_u32(smem + L::kQ + (2 * qb + map) * G::kQBytes) + off, src);
+        }
+        cp_async_arrive(&sm->q_full[qb]);
+        ++seg;
+      }
+      const int s = c % L::kSlots;
+      if (c >= L::kSlots &&
+          !(ok = mbar_wait_warp(&sm->empty[s], phase<L::kSlots>(c - L::kSlots), &sm->abort,
+                                kWaitNs)))
+        break;
+      const bool keys_slot = k < G::kKeySlots;
+      uint8_t *buf = smem + L::kRingAt + s * kSlotBytes + box * kBoxBytes;
+      if (lane == 0) {
+        if (k == 0) {
+          if (bad) report_bad_page(p.status);
+          sm->ring[it % kRing] = d;
+        }
+        if (rows > 0)
+          mbar_arrive_expect_tx(&sm->full[s], static_cast<uint32_t>(rows) * 2 *
+                                                  (keys_slot ? G::kKeyBox : 128));
+        else
+          mbar_arrive(&sm->full[s]);
+      }
+      __syncwarp();
+      if (have) {
+        const int map = G::kKeySlots == 1 ? box : k;
+        if (keys_slot)
+          tma_load_4d(buf + first_row * G::kKeyBox, map ? mk2 : mk1, &sm->full[s],
+                      G::kKeySlots == 1 ? 0 : 64 * box, row, d.hk, z);
+        else
+          tma_load_4d(buf + first_row * 128, mv, &sm->full[s],
+                      128 * (k - G::kKeySlots) + 64 * box, row, d.hk, z);
       }
     }
   }
-  // The end mark takes the next buffer's turn; then the copies still in flight
+  // The end mark takes the next slot's turn; then the copies still in flight
   // are awaited (bounded), so that none lands after the CTA is gone.
-  if (ok && (it < G::kStages || mbar_wait_warp(&sm->empty[it % G::kStages],
-                                               (it / G::kStages - 1) & 1, &sm->abort, kWaitNs))) {
+  if (ok && (c < L::kSlots || mbar_wait_warp(&sm->empty[c % L::kSlots],
+                                             phase<L::kSlots>(c - L::kSlots), &sm->abort, kWaitNs))) {
     if (lane == 0) {
-      sm->ring[it % G::kStages].flags = kStop;
-      mbar_arrive(&sm->full[it % G::kStages]);
+      sm->ring[it % kRing].flags = kStop;
+      mbar_arrive(&sm->full[c % L::kSlots]);
     }
-    ++it;
+    ++c;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   if (lane == 0) {
     volatile int never = 0;
-    for (uint32_t k = it > G::kStages ? it - G::kStages : 0; k < it; ++k)
-      mbar_wait(&sm->full[k % G::kStages], (k / G::kStages) & 1, &never, kDrainNs);
+    for (uint32_t k = c > L::kSlots ? c - L::kSlots : 0; k < c; ++k)
+      mbar_wait(&sm->full[k % L::kSlots], phase<L::kSlots>(k), &never, kDrainNs);
   }
 }
 
 // ---------------------------------------------------------------------------
-// The compute warps.  Warp w: map w & 1, quarter w >> 1 (of a tile's keys for
-// the first product, of the 2 d value columns for the second).
-// Accumulator fragments (16 x 8): lane = 4 g + t holds rows g, g + 8 and
-// columns 2 t, 2 t + 1; the rows are keys, then value columns, and the columns
-// always the queries 8 nt + 2 t + e of this row block.
+// The product warp.
 // ---------------------------------------------------------------------------
-template <int kD, bool kFp8, int kNT>
-__device__ void compute_warps(const FwdParams &p, uint8_t *stages, Smem<kD, kFp8, kNT> *sm) {
-  using G = Geo<kD, kFp8>;
-  constexpr int kRows = 8 * kNT;
-  constexpr int kSteps = kD / 16;   // of the first product's depth
-  constexpr int kMT = 2 * kD / 64;  // 16-column tiles of a warp's value quarter
+template <int kD, bool kFp8, int kNQ>
+__device__ void mma_warp(const FwdParams &p, uint8_t *smem, Ctrl<kNQ> *sm) {
+  using G = Geo<kD, kFp8, kNQ>;
+  using L = Layout<kD, kFp8, kNQ>;
+  const int lane = threadIdx.x % 32;
+  const uint32_t tmem = sm->tmem;
+  constexpr uint32_t kIdS = kFp8 ? (1u << 4) | ((G::kNS >> 3) << 17) | ((128u >> 4) << 24)
+                                 : idesc_bf16_f32(128, G::kNS, false);
+  constexpr uint32_t kIdO = idesc_bf16_f32(128, G::kPRows, false) | (1u << 15);  // A MN-major
+  const auto wait = [&](uint64_t *bar, uint32_t parity) {
+    return mbar_wait_warp(bar, parity, &sm->abort, kWaitNs);
+  };
+  const auto slot_at = [&](uint32_t c) {
+    return smem_u32(smem + L::kRingAt + (c % L::kSlots) * kSlotBytes);
+  };
+  uint32_t segs = 0;  // segments whose first tile's S has been issued
+
+  // S of tile t (its descriptor's flags are returned; -1 when a wait ran out).
+  const auto issue_s = [&](uint32_t t) -> int32_t {
+    const uint32_t c = t * G::kTileSlots;
+    if (!wait(&sm->full[c % L::kSlots], phase<L::kSlots>(c))) return -1;
+    const int32_t flags = *reinterpret_cast<volatile int32_t *>(&sm->ring[t % kRing].flags);
+    if (flags & kStop) {
+      if (lane == 0) mbar_arrive(&sm->s_full[t & 1]);
+      return flags;
+    }
+    if (flags & kFirst) {
+      if (!wait(&sm->q_full[segs & 1], phase<2>(segs))) return -1;
+      fence_async_proxy();  // the q rows came by ordinary copies
+      ++segs;
+    }
+    tc_fence_after_sync();
+    const uint32_t qb = (segs - 1) & 1;
+#pragma unroll
+    for (int map = 0; map < 2; ++map) {
+      if (map == 1 && G::kKeySlots == 2 &&
+          !wait(&sm->full[(c + 1) % L::kSlots], phase<L::kSlots>(c + 1)))
+        return -1;
+      const uint32_t k_at = slot_at(c + (G::kKeySlots == 2 ? map : 0)) +
+                            (G::kKeySlots == 1 ? map * kBoxBytes : 0);
+      const uint32_t q_at = smem_u32(smem + L::kQ + (2 * qb + map) * G::kQBytes);
+      const uint32_t acc = tmem + (t & 1) * 2 * G::kNS + map * G::kNS;
+#pragma unroll
+      for (int kk = 0; kk < G::kKeyRow / 32; ++kk) {  // 32 bytes of depth each
+        if (G::kKeyRow == 64) {
+          umma_e4m3(acc, smem_desc_sw64(k_at) + 2 * kk, smem_desc_sw64(q_at) + 2 * kk, kIdS, kk > 0);
+        } else {
+          const uint64_t a = smem_desc_sw128(k_at + (kk / 4) * kBoxBytes, 16, 1024) + 2 * (kk % 4);
+          const uint64_t q =
+              smem_desc_sw128(q_at + (kk / 4) * (G::kNS * 128), 16, 1024) + 2 * (kk % 4);
+          if (kFp8)
+            umma_e4m3(acc, a, q, kIdS, kk > 0);
+          else
+            umma_bf16(acc, a, q, kIdS, kk > 0);
+        }
+      }
+      if (G::kKeySlots == 2 || map == 1)
+        umma_commit_warp(&sm->empty[(c + (G::kKeySlots == 2 ? map : 0)) % L::kSlots]);
+    }
+    umma_commit_warp(&sm->s_full[t & 1]);
+    if (flags & kLast) umma_commit_warp(&sm->q_empty[qb]);
+    return flags;
+  };
+
+  uint32_t o_segs = 0;
+  int32_t flags = issue_s(0);
+  for (uint32_t t = 0; flags >= 0 && !(flags & kStop); ++t) {
+    // The next tile's S goes first where its keys are already there.
+    int32_t next = -2;
+    const auto next_ready = [&] {
+      const uint32_t c = (t + 1) * G::kTileSlots + G::kKeySlots - 1;
+      const uint32_t c0 = (t + 1) * G::kTileSlots;
+      return __all_sync(0xffffffffu, mbar_test(&sm->full[c0 % L::kSlots], phase<L::kSlots>(c0)) &&
+                                         mbar_test(&sm->full[c % L::kSlots], phase<L::kSlots>(c)));
+    };
+    if (next_ready()) next = issue_s(t + 1);
+    if (next == -1 || !wait(&sm->p_full[t & 1], phase<2>(t))) break;
+    if (next == -2 && next_ready() && (next = issue_s(t + 1)) == -1) break;
+    if (flags & kFirst) {
+      // O of the segment before last (this buffer) has been read.
+      if (o_segs >= G::kOBufs && !wait(&sm->o_empty[o_segs % G::kOBufs],
+                                       phase<G::kOBufs>(o_segs - G::kOBufs)))
+        break;
+      ++o_segs;
+    }
+    tc_fence_after_sync();
+    const uint32_t o_at = tmem + G::kTmemO + ((o_segs - 1) % G::kOBufs) * G::kOCols;
+    const uint32_t p_at = smem_u32(smem + L::kP + (t % G::kPBufs) * G::kPBytes);
+    bool ok = true;
+#pragma unroll
+    for (int k = 0; k < G::kValSlots; ++k) {
+      const uint32_t c = t * G::kTileSlots + G::kKeySlots + k;
+      if (!(ok = wait(&sm->full[c % L::kSlots], phase<L::kSlots>(c)))) break;
+      tc_fence_after_sync();
+      const uint64_t v = smem_desc_sw128(slot_at(c), kBoxBytes, 1024);
+#pragma unroll
+      for (int kk = 0; kk < kTile / 16; ++kk) {
+        const uint64_t w = smem_desc_sw128(p_at + (kk / 4) * (G::kPRows * 128), 16, 1024) + 2 * (kk % 4);
+        umma_bf16(o_at + k * G::kPRows, v + 128 * kk, w, kIdO, !(flags & kFirst) || kk > 0);
+      }
+      umma_commit_warp(&sm->empty[c % L::kSlots]);
+    }
+    if (!ok) break;
+    umma_commit_warp(&sm->pv_done[t & 1]);
+    flags = next == -2 ? issue_s(t + 1) : next;
+  }
+  // Never free tensor memory under a running product.
+  umma_commit_warp(&sm->drain);
+  volatile int never = 0;
+  mbar_wait_warp(&sm->drain, 0, &never, kDrainNs);
+}
+
+// ---------------------------------------------------------------------------
+// The softmax warps.  Warp w: map w / 4; its lanes are keys (then value
+// columns) 32 (w % 4) + lane of a tile, as tensor memory gives them to it.
+// ---------------------------------------------------------------------------
+template <int kD, bool kFp8, int kNQ>
+__device__ void softmax_warps(const FwdParams &p, uint8_t *smem, Ctrl<kNQ> *sm) {
+  using G = Geo<kD, kFp8, kNQ>;
+  using L = Layout<kD, kFp8, kNQ>;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int map = warp & 1, quarter = warp >> 1;
-  const int g = lane / 4, t = lane % 4;
+  const int map = warp / 4, quarter = warp % 4;
+  const int key = 32 * quarter + lane;  // of the tile
+  const uint32_t tmem = sm->tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+  // This thread's column of P: row q of it is at + q * 128 (hi), + kNQ * 128 more (lo).
+  const uint32_t p_col = (key / 64) * (G::kPRows * 128) + map * (2 * kNQ * 128) + (key % 8) * 2;
+  const uint32_t p_unit = (key % 64) / 8;
+  const auto v_row = [&](uint32_t t, int row, int u) {  // unit u of value row `row` of tile t
+    const uint32_t c = t * G::kTileSlots + G::kKeySlots + u / 16;
+    return reinterpret_cast<uint4 *>(smem + L::kRingAt + (c % L::kSlots) * kSlotBytes +
+                                     ((u / 8) % 2) * kBoxBytes + row * 128 + (u % 8) * 16);
+  };
 
-  uint32_t q[kSteps][kNT][2];
-  float o[kMT][kNT][4];
-  float m[kNT][2], l[kNT][2];
-  int32_t lim[kNT][2];  // last key that a row sees, -1 for none
+  float m[kNQ], l[kNQ];
   bool poisoned = false;
-
-  for (uint32_t it = 0;; ++it) {
-    const int s = it % G::kStages;
-    const bool ok = mbar_wait_warp(&sm->full[s], (it / G::kStages) & 1, &sm->abort, kWaitNs);
+  uint32_t late = 0, seg = 0;
+  for (uint32_t t = 0;; ++t) {
+    bool ok = mbar_wait_warp(&sm->s_full[t & 1], phase<2>(t), &sm->abort, kWaitNs);
     TileDesc d = {};
-    if (ok) d = sm->ring[s];
+    if (ok) d = sm->ring[t % kRing];
     const bool stop = !ok || (d.flags & kStop) != 0;
-    uint8_t *buf = stages + s * G::kStageBytes;
     const int32_t lim_min = p.causal ? d.len - p.N : d.len - 1;  // of a row that sees anything
     const bool masked = d.key0 + kTile - 1 > lim_min;
     const int32_t keys = d.len - d.key0;  // valid rows of the tile if below kTile
     const bool mixed = p.causal && p.N > 1 && masked;  // some rows see keys that others do not
-
-    if (!stop && (d.flags & kFirst)) {
-      poisoned = false;
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = d.rb * kRows + 8 * nt + 2 * t + e;
-          const int i = r / p.group;
-          const int32_t pos = d.len - p.N + i;
-          lim[nt][e] = r >= p.rows || pos < 0 ? -1 : p.causal ? pos : d.len - 1;
-          m[nt][e] = -INFINITY;
-          l[nt][e] = 0.f;
-        }
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) o[mt][nt][c] = 0.f;
-        // B fragments of q: lane (g, t) holds columns (queries) g, depth 2 t, 2 t + 1, + 8 (e4m3:
-        // the four bytes 4 t .. 4 t + 3, the order in which the keys' bytes are taken below).
-        const int r = d.rb * kRows + 8 * nt + g;
-        const bool real = r < p.rows;
-        const int i = real ? r / p.group : 0;
-        const int h = d.hk * p.group + (real ? r - i * p.group : 0);
-        const diffattn_strides &qs = map ? p.q2s : p.q1s;
-        const int64_t at = d.b * qs.b + h * qs.h + i * qs.n;
-        const uint8_t *src = static_cast<const uint8_t *>(map ? p.q2 : p.q1) +
-                             at * (kFp8 ? 1 : 2);
-#pragma unroll
-        for (int ks = 0; ks < kSteps; ++ks) {
-          if (kFp8) {
-            const uint32_t x =
-                real ? __ldg(reinterpret_cast<const uint32_t *>(src + 16 * ks + 4 * t)) : 0u;
-            q[ks][nt][0] = e4m3_pair(x);
-            q[ks][nt][1] = e4m3_pair(x >> 16);
-          } else {
-            q[ks][nt][0] =
-                real ? __ldg(reinterpret_cast<const uint32_t *>(src + 32 * ks + 4 * t)) : 0u;
-            q[ks][nt][1] =
-                real ? __ldg(reinterpret_cast<const uint32_t *>(src + 32 * ks + 4 * t + 16)) : 0u;
-          }
-        }
-      }
-    }
-    if (d.flags & kBad) poisoned = true;
-
-    // Rows of v behind the sequence's end hold anything (NaN too): zero them, as 0 * NaN would
-    // reach every row.  Where new tokens see different keys, a non-finite v row that only some of
-    // them see is noted, to be kept out of the product.
-    if (threadIdx.x == 0) sm->bad_rows[(it + 1) % 3] = 0;
-    if (!stop && keys < kTile) {
-      const int from = max(0, keys);
-      for (int c = threadIdx.x; c < (kTile - from) * (kD / 4); c += kConsumers) {
-        const int row = from + c / (kD / 4), u = c % (kD / 4);
-        *reinterpret_cast<uint4 *>(buf + 2 * G::kKeyBytes + ((u / 8) * kTile + row) * 128 +
-                                   (u % 8) * 16) = make_uint4(0, 0, 0, 0);
-      }
-    }
-    if (!stop && mixed) {
-      const int from = max(0, lim_min + 1 - d.key0), to = min(kTile, keys);
-      for (int c = threadIdx.x; c < (to - from) * (kD / 4); c += kConsumers) {
-        const int row = from + c / (kD / 4), u = c % (kD / 4);
-        const uint4 x = *reinterpret_cast<const uint4 *>(
-            buf + 2 * G::kKeyBytes + ((u / 8) * kTile + row) * 128 + (u % 8) * 16);
-        bool bad = false;
-        for (const uint32_t w : {x.x, x.y, x.z, x.w})
-          bad |= (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-        if (bad) atomicOr(&sm->bad_rows[it % 3], 1ull << row);
-      }
-    }
-
-    // S^T = K Q^T of this warp's 16 keys, in log2 units.
-    float x[kNT][4];
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) x[nt][c] = 0.f;
+    const int real = min(kNQ, p.rows - d.rb * kNQ);    // rows of this block
+    float x[kNQ];
     bool grew = false;
+    if (threadIdx.x == 0) sm->bad_rows[(t + 1) % 3] = 0;
     if (!stop) {
-      const uint32_t keys_at = smem_u32(buf + map * G::kKeyBytes);
-      const int row = 16 * quarter + (lane & 15);
-      if (!kFp8) {
+      if (d.flags & kFirst) {
+        poisoned = false;
+        late = 0;
 #pragma unroll
-        for (int ks = 0; ks < kSteps; ++ks) {
-          const int unit = 2 * (ks % 4) + (lane >> 4);
-          uint32_t a[4];
-          ldsm4(a, keys_at + ((ks / 4) * kTile + row) * 128 + ((unit ^ (row & 7)) << 4));
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) mma_bf16(x[nt], a, q[ks][nt][0], q[ks][nt][1]);
-        }
-      } else {
-#pragma unroll
-        for (int kp = 0; kp < kSteps / 2; ++kp) {
-          const int unit = 2 * kp + (lane >> 4);
-          const int swz = G::kKeyBox == 64 ? (row >> 1) & 3 : row & 7;
-          uint32_t w[4];
-          ldsm4(w, keys_at + row * G::kKeyBox + ((unit ^ swz) << 4));
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t a[4] = {e4m3_pair(w[2 * k]), e4m3_pair(w[2 * k + 1]),
-                                   e4m3_pair(w[2 * k] >> 16), e4m3_pair(w[2 * k + 1] >> 16)};
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
-              mma_f16(x[nt], a, q[2 * kp + k][nt][0], q[2 * kp + k][nt][1]);
-          }
+        for (int q = 0; q < kNQ; ++q) {
+          m[q] = -INFINITY;
+          l[q] = 0.f;
         }
       }
-      const int32_t j = d.key0 + 16 * quarter + g;
+      if (d.flags & kBad) poisoned = true;
+      tc_fence_after_sync();
+      uint32_t raw[kNQ];
+      tmem_load(tmem + (t & 1) * 2 * G::kNS + map * G::kNS, raw);
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
+      for (int q = 0; q < kNQ; ++q) x[q] = __uint_as_float(raw[q]) * p.scale_log2;
+      if (masked) {
+        // Row r sees keys up to its own position (causal) or all; padding rows see none.
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          x[nt][c] *= p.scale_log2;
-          if (masked && j + 8 * (c >> 1) > lim[nt][c & 1]) x[nt][c] = -INFINITY;
-          grew |= x[nt][c] > m[nt][c & 1] + kGrowth;
+        for (int q = 0; q < kNQ; ++q) {
+          if (q >= real) break;
+          const int32_t pos = d.len - p.N + (d.rb * kNQ + q) / p.group;
+          const int32_t lim = pos < 0 ? -1 : p.causal ? pos : d.len - 1;
+          if (d.key0 + key > lim) x[q] = -INFINITY;
         }
-      if (p.logits != nullptr) {
-        float *dst = p.logits + (static_cast<int64_t>(d.b) * p.kv_heads + d.hk) * 2 * p.rows * p.padded;
+      }
+      if (p.logits != nullptr && key < keys) {
+        float *dst = p.logits +
+                     ((static_cast<int64_t>(d.b) * p.kv_heads + d.hk) * 2 + map) * p.rows * p.padded +
+                     static_cast<int64_t>(d.rb) * kNQ * p.padded + d.key0 + key;
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
+        for (int q = 0; q < kNQ; ++q) {
+          if (q >= real) break;
+          if (dbg_ok(d.key0 + key < p.padded, p.status, 41)) dst[q * p.padded] = x[q];
+        }
+      }
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int r = d.rb * kRows + 8 * nt + 2 * t + (c & 1);
-            const int32_t key = j + 8 * (c >> 1);
-            if (r < p.rows && key < d.len &&
-                dbg_ok(key < p.padded, p.status, 41))
-              dst[(static_cast<int64_t>(map) * p.rows + r) * p.padded + key] = x[nt][c];
+      for (int q = 0; q < kNQ; ++q) {
+        if (q >= real) break;
+        grew |= x[q] > m[q] + kGrowth;
+      }
+      // P's buffer: the product that read it last is done.
+      if (t >= G::kPBufs)
+        ok = mbar_wait_warp(&sm->pv_done[(t - G::kPBufs) & 1], phase<2>(t - G::kPBufs), &sm->abort,
+                            kWaitNs);
+      // Rows of v behind the sequence's end hold anything (NaN too): zero them, as 0 * NaN would
+      // reach every row.  Where new tokens see different keys, a non-finite v row that only some
+      // of them see is noted, to be kept out of the product.
+      if (ok && (keys < kTile || mixed)) {
+#pragma unroll
+        for (int k = 0; k < G::kValSlots; ++k) {
+          const uint32_t c = t * G::kTileSlots + G::kKeySlots + k;
+          ok = ok && mbar_wait_warp(&sm->full[c % L::kSlots], phase<L::kSlots>(c), &sm->abort,
+                                    kWaitNs);
+        }
+        if (ok) {
+          constexpr int kUnits = kD / 4;
+          const int from = max(0, keys);
+          for (int k = threadIdx.x; k < (kTile - from) * kUnits; k += kConsumers)
+            *v_row(t, from + k / kUnits, k % kUnits) = make_uint4(0, 0, 0, 0);
+          if (mixed) {
+            const int lo = max(0, lim_min + 1 - d.key0), hi = min(kTile, keys);
+            for (int k = threadIdx.x; k < (hi - lo) * kUnits; k += kConsumers) {
+              const uint4 y = *v_row(t, lo + k / kUnits, k % kUnits);
+              bool bad = false;
+              for (const uint32_t w : {y.x, y.y, y.z, y.w})
+                bad |= (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+              if (bad) atomicOr(&sm->bad_rows[t % 3], 1u << (d.len - 1 - d.key0 - lo - k / kUnits));
+            }
           }
+        }
       }
     }
     if (!ok) *reinterpret_cast<volatile int *>(&sm->failed) = 1;
 
     // One barrier and vote of all eight warps: has a logit outgrown its reference (or did a wait
-    // run out)?  It also orders the zeroed rows, and last tile's P, before what follows.
+    // run out)?
     if (named_barrier_or(1, kConsumers, grew || !ok)) {
       if (*reinterpret_cast<volatile int *>(&sm->failed)) break;
-      float w[kNT][2];
+      if (!stop) {
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float y = fmaxf(x[nt][e], x[nt][e + 2]);
-          if (stop) y = -INFINITY;
-          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
-          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
-          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-          w[nt][e] = y;
-          if (g == 0) sm->wmax[map][quarter][8 * nt + 2 * t + e] = y;
+        for (int q = 0; q < kNQ; ++q) {
+          if (q >= real) break;
+          const float y = warp_max(x[q]);
+          if (lane == 0) sm->wmax[map][quarter][q] = y;
         }
-      named_barrier_sync(2, kConsumers);
+        // O moves with the reference, so the product before must be done.
+        if (!(d.flags & kFirst))
+          ok = mbar_wait_warp(&sm->pv_done[(t - 1) & 1], phase<2>(t - 1), &sm->abort, kWaitNs);
+      }
+      if (named_barrier_or(2, kConsumers, !ok)) break;
+      if (!stop) {
+        const uint32_t o_at = tmem + G::kTmemO + (seg % G::kOBufs) * G::kOCols + map * 2 * kNQ;
+        tc_fence_after_sync();
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
+        for (int q8 = 0; q8 < kNQ; q8 += 8) {
+          if (q8 >= real) break;
+          float f[8];
+          bool moved = false;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float n = m[nt][e];
+          for (int k = 0; k < 8; ++k) {
+            const int q = q8 + k;
+            f[k] = 1.f;
+            if (q < real) {
+              float y = m[q];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) n = fmaxf(n, sm->wmax[map][k][8 * nt + 2 * t + e]);
-          const float f = n == m[nt][e] ? 1.f : ex2_approx(m[nt][e] - n);
-          m[nt][e] = n;
-          l[nt][e] *= f;
+              for (int w = 0; w < 4; ++w) y = fmaxf(y, sm->wmax[map][w][q]);
+              if (y != m[q]) {
+                f[k] = ex2_approx(m[q] - y);
+                moved = true;
+              }
+              m[q] = y;
+              l[q] *= f[k];
+            }
+          }
+          if (moved && !(d.flags & kFirst)) {  // the same decision in every thread of the map
 #pragma unroll
-          for (int mt = 0; mt < kMT; ++mt) {
-            o[mt][nt][e] *= f;
-            o[mt][nt][e + 2] *= f;
+            for (int part = 0; part < 2 * G::kValSlots; ++part) {
+              const uint32_t at = o_at + (part / 2) * G::kPRows + (part % 2) * kNQ + q8;
+              uint32_t y[8];
+              tmem_ld_x8(at, y);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f[k]);
+              tmem_st_x8(at, y);
+            }
           }
         }
+        tmem_st_wait();
+      }
     }
     if (stop) break;
 
     // Rows of v to keep out of the product (rare): zero them in the buffer as well.
-    const unsigned long long bad_rows = mixed ? sm->bad_rows[it % 3] : 0ull;
+    const uint32_t bad_rows = mixed ? sm->bad_rows[t % 3] : 0u;
     if (bad_rows) {
-      for (int c = threadIdx.x; c < kTile * (kD / 4); c += kConsumers) {
-        const int row = c / (kD / 4), u = c % (kD / 4);
-        if ((bad_rows >> row) & 1)
-          *reinterpret_cast<uint4 *>(buf + 2 * G::kKeyBytes + ((u / 8) * kTile + row) * 128 +
-                                     (u % 8) * 16) = make_uint4(0, 0, 0, 0);
+      late |= bad_rows;
+      constexpr int kUnits = kD / 4;
+      for (int k = threadIdx.x; k < kTile * kUnits; k += kConsumers) {
+        const int back = d.len - 1 - d.key0 - k / kUnits;
+        if (back >= 0 && back < kMaxBad && ((bad_rows >> back) & 1))
+          *v_row(t, k / kUnits, k % kUnits) = make_uint4(0, 0, 0, 0);
       }
-      named_barrier_sync(2, kConsumers);
+      const int back = d.len - 1 - d.key0 - key;
+      if (back >= 0 && back < kMaxBad && ((bad_rows >> back) & 1)) {
+#pragma unroll
+        for (int q = 0; q < kNQ; ++q) sm->late[map][back][q] = x[q];
+      }
     }
 
-    // P = 2^(x - m), into shared memory as bf16 hi + lo, [query][key].
+    // P = 2^(x - m) as bf16 hi + lo.
+    uint8_t *p_at = smem + L::kP + (t % G::kPBufs) * G::kPBytes + p_col;
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int e = c & 1, key = 16 * quarter + g + 8 * (c >> 1);
-        float y = ex2_approx(x[nt][c] - m[nt][e]);
-        if (masked && d.key0 + key > lim[nt][e]) y = 0.f;
-        l[nt][e] += y;
-        const __nv_bfloat16 hi = __float2bfloat16_rn(y);
-        sm->p[map][0][8 * nt + 2 * t + e][key] = hi;
-        sm->p[map][1][8 * nt + 2 * t + e][key] = __float2bfloat16_rn(y - __bfloat162float(hi));
-      }
-    named_barrier_sync(3 + map, kConsumers / 2);
-
-    // O^T += V^T P^T over the tile's 64 keys, this warp's quarter of the columns.
-    const uint32_t v_at = smem_u32(buf + 2 * G::kKeyBytes);
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {  // 32 keys
-      uint32_t ph[kNT][4], pl[kNT][4];
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-        const int row = 8 * nt + (lane & 7), unit = 4 * half + (lane >> 3);
-        ldsm4(ph[nt], smem_u32(&sm->p[map][0][row][8 * unit]));
-        ldsm4(pl[nt], smem_u32(&sm->p[map][1][row][8 * unit]));
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {  // 16 keys
-        const int row = 32 * half + 16 * k + (lane & 7) + ((lane >> 4) << 3);
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-          const int unit = (quarter * kMT + mt) * 2 + ((lane >> 3) & 1);  // of 8 columns
-          uint32_t a[4];
-          ldsm4_t(a, v_at + ((unit / 8) * kTile + row) * 128 + (((unit % 8) ^ (row & 7)) << 4));
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) {
-            mma_bf16(o[mt][nt], a, ph[nt][2 * k], ph[nt][2 * k + 1]);
-            mma_bf16(o[mt][nt], a, pl[nt][2 * k], pl[nt][2 * k + 1]);
-          }
-        }
-      }
+    for (int q = 0; q < kNQ; ++q) {
+      if (q >= real) break;
+      float y = ex2_approx(x[q] - m[q]);
+      if (masked && x[q] == -INFINITY) y = 0.f;  // also where no key has been seen yet
+      l[q] += y;
+      const __nv_bfloat16 hi = __float2bfloat16_rn(y);
+      uint8_t *at = p_at + q * 128 + ((p_unit ^ (q & 7)) << 4);
+      *reinterpret_cast<__nv_bfloat16 *>(at) = hi;
+      *reinterpret_cast<__nv_bfloat16 *>(at + kNQ * 128) =
+          __float2bfloat16_rn(y - __bfloat162float(hi));
     }
-    if (bad_rows) {  // the kept-out rows, for the queries that do see them
-      for (int row = 0; row < kTile; ++row) {
-        if (!((bad_rows >> row) & 1)) continue;
-        const int32_t key = d.key0 + row;
-        const int32_t page =
-            p.page_table[static_cast<int64_t>(d.b) * p.max_pages + key / p.page_size];
-        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) continue;
-        const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.v_pages) +
-                                 page * p.vs.b + d.hk * p.vs.h +
-                                 (key % p.page_size) * p.vs.n;
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (key > lim[nt][e]) continue;
-            const int r = 8 * nt + 2 * t + e;
-            const float y = __bfloat162float(sm->p[map][0][r][row]) +
-                            __bfloat162float(sm->p[map][1][r][row]);
-#pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) {
-              const int col = (quarter * kMT + mt) * 16 + g;
-              o[mt][nt][e] += y * __bfloat162float(v[col]);
-              o[mt][nt][e + 2] += y * __bfloat162float(v[col + 8]);
-            }
-          }
-      }
-    }
-    if (keys < kTile || bad_rows)  // ordinary stores before the next copy into this buffer
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    fence_async_proxy();
+    tc_fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sm->empty[s]);
+    if (lane == 0) mbar_arrive(&sm->p_full[t & 1]);
     if (!(d.flags & kLast)) continue;
 
     // ---- end of the segment ----
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float y = group_sum(l[nt][e]);
-        if (g == 0) sm->lsum[map][quarter][8 * nt + 2 * t + e] = y;
-      }
-    named_barrier_sync(2, kConsumers);
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float y = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) y += sm->lsum[map][k][8 * nt + 2 * t + e];
-        l[nt][e] = poisoned ? NAN : y;
-      }
+    for (int q = 0; q < kNQ; ++q) {
+      if (q >= real) break;
+      const float y = warp_sum(l[q]);
+      if (lane == 0) sm->lsum[map][quarter][q] = poisoned ? NAN : y;
+    }
+    ok = mbar_wait_warp(&sm->pv_done[t & 1], phase<2>(t), &sm->abort, kWaitNs);
+    if (named_barrier_or(2, kConsumers, !ok)) break;
+    tc_fence_after_sync();
+    const auto l_of = [&](int mp, int q) {
+      return (sm->lsum[mp][0][q] + sm->lsum[mp][1][q]) + (sm->lsum[mp][2][q] + sm->lsum[mp][3][q]);
+    };
     const bool direct = (d.flags & kDirect) != 0;
     // The row's (m, l): per slot for the join, per item for the weights.
-    if (quarter == 0 && g == 0 && (!direct || p.item_ml != nullptr)) {
-      float2 *ml = direct ? p.item_ml + static_cast<int64_t>(d.item) * 2 * kRows
-                          : p.part_ml + static_cast<int64_t>(d.slot) * 2 * kRows;
+    if (quarter == 0 && lane == 0 && (!direct || p.item_ml != nullptr)) {
+      float2 *ml = (direct ? p.item_ml + static_cast<int64_t>(d.item) * 2 * kNQ
+                           : p.part_ml + static_cast<int64_t>(d.slot) * 2 * kNQ) +
+                   map * kNQ;
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          ml[map * kRows + 8 * nt + 2 * t + e] = make_float2(m[nt][e], l[nt][e]);
+      for (int q = 0; q < kNQ; ++q) {
+        if (q >= real) break;
+        ml[q] = make_float2(m[q], l_of(map, q));
+      }
     }
-    if (!direct) {
-      float *dst = p.part + (static_cast<int64_t>(d.slot) * 2 + map) * kRows * (2 * kD);
+    // References of both maps for the kept-out keys.
+    if (late && lane == 0 && quarter == 0) {
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
+      for (int q = 0; q < kNQ; ++q) sm->wmax[map][0][q] = m[q];
+    }
+    if (late) named_barrier_sync(2, kConsumers);
+    // d = 64: the two halves of the warps take turns at eight rows; d = 128: each has its half of
+    // the value columns for all rows.
+    const int half = warp / 4;
+    const int block = kD == 128 ? half : 0;
+    const int col = 128 * block + key;
+    const uint32_t o_at = tmem + G::kTmemO + (seg % G::kOBufs) * G::kOCols + block * G::kPRows;
+    float o[kNQ <= 8 || kD == 128 ? kNQ : kNQ / 2];
+    constexpr int kChunks = kNQ / 8;
+    constexpr int kStep = kD == 128 || kChunks == 1 ? 1 : 2;  // chunks per pass of the loop
+    const bool idle = kD == 64 && kChunks == 1 && half == 1;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int r = 8 * nt + 2 * t + (c & 1);
-          if (d.rb * kRows + r >= p.rows) continue;
-          if (!dbg_ok(d.slot >= 0 && d.slot < 2 * static_cast<int>(gridDim.x), p.status, 42))
-            continue;
+    for (int k = 0; k < kChunks / kStep; ++k) {
+      const int q8 = 8 * (kStep * k + (kStep == 2 ? half : 0));
+      if (idle || q8 >= real) break;
+      uint32_t o1[2][8], o2[2][8];
+      tmem_ld_x8(o_at + q8, o1[0]);
+      tmem_ld_x8(o_at + kNQ + q8, o1[1]);
+      tmem_ld_x8(o_at + 2 * kNQ + q8, o2[0]);
+      tmem_ld_x8(o_at + 3 * kNQ + q8, o2[1]);
 #pragma unroll
-          for (int mt = 0; mt < kMT; ++mt)
-            dst[r * (2 * kD) + (quarter * kMT + mt) * 16 + g + 8 * (c >> 1)] = o[mt][nt][c];
+      for (int e = 0; e < 8; ++e) {
+        const int q = q8 + e;
+        if (q >= real) break;
+        float y1 = __uint_as_float(o1[0][e]) + __uint_as_float(o1[1][e]);
+        float y2 = __uint_as_float(o2[0][e]) + __uint_as_float(o2[1][e]);
+        for (uint32_t rest = late; rest; rest &= rest - 1) {
+          const int back = __ffs(rest) - 1;
+          const int32_t pos = d.len - 1 - back;
+          const int32_t page =
+              p.page_table[static_cast<int64_t>(d.b) * p.max_pages + pos / p.page_size];
+          if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) continue;
+          const float v = __bfloat162float(
+              static_cast<const __nv_bfloat16 *>(p.v_pages)[page * p.vs.b + d.hk * p.vs.h +
+                                                            pos % p.page_size * p.vs.n + col]);
+          const float x1 = sm->late[0][back][q], x2 = sm->late[1][back][q];
+          if (x1 != -INFINITY) y1 += ex2_approx(x1 - sm->wmax[0][0][q]) * v;
+          if (x2 != -INFINITY) y2 += ex2_approx(x2 - sm->wmax[1][0][q]) * v;
         }
-      continue;
-    }
-    // Whole item: map 2's warps hand over -lambda o2, map 1's form o, its norm and the output.
-    if (map == 1) {
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = d.rb * kRows + 8 * nt + 2 * t + e;
-          if (r >= p.rows) continue;
-          const float f = -__ldg(p.lambda + d.hk * p.group + r % p.group) / l[nt][e];
-#pragma unroll
-          for (int mt = 0; mt < kMT; ++mt) {
-            const int col = (quarter * kMT + mt) * 16 + g;
-            sm->obuf[8 * nt + 2 * t + e][col] = f * o[mt][nt][e];
-            sm->obuf[8 * nt + 2 * t + e][col + 8] = f * o[mt][nt][e + 2];
-          }
-        }
-    }
-    named_barrier_sync(2, kConsumers);
-    if (map == 1) continue;
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const bool real = d.rb * kRows + 8 * nt + 2 * t + e < p.rows;
-        const float f = 1.f / l[nt][e];
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-          const int col = (quarter * kMT + mt) * 16 + g;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float &y = o[mt][nt][e + 2 * k];
-            y = real ? fmaf(f, y, sm->obuf[8 * nt + 2 * t + e][col + 8 * k]) : 0.f;
-            if (lim[nt][e] < 0 && !poisoned) y = 0.f;  // a row that sees no key
-          }
+        const int r = d.rb * kNQ + q;
+        if (direct) {
+          const float lam = __ldg(p.lambda + d.hk * p.group + r % p.group);
+          float y = y1 / l_of(0, q) - lam * (y2 / l_of(1, q));
+          if (d.len - p.N + r / p.group < 0 && !poisoned) y = 0.f;  // a row that sees no key
+          o[8 * k + e] = y;
+        } else if (dbg_ok(d.slot >= 0 && d.slot < 2 * static_cast<int>(gridDim.x), p.status, 42)) {
+          float *dst = p.part + (static_cast<int64_t>(d.slot) * 2 * kNQ + q) * (2 * kD) + col;
+          dst[0] = y1;
+          dst[kNQ * (2 * kD)] = y2;
         }
       }
-    // Row sums over the 2 d columns: this lane's, its warp's, the four warps'.
-    const auto row_sums = [&](float (&tot)[kNT][2]) {
+    }
+    tc_fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm->o_empty[seg % G::kOBufs]);
+    ++seg;
+    if (!direct) continue;
+
+    // Head norm: row sums over the lanes, the four quarters and (d = 128) both halves.
+    const auto row_sums = [&](bool square) {  // into rsum
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
+      for (int k = 0; k < kChunks / kStep; ++k) {
+        const int q8 = 8 * (kStep * k + (kStep == 2 ? half : 0));
+        if (idle || q8 >= real) break;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          tot[nt][e] = group_sum(tot[nt][e]);
-          if (g == 0) sm->rsum[0][quarter][8 * nt + 2 * t + e] = tot[nt][e];
+        for (int e = 0; e < 8; ++e) {
+          if (q8 + e >= real) break;
+          const float y = warp_sum(square ? o[8 * k + e] * o[8 * k + e] : o[8 * k + e]);
+          if (lane == 0) sm->rsum[kD == 128 ? half : 0][quarter][q8 + e] = y;
         }
-      named_barrier_sync(3, kConsumers / 2);
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          tot[nt][e] = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) tot[nt][e] += sm->rsum[0][k][8 * nt + 2 * t + e];
-        }
-      named_barrier_sync(3, kConsumers / 2);
+      }
+      named_barrier_sync(2, kConsumers);
     };
-    float gain[kNT][2];
+    const auto row_sum = [&](int q) {
+      float y = (sm->rsum[0][0][q] + sm->rsum[0][1][q]) + (sm->rsum[0][2][q] + sm->rsum[0][3][q]);
+      if (kD == 128)
+        y += (sm->rsum[1][0][q] + sm->rsum[1][1][q]) + (sm->rsum[1][2][q] + sm->rsum[1][3][q]);
+      return y;
+    };
     if (p.headnorm == 2) {
-      float mean[kNT][2];
+      row_sums(false);
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
+      for (int k = 0; k < kChunks / kStep; ++k) {
+        const int q8 = 8 * (kStep * k + (kStep == 2 ? half : 0));
+        if (idle || q8 >= real) break;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          mean[nt][e] = 0.f;
-#pragma unroll
-          for (int mt = 0; mt < kMT; ++mt) mean[nt][e] += o[mt][nt][e] + o[mt][nt][e + 2];
-        }
-      row_sums(mean);
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int mt = 0; mt < kMT; ++mt) o[mt][nt][c] -= mean[nt][c & 1] * (0.5f / kD);
-    }
-    if (p.headnorm) {
-      float sq[kNT][2];
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          sq[nt][e] = 0.f;
-#pragma unroll
-          for (int mt = 0; mt < kMT; ++mt)
-            sq[nt][e] += o[mt][nt][e] * o[mt][nt][e] + o[mt][nt][e + 2] * o[mt][nt][e + 2];
-        }
-      row_sums(sq);
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          gain[nt][e] = rsqrtf(sq[nt][e] * (0.5f / kD) + p.eps) * p.out_scale;
-    }
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = d.rb * kRows + 8 * nt + 2 * t + e;
-        if (r >= p.rows) continue;
-        const int i = r / p.group, h = d.hk * p.group + r - i * p.group;
-        __nv_bfloat16 *dst = p.out + d.b * p.outs.b + h * p.outs.h + i * p.outs.n;
-        const bool none = lim[nt][e] < 0 && !poisoned;
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int col = (quarter * kMT + mt) * 16 + g + 8 * k;
-            float y = o[mt][nt][e + 2 * k];
-            if (p.headnorm && !none) {
-              y *= gain[nt][e];
-              if (p.norm_w != nullptr) y *= __ldg(p.norm_w + h * (2 * kD) + col);
-            }
-            dst[col] = __float2bfloat16_rn(y);
-          }
+        for (int e = 0; e < 8; ++e)
+          if (q8 + e < real) o[8 * k + e] -= row_sum(q8 + e) * (0.5f / kD);
       }
+      named_barrier_sync(2, kConsumers);
+    }
+    if (p.headnorm) row_sums(true);
+#pragma unroll
+    for (int k = 0; k < kChunks / kStep; ++k) {
+      const int q8 = 8 * (kStep * k + (kStep == 2 ? half : 0));
+      if (idle || q8 >= real) break;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int q = q8 + e;
+        if (q >= real) break;
+        const int r = d.rb * kNQ + q;
+        const int i = r / p.group, h = d.hk * p.group + r - i * p.group;
+        float y = o[8 * k + e];
+        if (p.headnorm && (d.len - p.N + i >= 0 || poisoned)) {
+          y *= rsqrtf(row_sum(q) * (0.5f / kD) + p.eps) * p.out_scale;
+          if (p.norm_w != nullptr) y *= __ldg(p.norm_w + h * (2 * kD) + col);
+        }
+        p.out[d.b * p.outs.b + h * p.outs.h + i * p.outs.n + col] = __float2bfloat16_rn(y);
+      }
+    }
   }
 }
 
-template <int kD, bool kFp8, int kNT>
+template <int kD, bool kFp8, int kNQ>
 __global__ void __launch_bounds__(kThreads, 1)
     diffpaged_fwd_kernel(const __grid_constant__ CUtensorMap mk1,
                          const __grid_constant__ CUtensorMap mk2,
                          const __grid_constant__ CUtensorMap mv,
                          const __grid_constant__ FwdParams p) {
-  using G = Geo<kD, kFp8>;
+  using G = Geo<kD, kFp8, kNQ>;
+  using L = Layout<kD, kFp8, kNQ>;
   extern __shared__ uint8_t raw[];
-  uint8_t *stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  auto *sm = reinterpret_cast<Smem<kD, kFp8, kNT> *>(stages + G::kStages * G::kStageBytes);
+  uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  auto *sm = reinterpret_cast<Ctrl<kNQ> *>(smem + L::kCtrl);
+  const int warp = threadIdx.x / 32;
   grid_dependents_launch();
-  if (threadIdx.x == kConsumers) {
-    for (int s = 0; s < G::kStages; ++s) {
-      mbar_init(&sm->full[s], 1);
-      mbar_init(&sm->empty[s], kConsumers / 32);
+  Share share;
+  if (warp == kLoadWarp) {
+    if (threadIdx.x % 32 == 0) {
+      tma_prefetch_desc(&mk1);
+      tma_prefetch_desc(&mk2);
+      tma_prefetch_desc(&mv);
     }
+    share = find_share(p);
+  } else if (warp == kMmaWarp) {
+    tmem_alloc(&sm->tmem, G::kTmemCols);
+    tmem_relinquish();
+  } else if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kSlots; ++s) {
+      mbar_init(&sm->full[s], 1);
+      mbar_init(&sm->empty[s], 1);
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(&sm->q_full[k], 32);
+      mbar_init(&sm->q_empty[k], 1);
+      mbar_init(&sm->s_full[k], 1);
+      mbar_init(&sm->p_full[k], kConsumers / 32);
+      mbar_init(&sm->pv_done[k], 1);
+      mbar_init(&sm->o_empty[k], kConsumers / 32);
+    }
+    mbar_init(&sm->drain, 1);
     sm->abort = sm->failed = 0;
     for (int k = 0; k < 3; ++k) sm->bad_rows[k] = 0;
     fence_barrier_init();
   }
+  tc_fence_before_sync();
   __syncthreads();
-  if (threadIdx.x >= kConsumers)
-    load_warp<kD, kFp8, kNT>(p, &mk1, &mk2, &mv, stages, sm);
+  tc_fence_after_sync();
+  if (warp == kLoadWarp)
+    load_warp<kD, kFp8, kNQ>(p, &mk1, &mk2, &mv, smem, sm, share);
+  else if (warp == kMmaWarp)
+    mma_warp<kD, kFp8, kNQ>(p, smem, sm);
   else
-    compute_warps<kD, kFp8, kNT>(p, stages, sm);
+    softmax_warps<kD, kFp8, kNQ>(p, smem, sm);
+  __syncwarp();
+  tc_fence_before_sync();
   __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(sm->tmem, G::kTmemCols);
   if (threadIdx.x == 0 && *reinterpret_cast<volatile int *>(&sm->abort) && p.status != nullptr)
     atomicExch(p.status, static_cast<int32_t>(DIFFATTN_ERR_TIMEOUT));
 }
@@ -1063,17 +1198,16 @@ bool encode_pool(CUtensorMap *map, const void *base, int64_t width, const diffpa
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kD, bool kFp8, int kNT>
+template <int kD, bool kFp8, int kNQ>
 diffattn_status launch_main(const FwdParams &p, const CUtensorMap (&maps)[3], int ctas,
                             cudaStream_t stream) {
-  using G = Geo<kD, kFp8>;
-  constexpr size_t kBytes = 1024 + G::kStages * G::kStageBytes + sizeof(Smem<kD, kFp8, kNT>);
+  constexpr size_t kBytes = Layout<kD, kFp8, kNQ>::kBytes;
   static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
   static std::atomic<bool> attr_set[64];  // per device (concurrent callers may both set)
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DIFFATTN_ERR_CUDA;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(diffpaged_fwd_kernel<kD, kFp8, kNT>,
+    if (cudaFuncSetAttribute(diffpaged_fwd_kernel<kD, kFp8, kNQ>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kBytes)) != cudaSuccess)
       return DIFFATTN_ERR_CUDA;
@@ -1084,10 +1218,18 @@ diffattn_status launch_main(const FwdParams &p, const CUtensorMap (&maps)[3], in
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kBytes;
   cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, diffpaged_fwd_kernel<kD, kFp8, kNT>, maps[0], maps[1], maps[2],
+  return cudaLaunchKernelEx(&cfg, diffpaged_fwd_kernel<kD, kFp8, kNQ>, maps[0], maps[1], maps[2],
                             p) == cudaSuccess
              ? DIFFATTN_OK
              : DIFFATTN_ERR_CUDA;
+}
+
+template <int kD, bool kFp8>
+diffattn_status launch_rows(const FwdParams &p, const CUtensorMap (&maps)[3],
+                            const PagedFwdPlan &plan, cudaStream_t stream) {
+  if (plan.row_tile == 8) return launch_main<kD, kFp8, 8>(p, maps, plan.ctas, stream);
+  if (plan.row_tile == 16) return launch_main<kD, kFp8, 16>(p, maps, plan.ctas, stream);
+  return launch_main<kD, kFp8, 32>(p, maps, plan.ctas, stream);
 }
 
 template <int kD>
@@ -1119,8 +1261,8 @@ bool plan_paged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache, boo
   PagedFwdPlan &q = *plan;
   q = PagedFwdPlan{};
   const int64_t rows = desc.N * (desc.H / cache.kv_heads);
-  q.row_tiles = rows <= 8 ? 1 : 2;
-  const int64_t row_tile = 8 * q.row_tiles;
+  q.row_tile = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  const int64_t row_tile = q.row_tile;
   q.row_blocks = static_cast<int>((rows + row_tile - 1) / row_tile);
   const double items = static_cast<double>(desc.B) * static_cast<double>(cache.kv_heads) * q.row_blocks;
   if (items > INT32_MAX) return false;
@@ -1129,7 +1271,7 @@ bool plan_paged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache, boo
   const int64_t units = (most + kTile - 1) / kTile;
   q.padded = units * kTile;
   // One CTA per item where no item can have more tiles than the join's launch would cost.
-  q.whole = units <= 4;
+  q.whole = units <= 2;
   q.ctas = q.whole ? static_cast<int>(q.items) : sm_count;
   if (!q.whole && q.items * units < sm_count) q.ctas = static_cast<int>(q.items * units);
   const size_t slots = q.whole ? 0 : 2 * static_cast<size_t>(q.ctas);
@@ -1212,23 +1354,16 @@ diffattn_status launch_paged_fwd(const diffattn_desc &desc, const diffpaged_cach
       !encode_pool(&maps[2], cache.v, 2 * d, cache, cache.v_strides, false, p.piece_rows))
     return DIFFATTN_ERR_CUDA;
 
-  const bool two = plan.row_tiles == 2;
-  diffattn_status st;
-  if (d == 64)
-    st = fp8 ? (two ? launch_main<64, true, 2>(p, maps, plan.ctas, stream)
-                    : launch_main<64, true, 1>(p, maps, plan.ctas, stream))
-             : (two ? launch_main<64, false, 2>(p, maps, plan.ctas, stream)
-                    : launch_main<64, false, 1>(p, maps, plan.ctas, stream));
-  else
-    st = fp8 ? (two ? launch_main<128, true, 2>(p, maps, plan.ctas, stream)
-                    : launch_main<128, true, 1>(p, maps, plan.ctas, stream))
-             : (two ? launch_main<128, false, 2>(p, maps, plan.ctas, stream)
-                    : launch_main<128, false, 1>(p, maps, plan.ctas, stream));
+  const diffattn_status st =
+      d == 64 ? (fp8 ? launch_rows<64, true>(p, maps, plan, stream)
+                     : launch_rows<64, false>(p, maps, plan, stream))
+              : (fp8 ? launch_rows<128, true>(p, maps, plan, stream)
+                     : launch_rows<128, false>(p, maps, plan, stream));
   if (st != DIFFATTN_OK) return st;
   JoinParams jp;
   jp.f = p;
   jp.ctas = plan.whole ? 1 : plan.ctas;
-  jp.row_tile = 8 * plan.row_tiles;
+  jp.row_tile = plan.row_tile;
   jp.join_rows = p.rows < jp.row_tile ? p.rows : jp.row_tile;
   jp.weight_chunks =
       accumulate ? static_cast<int32_t>((plan.padded + kWeightKeys - 1) / kWeightKeys) : 0;

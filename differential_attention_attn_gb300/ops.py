@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -706,23 +707,44 @@ def _strides4(t):
     return Strides(s[0] if n[0] > 1 else head * n[1], head, row)
 
 
+def _strides_or_null(a, b, c):
+    """The strides argument of a paged call: NULL when all three tensors are contiguous."""
+    if a.is_contiguous() and b.is_contiguous() and c.is_contiguous():
+        return None
+    return (Strides * 3)(_strides4(a), _strides4(b), _strides4(c))
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_desc(B, H, N, d, code, causal, headnorm, eps, lambda_init):
+    """A descriptor without a status word, made once per set of values and only read."""
+    return make_desc(B, H, N, d, code, causal, headnorm, eps, lambda_init)
+
+
+def _paged_call_desc(B, H, N, d, code, causal, headnorm, eps, lambda_init, status):
+    if status is None:
+        return ctypes.byref(_paged_desc(B, H, N, d, code, causal, headnorm, eps, lambda_init))
+    return ctypes.byref(make_desc(B, H, N, d, code, causal, headnorm, eps, lambda_init, status))
+
+
 def _on_device(dev, stream):
-    """The stream of a call on tensors of device `dev`; refuses one of another device, and the
-    current device being another (its context would run the kernels)."""
+    """The handle of a call's stream, for tensors of device `dev`; refuses one of another device,
+    and the current device being another (its context would run the kernels)."""
     index = torch.cuda.current_device()
     if dev.index != index:
         raise ValueError(f"the cache is on cuda:{dev.index}, the current device is cuda:{index}")
     if stream is None:
-        return torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(index)
     if stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the cache on {dev}")
-    return stream
+    return stream.cuda_stream
 
 
-def _scratch(nbytes, dev, stream):
-    """A torch buffer that belongs to `stream`, so that its memory is reused only in its order."""
+def _new_on(stream, shape, dtype, dev):
+    """A torch buffer of `stream`'s memory (None: the current one's), reused only in its order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _workspace(workspace, need, dev, stream):
@@ -730,7 +752,7 @@ def _workspace(workspace, need, dev, stream):
     if workspace is None:
         if not need:
             return None, 0, None
-        workspace = _scratch(need, dev, stream)
+        workspace = _new_on(stream, need, torch.uint8, dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
@@ -746,16 +768,19 @@ def paged_append(cache, k1, k2, v, *, status=None, stream=None, raw_status: bool
     if k1.dim() != 4:
         raise ValueError("k1 must be [B, kv_heads, N, d]")
     B, H, N, d = cache.B, cache.kv_heads, k1.shape[2], cache.d
-    for name, t, width in (("k1", k1, d), ("k2", k2, d), ("v", v, 2 * d)):
-        if t.shape != (B, H, N, width) or t.dtype != torch.bfloat16:
-            raise ValueError(f"{name} must be {(B, H, N, width)} bfloat16")
-        if t.device != cache.device or t.stride(3) != 1:
-            raise ValueError(f"{name} must be on the cache's device with contiguous rows")
-    stream = _on_device(cache.device, stream)
-    desc = make_desc(B, H, N, d, cache.code, True, 0, 0.0, 0.0, status)
-    strides = (Strides * 3)(_strides4(k1), _strides4(k2), _strides4(v))
-    st = load().diffpaged_append(ctypes.byref(desc), cache._ref, k1.data_ptr(), k2.data_ptr(),
-                                 v.data_ptr(), strides, stream.cuda_stream)
+    dev, dtype = cache.device, torch.bfloat16
+    if k1.shape != (B, H, N, d) or k2.shape != k1.shape or v.shape != (B, H, N, 2 * d):
+        raise ValueError(f"k1 and k2 must be {(B, H, N, d)}, v {(B, H, N, 2 * d)}")
+    if k1.dtype != dtype or k2.dtype != dtype or v.dtype != dtype:
+        raise ValueError("k1, k2 and v must be bfloat16")
+    if k1.device != dev or k2.device != dev or v.device != dev:
+        raise ValueError("all tensors must be on the cache's device")
+    if k1.stride(3) != 1 or k2.stride(3) != 1 or v.stride(3) != 1:
+        raise ValueError("rows must be contiguous (last stride 1)")
+    handle = _on_device(dev, stream)
+    st = load().diffpaged_append(
+        _paged_call_desc(B, H, N, d, cache.code, True, 0, 0.0, 0.0, status), cache._ref,
+        k1.data_ptr(), k2.data_ptr(), v.data_ptr(), _strides_or_null(k1, k2, v), handle)
     if raw_status:
         return st
     _check(st)
@@ -802,19 +827,14 @@ def paged_fwd(cache, q1, q2, lam, *, causal: bool = True, headnorm: int = 1, nor
         raise ValueError("norm_w must be contiguous float32 [H, 2d]")
     if q1.device != dev or q2.device != dev or lam.device != dev:
         raise ValueError("all tensors must be on the cache's device")
-    stream = _on_device(dev, stream)
+    handle = _on_device(dev, stream)
     if out is None:
-        if stream == torch.cuda.current_stream():
-            out = torch.empty((B, H, N, 2 * d), dtype=torch.bfloat16, device=dev)
-        else:
-            with torch.cuda.stream(stream):
-                out = torch.empty((B, H, N, 2 * d), dtype=torch.bfloat16, device=dev)
+        out = _new_on(stream, (B, H, N, 2 * d), torch.bfloat16, dev)
     elif out.shape != (B, H, N, 2 * d) or out.dtype != torch.bfloat16 or out.device != dev or \
             out.stride(3) != 1:
         raise ValueError("out must be bfloat16 [B, H, N, 2d] with contiguous rows")
-    desc = make_desc(B, H, N, d, cache.code, causal, headnorm, eps, lambda_init, status)
-    ref, lib = ctypes.byref(desc), load()
-    need = 0
+    ref = _paged_call_desc(B, H, N, d, cache.code, causal, headnorm, eps, lambda_init, status)
+    lib, need = load(), 0
     if workspace is None:
         n = ctypes.c_size_t(0)
         st = lib.diffpaged_fwd_plan(ref, cache._ref, int(accumulate), ctypes.byref(n))
@@ -824,10 +844,9 @@ def paged_fwd(cache, q1, q2, lam, *, causal: bool = True, headnorm: int = 1, nor
             _check(st)
         need = n.value
     ws, ws_bytes, _keep = _workspace(workspace, need, dev, stream)
-    strides = (Strides * 3)(_strides4(q1), _strides4(q2), _strides4(out))
     st = lib.diffpaged_fwd(ref, cache._ref, q1.data_ptr(), q2.data_ptr(), lam.data_ptr(),
                            None if norm_w is None else norm_w.data_ptr(), out.data_ptr(),
-                           strides, int(accumulate), ws, ws_bytes, stream.cuda_stream)
+                           _strides_or_null(q1, q2, out), int(accumulate), ws, ws_bytes, handle)
     if raw_status:
         return st
     _check(st)
@@ -849,8 +868,7 @@ def paged_evict(cache, *, keep: int, recent: int = 0, workspace=None, status=Non
                 raw_status: bool = False):
     """`diffpaged_evict`: cut every sequence longer than `keep` to its last `recent` keys and
     the keep - recent of the largest weights, in place; updates cache.kv_len."""
-    stream = _on_device(cache.device, stream)
-    need = 0
+    handle, need = _on_device(cache.device, stream), 0
     if workspace is None:
         st, need = paged_evict_plan(cache, keep=keep, raw_status=True)
         if st != OK:
@@ -858,9 +876,9 @@ def paged_evict(cache, *, keep: int, recent: int = 0, workspace=None, status=Non
                 return st
             _check(st)
     ws, ws_bytes, _keep = _workspace(workspace, need, cache.device, stream)
-    desc = make_desc(cache.B, cache.kv_heads, 0, cache.d, cache.code, True, 0, 0.0, 0.0, status)
-    st = load().diffpaged_evict(ctypes.byref(desc), cache._ref, int(keep), int(recent), ws,
-                                ws_bytes, stream.cuda_stream)
+    ref = _paged_call_desc(cache.B, cache.kv_heads, 0, cache.d, cache.code, True, 0, 0.0, 0.0,
+                           status)
+    st = load().diffpaged_evict(ref, cache._ref, int(keep), int(recent), ws, ws_bytes, handle)
     if raw_status:
         return st
     _check(st)
