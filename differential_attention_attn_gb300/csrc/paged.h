@@ -12,7 +12,7 @@ namespace diffattn {
 constexpr int kPageGrain = 16;  // page sizes are multiples of this many rows
 
 // Forward: keys are taken in tiles of kPagedTile; the rows (new token, query
-// head) of one key/value head in blocks of 8, 16 or 32.
+// head) of one key/value head in blocks of 1, 2, 4 .. 32.
 constexpr int kPagedTile = 128;
 constexpr int kPagedMaxTokens = 16;
 constexpr int kPagedMaxGroup = 64;

@@ -56,7 +56,6 @@ constexpr int kThreads = kConsumers + 64;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kGrowth = 8.f;  // log2 units a logit may pass the reference maximum by
-constexpr int kMinShare = 1;    // tiles
 constexpr int kMaxBad = 16;     // new tokens of a call, so more than keys that only some of them see
 constexpr int kRing = 8;        // tile descriptors; at most 5 tiles are between load and epilogue
 constexpr int kBoxBytes = kTile * 128;   // 64 bf16 columns of a tile
@@ -70,6 +69,22 @@ struct TileDesc {
   int32_t len, flags, slot, item;
 };
 
+// Exact division of 0 <= n < 2^31 by a launch constant: a multiply and a shift.
+struct FastDiv {
+  uint32_t mul, shift, d;
+  __device__ __forceinline__ int32_t div(int32_t n) const {
+    return static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> shift);
+  }
+  __device__ __forceinline__ int32_t mod(int32_t n) const {
+    return n - div(n) * static_cast<int32_t>(d);
+  }
+};
+FastDiv fast_div(uint32_t d) {  // 2^(s - 1) < d <= 2^s, mul = ceil(2^(31 + s) / d)
+  uint32_t s = 0;
+  while ((uint64_t{1} << s) < d) ++s;
+  return {static_cast<uint32_t>(((uint64_t{1} << (31 + s)) + d - 1) / d), 31 + s, d};
+}
+
 struct FwdParams {
   const void *q1, *q2;
   const void *v_pages;
@@ -81,6 +96,7 @@ struct FwdParams {
   int32_t B, H, N, kv_heads, group, rows;  // rows = N * group
   int32_t num_pages, max_pages, page_size, piece_rows;
   int32_t row_blocks, causal, headnorm, whole;
+  FastDiv by_page, by_group;  // page_size, group
   float eps, out_scale, scale_log2;
   // Workspace (see PagedFwdPlan): partial O [2 C][2][NQ][2 d], their (m, l), one join record per
   // CTA, and for accumulate one record per item, whole items' (m, l) and all logits.
@@ -94,9 +110,12 @@ struct FwdParams {
   float *weights;
 };
 
-// kNQ: rows of a block (8, 16 or 32).
-template <int kD, bool kFp8, int kNQ>
+// kNR: rows of a block (1, 2, 4, 8, 16 or 32), padded to kNQ = 8, 16 or 32 in the products.
+template <int kD, bool kFp8, int kNR>
 struct Geo {
+  static constexpr int kNQ = kNR < 8 ? 8 : kNR;
+  static constexpr int kW = kNR < 8 ? kNR : 8;                      // rows taken at a time
+  static constexpr int kChunks = kNR / kW;
   static constexpr int kKeyRow = kFp8 ? kD : 2 * kD;                // bytes
   static constexpr int kKeyBox = kKeyRow < 128 ? kKeyRow : 128;     // bytes of a key box row
   static constexpr int kKeySlots = kKeyRow <= 128 ? 1 : 2;          // both maps in one, or each its own
@@ -104,10 +123,13 @@ struct Geo {
   static constexpr int kTileSlots = kKeySlots + kValSlots;
   static constexpr int kNS = kNQ < 16 ? 16 : kNQ;                   // columns of S (N is at least 16)
   static constexpr int kQBytes = kNS * kKeyRow;                     // one map's rows
-  static constexpr int kPRows = 4 * kNQ;                            // map 1 hi, lo, map 2 hi, lo
-  static constexpr int kPBytes = kPRows * 2 * kTile;
+  // P, N-major: a row of 4 kNQ bf16 per key (map 1 hi, lo, map 2 hi, lo), in blocks of at most
+  // 128 bytes.
+  static constexpr int kPCols = 4 * kNQ;
+  static constexpr int kPRow = kPCols * 2 < 128 ? kPCols * 2 : 128;
+  static constexpr int kPBytes = kTile * kPCols * 2;
   static constexpr int kPBufs = kNQ == 32 ? 1 : 2;
-  static constexpr int kOCols = kValSlots * kPRows;
+  static constexpr int kOCols = kValSlots * kPCols;
   static constexpr int kOBufs = kNQ == 32 && kD == 128 ? 1 : 2;
   static constexpr int kTmemO = 4 * kNS;                            // after two buffers of two S
   static constexpr int kTmemUsed = kTmemO + kOBufs * kOCols;
@@ -115,12 +137,13 @@ struct Geo {
   static_assert(kTmemUsed <= 512, "tensor memory");
 };
 
-template <int kNQ>
+template <int kNR>
 struct Ctrl {
-  float wmax[2][4][kNQ];
-  float lsum[2][4][kNQ];
-  float rsum[2][4][kNQ];
-  float late[2][kMaxBad][kNQ];  // logits of keys kept out of the product
+  float wmax[2][4][kNR];
+  float lsum[2][4][kNR];
+  float rsum[2][4][kNR];
+  float late[2][kMaxBad][kNR];  // logits of keys kept out of the product,
+  float ref[2][kNR];            // and the references they go with
   TileDesc ring[kRing];
   uint64_t full[6], empty[6];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_empty[2], drain;
@@ -129,19 +152,19 @@ struct Ctrl {
   int abort, failed;
 };
 
-template <int kD, bool kFp8, int kNQ>
+template <int kD, bool kFp8, int kNR>
 struct Layout {
-  using G = Geo<kD, kFp8, kNQ>;
+  using G = Geo<kD, kFp8, kNR>;
   static constexpr int kP = 0;
   static constexpr int kQ = kP + G::kPBufs * G::kPBytes;
   static constexpr int kFixed = kQ + 4 * G::kQBytes;  // then the ring, then Ctrl
   static constexpr int kRoom =
-      227 * 1024 - 1024 - static_cast<int>(sizeof(Ctrl<kNQ>)) - kFixed;
+      227 * 1024 - 1024 - static_cast<int>(sizeof(Ctrl<kNR>)) - kFixed;
   static constexpr int kSlots = kRoom / kSlotBytes < 6 ? kRoom / kSlotBytes : 6;
   static_assert(kSlots >= G::kTileSlots, "one tile must fit");
   static constexpr int kRingAt = kFixed;
   static constexpr int kCtrl = kRingAt + kSlots * kSlotBytes;
-  static constexpr int kBytes = 1024 + kCtrl + static_cast<int>(sizeof(Ctrl<kNQ>));
+  static constexpr int kBytes = 1024 + kCtrl + static_cast<int>(sizeof(Ctrl<kNR>));
 };
 
 __device__ __forceinline__ int32_t units_of(int32_t len, int32_t most) {
@@ -149,11 +172,6 @@ __device__ __forceinline__ int32_t units_of(int32_t len, int32_t most) {
   return (len + kTile - 1) / kTile;
 }
 
-__device__ __forceinline__ int64_t warp_sum64(int64_t x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -195,26 +213,52 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, ui
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Descriptor of K-major rows of 64 bytes with 64-byte swizzle (8-row groups 512 bytes apart).
+// Descriptor of rows of 64 bytes with 64-byte swizzle (8-row groups 512 bytes apart): K-major, or
+// MN-major operands at most 32 elements wide.
 __device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr) {
   return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (1ull << 16) |
          (static_cast<uint64_t>(512 >> 4) << 32) | (1ull << 46) | (4ull << 61);
 }
 
+// kN consecutive 32-bit tensor-memory columns of the thread's lane; valid after tmem_loaded().
 template <int kN>
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[kN]) {
-  if constexpr (kN == 8)
-    tmem_ld_x8(addr, r);
-  else if constexpr (kN == 16)
-    tmem_ld_x16(addr, r);
+  static_assert(kN == 1 || kN == 2 || kN == 4 || kN == 8, "columns");
+  if constexpr (kN == 1)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[0]) : "r"(addr) : "memory");
+  else if constexpr (kN == 2)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];"
+                 : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+  else if constexpr (kN == 4)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
   else
-    tmem_ld_x32(addr, r);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7]) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-      : "memory");
+// Waits for the thread's loads, passing r through so that no use moves before it.
+template <int kN>
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[kN]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]) : : "memory");
+#pragma unroll
+  for (int k = 1; k < kN; ++k) asm volatile("" : "+r"(r[k]));
+}
+template <int kN>
+__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[kN]) {
+  if constexpr (kN == 1)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr), "r"(r[0]) : "memory");
+  else if constexpr (kN == 2)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]) : "memory");
+  else if constexpr (kN == 4)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+  else
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
 }
 
 // Phase parity of the n-th use (from 0) of buffer n % kBufs.
@@ -223,106 +267,131 @@ __device__ __forceinline__ uint32_t phase(uint32_t n) {
   return (n / kBufs) & 1;
 }
 
-// The CTA's share of the tiles.
+// All items' tiles in order, cut into `ctas` shares of `each` or (the first `more`) each + 1.
+// Fewer than 2^31 tiles (checked at launch).
+struct Shares {
+  uint32_t ctas, each, more;
+  __device__ __forceinline__ uint32_t begin(uint32_t cta) const {
+    return cta * each + min(cta, more);
+  }
+  __device__ __forceinline__ uint32_t cta_of(uint32_t tile) const {
+    const uint32_t border = more * (each + 1);
+    return tile < border ? tile / (each + 1) : more + (tile - border) / each;
+  }
+};
+
+// The CTA's share: its first item (b, hk, rb) and tile within it.
 struct Share {
-  int64_t todo, total, begin, ctas;
+  Shares all;
+  uint32_t begin, todo;
   int32_t b, hk, rb, tile, len, units;
 };
 
-// Where this CTA's share begins: item (b, hk, rb) and tile within it (one warp, uniform).
-__device__ Share find_share(const FwdParams &p) {
+// One warp, uniform.
+__device__ __forceinline__ Share find_share(const FwdParams &p) {
   const int lane = threadIdx.x % 32;
   const int32_t most = p.max_pages * p.page_size;
-  Share s = {0, 0, 0, 1, 0, 0, 0, 0, 0, 1};
+  Share s = {{1, 1, 0}, 0, 0, 0, 0, 0, 0, 0, 1};
+  const uint32_t heads = p.kv_heads * p.row_blocks;  // items of a sequence
   if (p.whole) {
-    const uint32_t item = blockIdx.x;
-    s.rb = static_cast<int32_t>(item % p.row_blocks);
-    s.hk = static_cast<int32_t>(item / p.row_blocks % p.kv_heads);
-    s.b = static_cast<int32_t>(item / p.row_blocks / p.kv_heads);
+    s.b = blockIdx.x / heads;
+    const uint32_t item = blockIdx.x - s.b * heads;
+    s.hk = item / p.row_blocks;
+    s.rb = item - s.hk * p.row_blocks;
     s.len = __ldg(p.kv_len + s.b);
-    s.units = units_of(s.len, most);
-    s.todo = s.units;
+    s.todo = s.units = units_of(s.len, most);
     return s;
   }
-  const int64_t per_unit = static_cast<int64_t>(p.kv_heads) * p.row_blocks;  // items a sequence
+  uint32_t total = 0;
+  int32_t last[4];  // lengths of the last 128 sequences, four a lane
+#pragma unroll 1
   for (int32_t b0 = 0; b0 < p.B; b0 += 128) {
-    int32_t n[4];
+    uint32_t u = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int32_t x = b0 + 32 * k + lane;
-      n[k] = x < p.B ? units_of(__ldg(p.kv_len + x), most) : 0;
+      last[k] = x < p.B ? __ldg(p.kv_len + x) : 0;
     }
-    s.total += warp_sum64(static_cast<int64_t>(n[0]) + n[1] + n[2] + n[3]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (b0 + 32 * k + lane < p.B) u += units_of(last[k], most);
+    total += __reduce_add_sync(0xffffffffu, u);
   }
-  s.total *= per_unit;
-  // Every share has at least kMinShare tiles (the last CTAs may have none).
-  s.ctas = min(static_cast<int64_t>(gridDim.x), max(int64_t{1}, s.total / kMinShare));
-  if (blockIdx.x < s.ctas) {
-    s.begin = s.total * blockIdx.x / s.ctas;
-    s.todo = s.total * (blockIdx.x + 1) / s.ctas - s.begin;
-    int64_t left = s.begin;  // tiles before the share, counted down sequence by sequence
+  total *= heads;
+  // Every share has at least one tile (the last CTAs may have none).
+  s.all.ctas = min(gridDim.x, total);
+  s.all.each = total / s.all.ctas;
+  s.all.more = total - s.all.each * s.all.ctas;
+  if (blockIdx.x < s.all.ctas) {
+    s.begin = s.all.begin(blockIdx.x);
+    s.todo = s.all.each + (blockIdx.x < s.all.more ? 1 : 0);
+    uint32_t left = s.begin;  // tiles before the share, counted down sequence by sequence
+#pragma unroll 1
     for (int32_t b0 = 0; b0 < p.B; b0 += 32) {
       const int32_t x = b0 + lane;
-      const int64_t u = x < p.B ? units_of(__ldg(p.kv_len + x), most) * per_unit : 0;
-      int64_t incl = u;
+      const int32_t len = p.B <= 32 ? last[0] : x < p.B ? __ldg(p.kv_len + x) : 0;
+      const uint32_t u = x < p.B ? units_of(len, most) * heads : 0;
+      uint32_t incl = u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
       }
-      const int64_t all = __shfl_sync(0xffffffffu, incl, 31);
+      const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
       if (left < all) {
         const int at = __ffs(__ballot_sync(0xffffffffu, left < incl)) - 1;
         s.b = b0 + at;
         left -= __shfl_sync(0xffffffffu, incl - u, at);
+        s.len = __shfl_sync(0xffffffffu, len, at);
         break;
       }
       left -= all;
     }
-    s.len = __ldg(p.kv_len + s.b);
     s.units = units_of(s.len, most);
-    const int32_t item = static_cast<int32_t>(left / s.units);
-    s.tile = static_cast<int32_t>(left - static_cast<int64_t>(item) * s.units);
-    s.rb = item % p.row_blocks;
+    const uint32_t item = left / s.units;
+    s.tile = static_cast<int32_t>(left - item * s.units);
     s.hk = item / p.row_blocks;
-  }
-  // The join record of an item that is cut: written by the CTA whose share
-  // begins where that of the CTA with the item's first tile ends.
-  if (lane == 0) {
-    int4 rec = make_int4(-1, 0, 0, 0);
-    if (s.tile > 0) {
-      const int64_t start = s.begin - s.tile;
-      const int64_t c0 = ((start + 1) * s.ctas - 1) / s.total;
-      if (s.begin == s.total * (c0 + 1) / s.ctas)
-        rec = make_int4((s.b * p.kv_heads + s.hk) * p.row_blocks + s.rb,
-                        static_cast<int>(2 * c0 + (s.total * c0 / s.ctas < start ? 1 : 0)),
-                        static_cast<int>(((start + s.units) * s.ctas - 1) / s.total - c0 + 1), 0);
-    }
-    p.records[blockIdx.x] = rec;
+    s.rb = item - s.hk * p.row_blocks;
   }
   return s;
+}
+
+// The join record of an item that is cut: written by the CTA whose share
+// begins where that of the CTA with the item's first tile ends.
+__device__ __forceinline__ void write_record(const FwdParams &p, const Share &s) {
+  int4 rec = make_int4(-1, 0, 0, 0);
+  if (s.tile > 0) {
+    const uint32_t start = s.begin - s.tile;
+    const uint32_t c0 = s.all.cta_of(start);
+    if (s.begin == s.all.begin(c0 + 1))
+      rec = make_int4((s.b * p.kv_heads + s.hk) * p.row_blocks + s.rb,
+                      static_cast<int>(2 * c0 + (s.all.begin(c0) < start ? 1 : 0)),
+                      static_cast<int>(s.all.cta_of(start + s.units - 1) - c0 + 1), 0);
+  }
+  p.records[blockIdx.x] = rec;
 }
 
 // ---------------------------------------------------------------------------
 // The load warp: describes the share's tiles and issues their copies.
 // ---------------------------------------------------------------------------
-template <int kD, bool kFp8, int kNQ>
-__device__ void load_warp(const FwdParams &p, const CUtensorMap *mk1, const CUtensorMap *mk2,
-                          const CUtensorMap *mv, uint8_t *smem, Ctrl<kNQ> *sm, const Share &share) {
-  using G = Geo<kD, kFp8, kNQ>;
-  using L = Layout<kD, kFp8, kNQ>;
+template <int kD, bool kFp8, int kNR>
+__device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap *mk1,
+                                          const CUtensorMap *mk2, const CUtensorMap *mv,
+                                          uint8_t *smem, Ctrl<kNR> *sm, const Share &share) {
+  using G = Geo<kD, kFp8, kNR>;
+  using L = Layout<kD, kFp8, kNR>;
   const int lane = threadIdx.x % 32;
   const int32_t most = p.max_pages * p.page_size;
   int32_t b = share.b, hk = share.hk, rb = share.rb, tile = share.tile, len = share.len,
           units = share.units;
   // Each slot is two boxes wide and up to eight page pieces high: a lane each.
   const int piece = lane / 2, box = lane % 2;
-  const bool piece_ok = piece < kTile / p.piece_rows;
   const int first_row = piece * p.piece_rows;
+  const bool piece_ok = first_row < kTile;
   const auto page_of = [&](int32_t t) {  // this lane's page of tile t of the current sequence
     const int32_t key = t * kTile + first_row;
     return piece_ok && key < len && len <= most
-               ? __ldg(p.page_table + static_cast<int64_t>(b) * p.max_pages + key / p.page_size)
+               ? __ldg(p.page_table + static_cast<int64_t>(b) * p.max_pages + p.by_page.div(key))
                : 0;
   };
   bool ok = true;
@@ -332,7 +401,9 @@ __device__ void load_warp(const FwdParams &p, const CUtensorMap *mk1, const CUte
   int32_t seg_start = tile;
   int32_t slot = 2 * blockIdx.x;
   int32_t id = share.todo > 0 ? page_of(tile) : 0;
-  for (int64_t left = share.todo; ok && left > 0; --left, ++it) {
+  // Read once (by one row block), the pages leave L2 before anything else does.
+  const uint64_t policy = p.row_blocks == 1 ? l2_evict_first() : l2_evict_normal();
+  for (uint32_t left = share.todo; ok && left > 0; --left, ++it) {
     const bool valid_len = len >= 0 && len <= most;
     const bool seg_last = tile + 1 == units || left == 1;
     const int32_t page = id;
@@ -353,15 +424,14 @@ __device__ void load_warp(const FwdParams &p, const CUtensorMap *mk1, const CUte
     if (bad) d.flags |= kBad;
     if (p.item_records != nullptr && lane == 0 && tile == 0) {
       int32_t n = 1;
-      if (!p.whole) {
-        const int64_t start = share.begin + (share.todo - left);
-        n = static_cast<int32_t>(((start + units) * share.ctas - 1) / share.total - blockIdx.x + 1);
-      }
+      if (!p.whole)
+        n = static_cast<int32_t>(
+            share.all.cta_of(share.begin + (share.todo - left) + units - 1) - blockIdx.x + 1);
       p.item_records[d.item] = make_int2(slot, n);
     }
-    const int32_t row = (d.key0 + first_row) % p.page_size;
+    const int32_t row = p.by_page.mod(d.key0 + first_row);
     const int32_t z = bad_id ? 0 : page;
-    const int32_t rows = (keys + p.piece_rows - 1) / p.piece_rows * p.piece_rows;
+    const int32_t rows = (keys + p.piece_rows - 1) & -p.piece_rows;
     // Move on; the next tile's page numbers are fetched while buffers are awaited.
     if (seg_last) {
       seg_start = 0;
@@ -382,7 +452,7 @@ __device__ void load_warp(const FwdParams &p, const CUtensorMap *mk1, const CUte
       }
     }
     if (left > 1) id = page_of(tile);
-#pragma unroll
+#pragma unroll 1
     for (int k = 0; k < G::kTileSlots; ++k, ++c) {
       // The segment's q rows, between its first keys and values (the products may wait for them
       // before they free a slot for the values): 16-byte units into the swizzled operand layout.
@@ -392,12 +462,12 @@ __device__ void load_warp(const FwdParams &p, const CUtensorMap *mk1, const CUte
             !(ok = mbar_wait_warp(&sm->q_empty[qb], phase<2>(seg - 2), &sm->abort, kWaitNs)))
           break;
         constexpr int kUnits = G::kKeyRow / 16;
-        const int real = min(kNQ, p.rows - d.rb * kNQ);
+        const int real = min(kNR, p.rows - d.rb * kNR);
         for (int x = lane; x < 2 * real * kUnits; x += 32) {
           const int map = x >= real * kUnits, y = x - map * real * kUnits;
           const int q = y / kUnits, u = y % kUnits;
-          const int r = d.rb * kNQ + q;
-          const int i = r / p.group, h = d.hk * p.group + r - i * p.group;
+          const int r = d.rb * kNR + q;
+          const int i = p.by_group.div(r), h = d.hk * p.group + r - i * p.group;
           const diffattn_strides &qs = map ? p.q2s : p.q1s;
           const int64_t at = d.b * qs.b + h * qs.h + i * qs.n;
           const uint8_t *src =
@@ -418,30 +488,30 @@ __device__ void load_warp(const FwdParams &p, const CUtensorMap *mk1, const CUte
                                 kWaitNs)))
         break;
       const bool keys_slot = k < G::kKeySlots;
-      uint8_t *buf = smem + L::kRingAt + s * kSlotBytes + box * kBoxBytes;
+      const int row_bytes = keys_slot ? G::kKeyBox : 128;
       if (lane == 0) {
         if (k == 0) {
           if (bad) report_bad_page(p.status);
           sm->ring[it % kRing] = d;
         }
         if (rows > 0)
-          mbar_arrive_expect_tx(&sm->full[s], static_cast<uint32_t>(rows) * 2 *
-                                                  (keys_slot ? G::kKeyBox : 128));
+          mbar_arrive_expect_tx(&sm->full[s], static_cast<uint32_t>(rows) * 2 * row_bytes);
         else
           mbar_arrive(&sm->full[s]);
       }
       __syncwarp();
       if (have) {
-        const int map = G::kKeySlots == 1 ? box : k;
-        if (keys_slot)
-          tma_load_4d(buf + first_row * G::kKeyBox, map ? mk2 : mk1, &sm->full[s],
-                      G::kKeySlots == 1 ? 0 : 64 * box, row, d.hk, z);
-        else
-          tma_load_4d(buf + first_row * 128, mv, &sm->full[s],
-                      128 * (k - G::kKeySlots) + 64 * box, row, d.hk, z);
+        const CUtensorMap *map =
+            !keys_slot ? mv : (G::kKeySlots == 1 ? box : k) ? mk2 : mk1;
+        const int x = !keys_slot ? 128 * (k - G::kKeySlots) + 64 * box
+                                 : G::kKeySlots == 1 ? 0 : 64 * box;
+        tma_load_4d_hint(smem + L::kRingAt + s * kSlotBytes + box * kBoxBytes +
+                             first_row * row_bytes,
+                         map, &sm->full[s], x, row, d.hk, z, policy);
       }
     }
   }
+  if (!p.whole && lane == 0) write_record(p, share);
   // The end mark takes the next slot's turn; then the copies still in flight
   // are awaited (bounded), so that none lands after the CTA is gone.
   if (ok && (c < L::kSlots || mbar_wait_warp(&sm->empty[c % L::kSlots],
@@ -463,112 +533,124 @@ __device__ void load_warp(const FwdParams &p, const CUtensorMap *mk1, const CUte
 // ---------------------------------------------------------------------------
 // The product warp.
 // ---------------------------------------------------------------------------
-template <int kD, bool kFp8, int kNQ>
-__device__ void mma_warp(const FwdParams &p, uint8_t *smem, Ctrl<kNQ> *sm) {
-  using G = Geo<kD, kFp8, kNQ>;
-  using L = Layout<kD, kFp8, kNQ>;
+template <int kD, bool kFp8, int kNR>
+__device__ __forceinline__ void mma_warp(const FwdParams &p, uint8_t *smem, Ctrl<kNR> *sm) {
+  using G = Geo<kD, kFp8, kNR>;
+  using L = Layout<kD, kFp8, kNR>;
   const int lane = threadIdx.x % 32;
   const uint32_t tmem = sm->tmem;
   constexpr uint32_t kIdS = kFp8 ? (1u << 4) | ((G::kNS >> 3) << 17) | ((128u >> 4) << 24)
                                  : idesc_bf16_f32(128, G::kNS, false);
-  constexpr uint32_t kIdO = idesc_bf16_f32(128, G::kPRows, false) | (1u << 15);  // A MN-major
+  constexpr uint32_t kIdO = idesc_bf16_f32(128, G::kPCols, true) | (1u << 15);  // both MN-major
   const auto wait = [&](uint64_t *bar, uint32_t parity) {
     return mbar_wait_warp(bar, parity, &sm->abort, kWaitNs);
+  };
+  const auto ready = [&](uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_test(bar, parity));
   };
   const auto slot_at = [&](uint32_t c) {
     return smem_u32(smem + L::kRingAt + (c % L::kSlots) * kSlotBytes);
   };
-  uint32_t segs = 0;  // segments whose first tile's S has been issued
 
-  // S of tile t (its descriptor's flags are returned; -1 when a wait ran out).
-  const auto issue_s = [&](uint32_t t) -> int32_t {
-    const uint32_t c = t * G::kTileSlots;
-    if (!wait(&sm->full[c % L::kSlots], phase<L::kSlots>(c))) return -1;
-    const int32_t flags = *reinterpret_cast<volatile int32_t *>(&sm->ring[t % kRing].flags);
-    if (flags & kStop) {
-      if (lane == 0) mbar_arrive(&sm->s_full[t & 1]);
-      return flags;
-    }
-    if (flags & kFirst) {
-      if (!wait(&sm->q_full[segs & 1], phase<2>(segs))) return -1;
-      fence_async_proxy();  // the q rows came by ordinary copies
-      ++segs;
-    }
-    tc_fence_after_sync();
-    const uint32_t qb = (segs - 1) & 1;
-#pragma unroll
-    for (int map = 0; map < 2; ++map) {
-      if (map == 1 && G::kKeySlots == 2 &&
-          !wait(&sm->full[(c + 1) % L::kSlots], phase<L::kSlots>(c + 1)))
-        return -1;
-      const uint32_t k_at = slot_at(c + (G::kKeySlots == 2 ? map : 0)) +
-                            (G::kKeySlots == 1 ? map * kBoxBytes : 0);
-      const uint32_t q_at = smem_u32(smem + L::kQ + (2 * qb + map) * G::kQBytes);
-      const uint32_t acc = tmem + (t & 1) * 2 * G::kNS + map * G::kNS;
-#pragma unroll
-      for (int kk = 0; kk < G::kKeyRow / 32; ++kk) {  // 32 bytes of depth each
-        if (G::kKeyRow == 64) {
-          umma_e4m3(acc, smem_desc_sw64(k_at) + 2 * kk, smem_desc_sw64(q_at) + 2 * kk, kIdS, kk > 0);
-        } else {
-          const uint64_t a = smem_desc_sw128(k_at + (kk / 4) * kBoxBytes, 16, 1024) + 2 * (kk % 4);
-          const uint64_t q =
-              smem_desc_sw128(q_at + (kk / 4) * (G::kNS * 128), 16, 1024) + 2 * (kk % 4);
-          if (kFp8)
-            umma_e4m3(acc, a, q, kIdS, kk > 0);
-          else
-            umma_bf16(acc, a, q, kIdS, kk > 0);
+  // Tile t's turn in O and tile n's in S; n runs at most one ahead, where its keys are there.
+  // The tests below see the right phase: the slot's use before was consumed by tile n - 1 or
+  // earlier.
+  uint32_t t = 0, n = 0, segs = 0, o_segs = 0;
+  int32_t s_flags = 0, o_flags = 0, ahead_flags = 0;  // of S's last tile; of tiles t, t + 1
+  uint64_t since = 0;
+#pragma unroll 1
+  while (true) {
+    const uint32_t cs = n * G::kTileSlots;
+    if (n <= t + 1 && !(s_flags & kStop) && ready(&sm->full[cs % L::kSlots], phase<L::kSlots>(cs))) {
+      s_flags = *reinterpret_cast<volatile int32_t *>(&sm->ring[n % kRing].flags);
+      (n == t ? o_flags : ahead_flags) = s_flags;
+      if (s_flags & kStop) {
+        if (lane == 0) mbar_arrive(&sm->s_full[n & 1]);
+      } else {
+        if (s_flags & kFirst) {
+          if (!wait(&sm->q_full[segs & 1], phase<2>(segs))) break;
+          fence_async_proxy();  // the q rows came by ordinary copies
+          ++segs;
         }
-      }
-      if (G::kKeySlots == 2 || map == 1)
-        umma_commit_warp(&sm->empty[(c + (G::kKeySlots == 2 ? map : 0)) % L::kSlots]);
-    }
-    umma_commit_warp(&sm->s_full[t & 1]);
-    if (flags & kLast) umma_commit_warp(&sm->q_empty[qb]);
-    return flags;
-  };
-
-  uint32_t o_segs = 0;
-  int32_t flags = issue_s(0);
-  for (uint32_t t = 0; flags >= 0 && !(flags & kStop); ++t) {
-    // The next tile's S goes first where its keys are already there.
-    int32_t next = -2;
-    const auto next_ready = [&] {
-      const uint32_t c = (t + 1) * G::kTileSlots + G::kKeySlots - 1;
-      const uint32_t c0 = (t + 1) * G::kTileSlots;
-      return __all_sync(0xffffffffu, mbar_test(&sm->full[c0 % L::kSlots], phase<L::kSlots>(c0)) &&
-                                         mbar_test(&sm->full[c % L::kSlots], phase<L::kSlots>(c)));
-    };
-    if (next_ready()) next = issue_s(t + 1);
-    if (next == -1 || !wait(&sm->p_full[t & 1], phase<2>(t))) break;
-    if (next == -2 && next_ready() && (next = issue_s(t + 1)) == -1) break;
-    if (flags & kFirst) {
-      // O of the segment before last (this buffer) has been read.
-      if (o_segs >= G::kOBufs && !wait(&sm->o_empty[o_segs % G::kOBufs],
-                                       phase<G::kOBufs>(o_segs - G::kOBufs)))
-        break;
-      ++o_segs;
-    }
-    tc_fence_after_sync();
-    const uint32_t o_at = tmem + G::kTmemO + ((o_segs - 1) % G::kOBufs) * G::kOCols;
-    const uint32_t p_at = smem_u32(smem + L::kP + (t % G::kPBufs) * G::kPBytes);
-    bool ok = true;
+        tc_fence_after_sync();
+        const uint32_t qb = (segs - 1) & 1;
+#pragma unroll 1
+        for (int map = 0; map < 2; ++map) {
+          const uint32_t c = cs + (G::kKeySlots == 2 ? map : 0);
+          if (G::kKeySlots == 2 && map == 1 &&
+              !wait(&sm->full[c % L::kSlots], phase<L::kSlots>(c)))
+            break;
+          const uint32_t k_at = slot_at(c) + (G::kKeySlots == 1 ? map * kBoxBytes : 0);
+          const uint32_t q_at = smem_u32(smem + L::kQ + (2 * qb + map) * G::kQBytes);
+          const uint32_t acc = tmem + (n & 1) * 2 * G::kNS + map * G::kNS;
 #pragma unroll
-    for (int k = 0; k < G::kValSlots; ++k) {
-      const uint32_t c = t * G::kTileSlots + G::kKeySlots + k;
-      if (!(ok = wait(&sm->full[c % L::kSlots], phase<L::kSlots>(c)))) break;
-      tc_fence_after_sync();
-      const uint64_t v = smem_desc_sw128(slot_at(c), kBoxBytes, 1024);
-#pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk) {
-        const uint64_t w = smem_desc_sw128(p_at + (kk / 4) * (G::kPRows * 128), 16, 1024) + 2 * (kk % 4);
-        umma_bf16(o_at + k * G::kPRows, v + 128 * kk, w, kIdO, !(flags & kFirst) || kk > 0);
+          for (int kk = 0; kk < G::kKeyRow / 32; ++kk) {  // 32 bytes of depth each
+            if (G::kKeyRow == 64) {
+              umma_e4m3(acc, smem_desc_sw64(k_at) + 2 * kk, smem_desc_sw64(q_at) + 2 * kk, kIdS,
+                        kk > 0);
+            } else {
+              const uint64_t a =
+                  smem_desc_sw128(k_at, 16, 1024) + (kk / 4) * (kBoxBytes / 16) + 2 * (kk % 4);
+              const uint64_t q =
+                  smem_desc_sw128(q_at, 16, 1024) + (kk / 4) * (G::kNS * 8) + 2 * (kk % 4);
+              if (kFp8)
+                umma_e4m3(acc, a, q, kIdS, kk > 0);
+              else
+                umma_bf16(acc, a, q, kIdS, kk > 0);
+            }
+          }
+          if (G::kKeySlots == 2 || map == 1) umma_commit_warp(&sm->empty[c % L::kSlots]);
+        }
+        if (*reinterpret_cast<volatile int *>(&sm->abort)) break;
+        umma_commit_warp(&sm->s_full[n & 1]);
+        if (s_flags & kLast) umma_commit_warp(&sm->q_empty[qb]);
       }
-      umma_commit_warp(&sm->empty[c % L::kSlots]);
+      ++n;
+      since = 0;
     }
-    if (!ok) break;
-    umma_commit_warp(&sm->pv_done[t & 1]);
-    flags = next == -2 ? issue_s(t + 1) : next;
+    if (n > t && (o_flags & kStop)) break;
+    if (n > t && ready(&sm->p_full[t & 1], phase<2>(t))) {
+      if (o_flags & kFirst) {
+        // O of the segment before last (this buffer) has been read.
+        if (o_segs >= G::kOBufs &&
+            !wait(&sm->o_empty[o_segs % G::kOBufs], phase<G::kOBufs>(o_segs - G::kOBufs)))
+          break;
+        ++o_segs;
+      }
+      const uint32_t o_at = tmem + G::kTmemO + ((o_segs - 1) % G::kOBufs) * G::kOCols;
+      const uint32_t p_at = smem_u32(smem + L::kP + (t % G::kPBufs) * G::kPBytes);
+      bool ok = true;
+#pragma unroll 1
+      for (int k = 0; k < G::kValSlots; ++k) {
+        const uint32_t c = t * G::kTileSlots + G::kKeySlots + k;
+        if (!(ok = wait(&sm->full[c % L::kSlots], phase<L::kSlots>(c)))) break;
+        tc_fence_after_sync();
+        const uint64_t v = smem_desc_sw128(slot_at(c), kBoxBytes, 1024);
+        const uint64_t w = G::kPRow == 64 ? smem_desc_sw64(p_at)
+                                          : smem_desc_sw128(p_at, kTile * 128, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)  // 16 keys each
+          umma_bf16(o_at + k * G::kPCols, v + 128 * kk, w + G::kPRow * kk, kIdO,
+                    !(o_flags & kFirst) || kk > 0);
+        umma_commit_warp(&sm->empty[c % L::kSlots]);
+      }
+      if (!ok) break;
+      umma_commit_warp(&sm->pv_done[t & 1]);
+      o_flags = ahead_flags;
+      ++t;
+      since = 0;
+      continue;
+    }
+    // Nothing was ready: bounded, like every wait.
+    if (*reinterpret_cast<volatile int *>(&sm->abort)) break;
+    if (since == 0) {
+      since = globaltimer_ns();
+    } else if (globaltimer_ns() - since > kWaitNs) {
+      *reinterpret_cast<volatile int *>(&sm->abort) = 1;
+      break;
+    }
   }
+  __syncwarp();
   // Never free tensor memory under a running product.
   umma_commit_warp(&sm->drain);
   volatile int never = 0;
@@ -579,26 +661,26 @@ __device__ void mma_warp(const FwdParams &p, uint8_t *smem, Ctrl<kNQ> *sm) {
 // The softmax warps.  Warp w: map w / 4; its lanes are keys (then value
 // columns) 32 (w % 4) + lane of a tile, as tensor memory gives them to it.
 // ---------------------------------------------------------------------------
-template <int kD, bool kFp8, int kNQ>
-__device__ void softmax_warps(const FwdParams &p, uint8_t *smem, Ctrl<kNQ> *sm) {
-  using G = Geo<kD, kFp8, kNQ>;
-  using L = Layout<kD, kFp8, kNQ>;
+template <int kD, bool kFp8, int kNR>
+__device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem, Ctrl<kNR> *sm) {
+  using G = Geo<kD, kFp8, kNR>;
+  using L = Layout<kD, kFp8, kNR>;
+  constexpr int kNQ = G::kNQ, kW = G::kW, kChunks = G::kChunks;
+  constexpr int kVUnits = kD / 4;  // 16-byte units of a value row
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int map = warp / 4, quarter = warp % 4;
   const int key = 32 * quarter + lane;  // of the tile
   const uint32_t tmem = sm->tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-  // This thread's column of P: row q of it is at + q * 128 (hi), + kNQ * 128 more (lo).
-  const uint32_t p_col = (key / 64) * (G::kPRows * 128) + map * (2 * kNQ * 128) + (key % 8) * 2;
-  const uint32_t p_unit = (key % 64) / 8;
   const auto v_row = [&](uint32_t t, int row, int u) {  // unit u of value row `row` of tile t
     const uint32_t c = t * G::kTileSlots + G::kKeySlots + u / 16;
     return reinterpret_cast<uint4 *>(smem + L::kRingAt + (c % L::kSlots) * kSlotBytes +
                                      ((u / 8) % 2) * kBoxBytes + row * 128 + (u % 8) * 16);
   };
 
-  float m[kNQ], l[kNQ];
+  float m[kNR], l[kNR];
   bool poisoned = false;
   uint32_t late = 0, seg = 0;
+#pragma unroll 1
   for (uint32_t t = 0;; ++t) {
     bool ok = mbar_wait_warp(&sm->s_full[t & 1], phase<2>(t), &sm->abort, kWaitNs);
     TileDesc d = {};
@@ -608,8 +690,28 @@ __device__ void softmax_warps(const FwdParams &p, uint8_t *smem, Ctrl<kNQ> *sm) 
     const bool masked = d.key0 + kTile - 1 > lim_min;
     const int32_t keys = d.len - d.key0;  // valid rows of the tile if below kTile
     const bool mixed = p.causal && p.N > 1 && masked;  // some rows see keys that others do not
-    const int real = min(kNQ, p.rows - d.rb * kNQ);    // rows of this block
-    float x[kNQ];
+    const int real = kNR == 1 ? 1 : min(kNR, p.rows - d.rb * kNR);  // rows of this block
+    const uint32_t s_at = tmem + (t & 1) * 2 * G::kNS + map * G::kNS;
+
+    // This key's logits of rows kW k .. kW k + kW - 1, in log2 units; -inf where it is masked.
+    float x[kW];
+    const auto load_x = [&](int k) {
+      uint32_t raw[kW];
+      tmem_load(s_at + kW * k, raw);
+      tmem_loaded(raw);
+#pragma unroll
+      for (int e = 0; e < kW; ++e) x[e] = __uint_as_float(raw[e]) * p.scale_log2;
+      if (masked) {
+#pragma unroll
+        for (int e = 0; e < kW; ++e) {
+          // Row r sees keys up to its own position (causal) or all; padding rows see none.
+          const int32_t pos = d.len - p.N + p.by_group.div(d.rb * kNR + kW * k + e);
+          const int32_t lim = pos < 0 ? -1 : p.causal ? pos : d.len - 1;
+          if (d.key0 + key > lim) x[e] = -INFINITY;
+        }
+      }
+    };
+
     bool grew = false;
     if (threadIdx.x == 0) sm->bad_rows[(t + 1) % 3] = 0;
     if (!stop) {
@@ -617,41 +719,29 @@ __device__ void softmax_warps(const FwdParams &p, uint8_t *smem, Ctrl<kNQ> *sm) 
         poisoned = false;
         late = 0;
 #pragma unroll
-        for (int q = 0; q < kNQ; ++q) {
+        for (int q = 0; q < kNR; ++q) {
           m[q] = -INFINITY;
           l[q] = 0.f;
         }
       }
       if (d.flags & kBad) poisoned = true;
       tc_fence_after_sync();
-      uint32_t raw[kNQ];
-      tmem_load(tmem + (t & 1) * 2 * G::kNS + map * G::kNS, raw);
 #pragma unroll
-      for (int q = 0; q < kNQ; ++q) x[q] = __uint_as_float(raw[q]) * p.scale_log2;
-      if (masked) {
-        // Row r sees keys up to its own position (causal) or all; padding rows see none.
+      for (int k = 0; k < kChunks; ++k) {
+        if (kW * k >= real) break;
+        load_x(k);
 #pragma unroll
-        for (int q = 0; q < kNQ; ++q) {
-          if (q >= real) break;
-          const int32_t pos = d.len - p.N + (d.rb * kNQ + q) / p.group;
-          const int32_t lim = pos < 0 ? -1 : p.causal ? pos : d.len - 1;
-          if (d.key0 + key > lim) x[q] = -INFINITY;
+        for (int e = 0; e < kW; ++e)
+          grew |= kW * k + e < real && x[e] > m[kW * k + e] + kGrowth;
+        if (p.logits != nullptr && key < keys) {
+          float *dst = p.logits +
+                       ((static_cast<int64_t>(d.b) * p.kv_heads + d.hk) * 2 + map) * p.rows * p.padded +
+                       static_cast<int64_t>(d.rb * kNR + kW * k) * p.padded + d.key0 + key;
+#pragma unroll
+          for (int e = 0; e < kW; ++e)
+            if (kW * k + e < real && dbg_ok(d.key0 + key < p.padded, p.status, 41))
+              dst[e * p.padded] = x[e];
         }
-      }
-      if (p.logits != nullptr && key < keys) {
-        float *dst = p.logits +
-                     ((static_cast<int64_t>(d.b) * p.kv_heads + d.hk) * 2 + map) * p.rows * p.padded +
-                     static_cast<int64_t>(d.rb) * kNQ * p.padded + d.key0 + key;
-#pragma unroll
-        for (int q = 0; q < kNQ; ++q) {
-          if (q >= real) break;
-          if (dbg_ok(d.key0 + key < p.padded, p.status, 41)) dst[q * p.padded] = x[q];
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < kNQ; ++q) {
-        if (q >= real) break;
-        grew |= x[q] > m[q] + kGrowth;
       }
       // P's buffer: the product that read it last is done.
       if (t >= G::kPBufs)
@@ -661,25 +751,26 @@ __device__ void softmax_warps(const FwdParams &p, uint8_t *smem, Ctrl<kNQ> *sm) 
       // reach every row.  Where new tokens see different keys, a non-finite v row that only some
       // of them see is noted, to be kept out of the product.
       if (ok && (keys < kTile || mixed)) {
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < G::kValSlots; ++k) {
           const uint32_t c = t * G::kTileSlots + G::kKeySlots + k;
           ok = ok && mbar_wait_warp(&sm->full[c % L::kSlots], phase<L::kSlots>(c), &sm->abort,
                                     kWaitNs);
         }
         if (ok) {
-          constexpr int kUnits = kD / 4;
           const int from = max(0, keys);
-          for (int k = threadIdx.x; k < (kTile - from) * kUnits; k += kConsumers)
-            *v_row(t, from + k / kUnits, k % kUnits) = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+          for (int k = threadIdx.x; k < (kTile - from) * kVUnits; k += kConsumers)
+            *v_row(t, from + k / kVUnits, k % kVUnits) = make_uint4(0, 0, 0, 0);
           if (mixed) {
             const int lo = max(0, lim_min + 1 - d.key0), hi = min(kTile, keys);
-            for (int k = threadIdx.x; k < (hi - lo) * kUnits; k += kConsumers) {
-              const uint4 y = *v_row(t, lo + k / kUnits, k % kUnits);
+#pragma unroll 1
+            for (int k = threadIdx.x; k < (hi - lo) * kVUnits; k += kConsumers) {
+              const uint4 y = *v_row(t, lo + k / kVUnits, k % kVUnits);
               bool bad = false;
               for (const uint32_t w : {y.x, y.y, y.z, y.w})
                 bad |= (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-              if (bad) atomicOr(&sm->bad_rows[t % 3], 1u << (d.len - 1 - d.key0 - lo - k / kUnits));
+              if (bad) atomicOr(&sm->bad_rows[t % 3], 1u << (d.len - 1 - d.key0 - lo - k / kVUnits));
             }
           }
         }
@@ -691,15 +782,20 @@ __device__ void softmax_warps(const FwdParams &p, uint8_t *smem, Ctrl<kNQ> *sm) 
     // run out)?
     if (named_barrier_or(1, kConsumers, grew || !ok)) {
       if (*reinterpret_cast<volatile int *>(&sm->failed)) break;
+      const bool fresh = (d.flags & kFirst) != 0;  // nothing in O yet
       if (!stop) {
 #pragma unroll
-        for (int q = 0; q < kNQ; ++q) {
-          if (q >= real) break;
-          const float y = warp_max(x[q]);
-          if (lane == 0) sm->wmax[map][quarter][q] = y;
+        for (int k = 0; k < kChunks; ++k) {
+          if (kW * k >= real) break;
+          if (kChunks > 1) load_x(k);
+#pragma unroll
+          for (int e = 0; e < kW; ++e) {
+            const float y = warp_max(x[e]);
+            if (lane == 0) sm->wmax[map][quarter][kW * k + e] = y;
+          }
         }
         // O moves with the reference, so the product before must be done.
-        if (!(d.flags & kFirst))
+        if (!fresh)
           ok = mbar_wait_warp(&sm->pv_done[(t - 1) & 1], phase<2>(t - 1), &sm->abort, kWaitNs);
       }
       if (named_barrier_or(2, kConsumers, !ok)) break;
@@ -707,35 +803,31 @@ __device__ void softmax_warps(const FwdParams &p, uint8_t *smem, Ctrl<kNQ> *sm) 
         const uint32_t o_at = tmem + G::kTmemO + (seg % G::kOBufs) * G::kOCols + map * 2 * kNQ;
         tc_fence_after_sync();
 #pragma unroll
-        for (int q8 = 0; q8 < kNQ; q8 += 8) {
-          if (q8 >= real) break;
-          float f[8];
+        for (int k = 0; k < kChunks; ++k) {
+          if (kW * k >= real) break;
+          float f[kW];
           bool moved = false;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int q = q8 + k;
-            f[k] = 1.f;
-            if (q < real) {
-              float y = m[q];
+          for (int e = 0; e < kW; ++e) {
+            const int q = kW * k + e;
+            float y = m[q];
 #pragma unroll
-              for (int w = 0; w < 4; ++w) y = fmaxf(y, sm->wmax[map][w][q]);
-              if (y != m[q]) {
-                f[k] = ex2_approx(m[q] - y);
-                moved = true;
-              }
-              m[q] = y;
-              l[q] *= f[k];
-            }
+            for (int w = 0; w < 4; ++w) y = fmaxf(y, sm->wmax[map][w][q]);
+            f[e] = y == m[q] ? 1.f : ex2_approx(m[q] - y);
+            moved |= y != m[q];
+            m[q] = y;
+            l[q] *= f[e];
           }
-          if (moved && !(d.flags & kFirst)) {  // the same decision in every thread of the map
-#pragma unroll
+          if (moved && !fresh) {  // the same decision in every thread of the map
+#pragma unroll 1
             for (int part = 0; part < 2 * G::kValSlots; ++part) {
-              const uint32_t at = o_at + (part / 2) * G::kPRows + (part % 2) * kNQ + q8;
-              uint32_t y[8];
-              tmem_ld_x8(at, y);
+              const uint32_t at = o_at + (part / 2) * G::kPCols + (part % 2) * kNQ + kW * k;
+              uint32_t y[kW];
+              tmem_load(at, y);
+              tmem_loaded(y);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f[k]);
-              tmem_st_x8(at, y);
+              for (int e = 0; e < kW; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f[e]);
+              tmem_store(at, y);
             }
           }
         }
@@ -744,36 +836,58 @@ __device__ void softmax_warps(const FwdParams &p, uint8_t *smem, Ctrl<kNQ> *sm) 
     }
     if (stop) break;
 
-    // Rows of v to keep out of the product (rare): zero them in the buffer as well.
+    // Rows of v to keep out of the product (rare): zero them in the buffer as well, and keep
+    // their logits.
     const uint32_t bad_rows = mixed ? sm->bad_rows[t % 3] : 0u;
+    const int back = d.len - 1 - d.key0 - key;
+    const bool kept_out = bad_rows && back >= 0 && back < kMaxBad && ((bad_rows >> back) & 1);
     if (bad_rows) {
       late |= bad_rows;
-      constexpr int kUnits = kD / 4;
-      for (int k = threadIdx.x; k < kTile * kUnits; k += kConsumers) {
-        const int back = d.len - 1 - d.key0 - k / kUnits;
-        if (back >= 0 && back < kMaxBad && ((bad_rows >> back) & 1))
-          *v_row(t, k / kUnits, k % kUnits) = make_uint4(0, 0, 0, 0);
-      }
-      const int back = d.len - 1 - d.key0 - key;
-      if (back >= 0 && back < kMaxBad && ((bad_rows >> back) & 1)) {
-#pragma unroll
-        for (int q = 0; q < kNQ; ++q) sm->late[map][back][q] = x[q];
+#pragma unroll 1
+      for (int k = threadIdx.x; k < kTile * kVUnits; k += kConsumers) {
+        const int x_back = d.len - 1 - d.key0 - k / kVUnits;
+        if (x_back >= 0 && x_back < kMaxBad && ((bad_rows >> x_back) & 1))
+          *v_row(t, k / kVUnits, k % kVUnits) = make_uint4(0, 0, 0, 0);
       }
     }
 
     // P = 2^(x - m) as bf16 hi + lo.
-    uint8_t *p_at = smem + L::kP + (t % G::kPBufs) * G::kPBytes + p_col;
+    uint8_t *p_buf = smem + L::kP + (t % G::kPBufs) * G::kPBytes;
 #pragma unroll
-    for (int q = 0; q < kNQ; ++q) {
-      if (q >= real) break;
-      float y = ex2_approx(x[q] - m[q]);
-      if (masked && x[q] == -INFINITY) y = 0.f;  // also where no key has been seen yet
-      l[q] += y;
-      const __nv_bfloat16 hi = __float2bfloat16_rn(y);
-      uint8_t *at = p_at + q * 128 + ((p_unit ^ (q & 7)) << 4);
-      *reinterpret_cast<__nv_bfloat16 *>(at) = hi;
-      *reinterpret_cast<__nv_bfloat16 *>(at + kNQ * 128) =
-          __float2bfloat16_rn(y - __bfloat162float(hi));
+    for (int k = 0; k < kChunks; ++k) {
+      if (kW * k >= real) break;
+      if (kChunks > 1) load_x(k);
+      uint32_t hi[kW > 1 ? kW / 2 : 1], lo[kW > 1 ? kW / 2 : 1];
+      float y[kW > 1 ? kW : 2];
+      y[1] = 0.f;
+#pragma unroll
+      for (int e = 0; e < kW; ++e) {
+        if (kept_out) sm->late[map][back][kW * k + e] = x[e];
+        y[e] = ex2_approx(x[e] - m[kW * k + e]);
+        if (masked && x[e] == -INFINITY) y[e] = 0.f;  // also where no key has been seen yet
+        l[kW * k + e] += y[e];
+      }
+#pragma unroll
+      for (int e = 0; e < (kW > 1 ? kW / 2 : 1); ++e) {
+        hi[e] = pack_bf16x2(y[2 * e], y[2 * e + 1]);
+        lo[e] = pack_bf16x2(y[2 * e] - __uint_as_float(hi[e] << 16),
+                            y[2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u));
+      }
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        const int unit = (map * 2 + part) * (kNQ / 8) + k;  // of eight columns
+        const uint32_t *src = part ? lo : hi;
+        uint8_t *at = p_buf + (unit / 8) * (kTile * 128) + key * G::kPRow +
+                      (((unit % 8) ^ (G::kPRow == 64 ? (key >> 1) & 3 : key & 7)) << 4);
+        if constexpr (kW == 1)
+          *reinterpret_cast<uint16_t *>(at) = static_cast<uint16_t>(src[0]);
+        else if constexpr (kW == 2)
+          *reinterpret_cast<uint32_t *>(at) = src[0];
+        else if constexpr (kW == 4)
+          *reinterpret_cast<uint2 *>(at) = make_uint2(src[0], src[1]);
+        else
+          *reinterpret_cast<uint4 *>(at) = make_uint4(src[0], src[1], src[2], src[3]);
+      }
     }
     fence_async_proxy();
     tc_fence_before_sync();
@@ -783,10 +897,14 @@ __device__ void softmax_warps(const FwdParams &p, uint8_t *smem, Ctrl<kNQ> *sm) 
 
     // ---- end of the segment ----
 #pragma unroll
-    for (int q = 0; q < kNQ; ++q) {
+    for (int q = 0; q < kNR; ++q) {
       if (q >= real) break;
       const float y = warp_sum(l[q]);
       if (lane == 0) sm->lsum[map][quarter][q] = poisoned ? NAN : y;
+    }
+    if (late && lane == 0 && quarter == 0) {  // references of both maps for the kept-out keys
+#pragma unroll
+      for (int q = 0; q < kNR; ++q) sm->ref[map][q] = m[q];
     }
     ok = mbar_wait_warp(&sm->pv_done[t & 1], phase<2>(t), &sm->abort, kWaitNs);
     if (named_barrier_or(2, kConsumers, !ok)) break;
@@ -797,69 +915,63 @@ __device__ void softmax_warps(const FwdParams &p, uint8_t *smem, Ctrl<kNQ> *sm) 
     const bool direct = (d.flags & kDirect) != 0;
     // The row's (m, l): per slot for the join, per item for the weights.
     if (quarter == 0 && lane == 0 && (!direct || p.item_ml != nullptr)) {
-      float2 *ml = (direct ? p.item_ml + static_cast<int64_t>(d.item) * 2 * kNQ
-                           : p.part_ml + static_cast<int64_t>(d.slot) * 2 * kNQ) +
-                   map * kNQ;
+      float2 *ml = (direct ? p.item_ml + static_cast<int64_t>(d.item) * 2 * kNR
+                           : p.part_ml + static_cast<int64_t>(d.slot) * 2 * kNR) +
+                   map * kNR;
 #pragma unroll
-      for (int q = 0; q < kNQ; ++q) {
+      for (int q = 0; q < kNR; ++q) {
         if (q >= real) break;
         ml[q] = make_float2(m[q], l_of(map, q));
       }
     }
-    // References of both maps for the kept-out keys.
-    if (late && lane == 0 && quarter == 0) {
-#pragma unroll
-      for (int q = 0; q < kNQ; ++q) sm->wmax[map][0][q] = m[q];
-    }
-    if (late) named_barrier_sync(2, kConsumers);
     // d = 64: the two halves of the warps take turns at eight rows; d = 128: each has its half of
     // the value columns for all rows.
+    constexpr int kStep = kD == 128 || kChunks == 1 ? 1 : 2;  // chunks per turn
     const int half = warp / 4;
     const int block = kD == 128 ? half : 0;
     const int col = 128 * block + key;
-    const uint32_t o_at = tmem + G::kTmemO + (seg % G::kOBufs) * G::kOCols + block * G::kPRows;
-    float o[kNQ <= 8 || kD == 128 ? kNQ : kNQ / 2];
-    constexpr int kChunks = kNQ / 8;
-    constexpr int kStep = kD == 128 || kChunks == 1 ? 1 : 2;  // chunks per pass of the loop
     const bool idle = kD == 64 && kChunks == 1 && half == 1;
+    const uint32_t o_at = tmem + G::kTmemO + (seg % G::kOBufs) * G::kOCols + block * G::kPCols;
+    float o[kW * kChunks / kStep];
 #pragma unroll
     for (int k = 0; k < kChunks / kStep; ++k) {
-      const int q8 = 8 * (kStep * k + (kStep == 2 ? half : 0));
-      if (idle || q8 >= real) break;
-      uint32_t o1[2][8], o2[2][8];
-      tmem_ld_x8(o_at + q8, o1[0]);
-      tmem_ld_x8(o_at + kNQ + q8, o1[1]);
-      tmem_ld_x8(o_at + 2 * kNQ + q8, o2[0]);
-      tmem_ld_x8(o_at + 3 * kNQ + q8, o2[1]);
+      const int q0 = kW * (kStep * k + (kStep == 2 ? half : 0));
+      if (idle || q0 >= real) break;
+      uint32_t part[4][kW];  // map 1 hi, lo, map 2 hi, lo
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int q = q8 + e;
+      for (int e = 0; e < 4; ++e) tmem_load(o_at + e * kNQ + q0, part[e]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tmem_loaded(part[e]);
+#pragma unroll
+      for (int e = 0; e < kW; ++e) {
+        const int q = q0 + e;
         if (q >= real) break;
-        float y1 = __uint_as_float(o1[0][e]) + __uint_as_float(o1[1][e]);
-        float y2 = __uint_as_float(o2[0][e]) + __uint_as_float(o2[1][e]);
+        float y1 = __uint_as_float(part[0][e]) + __uint_as_float(part[1][e]);
+        float y2 = __uint_as_float(part[2][e]) + __uint_as_float(part[3][e]);
+#pragma unroll 1
         for (uint32_t rest = late; rest; rest &= rest - 1) {
-          const int back = __ffs(rest) - 1;
-          const int32_t pos = d.len - 1 - back;
+          const int x_back = __ffs(rest) - 1;
+          const int32_t pos = d.len - 1 - x_back;
           const int32_t page =
-              p.page_table[static_cast<int64_t>(d.b) * p.max_pages + pos / p.page_size];
+              p.page_table[static_cast<int64_t>(d.b) * p.max_pages + p.by_page.div(pos)];
           if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) continue;
           const float v = __bfloat162float(
               static_cast<const __nv_bfloat16 *>(p.v_pages)[page * p.vs.b + d.hk * p.vs.h +
-                                                            pos % p.page_size * p.vs.n + col]);
-          const float x1 = sm->late[0][back][q], x2 = sm->late[1][back][q];
-          if (x1 != -INFINITY) y1 += ex2_approx(x1 - sm->wmax[0][0][q]) * v;
-          if (x2 != -INFINITY) y2 += ex2_approx(x2 - sm->wmax[1][0][q]) * v;
+                                                            p.by_page.mod(pos) * p.vs.n + col]);
+          const float x1 = sm->late[0][x_back][q], x2 = sm->late[1][x_back][q];
+          if (x1 != -INFINITY) y1 += ex2_approx(x1 - sm->ref[0][q]) * v;
+          if (x2 != -INFINITY) y2 += ex2_approx(x2 - sm->ref[1][q]) * v;
         }
-        const int r = d.rb * kNQ + q;
+        const int r = d.rb * kNR + q;
         if (direct) {
-          const float lam = __ldg(p.lambda + d.hk * p.group + r % p.group);
+          const float lam = __ldg(p.lambda + d.hk * p.group + p.by_group.mod(r));
           float y = y1 / l_of(0, q) - lam * (y2 / l_of(1, q));
-          if (d.len - p.N + r / p.group < 0 && !poisoned) y = 0.f;  // a row that sees no key
-          o[8 * k + e] = y;
+          if (d.len - p.N + p.by_group.div(r) < 0 && !poisoned) y = 0.f;  // a row that sees no key
+          o[kW * k + e] = y;
         } else if (dbg_ok(d.slot >= 0 && d.slot < 2 * static_cast<int>(gridDim.x), p.status, 42)) {
-          float *dst = p.part + (static_cast<int64_t>(d.slot) * 2 * kNQ + q) * (2 * kD) + col;
+          float *dst = p.part + (static_cast<int64_t>(d.slot) * 2 * kNR + q) * (2 * kD) + col;
           dst[0] = y1;
-          dst[kNQ * (2 * kD)] = y2;
+          dst[kNR * (2 * kD)] = y2;
         }
       }
     }
@@ -870,50 +982,50 @@ __device__ void softmax_warps(const FwdParams &p, uint8_t *smem, Ctrl<kNQ> *sm) 
     if (!direct) continue;
 
     // Head norm: row sums over the lanes, the four quarters and (d = 128) both halves.
-    const auto row_sums = [&](bool square) {  // into rsum
-#pragma unroll
-      for (int k = 0; k < kChunks / kStep; ++k) {
-        const int q8 = 8 * (kStep * k + (kStep == 2 ? half : 0));
-        if (idle || q8 >= real) break;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (q8 + e >= real) break;
-          const float y = warp_sum(square ? o[8 * k + e] * o[8 * k + e] : o[8 * k + e]);
-          if (lane == 0) sm->rsum[kD == 128 ? half : 0][quarter][q8 + e] = y;
-        }
-      }
-      named_barrier_sync(2, kConsumers);
-    };
     const auto row_sum = [&](int q) {
       float y = (sm->rsum[0][0][q] + sm->rsum[0][1][q]) + (sm->rsum[0][2][q] + sm->rsum[0][3][q]);
       if (kD == 128)
         y += (sm->rsum[1][0][q] + sm->rsum[1][1][q]) + (sm->rsum[1][2][q] + sm->rsum[1][3][q]);
       return y;
     };
-    if (p.headnorm == 2) {
-      row_sums(false);
+#pragma unroll 1
+    for (int pass = p.headnorm == 2 ? 0 : 1; pass < 2 && p.headnorm; ++pass) {  // mean, then square
 #pragma unroll
       for (int k = 0; k < kChunks / kStep; ++k) {
-        const int q8 = 8 * (kStep * k + (kStep == 2 ? half : 0));
-        if (idle || q8 >= real) break;
+        const int q0 = kW * (kStep * k + (kStep == 2 ? half : 0));
+        if (idle || q0 >= real) break;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (q8 + e < real) o[8 * k + e] -= row_sum(q8 + e) * (0.5f / kD);
+        for (int e = 0; e < kW; ++e) {
+          if (q0 + e >= real) break;
+          const float y = o[kW * k + e];
+          const float z = warp_sum(pass ? y * y : y);
+          if (lane == 0) sm->rsum[kD == 128 ? half : 0][quarter][q0 + e] = z;
+        }
       }
       named_barrier_sync(2, kConsumers);
+      if (pass == 0) {
+#pragma unroll
+        for (int k = 0; k < kChunks / kStep; ++k) {
+          const int q0 = kW * (kStep * k + (kStep == 2 ? half : 0));
+          if (idle || q0 >= real) break;
+#pragma unroll
+          for (int e = 0; e < kW; ++e)
+            if (q0 + e < real) o[kW * k + e] -= row_sum(q0 + e) * (0.5f / kD);
+        }
+        named_barrier_sync(2, kConsumers);
+      }
     }
-    if (p.headnorm) row_sums(true);
 #pragma unroll
     for (int k = 0; k < kChunks / kStep; ++k) {
-      const int q8 = 8 * (kStep * k + (kStep == 2 ? half : 0));
-      if (idle || q8 >= real) break;
+      const int q0 = kW * (kStep * k + (kStep == 2 ? half : 0));
+      if (idle || q0 >= real) break;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int q = q8 + e;
+      for (int e = 0; e < kW; ++e) {
+        const int q = q0 + e;
         if (q >= real) break;
-        const int r = d.rb * kNQ + q;
-        const int i = r / p.group, h = d.hk * p.group + r - i * p.group;
-        float y = o[8 * k + e];
+        const int r = d.rb * kNR + q;
+        const int i = p.by_group.div(r), h = d.hk * p.group + r - i * p.group;
+        float y = o[kW * k + e];
         if (p.headnorm && (d.len - p.N + i >= 0 || poisoned)) {
           y *= rsqrtf(row_sum(q) * (0.5f / kD) + p.eps) * p.out_scale;
           if (p.norm_w != nullptr) y *= __ldg(p.norm_w + h * (2 * kD) + col);
@@ -924,17 +1036,17 @@ __device__ void softmax_warps(const FwdParams &p, uint8_t *smem, Ctrl<kNQ> *sm) 
   }
 }
 
-template <int kD, bool kFp8, int kNQ>
+template <int kD, bool kFp8, int kNR>
 __global__ void __launch_bounds__(kThreads, 1)
     diffpaged_fwd_kernel(const __grid_constant__ CUtensorMap mk1,
                          const __grid_constant__ CUtensorMap mk2,
                          const __grid_constant__ CUtensorMap mv,
                          const __grid_constant__ FwdParams p) {
-  using G = Geo<kD, kFp8, kNQ>;
-  using L = Layout<kD, kFp8, kNQ>;
+  using G = Geo<kD, kFp8, kNR>;
+  using L = Layout<kD, kFp8, kNR>;
   extern __shared__ uint8_t raw[];
   uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  auto *sm = reinterpret_cast<Ctrl<kNQ> *>(smem + L::kCtrl);
+  auto *sm = reinterpret_cast<Ctrl<kNR> *>(smem + L::kCtrl);
   const int warp = threadIdx.x / 32;
   grid_dependents_launch();
   Share share;
@@ -944,6 +1056,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&mk2);
       tma_prefetch_desc(&mv);
     }
+    grid_dependency_wait();  // the setup up to here overlaps the kernel before
     share = find_share(p);
   } else if (warp == kMmaWarp) {
     tmem_alloc(&sm->tmem, G::kTmemCols);
@@ -970,11 +1083,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   if (warp == kLoadWarp)
-    load_warp<kD, kFp8, kNQ>(p, &mk1, &mk2, &mv, smem, sm, share);
+    load_warp<kD, kFp8, kNR>(p, &mk1, &mk2, &mv, smem, sm, share);
   else if (warp == kMmaWarp)
-    mma_warp<kD, kFp8, kNQ>(p, smem, sm);
+    mma_warp<kD, kFp8, kNR>(p, smem, sm);
   else
-    softmax_warps<kD, kFp8, kNQ>(p, smem, sm);
+    softmax_warps<kD, kFp8, kNR>(p, smem, sm);
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
@@ -1198,16 +1311,16 @@ bool encode_pool(CUtensorMap *map, const void *base, int64_t width, const diffpa
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kD, bool kFp8, int kNQ>
+template <int kD, bool kFp8, int kNR>
 diffattn_status launch_main(const FwdParams &p, const CUtensorMap (&maps)[3], int ctas,
                             cudaStream_t stream) {
-  constexpr size_t kBytes = Layout<kD, kFp8, kNQ>::kBytes;
+  constexpr size_t kBytes = Layout<kD, kFp8, kNR>::kBytes;
   static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
   static std::atomic<bool> attr_set[64];  // per device (concurrent callers may both set)
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DIFFATTN_ERR_CUDA;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(diffpaged_fwd_kernel<kD, kFp8, kNQ>,
+    if (cudaFuncSetAttribute(diffpaged_fwd_kernel<kD, kFp8, kNR>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kBytes)) != cudaSuccess)
       return DIFFATTN_ERR_CUDA;
@@ -1218,7 +1331,12 @@ diffattn_status launch_main(const FwdParams &p, const CUtensorMap (&maps)[3], in
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kBytes;
   cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, diffpaged_fwd_kernel<kD, kFp8, kNQ>, maps[0], maps[1], maps[2],
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, diffpaged_fwd_kernel<kD, kFp8, kNR>, maps[0], maps[1], maps[2],
                             p) == cudaSuccess
              ? DIFFATTN_OK
              : DIFFATTN_ERR_CUDA;
@@ -1227,9 +1345,14 @@ diffattn_status launch_main(const FwdParams &p, const CUtensorMap (&maps)[3], in
 template <int kD, bool kFp8>
 diffattn_status launch_rows(const FwdParams &p, const CUtensorMap (&maps)[3],
                             const PagedFwdPlan &plan, cudaStream_t stream) {
-  if (plan.row_tile == 8) return launch_main<kD, kFp8, 8>(p, maps, plan.ctas, stream);
-  if (plan.row_tile == 16) return launch_main<kD, kFp8, 16>(p, maps, plan.ctas, stream);
-  return launch_main<kD, kFp8, 32>(p, maps, plan.ctas, stream);
+  switch (plan.row_tile) {
+    case 1: return launch_main<kD, kFp8, 1>(p, maps, plan.ctas, stream);
+    case 2: return launch_main<kD, kFp8, 2>(p, maps, plan.ctas, stream);
+    case 4: return launch_main<kD, kFp8, 4>(p, maps, plan.ctas, stream);
+    case 8: return launch_main<kD, kFp8, 8>(p, maps, plan.ctas, stream);
+    case 16: return launch_main<kD, kFp8, 16>(p, maps, plan.ctas, stream);
+    default: return launch_main<kD, kFp8, 32>(p, maps, plan.ctas, stream);
+  }
 }
 
 template <int kD>
@@ -1261,7 +1384,8 @@ bool plan_paged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache, boo
   PagedFwdPlan &q = *plan;
   q = PagedFwdPlan{};
   const int64_t rows = desc.N * (desc.H / cache.kv_heads);
-  q.row_tile = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  q.row_tile = 1;
+  while (q.row_tile < rows && q.row_tile < 32) q.row_tile *= 2;
   const int64_t row_tile = q.row_tile;
   q.row_blocks = static_cast<int>((rows + row_tile - 1) / row_tile);
   const double items = static_cast<double>(desc.B) * static_cast<double>(cache.kv_heads) * q.row_blocks;
@@ -1271,7 +1395,8 @@ bool plan_paged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache, boo
   const int64_t units = (most + kTile - 1) / kTile;
   q.padded = units * kTile;
   // One CTA per item where no item can have more tiles than the join's launch would cost.
-  q.whole = units <= 2;
+  if (items * static_cast<double>(units) >= 2147483648.0) return false;
+  q.whole = units <= 2 && q.items <= sm_count;
   q.ctas = q.whole ? static_cast<int>(q.items) : sm_count;
   if (!q.whole && q.items * units < sm_count) q.ctas = static_cast<int>(q.items * units);
   const size_t slots = q.whole ? 0 : 2 * static_cast<size_t>(q.ctas);
@@ -1328,6 +1453,8 @@ diffattn_status launch_paged_fwd(const diffattn_desc &desc, const diffpaged_cach
   p.page_size = cache.page_size;
   p.piece_rows = cache.page_size % 64 == 0 ? 64 : cache.page_size % 32 == 0 ? 32 : 16;
   p.row_blocks = plan.row_blocks;
+  p.by_page = fast_div(static_cast<uint32_t>(p.page_size));
+  p.by_group = fast_div(static_cast<uint32_t>(p.group));
   p.causal = desc.causal ? 1 : 0;
   p.headnorm = desc.headnorm;
   p.whole = plan.whole ? 1 : 0;
