@@ -24,7 +24,7 @@ struct PagedFwdPlan {
   int row_blocks;  // row blocks per key/value head
   int64_t items;   // B * kv_heads * row_blocks
   int64_t padded;  // keys per sequence in the logit buffer, a multiple of kPagedTile
-  size_t part, stats, records, items_rec, item_stats, logits;  // workspace offsets, bytes
+  size_t part, stats, item_stats, logits;  // workspace offsets, bytes
   size_t bytes;
 };
 

@@ -51,13 +51,13 @@ namespace {
 
 constexpr int kTile = kPagedTile;
 constexpr int kConsumers = 256;  // softmax and epilogue threads
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = kConsumers + 64;
+constexpr int kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10;
+constexpr int kThreads = kConsumers + 96;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kGrowth = 8.f;  // log2 units a logit may pass the reference maximum by
 constexpr int kMaxBad = 16;     // new tokens of a call, so more than keys that only some of them see
-constexpr int kRing = 8;        // tile descriptors; at most 5 tiles are between load and epilogue
+constexpr int kRing = 8;        // tile descriptors; fewer tiles are between load and epilogue
 constexpr int kBoxBytes = kTile * 128;   // 64 bf16 columns of a tile
 constexpr int kSlotBytes = 2 * kBoxBytes;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -65,7 +65,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 enum : int32_t { kFirst = 1, kLast = 2, kStop = 4, kBad = 8, kDirect = 16 };
 
 struct TileDesc {
-  int32_t b, hk, rb, key0;
+  int32_t b, hk, real, key0;  // real: rows of the block
   int32_t len, flags, slot, item;
 };
 
@@ -98,16 +98,21 @@ struct FwdParams {
   int32_t row_blocks, causal, headnorm, whole;
   FastDiv by_page, by_group;  // page_size, group
   float eps, out_scale, scale_log2;
-  // Workspace (see PagedFwdPlan): partial O [2 C][2][NQ][2 d], their (m, l), one join record per
-  // CTA, and for accumulate one record per item, whole items' (m, l) and all logits.
+  // Workspace (see PagedFwdPlan): partial O [2 C][2][NR][2 d] and their (m, l), and for accumulate
+  // whole items' (m, l) and all logits.
   float *part;
   float2 *part_ml;
-  int4 *records;
-  int2 *item_records;
   float2 *item_ml;
   float *logits;  // [B * kv_heads][2][rows][padded], log2 units, or null
   int64_t padded;
   float *weights;
+};
+
+// One row of a segment, as the softmax warps need it.
+struct RowInfo {
+  int32_t last;   // the last key that it sees, -1 for none
+  int32_t head;   // query head
+  int64_t out;    // element offset of its output
 };
 
 // kNR: rows of a block (1, 2, 4, 8, 16 or 32), padded to kNQ = 8, 16 or 32 in the products.
@@ -145,7 +150,8 @@ struct Ctrl {
   float late[2][kMaxBad][kNR];  // logits of keys kept out of the product,
   float ref[2][kNR];            // and the references they go with
   TileDesc ring[kRing];
-  uint64_t full[6], empty[6];
+  RowInfo rows[kRing][kNR];  // by segment
+  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_empty[2], drain;
   uint32_t bad_rows[3];
   uint32_t tmem;
@@ -160,10 +166,14 @@ struct Layout {
   static constexpr int kFixed = kQ + 4 * G::kQBytes;  // then the ring, then Ctrl
   static constexpr int kRoom =
       227 * 1024 - 1024 - static_cast<int>(sizeof(Ctrl<kNR>)) - kFixed;
+  // The ring of keys and that of values: each is filled by a warp of its own and emptied in order.
   static constexpr int kSlots = kRoom / kSlotBytes < 6 ? kRoom / kSlotBytes : 6;
-  static_assert(kSlots >= G::kTileSlots, "one tile must fit");
-  static constexpr int kRingAt = kFixed;
-  static constexpr int kCtrl = kRingAt + kSlots * kSlotBytes;
+  static constexpr int kShare = kSlots * G::kKeySlots / G::kTileSlots;
+  static constexpr int kKeyRing = kShare < G::kKeySlots ? G::kKeySlots : kShare;
+  static constexpr int kValRing = kSlots - kKeyRing;
+  static_assert(kValRing >= G::kValSlots, "one tile must fit");
+  static constexpr int kKeyAt = kFixed, kValAt = kKeyAt + kKeyRing * kSlotBytes;
+  static constexpr int kCtrl = kFixed + kSlots * kSlotBytes;
   static constexpr int kBytes = 1024 + kCtrl + static_cast<int>(sizeof(Ctrl<kNR>));
 };
 
@@ -287,15 +297,15 @@ struct Share {
   int32_t b, hk, rb, tile, len, units;
 };
 
-// One warp, uniform.
-__device__ __forceinline__ Share find_share(const FwdParams &p) {
+// CTA `cta`'s share of `ctas` CTAs (one warp, uniform).
+__device__ __forceinline__ Share find_share(const FwdParams &p, uint32_t cta, uint32_t ctas) {
   const int lane = threadIdx.x % 32;
   const int32_t most = p.max_pages * p.page_size;
   Share s = {{1, 1, 0}, 0, 0, 0, 0, 0, 0, 0, 1};
   const uint32_t heads = p.kv_heads * p.row_blocks;  // items of a sequence
   if (p.whole) {
-    s.b = blockIdx.x / heads;
-    const uint32_t item = blockIdx.x - s.b * heads;
+    s.b = cta / heads;
+    const uint32_t item = cta - s.b * heads;
     s.hk = item / p.row_blocks;
     s.rb = item - s.hk * p.row_blocks;
     s.len = __ldg(p.kv_len + s.b);
@@ -319,12 +329,12 @@ __device__ __forceinline__ Share find_share(const FwdParams &p) {
   }
   total *= heads;
   // Every share has at least one tile (the last CTAs may have none).
-  s.all.ctas = min(gridDim.x, total);
+  s.all.ctas = min(ctas, total);
   s.all.each = total / s.all.ctas;
   s.all.more = total - s.all.each * s.all.ctas;
-  if (blockIdx.x < s.all.ctas) {
-    s.begin = s.all.begin(blockIdx.x);
-    s.todo = s.all.each + (blockIdx.x < s.all.more ? 1 : 0);
+  if (cta < s.all.ctas) {
+    s.begin = s.all.begin(cta);
+    s.todo = s.all.each + (cta < s.all.more ? 1 : 0);
     uint32_t left = s.begin;  // tiles before the share, counted down sequence by sequence
 #pragma unroll 1
     for (int32_t b0 = 0; b0 < p.B; b0 += 32) {
@@ -356,25 +366,27 @@ __device__ __forceinline__ Share find_share(const FwdParams &p) {
   return s;
 }
 
-// The join record of an item that is cut: written by the CTA whose share
-// begins where that of the CTA with the item's first tile ends.
-__device__ __forceinline__ void write_record(const FwdParams &p, const Share &s) {
-  int4 rec = make_int4(-1, 0, 0, 0);
-  if (s.tile > 0) {
-    const uint32_t start = s.begin - s.tile;
-    const uint32_t c0 = s.all.cta_of(start);
-    if (s.begin == s.all.begin(c0 + 1))
-      rec = make_int4((s.b * p.kv_heads + s.hk) * p.row_blocks + s.rb,
-                      static_cast<int>(2 * c0 + (s.all.begin(c0) < start ? 1 : 0)),
-                      static_cast<int>(s.all.cta_of(start + s.units - 1) - c0 + 1), 0);
+// The parts that an item's tiles start .. start + units - 1 are cut into: CTA c0's is in slot
+// 2 c0 + 1 where its share begins before the item and in 2 c0 otherwise, the next ones' in
+// 2 (c0 + 1), 2 (c0 + 2) ..
+struct Parts {
+  int32_t first, n;
+  __device__ __forceinline__ int32_t slot(int32_t k) const {
+    return k == 0 ? first : 2 * (first / 2 + k);
   }
-  p.records[blockIdx.x] = rec;
+};
+__device__ __forceinline__ Parts parts_of(const Shares &all, uint32_t start, uint32_t units) {
+  const uint32_t c0 = all.cta_of(start);
+  return {static_cast<int32_t>(2 * c0 + (all.begin(c0) < start ? 1 : 0)),
+          static_cast<int32_t>(all.cta_of(start + units - 1) - c0 + 1)};
 }
 
 // ---------------------------------------------------------------------------
-// The load warp: describes the share's tiles and issues their copies.
+// The load warps, one for the keys (with the tiles' descriptions and the q rows) and one for the
+// values: a copy takes one thread 80 to 130 cycles to issue, and a tile in pages of 16 rows has 32
+// of them, which one warp issues more slowly than HBM delivers.
 // ---------------------------------------------------------------------------
-template <int kD, bool kFp8, int kNR>
+template <int kD, bool kFp8, int kNR, bool kKeys>
 __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap *mk1,
                                           const CUtensorMap *mk2, const CUtensorMap *mv,
                                           uint8_t *smem, Ctrl<kNR> *sm, const Share &share) {
@@ -395,7 +407,6 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
                : 0;
   };
   bool ok = true;
-  uint32_t c = 0;      // slots used
   uint32_t it = 0;     // tiles
   uint32_t seg = 0;    // segments (the share's parts of items)
   int32_t seg_start = tile;
@@ -403,35 +414,44 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
   int32_t id = share.todo > 0 ? page_of(tile) : 0;
   // Read once (by one row block), the pages leave L2 before anything else does.
   const uint64_t policy = p.row_blocks == 1 ? l2_evict_first() : l2_evict_normal();
+  constexpr int kPerTile = kKeys ? G::kKeySlots : G::kValSlots;
+  constexpr int kSlots = kKeys ? L::kKeyRing : L::kValRing;
+  uint64_t *full = kKeys ? sm->k_full : sm->v_full;
+  uint64_t *empty = kKeys ? sm->k_empty : sm->v_empty;
+  uint8_t *ring = smem + (kKeys ? L::kKeyAt : L::kValAt) + box * kBoxBytes;
+  const auto freed = [&](uint32_t c) {  // the slot of use c is free again
+    return c < kSlots ||
+           mbar_wait_warp(&empty[c % kSlots], phase<kSlots>(c - kSlots), &sm->abort, kWaitNs);
+  };
+#pragma unroll 1
   for (uint32_t left = share.todo; ok && left > 0; --left, ++it) {
     const bool valid_len = len >= 0 && len <= most;
     const bool seg_last = tile + 1 == units || left == 1;
-    const int32_t page = id;
-    TileDesc d;
-    d.b = b;
-    d.hk = hk;
-    d.rb = rb;
-    d.key0 = tile * kTile;
-    d.len = valid_len ? len : 0;
-    d.slot = slot;
-    d.flags = (tile == seg_start ? kFirst : 0) | (seg_last ? kLast : 0) |
-              (seg_start == 0 && tile + 1 == units ? kDirect : 0);
-    d.item = (b * p.kv_heads + hk) * p.row_blocks + rb;
-    const int32_t keys = max(0, min(kTile, d.len - d.key0));  // 0 for an idle sequence
+    const int32_t page = id, head = hk, key0 = tile * kTile;
+    const int32_t tile_len = valid_len ? len : 0;
+    const int32_t keys = max(0, min(kTile, tile_len - key0));  // 0 for an idle sequence
     const bool have = piece_ok && first_row < keys;
     const bool bad_id = have && static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages);
-    const bool bad = __any_sync(0xffffffffu, bad_id) || !valid_len;
-    if (bad) d.flags |= kBad;
-    if (p.item_records != nullptr && lane == 0 && tile == 0) {
-      int32_t n = 1;
-      if (!p.whole)
-        n = static_cast<int32_t>(
-            share.all.cta_of(share.begin + (share.todo - left) + units - 1) - blockIdx.x + 1);
-      p.item_records[d.item] = make_int2(slot, n);
-    }
-    const int32_t row = p.by_page.mod(d.key0 + first_row);
+    const int32_t row = p.by_page.mod(key0 + first_row);
     const int32_t z = bad_id ? 0 : page;
     const int32_t rows = (keys + p.piece_rows - 1) & -p.piece_rows;
+    const bool seg_first = tile == seg_start;
+    TileDesc d;
+    int32_t q_row = 0;
+    if (kKeys) {
+      const bool bad = __any_sync(0xffffffffu, bad_id) || !valid_len;
+      d.b = b;
+      d.hk = hk;
+      d.real = min(kNR, p.rows - rb * kNR);
+      d.key0 = key0;
+      d.len = tile_len;
+      d.slot = slot;
+      d.flags = (seg_first ? kFirst : 0) | (seg_last ? kLast : 0) | (bad ? kBad : 0) |
+                (seg_start == 0 && tile + 1 == units ? kDirect : 0);
+      d.item = (b * p.kv_heads + hk) * p.row_blocks + rb;
+      q_row = rb * kNR;
+      if (bad && lane == 0) report_bad_page(p.status);
+    }
     // Move on; the next tile's page numbers are fetched while buffers are awaited.
     if (seg_last) {
       seg_start = 0;
@@ -452,81 +472,80 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
       }
     }
     if (left > 1) id = page_of(tile);
+    if (kKeys && seg_first && lane < kNR) {  // the segment's rows
+      const int32_t r = q_row + lane;
+      const int32_t i = p.by_group.div(r), pos = tile_len - p.N + i;
+      RowInfo info;
+      info.last = r >= p.rows || pos < 0 ? -1 : p.causal ? pos : tile_len - 1;
+      info.head = d.hk * p.group + r - i * p.group;
+      info.out = d.b * p.outs.b + info.head * p.outs.h + i * p.outs.n;
+      sm->rows[seg % kRing][lane] = info;
+    }
+    __syncwarp();
 #pragma unroll 1
-    for (int k = 0; k < G::kTileSlots; ++k, ++c) {
-      // The segment's q rows, between its first keys and values (the products may wait for them
-      // before they free a slot for the values): 16-byte units into the swizzled operand layout.
-      if (k == G::kKeySlots && (d.flags & kFirst)) {
-        const uint32_t qb = seg & 1;
-        if (seg >= 2 &&
-            !(ok = mbar_wait_warp(&sm->q_empty[qb], phase<2>(seg - 2), &sm->abort, kWaitNs)))
-          break;
-        constexpr int kUnits = G::kKeyRow / 16;
-        const int real = min(kNR, p.rows - d.rb * kNR);
-        for (int x = lane; x < 2 * real * kUnits; x += 32) {
-          const int map = x >= real * kUnits, y = x - map * real * kUnits;
-          const int q = y / kUnits, u = y % kUnits;
-          const int r = d.rb * kNR + q;
-          const int i = p.by_group.div(r), h = d.hk * p.group + r - i * p.group;
-          const diffattn_strides &qs = map ? p.q2s : p.q1s;
-          const int64_t at = d.b * qs.b + h * qs.h + i * qs.n;
-          const uint8_t *src =
-              static_cast<const uint8_t *>(map ? p.q2 : p.q1) + at * (kFp8 ? 1 : 2) + 16 * u;
-          uint32_t off;
-          if (G::kKeyRow == 64)
-            off = q * 64 + ((u ^ ((q >> 1) & 3)) << 4);
-          else
-            off = (u / 8) * (G::kNS * 128) + q * 128 + (((u % 8) ^ (q & 7)) << 4);
-          cp_async16(smem_u32(smem + L::kQ + (2 * qb + map) * G::kQBytes) + off, src);
-        }
-        cp_async_arrive(&sm->q_full[qb]);
-        ++seg;
-      }
-      const int s = c % L::kSlots;
-      if (c >= L::kSlots &&
-          !(ok = mbar_wait_warp(&sm->empty[s], phase<L::kSlots>(c - L::kSlots), &sm->abort,
-                                kWaitNs)))
-        break;
-      const bool keys_slot = k < G::kKeySlots;
-      const int row_bytes = keys_slot ? G::kKeyBox : 128;
+    for (int k = 0; k < kPerTile; ++k) {
+      const uint32_t c = it * kPerTile + k;
+      const int s = c % kSlots;
+      if (!(ok = freed(c))) break;
+      const int row_bytes = kKeys ? G::kKeyBox : 128;
       if (lane == 0) {
-        if (k == 0) {
-          if (bad) report_bad_page(p.status);
-          sm->ring[it % kRing] = d;
-        }
+        if (kKeys && k == 0) sm->ring[it % kRing] = d;
         if (rows > 0)
-          mbar_arrive_expect_tx(&sm->full[s], static_cast<uint32_t>(rows) * 2 * row_bytes);
+          mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(rows) * 2 * row_bytes);
         else
-          mbar_arrive(&sm->full[s]);
+          mbar_arrive(&full[s]);
       }
       __syncwarp();
       if (have) {
-        const CUtensorMap *map =
-            !keys_slot ? mv : (G::kKeySlots == 1 ? box : k) ? mk2 : mk1;
-        const int x = !keys_slot ? 128 * (k - G::kKeySlots) + 64 * box
-                                 : G::kKeySlots == 1 ? 0 : 64 * box;
-        tma_load_4d_hint(smem + L::kRingAt + s * kSlotBytes + box * kBoxBytes +
-                             first_row * row_bytes,
-                         map, &sm->full[s], x, row, d.hk, z, policy);
+        const CUtensorMap *map = !kKeys ? mv : (G::kKeySlots == 1 ? box : k) ? mk2 : mk1;
+        const int x = !kKeys ? 128 * k + 64 * box : G::kKeySlots == 1 ? 0 : 64 * box;
+        tma_load_4d_hint(ring + s * kSlotBytes + first_row * row_bytes, map, &full[s], x, row, head,
+                         z, policy);
       }
     }
+    // The segment's q rows: 16-byte units into the swizzled operand layout.
+    if (kKeys && ok && seg_first) {
+      const uint32_t qb = seg & 1;
+      if (seg >= 2 &&
+          !(ok = mbar_wait_warp(&sm->q_empty[qb], phase<2>(seg - 2), &sm->abort, kWaitNs)))
+        break;
+      constexpr int kUnits = G::kKeyRow / 16;
+#pragma unroll 1
+      for (int x = lane; x < 2 * d.real * kUnits; x += 32) {
+        const int map = x >= d.real * kUnits, y = x - map * d.real * kUnits;
+        const int q = y / kUnits, u = y % kUnits;
+        const int r = q_row + q;
+        const int i = p.by_group.div(r), h = d.hk * p.group + r - i * p.group;
+        const diffattn_strides &qs = map ? p.q2s : p.q1s;
+        const int64_t at = d.b * qs.b + h * qs.h + i * qs.n;
+        const uint8_t *src =
+            static_cast<const uint8_t *>(map ? p.q2 : p.q1) + at * (kFp8 ? 1 : 2) + 16 * u;
+        uint32_t off;
+        if (G::kKeyRow == 64)
+          off = q * 64 + ((u ^ ((q >> 1) & 3)) << 4);
+        else
+          off = (u / 8) * (G::kNS * 128) + q * 128 + (((u % 8) ^ (q & 7)) << 4);
+        cp_async16(smem_u32(smem + L::kQ + (2 * qb + map) * G::kQBytes) + off, src);
+      }
+      cp_async_arrive(&sm->q_full[qb]);
+      ++seg;
+    }
   }
-  if (!p.whole && lane == 0) write_record(p, share);
   // The end mark takes the next slot's turn; then the copies still in flight
   // are awaited (bounded), so that none lands after the CTA is gone.
-  if (ok && (c < L::kSlots || mbar_wait_warp(&sm->empty[c % L::kSlots],
-                                             phase<L::kSlots>(c - L::kSlots), &sm->abort, kWaitNs))) {
+  uint32_t end = it * kPerTile;
+  if (kKeys && ok && freed(end)) {
     if (lane == 0) {
       sm->ring[it % kRing].flags = kStop;
-      mbar_arrive(&sm->full[c % L::kSlots]);
+      mbar_arrive(&full[end % kSlots]);
     }
-    ++c;
+    ++end;
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (kKeys) asm volatile("cp.async.wait_all;" ::: "memory");
   if (lane == 0) {
     volatile int never = 0;
-    for (uint32_t k = c > L::kSlots ? c - L::kSlots : 0; k < c; ++k)
-      mbar_wait(&sm->full[k % L::kSlots], phase<L::kSlots>(k), &never, kDrainNs);
+    for (uint32_t c = end > kSlots ? end - kSlots : 0; c < end; ++c)
+      mbar_wait(&full[c % kSlots], phase<kSlots>(c), &never, kDrainNs);
   }
 }
 
@@ -548,20 +567,17 @@ __device__ __forceinline__ void mma_warp(const FwdParams &p, uint8_t *smem, Ctrl
   const auto ready = [&](uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_test(bar, parity));
   };
-  const auto slot_at = [&](uint32_t c) {
-    return smem_u32(smem + L::kRingAt + (c % L::kSlots) * kSlotBytes);
-  };
 
   // Tile t's turn in O and tile n's in S; n runs at most one ahead, where its keys are there.
-  // The tests below see the right phase: the slot's use before was consumed by tile n - 1 or
-  // earlier.
+  // The tests see the right phase: the slot's use before was consumed by an earlier tile.
   uint32_t t = 0, n = 0, segs = 0, o_segs = 0;
   int32_t s_flags = 0, o_flags = 0, ahead_flags = 0;  // of S's last tile; of tiles t, t + 1
   uint64_t since = 0;
 #pragma unroll 1
   while (true) {
-    const uint32_t cs = n * G::kTileSlots;
-    if (n <= t + 1 && !(s_flags & kStop) && ready(&sm->full[cs % L::kSlots], phase<L::kSlots>(cs))) {
+    const uint32_t cs = n * G::kKeySlots;
+    if (n <= t + 1 && !(s_flags & kStop) &&
+        ready(&sm->k_full[cs % L::kKeyRing], phase<L::kKeyRing>(cs))) {
       s_flags = *reinterpret_cast<volatile int32_t *>(&sm->ring[n % kRing].flags);
       (n == t ? o_flags : ahead_flags) = s_flags;
       if (s_flags & kStop) {
@@ -578,9 +594,10 @@ __device__ __forceinline__ void mma_warp(const FwdParams &p, uint8_t *smem, Ctrl
         for (int map = 0; map < 2; ++map) {
           const uint32_t c = cs + (G::kKeySlots == 2 ? map : 0);
           if (G::kKeySlots == 2 && map == 1 &&
-              !wait(&sm->full[c % L::kSlots], phase<L::kSlots>(c)))
+              !wait(&sm->k_full[c % L::kKeyRing], phase<L::kKeyRing>(c)))
             break;
-          const uint32_t k_at = slot_at(c) + (G::kKeySlots == 1 ? map * kBoxBytes : 0);
+          const uint32_t k_at = smem_u32(smem + L::kKeyAt + (c % L::kKeyRing) * kSlotBytes) +
+                                (G::kKeySlots == 1 ? map * kBoxBytes : 0);
           const uint32_t q_at = smem_u32(smem + L::kQ + (2 * qb + map) * G::kQBytes);
           const uint32_t acc = tmem + (n & 1) * 2 * G::kNS + map * G::kNS;
 #pragma unroll
@@ -599,7 +616,7 @@ __device__ __forceinline__ void mma_warp(const FwdParams &p, uint8_t *smem, Ctrl
                 umma_bf16(acc, a, q, kIdS, kk > 0);
             }
           }
-          if (G::kKeySlots == 2 || map == 1) umma_commit_warp(&sm->empty[c % L::kSlots]);
+          if (G::kKeySlots == 2 || map == 1) umma_commit_warp(&sm->k_empty[c % L::kKeyRing]);
         }
         if (*reinterpret_cast<volatile int *>(&sm->abort)) break;
         umma_commit_warp(&sm->s_full[n & 1]);
@@ -622,17 +639,18 @@ __device__ __forceinline__ void mma_warp(const FwdParams &p, uint8_t *smem, Ctrl
       bool ok = true;
 #pragma unroll 1
       for (int k = 0; k < G::kValSlots; ++k) {
-        const uint32_t c = t * G::kTileSlots + G::kKeySlots + k;
-        if (!(ok = wait(&sm->full[c % L::kSlots], phase<L::kSlots>(c)))) break;
+        const uint32_t c = t * G::kValSlots + k;
+        if (!(ok = wait(&sm->v_full[c % L::kValRing], phase<L::kValRing>(c)))) break;
         tc_fence_after_sync();
-        const uint64_t v = smem_desc_sw128(slot_at(c), kBoxBytes, 1024);
+        const uint64_t v = smem_desc_sw128(
+            smem_u32(smem + L::kValAt + (c % L::kValRing) * kSlotBytes), kBoxBytes, 1024);
         const uint64_t w = G::kPRow == 64 ? smem_desc_sw64(p_at)
                                           : smem_desc_sw128(p_at, kTile * 128, 1024);
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)  // 16 keys each
           umma_bf16(o_at + k * G::kPCols, v + 128 * kk, w + G::kPRow * kk, kIdO,
                     !(o_flags & kFirst) || kk > 0);
-        umma_commit_warp(&sm->empty[c % L::kSlots]);
+        umma_commit_warp(&sm->v_empty[c % L::kValRing]);
       }
       if (!ok) break;
       umma_commit_warp(&sm->pv_done[t & 1]);
@@ -672,8 +690,8 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
   const int key = 32 * quarter + lane;  // of the tile
   const uint32_t tmem = sm->tmem + (static_cast<uint32_t>(32 * quarter) << 16);
   const auto v_row = [&](uint32_t t, int row, int u) {  // unit u of value row `row` of tile t
-    const uint32_t c = t * G::kTileSlots + G::kKeySlots + u / 16;
-    return reinterpret_cast<uint4 *>(smem + L::kRingAt + (c % L::kSlots) * kSlotBytes +
+    const uint32_t c = t * G::kValSlots + u / 16;
+    return reinterpret_cast<uint4 *>(smem + L::kValAt + (c % L::kValRing) * kSlotBytes +
                                      ((u / 8) % 2) * kBoxBytes + row * 128 + (u % 8) * 16);
   };
 
@@ -690,7 +708,8 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
     const bool masked = d.key0 + kTile - 1 > lim_min;
     const int32_t keys = d.len - d.key0;  // valid rows of the tile if below kTile
     const bool mixed = p.causal && p.N > 1 && masked;  // some rows see keys that others do not
-    const int real = kNR == 1 ? 1 : min(kNR, p.rows - d.rb * kNR);  // rows of this block
+    const int real = kNR == 1 ? 1 : d.real;
+    const RowInfo *rows = sm->rows[seg % kRing];
     const uint32_t s_at = tmem + (t & 1) * 2 * G::kNS + map * G::kNS;
 
     // This key's logits of rows kW k .. kW k + kW - 1, in log2 units; -inf where it is masked.
@@ -703,12 +722,8 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
       for (int e = 0; e < kW; ++e) x[e] = __uint_as_float(raw[e]) * p.scale_log2;
       if (masked) {
 #pragma unroll
-        for (int e = 0; e < kW; ++e) {
-          // Row r sees keys up to its own position (causal) or all; padding rows see none.
-          const int32_t pos = d.len - p.N + p.by_group.div(d.rb * kNR + kW * k + e);
-          const int32_t lim = pos < 0 ? -1 : p.causal ? pos : d.len - 1;
-          if (d.key0 + key > lim) x[e] = -INFINITY;
-        }
+        for (int e = 0; e < kW; ++e)
+          if (d.key0 + key > rows[kW * k + e].last) x[e] = -INFINITY;
       }
     };
 
@@ -736,7 +751,8 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
         if (p.logits != nullptr && key < keys) {
           float *dst = p.logits +
                        ((static_cast<int64_t>(d.b) * p.kv_heads + d.hk) * 2 + map) * p.rows * p.padded +
-                       static_cast<int64_t>(d.rb * kNR + kW * k) * p.padded + d.key0 + key;
+                       static_cast<int64_t>(d.item % p.row_blocks * kNR + kW * k) * p.padded +
+                       d.key0 + key;
 #pragma unroll
           for (int e = 0; e < kW; ++e)
             if (kW * k + e < real && dbg_ok(d.key0 + key < p.padded, p.status, 41))
@@ -753,9 +769,9 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
       if (ok && (keys < kTile || mixed)) {
 #pragma unroll 1
         for (int k = 0; k < G::kValSlots; ++k) {
-          const uint32_t c = t * G::kTileSlots + G::kKeySlots + k;
-          ok = ok && mbar_wait_warp(&sm->full[c % L::kSlots], phase<L::kSlots>(c), &sm->abort,
-                                    kWaitNs);
+          const uint32_t c = t * G::kValSlots + k;
+          ok = ok && mbar_wait_warp(&sm->v_full[c % L::kValRing], phase<L::kValRing>(c),
+                                    &sm->abort, kWaitNs);
         }
         if (ok) {
           const int from = max(0, keys);
@@ -962,11 +978,10 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
           if (x1 != -INFINITY) y1 += ex2_approx(x1 - sm->ref[0][q]) * v;
           if (x2 != -INFINITY) y2 += ex2_approx(x2 - sm->ref[1][q]) * v;
         }
-        const int r = d.rb * kNR + q;
         if (direct) {
-          const float lam = __ldg(p.lambda + d.hk * p.group + p.by_group.mod(r));
+          const float lam = __ldg(p.lambda + rows[q].head);
           float y = y1 / l_of(0, q) - lam * (y2 / l_of(1, q));
-          if (d.len - p.N + p.by_group.div(r) < 0 && !poisoned) y = 0.f;  // a row that sees no key
+          if (rows[q].last < 0 && !poisoned) y = 0.f;  // a row that sees no key
           o[kW * k + e] = y;
         } else if (dbg_ok(d.slot >= 0 && d.slot < 2 * static_cast<int>(gridDim.x), p.status, 42)) {
           float *dst = p.part + (static_cast<int64_t>(d.slot) * 2 * kNR + q) * (2 * kD) + col;
@@ -1023,14 +1038,12 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
       for (int e = 0; e < kW; ++e) {
         const int q = q0 + e;
         if (q >= real) break;
-        const int r = d.rb * kNR + q;
-        const int i = p.by_group.div(r), h = d.hk * p.group + r - i * p.group;
         float y = o[kW * k + e];
-        if (p.headnorm && (d.len - p.N + i >= 0 || poisoned)) {
+        if (p.headnorm && (rows[q].last >= 0 || poisoned)) {
           y *= rsqrtf(row_sum(q) * (0.5f / kD) + p.eps) * p.out_scale;
-          if (p.norm_w != nullptr) y *= __ldg(p.norm_w + h * (2 * kD) + col);
+          if (p.norm_w != nullptr) y *= __ldg(p.norm_w + rows[q].head * (2 * kD) + col);
         }
-        p.out[d.b * p.outs.b + h * p.outs.h + i * p.outs.n + col] = __float2bfloat16_rn(y);
+        p.out[rows[q].out + col] = __float2bfloat16_rn(y);
       }
     }
   }
@@ -1048,23 +1061,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   auto *sm = reinterpret_cast<Ctrl<kNR> *>(smem + L::kCtrl);
   const int warp = threadIdx.x / 32;
-  grid_dependents_launch();
   Share share;
-  if (warp == kLoadWarp) {
+  if (warp == kKeyWarp || warp == kValueWarp) {
     if (threadIdx.x % 32 == 0) {
-      tma_prefetch_desc(&mk1);
-      tma_prefetch_desc(&mk2);
-      tma_prefetch_desc(&mv);
+      if (warp == kKeyWarp) {
+        tma_prefetch_desc(&mk1);
+        tma_prefetch_desc(&mk2);
+      } else {
+        tma_prefetch_desc(&mv);
+      }
     }
-    grid_dependency_wait();  // the setup up to here overlaps the kernel before
-    share = find_share(p);
+    // The setup up to here overlaps the kernel before; the kernel after may start its own from
+    // here on, so that what it reads before it waits for this one is what this one reads.
+    grid_dependency_wait();
+    grid_dependents_launch();
+    share = find_share(p, blockIdx.x, gridDim.x);
   } else if (warp == kMmaWarp) {
     tmem_alloc(&sm->tmem, G::kTmemCols);
     tmem_relinquish();
   } else if (threadIdx.x == 0) {
-    for (int s = 0; s < L::kSlots; ++s) {
-      mbar_init(&sm->full[s], 1);
-      mbar_init(&sm->empty[s], 1);
+    for (int s = 0; s < L::kKeyRing; ++s) {
+      mbar_init(&sm->k_full[s], 1);
+      mbar_init(&sm->k_empty[s], 1);
+    }
+    for (int s = 0; s < L::kValRing; ++s) {
+      mbar_init(&sm->v_full[s], 1);
+      mbar_init(&sm->v_empty[s], 1);
     }
     for (int k = 0; k < 2; ++k) {
       mbar_init(&sm->q_full[k], 32);
@@ -1082,8 +1104,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == kLoadWarp)
-    load_warp<kD, kFp8, kNR>(p, &mk1, &mk2, &mv, smem, sm, share);
+  if (warp == kKeyWarp)
+    load_warp<kD, kFp8, kNR, true>(p, &mk1, &mk2, &mv, smem, sm, share);
+  else if (warp == kValueWarp)
+    load_warp<kD, kFp8, kNR, false>(p, &mk1, &mk2, &mv, smem, sm, share);
   else if (warp == kMmaWarp)
     mma_warp<kD, kFp8, kNR>(p, smem, sm);
   else
@@ -1098,9 +1122,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------------------
 // The second kernel: joins the items that a CTA boundary cut and adds the
-// keys' weights.  Launched dependent on the first, whose end it awaits.
+// keys' weights.  Launched dependent on the first: it works out from kv_len
+// what is cut where while that one runs, and then awaits its end.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
+constexpr int kMaxParts = 256;                 // more than SMs
 constexpr int kWeightKeys = 4 * kJoinThreads;  // keys per weight block, four a thread
 
 struct JoinParams {
@@ -1109,9 +1135,13 @@ struct JoinParams {
   int32_t weight_chunks;              // per (sequence, key/value head); 0 without weights
 };
 
+__device__ __forceinline__ bool timed_out(const FwdParams &p) {
+  return p.status != nullptr &&
+         *reinterpret_cast<volatile const int32_t *>(p.status) == DIFFATTN_ERR_TIMEOUT;
+}
+
 __device__ __forceinline__ float block_sum(float x, float *scratch) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  x = warp_sum(x);
   if (threadIdx.x % 32 == 0) scratch[threadIdx.x / 32] = x;
   __syncthreads();
   float y = 0.f;
@@ -1121,60 +1151,79 @@ __device__ __forceinline__ float block_sum(float x, float *scratch) {
   return y;
 }
 
-// Slot of the k-th part of an item whose first part has slot `first`.
-__device__ __forceinline__ int part_slot(int first, int k) {
-  return k == 0 ? first : 2 * (first / 2 + k);
-}
-
-__device__ __forceinline__ bool parts_ok(int first, int n, int ctas) {
-  return first >= 0 && n >= 1 && first / 2 + n <= ctas;
-}
-
-// Block (boundary, row): one row of the item cut at that boundary.
+// Block (boundary, row): one row of the item cut at that boundary, done by the first boundary of
+// each item.
 template <int kD>
-__device__ void join_row(const JoinParams &jp, bool timed_out) {
+__device__ void join_row(const JoinParams &jp) {
   const FwdParams &p = jp.f;
-  __shared__ float factor[2][512];
+  __shared__ float factor[2][kMaxParts];
   __shared__ float scratch[kJoinThreads / 32];
   __shared__ float half[2][2 * kD];
-  const int boundary = 1 + blockIdx.x / jp.join_rows, row = blockIdx.x % jp.join_rows;
-  const int4 rec = p.records[boundary];
-  if (rec.x < 0 || !parts_ok(rec.y, rec.z, jp.ctas) || rec.z > 512) return;
-  const int rb = rec.x % p.row_blocks, bh = rec.x / p.row_blocks;
+  __shared__ int4 cut;  // item, its parts, the sequence's length; item -1: nothing to do
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int row = blockIdx.x % jp.join_rows;
+  if (warp == 0) {
+    const uint32_t cta = 1 + blockIdx.x / jp.join_rows;
+    const Share s = find_share(p, cta, jp.ctas);
+    int4 x = make_int4(-1, 0, 0, 0);
+    if (s.tile > 0) {
+      const uint32_t start = s.begin - s.tile;
+      const Parts parts = parts_of(s.all, start, s.units);
+      if (parts.first / 2 + 1 == static_cast<int>(cta) && s.rb * jp.row_tile + row < p.rows)
+        x = make_int4((s.b * p.kv_heads + s.hk) * p.row_blocks + s.rb, parts.first, parts.n, s.len);
+    }
+    if (lane == 0) cut = x;
+  }
+  __syncthreads();
+  if (cut.x < 0 || cut.z > kMaxParts) return;
+  const Parts parts = {cut.y, cut.z};
+  const int32_t len = cut.w;
+  const int rb = cut.x % p.row_blocks, bh = cut.x / p.row_blocks;
   const int hk = bh % p.kv_heads, b = bh / p.kv_heads;
   const int r = rb * jp.row_tile + row;
-  if (r >= p.rows) return;
-  const int i = r / p.group, h = hk * p.group + r - i * p.group;
-  const int n = rec.z;
+  const int i = p.by_group.div(r), h = hk * p.group + r - i * p.group;
+  constexpr int kGroups = kJoinThreads / (2 * kD);  // threads per column: 2 (d = 64) or 1
+  constexpr int kAhead = 4;
+  const int col = threadIdx.x % (2 * kD), part = threadIdx.x / (2 * kD);
+  const float *src = p.part + static_cast<int64_t>(row) * (2 * kD) + col;
+  const int64_t map_step = static_cast<int64_t>(jp.row_tile) * (2 * kD);
+  grid_dependency_wait();
 
-  // Factors 2^(m_s - M) / l, l = sum 2^(m_s - M) l_s, of both maps: warps 0 and 1.
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // The first parts' values are on their way while the factors 2^(m_s - M) / l of both maps,
+  // l = sum 2^(m_s - M) l_s, are formed by warps 0 and 1.
+  float ahead[kAhead][2];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if (part + kGroups * k < parts.n) {
+      const float *x = src + parts.slot(part + kGroups * k) * 2 * map_step;
+      ahead[k][0] = x[0];
+      ahead[k][1] = x[map_step];
+    }
   if (warp < 2) {
     float top = -INFINITY, sum = 0.f;
-    for (int k = lane; k < n; k += 32)
-      top = fmaxf(top, p.part_ml[(part_slot(rec.y, k) * 2ll + warp) * jp.row_tile + row].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    for (int k = lane; k < n; k += 32) {
-      const float2 ml = p.part_ml[(part_slot(rec.y, k) * 2ll + warp) * jp.row_tile + row];
+    for (int k = lane; k < parts.n; k += 32)
+      top = fmaxf(top, p.part_ml[(parts.slot(k) * 2ll + warp) * jp.row_tile + row].x);
+    top = warp_max(top);
+    for (int k = lane; k < parts.n; k += 32) {
+      const float2 ml = p.part_ml[(parts.slot(k) * 2ll + warp) * jp.row_tile + row];
       const float f = ml.x == top ? 1.f : exp2f(ml.x - top);
       factor[warp][k] = f;
       sum += f * ml.y;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    sum = warp_sum(sum);
     const float c = (warp ? -__ldg(p.lambda + h) : 1.f) / sum;
-    for (int k = lane; k < n; k += 32) factor[warp][k] *= c;
+    for (int k = lane; k < parts.n; k += 32) factor[warp][k] *= c;
   }
   __syncthreads();
-  constexpr int kGroups = kJoinThreads / (2 * kD);  // threads per column: 2 (d = 64) or 1
-  const int col = threadIdx.x % (2 * kD), part = threadIdx.x / (2 * kD);
-  const float *src = p.part + static_cast<int64_t>(row) * (2 * kD) + col;
-  const int64_t map_step = static_cast<int64_t>(jp.row_tile) * (2 * kD);
   float o = 0.f;
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if (part + kGroups * k < parts.n)
+      o = fmaf(factor[0][part + kGroups * k], ahead[k][0],
+               fmaf(factor[1][part + kGroups * k], ahead[k][1], o));
 #pragma unroll 4
-  for (int k = part; k < n; k += kGroups) {
-    const float *x = src + part_slot(rec.y, k) * 2 * map_step;
+  for (int k = part + kGroups * kAhead; k < parts.n; k += kGroups) {
+    const float *x = src + parts.slot(k) * 2 * map_step;
     o = fmaf(factor[0][k], x[0], fmaf(factor[1][k], x[map_step], o));
   }
   if (kGroups == 2) {
@@ -1182,62 +1231,89 @@ __device__ void join_row(const JoinParams &jp, bool timed_out) {
     __syncthreads();
     o = half[0][col] + half[kGroups - 1][col];
   }
-  const int32_t len = p.kv_len[b];
-  if (len - p.N + i < 0) o = 0.f;  // padding: sees no key (the factors are not numbers)
+  const bool none = len - p.N + i < 0;  // padding: sees no key (the factors are not numbers)
+  if (none) o = 0.f;
   const float mine = part == 0 ? 1.f : 0.f;  // each column counted once
   if (p.headnorm == 2) o -= block_sum(mine * o, scratch) * (0.5f / kD);
   if (p.headnorm) {
     const float ss = block_sum(mine * o * o, scratch);
     float y = rsqrtf(ss * (0.5f / kD) + p.eps) * p.out_scale;
     if (p.norm_w != nullptr) y *= __ldg(p.norm_w + h * (2 * kD) + col);
-    o = len - p.N + i < 0 ? 0.f : o * y;
+    o = none ? 0.f : o * y;
   }
   if (part == 0)
     p.out[b * p.outs.b + h * p.outs.h + i * p.outs.n + col] =
-        __float2bfloat16_rn(timed_out ? NAN : o);
+        __float2bfloat16_rn(timed_out(p) ? NAN : o);
 }
 
 // Block (sequence, key/value head, 1024 keys): weights[j] += sum_r |map1 - lambda map2|.
-__device__ void add_weights(const JoinParams &jp, int64_t block) {
+__device__ void add_weights(const JoinParams &jp, uint32_t block) {
   const FwdParams &p = jp.f;
   extern __shared__ float4 row_stat[];  // per row: M1, 1 / l1, M2, lambda / l2
-  const int chunk = static_cast<int>(block % jp.weight_chunks);
-  const int bh = static_cast<int>(block / jp.weight_chunks);
-  const int hk = bh % p.kv_heads, b = bh / p.kv_heads;
+  __shared__ Shares all;
+  __shared__ uint32_t before;  // tiles of the sequences before, in one head and row block
+  const uint32_t bh = block / jp.weight_chunks;
+  const int chunk = static_cast<int>(block - bh * jp.weight_chunks);
+  const int b = static_cast<int>(bh / p.kv_heads), hk = static_cast<int>(bh - b * p.kv_heads);
   const int32_t len = __ldg(p.kv_len + b);
-  if (len < 0 || len > p.max_pages * p.page_size || chunk * kWeightKeys >= len) return;
+  const int32_t most = p.max_pages * p.page_size;
+  if (len < 0 || len > most || chunk * kWeightKeys >= len) return;
   const int32_t *table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
   bool bad = false;
   for (int k = threadIdx.x; k * p.page_size < len; k += kJoinThreads)
     bad |= static_cast<uint32_t>(__ldg(table + k)) >= static_cast<uint32_t>(p.num_pages);
+  if (threadIdx.x < 32) {
+    uint32_t total = 0, mine = 0;
+    for (int32_t x = threadIdx.x; x < p.B; x += 32) {
+      const uint32_t u = units_of(__ldg(p.kv_len + x), most);
+      total += u;
+      mine += x < b ? u : 0;
+    }
+    total = __reduce_add_sync(0xffffffffu, total) * p.kv_heads * p.row_blocks;
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (threadIdx.x == 0) {
+      all.ctas = min(static_cast<uint32_t>(jp.ctas), total);
+      all.each = total / all.ctas;
+      all.more = total - all.each * all.ctas;
+      before = mine;
+    }
+  }
   if (__syncthreads_or(bad)) return;  // the sequence's weights stay as they are
+  const int32_t key = chunk * kWeightKeys + 4 * static_cast<int32_t>(threadIdx.x);
+  const int32_t page = key < len ? __ldg(table + p.by_page.div(key)) : 0;
+  const uint32_t units = units_of(len, most);
+  const uint32_t first_tile = before * p.kv_heads * p.row_blocks + hk * p.row_blocks * units;
+  grid_dependency_wait();
+  if (timed_out(p)) return;
   for (int k = threadIdx.x; k < 2 * p.rows; k += kJoinThreads) {
     const int map = k & 1, r = k >> 1;
-    const int item = bh * p.row_blocks + r / jp.row_tile, row = r % jp.row_tile;
-    const int2 rec = p.item_records[item];
+    const int rb = r / jp.row_tile, row = r - rb * jp.row_tile;
+    Parts parts = {0, 1};
+    if (!p.whole) parts = parts_of(all, first_tile + rb * units, units);
     float top, sum;
-    if (rec.y == 1) {
-      const float2 ml = p.item_ml[(item * 2ll + map) * jp.row_tile + row];
+    if (parts.n == 1) {
+      const float2 ml =
+          p.item_ml[((static_cast<int64_t>(bh) * p.row_blocks + rb) * 2 + map) * jp.row_tile + row];
       top = ml.x;
       sum = ml.y;
     } else {
       top = -INFINITY;
       sum = 0.f;
-      const int n = parts_ok(rec.x, rec.y, jp.ctas) ? rec.y : 0;
-      for (int s = 0; s < n; ++s)
-        top = fmaxf(top, p.part_ml[(part_slot(rec.x, s) * 2ll + map) * jp.row_tile + row].x);
-      for (int s = 0; s < n; ++s) {
-        const float2 ml = p.part_ml[(part_slot(rec.x, s) * 2ll + map) * jp.row_tile + row];
+      for (int s = 0; s < parts.n; ++s)
+        top = fmaxf(top, p.part_ml[(parts.slot(s) * 2ll + map) * jp.row_tile + row].x);
+      for (int s = 0; s < parts.n; ++s) {
+        const float2 ml = p.part_ml[(parts.slot(s) * 2ll + map) * jp.row_tile + row];
         sum = fmaf(ml.x == top ? 1.f : exp2f(ml.x - top), ml.y, sum);
       }
     }
-    const bool none = len - p.N + r / p.group < 0;  // the row sees no key: it adds nothing
+    const int i = p.by_group.div(r);
+    const bool none = len - p.N + i < 0;  // the row sees no key: it adds nothing
     float *dst = reinterpret_cast<float *>(row_stat + r) + 2 * map;
     dst[0] = none ? 0.f : top;
-    dst[1] = none ? 0.f : (map ? __ldg(p.lambda + hk * p.group + r % p.group) : 1.f) / sum;
+    dst[1] = none ? 0.f
+                  : (map ? __ldg(p.lambda + hk * p.group + r - i * p.group) : 1.f) / sum;
   }
   __syncthreads();
-  const int32_t key = chunk * kWeightKeys + 4 * static_cast<int32_t>(threadIdx.x);
   if (key >= len) return;
   const float *x1 = p.logits + static_cast<int64_t>(bh) * 2 * p.rows * p.padded + key;
   const float *x2 = x1 + p.rows * p.padded;
@@ -1253,9 +1329,8 @@ __device__ void add_weights(const JoinParams &jp, int64_t block) {
     w[2] += fabsf(exp2f(a.z - st.x) * st.y - exp2f(c.z - st.z) * st.w);
     w[3] += fabsf(exp2f(a.w - st.x) * st.y - exp2f(c.w - st.z) * st.w);
   }
-  const int32_t page = __ldg(table + key / p.page_size);
   float *dst = p.weights + (static_cast<int64_t>(page) * p.kv_heads + hk) * p.page_size +
-               key % p.page_size;
+               p.by_page.mod(key);
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     if (key + k < len) dst[k] += w[k];
@@ -1264,14 +1339,10 @@ __device__ void add_weights(const JoinParams &jp, int64_t block) {
 template <int kD>
 __global__ void __launch_bounds__(kJoinThreads)
     diffpaged_join_kernel(const __grid_constant__ JoinParams jp) {
-  grid_dependency_wait();
-  const bool timed_out =
-      jp.f.status != nullptr &&
-      *reinterpret_cast<volatile const int32_t *>(jp.f.status) == DIFFATTN_ERR_TIMEOUT;
-  const int64_t joins = static_cast<int64_t>(jp.ctas - 1) * jp.join_rows;
+  const uint32_t joins = static_cast<uint32_t>(jp.ctas - 1) * jp.join_rows;
   if (blockIdx.x < joins)
-    join_row<kD>(jp, timed_out);
-  else if (!timed_out)
+    join_row<kD>(jp);
+  else
     add_weights(jp, blockIdx.x - joins);
 }
 
@@ -1408,12 +1479,10 @@ bool plan_paged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache, boo
   };
   q.part = take(slots * 2 * row_tile * 2 * desc.d * sizeof(float));
   q.stats = take(slots * 2 * row_tile * sizeof(float2));
-  q.records = take(q.whole ? 0 : q.ctas * sizeof(int4));
   if (accumulate) {
     const double logits = static_cast<double>(desc.B) * static_cast<double>(cache.kv_heads) * 2.0 *
                           static_cast<double>(rows) * static_cast<double>(q.padded) * 4.0;
     if (logits > 1.0e18) return false;
-    q.items_rec = take(q.items * sizeof(int2));
     q.item_stats = take(q.items * 2 * row_tile * sizeof(float2));
     q.logits = take(static_cast<size_t>(desc.B * cache.kv_heads * 2 * rows * q.padded) * sizeof(float));
   }
@@ -1465,10 +1534,8 @@ diffattn_status launch_paged_fwd(const diffattn_desc &desc, const diffpaged_cach
   if (!plan.whole) {
     p.part = reinterpret_cast<float *>(ws + plan.part);
     p.part_ml = reinterpret_cast<float2 *>(ws + plan.stats);
-    p.records = reinterpret_cast<int4 *>(ws + plan.records);
   }
   if (accumulate) {
-    p.item_records = reinterpret_cast<int2 *>(ws + plan.items_rec);
     p.item_ml = reinterpret_cast<float2 *>(ws + plan.item_stats);
     p.logits = reinterpret_cast<float *>(ws + plan.logits);
     p.weights = cache.weights;
