@@ -51,8 +51,9 @@ namespace {
 
 constexpr int kTile = kPagedTile;
 constexpr int kConsumers = 256;  // softmax and epilogue threads
-constexpr int kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10;
-constexpr int kThreads = kConsumers + 96;
+// Warps 0-2 issue, 4-11 (a multiple of four, for their quarters of tensor memory) do the softmax.
+constexpr int kMmaWarp = 0, kKeyWarp = 1, kValueWarp = 2, kSoftmaxWarp = 4;
+constexpr int kThreads = 128 + kConsumers;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kGrowth = 8.f;  // log2 units a logit may pass the reference maximum by
@@ -67,6 +68,7 @@ enum : int32_t { kFirst = 1, kLast = 2, kStop = 4, kBad = 8, kDirect = 16 };
 struct TileDesc {
   int32_t b, hk, real, key0;  // real: rows of the block
   int32_t len, flags, slot, item;
+  int32_t steps, pad[3];  // 16-key steps of the second product (one for an idle sequence)
 };
 
 // Exact division of 0 <= n < 2^31 by a launch constant: a multiply and a shift.
@@ -144,12 +146,13 @@ struct Geo {
 
 template <int kNR>
 struct Ctrl {
+  float m[2][2][kNR];  // reference maxima of both maps' rows, two copies in turn
   float wmax[2][4][kNR];
-  float lsum[2][4][kNR];
+  float lsum[2][2][4][kNR];  // by segment parity
   float rsum[2][4][kNR];
-  float late[2][kMaxBad][kNR];  // logits of keys kept out of the product,
-  float ref[2][kNR];            // and the references they go with
-  TileDesc ring[kRing];
+  float late[2][2][kMaxBad][kNR];  // by segment parity: logits of keys kept out of the product,
+  float ref[2][2][kNR];         // and rows' references, by segment parity
+  TileDesc ring[kRing], done[2];  // done: a segment's last tile, by segment parity
   RowInfo rows[kRing][kNR];  // by segment
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_empty[2], drain;
@@ -206,23 +209,31 @@ __device__ __forceinline__ void fence_async_proxy() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// tcgen05.mma of a converged warp (one elected lane issues).
-__device__ __forceinline__ void umma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
+// tcgen05.mma of a converged warp (one elected lane issues).  The operands' descriptors come as
+// their low words (start address, leading-dimension offset), which advance, and their high words
+// (stride-dimension offset, layout), which do not: two 32-bit additions a product.
+template <bool kFp8>
+__device__ __forceinline__ void umma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t a_hi,
+                                     uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+  if (kFp8)
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(a_hi), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(a_hi), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
-__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
+__device__ __forceinline__ uint32_t low(uint64_t x) { return static_cast<uint32_t>(x); }
+__device__ __forceinline__ uint32_t high(uint64_t x) { return static_cast<uint32_t>(x >> 32); }
 // Descriptor of rows of 64 bytes with 64-byte swizzle (8-row groups 512 bytes apart): K-major, or
 // MN-major operands at most 32 elements wide.
 __device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr) {
@@ -449,6 +460,7 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
       d.flags = (seg_first ? kFirst : 0) | (seg_last ? kLast : 0) | (bad ? kBad : 0) |
                 (seg_start == 0 && tile + 1 == units ? kDirect : 0);
       d.item = (b * p.kv_heads + hk) * p.row_blocks + rb;
+      d.steps = max(1, (keys + 15) / 16);
       q_row = rb * kNR;
       if (bad && lane == 0) report_bad_page(p.status);
     }
@@ -472,24 +484,26 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
       }
     }
     if (left > 1) id = page_of(tile);
-    if (kKeys && seg_first && lane < kNR) {  // the segment's rows
-      const int32_t r = q_row + lane;
-      const int32_t i = p.by_group.div(r), pos = tile_len - p.N + i;
-      RowInfo info;
-      info.last = r >= p.rows || pos < 0 ? -1 : p.causal ? pos : tile_len - 1;
-      info.head = d.hk * p.group + r - i * p.group;
-      info.out = d.b * p.outs.b + info.head * p.outs.h + i * p.outs.n;
-      sm->rows[seg % kRing][lane] = info;
-    }
-    __syncwarp();
 #pragma unroll 1
     for (int k = 0; k < kPerTile; ++k) {
       const uint32_t c = it * kPerTile + k;
       const int s = c % kSlots;
       if (!(ok = freed(c))) break;
       const int row_bytes = kKeys ? G::kKeyBox : 128;
+      if (kKeys && k == 0) {
+        if (lane == 0) sm->ring[it % kRing] = d;
+        if (seg_first && lane < kNR) {  // the segment's rows
+          const int32_t r = q_row + lane;
+          const int32_t i = p.by_group.div(r), pos = tile_len - p.N + i;
+          RowInfo info;
+          info.last = r >= p.rows || pos < 0 ? -1 : p.causal ? pos : tile_len - 1;
+          info.head = d.hk * p.group + r - i * p.group;
+          info.out = d.b * p.outs.b + info.head * p.outs.h + i * p.outs.n;
+          sm->rows[seg % kRing][lane] = info;
+        }
+        __syncwarp();
+      }
       if (lane == 0) {
-        if (kKeys && k == 0) sm->ring[it % kRing] = d;
         if (rows > 0)
           mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(rows) * 2 * row_bytes);
         else
@@ -572,6 +586,7 @@ __device__ __forceinline__ void mma_warp(const FwdParams &p, uint8_t *smem, Ctrl
   // The tests see the right phase: the slot's use before was consumed by an earlier tile.
   uint32_t t = 0, n = 0, segs = 0, o_segs = 0;
   int32_t s_flags = 0, o_flags = 0, ahead_flags = 0;  // of S's last tile; of tiles t, t + 1
+  int32_t o_steps = 0, ahead_steps = 0;               // 16-key steps with keys in them
   uint64_t since = 0;
 #pragma unroll 1
   while (true) {
@@ -580,6 +595,8 @@ __device__ __forceinline__ void mma_warp(const FwdParams &p, uint8_t *smem, Ctrl
         ready(&sm->k_full[cs % L::kKeyRing], phase<L::kKeyRing>(cs))) {
       s_flags = *reinterpret_cast<volatile int32_t *>(&sm->ring[n % kRing].flags);
       (n == t ? o_flags : ahead_flags) = s_flags;
+      (n == t ? o_steps : ahead_steps) =
+          *reinterpret_cast<volatile int32_t *>(&sm->ring[n % kRing].steps);
       if (s_flags & kStop) {
         if (lane == 0) mbar_arrive(&sm->s_full[n & 1]);
       } else {
@@ -600,22 +617,13 @@ __device__ __forceinline__ void mma_warp(const FwdParams &p, uint8_t *smem, Ctrl
                                 (G::kKeySlots == 1 ? map * kBoxBytes : 0);
           const uint32_t q_at = smem_u32(smem + L::kQ + (2 * qb + map) * G::kQBytes);
           const uint32_t acc = tmem + (n & 1) * 2 * G::kNS + map * G::kNS;
+          const uint64_t a = G::kKeyRow == 64 ? smem_desc_sw64(k_at) : smem_desc_sw128(k_at, 16, 1024);
+          const uint64_t b = G::kKeyRow == 64 ? smem_desc_sw64(q_at) : smem_desc_sw128(q_at, 16, 1024);
 #pragma unroll
-          for (int kk = 0; kk < G::kKeyRow / 32; ++kk) {  // 32 bytes of depth each
-            if (G::kKeyRow == 64) {
-              umma_e4m3(acc, smem_desc_sw64(k_at) + 2 * kk, smem_desc_sw64(q_at) + 2 * kk, kIdS,
-                        kk > 0);
-            } else {
-              const uint64_t a =
-                  smem_desc_sw128(k_at, 16, 1024) + (kk / 4) * (kBoxBytes / 16) + 2 * (kk % 4);
-              const uint64_t q =
-                  smem_desc_sw128(q_at, 16, 1024) + (kk / 4) * (G::kNS * 8) + 2 * (kk % 4);
-              if (kFp8)
-                umma_e4m3(acc, a, q, kIdS, kk > 0);
-              else
-                umma_bf16(acc, a, q, kIdS, kk > 0);
-            }
-          }
+          for (int kk = 0; kk < G::kKeyRow / 32; ++kk)  // 32 bytes of depth each
+            umma<kFp8>(acc, low(a) + (kk / 4) * (kBoxBytes / 16) + 2 * (kk % 4),
+                       low(b) + (kk / 4) * (G::kNS * 8) + 2 * (kk % 4), high(a), high(b), kIdS,
+                       kk > 0);
           if (G::kKeySlots == 2 || map == 1) umma_commit_warp(&sm->k_empty[c % L::kKeyRing]);
         }
         if (*reinterpret_cast<volatile int *>(&sm->abort)) break;
@@ -648,13 +656,15 @@ __device__ __forceinline__ void mma_warp(const FwdParams &p, uint8_t *smem, Ctrl
                                           : smem_desc_sw128(p_at, kTile * 128, 1024);
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)  // 16 keys each
-          umma_bf16(o_at + k * G::kPCols, v + 128 * kk, w + G::kPRow * kk, kIdO,
-                    !(o_flags & kFirst) || kk > 0);
+          if (kk < o_steps)
+            umma<false>(o_at + k * G::kPCols, low(v) + 128 * kk, low(w) + G::kPRow * kk, high(v),
+                        high(w), kIdO, !(o_flags & kFirst) || kk > 0);
         umma_commit_warp(&sm->v_empty[c % L::kValRing]);
       }
       if (!ok) break;
       umma_commit_warp(&sm->pv_done[t & 1]);
       o_flags = ahead_flags;
+      o_steps = ahead_steps;
       ++t;
       since = 0;
       continue;
@@ -685,7 +695,7 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
   using L = Layout<kD, kFp8, kNR>;
   constexpr int kNQ = G::kNQ, kW = G::kW, kChunks = G::kChunks;
   constexpr int kVUnits = kD / 4;  // 16-byte units of a value row
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int tid = threadIdx.x - 32 * kSoftmaxWarp, warp = tid / 32, lane = tid % 32;
   const int map = warp / 4, quarter = warp % 4;
   const int key = 32 * quarter + lane;  // of the tile
   const uint32_t tmem = sm->tmem + (static_cast<uint32_t>(32 * quarter) << 16);
@@ -695,9 +705,34 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
                                      ((u / 8) % 2) * kBoxBytes + row * 128 + (u % 8) * 16);
   };
 
-  float m[kNR], l[kNR];
-  bool poisoned = false;
+  float l[kNR];
+  int m_turn = 0;
+  bool poisoned = false, healthy = true;
   uint32_t late = 0, seg = 0;
+  // A segment's end waits for its last product, so it is done after the next tile's P.
+  bool pending = false, done_poisoned = false;
+  uint32_t done_late = 0;
+  // What the keys kept out of the product add to column `col` of row q of both maps.
+  const auto late_sums = [&](int q, int col) {
+    float2 y = make_float2(0.f, 0.f);
+    const int parity = (seg - 1) & 1;
+    const TileDesc &done = sm->done[parity];
+#pragma unroll 1
+    for (uint32_t rest = done_late; rest; rest &= rest - 1) {
+      const int back = __ffs(rest) - 1;
+      const int32_t pos = done.len - 1 - back;
+      const int32_t page =
+          p.page_table[static_cast<int64_t>(done.b) * p.max_pages + p.by_page.div(pos)];
+      if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) continue;
+      const float v = __bfloat162float(
+          static_cast<const __nv_bfloat16 *>(p.v_pages)[page * p.vs.b + done.hk * p.vs.h +
+                                                        p.by_page.mod(pos) * p.vs.n + col]);
+      const float x1 = sm->late[parity][0][back][q], x2 = sm->late[parity][1][back][q];
+      if (x1 != -INFINITY) y.x += ex2_approx(x1 - sm->ref[parity][0][q]) * v;
+      if (x2 != -INFINITY) y.y += ex2_approx(x2 - sm->ref[parity][1][q]) * v;
+    }
+    return y;
+  };
 #pragma unroll 1
   for (uint32_t t = 0;; ++t) {
     bool ok = mbar_wait_warp(&sm->s_full[t & 1], phase<2>(t), &sm->abort, kWaitNs);
@@ -712,59 +747,55 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
     const RowInfo *rows = sm->rows[seg % kRing];
     const uint32_t s_at = tmem + (t & 1) * 2 * G::kNS + map * G::kNS;
 
-    // This key's logits of rows kW k .. kW k + kW - 1, in log2 units; -inf where it is masked.
-    float x[kW];
-    const auto load_x = [&](int k) {
-      uint32_t raw[kW];
-      tmem_load(s_at + kW * k, raw);
-      tmem_loaded(raw);
-#pragma unroll
-      for (int e = 0; e < kW; ++e) x[e] = __uint_as_float(raw[e]) * p.scale_log2;
-      if (masked) {
-#pragma unroll
-        for (int e = 0; e < kW; ++e)
-          if (d.key0 + key > rows[kW * k + e].last) x[e] = -INFINITY;
-      }
-    };
+    const bool fresh = (d.flags & kFirst) != 0;  // nothing in O yet
+    const float(*m)[kNR] = sm->m[m_turn];
 
+    // This key's logits of the rows, in log2 units; -inf where it is masked.
+    float x[kNR];
     bool grew = false;
-    if (threadIdx.x == 0) sm->bad_rows[(t + 1) % 3] = 0;
+    if (tid == 0) sm->bad_rows[(t + 1) % 3] = 0;
     if (!stop) {
-      if (d.flags & kFirst) {
+      if (fresh) {
         poisoned = false;
         late = 0;
 #pragma unroll
-        for (int q = 0; q < kNR; ++q) {
-          m[q] = -INFINITY;
-          l[q] = 0.f;
-        }
+        for (int q = 0; q < kNR; ++q) l[q] = 0.f;
       }
       if (d.flags & kBad) poisoned = true;
+      grew = fresh;  // the first tile sets the references
       tc_fence_after_sync();
+      uint32_t raw[kChunks][kW];
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) tmem_load(s_at + kW * k, raw[k]);
 #pragma unroll
       for (int k = 0; k < kChunks; ++k) {
-        if (kW * k >= real) break;
-        load_x(k);
+        tmem_loaded(raw[k]);
 #pragma unroll
-        for (int e = 0; e < kW; ++e)
-          grew |= kW * k + e < real && x[e] > m[kW * k + e] + kGrowth;
-        if (p.logits != nullptr && key < keys) {
-          float *dst = p.logits +
-                       ((static_cast<int64_t>(d.b) * p.kv_heads + d.hk) * 2 + map) * p.rows * p.padded +
-                       static_cast<int64_t>(d.item % p.row_blocks * kNR + kW * k) * p.padded +
-                       d.key0 + key;
+        for (int e = 0; e < kW; ++e) x[kW * k + e] = __uint_as_float(raw[k][e]) * p.scale_log2;
+      }
+      if (masked) {
 #pragma unroll
-          for (int e = 0; e < kW; ++e)
-            if (kW * k + e < real && dbg_ok(d.key0 + key < p.padded, p.status, 41))
-              dst[e * p.padded] = x[e];
-        }
+        for (int q = 0; q < kNR; ++q)
+          if (d.key0 + key > rows[q].last) x[q] = -INFINITY;
+      }
+      if (!fresh) {
+#pragma unroll
+        for (int q = 0; q < kNR; ++q) grew |= q < real && x[q] > m[map][q] + kGrowth;
+      }
+      if (p.logits != nullptr && key < keys) {
+        float *dst = p.logits +
+                     ((static_cast<int64_t>(d.b) * p.kv_heads + d.hk) * 2 + map) * p.rows * p.padded +
+                     static_cast<int64_t>(d.item % p.row_blocks * kNR) * p.padded + d.key0 + key;
+#pragma unroll
+        for (int q = 0; q < kNR; ++q)
+          if (q < real && dbg_ok(d.key0 + key < p.padded, p.status, 41)) dst[q * p.padded] = x[q];
       }
       // P's buffer: the product that read it last is done.
       if (t >= G::kPBufs)
         ok = mbar_wait_warp(&sm->pv_done[(t - G::kPBufs) & 1], phase<2>(t - G::kPBufs), &sm->abort,
                             kWaitNs);
-      // Rows of v behind the sequence's end hold anything (NaN too): zero them, as 0 * NaN would
-      // reach every row.  Where new tokens see different keys, a non-finite v row that only some
+      // Rows of v behind the sequence's end hold anything (NaN too): zero those that the product
+      // still takes in its last step of 16, as 0 * NaN would reach every row.  Where new tokens see different keys, a non-finite v row that only some
       // of them see is noted, to be kept out of the product.
       if (ok && (keys < kTile || mixed)) {
 #pragma unroll 1
@@ -776,12 +807,12 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
         if (ok) {
           const int from = max(0, keys);
 #pragma unroll 1
-          for (int k = threadIdx.x; k < (kTile - from) * kVUnits; k += kConsumers)
+          for (int k = tid; k < (16 * d.steps - from) * kVUnits; k += kConsumers)
             *v_row(t, from + k / kVUnits, k % kVUnits) = make_uint4(0, 0, 0, 0);
           if (mixed) {
             const int lo = max(0, lim_min + 1 - d.key0), hi = min(kTile, keys);
 #pragma unroll 1
-            for (int k = threadIdx.x; k < (hi - lo) * kVUnits; k += kConsumers) {
+            for (int k = tid; k < (hi - lo) * kVUnits; k += kConsumers) {
               const uint4 y = *v_row(t, lo + k / kVUnits, k % kVUnits);
               bool bad = false;
               for (const uint32_t w : {y.x, y.y, y.z, y.w})
@@ -792,23 +823,19 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
         }
       }
     }
+    ok = ok && healthy;
     if (!ok) *reinterpret_cast<volatile int *>(&sm->failed) = 1;
 
     // One barrier and vote of all eight warps: has a logit outgrown its reference (or did a wait
     // run out)?
     if (named_barrier_or(1, kConsumers, grew || !ok)) {
       if (*reinterpret_cast<volatile int *>(&sm->failed)) break;
-      const bool fresh = (d.flags & kFirst) != 0;  // nothing in O yet
       if (!stop) {
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-          if (kW * k >= real) break;
-          if (kChunks > 1) load_x(k);
-#pragma unroll
-          for (int e = 0; e < kW; ++e) {
-            const float y = warp_max(x[e]);
-            if (lane == 0) sm->wmax[map][quarter][kW * k + e] = y;
-          }
+        for (int q = 0; q < kNR; ++q) {
+          if (q >= real) break;
+          const float y = warp_max(x[q]);
+          if (lane == 0) sm->wmax[map][quarter][q] = y;
         }
         // O moves with the reference, so the product before must be done.
         if (!fresh)
@@ -816,42 +843,48 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
       }
       if (named_barrier_or(2, kConsumers, !ok)) break;
       if (!stop) {
-        const uint32_t o_at = tmem + G::kTmemO + (seg % G::kOBufs) * G::kOCols + map * 2 * kNQ;
-        tc_fence_after_sync();
+        const auto new_m = [&](int q) {
+          const float(*w)[kNR] = sm->wmax[map];
+          const float y = fmaxf(fmaxf(w[0][q], w[1][q]), fmaxf(w[2][q], w[3][q]));
+          return fresh ? y : fmaxf(m[map][q], y);
+        };
+        if (quarter == 0 && lane < real) sm->m[m_turn ^ 1][map][lane] = new_m(lane);
+        if (!fresh) {
+          const uint32_t o_at = tmem + G::kTmemO + (seg % G::kOBufs) * G::kOCols + map * 2 * kNQ;
+          tc_fence_after_sync();
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-          if (kW * k >= real) break;
-          float f[kW];
-          bool moved = false;
+          for (int k = 0; k < kChunks; ++k) {
+            if (kW * k >= real) break;
+            float f[kW];
+            bool moved = false;
 #pragma unroll
-          for (int e = 0; e < kW; ++e) {
-            const int q = kW * k + e;
-            float y = m[q];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) y = fmaxf(y, sm->wmax[map][w][q]);
-            f[e] = y == m[q] ? 1.f : ex2_approx(m[q] - y);
-            moved |= y != m[q];
-            m[q] = y;
-            l[q] *= f[e];
-          }
-          if (moved && !fresh) {  // the same decision in every thread of the map
+            for (int e = 0; e < kW; ++e) {
+              const int q = kW * k + e;
+              const float old = m[map][q], y = new_m(q);
+              f[e] = y == old ? 1.f : ex2_approx(old - y);
+              moved |= q < real && y != old;
+              l[q] *= f[e];
+            }
+            if (moved) {  // the same decision in every thread of the map
 #pragma unroll 1
-            for (int part = 0; part < 2 * G::kValSlots; ++part) {
-              const uint32_t at = o_at + (part / 2) * G::kPCols + (part % 2) * kNQ + kW * k;
-              uint32_t y[kW];
-              tmem_load(at, y);
-              tmem_loaded(y);
+              for (int part = 0; part < 2 * G::kValSlots; ++part) {
+                const uint32_t at = o_at + (part / 2) * G::kPCols + (part % 2) * kNQ + kW * k;
+                uint32_t y[kW];
+                tmem_load(at, y);
+                tmem_loaded(y);
 #pragma unroll
-              for (int e = 0; e < kW; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f[e]);
-              tmem_store(at, y);
+                for (int e = 0; e < kW; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f[e]);
+                tmem_store(at, y);
+              }
             }
           }
+          tmem_st_wait();
         }
-        tmem_st_wait();
       }
+      named_barrier_sync(2, kConsumers);
+      m_turn ^= 1;
     }
-    if (stop) break;
-
+    if (!stop) {
     // Rows of v to keep out of the product (rare): zero them in the buffer as well, and keep
     // their logits.
     const uint32_t bad_rows = mixed ? sm->bad_rows[t % 3] : 0u;
@@ -860,7 +893,7 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
     if (bad_rows) {
       late |= bad_rows;
 #pragma unroll 1
-      for (int k = threadIdx.x; k < kTile * kVUnits; k += kConsumers) {
+      for (int k = tid; k < kTile * kVUnits; k += kConsumers) {
         const int x_back = d.len - 1 - d.key0 - k / kVUnits;
         if (x_back >= 0 && x_back < kMaxBad && ((bad_rows >> x_back) & 1))
           *v_row(t, k / kVUnits, k % kVUnits) = make_uint4(0, 0, 0, 0);
@@ -872,15 +905,15 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
       if (kW * k >= real) break;
-      if (kChunks > 1) load_x(k);
       uint32_t hi[kW > 1 ? kW / 2 : 1], lo[kW > 1 ? kW / 2 : 1];
       float y[kW > 1 ? kW : 2];
       y[1] = 0.f;
 #pragma unroll
       for (int e = 0; e < kW; ++e) {
-        if (kept_out) sm->late[map][back][kW * k + e] = x[e];
-        y[e] = ex2_approx(x[e] - m[kW * k + e]);
-        if (masked && x[e] == -INFINITY) y[e] = 0.f;  // also where no key has been seen yet
+        const float xe = x[kW * k + e];
+        if (kept_out) sm->late[seg & 1][map][back][kW * k + e] = xe;
+        y[e] = ex2_approx(xe - sm->m[m_turn][map][kW * k + e]);
+        if (masked && xe == -INFINITY) y[e] = 0.f;  // also where no key has been seen yet
         l[kW * k + e] += y[e];
       }
 #pragma unroll
@@ -909,142 +942,165 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
     tc_fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm->p_full[t & 1]);
-    if (!(d.flags & kLast)) continue;
+    }
 
-    // ---- end of the segment ----
+    // ---- the end of the segment before ----
+    if (pending) {
+      pending = false;
+      const RowInfo *done_rows = sm->rows[(seg - 1) % kRing];
+      const int parity = (seg - 1) & 1;
+      const TileDesc &done = sm->done[parity];
+      const int done_real = kNR == 1 ? 1 : done.real;
+      const bool direct = (done.flags & kDirect) != 0;
+      // d = 64: the two halves of the warps take turns at eight rows; d = 128: each has its half
+      // of the value columns for all rows.
+      constexpr int kStep = kD == 128 || kChunks == 1 ? 1 : 2;  // chunks per turn
+      constexpr int kMine = kW * kChunks / kStep;               // rows of a thread
+      const int half = warp / 4;
+      const int block = kD == 128 ? half : 0;
+      const int col = 128 * block + key;
+      const bool idle = kD == 64 && kChunks == 1 && half == 1;
+      const uint32_t o_at =
+          tmem + G::kTmemO + ((seg - 1) % G::kOBufs) * G::kOCols + block * G::kPCols;
+      // What the output needs from global memory, on its way during the wait.
+      constexpr bool kEarly = kMine <= 4;
+      float lam[kEarly ? kMine : 1], gain[kEarly ? kMine : 1];
+      if (kEarly && direct && !idle) {
 #pragma unroll
-    for (int q = 0; q < kNR; ++q) {
-      if (q >= real) break;
-      const float y = warp_sum(l[q]);
-      if (lane == 0) sm->lsum[map][quarter][q] = poisoned ? NAN : y;
-    }
-    if (late && lane == 0 && quarter == 0) {  // references of both maps for the kept-out keys
-#pragma unroll
-      for (int q = 0; q < kNR; ++q) sm->ref[map][q] = m[q];
-    }
-    ok = mbar_wait_warp(&sm->pv_done[t & 1], phase<2>(t), &sm->abort, kWaitNs);
-    if (named_barrier_or(2, kConsumers, !ok)) break;
-    tc_fence_after_sync();
-    const auto l_of = [&](int mp, int q) {
-      return (sm->lsum[mp][0][q] + sm->lsum[mp][1][q]) + (sm->lsum[mp][2][q] + sm->lsum[mp][3][q]);
-    };
-    const bool direct = (d.flags & kDirect) != 0;
-    // The row's (m, l): per slot for the join, per item for the weights.
-    if (quarter == 0 && lane == 0 && (!direct || p.item_ml != nullptr)) {
-      float2 *ml = (direct ? p.item_ml + static_cast<int64_t>(d.item) * 2 * kNR
-                           : p.part_ml + static_cast<int64_t>(d.slot) * 2 * kNR) +
-                   map * kNR;
-#pragma unroll
-      for (int q = 0; q < kNR; ++q) {
-        if (q >= real) break;
-        ml[q] = make_float2(m[q], l_of(map, q));
-      }
-    }
-    // d = 64: the two halves of the warps take turns at eight rows; d = 128: each has its half of
-    // the value columns for all rows.
-    constexpr int kStep = kD == 128 || kChunks == 1 ? 1 : 2;  // chunks per turn
-    const int half = warp / 4;
-    const int block = kD == 128 ? half : 0;
-    const int col = 128 * block + key;
-    const bool idle = kD == 64 && kChunks == 1 && half == 1;
-    const uint32_t o_at = tmem + G::kTmemO + (seg % G::kOBufs) * G::kOCols + block * G::kPCols;
-    float o[kW * kChunks / kStep];
-#pragma unroll
-    for (int k = 0; k < kChunks / kStep; ++k) {
-      const int q0 = kW * (kStep * k + (kStep == 2 ? half : 0));
-      if (idle || q0 >= real) break;
-      uint32_t part[4][kW];  // map 1 hi, lo, map 2 hi, lo
-#pragma unroll
-      for (int e = 0; e < 4; ++e) tmem_load(o_at + e * kNQ + q0, part[e]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) tmem_loaded(part[e]);
-#pragma unroll
-      for (int e = 0; e < kW; ++e) {
-        const int q = q0 + e;
-        if (q >= real) break;
-        float y1 = __uint_as_float(part[0][e]) + __uint_as_float(part[1][e]);
-        float y2 = __uint_as_float(part[2][e]) + __uint_as_float(part[3][e]);
-#pragma unroll 1
-        for (uint32_t rest = late; rest; rest &= rest - 1) {
-          const int x_back = __ffs(rest) - 1;
-          const int32_t pos = d.len - 1 - x_back;
-          const int32_t page =
-              p.page_table[static_cast<int64_t>(d.b) * p.max_pages + p.by_page.div(pos)];
-          if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) continue;
-          const float v = __bfloat162float(
-              static_cast<const __nv_bfloat16 *>(p.v_pages)[page * p.vs.b + d.hk * p.vs.h +
-                                                            p.by_page.mod(pos) * p.vs.n + col]);
-          const float x1 = sm->late[0][x_back][q], x2 = sm->late[1][x_back][q];
-          if (x1 != -INFINITY) y1 += ex2_approx(x1 - sm->ref[0][q]) * v;
-          if (x2 != -INFINITY) y2 += ex2_approx(x2 - sm->ref[1][q]) * v;
-        }
-        if (direct) {
-          const float lam = __ldg(p.lambda + rows[q].head);
-          float y = y1 / l_of(0, q) - lam * (y2 / l_of(1, q));
-          if (rows[q].last < 0 && !poisoned) y = 0.f;  // a row that sees no key
-          o[kW * k + e] = y;
-        } else if (dbg_ok(d.slot >= 0 && d.slot < 2 * static_cast<int>(gridDim.x), p.status, 42)) {
-          float *dst = p.part + (static_cast<int64_t>(d.slot) * 2 * kNR + q) * (2 * kD) + col;
-          dst[0] = y1;
-          dst[kNR * (2 * kD)] = y2;
+        for (int e = 0; e < kMine; ++e) {
+          const int q = kStep == 2 ? 8 * half + e : e;
+          if (q >= done_real) break;
+          lam[e] = __ldg(p.lambda + done_rows[q].head);
+          gain[e] = p.headnorm && p.norm_w != nullptr
+                        ? __ldg(p.norm_w + done_rows[q].head * (2 * kD) + col)
+                        : 1.f;
         }
       }
-    }
-    tc_fence_before_sync();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm->o_empty[seg % G::kOBufs]);
-    ++seg;
-    if (!direct) continue;
-
-    // Head norm: row sums over the lanes, the four quarters and (d = 128) both halves.
-    const auto row_sum = [&](int q) {
-      float y = (sm->rsum[0][0][q] + sm->rsum[0][1][q]) + (sm->rsum[0][2][q] + sm->rsum[0][3][q]);
-      if (kD == 128)
-        y += (sm->rsum[1][0][q] + sm->rsum[1][1][q]) + (sm->rsum[1][2][q] + sm->rsum[1][3][q]);
-      return y;
-    };
-#pragma unroll 1
-    for (int pass = p.headnorm == 2 ? 0 : 1; pass < 2 && p.headnorm; ++pass) {  // mean, then square
+      const uint32_t td = t - 1;
+      if (!mbar_wait_warp(&sm->pv_done[td & 1], phase<2>(td), &sm->abort, kWaitNs)) {
+        healthy = false;  // the next vote ends the loop
+        *reinterpret_cast<volatile int *>(&sm->failed) = 1;
+      }
+      tc_fence_after_sync();
+      const auto l_of = [&](int mp, int q) {
+        const float(*x)[kNR] = sm->lsum[parity][mp];
+        return (x[0][q] + x[1][q]) + (x[2][q] + x[3][q]);
+      };
+      float o[kMine];
 #pragma unroll
       for (int k = 0; k < kChunks / kStep; ++k) {
         const int q0 = kW * (kStep * k + (kStep == 2 ? half : 0));
-        if (idle || q0 >= real) break;
+        if (idle || q0 >= done_real) break;
+        uint32_t part[4][kW];  // map 1 hi, lo, map 2 hi, lo
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tmem_load(o_at + e * kNQ + q0, part[e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tmem_loaded(part[e]);
 #pragma unroll
         for (int e = 0; e < kW; ++e) {
-          if (q0 + e >= real) break;
-          const float y = o[kW * k + e];
-          const float z = warp_sum(pass ? y * y : y);
-          if (lane == 0) sm->rsum[kD == 128 ? half : 0][quarter][q0 + e] = z;
+          const int q = q0 + e;
+          if (q >= done_real) break;
+          float y1 = __uint_as_float(part[0][e]) + __uint_as_float(part[1][e]);
+          float y2 = __uint_as_float(part[2][e]) + __uint_as_float(part[3][e]);
+          if (done_late) {
+            const float2 more = late_sums(q, col);
+            y1 += more.x;
+            y2 += more.y;
+          }
+          if (direct) {
+            const float lm = kEarly ? lam[kW * k + e] : __ldg(p.lambda + done_rows[q].head);
+            float y = y1 / l_of(0, q) - lm * (y2 / l_of(1, q));
+            if (done_rows[q].last < 0 && !done_poisoned) y = 0.f;  // a row that sees no key
+            o[kW * k + e] = y;
+          } else if (dbg_ok(done.slot >= 0 && done.slot < 2 * static_cast<int>(gridDim.x),
+                            p.status, 42)) {
+            float *dst = p.part + (static_cast<int64_t>(done.slot) * 2 * kNR + q) * (2 * kD) + col;
+            dst[0] = y1;
+            dst[kNR * (2 * kD)] = y2;
+          }
         }
       }
-      named_barrier_sync(2, kConsumers);
-      if (pass == 0) {
+      // The row's (m, l): per slot for the join, per item for the weights.
+      if (quarter == 0 && (!direct || p.item_ml != nullptr)) {
+        float2 *ml = (direct ? p.item_ml + static_cast<int64_t>(done.item) * 2 * kNR
+                             : p.part_ml + static_cast<int64_t>(done.slot) * 2 * kNR) +
+                     map * kNR;
+        if (lane < done_real) ml[lane] = make_float2(sm->ref[parity][map][lane], l_of(map, lane));
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->o_empty[(seg - 1) % G::kOBufs]);
+      if (direct) {
+        // Head norm: row sums over the lanes, the four quarters and (d = 128) both halves.
+        const auto row_sum = [&](int q) {
+          float y =
+              (sm->rsum[0][0][q] + sm->rsum[0][1][q]) + (sm->rsum[0][2][q] + sm->rsum[0][3][q]);
+          if (kD == 128)
+            y += (sm->rsum[1][0][q] + sm->rsum[1][1][q]) + (sm->rsum[1][2][q] + sm->rsum[1][3][q]);
+          return y;
+        };
+#pragma unroll 1
+        for (int pass = p.headnorm == 2 ? 0 : 1; pass < 2 && p.headnorm; ++pass) {  // mean, square
+#pragma unroll
+          for (int k = 0; k < kChunks / kStep; ++k) {
+            const int q0 = kW * (kStep * k + (kStep == 2 ? half : 0));
+            if (idle || q0 >= done_real) break;
+#pragma unroll
+            for (int e = 0; e < kW; ++e) {
+              if (q0 + e >= done_real) break;
+              const float y = o[kW * k + e];
+              const float z = warp_sum(pass ? y * y : y);
+              if (lane == 0) sm->rsum[kD == 128 ? half : 0][quarter][q0 + e] = z;
+            }
+          }
+          named_barrier_sync(2, kConsumers);
+          if (pass == 0) {
+#pragma unroll
+            for (int k = 0; k < kChunks / kStep; ++k) {
+              const int q0 = kW * (kStep * k + (kStep == 2 ? half : 0));
+              if (idle || q0 >= done_real) break;
+#pragma unroll
+              for (int e = 0; e < kW; ++e)
+                if (q0 + e < done_real) o[kW * k + e] -= row_sum(q0 + e) * (0.5f / kD);
+            }
+            named_barrier_sync(2, kConsumers);
+          }
+        }
 #pragma unroll
         for (int k = 0; k < kChunks / kStep; ++k) {
           const int q0 = kW * (kStep * k + (kStep == 2 ? half : 0));
-          if (idle || q0 >= real) break;
+          if (idle || q0 >= done_real) break;
 #pragma unroll
-          for (int e = 0; e < kW; ++e)
-            if (q0 + e < real) o[kW * k + e] -= row_sum(q0 + e) * (0.5f / kD);
+          for (int e = 0; e < kW; ++e) {
+            const int q = q0 + e;
+            if (q >= done_real) break;
+            float y = o[kW * k + e];
+            if (p.headnorm && (done_rows[q].last >= 0 || done_poisoned)) {
+              y *= rsqrtf(row_sum(q) * (0.5f / kD) + p.eps) * p.out_scale;
+              if (kEarly)
+                y *= gain[kW * k + e];
+              else if (p.norm_w != nullptr)
+                y *= __ldg(p.norm_w + done_rows[q].head * (2 * kD) + col);
+            }
+            p.out[done_rows[q].out + col] = __float2bfloat16_rn(y);
+          }
         }
-        named_barrier_sync(2, kConsumers);
       }
     }
+    if (stop) break;
+    if (d.flags & kLast) {  // this segment's sums and references, read after the next vote
 #pragma unroll
-    for (int k = 0; k < kChunks / kStep; ++k) {
-      const int q0 = kW * (kStep * k + (kStep == 2 ? half : 0));
-      if (idle || q0 >= real) break;
-#pragma unroll
-      for (int e = 0; e < kW; ++e) {
-        const int q = q0 + e;
+      for (int q = 0; q < kNR; ++q) {
         if (q >= real) break;
-        float y = o[kW * k + e];
-        if (p.headnorm && (rows[q].last >= 0 || poisoned)) {
-          y *= rsqrtf(row_sum(q) * (0.5f / kD) + p.eps) * p.out_scale;
-          if (p.norm_w != nullptr) y *= __ldg(p.norm_w + rows[q].head * (2 * kD) + col);
-        }
-        p.out[rows[q].out + col] = __float2bfloat16_rn(y);
+        const float y = warp_sum(l[q]);
+        if (lane == 0) sm->lsum[seg & 1][map][quarter][q] = poisoned ? NAN : y;
       }
+      if (quarter == 0 && lane < real) sm->ref[seg & 1][map][lane] = sm->m[m_turn][map][lane];
+      if (tid == 0) sm->done[seg & 1] = d;
+      done_poisoned = poisoned;
+      done_late = late;
+      pending = true;
+      ++seg;
     }
   }
 }
@@ -1079,7 +1135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     tmem_alloc(&sm->tmem, G::kTmemCols);
     tmem_relinquish();
-  } else if (threadIdx.x == 0) {
+  } else if (threadIdx.x == 32 * kSoftmaxWarp) {
     for (int s = 0; s < L::kKeyRing; ++s) {
       mbar_init(&sm->k_full[s], 1);
       mbar_init(&sm->k_empty[s], 1);
@@ -1110,7 +1166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     load_warp<kD, kFp8, kNR, false>(p, &mk1, &mk2, &mv, smem, sm, share);
   else if (warp == kMmaWarp)
     mma_warp<kD, kFp8, kNR>(p, smem, sm);
-  else
+  else if (warp >= kSoftmaxWarp)
     softmax_warps<kD, kFp8, kNR>(p, smem, sm);
   __syncwarp();
   tc_fence_before_sync();
@@ -1285,50 +1341,63 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
   const uint32_t first_tile = before * p.kv_heads * p.row_blocks + hk * p.row_blocks * units;
   grid_dependency_wait();
   if (timed_out(p)) return;
-  for (int k = threadIdx.x; k < 2 * p.rows; k += kJoinThreads) {
+  // The first rows' logits are on their way while the statistics are formed, a warp per row and
+  // map.
+  const float *x1 = p.logits + static_cast<int64_t>(bh) * 2 * p.rows * p.padded + key;
+  const float *x2 = x1 + p.rows * p.padded;
+  constexpr int kAhead = 1;
+  float4 ahead[kAhead][2];
+#pragma unroll
+  for (int r = 0; r < kAhead; ++r)
+    if (r < p.rows && key < len) {
+      ahead[r][0] = *reinterpret_cast<const float4 *>(x1 + r * p.padded);
+      ahead[r][1] = *reinterpret_cast<const float4 *>(x2 + r * p.padded);
+    }
+  const int lane = threadIdx.x % 32;
+#pragma unroll 2
+  for (int k = threadIdx.x / 32; k < 2 * p.rows; k += kJoinThreads / 32) {
     const int map = k & 1, r = k >> 1;
     const int rb = r / jp.row_tile, row = r - rb * jp.row_tile;
     Parts parts = {0, 1};
     if (!p.whole) parts = parts_of(all, first_tile + rb * units, units);
-    float top, sum;
-    if (parts.n == 1) {
+    float top = -INFINITY, sum = 0.f;
+    for (int s = lane; s < parts.n; s += 32) {
       const float2 ml =
-          p.item_ml[((static_cast<int64_t>(bh) * p.row_blocks + rb) * 2 + map) * jp.row_tile + row];
-      top = ml.x;
-      sum = ml.y;
-    } else {
-      top = -INFINITY;
-      sum = 0.f;
-      for (int s = 0; s < parts.n; ++s)
-        top = fmaxf(top, p.part_ml[(parts.slot(s) * 2ll + map) * jp.row_tile + row].x);
-      for (int s = 0; s < parts.n; ++s) {
-        const float2 ml = p.part_ml[(parts.slot(s) * 2ll + map) * jp.row_tile + row];
-        sum = fmaf(ml.x == top ? 1.f : exp2f(ml.x - top), ml.y, sum);
-      }
+          parts.n == 1
+              ? p.item_ml[((static_cast<int64_t>(bh) * p.row_blocks + rb) * 2 + map) * jp.row_tile + row]
+              : p.part_ml[(parts.slot(s) * 2ll + map) * jp.row_tile + row];
+      const float y = fmaxf(top, ml.x);
+      sum = (top == y ? sum : sum * exp2f(top - y)) + (ml.x == y ? ml.y : exp2f(ml.x - y) * ml.y);
+      top = y;
     }
+    const float y = warp_max(top);
+    sum = warp_sum(top == y ? sum : sum * exp2f(top - y));
     const int i = p.by_group.div(r);
     const bool none = len - p.N + i < 0;  // the row sees no key: it adds nothing
-    float *dst = reinterpret_cast<float *>(row_stat + r) + 2 * map;
-    dst[0] = none ? 0.f : top;
-    dst[1] = none ? 0.f
-                  : (map ? __ldg(p.lambda + hk * p.group + r - i * p.group) : 1.f) / sum;
+    if (lane == 0) {
+      float *dst = reinterpret_cast<float *>(row_stat + r) + 2 * map;
+      dst[0] = none ? 0.f : y;
+      dst[1] = none ? 0.f
+                    : (map ? __ldg(p.lambda + hk * p.group + r - i * p.group) : 1.f) / sum;
+    }
   }
   __syncthreads();
   if (key >= len) return;
-  const float *x1 = p.logits + static_cast<int64_t>(bh) * 2 * p.rows * p.padded + key;
-  const float *x2 = x1 + p.rows * p.padded;
   float w[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int r = 0; r < p.rows; ++r) {
-    const float4 a = *reinterpret_cast<const float4 *>(x1 + r * p.padded);
-    const float4 c = *reinterpret_cast<const float4 *>(x2 + r * p.padded);
-    const float4 st = row_stat[r];
-    if (st.y == 0.f) continue;
+  const auto add = [&](const float4 &a, const float4 &c, const float4 &st) {
+    if (st.y == 0.f) return;
     w[0] += fabsf(exp2f(a.x - st.x) * st.y - exp2f(c.x - st.z) * st.w);
     w[1] += fabsf(exp2f(a.y - st.x) * st.y - exp2f(c.y - st.z) * st.w);
     w[2] += fabsf(exp2f(a.z - st.x) * st.y - exp2f(c.z - st.z) * st.w);
     w[3] += fabsf(exp2f(a.w - st.x) * st.y - exp2f(c.w - st.z) * st.w);
-  }
+  };
+#pragma unroll
+  for (int r = 0; r < kAhead; ++r)
+    if (r < p.rows) add(ahead[r][0], ahead[r][1], row_stat[r]);
+#pragma unroll 4
+  for (int r = kAhead; r < p.rows; ++r)
+    add(*reinterpret_cast<const float4 *>(x1 + r * p.padded),
+        *reinterpret_cast<const float4 *>(x2 + r * p.padded), row_stat[r]);
   float *dst = p.weights + (static_cast<int64_t>(page) * p.kv_heads + hk) * p.page_size +
                p.by_page.mod(key);
 #pragma unroll
@@ -1337,7 +1406,7 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
 }
 
 template <int kD>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, 6)
     diffpaged_join_kernel(const __grid_constant__ JoinParams jp) {
   const uint32_t joins = static_cast<uint32_t>(jp.ctas - 1) * jp.join_rows;
   if (blockIdx.x < joins)
