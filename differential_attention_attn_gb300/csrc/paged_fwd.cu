@@ -1025,7 +1025,8 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
         float2 *ml = (direct ? p.item_ml + static_cast<int64_t>(done.item) * 2 * kNR
                              : p.part_ml + static_cast<int64_t>(done.slot) * 2 * kNR) +
                      map * kNR;
-        if (lane < done_real) ml[lane] = make_float2(sm->ref[parity][map][lane], l_of(map, lane));
+        if (lane < done_real)
+          ml[lane] = make_float2(sm->ref[parity][map][lane], done_poisoned ? -1.f : l_of(map, lane));
       }
       tc_fence_before_sync();
       __syncwarp();
@@ -1182,13 +1183,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 // what is cut where while that one runs, and then awaits its end.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
-constexpr int kMaxParts = 256;                 // more than SMs
-constexpr int kWeightKeys = 4 * kJoinThreads;  // keys per weight block, four a thread
+constexpr int kMaxParts = 256;       // more than SMs
+constexpr int kWeightBlocks = 1216;  // in all, about: two rounds of four per SM
 
 struct JoinParams {
   FwdParams f;
   int32_t ctas, join_rows, row_tile;  // row_tile: rows of a block of the main kernel
-  int32_t weight_chunks;              // per (sequence, key/value head); 0 without weights
+  int32_t by_item;                    // joins are numbered by item, else by boundary
+  uint32_t joins;                     // blocks that join
+  int32_t weight_blocks;              // per (sequence, key/value head); 0 without weights
+  int32_t row_groups;                 // warps that share a key's rows (1, 2, 4 or 8)
 };
 
 __device__ __forceinline__ bool timed_out(const FwdParams &p) {
@@ -1207,26 +1211,57 @@ __device__ __forceinline__ float block_sum(float x, float *scratch) {
   return y;
 }
 
-// Block (boundary, row): one row of the item cut at that boundary, done by the first boundary of
-// each item.
+// The shares of all tiles and the tiles, per head and row block, before sequence b (one warp).
+__device__ __forceinline__ Shares all_shares(const FwdParams &p, uint32_t ctas, int32_t b,
+                                             uint32_t *before) {
+  const int32_t most = p.max_pages * p.page_size;
+  uint32_t total = 0, mine = 0;
+  for (int32_t x = threadIdx.x % 32; x < p.B; x += 32) {
+    const uint32_t u = units_of(__ldg(p.kv_len + x), most);
+    total += u;
+    mine += x < b ? u : 0;
+  }
+  total = __reduce_add_sync(0xffffffffu, total) * p.kv_heads * p.row_blocks;
+  *before = __reduce_add_sync(0xffffffffu, mine);
+  Shares all;
+  all.ctas = min(ctas, total);
+  all.each = total / all.ctas;
+  all.more = total - all.each * all.ctas;
+  return all;
+}
+
+// Block (cut item, row): joins one row.  The cut items are found from the boundaries between
+// shares (each item by its first one) or, where these are fewer, from all items.
 template <int kD>
 __device__ void join_row(const JoinParams &jp) {
   const FwdParams &p = jp.f;
   __shared__ float factor[2][kMaxParts];
   __shared__ float scratch[kJoinThreads / 32];
-  __shared__ float half[2][2 * kD];
+  __shared__ float half[2 * kD];
   __shared__ int4 cut;  // item, its parts, the sequence's length; item -1: nothing to do
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int row = blockIdx.x % jp.join_rows;
+  const uint32_t which = blockIdx.x / jp.join_rows;
+  const int row = static_cast<int>(blockIdx.x - which * jp.join_rows);
   if (warp == 0) {
-    const uint32_t cta = 1 + blockIdx.x / jp.join_rows;
-    const Share s = find_share(p, cta, jp.ctas);
     int4 x = make_int4(-1, 0, 0, 0);
-    if (s.tile > 0) {
-      const uint32_t start = s.begin - s.tile;
-      const Parts parts = parts_of(s.all, start, s.units);
-      if (parts.first / 2 + 1 == static_cast<int>(cta) && s.rb * jp.row_tile + row < p.rows)
-        x = make_int4((s.b * p.kv_heads + s.hk) * p.row_blocks + s.rb, parts.first, parts.n, s.len);
+    Parts parts = {0, 1};
+    if (jp.by_item) {
+      const uint32_t bh = which / p.row_blocks;
+      const int32_t b = static_cast<int32_t>(bh / p.kv_heads);
+      uint32_t before;
+      const Shares all = all_shares(p, jp.ctas, b, &before);
+      const int32_t len = __ldg(p.kv_len + b);
+      const uint32_t units = units_of(len, p.max_pages * p.page_size);
+      const uint32_t heads = p.kv_heads * p.row_blocks;
+      parts = parts_of(all, before * heads + (which - b * heads) * units, units);
+      if (parts.n > 1) x = make_int4(static_cast<int>(which), parts.first, parts.n, len);
+    } else {
+      const Share s = find_share(p, which + 1, jp.ctas);
+      if (s.tile > 0) {
+        parts = parts_of(s.all, s.begin - s.tile, s.units);
+        if (parts.first / 2 == static_cast<int>(which))
+          x = make_int4((s.b * p.kv_heads + s.hk) * p.row_blocks + s.rb, parts.first, parts.n, s.len);
+      }
     }
     if (lane == 0) cut = x;
   }
@@ -1237,16 +1272,19 @@ __device__ void join_row(const JoinParams &jp) {
   const int rb = cut.x % p.row_blocks, bh = cut.x / p.row_blocks;
   const int hk = bh % p.kv_heads, b = bh / p.kv_heads;
   const int r = rb * jp.row_tile + row;
+  if (r >= p.rows) return;
   const int i = p.by_group.div(r), h = hk * p.group + r - i * p.group;
   constexpr int kGroups = kJoinThreads / (2 * kD);  // threads per column: 2 (d = 64) or 1
   constexpr int kAhead = 4;
   const int col = threadIdx.x % (2 * kD), part = threadIdx.x / (2 * kD);
   const float *src = p.part + static_cast<int64_t>(row) * (2 * kD) + col;
   const int64_t map_step = static_cast<int64_t>(jp.row_tile) * (2 * kD);
+  const float lam = __ldg(p.lambda + h);
+  const float gain = p.headnorm && p.norm_w != nullptr ? __ldg(p.norm_w + h * (2 * kD) + col) : 1.f;
   grid_dependency_wait();
 
   // The first parts' values are on their way while the factors 2^(m_s - M) / l of both maps,
-  // l = sum 2^(m_s - M) l_s, are formed by warps 0 and 1.
+  // l = sum 2^(m_s - M) l_s, are formed by warps 0 and 1 (l_s < 0: a bad page or length).
   float ahead[kAhead][2];
 #pragma unroll
   for (int k = 0; k < kAhead; ++k)
@@ -1257,6 +1295,7 @@ __device__ void join_row(const JoinParams &jp) {
     }
   if (warp < 2) {
     float top = -INFINITY, sum = 0.f;
+    bool bad = false;
     for (int k = lane; k < parts.n; k += 32)
       top = fmaxf(top, p.part_ml[(parts.slot(k) * 2ll + warp) * jp.row_tile + row].x);
     top = warp_max(top);
@@ -1265,9 +1304,11 @@ __device__ void join_row(const JoinParams &jp) {
       const float f = ml.x == top ? 1.f : exp2f(ml.x - top);
       factor[warp][k] = f;
       sum += f * ml.y;
+      bad |= ml.y < 0.f;
     }
     sum = warp_sum(sum);
-    const float c = (warp ? -__ldg(p.lambda + h) : 1.f) / sum;
+    if (__any_sync(0xffffffffu, bad)) sum = NAN;
+    const float c = (warp ? -lam : 1.f) / sum;
     for (int k = lane; k < parts.n; k += 32) factor[warp][k] *= c;
   }
   __syncthreads();
@@ -1283,136 +1324,173 @@ __device__ void join_row(const JoinParams &jp) {
     o = fmaf(factor[0][k], x[0], fmaf(factor[1][k], x[map_step], o));
   }
   if (kGroups == 2) {
-    half[part][col] = o;
+    if (part == 1) half[col] = o;
     __syncthreads();
-    o = half[0][col] + half[kGroups - 1][col];
+    if (part == 0) o += half[col];
   }
   const bool none = len - p.N + i < 0;  // padding: sees no key (the factors are not numbers)
-  if (none) o = 0.f;
-  const float mine = part == 0 ? 1.f : 0.f;  // each column counted once
-  if (p.headnorm == 2) o -= block_sum(mine * o, scratch) * (0.5f / kD);
+  if (none || part != 0) o = 0.f;       // each column counted once
+  if (p.headnorm == 2) {
+    o -= block_sum(o, scratch) * (0.5f / kD);
+    if (part != 0) o = 0.f;
+  }
   if (p.headnorm) {
-    const float ss = block_sum(mine * o * o, scratch);
-    float y = rsqrtf(ss * (0.5f / kD) + p.eps) * p.out_scale;
-    if (p.norm_w != nullptr) y *= __ldg(p.norm_w + h * (2 * kD) + col);
-    o = none ? 0.f : o * y;
+    const float ss = block_sum(o * o, scratch);
+    if (!none) o *= rsqrtf(ss * (0.5f / kD) + p.eps) * p.out_scale * gain;
   }
   if (part == 0)
     p.out[b * p.outs.b + h * p.outs.h + i * p.outs.n + col] =
         __float2bfloat16_rn(timed_out(p) ? NAN : o);
 }
 
-// Block (sequence, key/value head, 1024 keys): weights[j] += sum_r |map1 - lambda map2|.
+// Block (sequence, key/value head, k): weights[j] += sum_r |map1 - lambda map2| of every
+// weight_blocks-th run of keys.  A thread takes four keys of every row_groups-th row, at most four
+// rows of both maps in flight; the groups' sums are added in their order.
 __device__ void add_weights(const JoinParams &jp, uint32_t block) {
   const FwdParams &p = jp.f;
   extern __shared__ float4 row_stat[];  // per row: M1, 1 / l1, M2, lambda / l2
-  __shared__ Shares all;
-  __shared__ uint32_t before;  // tiles of the sequences before, in one head and row block
-  const uint32_t bh = block / jp.weight_chunks;
-  const int chunk = static_cast<int>(block - bh * jp.weight_chunks);
+  __shared__ float4 sums[kJoinThreads];
+  __shared__ Shares shared_all;
+  __shared__ uint32_t shared_before;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int groups = jp.row_groups, group = warp & (groups - 1);
+  const int run = kJoinThreads * 4 / groups;  // keys of a pass
+  const uint32_t bh = block / jp.weight_blocks;
   const int b = static_cast<int>(bh / p.kv_heads), hk = static_cast<int>(bh - b * p.kv_heads);
   const int32_t len = __ldg(p.kv_len + b);
   const int32_t most = p.max_pages * p.page_size;
-  if (len < 0 || len > most || chunk * kWeightKeys >= len) return;
-  const int32_t *table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-  bool bad = false;
-  for (int k = threadIdx.x; k * p.page_size < len; k += kJoinThreads)
-    bad |= static_cast<uint32_t>(__ldg(table + k)) >= static_cast<uint32_t>(p.num_pages);
-  if (threadIdx.x < 32) {
-    uint32_t total = 0, mine = 0;
-    for (int32_t x = threadIdx.x; x < p.B; x += 32) {
-      const uint32_t u = units_of(__ldg(p.kv_len + x), most);
-      total += u;
-      mine += x < b ? u : 0;
-    }
-    total = __reduce_add_sync(0xffffffffu, total) * p.kv_heads * p.row_blocks;
-    mine = __reduce_add_sync(0xffffffffu, mine);
-    if (threadIdx.x == 0) {
-      all.ctas = min(static_cast<uint32_t>(jp.ctas), total);
-      all.each = total / all.ctas;
-      all.more = total - all.each * all.ctas;
-      before = mine;
-    }
-  }
-  if (__syncthreads_or(bad)) return;  // the sequence's weights stay as they are
-  const int32_t key = chunk * kWeightKeys + 4 * static_cast<int32_t>(threadIdx.x);
-  const int32_t page = key < len ? __ldg(table + p.by_page.div(key)) : 0;
-  const uint32_t units = units_of(len, most);
-  const uint32_t first_tile = before * p.kv_heads * p.row_blocks + hk * p.row_blocks * units;
-  grid_dependency_wait();
-  if (timed_out(p)) return;
-  // The first rows' logits are on their way while the statistics are formed, a warp per row and
-  // map.
-  const float *x1 = p.logits + static_cast<int64_t>(bh) * 2 * p.rows * p.padded + key;
-  const float *x2 = x1 + p.rows * p.padded;
-  constexpr int kAhead = 1;
-  float4 ahead[kAhead][2];
-#pragma unroll
-  for (int r = 0; r < kAhead; ++r)
-    if (r < p.rows && key < len) {
-      ahead[r][0] = *reinterpret_cast<const float4 *>(x1 + r * p.padded);
-      ahead[r][1] = *reinterpret_cast<const float4 *>(x2 + r * p.padded);
-    }
-  const int lane = threadIdx.x % 32;
-#pragma unroll 2
-  for (int k = threadIdx.x / 32; k < 2 * p.rows; k += kJoinThreads / 32) {
-    const int map = k & 1, r = k >> 1;
-    const int rb = r / jp.row_tile, row = r - rb * jp.row_tile;
-    Parts parts = {0, 1};
-    if (!p.whole) parts = parts_of(all, first_tile + rb * units, units);
-    float top = -INFINITY, sum = 0.f;
-    for (int s = lane; s < parts.n; s += 32) {
-      const float2 ml =
-          parts.n == 1
-              ? p.item_ml[((static_cast<int64_t>(bh) * p.row_blocks + rb) * 2 + map) * jp.row_tile + row]
-              : p.part_ml[(parts.slot(s) * 2ll + map) * jp.row_tile + row];
-      const float y = fmaxf(top, ml.x);
-      sum = (top == y ? sum : sum * exp2f(top - y)) + (ml.x == y ? ml.y : exp2f(ml.x - y) * ml.y);
-      top = y;
-    }
-    const float y = warp_max(top);
-    sum = warp_sum(top == y ? sum : sum * exp2f(top - y));
-    const int i = p.by_group.div(r);
-    const bool none = len - p.N + i < 0;  // the row sees no key: it adds nothing
+  const int32_t first = static_cast<int32_t>(block - bh * jp.weight_blocks) * run;
+  if (len < 0 || len > most || first >= len) return;
+  if (warp == 0 && !p.whole) {
+    uint32_t before;
+    const Shares all = all_shares(p, jp.ctas, b, &before);
     if (lane == 0) {
-      float *dst = reinterpret_cast<float *>(row_stat + r) + 2 * map;
-      dst[0] = none ? 0.f : y;
-      dst[1] = none ? 0.f
-                    : (map ? __ldg(p.lambda + hk * p.group + r - i * p.group) : 1.f) / sum;
+      shared_all = all;
+      shared_before = before;
     }
   }
   __syncthreads();
-  if (key >= len) return;
-  float w[4] = {0.f, 0.f, 0.f, 0.f};
-  const auto add = [&](const float4 &a, const float4 &c, const float4 &st) {
-    if (st.y == 0.f) return;
-    w[0] += fabsf(exp2f(a.x - st.x) * st.y - exp2f(c.x - st.z) * st.w);
-    w[1] += fabsf(exp2f(a.y - st.x) * st.y - exp2f(c.y - st.z) * st.w);
-    w[2] += fabsf(exp2f(a.z - st.x) * st.y - exp2f(c.z - st.z) * st.w);
-    w[3] += fabsf(exp2f(a.w - st.x) * st.y - exp2f(c.w - st.z) * st.w);
+  const uint32_t units = units_of(len, most);
+  grid_dependency_wait();
+  if (timed_out(p)) return;
+
+  // A pass's first loads: its logits of this warp's first four rows, and the weights they go to.
+  const int32_t *table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+  const float *logits = p.logits + static_cast<int64_t>(bh) * 2 * p.rows * p.padded;
+  int32_t key = first + (warp / groups) * 128 + 4 * lane;
+  float4 x1[4], x2[4];
+  float *dst = nullptr;
+  const auto load_rows = [&](int r0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = r0 + k * groups;
+      if (r < p.rows && key < len) {
+        x1[k] = *reinterpret_cast<const float4 *>(logits + r * p.padded + key);
+        x2[k] = *reinterpret_cast<const float4 *>(logits + (p.rows + r) * p.padded + key);
+      }
+    }
   };
-#pragma unroll
-  for (int r = 0; r < kAhead; ++r)
-    if (r < p.rows) add(ahead[r][0], ahead[r][1], row_stat[r]);
+  const auto load_pass = [&] {
+    load_rows(group);
+    if (key < len && group == 0)
+      dst = p.weights +
+            (static_cast<int64_t>(__ldg(table + p.by_page.div(key))) * p.kv_heads + hk) * p.page_size +
+            p.by_page.mod(key);
+  };
+  load_pass();
+
+  // The rows' statistics, a warp per row and map: the first 32 parts' in one load.
+  bool bad = false;
 #pragma unroll 4
-  for (int r = kAhead; r < p.rows; ++r)
-    add(*reinterpret_cast<const float4 *>(x1 + r * p.padded),
-        *reinterpret_cast<const float4 *>(x2 + r * p.padded), row_stat[r]);
-  float *dst = p.weights + (static_cast<int64_t>(page) * p.kv_heads + hk) * p.page_size +
-               p.by_page.mod(key);
+  for (int k = warp; k < 2 * p.rows; k += kJoinThreads / 32) {
+    const int map = k & 1, r = k >> 1;
+    const int rb = r / jp.row_tile, row = r - rb * jp.row_tile;
+    Parts parts = {0, 1};
+    if (!p.whole)
+      parts = parts_of(shared_all,
+                       shared_before * p.kv_heads * p.row_blocks + (hk * p.row_blocks + rb) * units,
+                       units);
+    const auto state = [&](int s) {
+      return parts.n == 1
+                 ? p.item_ml[((static_cast<int64_t>(bh) * p.row_blocks + rb) * 2 + map) * jp.row_tile + row]
+                 : p.part_ml[(parts.slot(s) * 2ll + map) * jp.row_tile + row];
+    };
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < parts.n) ml = state(lane);
+    bad |= ml.y < 0.f;
+    for (int s = lane + 32; s < parts.n; s += 32) {
+      const float2 more = state(s);
+      bad |= more.y < 0.f;
+      const float y = fmaxf(ml.x, more.x);
+      ml.y = (ml.x == y ? ml.y : ml.y * exp2f(ml.x - y)) +
+             (more.x == y ? more.y : exp2f(more.x - y) * more.y);
+      ml.x = y;
+    }
+    const float y = warp_max(ml.x);
+    const float sum = warp_sum(ml.x == y ? ml.y : ml.y * exp2f(ml.x - y));
+    const int i = p.by_group.div(r);
+    const bool none = len - p.N + i < 0;  // the row sees no key: it adds nothing
+    if (lane == 0) {
+      float *out = reinterpret_cast<float *>(row_stat + r) + 2 * map;
+      out[0] = none ? 0.f : y;
+      out[1] = none ? 0.f
+                    : (map ? __ldg(p.lambda + hk * p.group + r - i * p.group) : 1.f) / sum;
+    }
+  }
+  if (__syncthreads_or(bad)) return;  // a bad page: the sequence's weights stay as they are
+#pragma unroll 1
+  for (int32_t at = first; at < len; at += run * jp.weight_blocks) {
+    float w[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int r0 = group; r0 < p.rows; r0 += 4 * groups) {
+      if (r0 != group) load_rows(r0);
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (key + k < len) dst[k] += w[k];
+      for (int k = 0; k < 4; ++k) {
+        const int r = r0 + k * groups;
+        if (r >= p.rows) break;
+        const float4 st = row_stat[r];
+        if (st.y == 0.f) continue;
+        w[0] += fabsf(exp2f(x1[k].x - st.x) * st.y - exp2f(x2[k].x - st.z) * st.w);
+        w[1] += fabsf(exp2f(x1[k].y - st.x) * st.y - exp2f(x2[k].y - st.z) * st.w);
+        w[2] += fabsf(exp2f(x1[k].z - st.x) * st.y - exp2f(x2[k].z - st.z) * st.w);
+        w[3] += fabsf(exp2f(x1[k].w - st.x) * st.y - exp2f(x2[k].w - st.z) * st.w);
+      }
+    }
+    const int32_t here = key;
+    float *to = dst;
+    float old[4] = {0.f, 0.f, 0.f, 0.f};
+    if (group == 0)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (here + k < len) old[k] = to[k];
+    key += run * jp.weight_blocks;
+    if (at + run * jp.weight_blocks < len) load_pass();
+    if (groups > 1) {
+      sums[threadIdx.x] = make_float4(w[0], w[1], w[2], w[3]);
+      __syncthreads();
+      if (group == 0)
+        for (int k = 1; k < groups; ++k) {
+          const float4 y = sums[threadIdx.x + 32 * k];
+          w[0] += y.x;
+          w[1] += y.y;
+          w[2] += y.z;
+          w[3] += y.w;
+        }
+      __syncthreads();
+    }
+    if (group == 0)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (here + k < len) to[k] = old[k] + w[k];
+  }
 }
 
 template <int kD>
-__global__ void __launch_bounds__(kJoinThreads, 6)
+__global__ void __launch_bounds__(kJoinThreads, 4)
     diffpaged_join_kernel(const __grid_constant__ JoinParams jp) {
-  const uint32_t joins = static_cast<uint32_t>(jp.ctas - 1) * jp.join_rows;
-  if (blockIdx.x < joins)
+  if (blockIdx.x < jp.joins)
     join_row<kD>(jp);
   else
-    add_weights(jp, blockIdx.x - joins);
+    add_weights(jp, blockIdx.x - jp.joins);
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -1497,14 +1575,13 @@ diffattn_status launch_rows(const FwdParams &p, const CUtensorMap (&maps)[3],
 
 template <int kD>
 diffattn_status launch_join(const JoinParams &jp, cudaStream_t stream) {
-  const int64_t blocks = static_cast<int64_t>(jp.ctas - 1) * jp.join_rows +
-                         static_cast<int64_t>(jp.f.B) * jp.f.kv_heads * jp.weight_chunks;
+  const int64_t blocks = static_cast<int64_t>(jp.joins) + static_cast<int64_t>(jp.f.B) * jp.f.kv_heads * jp.weight_blocks;
   if (blocks == 0) return DIFFATTN_OK;
   if (blocks > INT32_MAX) return DIFFATTN_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = jp.weight_chunks ? sizeof(float4) * jp.f.rows : 0;
+  cfg.dynamicSmemBytes = jp.weight_blocks ? sizeof(float4) * jp.f.rows : 0;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1534,9 +1611,12 @@ bool plan_paged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache, boo
   const int64_t most = cache.max_pages * cache.page_size;
   const int64_t units = (most + kTile - 1) / kTile;
   q.padded = units * kTile;
-  // One CTA per item where no item can have more tiles than the join's launch would cost.
+  // One CTA per item, and nothing to join, where equal shares would save less time than the join
+  // and the second segment of most CTAs take (6 us, of 1 us a tile).  64 items of 8 tiles on 152
+  // SMs: 12.6 us, in shares 14.6 us; of 16 tiles 20.2 us and 18.3 us.  16 items of 4 tiles: 8.1
+  // and 9.1 us, of 8 tiles 11.7 and 9.5 us.
   if (items * static_cast<double>(units) >= 2147483648.0) return false;
-  q.whole = units <= 2 && q.items <= sm_count;
+  q.whole = q.items <= sm_count && units * (sm_count - q.items) <= int64_t{6} * sm_count;
   q.ctas = q.whole ? static_cast<int>(q.items) : sm_count;
   if (!q.whole && q.items * units < sm_count) q.ctas = static_cast<int>(q.items * units);
   const size_t slots = q.whole ? 0 : 2 * static_cast<size_t>(q.ctas);
@@ -1623,13 +1703,23 @@ diffattn_status launch_paged_fwd(const diffattn_desc &desc, const diffpaged_cach
               : (fp8 ? launch_rows<128, true>(p, maps, plan, stream)
                      : launch_rows<128, false>(p, maps, plan, stream));
   if (st != DIFFATTN_OK) return st;
-  JoinParams jp;
+  JoinParams jp = {};
   jp.f = p;
   jp.ctas = plan.whole ? 1 : plan.ctas;
   jp.row_tile = plan.row_tile;
   jp.join_rows = p.rows < jp.row_tile ? p.rows : jp.row_tile;
-  jp.weight_chunks =
-      accumulate ? static_cast<int32_t>((plan.padded + kWeightKeys - 1) / kWeightKeys) : 0;
+  // Cut items are at most one per boundary.
+  const int64_t cuts = plan.whole ? 0 : plan.ctas - 1;
+  jp.by_item = plan.items < cuts ? 1 : 0;
+  jp.joins = static_cast<uint32_t>((jp.by_item ? plan.items : cuts) * jp.join_rows);
+  jp.row_groups = p.rows <= 4 ? 1 : p.rows <= 8 ? 2 : p.rows <= 16 ? 4 : 8;
+  if (accumulate) {
+    // As many blocks as find work, but not more than a few per SM: each forms the rows' statistics.
+    const int64_t run = 4 * kJoinThreads / jp.row_groups, heads = desc.B * cache.kv_heads;
+    const int64_t runs = (plan.padded + run - 1) / run;
+    const int64_t share = (int64_t{kWeightBlocks} + heads - 1) / heads;
+    jp.weight_blocks = static_cast<int32_t>(runs < share ? runs : share);
+  }
   return d == 64 ? launch_join<64>(jp, stream) : launch_join<128>(jp, stream);
 }
 
