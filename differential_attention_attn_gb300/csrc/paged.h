@@ -4,6 +4,8 @@
 
 #include <cuda_runtime.h>
 
+#include <cstdint>
+
 #include "../../include/diffattn_paged.h"
 #include "internal.h"
 
@@ -46,6 +48,22 @@ size_t paged_evict_bytes(const diffattn_desc &desc, const diffpaged_cache &cache
 diffattn_status launch_paged_evict(const diffattn_desc &desc, const diffpaged_cache &cache,
                                    int64_t keep, int64_t recent, void *workspace,
                                    cudaStream_t stream);
+
+// Exact division of 0 <= n < 2^31 by a launch constant: a multiply and a shift.
+struct FastDiv {
+  uint32_t mul, shift, d;
+  __device__ __forceinline__ int32_t div(int32_t n) const {
+    return static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> shift);
+  }
+  __device__ __forceinline__ int32_t mod(int32_t n) const {
+    return n - div(n) * static_cast<int32_t>(d);
+  }
+};
+inline FastDiv fast_div(uint32_t d) {  // 2^(s - 1) < d <= 2^s, mul = ceil(2^(31 + s) / d)
+  uint32_t s = 0;
+  while ((uint64_t{1} << s) < d) ++s;
+  return {static_cast<uint32_t>(((uint64_t{1} << (31 + s)) + d - 1) / d), 31 + s, d};
+}
 
 // Stores DIFFATTN_ERR_PAGE in the call's status word unless another code is there.
 __device__ __forceinline__ void report_bad_page(int32_t *status) {

@@ -9,9 +9,8 @@
 //
 // Bound: a copy, so HBM bandwidth for prompts (B Hkv N rows of 8 d bytes read
 // and written) and the chain length -> page number -> store for a few tokens.
-// One warp takes whole rows: a row of k1 | k2 | v is 32 (d = 64) or 64 sixteen-
-// byte units, so each lane moves one or two units a row and every access is
-// a full 128-byte line.
+// A row of k1 | k2 | v is 32 (d = 64) or 64 sixteen-byte units, so each lane of
+// a warp moves one or two of them and every access is a full 128-byte line.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -20,11 +19,13 @@
 
 #include "debug_check.cuh"
 #include "paged.h"
+#include "ptx.cuh"
 
 namespace diffattn {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr uint32_t kFewRows = 16384;
 
 struct AppendParams {
   const uint8_t *src[3];  // k1, k2, v (bf16)
@@ -37,6 +38,7 @@ struct AppendParams {
   int32_t *status;
   uint32_t rows;  // B * kv_heads * N
   uint32_t N, kv_heads, page_size, max_pages, num_pages;
+  FastDiv by_n, by_heads, by_page;
 };
 
 // Eight bf16 values of each of two 16-byte units as sixteen e4m3 values.
@@ -57,31 +59,26 @@ __device__ __forceinline__ uint4 to_e4m3(const uint4 &a, const uint4 &b) {
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// kRows rows per warp, whose loads are all in flight before the first store.
-template <int kD, bool kFp8, int kRows>
-__global__ void __launch_bounds__(kWarps * 32) diffpaged_append_kernel(const AppendParams p) {
+// A warp per row.  kEager: the row is loaded while its place is looked up, the shortest chain for a
+// few new tokens; otherwise only once it is known to be no padding, which costs a prompt without
+// padding less (27.2 us for 131072 rows at d = 64, eager 23.6) than eager loads cost one of which
+// half is padding (14.2 us for 65568 rows of e4m3 keys at d = 128, eager 21.4).
+template <int kD, bool kFp8, bool kEager>
+__global__ void __launch_bounds__(kWarps * 32, 8) diffpaged_append_kernel(const AppendParams p) {
   constexpr int kKeyUnits = kFp8 ? kD / 16 : kD / 8;  // 16-byte units stored per key row
   constexpr int kUnits = 2 * kKeyUnits + kD / 4;
   constexpr int kPerLane = (kUnits + 31) / 32;
   const int lane = threadIdx.x % 32;
-  const uint32_t row0 = (blockIdx.x * kWarps + threadIdx.x / 32) * kRows;
-  if (row0 >= p.rows) return;
+  const uint32_t row = blockIdx.x * kWarps + threadIdx.x / 32;
+  if (row >= p.rows) return;
+  const uint32_t bh = p.by_n.div(row), i = row - bh * p.N;
+  const uint32_t b = p.by_heads.div(bh), h = bh - b * p.kv_heads;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int32_t len = __ldg(p.kv_len + b);
 
-  uint32_t bs[kRows], hs[kRows], is[kRows];
-  int32_t at[kRows];
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    const uint32_t row = row0 + r < p.rows ? row0 + r : p.rows - 1;
-    const uint32_t bh = row / p.N;
-    is[r] = row - bh * p.N;
-    bs[r] = bh / p.kv_heads;
-    hs[r] = bh - bs[r] * p.kv_heads;
-    at[r] = __ldg(p.kv_len + bs[r]);
-  }
-  // The rows' data does not depend on the places: load it meanwhile.
-  uint4 x[kRows][kPerLane], y[kRows][kPerLane];
-#pragma unroll
-  for (int r = 0; r < kRows; ++r)
+  uint4 x[kPerLane], y[kPerLane];
+  const auto load = [&] {
 #pragma unroll
     for (int u = 0; u < kPerLane; ++u) {
       const int unit = lane + 32 * u;
@@ -89,64 +86,55 @@ __global__ void __launch_bounds__(kWarps * 32) diffpaged_append_kernel(const App
         const int t = unit < kKeyUnits ? 0 : unit < 2 * kKeyUnits ? 1 : 2;
         const int off = unit - t * kKeyUnits;
         const bool wide = kFp8 && t < 2;  // sixteen bf16 in, sixteen bytes out
-        const uint8_t *s = p.src[t] + bs[r] * p.src_b[t] + hs[r] * p.src_h[t] +
-                           is[r] * p.src_n[t] + off * (wide ? 32 : 16);
-        x[r][u] = __ldg(reinterpret_cast<const uint4 *>(s));
-        if (wide) y[r][u] = __ldg(reinterpret_cast<const uint4 *>(s) + 1);
+        const uint8_t *s = p.src[t] + b * p.src_b[t] + h * p.src_h[t] + i * p.src_n[t] +
+                           off * (wide ? 32 : 16);
+        x[u] = __ldg(reinterpret_cast<const uint4 *>(s));
+        if (wide) y[u] = __ldg(reinterpret_cast<const uint4 *>(s) + 1);
       }
     }
-  int32_t page[kRows];
-  uint32_t slot[kRows];
+  };
+  if (kEager) load();
+  const int32_t t = len - static_cast<int32_t>(p.N) + static_cast<int32_t>(i);
+  if (len < 0 || static_cast<uint32_t>(len) > p.max_pages * p.page_size) {
+    report_bad_page(p.status);
+    return;
+  }
+  if (t < 0) return;
+  const int32_t n = p.by_page.div(t), slot = t - n * static_cast<int32_t>(p.page_size);
+  const int32_t page = __ldg(p.page_table + static_cast<int64_t>(b) * p.max_pages + n);
+  if (!kEager) load();
+  if (static_cast<uint32_t>(page) >= p.num_pages) {
+    report_bad_page(p.status);
+    return;
+  }
+  if (!dbg_ok(slot >= 0 && static_cast<uint32_t>(slot) < p.page_size, p.status, 40)) return;
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    const uint32_t most = p.max_pages * p.page_size;
-    const bool fits = at[r] >= 0 && static_cast<uint32_t>(at[r]) <= most;
-    const int32_t t = at[r] - static_cast<int32_t>(p.N) + static_cast<int32_t>(is[r]);
-    page[r] = -1;
-    slot[r] = 0;
-    if (!fits) report_bad_page(p.status);
-    if (fits && t >= 0 && row0 + r < p.rows) {
-      const uint32_t n = static_cast<uint32_t>(t) / p.page_size;
-      slot[r] = static_cast<uint32_t>(t) - n * p.page_size;
-      page[r] = __ldg(p.page_table + static_cast<int64_t>(bs[r]) * p.max_pages + n);
-      if (static_cast<uint32_t>(page[r]) >= p.num_pages) {
-        page[r] = -1;
-        report_bad_page(p.status);
-      }
+  for (int u = 0; u < kPerLane; ++u) {
+    const int unit = lane + 32 * u;
+    if (unit < kUnits) {
+      const int k = unit < kKeyUnits ? 0 : unit < 2 * kKeyUnits ? 1 : 2;
+      const int off = unit - k * kKeyUnits;
+      uint8_t *d = p.dst[k] + page * p.dst_p[k] + h * p.dst_h[k] + slot * p.dst_n[k] + off * 16;
+      *reinterpret_cast<uint4 *>(d) = (kFp8 && k < 2) ? to_e4m3(x[u], y[u]) : x[u];
     }
   }
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    if (page[r] < 0) continue;
-    if (!dbg_ok(static_cast<uint32_t>(page[r]) < p.num_pages && slot[r] < p.page_size, p.status,
-                40))
-      continue;
-#pragma unroll
-    for (int u = 0; u < kPerLane; ++u) {
-      const int unit = lane + 32 * u;
-      if (unit < kUnits) {
-        const int t = unit < kKeyUnits ? 0 : unit < 2 * kKeyUnits ? 1 : 2;
-        const int off = unit - t * kKeyUnits;
-        uint8_t *d = p.dst[t] + page[r] * p.dst_p[t] + hs[r] * p.dst_h[t] +
-                     static_cast<int64_t>(slot[r]) * p.dst_n[t] + off * 16;
-        *reinterpret_cast<uint4 *>(d) = (kFp8 && t < 2) ? to_e4m3(x[r][u], y[r][u]) : x[r][u];
-      }
-    }
-    if (lane == 0 && p.weights != nullptr)
-      p.weights[(static_cast<int64_t>(page[r]) * p.kv_heads + hs[r]) * p.page_size + slot[r]] = 0.f;
-  }
+  if (lane == 0 && p.weights != nullptr)
+    p.weights[(static_cast<int64_t>(page) * p.kv_heads + h) * p.page_size + slot] = 0.f;
 }
 
 template <int kD, bool kFp8>
 cudaError_t launch(const AppendParams &p, cudaStream_t stream) {
-  // Few rows: one per warp, for the shortest chain.  Many: four, for more loads in flight.
-  const uint32_t per_block = kWarps * (p.rows <= 16384 ? 1 : 4);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.rows + per_block - 1) / per_block);
+  cfg.gridDim = dim3((p.rows + kWarps - 1) / kWarps);
   cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = stream;
-  return p.rows <= 16384 ? cudaLaunchKernelEx(&cfg, diffpaged_append_kernel<kD, kFp8, 1>, p)
-                         : cudaLaunchKernelEx(&cfg, diffpaged_append_kernel<kD, kFp8, 4>, p);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return p.rows <= kFewRows ? cudaLaunchKernelEx(&cfg, diffpaged_append_kernel<kD, kFp8, true>, p)
+                            : cudaLaunchKernelEx(&cfg, diffpaged_append_kernel<kD, kFp8, false>, p);
 }
 
 }  // namespace
@@ -187,6 +175,9 @@ diffattn_status launch_paged_append(const diffattn_desc &desc, const diffpaged_c
   p.page_size = static_cast<uint32_t>(cache.page_size);
   p.max_pages = static_cast<uint32_t>(cache.max_pages);
   p.num_pages = static_cast<uint32_t>(cache.num_pages);
+  p.by_n = fast_div(p.N);
+  p.by_heads = fast_div(p.kv_heads);
+  p.by_page = fast_div(p.page_size);
   const cudaError_t e = desc.d == 64 ? (fp8 ? launch<64, true>(p, stream) : launch<64, false>(p, stream))
                                      : (fp8 ? launch<128, true>(p, stream) : launch<128, false>(p, stream));
   return e == cudaSuccess ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;

@@ -10,14 +10,17 @@
 //      order is theirs (sign flipped or all bits; NaN as +infinity, -0 as 0);
 //      three histogram passes over 11 + 11 + 10 bits find the k-th largest
 //      value T and how many equal to T still fit; a scan in position order
-//      then writes the list of kept positions and moves the weights.
+//      then writes the list of kept places and moves the weights.  A thread
+//      holds up to 16 consecutive weights in registers, so up to 16384 keys
+//      are read once and ordered by one scan; longer sequences take more
+//      rounds over a copy.
 //   2. Move (one block per item and 128-byte column slice of k1, k2, v).  A
 //      kept row's place is at or before its source, and sources ascend, so
 //      blocks of rows taken in order only need all loads of a block before
-//      its stores; the slices are independent of one another.
+//      its stores; the slices are independent of one another.  The next
+//      rows' places are fetched while a block of rows is on its way.
 //
-// Bound: HBM, each kept row read and written once; the selection reads the
-// weights once and then works in the cache.
+// Bound: HBM, each kept row read and written once.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -31,7 +34,9 @@ namespace {
 
 constexpr int kSelectThreads = 1024;
 constexpr int kMoveThreads = 256;
-constexpr int kBatch = 8;  // 16-byte units a thread has in flight
+constexpr int kBatch = 4;   // 16-byte units of a thread in a block of rows
+constexpr int kAhead = 3;   // blocks of rows in flight
+constexpr int kHeld = 16;   // weights that a thread of the selection holds
 
 struct EvictParams {
   uint8_t *pool[3];
@@ -43,9 +48,10 @@ struct EvictParams {
   int32_t *status;
   int32_t B, kv_heads, num_pages, max_pages, page_size;
   int32_t keep, recent;
+  FastDiv by_page;
   int64_t padded;   // entries per item of copy
-  float *copy;      // [items][padded] the item's weights, by position
-  int32_t *list;    // [items][keep] source position of each kept row
+  float *copy;      // [items][padded] the item's weights by position, where they take rounds
+  int2 *list;       // [items][keep] page and slot of each kept row
   int2 *plan;       // [items] {rows already in place, 1}; {0, 0}: nothing to do
 };
 
@@ -82,14 +88,20 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *scratch, ui
   return before + incl - x;
 }
 
+__device__ __forceinline__ bool in_order(uint32_t key, uint32_t prefix, int shift) {
+  return shift >= 32 || key >> shift == prefix >> shift;
+}
+
 __global__ void __launch_bounds__(kSelectThreads) diffpaged_select_kernel(const EvictParams p) {
   __shared__ uint32_t hist[2048];
   __shared__ uint32_t scratch[32];
   __shared__ uint32_t found[2];
-  grid_dependents_launch();
   const int item = blockIdx.x, tid = threadIdx.x;
   const int b = item / p.kv_heads, hk = item % p.kv_heads;
-  const int32_t len = p.kv_len[b];
+  for (int i = tid; i < 2048; i += kSelectThreads) hist[i] = 0;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int32_t len = __ldg(p.kv_len + b);
   const bool bad_len = len < 0 || len > p.max_pages * p.page_size;
   if (bad_len || len <= p.keep) {
     if (tid == 0) {
@@ -99,49 +111,78 @@ __global__ void __launch_bounds__(kSelectThreads) diffpaged_select_kernel(const 
     return;
   }
   const int32_t *table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-  bool bad = false;
-  for (int k = tid; k * p.page_size < len; k += kSelectThreads)
-    bad |= static_cast<uint32_t>(table[k]) >= static_cast<uint32_t>(p.num_pages);
-  if (__syncthreads_or(bad)) {
-    if (tid == 0) {
-      report_bad_page(p.status);
-      p.plan[item] = make_int2(0, 0);
-    }
-    return;
-  }
   const int32_t old = len - p.recent;
   const uint32_t k_keep = p.keep - p.recent;
   float *copy = p.copy + item * p.padded;
-  const auto weight_at = [&](int32_t j) -> float * {
-    return p.weights + (static_cast<int64_t>(table[j / p.page_size]) * p.kv_heads + hk) * p.page_size +
-           j % p.page_size;
+  const auto weights_of = [&](int32_t page) {
+    return p.weights + (static_cast<int64_t>(page) * p.kv_heads + hk) * p.page_size;
+  };
+
+  // Rounds of 1024 threads x `each` consecutive positions, in groups of four (which no page
+  // boundary cuts); one round up to 16384 positions.
+  const int32_t each = min(kHeld, ((len + kSelectThreads - 1) / kSelectThreads + 3) & ~3);
+  const int32_t per_round = each * kSelectThreads;
+  const bool single = len <= per_round;
+  float w[kHeld];
+  bool bad = false;
+  const auto load = [&](int32_t at, bool first) {  // this thread's weights of the round at `at`
+    const int32_t j0 = at + tid * each;
+#pragma unroll
+    for (int g = 0; g < kHeld; g += 4) {
+      if (g >= each || j0 + g >= len) break;
+      const float *src = copy + j0 + g;
+      if (first) {
+        const int32_t n = p.by_page.div(j0 + g);
+        const int32_t page = __ldg(table + n);
+        bad |= static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages);
+        if (bad) break;
+        src = weights_of(page) + (j0 + g - n * p.page_size);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j0 + g + e < len) w[g + e] = src[e];
+    }
   };
 
   // The k-th largest key, from its leading bits down.
   uint32_t prefix = 0, need = k_keep;  // need: how many are still to be found at or below prefix
   const int shift[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
-#pragma unroll
+#pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
-    for (int i = tid; i < 2048; i += kSelectThreads) hist[i] = 0;
-    __syncthreads();
-    const uint32_t high = pass == 0 ? 0 : prefix >> (shift[pass] + bits[pass]);
-    for (int32_t j = tid; j < (pass == 0 ? len : old); j += kSelectThreads) {
-      float w;
-      if (pass == 0)
-        copy[j] = w = *weight_at(j);
-      else
-        w = copy[j];
-      const uint32_t key = order_key(w);
-      if (j < old && (pass == 0 || key >> (shift[pass] + bits[pass]) == high))
-        atomicAdd(&hist[(key >> shift[pass]) & ((1u << bits[pass]) - 1)], 1u);
+    for (int32_t at = 0; at < len; at += per_round) {
+      if (pass == 0 || !single) load(at, pass == 0);
+      const int32_t j0 = at + tid * each;
+#pragma unroll
+      for (int g = 0; g < kHeld; ++g) {
+        if (g >= each) break;
+        const int32_t j = j0 + g;
+        if (pass == 0 && !single && j < len) copy[j] = w[g];
+        const uint32_t key = order_key(w[g]);
+        const bool counts = j < old && in_order(key, prefix, shift[pass] + bits[pass]);
+        const uint32_t bin = counts ? (key >> shift[pass]) & ((1u << bits[pass]) - 1) : 0xFFFFFFFFu;
+        // Equal weights fill one bin: a warp that agrees adds once.
+        int same;
+        __match_all_sync(0xffffffffu, bin, &same);
+        if (same) {
+          if (counts && tid % 32 == 0) atomicAdd(&hist[bin], 32u);
+        } else if (counts) {
+          atomicAdd(&hist[bin], 1u);
+        }
+      }
     }
-    __syncthreads();
+    if (__syncthreads_or(bad)) {  // a page of the sequence is not one: it stays as it is
+      if (tid == 0) {
+        report_bad_page(p.status);
+        p.plan[item] = make_int2(0, 0);
+      }
+      return;
+    }
     // Thread t holds bins 2047 - 2 t and 2046 - 2 t: sums from the largest bin down.
     const uint32_t hi = hist[2047 - 2 * tid], lo = hist[2046 - 2 * tid];
+    hist[2047 - 2 * tid] = hist[2046 - 2 * tid] = 0;
+    if (tid == 0) found[0] = found[1] = 0;
     uint32_t total;
     const uint32_t above = block_scan(hi + lo, scratch, &total);
-    if (tid == 0) found[0] = found[1] = 0;
-    __syncthreads();
     if (need > above && need <= above + hi + lo) {
       const bool in_hi = need <= above + hi;
       found[0] = in_hi ? 2047 - 2 * tid : 2046 - 2 * tid;
@@ -150,74 +191,125 @@ __global__ void __launch_bounds__(kSelectThreads) diffpaged_select_kernel(const 
     __syncthreads();
     prefix |= found[0] << shift[pass];
     need = found[1];
-    __syncthreads();
   }
 
-  // Kept positions in order: keys above T, and the first `need` equal to it.
+  // Kept places in order: keys above T, the first `need` equal to it, and the last `recent`.
   uint32_t equal_before = 0, kept = 0;
-  int32_t *list = p.list + static_cast<int64_t>(item) * p.keep;
-  uint32_t in_place = 0;  // leading positions that all stay
-  for (int32_t j0 = 0; j0 < old; j0 += kSelectThreads) {
-    const int32_t j = j0 + tid;
-    const float w = j < old ? copy[j] : 0.f;
-    const uint32_t key = j < old ? order_key(w) : 0;
-    const bool equal = k_keep > 0 && j < old && key == prefix;
-    uint32_t total, all_equal;
-    const uint32_t eq = block_scan(equal, scratch, &all_equal);
-    const bool stays = k_keep > 0 && j < old && (key > prefix || (equal && equal_before + eq < need));
-    const uint32_t at = kept + block_scan(stays, scratch, &total);
-    if (stays && dbg_ok(at < k_keep, p.status, 50)) {
-      list[at] = j;
-      *weight_at(static_cast<int32_t>(at)) = w;
+  int2 *list = p.list + static_cast<int64_t>(item) * p.keep;
+  uint32_t in_place = 0xFFFFFFFFu;  // the first position that does not stay
+  for (int32_t at = 0; at < len; at += per_round) {
+    if (!single) load(at, false);
+    const int32_t j0 = at + tid * each;
+    uint32_t equal = 0, all_equal = 0;
+#pragma unroll
+    for (int g = 0; g < kHeld; ++g)
+      if (g < each && j0 + g < old) equal += order_key(w[g]) == prefix ? 1 : 0;
+    uint32_t eq = equal_before + block_scan(equal, scratch, &all_equal);
+    uint32_t mask = 0;
+#pragma unroll
+    for (int g = 0; g < kHeld; ++g) {
+      const int32_t j = j0 + g;
+      if (g >= each || j >= len) break;
+      const uint32_t key = order_key(w[g]);
+      const bool is_equal = key == prefix;
+      const bool stays = j >= old || (k_keep > 0 && (key > prefix || (is_equal && eq < need)));
+      if (j < old && is_equal) ++eq;
+      if (stays)
+        mask |= 1u << g;
+      else
+        in_place = min(in_place, static_cast<uint32_t>(j));
     }
-    if (in_place == static_cast<uint32_t>(j0) && total == static_cast<uint32_t>(kSelectThreads))
-      in_place = j0 + kSelectThreads;
+    uint32_t total;
+    uint32_t to = kept + block_scan(__popc(mask), scratch, &total);
+    // Every weight of this round has been read (and, in more rounds, of all: from the copy).
+#pragma unroll
+    for (int g = 0; g < kHeld; ++g) {
+      if (!((mask >> g) & 1) || !dbg_ok(to < static_cast<uint32_t>(p.keep), p.status, 50)) continue;
+      const int32_t n = p.by_page.div(j0 + g), m = p.by_page.div(static_cast<int32_t>(to));
+      list[to] = make_int2(__ldg(table + n), j0 + g - n * p.page_size);
+      weights_of(__ldg(table + m))[to - m * p.page_size] = w[g];
+      ++to;
+    }
     equal_before += all_equal;
     kept += total;
   }
-  for (int32_t j = old + tid; j < len; j += kSelectThreads) {
-    const int32_t at = static_cast<int32_t>(k_keep) + j - old;
-    list[at] = j;
-    *weight_at(at) = copy[j];
+  in_place = __reduce_min_sync(0xffffffffu, in_place);
+  if (tid % 32 == 0) scratch[tid / 32] = in_place;
+  __syncthreads();
+  if (tid < 32) {
+    in_place = __reduce_min_sync(0xffffffffu, scratch[tid]);
+    if (tid == 0) p.plan[item] = make_int2(min(static_cast<int32_t>(in_place), p.keep), 1);
   }
-  if (tid == 0) p.plan[item] = make_int2(static_cast<int32_t>(in_place), 1);
 }
 
 __global__ void __launch_bounds__(kMoveThreads) diffpaged_move_kernel(const EvictParams p,
                                                                       int slices) {
-  grid_dependency_wait();
   const int item = blockIdx.x / slices;
-  int slice = blockIdx.x % slices;
-  const int b = item / p.kv_heads, hk = item % p.kv_heads;
-  const int2 plan = p.plan[item];
-  if (plan.y == 0) return;
-  if (slice == 0 && hk == 0 && threadIdx.x == 0) p.kv_len[b] = p.keep;
+  int slice = blockIdx.x - item * slices;
+  const int b = item / p.kv_heads, hk = item - b * p.kv_heads;
   int t = 0;
   while (slice >= (p.width_b[t] + 127) / 128) slice -= (p.width_b[t++] + 127) / 128;
   const int units = p.width_b[t] < 128 ? p.width_b[t] / 16 : 8;  // 16-byte units of the slice
-  const int unit = threadIdx.x % units, line = threadIdx.x / units;
+  const int unit = threadIdx.x & (units - 1), line = threadIdx.x / units;
   const int lines = kMoveThreads / units;  // rows taken side by side
   uint8_t *base = p.pool[t] + hk * p.head_b[t] + slice * 128 + unit * 16;
+  const int64_t page_b = p.page_b[t], row_b = p.row_b[t];
   const int32_t *table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-  const int32_t *list = p.list + static_cast<int64_t>(item) * p.keep;
-  const auto row_at = [&](int32_t j) {
-    return reinterpret_cast<uint4 *>(base + table[j / p.page_size] * p.page_b[t] +
-                                     j % p.page_size * p.row_b[t]);
+  const int2 *list = p.list + static_cast<int64_t>(item) * p.keep;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int2 plan = p.plan[item];
+  if (plan.y == 0) return;
+  if (blockIdx.x == b * p.kv_heads * slices && threadIdx.x == 0) p.kv_len[b] = p.keep;
+  // A ring of row blocks in shared memory.  A thread stores what it loaded itself; the barrier
+  // makes every source of a block be read before any of its places is written, and the sources of
+  // the blocks after lie behind those places.
+  __shared__ uint4 ring[kAhead][kBatch][kMoveThreads];
+  int2 from[kBatch];  // places of the next block's rows
+  const auto look_up = [&](int32_t first) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int32_t at = first + u * lines + line;
+      if (at < p.keep) from[u] = list[at];
+    }
   };
-  for (int32_t first = plan.x; first < p.keep; first += lines * kBatch) {
-    uint4 x[kBatch];
+  const auto fetch = [&](int32_t first, int stage) {
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int32_t at = first + u * lines + line;
-      if (at < p.keep) x[u] = *row_at(list[at]);
-    }
-    __syncthreads();  // every source of these rows is read before any of their places is written
+    for (int u = 0; u < kBatch; ++u)
+      if (first + u * lines + line < p.keep)
+        cp_async16(smem_u32(&ring[stage][u][threadIdx.x]),
+                   base + from[u].x * page_b + from[u].y * row_b);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  const int32_t step = lines * kBatch;
+  int32_t ahead = plan.x;
+  look_up(ahead);
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int32_t at = first + u * lines + line;
-      if (at < p.keep) *row_at(at) = x[u];
-    }
+  for (int k = 0; k < kAhead - 1; ++k) {
+    fetch(ahead, k);
+    ahead += step;
+    look_up(ahead);
   }
+  int stage = 0;
+#pragma unroll 1
+  for (int32_t first = plan.x; first < p.keep; first += step) {
+    fetch(ahead, (stage + kAhead - 1) % kAhead);
+    ahead += step;
+    look_up(ahead);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int32_t at = first + u * lines + line;
+      if (at < p.keep) {
+        const int32_t n = p.by_page.div(at);
+        *reinterpret_cast<uint4 *>(base + __ldg(table + n) * page_b +
+                                   (at - n * p.page_size) * row_b) = ring[stage][u][threadIdx.x];
+      }
+    }
+    stage = (stage + 1) % kAhead;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
@@ -234,8 +326,9 @@ EvictLayout layout(const diffattn_desc &desc, const diffpaged_cache &cache, int6
   l.padded = most;
   const int64_t kept = keep < most ? keep : most;
   l.copy = 0;
-  l.list = round256(static_cast<size_t>(items * most) * sizeof(float));
-  l.plan = l.list + round256(static_cast<size_t>(items * kept) * sizeof(int32_t));
+  const int64_t copied = most > kHeld * kSelectThreads ? most : 0;
+  l.list = round256(static_cast<size_t>(items * copied) * sizeof(float));
+  l.plan = l.list + round256(static_cast<size_t>(items * kept) * sizeof(int2));
   l.bytes = l.plan + round256(static_cast<size_t>(items) * sizeof(int2));
   return l;
 }
@@ -278,25 +371,26 @@ diffattn_status launch_paged_evict(const diffattn_desc &desc, const diffpaged_ca
   p.page_size = cache.page_size;
   p.keep = static_cast<int32_t>(keep);
   p.recent = static_cast<int32_t>(recent);
+  p.by_page = fast_div(static_cast<uint32_t>(p.page_size));
   p.padded = l.padded;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   p.copy = reinterpret_cast<float *>(ws + l.copy);
-  p.list = reinterpret_cast<int32_t *>(ws + l.list);
+  p.list = reinterpret_cast<int2 *>(ws + l.list);
   p.plan = reinterpret_cast<int2 *>(ws + l.plan);
   const double items = static_cast<double>(desc.B) * static_cast<double>(cache.kv_heads);
   if (items * slices > INT32_MAX) return DIFFATTN_ERR_UNSUPPORTED;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(items));
   cfg.blockDim = dim3(kSelectThreads);
   cfg.stream = stream;
-  if (cudaLaunchKernelEx(&cfg, diffpaged_select_kernel, p) != cudaSuccess) return DIFFATTN_ERR_CUDA;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(items) * slices);
-  cfg.blockDim = dim3(kMoveThreads);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, diffpaged_select_kernel, p) != cudaSuccess) return DIFFATTN_ERR_CUDA;
+  cfg.gridDim = dim3(static_cast<unsigned>(items) * slices);
+  cfg.blockDim = dim3(kMoveThreads);
   return cudaLaunchKernelEx(&cfg, diffpaged_move_kernel, p, slices) == cudaSuccess
              ? DIFFATTN_OK
              : DIFFATTN_ERR_CUDA;

@@ -71,22 +71,6 @@ struct TileDesc {
   int32_t steps, pad[3];  // 16-key steps of the second product (one for an idle sequence)
 };
 
-// Exact division of 0 <= n < 2^31 by a launch constant: a multiply and a shift.
-struct FastDiv {
-  uint32_t mul, shift, d;
-  __device__ __forceinline__ int32_t div(int32_t n) const {
-    return static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> shift);
-  }
-  __device__ __forceinline__ int32_t mod(int32_t n) const {
-    return n - div(n) * static_cast<int32_t>(d);
-  }
-};
-FastDiv fast_div(uint32_t d) {  // 2^(s - 1) < d <= 2^s, mul = ceil(2^(31 + s) / d)
-  uint32_t s = 0;
-  while ((uint64_t{1} << s) < d) ++s;
-  return {static_cast<uint32_t>(((uint64_t{1} << (31 + s)) + d - 1) / d), 31 + s, d};
-}
-
 struct FwdParams {
   const void *q1, *q2;
   const void *v_pages;
@@ -196,10 +180,6 @@ __device__ __forceinline__ float warp_max(float x) {
   return x;
 }
 
-// Sixteen bytes from global to shared memory, asynchronously.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 // One arrival on the barrier when this thread's cp.async copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
