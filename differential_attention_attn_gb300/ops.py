@@ -9,7 +9,6 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import functools
 import os
 import re
 import threading
@@ -689,13 +688,29 @@ class PagedCache:
         self.page_table, self.kv_len, self.weights = page_table, kv_len, weights
         self.B, self.kv_heads, self.d, self.page_size = B, heads, d, page
         self.device, self.dtype = k1.device, k1.dtype
+        self.index = k1.get_device()
         self.code = E4M3_QK if k1.dtype == torch.float8_e4m3fn else BF16
+        self._descs = {}
         self._struct = PagedCacheStruct(
             k1.data_ptr(), k2.data_ptr(), v.data_ptr(),
             0 if weights is None else weights.data_ptr(), page_table.data_ptr(),
             kv_len.data_ptr(), *(_strides4(t) for t in (k1, k2, v)), pages, heads, max_pages,
             page, 0)
         self._ref = ctypes.byref(self._struct)
+
+    def _desc(self, H, N, causal, headnorm, eps, lambda_init, status):
+        """The descriptor of a call; without a status word made once per set of values."""
+        if status is not None:
+            return ctypes.byref(make_desc(self.B, H, N, self.d, self.code, causal, headnorm, eps,
+                                          lambda_init, status))
+        key = (H, N, causal, headnorm, eps, lambda_init)
+        ref = self._descs.get(key)
+        if ref is None:
+            if len(self._descs) >= 256:
+                self._descs.clear()
+            ref = self._descs[key] = ctypes.byref(
+                make_desc(self.B, H, N, self.d, self.code, causal, headnorm, eps, lambda_init))
+        return ref
 
 
 def _strides4(t):
@@ -711,31 +726,21 @@ def _strides_or_null(a, b, c):
     """The strides argument of a paged call: NULL when all three tensors are contiguous."""
     if a.is_contiguous() and b.is_contiguous() and c.is_contiguous():
         return None
+    if a.stride(3) != 1 or b.stride(3) != 1 or c.stride(3) != 1:
+        raise ValueError("rows must be contiguous (last stride 1)")
     return (Strides * 3)(_strides4(a), _strides4(b), _strides4(c))
 
 
-@functools.lru_cache(maxsize=1024)
-def _paged_desc(B, H, N, d, code, causal, headnorm, eps, lambda_init):
-    """A descriptor without a status word, made once per set of values and only read."""
-    return make_desc(B, H, N, d, code, causal, headnorm, eps, lambda_init)
-
-
-def _paged_call_desc(B, H, N, d, code, causal, headnorm, eps, lambda_init, status):
-    if status is None:
-        return ctypes.byref(_paged_desc(B, H, N, d, code, causal, headnorm, eps, lambda_init))
-    return ctypes.byref(make_desc(B, H, N, d, code, causal, headnorm, eps, lambda_init, status))
-
-
-def _on_device(dev, stream):
-    """The handle of a call's stream, for tensors of device `dev`; refuses one of another device,
-    and the current device being another (its context would run the kernels)."""
+def _stream_on(cache, stream):
+    """The handle of a call's stream; refuses one of another device than the cache's, and the
+    current device being another (its context would run the kernels)."""
     index = torch.cuda.current_device()
-    if dev.index != index:
-        raise ValueError(f"the cache is on cuda:{dev.index}, the current device is cuda:{index}")
+    if cache.index != index:
+        raise ValueError(f"the cache is on cuda:{cache.index}, the current device is cuda:{index}")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(index)
-    if stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the cache on {dev}")
+    if stream.device != cache.device:
+        raise ValueError(f"the stream is on {stream.device}, the cache on {cache.device}")
     return stream.cuda_stream
 
 
@@ -747,15 +752,15 @@ def _new_on(stream, shape, dtype, dev):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _workspace(workspace, need, dev, stream):
+def _workspace(workspace, need, cache, stream):
     """(pointer, bytes, buffer to keep) of a call's workspace: the caller's, or one of its own."""
     if workspace is None:
         if not need:
             return None, 0, None
-        workspace = _new_on(stream, need, torch.uint8, dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
+        workspace = _new_on(stream, need, torch.uint8, cache.device)
+    elif workspace.get_device() != cache.index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    return workspace.data_ptr(), workspace.nbytes, workspace
 
 
 def paged_append(cache, k1, k2, v, *, status=None, stream=None, raw_status: bool = False):
@@ -765,22 +770,21 @@ def paged_append(cache, k1, k2, v, *, status=None, stream=None, raw_status: bool
     k1, k2: bf16 [B, kv_heads, N, d] (rounded to e4m3 where the cache holds that); v: bf16
     [B, kv_heads, N, 2d]; views of any layout with contiguous rows.
     """
-    if k1.dim() != 4:
-        raise ValueError("k1 must be [B, kv_heads, N, d]")
-    B, H, N, d = cache.B, cache.kv_heads, k1.shape[2], cache.d
-    dev, dtype = cache.device, torch.bfloat16
-    if k1.shape != (B, H, N, d) or k2.shape != k1.shape or v.shape != (B, H, N, 2 * d):
-        raise ValueError(f"k1 and k2 must be {(B, H, N, d)}, v {(B, H, N, 2 * d)}")
+    shape = k1.shape
+    B, H, d = cache.B, cache.kv_heads, cache.d
+    if len(shape) != 4 or shape[0] != B or shape[1] != H or shape[3] != d or \
+            k2.shape != shape or v.shape != (B, H, shape[2], 2 * d):
+        raise ValueError(f"k1 and k2 must be [{B}, {H}, N, {d}], v [{B}, {H}, N, {2 * d}]")
+    dtype, index = torch.bfloat16, cache.index
     if k1.dtype != dtype or k2.dtype != dtype or v.dtype != dtype:
         raise ValueError("k1, k2 and v must be bfloat16")
-    if k1.device != dev or k2.device != dev or v.device != dev:
+    if k1.get_device() != index or k2.get_device() != index or v.get_device() != index:
         raise ValueError("all tensors must be on the cache's device")
-    if k1.stride(3) != 1 or k2.stride(3) != 1 or v.stride(3) != 1:
-        raise ValueError("rows must be contiguous (last stride 1)")
-    handle = _on_device(dev, stream)
-    st = load().diffpaged_append(
-        _paged_call_desc(B, H, N, d, cache.code, True, 0, 0.0, 0.0, status), cache._ref,
-        k1.data_ptr(), k2.data_ptr(), v.data_ptr(), _strides_or_null(k1, k2, v), handle)
+    strides = _strides_or_null(k1, k2, v)
+    handle = _stream_on(cache, stream)
+    st = (_lib or load()).diffpaged_append(
+        cache._desc(H, shape[2], True, 0, 0.0, 0.0, status), cache._ref, k1.data_ptr(),
+        k2.data_ptr(), v.data_ptr(), strides, handle)
     if raw_status:
         return st
     _check(st)
@@ -810,31 +814,28 @@ def paged_fwd(cache, q1, q2, lam, *, causal: bool = True, headnorm: int = 1, nor
     workspace: a CUDA tensor of at least paged_fwd_plan bytes (a torch buffer when None).
     Returns bf16 out [B, H, N, 2d] (of `stream`'s memory when allocated here).
     """
-    if q1.dim() != 4:
-        raise ValueError("q1 must be [B, H, N, d]")
-    B, H, N, d = q1.shape
-    dev = cache.device
-    if B != cache.B or d != cache.d or q2.shape != q1.shape:
-        raise ValueError(f"q1 and q2 must be [{cache.B}, H, N, {cache.d}]")
+    shape, d, index, f32 = q1.shape, cache.d, cache.index, torch.float32
+    if len(shape) != 4 or shape[0] != cache.B or shape[3] != d or q2.shape != shape:
+        raise ValueError(f"q1 and q2 must be [{cache.B}, H, N, {d}]")
+    H, N = shape[1], shape[2]
     if q1.dtype != cache.dtype or q2.dtype != cache.dtype:
         raise ValueError(f"q1 and q2 must be {cache.dtype}, as the cache's keys")
-    if q1.stride(3) != 1 or q2.stride(3) != 1:
-        raise ValueError("rows must be contiguous (last stride 1)")
-    if lam.dtype != torch.float32 or lam.numel() != H or not lam.is_contiguous():
-        raise ValueError("lam must be contiguous float32 [H]")
-    if norm_w is not None and (norm_w.dtype != torch.float32 or norm_w.numel() != H * 2 * d or
-                               not norm_w.is_contiguous() or norm_w.device != dev):
-        raise ValueError("norm_w must be contiguous float32 [H, 2d]")
-    if q1.device != dev or q2.device != dev or lam.device != dev:
+    if q1.get_device() != index or q2.get_device() != index or lam.get_device() != index:
         raise ValueError("all tensors must be on the cache's device")
-    handle = _on_device(dev, stream)
+    if lam.dtype != f32 or lam.numel() != H or not lam.is_contiguous():
+        raise ValueError("lam must be contiguous float32 [H]")
+    if norm_w is not None and (norm_w.dtype != f32 or norm_w.numel() != H * 2 * d or
+                               not norm_w.is_contiguous() or norm_w.get_device() != index):
+        raise ValueError("norm_w must be contiguous float32 [H, 2d] on the cache's device")
+    handle = _stream_on(cache, stream)
     if out is None:
-        out = _new_on(stream, (B, H, N, 2 * d), torch.bfloat16, dev)
-    elif out.shape != (B, H, N, 2 * d) or out.dtype != torch.bfloat16 or out.device != dev or \
-            out.stride(3) != 1:
-        raise ValueError("out must be bfloat16 [B, H, N, 2d] with contiguous rows")
-    ref = _paged_call_desc(B, H, N, d, cache.code, causal, headnorm, eps, lambda_init, status)
-    lib, need = load(), 0
+        out = _new_on(stream, (shape[0], H, N, 2 * d), torch.bfloat16, cache.device)
+    elif out.shape != (shape[0], H, N, 2 * d) or out.dtype != torch.bfloat16 or \
+            out.get_device() != index:
+        raise ValueError("out must be bfloat16 [B, H, N, 2d] on the cache's device")
+    strides = _strides_or_null(q1, q2, out)
+    ref = cache._desc(H, N, causal, headnorm, eps, lambda_init, status)
+    lib, need = _lib or load(), 0
     if workspace is None:
         n = ctypes.c_size_t(0)
         st = lib.diffpaged_fwd_plan(ref, cache._ref, int(accumulate), ctypes.byref(n))
@@ -843,10 +844,10 @@ def paged_fwd(cache, q1, q2, lam, *, causal: bool = True, headnorm: int = 1, nor
                 return st
             _check(st)
         need = n.value
-    ws, ws_bytes, _keep = _workspace(workspace, need, dev, stream)
+    ws, ws_bytes, _keep = _workspace(workspace, need, cache, stream)
     st = lib.diffpaged_fwd(ref, cache._ref, q1.data_ptr(), q2.data_ptr(), lam.data_ptr(),
                            None if norm_w is None else norm_w.data_ptr(), out.data_ptr(),
-                           _strides_or_null(q1, q2, out), int(accumulate), ws, ws_bytes, handle)
+                           strides, int(accumulate), ws, ws_bytes, handle)
     if raw_status:
         return st
     _check(st)
@@ -868,17 +869,16 @@ def paged_evict(cache, *, keep: int, recent: int = 0, workspace=None, status=Non
                 raw_status: bool = False):
     """`diffpaged_evict`: cut every sequence longer than `keep` to its last `recent` keys and
     the keep - recent of the largest weights, in place; updates cache.kv_len."""
-    handle, need = _on_device(cache.device, stream), 0
+    handle, need = _stream_on(cache, stream), 0
     if workspace is None:
         st, need = paged_evict_plan(cache, keep=keep, raw_status=True)
         if st != OK:
             if raw_status:
                 return st
             _check(st)
-    ws, ws_bytes, _keep = _workspace(workspace, need, cache.device, stream)
-    ref = _paged_call_desc(cache.B, cache.kv_heads, 0, cache.d, cache.code, True, 0, 0.0, 0.0,
-                           status)
-    st = load().diffpaged_evict(ref, cache._ref, int(keep), int(recent), ws, ws_bytes, handle)
+    ws, ws_bytes, _keep = _workspace(workspace, need, cache, stream)
+    ref = cache._desc(cache.kv_heads, 0, True, 0, 0.0, 0.0, status)
+    st = (_lib or load()).diffpaged_evict(ref, cache._ref, int(keep), int(recent), ws, ws_bytes, handle)
     if raw_status:
         return st
     _check(st)
