@@ -61,6 +61,7 @@ constexpr int kMaxBad = 16;     // new tokens of a call, so more than keys that 
 constexpr int kRing = 8;        // tile descriptors; fewer tiles are between load and epilogue
 constexpr int kBoxBytes = kTile * 128;   // 64 bf16 columns of a tile
 constexpr int kSlotBytes = 2 * kBoxBytes;
+constexpr int kItemCost = 2;    // steps, see Shares
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum : int32_t { kFirst = 1, kLast = 2, kStop = 4, kBad = 8, kDirect = 16 };
@@ -268,24 +269,35 @@ __device__ __forceinline__ uint32_t phase(uint32_t n) {
   return (n / kBufs) & 1;
 }
 
-// All items' tiles in order, cut into `ctas` shares of `each` or (the first `more`) each + 1.
-// Fewer than 2^31 tiles (checked at launch).
+// Work is laid out on a line: kItemCost steps that hold nothing for each item, then its tiles, a
+// step each.  (A segment costs its CTA about as much as two tiles beside its tiles: a CTA with ten
+// short items took 91 us where the others took 65.)  `ctas` shares cut the line into `each` or (the
+// first `more`) each + 1 steps.  Fewer than 2^31 steps (checked at launch).
 struct Shares {
   uint32_t ctas, each, more;
   __device__ __forceinline__ uint32_t begin(uint32_t cta) const {
     return cta * each + min(cta, more);
   }
-  __device__ __forceinline__ uint32_t cta_of(uint32_t tile) const {
+  __device__ __forceinline__ uint32_t cta_of(uint32_t step) const {
     const uint32_t border = more * (each + 1);
-    return tile < border ? tile / (each + 1) : more + (tile - border) / each;
+    return step < border ? step / (each + 1) : more + (step - border) / each;
   }
 };
+__device__ __forceinline__ Shares cut_line(uint32_t steps, uint32_t ctas) {
+  Shares s;
+  s.ctas = min(ctas, steps);
+  s.each = steps / s.ctas;
+  s.more = steps - s.each * s.ctas;
+  return s;
+}
 
-// The CTA's share: its first item (b, hk, rb) and tile within it.
+// The CTA's share: the item (b, hk, rb) that it begins in, the steps from that item's first one to
+// the share's begin and end, and the item's tiles.
 struct Share {
   Shares all;
-  uint32_t begin, todo;
-  int32_t b, hk, rb, tile, len, units;
+  uint32_t begin;     // of the share
+  int32_t off, end;   // from the item's first step; end = off: nothing
+  int32_t b, hk, rb, len, units;
 };
 
 // CTA `cta`'s share of `ctas` CTAs (one warp, uniform).
@@ -300,7 +312,8 @@ __device__ __forceinline__ Share find_share(const FwdParams &p, uint32_t cta, ui
     s.hk = item / p.row_blocks;
     s.rb = item - s.hk * p.row_blocks;
     s.len = __ldg(p.kv_len + s.b);
-    s.todo = s.units = units_of(s.len, most);
+    s.units = units_of(s.len, most);
+    s.end = kItemCost + s.units;
     return s;
   }
   uint32_t total = 0;
@@ -315,23 +328,18 @@ __device__ __forceinline__ Share find_share(const FwdParams &p, uint32_t cta, ui
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (b0 + 32 * k + lane < p.B) u += units_of(last[k], most);
+      if (b0 + 32 * k + lane < p.B) u += kItemCost + units_of(last[k], most);
     total += __reduce_add_sync(0xffffffffu, u);
   }
-  total *= heads;
-  // Every share has at least one tile (the last CTAs may have none).
-  s.all.ctas = min(ctas, total);
-  s.all.each = total / s.all.ctas;
-  s.all.more = total - s.all.each * s.all.ctas;
+  s.all = cut_line(total * heads, ctas);
   if (cta < s.all.ctas) {
     s.begin = s.all.begin(cta);
-    s.todo = s.all.each + (cta < s.all.more ? 1 : 0);
-    uint32_t left = s.begin;  // tiles before the share, counted down sequence by sequence
+    uint32_t left = s.begin;  // steps before the share, counted down sequence by sequence
 #pragma unroll 1
     for (int32_t b0 = 0; b0 < p.B; b0 += 32) {
       const int32_t x = b0 + lane;
       const int32_t len = p.B <= 32 ? last[0] : x < p.B ? __ldg(p.kv_len + x) : 0;
-      const uint32_t u = x < p.B ? units_of(len, most) * heads : 0;
+      const uint32_t u = x < p.B ? (kItemCost + units_of(len, most)) * heads : 0;
       uint32_t incl = u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -349,17 +357,18 @@ __device__ __forceinline__ Share find_share(const FwdParams &p, uint32_t cta, ui
       left -= all;
     }
     s.units = units_of(s.len, most);
-    const uint32_t item = left / s.units;
-    s.tile = static_cast<int32_t>(left - item * s.units);
+    const uint32_t item = left / (kItemCost + s.units);
+    s.off = static_cast<int32_t>(left - item * (kItemCost + s.units));
+    s.end = s.off + static_cast<int32_t>(s.all.each + (cta < s.all.more ? 1 : 0));
     s.hk = item / p.row_blocks;
     s.rb = item - s.hk * p.row_blocks;
   }
   return s;
 }
 
-// The parts that an item's tiles start .. start + units - 1 are cut into: CTA c0's is in slot
-// 2 c0 + 1 where its share begins before the item and in 2 c0 otherwise, the next ones' in
-// 2 (c0 + 1), 2 (c0 + 2) ..
+// The parts that the item whose steps begin at `start` is cut into: that of the CTA c0 with its
+// first tile is in slot 2 c0 + 1 where its share begins before the item and in 2 c0 otherwise, the
+// next ones' in 2 (c0 + 1), 2 (c0 + 2) ..
 struct Parts {
   int32_t first, n;
   __device__ __forceinline__ int32_t slot(int32_t k) const {
@@ -367,9 +376,9 @@ struct Parts {
   }
 };
 __device__ __forceinline__ Parts parts_of(const Shares &all, uint32_t start, uint32_t units) {
-  const uint32_t c0 = all.cta_of(start);
+  const uint32_t c0 = all.cta_of(start + kItemCost);
   return {static_cast<int32_t>(2 * c0 + (all.begin(c0) < start ? 1 : 0)),
-          static_cast<int32_t>(all.cta_of(start + units - 1) - c0 + 1)};
+          static_cast<int32_t>(all.cta_of(start + kItemCost + units - 1) - c0 + 1)};
 }
 
 // ---------------------------------------------------------------------------
@@ -385,8 +394,9 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
   using L = Layout<kD, kFp8, kNR>;
   const int lane = threadIdx.x % 32;
   const int32_t most = p.max_pages * p.page_size;
-  int32_t b = share.b, hk = share.hk, rb = share.rb, tile = share.tile, len = share.len,
-          units = share.units;
+  int32_t b = share.b, hk = share.hk, rb = share.rb, len = share.len, units = share.units;
+  int32_t tile = max(0, share.off - kItemCost);  // of the current item
+  int32_t end = share.end - kItemCost;           // the share's end, in tiles of that item
   // Each slot is two boxes wide and up to eight page pieces high: a lane each.
   const int piece = lane / 2, box = lane % 2;
   const int first_row = piece * p.piece_rows;
@@ -402,7 +412,23 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
   uint32_t seg = 0;    // segments (the share's parts of items)
   int32_t seg_start = tile;
   int32_t slot = 2 * blockIdx.x;
-  int32_t id = share.todo > 0 ? page_of(tile) : 0;
+  // To the next item with a tile in the share (the first may be cut before its tiles).
+  const auto next_item = [&] {
+    end -= units + kItemCost;
+    tile = 0;
+    if (++rb == p.row_blocks) {
+      rb = 0;
+      if (++hk == p.kv_heads) {
+        hk = 0;
+        ++b;
+        if (end > 0) {
+          len = __ldg(p.kv_len + b);
+          units = units_of(len, most);
+        }
+      }
+    }
+  };
+  int32_t id = tile < end ? page_of(tile) : 0;
   // Read once (by one row block), the pages leave L2 before anything else does.
   const uint64_t policy = p.row_blocks == 1 ? l2_evict_first() : l2_evict_normal();
   constexpr int kPerTile = kKeys ? G::kKeySlots : G::kValSlots;
@@ -415,9 +441,9 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
            mbar_wait_warp(&empty[c % kSlots], phase<kSlots>(c - kSlots), &sm->abort, kWaitNs);
   };
 #pragma unroll 1
-  for (uint32_t left = share.todo; ok && left > 0; --left, ++it) {
+  for (; ok && tile < end; ++it) {
     const bool valid_len = len >= 0 && len <= most;
-    const bool seg_last = tile + 1 == units || left == 1;
+    const bool seg_last = tile + 1 == units || tile + 1 == end;
     const int32_t page = id, head = hk, key0 = tile * kTile;
     const int32_t tile_len = valid_len ? len : 0;
     const int32_t keys = max(0, min(kTile, tile_len - key0));  // 0 for an idle sequence
@@ -449,21 +475,8 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
       seg_start = 0;
       slot = 2 * blockIdx.x + 1;
     }
-    if (++tile == units) {
-      tile = 0;
-      if (++rb == p.row_blocks) {
-        rb = 0;
-        if (++hk == p.kv_heads) {
-          hk = 0;
-          ++b;
-          if (left > 1) {
-            len = __ldg(p.kv_len + b);
-            units = units_of(len, most);
-          }
-        }
-      }
-    }
-    if (left > 1) id = page_of(tile);
+    if (++tile == units) next_item();
+    if (tile < end) id = page_of(tile);
 #pragma unroll 1
     for (int k = 0; k < kPerTile; ++k) {
       const uint32_t c = it * kPerTile + k;
@@ -527,18 +540,18 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
   }
   // The end mark takes the next slot's turn; then the copies still in flight
   // are awaited (bounded), so that none lands after the CTA is gone.
-  uint32_t end = it * kPerTile;
-  if (kKeys && ok && freed(end)) {
+  uint32_t uses = it * kPerTile;
+  if (kKeys && ok && freed(uses)) {
     if (lane == 0) {
       sm->ring[it % kRing].flags = kStop;
-      mbar_arrive(&full[end % kSlots]);
+      mbar_arrive(&full[uses % kSlots]);
     }
-    ++end;
+    ++uses;
   }
   if (kKeys) asm volatile("cp.async.wait_all;" ::: "memory");
   if (lane == 0) {
     volatile int never = 0;
-    for (uint32_t c = end > kSlots ? end - kSlots : 0; c < end; ++c)
+    for (uint32_t c = uses > kSlots ? uses - kSlots : 0; c < uses; ++c)
       mbar_wait(&full[c % kSlots], phase<kSlots>(c), &never, kDrainNs);
   }
 }
@@ -1191,23 +1204,19 @@ __device__ __forceinline__ float block_sum(float x, float *scratch) {
   return y;
 }
 
-// The shares of all tiles and the tiles, per head and row block, before sequence b (one warp).
+// The shares, and the steps per head and row block before sequence b (one warp).
 __device__ __forceinline__ Shares all_shares(const FwdParams &p, uint32_t ctas, int32_t b,
                                              uint32_t *before) {
   const int32_t most = p.max_pages * p.page_size;
   uint32_t total = 0, mine = 0;
   for (int32_t x = threadIdx.x % 32; x < p.B; x += 32) {
-    const uint32_t u = units_of(__ldg(p.kv_len + x), most);
+    const uint32_t u = kItemCost + units_of(__ldg(p.kv_len + x), most);
     total += u;
     mine += x < b ? u : 0;
   }
-  total = __reduce_add_sync(0xffffffffu, total) * p.kv_heads * p.row_blocks;
+  total = __reduce_add_sync(0xffffffffu, total);
   *before = __reduce_add_sync(0xffffffffu, mine);
-  Shares all;
-  all.ctas = min(ctas, total);
-  all.each = total / all.ctas;
-  all.more = total - all.each * all.ctas;
-  return all;
+  return cut_line(total * p.kv_heads * p.row_blocks, ctas);
 }
 
 // Block (cut item, row): joins one row.  The cut items are found from the boundaries between
@@ -1233,12 +1242,12 @@ __device__ void join_row(const JoinParams &jp) {
       const int32_t len = __ldg(p.kv_len + b);
       const uint32_t units = units_of(len, p.max_pages * p.page_size);
       const uint32_t heads = p.kv_heads * p.row_blocks;
-      parts = parts_of(all, before * heads + (which - b * heads) * units, units);
+      parts = parts_of(all, before * heads + (which - b * heads) * (kItemCost + units), units);
       if (parts.n > 1) x = make_int4(static_cast<int>(which), parts.first, parts.n, len);
     } else {
       const Share s = find_share(p, which + 1, jp.ctas);
-      if (s.tile > 0) {
-        parts = parts_of(s.all, s.begin - s.tile, s.units);
+      if (s.off > kItemCost) {
+        parts = parts_of(s.all, s.begin - s.off, s.units);
         if (parts.first / 2 == static_cast<int>(which))
           x = make_int4((s.b * p.kv_heads + s.hk) * p.row_blocks + s.rb, parts.first, parts.n, s.len);
       }
@@ -1388,7 +1397,8 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
     Parts parts = {0, 1};
     if (!p.whole)
       parts = parts_of(shared_all,
-                       shared_before * p.kv_heads * p.row_blocks + (hk * p.row_blocks + rb) * units,
+                       shared_before * p.kv_heads * p.row_blocks +
+                           (hk * p.row_blocks + rb) * (kItemCost + units),
                        units);
     const auto state = [&](int s) {
       return parts.n == 1
@@ -1595,10 +1605,11 @@ bool plan_paged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache, boo
   // and the second segment of most CTAs take (6 us, of 1 us a tile).  64 items of 8 tiles on 152
   // SMs: 12.6 us, in shares 14.6 us; of 16 tiles 20.2 us and 18.3 us.  16 items of 4 tiles: 8.1
   // and 9.1 us, of 8 tiles 11.7 and 9.5 us.
-  if (items * static_cast<double>(units) >= 2147483648.0) return false;
+  if (items * static_cast<double>(units + kItemCost) >= 2147483648.0) return false;
   q.whole = q.items <= sm_count && units * (sm_count - q.items) <= int64_t{6} * sm_count;
   q.ctas = q.whole ? static_cast<int>(q.items) : sm_count;
-  if (!q.whole && q.items * units < sm_count) q.ctas = static_cast<int>(q.items * units);
+  if (!q.whole && q.items * (units + kItemCost) < sm_count)
+    q.ctas = static_cast<int>(q.items * (units + kItemCost));
   const size_t slots = q.whole ? 0 : 2 * static_cast<size_t>(q.ctas);
   size_t at = 0;
   const auto take = [&at](size_t bytes) {
