@@ -10,10 +10,8 @@
 //      order is theirs (sign flipped or all bits; NaN as +infinity, -0 as 0);
 //      three histogram passes over 11 + 11 + 10 bits find the k-th largest
 //      value T and how many equal to T still fit; a scan in position order
-//      then writes the list of kept places and moves the weights.  A thread
-//      holds up to 16 consecutive weights in registers, so up to 16384 keys
-//      are read once and ordered by one scan; longer sequences take more
-//      rounds over a copy.
+//      then writes the list of kept places and moves the weights.  Up to
+//      16384 weights are held in shared memory, more in the workspace.
 //   2. Move (one block per item and 128-byte column slice of k1, k2, v).  A
 //      kept row's place is at or before its source, and sources ascend, so
 //      blocks of rows taken in order only need all loads of a block before
@@ -23,6 +21,7 @@
 // Bound: HBM, each kept row read and written once.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "debug_check.cuh"
@@ -33,10 +32,12 @@ namespace diffattn {
 namespace {
 
 constexpr int kSelectThreads = 1024;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kBins = 2048 / kSelectThreads;  // of a histogram, per thread
 constexpr int kMoveThreads = 256;
 constexpr int kBatch = 4;   // 16-byte units of a thread in a block of rows
 constexpr int kAhead = 3;   // blocks of rows in flight
-constexpr int kHeld = 16;   // weights that a thread of the selection holds
+constexpr int kHeld = 16384;  // weights that the selection holds in shared memory
 
 struct EvictParams {
   uint8_t *pool[3];
@@ -56,12 +57,14 @@ struct EvictParams {
 };
 
 __device__ __forceinline__ uint32_t order_key(float w) {
-  if (isnan(w)) w = INFINITY;
-  const uint32_t x = __float_as_uint(w + 0.f);  // -0 becomes 0
-  return (x & 0x80000000u) ? ~x : x | 0x80000000u;
+  uint32_t x = __float_as_uint(w);
+  if ((x & 0x7FFFFFFFu) > 0x7F800000u) x = 0x7F800000u;
+  if (x == 0x80000000u) x = 0;
+  return x ^ (static_cast<uint32_t>(static_cast<int32_t>(x) >> 31) | 0x80000000u);
 }
 
-// Exclusive prefix sum over the block; *total gets the whole sum.
+// Exclusive prefix sum over the block; *total gets the whole sum.  Two barriers; the caller has one
+// more between calls that use the same scratch.
 __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *scratch, uint32_t *total) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   uint32_t incl = x;
@@ -72,31 +75,21 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *scratch, ui
   }
   if (lane == 31) scratch[warp] = incl;
   __syncthreads();
-  if (warp == 0) {
-    uint32_t s = scratch[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    scratch[lane] = s;
-  }
-  __syncthreads();
-  const uint32_t before = warp == 0 ? 0 : scratch[warp - 1];
-  *total = scratch[31];
-  __syncthreads();
-  return before + incl - x;
+  // Every warp sums the warps before it.
+  const uint32_t mine = lane < kSelectWarps ? scratch[lane] : 0;
+  *total = __reduce_add_sync(0xffffffffu, mine);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0) + incl - x;
 }
 
-__device__ __forceinline__ bool in_order(uint32_t key, uint32_t prefix, int shift) {
-  return shift >= 32 || key >> shift == prefix >> shift;
-}
-
+// The loops are kept rolled: a block runs each once or a few times, so what code it has to fetch
+// counts for more than what it executes (unrolled over registers the same steps took 20 us where
+// these take 11, for 8192 keys an item).
 __global__ void __launch_bounds__(kSelectThreads) diffpaged_select_kernel(const EvictParams p) {
+  extern __shared__ float held[];
   __shared__ uint32_t hist[2048];
-  __shared__ uint32_t scratch[32];
+  __shared__ uint32_t scratch[2][kSelectWarps];
   __shared__ uint32_t found[2];
-  const int item = blockIdx.x, tid = threadIdx.x;
+  const int item = blockIdx.x, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int b = item / p.kv_heads, hk = item % p.kv_heads;
   for (int i = tid; i < 2048; i += kSelectThreads) hist[i] = 0;
   grid_dependency_wait();
@@ -113,132 +106,123 @@ __global__ void __launch_bounds__(kSelectThreads) diffpaged_select_kernel(const 
   const int32_t *table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
   const int32_t old = len - p.recent;
   const uint32_t k_keep = p.keep - p.recent;
-  float *copy = p.copy + item * p.padded;
+  float *w = len <= kHeld ? held : p.copy + item * p.padded;  // the weights by position
   const auto weights_of = [&](int32_t page) {
     return p.weights + (static_cast<int64_t>(page) * p.kv_heads + hk) * p.page_size;
   };
-
-  // Rounds of 1024 threads x `each` consecutive positions, in groups of four (which no page
-  // boundary cuts); one round up to 16384 positions.
-  const int32_t each = min(kHeld, ((len + kSelectThreads - 1) / kSelectThreads + 3) & ~3);
-  const int32_t per_round = each * kSelectThreads;
-  const bool single = len <= per_round;
-  float w[kHeld];
-  bool bad = false;
-  const auto load = [&](int32_t at, bool first) {  // this thread's weights of the round at `at`
-    const int32_t j0 = at + tid * each;
-#pragma unroll
-    for (int g = 0; g < kHeld; g += 4) {
-      if (g >= each || j0 + g >= len) break;
-      const float *src = copy + j0 + g;
-      if (first) {
-        const int32_t n = p.by_page.div(j0 + g);
-        const int32_t page = __ldg(table + n);
-        bad |= static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages);
-        if (bad) break;
-        src = weights_of(page) + (j0 + g - n * p.page_size);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (j0 + g + e < len) w[g + e] = src[e];
-    }
-  };
+  __syncthreads();
 
   // The k-th largest key, from its leading bits down.
   uint32_t prefix = 0, need = k_keep;  // need: how many are still to be found at or below prefix
-  const int shift[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
+  bool bad = false;
+  const auto count = [&](float x, int32_t j, int shift, int bits) {
+    const uint32_t key = order_key(x);
+    if (j < old && (shift + bits >= 32 || (key ^ prefix) >> (shift + bits) == 0))
+      atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1u);
+  };
+#pragma unroll 4
+  for (int32_t j = tid; j < len; j += kSelectThreads) {
+    const int32_t n = p.by_page.div(j);
+    const int32_t page = __ldg(table + n);
+    if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) {
+      bad = true;
+    } else {
+      const float x = weights_of(page)[j - n * p.page_size];
+      w[j] = x;
+      count(x, j, 21, 11);
+    }
+  }
+  if (__syncthreads_or(bad)) {  // a page of the sequence is not one: it stays as it is
+    if (tid == 0) {
+      report_bad_page(p.status);
+      p.plan[item] = make_int2(0, 0);
+    }
+    return;
+  }
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
-    for (int32_t at = 0; at < len; at += per_round) {
-      if (pass == 0 || !single) load(at, pass == 0);
-      const int32_t j0 = at + tid * each;
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass < 2 ? 11 : 10;
+    if (pass > 0) {
+#pragma unroll 1
+      for (int32_t j = tid; j < old; j += kSelectThreads) count(w[j], j, shift, bits);
+      __syncthreads();
+    }
+    // Thread t holds the kBins bins below 2048 - kBins t: sums from the largest bin down.
+    uint32_t bin_of[kBins], mine = 0;
 #pragma unroll
-      for (int g = 0; g < kHeld; ++g) {
-        if (g >= each) break;
-        const int32_t j = j0 + g;
-        if (pass == 0 && !single && j < len) copy[j] = w[g];
-        const uint32_t key = order_key(w[g]);
-        const bool counts = j < old && in_order(key, prefix, shift[pass] + bits[pass]);
-        const uint32_t bin = counts ? (key >> shift[pass]) & ((1u << bits[pass]) - 1) : 0xFFFFFFFFu;
-        // Equal weights fill one bin: a warp that agrees adds once.
-        int same;
-        __match_all_sync(0xffffffffu, bin, &same);
-        if (same) {
-          if (counts && tid % 32 == 0) atomicAdd(&hist[bin], 32u);
-        } else if (counts) {
-          atomicAdd(&hist[bin], 1u);
-        }
-      }
+    for (int k = 0; k < kBins; ++k) {
+      bin_of[k] = hist[2047 - kBins * tid - k];
+      hist[2047 - kBins * tid - k] = 0;
+      mine += bin_of[k];
     }
-    if (__syncthreads_or(bad)) {  // a page of the sequence is not one: it stays as it is
-      if (tid == 0) {
-        report_bad_page(p.status);
-        p.plan[item] = make_int2(0, 0);
-      }
-      return;
-    }
-    // Thread t holds bins 2047 - 2 t and 2046 - 2 t: sums from the largest bin down.
-    const uint32_t hi = hist[2047 - 2 * tid], lo = hist[2046 - 2 * tid];
-    hist[2047 - 2 * tid] = hist[2046 - 2 * tid] = 0;
     if (tid == 0) found[0] = found[1] = 0;
     uint32_t total;
-    const uint32_t above = block_scan(hi + lo, scratch, &total);
-    if (need > above && need <= above + hi + lo) {
-      const bool in_hi = need <= above + hi;
-      found[0] = in_hi ? 2047 - 2 * tid : 2046 - 2 * tid;
-      found[1] = need - above - (in_hi ? 0 : hi);
+    uint32_t above = block_scan(mine, scratch[0], &total);
+#pragma unroll
+    for (int k = 0; k < kBins; ++k) {
+      if (need > above && need <= above + bin_of[k]) {
+        found[0] = 2047 - kBins * tid - k;
+        found[1] = need - above;
+      }
+      above += bin_of[k];
     }
     __syncthreads();
-    prefix |= found[0] << shift[pass];
+    prefix |= found[0] << shift;
     need = found[1];
   }
+  if (k_keep == 0) prefix = 0xFFFFFFFFu;  // above every key
 
-  // Kept places in order: keys above T, the first `need` equal to it, and the last `recent`.
-  uint32_t equal_before = 0, kept = 0;
-  int2 *list = p.list + static_cast<int64_t>(item) * p.keep;
-  uint32_t in_place = 0xFFFFFFFFu;  // the first position that does not stay
-  for (int32_t at = 0; at < len; at += per_round) {
-    if (!single) load(at, false);
-    const int32_t j0 = at + tid * each;
-    uint32_t equal = 0, all_equal = 0;
-#pragma unroll
-    for (int g = 0; g < kHeld; ++g)
-      if (g < each && j0 + g < old) equal += order_key(w[g]) == prefix ? 1 : 0;
-    uint32_t eq = equal_before + block_scan(equal, scratch, &all_equal);
-    uint32_t mask = 0;
-#pragma unroll
-    for (int g = 0; g < kHeld; ++g) {
-      const int32_t j = j0 + g;
-      if (g >= each || j >= len) break;
-      const uint32_t key = order_key(w[g]);
-      const bool is_equal = key == prefix;
-      const bool stays = j >= old || (k_keep > 0 && (key > prefix || (is_equal && eq < need)));
-      if (j < old && is_equal) ++eq;
-      if (stays)
-        mask |= 1u << g;
-      else
-        in_place = min(in_place, static_cast<uint32_t>(j));
-    }
-    uint32_t total;
-    uint32_t to = kept + block_scan(__popc(mask), scratch, &total);
-    // Every weight of this round has been read (and, in more rounds, of all: from the copy).
-#pragma unroll
-    for (int g = 0; g < kHeld; ++g) {
-      if (!((mask >> g) & 1) || !dbg_ok(to < static_cast<uint32_t>(p.keep), p.status, 50)) continue;
-      const int32_t n = p.by_page.div(j0 + g), m = p.by_page.div(static_cast<int32_t>(to));
-      list[to] = make_int2(__ldg(table + n), j0 + g - n * p.page_size);
-      weights_of(__ldg(table + m))[to - m * p.page_size] = w[g];
-      ++to;
-    }
-    equal_before += all_equal;
-    kept += total;
+  // Kept places in order: keys above T, the first `need` equal to it, and the last `recent`.  Each
+  // warp has a run of positions, 32 a step; the warps before it tell it where its own go.
+  const int32_t steps = (len + 32 * kSelectWarps - 1) / (32 * kSelectWarps);
+  const int32_t from = warp * steps * 32, to = min(len, from + steps * 32);
+  uint32_t above_t = 0, equal_t = 0;
+#pragma unroll 1
+  for (int32_t j0 = from; j0 < to; j0 += 32) {
+    const int32_t j = j0 + lane;
+    const uint32_t key = j < old ? order_key(w[j]) : 0;
+    above_t += __popc(__ballot_sync(0xffffffffu, j < to && (j >= old || key > prefix)));
+    equal_t += __popc(__ballot_sync(0xffffffffu, j < old && j < to && key == prefix));
   }
-  in_place = __reduce_min_sync(0xffffffffu, in_place);
-  if (tid % 32 == 0) scratch[tid / 32] = in_place;
+  if (lane == 0) {
+    scratch[0][warp] = above_t;
+    scratch[1][warp] = equal_t;
+  }
   __syncthreads();
-  if (tid < 32) {
-    in_place = __reduce_min_sync(0xffffffffu, scratch[tid]);
-    if (tid == 0) p.plan[item] = make_int2(min(static_cast<int32_t>(in_place), p.keep), 1);
+  const bool before = lane < warp && lane < kSelectWarps;
+  uint32_t equal_before = __reduce_add_sync(0xffffffffu, before ? scratch[1][lane] : 0);
+  uint32_t at = __reduce_add_sync(0xffffffffu, before ? scratch[0][lane] : 0) + min(need, equal_before);
+  int2 *list = p.list + static_cast<int64_t>(item) * p.keep;
+  const uint32_t lower = (1u << lane) - 1;
+  uint32_t in_place = 0xFFFFFFFFu;  // the first position that does not stay
+#pragma unroll 1
+  for (int32_t j0 = from; j0 < to; j0 += 32) {
+    const int32_t j = j0 + lane;
+    const float x = j < to ? w[j] : 0.f;
+    const uint32_t key = j < old ? order_key(x) : 0;
+    const bool is_equal = j < old && j < to && key == prefix;
+    const uint32_t equals = __ballot_sync(0xffffffffu, is_equal);
+    const bool stays =
+        j < to && (j >= old || key > prefix ||
+                   (is_equal && equal_before + __popc(equals & lower) < need));
+    const uint32_t kept = __ballot_sync(0xffffffffu, stays);
+    const uint32_t dst = at + __popc(kept & lower);
+    if (stays && dbg_ok(dst < static_cast<uint32_t>(p.keep), p.status, 50)) {
+      const int32_t n = p.by_page.div(j), m = p.by_page.div(static_cast<int32_t>(dst));
+      list[dst] = make_int2(__ldg(table + n), j - n * p.page_size);
+      weights_of(__ldg(table + m))[static_cast<int32_t>(dst) - m * p.page_size] = x;
+    }
+    const uint32_t gone = __ballot_sync(0xffffffffu, j < to && !stays);
+    if (gone) in_place = min(in_place, static_cast<uint32_t>(j0 + __ffs(gone) - 1));
+    equal_before += __popc(equals);
+    at += __popc(kept);
+  }
+  __syncthreads();
+  if (lane == 0) scratch[0][warp] = in_place;
+  __syncthreads();
+  if (warp == 0) {
+    in_place = __reduce_min_sync(0xffffffffu, lane < kSelectWarps ? scratch[0][lane] : 0xFFFFFFFFu);
+    if (lane == 0) p.plan[item] = make_int2(min(static_cast<int32_t>(in_place), p.keep), 1);
   }
 }
 
@@ -326,7 +310,7 @@ EvictLayout layout(const diffattn_desc &desc, const diffpaged_cache &cache, int6
   l.padded = most;
   const int64_t kept = keep < most ? keep : most;
   l.copy = 0;
-  const int64_t copied = most > kHeld * kSelectThreads ? most : 0;
+  const int64_t copied = most > kHeld ? most : 0;
   l.list = round256(static_cast<size_t>(items * copied) * sizeof(float));
   l.plan = l.list + round256(static_cast<size_t>(items * kept) * sizeof(int2));
   l.bytes = l.plan + round256(static_cast<size_t>(items) * sizeof(int2));
@@ -385,12 +369,24 @@ diffattn_status launch_paged_evict(const diffattn_desc &desc, const diffpaged_ca
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(items));
   cfg.blockDim = dim3(kSelectThreads);
+  const int64_t most = cache.max_pages * cache.page_size;
+  cfg.dynamicSmemBytes = sizeof(float) * static_cast<size_t>(most < kHeld ? most : kHeld);
+  static std::atomic<bool> attr_set[64];  // per device (concurrent callers may both set)
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DIFFATTN_ERR_CUDA;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(diffpaged_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(sizeof(float) * kHeld)) != cudaSuccess)
+      return DIFFATTN_ERR_CUDA;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, diffpaged_select_kernel, p) != cudaSuccess) return DIFFATTN_ERR_CUDA;
   cfg.gridDim = dim3(static_cast<unsigned>(items) * slices);
   cfg.blockDim = dim3(kMoveThreads);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, diffpaged_move_kernel, p, slices) == cudaSuccess
              ? DIFFATTN_OK
              : DIFFATTN_ERR_CUDA;
