@@ -482,7 +482,14 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
       const uint32_t c = it * kPerTile + k;
       const int s = c % kSlots;
       if (!(ok = freed(c))) break;
+      // The copies first; their barrier's phase ends no sooner than the arrival below them.
       const int row_bytes = kKeys ? G::kKeyBox : 128;
+      if (have) {
+        const CUtensorMap *map = !kKeys ? mv : (G::kKeySlots == 1 ? box : k) ? mk2 : mk1;
+        const int x = !kKeys ? 128 * k + 64 * box : G::kKeySlots == 1 ? 0 : 64 * box;
+        tma_load_4d_hint(ring + s * kSlotBytes + first_row * row_bytes, map, &full[s], x, row, head,
+                         z, policy);
+      }
       if (kKeys && k == 0) {
         if (lane == 0) sm->ring[it % kRing] = d;
         if (seg_first && lane < kNR) {  // the segment's rows
@@ -494,20 +501,13 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
           info.out = d.b * p.outs.b + info.head * p.outs.h + i * p.outs.n;
           sm->rows[seg % kRing][lane] = info;
         }
-        __syncwarp();
       }
+      __syncwarp();
       if (lane == 0) {
         if (rows > 0)
           mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(rows) * 2 * row_bytes);
         else
           mbar_arrive(&full[s]);
-      }
-      __syncwarp();
-      if (have) {
-        const CUtensorMap *map = !kKeys ? mv : (G::kKeySlots == 1 ? box : k) ? mk2 : mk1;
-        const int x = !kKeys ? 128 * k + 64 * box : G::kKeySlots == 1 ? 0 : 64 * box;
-        tma_load_4d_hint(ring + s * kSlotBytes + first_row * row_bytes, map, &full[s], x, row, head,
-                         z, policy);
       }
     }
     // The segment's q rows: 16-byte units into the swizzled operand layout.
@@ -1124,8 +1124,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The setup up to here overlaps the kernel before; the kernel after may start its own from
     // here on, so that what it reads before it waits for this one is what this one reads.
     grid_dependency_wait();
-    grid_dependents_launch();
     share = find_share(p, blockIdx.x, gridDim.x);
+    grid_dependents_launch();
   } else if (warp == kMmaWarp) {
     tmem_alloc(&sm->tmem, G::kTmemCols);
     tmem_relinquish();
