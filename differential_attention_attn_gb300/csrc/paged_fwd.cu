@@ -50,10 +50,9 @@ namespace diffattn {
 namespace {
 
 constexpr int kTile = kPagedTile;
-constexpr int kConsumers = 256;  // softmax and epilogue threads
-// Warps 0-2 issue, 4-11 (a multiple of four, for their quarters of tensor memory) do the softmax.
+// Warps 0-2 issue, those from 4 on (a multiple of four, for their quarters of tensor memory) do the
+// softmax.
 constexpr int kMmaWarp = 0, kKeyWarp = 1, kValueWarp = 2, kSoftmaxWarp = 4;
-constexpr int kThreads = 128 + kConsumers;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kGrowth = 8.f;  // log2 units a logit may pass the reference maximum by
@@ -106,8 +105,13 @@ struct RowInfo {
 template <int kD, bool kFp8, int kNR>
 struct Geo {
   static constexpr int kNQ = kNR < 8 ? 8 : kNR;
-  static constexpr int kW = kNR < 8 ? kNR : 8;                      // rows taken at a time
-  static constexpr int kChunks = kNR / kW;
+  // Softmax threads: one per key and map, two from 8 rows on, with half of the rows each.
+  static constexpr int kSets = kNR < 8 ? 1 : 2;
+  static constexpr int kConsumers = 2 * kTile * kSets;
+  static constexpr int kThreads = 32 * kSoftmaxWarp + kConsumers;
+  static constexpr int kMine = kNR / kSets;                         // rows of a thread
+  static constexpr int kW = kMine < 8 ? kMine : 8;                  // of them at a time
+  static constexpr int kChunks = kMine / kW;
   static constexpr int kKeyRow = kFp8 ? kD : 2 * kD;                // bytes
   static constexpr int kKeyBox = kKeyRow < 128 ? kKeyRow : 128;     // bytes of a key box row
   static constexpr int kKeySlots = kKeyRow <= 128 ? 1 : 2;          // both maps in one, or each its own
@@ -686,10 +690,12 @@ template <int kD, bool kFp8, int kNR>
 __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem, Ctrl<kNR> *sm) {
   using G = Geo<kD, kFp8, kNR>;
   using L = Layout<kD, kFp8, kNR>;
-  constexpr int kNQ = G::kNQ, kW = G::kW, kChunks = G::kChunks;
+  constexpr int kNQ = G::kNQ, kW = G::kW, kChunks = G::kChunks, kMine = G::kMine;
+  constexpr int kConsumers = G::kConsumers;
   constexpr int kVUnits = kD / 4;  // 16-byte units of a value row
   const int tid = threadIdx.x - 32 * kSoftmaxWarp, warp = tid / 32, lane = tid % 32;
-  const int map = warp / 4, quarter = warp % 4;
+  const int group = warp / 4, quarter = warp % 4;
+  const int map = group & 1, r0 = (group >> 1) * kMine;  // rows r0 .. r0 + kMine - 1
   const int key = 32 * quarter + lane;  // of the tile
   const uint32_t tmem = sm->tmem + (static_cast<uint32_t>(32 * quarter) << 16);
   const auto v_row = [&](uint32_t t, int row, int u) {  // unit u of value row `row` of tile t
@@ -698,7 +704,7 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
                                      ((u / 8) % 2) * kBoxBytes + row * 128 + (u % 8) * 16);
   };
 
-  float l[kNR];
+  float l[kMine];
   int m_turn = 0;
   bool poisoned = false, healthy = true;
   uint32_t late = 0, seg = 0;
@@ -736,15 +742,15 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
     const bool masked = d.key0 + kTile - 1 > lim_min;
     const int32_t keys = d.len - d.key0;  // valid rows of the tile if below kTile
     const bool mixed = p.causal && p.N > 1 && masked;  // some rows see keys that others do not
-    const int real = kNR == 1 ? 1 : d.real;
-    const RowInfo *rows = sm->rows[seg % kRing];
-    const uint32_t s_at = tmem + (t & 1) * 2 * G::kNS + map * G::kNS;
+    const int real = kNR == 1 ? 1 : min(d.real - r0, kMine);  // rows of this thread (0 or less: none)
+    const RowInfo *rows = sm->rows[seg % kRing] + r0;
+    const uint32_t s_at = tmem + (t & 1) * 2 * G::kNS + map * G::kNS + r0;
 
     const bool fresh = (d.flags & kFirst) != 0;  // nothing in O yet
-    const float(*m)[kNR] = sm->m[m_turn];
+    const float *m = sm->m[m_turn][map] + r0;
 
     // This key's logits of the rows, in log2 units; -inf where it is masked.
-    float x[kNR];
+    float x[kMine];
     bool grew = false;
     if (tid == 0) sm->bad_rows[(t + 1) % 3] = 0;
     if (!stop) {
@@ -752,7 +758,7 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
         poisoned = false;
         late = 0;
 #pragma unroll
-        for (int q = 0; q < kNR; ++q) l[q] = 0.f;
+        for (int q = 0; q < kMine; ++q) l[q] = 0.f;
       }
       if (d.flags & kBad) poisoned = true;
       grew = fresh;  // the first tile sets the references
@@ -768,19 +774,19 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
       }
       if (masked) {
 #pragma unroll
-        for (int q = 0; q < kNR; ++q)
+        for (int q = 0; q < kMine; ++q)
           if (d.key0 + key > rows[q].last) x[q] = -INFINITY;
       }
       if (!fresh) {
 #pragma unroll
-        for (int q = 0; q < kNR; ++q) grew |= q < real && x[q] > m[map][q] + kGrowth;
+        for (int q = 0; q < kMine; ++q) grew |= q < real && x[q] > m[q] + kGrowth;
       }
       if (p.logits != nullptr && key < keys) {
-        float *dst = p.logits +
-                     ((static_cast<int64_t>(d.b) * p.kv_heads + d.hk) * 2 + map) * p.rows * p.padded +
-                     static_cast<int64_t>(d.item % p.row_blocks * kNR) * p.padded + d.key0 + key;
+        const int64_t bh = static_cast<int64_t>(d.b) * p.kv_heads + d.hk;
+        float *dst = p.logits + ((bh * 2 + map) * p.rows + d.item % p.row_blocks * kNR + r0) * p.padded +
+                     d.key0 + key;
 #pragma unroll
-        for (int q = 0; q < kNR; ++q)
+        for (int q = 0; q < kMine; ++q)
           if (q < real && dbg_ok(d.key0 + key < p.padded, p.status, 41)) dst[q * p.padded] = x[q];
       }
       // P's buffer: the product that read it last is done.
@@ -825,10 +831,10 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
       if (*reinterpret_cast<volatile int *>(&sm->failed)) break;
       if (!stop) {
 #pragma unroll
-        for (int q = 0; q < kNR; ++q) {
+        for (int q = 0; q < kMine; ++q) {
           if (q >= real) break;
           const float y = warp_max(x[q]);
-          if (lane == 0) sm->wmax[map][quarter][q] = y;
+          if (lane == 0) sm->wmax[map][quarter][r0 + q] = y;
         }
         // O moves with the reference, so the product before must be done.
         if (!fresh)
@@ -838,12 +844,13 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
       if (!stop) {
         const auto new_m = [&](int q) {
           const float(*w)[kNR] = sm->wmax[map];
-          const float y = fmaxf(fmaxf(w[0][q], w[1][q]), fmaxf(w[2][q], w[3][q]));
-          return fresh ? y : fmaxf(m[map][q], y);
+          const float y = fmaxf(fmaxf(w[0][r0 + q], w[1][r0 + q]), fmaxf(w[2][r0 + q], w[3][r0 + q]));
+          return fresh ? y : fmaxf(m[q], y);
         };
-        if (quarter == 0 && lane < real) sm->m[m_turn ^ 1][map][lane] = new_m(lane);
+        if (quarter == 0 && lane < real) sm->m[m_turn ^ 1][map][r0 + lane] = new_m(lane);
         if (!fresh) {
-          const uint32_t o_at = tmem + G::kTmemO + (seg % G::kOBufs) * G::kOCols + map * 2 * kNQ;
+          const uint32_t o_at =
+              tmem + G::kTmemO + (seg % G::kOBufs) * G::kOCols + map * 2 * kNQ + r0;
           tc_fence_after_sync();
 #pragma unroll
           for (int k = 0; k < kChunks; ++k) {
@@ -853,7 +860,7 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
 #pragma unroll
             for (int e = 0; e < kW; ++e) {
               const int q = kW * k + e;
-              const float old = m[map][q], y = new_m(q);
+              const float old = m[q], y = new_m(q);
               f[e] = y == old ? 1.f : ex2_approx(old - y);
               moved |= q < real && y != old;
               l[q] *= f[e];
@@ -904,8 +911,8 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
 #pragma unroll
       for (int e = 0; e < kW; ++e) {
         const float xe = x[kW * k + e];
-        if (kept_out) sm->late[seg & 1][map][back][kW * k + e] = xe;
-        y[e] = ex2_approx(xe - sm->m[m_turn][map][kW * k + e]);
+        if (kept_out) sm->late[seg & 1][map][back][r0 + kW * k + e] = xe;
+        y[e] = ex2_approx(xe - sm->m[m_turn][map][r0 + kW * k + e]);
         if (masked && xe == -INFINITY) y[e] = 0.f;  // also where no key has been seen yet
         l[kW * k + e] += y[e];
       }
@@ -917,10 +924,11 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
       }
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
-        const int unit = (map * 2 + part) * (kNQ / 8) + k;  // of eight columns
+        const int unit = (map * 2 + part) * (kNQ / 8) + r0 / 8 + k;  // of eight columns
         const uint32_t *src = part ? lo : hi;
         uint8_t *at = p_buf + (unit / 8) * (kTile * 128) + key * G::kPRow +
-                      (((unit % 8) ^ (G::kPRow == 64 ? (key >> 1) & 3 : key & 7)) << 4);
+                      (((unit % 8) ^ (G::kPRow == 64 ? (key >> 1) & 3 : key & 7)) << 4) +
+                      2 * (r0 % 8);
         if constexpr (kW == 1)
           *reinterpret_cast<uint16_t *>(at) = static_cast<uint16_t>(src[0]);
         else if constexpr (kW == 2)
@@ -945,23 +953,25 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
       const TileDesc &done = sm->done[parity];
       const int done_real = kNR == 1 ? 1 : done.real;
       const bool direct = (done.flags & kDirect) != 0;
-      // d = 64: the two halves of the warps take turns at eight rows; d = 128: each has its half
-      // of the value columns for all rows.
-      constexpr int kStep = kD == 128 || kChunks == 1 ? 1 : 2;  // chunks per turn
-      constexpr int kMine = kW * kChunks / kStep;               // rows of a thread
-      const int half = warp / 4;
-      const int block = kD == 128 ? half : 0;
+      // A thread has one value column.  The groups of four warps share the rows, kTake at a turn;
+      // for d = 128 every other group has the second 128 columns.
+      constexpr int kShares = kD == 128 ? G::kSets : 2 * G::kSets;
+      constexpr int kTake = kNR / kShares < 1 ? 1 : kNR / kShares < 8 ? kNR / kShares : 8;
+      constexpr int kTurns = (kNR + kShares * kTake - 1) / (kShares * kTake);
+      constexpr int kHas = kTake * kTurns;
+      const int block = kD == 128 ? group & 1 : 0;
+      const int share = kD == 128 ? group >> 1 : group;
       const int col = 128 * block + key;
-      const bool idle = kD == 64 && kChunks == 1 && half == 1;
+      const auto row_at = [&](int k) { return kTake * (kShares * k + share); };  // of turn k
       const uint32_t o_at =
           tmem + G::kTmemO + ((seg - 1) % G::kOBufs) * G::kOCols + block * G::kPCols;
       // What the output needs from global memory, on its way during the wait.
-      constexpr bool kEarly = kMine <= 4;
-      float lam[kEarly ? kMine : 1], gain[kEarly ? kMine : 1];
-      if (kEarly && direct && !idle) {
+      constexpr bool kEarly = kHas <= 4;
+      float lam[kEarly ? kHas : 1], gain[kEarly ? kHas : 1];
+      if (kEarly && direct) {
 #pragma unroll
-        for (int e = 0; e < kMine; ++e) {
-          const int q = kStep == 2 ? 8 * half + e : e;
+        for (int e = 0; e < kHas; ++e) {
+          const int q = row_at(e / kTake) + e % kTake;
           if (q >= done_real) break;
           lam[e] = __ldg(p.lambda + done_rows[q].head);
           gain[e] = p.headnorm && p.norm_w != nullptr
@@ -979,18 +989,18 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
         const float(*x)[kNR] = sm->lsum[parity][mp];
         return (x[0][q] + x[1][q]) + (x[2][q] + x[3][q]);
       };
-      float o[kMine];
+      float o[kHas];
 #pragma unroll
-      for (int k = 0; k < kChunks / kStep; ++k) {
-        const int q0 = kW * (kStep * k + (kStep == 2 ? half : 0));
-        if (idle || q0 >= done_real) break;
-        uint32_t part[4][kW];  // map 1 hi, lo, map 2 hi, lo
+      for (int k = 0; k < kTurns; ++k) {
+        const int q0 = row_at(k);
+        if (q0 >= done_real) break;
+        uint32_t part[4][kTake];  // map 1 hi, lo, map 2 hi, lo
 #pragma unroll
         for (int e = 0; e < 4; ++e) tmem_load(o_at + e * kNQ + q0, part[e]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) tmem_loaded(part[e]);
 #pragma unroll
-        for (int e = 0; e < kW; ++e) {
+        for (int e = 0; e < kTake; ++e) {
           const int q = q0 + e;
           if (q >= done_real) break;
           float y1 = __uint_as_float(part[0][e]) + __uint_as_float(part[1][e]);
@@ -1001,10 +1011,10 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
             y2 += more.y;
           }
           if (direct) {
-            const float lm = kEarly ? lam[kW * k + e] : __ldg(p.lambda + done_rows[q].head);
+            const float lm = kEarly ? lam[kTake * k + e] : __ldg(p.lambda + done_rows[q].head);
             float y = y1 / l_of(0, q) - lm * (y2 / l_of(1, q));
             if (done_rows[q].last < 0 && !done_poisoned) y = 0.f;  // a row that sees no key
-            o[kW * k + e] = y;
+            o[kTake * k + e] = y;
           } else if (dbg_ok(done.slot >= 0 && done.slot < 2 * static_cast<int>(gridDim.x),
                             p.status, 42)) {
             float *dst = p.part + (static_cast<int64_t>(done.slot) * 2 * kNR + q) * (2 * kD) + col;
@@ -1014,7 +1024,7 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
         }
       }
       // The row's (m, l): per slot for the join, per item for the weights.
-      if (quarter == 0 && (!direct || p.item_ml != nullptr)) {
+      if (quarter == 0 && r0 == 0 && (!direct || p.item_ml != nullptr)) {
         float2 *ml = (direct ? p.item_ml + static_cast<int64_t>(done.item) * 2 * kNR
                              : p.part_ml + static_cast<int64_t>(done.slot) * 2 * kNR) +
                      map * kNR;
@@ -1036,43 +1046,43 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
 #pragma unroll 1
         for (int pass = p.headnorm == 2 ? 0 : 1; pass < 2 && p.headnorm; ++pass) {  // mean, square
 #pragma unroll
-          for (int k = 0; k < kChunks / kStep; ++k) {
-            const int q0 = kW * (kStep * k + (kStep == 2 ? half : 0));
-            if (idle || q0 >= done_real) break;
+          for (int k = 0; k < kTurns; ++k) {
+            const int q0 = row_at(k);
+            if (q0 >= done_real) break;
 #pragma unroll
-            for (int e = 0; e < kW; ++e) {
+            for (int e = 0; e < kTake; ++e) {
               if (q0 + e >= done_real) break;
-              const float y = o[kW * k + e];
+              const float y = o[kTake * k + e];
               const float z = warp_sum(pass ? y * y : y);
-              if (lane == 0) sm->rsum[kD == 128 ? half : 0][quarter][q0 + e] = z;
+              if (lane == 0) sm->rsum[block][quarter][q0 + e] = z;
             }
           }
           named_barrier_sync(2, kConsumers);
           if (pass == 0) {
 #pragma unroll
-            for (int k = 0; k < kChunks / kStep; ++k) {
-              const int q0 = kW * (kStep * k + (kStep == 2 ? half : 0));
-              if (idle || q0 >= done_real) break;
+            for (int k = 0; k < kTurns; ++k) {
+              const int q0 = row_at(k);
+              if (q0 >= done_real) break;
 #pragma unroll
-              for (int e = 0; e < kW; ++e)
-                if (q0 + e < done_real) o[kW * k + e] -= row_sum(q0 + e) * (0.5f / kD);
+              for (int e = 0; e < kTake; ++e)
+                if (q0 + e < done_real) o[kTake * k + e] -= row_sum(q0 + e) * (0.5f / kD);
             }
             named_barrier_sync(2, kConsumers);
           }
         }
 #pragma unroll
-        for (int k = 0; k < kChunks / kStep; ++k) {
-          const int q0 = kW * (kStep * k + (kStep == 2 ? half : 0));
-          if (idle || q0 >= done_real) break;
+        for (int k = 0; k < kTurns; ++k) {
+          const int q0 = row_at(k);
+          if (q0 >= done_real) break;
 #pragma unroll
-          for (int e = 0; e < kW; ++e) {
+          for (int e = 0; e < kTake; ++e) {
             const int q = q0 + e;
             if (q >= done_real) break;
-            float y = o[kW * k + e];
+            float y = o[kTake * k + e];
             if (p.headnorm && (done_rows[q].last >= 0 || done_poisoned)) {
               y *= rsqrtf(row_sum(q) * (0.5f / kD) + p.eps) * p.out_scale;
               if (kEarly)
-                y *= gain[kW * k + e];
+                y *= gain[kTake * k + e];
               else if (p.norm_w != nullptr)
                 y *= __ldg(p.norm_w + done_rows[q].head * (2 * kD) + col);
             }
@@ -1084,12 +1094,13 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
     if (stop) break;
     if (d.flags & kLast) {  // this segment's sums and references, read after the next vote
 #pragma unroll
-      for (int q = 0; q < kNR; ++q) {
+      for (int q = 0; q < kMine; ++q) {
         if (q >= real) break;
         const float y = warp_sum(l[q]);
-        if (lane == 0) sm->lsum[seg & 1][map][quarter][q] = poisoned ? NAN : y;
+        if (lane == 0) sm->lsum[seg & 1][map][quarter][r0 + q] = poisoned ? NAN : y;
       }
-      if (quarter == 0 && lane < real) sm->ref[seg & 1][map][lane] = sm->m[m_turn][map][lane];
+      if (quarter == 0 && lane < real)
+        sm->ref[seg & 1][map][r0 + lane] = sm->m[m_turn][map][r0 + lane];
       if (tid == 0) sm->done[seg & 1] = d;
       done_poisoned = poisoned;
       done_late = late;
@@ -1100,7 +1111,7 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
 }
 
 template <int kD, bool kFp8, int kNR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Geo<kD, kFp8, kNR>::kThreads, 1)
     diffpaged_fwd_kernel(const __grid_constant__ CUtensorMap mk1,
                          const __grid_constant__ CUtensorMap mk2,
                          const __grid_constant__ CUtensorMap mv,
@@ -1142,9 +1153,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm->q_full[k], 32);
       mbar_init(&sm->q_empty[k], 1);
       mbar_init(&sm->s_full[k], 1);
-      mbar_init(&sm->p_full[k], kConsumers / 32);
+      mbar_init(&sm->p_full[k], G::kConsumers / 32);
       mbar_init(&sm->pv_done[k], 1);
-      mbar_init(&sm->o_empty[k], kConsumers / 32);
+      mbar_init(&sm->o_empty[k], G::kConsumers / 32);
     }
     mbar_init(&sm->drain, 1);
     sm->abort = sm->failed = 0;
@@ -1439,10 +1450,10 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
         if (r >= p.rows) break;
         const float4 st = row_stat[r];
         if (st.y == 0.f) continue;
-        w[0] += fabsf(exp2f(x1[k].x - st.x) * st.y - exp2f(x2[k].x - st.z) * st.w);
-        w[1] += fabsf(exp2f(x1[k].y - st.x) * st.y - exp2f(x2[k].y - st.z) * st.w);
-        w[2] += fabsf(exp2f(x1[k].z - st.x) * st.y - exp2f(x2[k].z - st.z) * st.w);
-        w[3] += fabsf(exp2f(x1[k].w - st.x) * st.y - exp2f(x2[k].w - st.z) * st.w);
+        w[0] += fabsf(ex2_approx(x1[k].x - st.x) * st.y - ex2_approx(x2[k].x - st.z) * st.w);
+        w[1] += fabsf(ex2_approx(x1[k].y - st.x) * st.y - ex2_approx(x2[k].y - st.z) * st.w);
+        w[2] += fabsf(ex2_approx(x1[k].z - st.x) * st.y - ex2_approx(x2[k].z - st.z) * st.w);
+        w[3] += fabsf(ex2_approx(x1[k].w - st.x) * st.y - ex2_approx(x2[k].w - st.z) * st.w);
       }
     }
     const int32_t here = key;
@@ -1536,7 +1547,7 @@ diffattn_status launch_main(const FwdParams &p, const CUtensorMap (&maps)[3], in
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Geo<kD, kFp8, kNR>::kThreads);
   cfg.dynamicSmemBytes = kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
