@@ -749,8 +749,18 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
     const bool fresh = (d.flags & kFirst) != 0;  // nothing in O yet
     const float *m = sm->m[m_turn][map] + r0;
 
-    // This key's logits of the rows, in log2 units; -inf where it is masked.
-    float x[kMine];
+    // This key's products with rows kW k .. (kept in registers while they are few, else read from
+    // tensor memory again), and as logits in log2 units, -inf where the key is masked.
+    constexpr bool kKeep = kChunks == 1;
+    uint32_t raw[kW];
+    const auto load = [&](int k) {
+      tmem_load(s_at + kW * k, raw);
+      tmem_loaded(raw);
+    };
+    const auto logit = [&](int k, int e) {
+      const float x = __uint_as_float(raw[e]) * p.scale_log2;
+      return masked && d.key0 + key > rows[kW * k + e].last ? -INFINITY : x;
+    };
     bool grew = false;
     if (tid == 0) sm->bad_rows[(t + 1) % 3] = 0;
     if (!stop) {
@@ -761,34 +771,34 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
         for (int q = 0; q < kMine; ++q) l[q] = 0.f;
       }
       if (d.flags & kBad) poisoned = true;
-      grew = fresh;  // the first tile sets the references
       tc_fence_after_sync();
-      uint32_t raw[kChunks][kW];
-#pragma unroll
-      for (int k = 0; k < kChunks; ++k) tmem_load(s_at + kW * k, raw[k]);
+      float top = -INFINITY;  // how far a logit is above its reference
 #pragma unroll
       for (int k = 0; k < kChunks; ++k) {
-        tmem_loaded(raw[k]);
+        if (kW * k >= real) break;
+        load(k);
+        if (!fresh) {
+          if (masked) {
 #pragma unroll
-        for (int e = 0; e < kW; ++e) x[kW * k + e] = __uint_as_float(raw[k][e]) * p.scale_log2;
-      }
-      if (masked) {
+            for (int e = 0; e < kW; ++e) top = fmaxf(top, logit(k, e) - m[kW * k + e]);
+          } else {
 #pragma unroll
-        for (int q = 0; q < kMine; ++q)
-          if (d.key0 + key > rows[q].last) x[q] = -INFINITY;
-      }
-      if (!fresh) {
+            for (int e = 0; e < kW; ++e)
+              top = fmaxf(top, fmaf(__uint_as_float(raw[e]), p.scale_log2, -m[kW * k + e]));
+          }
+        }
+        if (p.logits != nullptr && key < keys) {
+          const int64_t bh = static_cast<int64_t>(d.b) * p.kv_heads + d.hk;
+          float *dst = p.logits +
+                       ((bh * 2 + map) * p.rows + d.item % p.row_blocks * kNR + r0 + kW * k) * p.padded +
+                       d.key0 + key;
 #pragma unroll
-        for (int q = 0; q < kMine; ++q) grew |= q < real && x[q] > m[q] + kGrowth;
+          for (int e = 0; e < kW; ++e)
+            if (kW * k + e < real && dbg_ok(d.key0 + key < p.padded, p.status, 41))
+              dst[e * p.padded] = logit(k, e);
+        }
       }
-      if (p.logits != nullptr && key < keys) {
-        const int64_t bh = static_cast<int64_t>(d.b) * p.kv_heads + d.hk;
-        float *dst = p.logits + ((bh * 2 + map) * p.rows + d.item % p.row_blocks * kNR + r0) * p.padded +
-                     d.key0 + key;
-#pragma unroll
-        for (int q = 0; q < kMine; ++q)
-          if (q < real && dbg_ok(d.key0 + key < p.padded, p.status, 41)) dst[q * p.padded] = x[q];
-      }
+      grew = fresh || top > kGrowth;  // the first tile sets the references
       // P's buffer: the product that read it last is done.
       if (t >= G::kPBufs)
         ok = mbar_wait_warp(&sm->pv_done[(t - G::kPBufs) & 1], phase<2>(t - G::kPBufs), &sm->abort,
@@ -831,10 +841,14 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
       if (*reinterpret_cast<volatile int *>(&sm->failed)) break;
       if (!stop) {
 #pragma unroll
-        for (int q = 0; q < kMine; ++q) {
-          if (q >= real) break;
-          const float y = warp_max(x[q]);
-          if (lane == 0) sm->wmax[map][quarter][r0 + q] = y;
+        for (int k = 0; k < kChunks; ++k) {
+          if (kW * k >= real) break;
+          if (!kKeep) load(k);
+#pragma unroll
+          for (int e = 0; e < kW; ++e) {
+            const float y = warp_max(logit(k, e));
+            if (lane == 0) sm->wmax[map][quarter][r0 + kW * k + e] = y;
+          }
         }
         // O moves with the reference, so the product before must be done.
         if (!fresh)
@@ -847,7 +861,9 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
           const float y = fmaxf(fmaxf(w[0][r0 + q], w[1][r0 + q]), fmaxf(w[2][r0 + q], w[3][r0 + q]));
           return fresh ? y : fmaxf(m[q], y);
         };
-        if (quarter == 0 && lane < real) sm->m[m_turn ^ 1][map][r0 + lane] = new_m(lane);
+        // Rows that are not there never grow.
+        if (quarter == 0 && lane < kMine)
+          sm->m[m_turn ^ 1][map][r0 + lane] = lane < real ? new_m(lane) : INFINITY;
         if (!fresh) {
           const uint32_t o_at =
               tmem + G::kTmemO + (seg % G::kOBufs) * G::kOCols + map * 2 * kNQ + r0;
@@ -861,7 +877,7 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
             for (int e = 0; e < kW; ++e) {
               const int q = kW * k + e;
               const float old = m[q], y = new_m(q);
-              f[e] = y == old ? 1.f : ex2_approx(old - y);
+              f[e] = q < real && y != old ? ex2_approx(old - y) : 1.f;
               moved |= q < real && y != old;
               l[q] *= f[e];
             }
@@ -905,15 +921,21 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
       if (kW * k >= real) break;
+      if (!kKeep) load(k);
       uint32_t hi[kW > 1 ? kW / 2 : 1], lo[kW > 1 ? kW / 2 : 1];
       float y[kW > 1 ? kW : 2];
       y[1] = 0.f;
 #pragma unroll
       for (int e = 0; e < kW; ++e) {
-        const float xe = x[kW * k + e];
-        if (kept_out) sm->late[seg & 1][map][back][r0 + kW * k + e] = xe;
-        y[e] = ex2_approx(xe - sm->m[m_turn][map][r0 + kW * k + e]);
-        if (masked && xe == -INFINITY) y[e] = 0.f;  // also where no key has been seen yet
+        const int q = kW * k + e;
+        const float ref = sm->m[m_turn][map][r0 + q];
+        if (masked) {
+          const float x = logit(k, e);
+          if (kept_out) sm->late[seg & 1][map][back][r0 + q] = x;
+          y[e] = x == -INFINITY ? 0.f : ex2_approx(x - ref);  // also where no key has been seen yet
+        } else {
+          y[e] = ex2_approx(fmaf(__uint_as_float(raw[e]), p.scale_log2, -ref));
+        }
         l[kW * k + e] += y[e];
       }
 #pragma unroll
