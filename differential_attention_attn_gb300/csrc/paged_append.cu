@@ -178,8 +178,11 @@ diffattn_status launch_paged_append(const diffattn_desc &desc, const diffpaged_c
   p.by_n = fast_div(p.N);
   p.by_heads = fast_div(p.kv_heads);
   p.by_page = fast_div(p.page_size);
-  const cudaError_t e = desc.d == 64 ? (fp8 ? launch<64, true>(p, stream) : launch<64, false>(p, stream))
-                                     : (fp8 ? launch<128, true>(p, stream) : launch<128, false>(p, stream));
+  cudaError_t e;
+  if (desc.d == 64)
+    e = fp8 ? launch<64, true>(p, stream) : launch<64, false>(p, stream);
+  else
+    e = fp8 ? launch<128, true>(p, stream) : launch<128, false>(p, stream);
   return e == cudaSuccess ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
 }
 

@@ -191,7 +191,8 @@ __global__ void __launch_bounds__(kSelectThreads) diffpaged_select_kernel(const 
   __syncthreads();
   const bool before = lane < warp && lane < kSelectWarps;
   uint32_t equal_before = __reduce_add_sync(0xffffffffu, before ? scratch[1][lane] : 0);
-  uint32_t at = __reduce_add_sync(0xffffffffu, before ? scratch[0][lane] : 0) + min(need, equal_before);
+  uint32_t at = __reduce_add_sync(0xffffffffu, before ? scratch[0][lane] : 0) +
+                min(need, equal_before);
   int2 *list = p.list + static_cast<int64_t>(item) * p.keep;
   const uint32_t lower = (1u << lane) - 1;
   uint32_t in_place = 0xFFFFFFFFu;  // the first position that does not stay

@@ -1,374 +1,18 @@
-// diffpaged_fwd: the differential head's forward of a few new tokens per
-// sequence over a paged key/value cache.
-//
-// The mathematics.  The rows of one (sequence, key/value head) are r = (token
-// i, query head g of the group), R = N * G of them, all reading the same keys:
-//   x_m[r, j] = q_m[r] . k_m[j] / sqrt(d),  map_m = softmax_j(x_m),  m = 1, 2
-//   o[r] = sum_j (map1[r, j] - lambda_h map2[r, j]) v[j], then the head norm.
-// Each map is an ordinary softmax, so the keys are taken in one pass with a
-// running reference maximum and sum per row and map (fp32, log2 units), and
-// ranges of keys done by different CTAs join exactly: with M = max m_s,
-//   O = sum_s 2^(m_s - M) O_s,  l = sum_s 2^(m_s - M) l_s,  o = O / l.
-//
-// What bounds it: each key is read once (8 d bytes in bf16) for 12 d R
-// multiply-adds, so for the R <= 32 rows of a block this is HBM-bound, and
-// everything here serves to keep loads in flight.
-//
-//   - Work is counted in tiles of 128 keys over all sequences and heads, and
-//     every CTA (one per SM) takes the same number of consecutive tiles,
-//     found from kv_len on the device; a ragged batch is balanced and a graph
-//     replays with new lengths.  Items cut by a CTA boundary leave partial
-//     states, which a second kernel (launched dependent on the first) joins.
-//     With few tiles in all, one CTA takes each item and nothing is joined.
-//   - One warp issues TMA copies of page pieces (16 to 64 rows, by the page
-//     size) into a ring of 32 KB buffers: the keys of both maps (d = 64), one
-//     map's keys or half the value columns (d = 128).
-//   - One warp issues the products, keys and value columns on the 128-row side
-//     of tcgen05.mma, where the tile fills it, and the few rows r on the other:
-//       S_m^T = K_m Q_m^T            (128 keys x rows)
-//       O^T  += V^T [P1 | P2]^T      (128 value columns x rows of both maps)
-//     so V is read once for both maps and O stays in tensor memory.
-//   - Eight warps do the softmax, a thread per key and map.  The reference
-//     maximum moves only when some logit passes it by 2^8: one barrier with a
-//     vote per tile instead of a reduction over the keys.
-//   - P enters the second product as bf16 hi + lo side by side (relative
-//     error 2^-17): o1 - lambda o2 cancels and the head norm scales the
-//     difference back up, so a plain bf16 P would show; the wider product is
-//     hidden behind the loads.
+// diffpaged_fwd: the plan, the launch and the second kernel (the main kernel is
+// in paged_fwd.cuh).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cmath>
 #include <cstdint>
 
 #include "debug_check.cuh"
 #include "paged.h"
+#include "paged_fwd.cuh"
 #include "ptx.cuh"
 
 namespace diffattn {
 namespace {
-
-constexpr int kTile = kPagedTile;
-// Warps 0-2 issue, those from 4 on (a multiple of four, for their quarters of tensor memory) do the
-// softmax.
-constexpr int kMmaWarp = 0, kKeyWarp = 1, kValueWarp = 2, kSoftmaxWarp = 4;
-constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr uint64_t kDrainNs = 200000000ull;
-constexpr float kGrowth = 8.f;  // log2 units a logit may pass the reference maximum by
-constexpr int kMaxBad = 16;     // new tokens of a call, so more than keys that only some of them see
-constexpr int kRing = 8;        // tile descriptors; fewer tiles are between load and epilogue
-constexpr int kBoxBytes = kTile * 128;   // 64 bf16 columns of a tile
-constexpr int kSlotBytes = 2 * kBoxBytes;
-constexpr int kItemCost = 2;    // steps, see Shares
-constexpr float kLog2e = 1.4426950408889634f;
-
-enum : int32_t { kFirst = 1, kLast = 2, kStop = 4, kBad = 8, kDirect = 16 };
-
-struct TileDesc {
-  int32_t b, hk, real, key0;  // real: rows of the block
-  int32_t len, flags, slot, item;
-  int32_t steps, pad[3];  // 16-key steps of the second product (one for an idle sequence)
-};
-
-struct FwdParams {
-  const void *q1, *q2;
-  const void *v_pages;
-  const float *lambda, *norm_w;
-  __nv_bfloat16 *out;
-  const int32_t *page_table, *kv_len;
-  int32_t *status;
-  diffattn_strides q1s, q2s, outs, vs;
-  int32_t B, H, N, kv_heads, group, rows;  // rows = N * group
-  int32_t num_pages, max_pages, page_size, piece_rows;
-  int32_t row_blocks, causal, headnorm, whole;
-  FastDiv by_page, by_group;  // page_size, group
-  float eps, out_scale, scale_log2;
-  // Workspace (see PagedFwdPlan): partial O [2 C][2][NR][2 d] and their (m, l), and for accumulate
-  // whole items' (m, l) and all logits.
-  float *part;
-  float2 *part_ml;
-  float2 *item_ml;
-  float *logits;  // [B * kv_heads][2][rows][padded], log2 units, or null
-  int64_t padded;
-  float *weights;
-};
-
-// One row of a segment, as the softmax warps need it.
-struct RowInfo {
-  int32_t last;   // the last key that it sees, -1 for none
-  int32_t head;   // query head
-  int64_t out;    // element offset of its output
-};
-
-// kNR: rows of a block (1, 2, 4, 8, 16 or 32), padded to kNQ = 8, 16 or 32 in the products.
-template <int kD, bool kFp8, int kNR>
-struct Geo {
-  static constexpr int kNQ = kNR < 8 ? 8 : kNR;
-  // Softmax threads: one per key and map, two from 8 rows on, with half of the rows each.
-  static constexpr int kSets = kNR < 8 ? 1 : 2;
-  static constexpr int kConsumers = 2 * kTile * kSets;
-  static constexpr int kThreads = 32 * kSoftmaxWarp + kConsumers;
-  static constexpr int kMine = kNR / kSets;                         // rows of a thread
-  static constexpr int kW = kMine < 8 ? kMine : 8;                  // of them at a time
-  static constexpr int kChunks = kMine / kW;
-  static constexpr int kKeyRow = kFp8 ? kD : 2 * kD;                // bytes
-  static constexpr int kKeyBox = kKeyRow < 128 ? kKeyRow : 128;     // bytes of a key box row
-  static constexpr int kKeySlots = kKeyRow <= 128 ? 1 : 2;          // both maps in one, or each its own
-  static constexpr int kValSlots = kD / 64;                         // 128 value columns each
-  static constexpr int kTileSlots = kKeySlots + kValSlots;
-  static constexpr int kNS = kNQ < 16 ? 16 : kNQ;                   // columns of S (N is at least 16)
-  static constexpr int kQBytes = kNS * kKeyRow;                     // one map's rows
-  // P, N-major: a row of 4 kNQ bf16 per key (map 1 hi, lo, map 2 hi, lo), in blocks of at most
-  // 128 bytes.
-  static constexpr int kPCols = 4 * kNQ;
-  static constexpr int kPRow = kPCols * 2 < 128 ? kPCols * 2 : 128;
-  static constexpr int kPBytes = kTile * kPCols * 2;
-  static constexpr int kPBufs = kNQ == 32 ? 1 : 2;
-  static constexpr int kOCols = kValSlots * kPCols;
-  static constexpr int kOBufs = kNQ == 32 && kD == 128 ? 1 : 2;
-  static constexpr int kTmemO = 4 * kNS;                            // after two buffers of two S
-  static constexpr int kTmemUsed = kTmemO + kOBufs * kOCols;
-  static constexpr int kTmemCols = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
-  static_assert(kTmemUsed <= 512, "tensor memory");
-};
-
-template <int kNR>
-struct Ctrl {
-  float m[2][2][kNR];  // reference maxima of both maps' rows, two copies in turn
-  float wmax[2][4][kNR];
-  float lsum[2][2][4][kNR];  // by segment parity
-  float rsum[2][4][kNR];
-  float late[2][2][kMaxBad][kNR];  // by segment parity: logits of keys kept out of the product,
-  float ref[2][2][kNR];         // and rows' references, by segment parity
-  TileDesc ring[kRing], done[2];  // done: a segment's last tile, by segment parity
-  RowInfo rows[kRing][kNR];  // by segment
-  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_empty[2], drain;
-  uint32_t bad_rows[3];
-  uint32_t tmem;
-  int abort, failed;
-};
-
-template <int kD, bool kFp8, int kNR>
-struct Layout {
-  using G = Geo<kD, kFp8, kNR>;
-  static constexpr int kP = 0;
-  static constexpr int kQ = kP + G::kPBufs * G::kPBytes;
-  static constexpr int kFixed = kQ + 4 * G::kQBytes;  // then the ring, then Ctrl
-  static constexpr int kRoom =
-      227 * 1024 - 1024 - static_cast<int>(sizeof(Ctrl<kNR>)) - kFixed;
-  // The ring of keys and that of values: each is filled by a warp of its own and emptied in order.
-  static constexpr int kSlots = kRoom / kSlotBytes < 6 ? kRoom / kSlotBytes : 6;
-  static constexpr int kShare = kSlots * G::kKeySlots / G::kTileSlots;
-  static constexpr int kKeyRing = kShare < G::kKeySlots ? G::kKeySlots : kShare;
-  static constexpr int kValRing = kSlots - kKeyRing;
-  static_assert(kValRing >= G::kValSlots, "one tile must fit");
-  static constexpr int kKeyAt = kFixed, kValAt = kKeyAt + kKeyRing * kSlotBytes;
-  static constexpr int kCtrl = kFixed + kSlots * kSlotBytes;
-  static constexpr int kBytes = 1024 + kCtrl + static_cast<int>(sizeof(Ctrl<kNR>));
-};
-
-__device__ __forceinline__ int32_t units_of(int32_t len, int32_t most) {
-  if (len <= 0 || len > most) return 1;  // an idle or invalid sequence still has rows to write
-  return (len + kTile - 1) / kTile;
-}
-
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
-}
-
-// One arrival on the barrier when this thread's cp.async copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
-}
-__device__ __forceinline__ void fence_async_proxy() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// tcgen05.mma of a converged warp (one elected lane issues).  The operands' descriptors come as
-// their low words (start address, leading-dimension offset), which advance, and their high words
-// (stride-dimension offset, layout), which do not: two 32-bit additions a product.
-template <bool kFp8>
-__device__ __forceinline__ void umma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t a_hi,
-                                     uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
-  if (kFp8)
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %4};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n\t}" ::"r"(d),
-        "r"(a_lo), "r"(b_lo), "r"(a_hi), "r"(b_hi), "r"(idesc), "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %4};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
-        "r"(a_lo), "r"(b_lo), "r"(a_hi), "r"(b_hi), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-__device__ __forceinline__ uint32_t low(uint64_t x) { return static_cast<uint32_t>(x); }
-__device__ __forceinline__ uint32_t high(uint64_t x) { return static_cast<uint32_t>(x >> 32); }
-// Descriptor of rows of 64 bytes with 64-byte swizzle (8-row groups 512 bytes apart): K-major, or
-// MN-major operands at most 32 elements wide.
-__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (1ull << 16) |
-         (static_cast<uint64_t>(512 >> 4) << 32) | (1ull << 46) | (4ull << 61);
-}
-
-// kN consecutive 32-bit tensor-memory columns of the thread's lane; valid after tmem_loaded().
-template <int kN>
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[kN]) {
-  static_assert(kN == 1 || kN == 2 || kN == 4 || kN == 8, "columns");
-  if constexpr (kN == 1)
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[0]) : "r"(addr) : "memory");
-  else if constexpr (kN == 2)
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];"
-                 : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
-  else if constexpr (kN == 4)
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-  else
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                   "=r"(r[6]), "=r"(r[7]) : "r"(addr) : "memory");
-}
-// Waits for the thread's loads, passing r through so that no use moves before it.
-template <int kN>
-__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[kN]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]) : : "memory");
-#pragma unroll
-  for (int k = 1; k < kN; ++k) asm volatile("" : "+r"(r[k]));
-}
-template <int kN>
-__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[kN]) {
-  if constexpr (kN == 1)
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr), "r"(r[0]) : "memory");
-  else if constexpr (kN == 2)
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(r[0]),
-                 "r"(r[1]) : "memory");
-  else if constexpr (kN == 4)
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
-                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
-  else
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-        : "memory");
-}
-
-// Phase parity of the n-th use (from 0) of buffer n % kBufs.
-template <int kBufs>
-__device__ __forceinline__ uint32_t phase(uint32_t n) {
-  return (n / kBufs) & 1;
-}
-
-// Work is laid out on a line: kItemCost steps that hold nothing for each item, then its tiles, a
-// step each.  (A segment costs its CTA about as much as two tiles beside its tiles: a CTA with ten
-// short items took 91 us where the others took 65.)  `ctas` shares cut the line into `each` or (the
-// first `more`) each + 1 steps.  Fewer than 2^31 steps (checked at launch).
-struct Shares {
-  uint32_t ctas, each, more;
-  __device__ __forceinline__ uint32_t begin(uint32_t cta) const {
-    return cta * each + min(cta, more);
-  }
-  __device__ __forceinline__ uint32_t cta_of(uint32_t step) const {
-    const uint32_t border = more * (each + 1);
-    return step < border ? step / (each + 1) : more + (step - border) / each;
-  }
-};
-__device__ __forceinline__ Shares cut_line(uint32_t steps, uint32_t ctas) {
-  Shares s;
-  s.ctas = min(ctas, steps);
-  s.each = steps / s.ctas;
-  s.more = steps - s.each * s.ctas;
-  return s;
-}
-
-// The CTA's share: the item (b, hk, rb) that it begins in, the steps from that item's first one to
-// the share's begin and end, and the item's tiles.
-struct Share {
-  Shares all;
-  uint32_t begin;     // of the share
-  int32_t off, end;   // from the item's first step; end = off: nothing
-  int32_t b, hk, rb, len, units;
-};
-
-// CTA `cta`'s share of `ctas` CTAs (one warp, uniform).
-__device__ __forceinline__ Share find_share(const FwdParams &p, uint32_t cta, uint32_t ctas) {
-  const int lane = threadIdx.x % 32;
-  const int32_t most = p.max_pages * p.page_size;
-  Share s = {{1, 1, 0}, 0, 0, 0, 0, 0, 0, 0, 1};
-  const uint32_t heads = p.kv_heads * p.row_blocks;  // items of a sequence
-  if (p.whole) {
-    s.b = cta / heads;
-    const uint32_t item = cta - s.b * heads;
-    s.hk = item / p.row_blocks;
-    s.rb = item - s.hk * p.row_blocks;
-    s.len = __ldg(p.kv_len + s.b);
-    s.units = units_of(s.len, most);
-    s.end = kItemCost + s.units;
-    return s;
-  }
-  uint32_t total = 0;
-  int32_t last[4];  // lengths of the last 128 sequences, four a lane
-#pragma unroll 1
-  for (int32_t b0 = 0; b0 < p.B; b0 += 128) {
-    uint32_t u = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int32_t x = b0 + 32 * k + lane;
-      last[k] = x < p.B ? __ldg(p.kv_len + x) : 0;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (b0 + 32 * k + lane < p.B) u += kItemCost + units_of(last[k], most);
-    total += __reduce_add_sync(0xffffffffu, u);
-  }
-  s.all = cut_line(total * heads, ctas);
-  if (cta < s.all.ctas) {
-    s.begin = s.all.begin(cta);
-    uint32_t left = s.begin;  // steps before the share, counted down sequence by sequence
-#pragma unroll 1
-    for (int32_t b0 = 0; b0 < p.B; b0 += 32) {
-      const int32_t x = b0 + lane;
-      const int32_t len = p.B <= 32 ? last[0] : x < p.B ? __ldg(p.kv_len + x) : 0;
-      const uint32_t u = x < p.B ? (kItemCost + units_of(len, most)) * heads : 0;
-      uint32_t incl = u;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
-      if (left < all) {
-        const int at = __ffs(__ballot_sync(0xffffffffu, left < incl)) - 1;
-        s.b = b0 + at;
-        left -= __shfl_sync(0xffffffffu, incl - u, at);
-        s.len = __shfl_sync(0xffffffffu, len, at);
-        break;
-      }
-      left -= all;
-    }
-    s.units = units_of(s.len, most);
-    const uint32_t item = left / (kItemCost + s.units);
-    s.off = static_cast<int32_t>(left - item * (kItemCost + s.units));
-    s.end = s.off + static_cast<int32_t>(s.all.each + (cta < s.all.more ? 1 : 0));
-    s.hk = item / p.row_blocks;
-    s.rb = item - s.hk * p.row_blocks;
-  }
-  return s;
-}
 
 // The parts that the item whose steps begin at `start` is cut into: that of the CTA c0 with its
 // first tile is in slot 2 c0 + 1 where its share begins before the item and in 2 c0 otherwise, the
@@ -383,824 +27,6 @@ __device__ __forceinline__ Parts parts_of(const Shares &all, uint32_t start, uin
   const uint32_t c0 = all.cta_of(start + kItemCost);
   return {static_cast<int32_t>(2 * c0 + (all.begin(c0) < start ? 1 : 0)),
           static_cast<int32_t>(all.cta_of(start + kItemCost + units - 1) - c0 + 1)};
-}
-
-// ---------------------------------------------------------------------------
-// The load warps, one for the keys (with the tiles' descriptions and the q rows) and one for the
-// values: a copy takes one thread 80 to 130 cycles to issue, and a tile in pages of 16 rows has 32
-// of them, which one warp issues more slowly than HBM delivers.
-// ---------------------------------------------------------------------------
-template <int kD, bool kFp8, int kNR, bool kKeys>
-__device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap *mk1,
-                                          const CUtensorMap *mk2, const CUtensorMap *mv,
-                                          uint8_t *smem, Ctrl<kNR> *sm, const Share &share) {
-  using G = Geo<kD, kFp8, kNR>;
-  using L = Layout<kD, kFp8, kNR>;
-  const int lane = threadIdx.x % 32;
-  const int32_t most = p.max_pages * p.page_size;
-  int32_t b = share.b, hk = share.hk, rb = share.rb, len = share.len, units = share.units;
-  int32_t tile = max(0, share.off - kItemCost);  // of the current item
-  int32_t end = share.end - kItemCost;           // the share's end, in tiles of that item
-  // Each slot is two boxes wide and up to eight page pieces high: a lane each.
-  const int piece = lane / 2, box = lane % 2;
-  const int first_row = piece * p.piece_rows;
-  const bool piece_ok = first_row < kTile;
-  const auto page_of = [&](int32_t t) {  // this lane's page of tile t of the current sequence
-    const int32_t key = t * kTile + first_row;
-    return piece_ok && key < len && len <= most
-               ? __ldg(p.page_table + static_cast<int64_t>(b) * p.max_pages + p.by_page.div(key))
-               : 0;
-  };
-  bool ok = true;
-  uint32_t it = 0;     // tiles
-  uint32_t seg = 0;    // segments (the share's parts of items)
-  int32_t seg_start = tile;
-  int32_t slot = 2 * blockIdx.x;
-  // To the next item with a tile in the share (the first may be cut before its tiles).
-  const auto next_item = [&] {
-    end -= units + kItemCost;
-    tile = 0;
-    if (++rb == p.row_blocks) {
-      rb = 0;
-      if (++hk == p.kv_heads) {
-        hk = 0;
-        ++b;
-        if (end > 0) {
-          len = __ldg(p.kv_len + b);
-          units = units_of(len, most);
-        }
-      }
-    }
-  };
-  int32_t id = tile < end ? page_of(tile) : 0;
-  // Read once (by one row block), the pages leave L2 before anything else does.
-  const uint64_t policy = p.row_blocks == 1 ? l2_evict_first() : l2_evict_normal();
-  constexpr int kPerTile = kKeys ? G::kKeySlots : G::kValSlots;
-  constexpr int kSlots = kKeys ? L::kKeyRing : L::kValRing;
-  uint64_t *full = kKeys ? sm->k_full : sm->v_full;
-  uint64_t *empty = kKeys ? sm->k_empty : sm->v_empty;
-  uint8_t *ring = smem + (kKeys ? L::kKeyAt : L::kValAt) + box * kBoxBytes;
-  const auto freed = [&](uint32_t c) {  // the slot of use c is free again
-    return c < kSlots ||
-           mbar_wait_warp(&empty[c % kSlots], phase<kSlots>(c - kSlots), &sm->abort, kWaitNs);
-  };
-#pragma unroll 1
-  for (; ok && tile < end; ++it) {
-    const bool valid_len = len >= 0 && len <= most;
-    const bool seg_last = tile + 1 == units || tile + 1 == end;
-    const int32_t page = id, head = hk, key0 = tile * kTile;
-    const int32_t tile_len = valid_len ? len : 0;
-    const int32_t keys = max(0, min(kTile, tile_len - key0));  // 0 for an idle sequence
-    const bool have = piece_ok && first_row < keys;
-    const bool bad_id = have && static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages);
-    const int32_t row = p.by_page.mod(key0 + first_row);
-    const int32_t z = bad_id ? 0 : page;
-    const int32_t rows = (keys + p.piece_rows - 1) & -p.piece_rows;
-    const bool seg_first = tile == seg_start;
-    TileDesc d;
-    int32_t q_row = 0;
-    if (kKeys) {
-      const bool bad = __any_sync(0xffffffffu, bad_id) || !valid_len;
-      d.b = b;
-      d.hk = hk;
-      d.real = min(kNR, p.rows - rb * kNR);
-      d.key0 = key0;
-      d.len = tile_len;
-      d.slot = slot;
-      d.flags = (seg_first ? kFirst : 0) | (seg_last ? kLast : 0) | (bad ? kBad : 0) |
-                (seg_start == 0 && tile + 1 == units ? kDirect : 0);
-      d.item = (b * p.kv_heads + hk) * p.row_blocks + rb;
-      d.steps = max(1, (keys + 15) / 16);
-      q_row = rb * kNR;
-      if (bad && lane == 0) report_bad_page(p.status);
-    }
-    // Move on; the next tile's page numbers are fetched while buffers are awaited.
-    if (seg_last) {
-      seg_start = 0;
-      slot = 2 * blockIdx.x + 1;
-    }
-    if (++tile == units) next_item();
-    if (tile < end) id = page_of(tile);
-#pragma unroll 1
-    for (int k = 0; k < kPerTile; ++k) {
-      const uint32_t c = it * kPerTile + k;
-      const int s = c % kSlots;
-      if (!(ok = freed(c))) break;
-      // The copies first; their barrier's phase ends no sooner than the arrival below them.
-      const int row_bytes = kKeys ? G::kKeyBox : 128;
-      if (have) {
-        const CUtensorMap *map = !kKeys ? mv : (G::kKeySlots == 1 ? box : k) ? mk2 : mk1;
-        const int x = !kKeys ? 128 * k + 64 * box : G::kKeySlots == 1 ? 0 : 64 * box;
-        tma_load_4d_hint(ring + s * kSlotBytes + first_row * row_bytes, map, &full[s], x, row, head,
-                         z, policy);
-      }
-      if (kKeys && k == 0) {
-        if (lane == 0) sm->ring[it % kRing] = d;
-        if (seg_first && lane < kNR) {  // the segment's rows
-          const int32_t r = q_row + lane;
-          const int32_t i = p.by_group.div(r), pos = tile_len - p.N + i;
-          RowInfo info;
-          info.last = r >= p.rows || pos < 0 ? -1 : p.causal ? pos : tile_len - 1;
-          info.head = d.hk * p.group + r - i * p.group;
-          info.out = d.b * p.outs.b + info.head * p.outs.h + i * p.outs.n;
-          sm->rows[seg % kRing][lane] = info;
-        }
-      }
-      __syncwarp();
-      if (lane == 0) {
-        if (rows > 0)
-          mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(rows) * 2 * row_bytes);
-        else
-          mbar_arrive(&full[s]);
-      }
-    }
-    // The segment's q rows: 16-byte units into the swizzled operand layout.
-    if (kKeys && ok && seg_first) {
-      const uint32_t qb = seg & 1;
-      if (seg >= 2 &&
-          !(ok = mbar_wait_warp(&sm->q_empty[qb], phase<2>(seg - 2), &sm->abort, kWaitNs)))
-        break;
-      constexpr int kUnits = G::kKeyRow / 16;
-#pragma unroll 1
-      for (int x = lane; x < 2 * d.real * kUnits; x += 32) {
-        const int map = x >= d.real * kUnits, y = x - map * d.real * kUnits;
-        const int q = y / kUnits, u = y % kUnits;
-        const int r = q_row + q;
-        const int i = p.by_group.div(r), h = d.hk * p.group + r - i * p.group;
-        const diffattn_strides &qs = map ? p.q2s : p.q1s;
-        const int64_t at = d.b * qs.b + h * qs.h + i * qs.n;
-        const uint8_t *src =
-            static_cast<const uint8_t *>(map ? p.q2 : p.q1) + at * (kFp8 ? 1 : 2) + 16 * u;
-        uint32_t off;
-        if (G::kKeyRow == 64)
-          off = q * 64 + ((u ^ ((q >> 1) & 3)) << 4);
-        else
-          off = (u / 8) * (G::kNS * 128) + q * 128 + (((u % 8) ^ (q & 7)) << 4);
-        cp_async16(smem_u32(smem + L::kQ + (2 * qb + map) * G::kQBytes) + off, src);
-      }
-      cp_async_arrive(&sm->q_full[qb]);
-      ++seg;
-    }
-  }
-  // The end mark takes the next slot's turn; then the copies still in flight
-  // are awaited (bounded), so that none lands after the CTA is gone.
-  uint32_t uses = it * kPerTile;
-  if (kKeys && ok && freed(uses)) {
-    if (lane == 0) {
-      sm->ring[it % kRing].flags = kStop;
-      mbar_arrive(&full[uses % kSlots]);
-    }
-    ++uses;
-  }
-  if (kKeys) asm volatile("cp.async.wait_all;" ::: "memory");
-  if (lane == 0) {
-    volatile int never = 0;
-    for (uint32_t c = uses > kSlots ? uses - kSlots : 0; c < uses; ++c)
-      mbar_wait(&full[c % kSlots], phase<kSlots>(c), &never, kDrainNs);
-  }
-}
-
-// ---------------------------------------------------------------------------
-// The product warp.
-// ---------------------------------------------------------------------------
-template <int kD, bool kFp8, int kNR>
-__device__ __forceinline__ void mma_warp(const FwdParams &p, uint8_t *smem, Ctrl<kNR> *sm) {
-  using G = Geo<kD, kFp8, kNR>;
-  using L = Layout<kD, kFp8, kNR>;
-  const int lane = threadIdx.x % 32;
-  const uint32_t tmem = sm->tmem;
-  constexpr uint32_t kIdS = kFp8 ? (1u << 4) | ((G::kNS >> 3) << 17) | ((128u >> 4) << 24)
-                                 : idesc_bf16_f32(128, G::kNS, false);
-  constexpr uint32_t kIdO = idesc_bf16_f32(128, G::kPCols, true) | (1u << 15);  // both MN-major
-  const auto wait = [&](uint64_t *bar, uint32_t parity) {
-    return mbar_wait_warp(bar, parity, &sm->abort, kWaitNs);
-  };
-  const auto ready = [&](uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_test(bar, parity));
-  };
-
-  // Tile t's turn in O and tile n's in S; n runs at most one ahead, where its keys are there.
-  // The tests see the right phase: the slot's use before was consumed by an earlier tile.
-  uint32_t t = 0, n = 0, segs = 0, o_segs = 0;
-  int32_t s_flags = 0, o_flags = 0, ahead_flags = 0;  // of S's last tile; of tiles t, t + 1
-  int32_t o_steps = 0, ahead_steps = 0;               // 16-key steps with keys in them
-  uint64_t since = 0;
-#pragma unroll 1
-  while (true) {
-    const uint32_t cs = n * G::kKeySlots;
-    if (n <= t + 1 && !(s_flags & kStop) &&
-        ready(&sm->k_full[cs % L::kKeyRing], phase<L::kKeyRing>(cs))) {
-      s_flags = *reinterpret_cast<volatile int32_t *>(&sm->ring[n % kRing].flags);
-      (n == t ? o_flags : ahead_flags) = s_flags;
-      (n == t ? o_steps : ahead_steps) =
-          *reinterpret_cast<volatile int32_t *>(&sm->ring[n % kRing].steps);
-      if (s_flags & kStop) {
-        if (lane == 0) mbar_arrive(&sm->s_full[n & 1]);
-      } else {
-        if (s_flags & kFirst) {
-          if (!wait(&sm->q_full[segs & 1], phase<2>(segs))) break;
-          fence_async_proxy();  // the q rows came by ordinary copies
-          ++segs;
-        }
-        tc_fence_after_sync();
-        const uint32_t qb = (segs - 1) & 1;
-#pragma unroll 1
-        for (int map = 0; map < 2; ++map) {
-          const uint32_t c = cs + (G::kKeySlots == 2 ? map : 0);
-          if (G::kKeySlots == 2 && map == 1 &&
-              !wait(&sm->k_full[c % L::kKeyRing], phase<L::kKeyRing>(c)))
-            break;
-          const uint32_t k_at = smem_u32(smem + L::kKeyAt + (c % L::kKeyRing) * kSlotBytes) +
-                                (G::kKeySlots == 1 ? map * kBoxBytes : 0);
-          const uint32_t q_at = smem_u32(smem + L::kQ + (2 * qb + map) * G::kQBytes);
-          const uint32_t acc = tmem + (n & 1) * 2 * G::kNS + map * G::kNS;
-          const uint64_t a = G::kKeyRow == 64 ? smem_desc_sw64(k_at) : smem_desc_sw128(k_at, 16, 1024);
-          const uint64_t b = G::kKeyRow == 64 ? smem_desc_sw64(q_at) : smem_desc_sw128(q_at, 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < G::kKeyRow / 32; ++kk)  // 32 bytes of depth each
-            umma<kFp8>(acc, low(a) + (kk / 4) * (kBoxBytes / 16) + 2 * (kk % 4),
-                       low(b) + (kk / 4) * (G::kNS * 8) + 2 * (kk % 4), high(a), high(b), kIdS,
-                       kk > 0);
-          if (G::kKeySlots == 2 || map == 1) umma_commit_warp(&sm->k_empty[c % L::kKeyRing]);
-        }
-        if (*reinterpret_cast<volatile int *>(&sm->abort)) break;
-        umma_commit_warp(&sm->s_full[n & 1]);
-        if (s_flags & kLast) umma_commit_warp(&sm->q_empty[qb]);
-      }
-      ++n;
-      since = 0;
-    }
-    if (n > t && (o_flags & kStop)) break;
-    if (n > t && ready(&sm->p_full[t & 1], phase<2>(t))) {
-      if (o_flags & kFirst) {
-        // O of the segment before last (this buffer) has been read.
-        if (o_segs >= G::kOBufs &&
-            !wait(&sm->o_empty[o_segs % G::kOBufs], phase<G::kOBufs>(o_segs - G::kOBufs)))
-          break;
-        ++o_segs;
-      }
-      const uint32_t o_at = tmem + G::kTmemO + ((o_segs - 1) % G::kOBufs) * G::kOCols;
-      const uint32_t p_at = smem_u32(smem + L::kP + (t % G::kPBufs) * G::kPBytes);
-      bool ok = true;
-#pragma unroll 1
-      for (int k = 0; k < G::kValSlots; ++k) {
-        const uint32_t c = t * G::kValSlots + k;
-        if (!(ok = wait(&sm->v_full[c % L::kValRing], phase<L::kValRing>(c)))) break;
-        tc_fence_after_sync();
-        const uint64_t v = smem_desc_sw128(
-            smem_u32(smem + L::kValAt + (c % L::kValRing) * kSlotBytes), kBoxBytes, 1024);
-        const uint64_t w = G::kPRow == 64 ? smem_desc_sw64(p_at)
-                                          : smem_desc_sw128(p_at, kTile * 128, 1024);
-#pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)  // 16 keys each
-          if (kk < o_steps)
-            umma<false>(o_at + k * G::kPCols, low(v) + 128 * kk, low(w) + G::kPRow * kk, high(v),
-                        high(w), kIdO, !(o_flags & kFirst) || kk > 0);
-        umma_commit_warp(&sm->v_empty[c % L::kValRing]);
-      }
-      if (!ok) break;
-      umma_commit_warp(&sm->pv_done[t & 1]);
-      o_flags = ahead_flags;
-      o_steps = ahead_steps;
-      ++t;
-      since = 0;
-      continue;
-    }
-    // Nothing was ready: bounded, like every wait.
-    if (*reinterpret_cast<volatile int *>(&sm->abort)) break;
-    if (since == 0) {
-      since = globaltimer_ns();
-    } else if (globaltimer_ns() - since > kWaitNs) {
-      *reinterpret_cast<volatile int *>(&sm->abort) = 1;
-      break;
-    }
-  }
-  __syncwarp();
-  // Never free tensor memory under a running product.
-  umma_commit_warp(&sm->drain);
-  volatile int never = 0;
-  mbar_wait_warp(&sm->drain, 0, &never, kDrainNs);
-}
-
-// ---------------------------------------------------------------------------
-// The softmax warps.  Warp w: map w / 4; its lanes are keys (then value
-// columns) 32 (w % 4) + lane of a tile, as tensor memory gives them to it.
-// ---------------------------------------------------------------------------
-template <int kD, bool kFp8, int kNR>
-__device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem, Ctrl<kNR> *sm) {
-  using G = Geo<kD, kFp8, kNR>;
-  using L = Layout<kD, kFp8, kNR>;
-  constexpr int kNQ = G::kNQ, kW = G::kW, kChunks = G::kChunks, kMine = G::kMine;
-  constexpr int kConsumers = G::kConsumers;
-  constexpr int kVUnits = kD / 4;  // 16-byte units of a value row
-  const int tid = threadIdx.x - 32 * kSoftmaxWarp, warp = tid / 32, lane = tid % 32;
-  const int group = warp / 4, quarter = warp % 4;
-  const int map = group & 1, r0 = (group >> 1) * kMine;  // rows r0 .. r0 + kMine - 1
-  const int key = 32 * quarter + lane;  // of the tile
-  const uint32_t tmem = sm->tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-  const auto v_row = [&](uint32_t t, int row, int u) {  // unit u of value row `row` of tile t
-    const uint32_t c = t * G::kValSlots + u / 16;
-    return reinterpret_cast<uint4 *>(smem + L::kValAt + (c % L::kValRing) * kSlotBytes +
-                                     ((u / 8) % 2) * kBoxBytes + row * 128 + (u % 8) * 16);
-  };
-
-  float l[kMine];
-  int m_turn = 0;
-  bool poisoned = false, healthy = true;
-  uint32_t late = 0, seg = 0;
-  // A segment's end waits for its last product, so it is done after the next tile's P.
-  bool pending = false, done_poisoned = false;
-  uint32_t done_late = 0;
-  // What the keys kept out of the product add to column `col` of row q of both maps.
-  const auto late_sums = [&](int q, int col) {
-    float2 y = make_float2(0.f, 0.f);
-    const int parity = (seg - 1) & 1;
-    const TileDesc &done = sm->done[parity];
-#pragma unroll 1
-    for (uint32_t rest = done_late; rest; rest &= rest - 1) {
-      const int back = __ffs(rest) - 1;
-      const int32_t pos = done.len - 1 - back;
-      const int32_t page =
-          p.page_table[static_cast<int64_t>(done.b) * p.max_pages + p.by_page.div(pos)];
-      if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) continue;
-      const float v = __bfloat162float(
-          static_cast<const __nv_bfloat16 *>(p.v_pages)[page * p.vs.b + done.hk * p.vs.h +
-                                                        p.by_page.mod(pos) * p.vs.n + col]);
-      const float x1 = sm->late[parity][0][back][q], x2 = sm->late[parity][1][back][q];
-      if (x1 != -INFINITY) y.x += ex2_approx(x1 - sm->ref[parity][0][q]) * v;
-      if (x2 != -INFINITY) y.y += ex2_approx(x2 - sm->ref[parity][1][q]) * v;
-    }
-    return y;
-  };
-#pragma unroll 1
-  for (uint32_t t = 0;; ++t) {
-    bool ok = mbar_wait_warp(&sm->s_full[t & 1], phase<2>(t), &sm->abort, kWaitNs);
-    TileDesc d = {};
-    if (ok) d = sm->ring[t % kRing];
-    const bool stop = !ok || (d.flags & kStop) != 0;
-    const int32_t lim_min = p.causal ? d.len - p.N : d.len - 1;  // of a row that sees anything
-    const bool masked = d.key0 + kTile - 1 > lim_min;
-    const int32_t keys = d.len - d.key0;  // valid rows of the tile if below kTile
-    const bool mixed = p.causal && p.N > 1 && masked;  // some rows see keys that others do not
-    const int real = kNR == 1 ? 1 : min(d.real - r0, kMine);  // rows of this thread (0 or less: none)
-    const RowInfo *rows = sm->rows[seg % kRing] + r0;
-    const uint32_t s_at = tmem + (t & 1) * 2 * G::kNS + map * G::kNS + r0;
-
-    const bool fresh = (d.flags & kFirst) != 0;  // nothing in O yet
-    const float *m = sm->m[m_turn][map] + r0;
-
-    // This key's products with rows kW k .. (kept in registers while they are few, else read from
-    // tensor memory again), and as logits in log2 units, -inf where the key is masked.
-    constexpr bool kKeep = kChunks == 1;
-    uint32_t raw[kW];
-    const auto load = [&](int k) {
-      tmem_load(s_at + kW * k, raw);
-      tmem_loaded(raw);
-    };
-    const auto logit = [&](int k, int e) {
-      const float x = __uint_as_float(raw[e]) * p.scale_log2;
-      return masked && d.key0 + key > rows[kW * k + e].last ? -INFINITY : x;
-    };
-    bool grew = false;
-    if (tid == 0) sm->bad_rows[(t + 1) % 3] = 0;
-    if (!stop) {
-      if (fresh) {
-        poisoned = false;
-        late = 0;
-#pragma unroll
-        for (int q = 0; q < kMine; ++q) l[q] = 0.f;
-      }
-      if (d.flags & kBad) poisoned = true;
-      tc_fence_after_sync();
-      float top = -INFINITY;  // how far a logit is above its reference
-#pragma unroll
-      for (int k = 0; k < kChunks; ++k) {
-        if (kW * k >= real) break;
-        load(k);
-        if (!fresh) {
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < kW; ++e) top = fmaxf(top, logit(k, e) - m[kW * k + e]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < kW; ++e)
-              top = fmaxf(top, fmaf(__uint_as_float(raw[e]), p.scale_log2, -m[kW * k + e]));
-          }
-        }
-        if (p.logits != nullptr && key < keys) {
-          const int64_t bh = static_cast<int64_t>(d.b) * p.kv_heads + d.hk;
-          float *dst = p.logits +
-                       ((bh * 2 + map) * p.rows + d.item % p.row_blocks * kNR + r0 + kW * k) * p.padded +
-                       d.key0 + key;
-#pragma unroll
-          for (int e = 0; e < kW; ++e)
-            if (kW * k + e < real && dbg_ok(d.key0 + key < p.padded, p.status, 41))
-              dst[e * p.padded] = logit(k, e);
-        }
-      }
-      grew = fresh || top > kGrowth;  // the first tile sets the references
-      // P's buffer: the product that read it last is done.
-      if (t >= G::kPBufs)
-        ok = mbar_wait_warp(&sm->pv_done[(t - G::kPBufs) & 1], phase<2>(t - G::kPBufs), &sm->abort,
-                            kWaitNs);
-      // Rows of v behind the sequence's end hold anything (NaN too): zero those that the product
-      // still takes in its last step of 16, as 0 * NaN would reach every row.  Where new tokens see different keys, a non-finite v row that only some
-      // of them see is noted, to be kept out of the product.
-      if (ok && (keys < kTile || mixed)) {
-#pragma unroll 1
-        for (int k = 0; k < G::kValSlots; ++k) {
-          const uint32_t c = t * G::kValSlots + k;
-          ok = ok && mbar_wait_warp(&sm->v_full[c % L::kValRing], phase<L::kValRing>(c),
-                                    &sm->abort, kWaitNs);
-        }
-        if (ok) {
-          const int from = max(0, keys);
-#pragma unroll 1
-          for (int k = tid; k < (16 * d.steps - from) * kVUnits; k += kConsumers)
-            *v_row(t, from + k / kVUnits, k % kVUnits) = make_uint4(0, 0, 0, 0);
-          if (mixed) {
-            const int lo = max(0, lim_min + 1 - d.key0), hi = min(kTile, keys);
-#pragma unroll 1
-            for (int k = tid; k < (hi - lo) * kVUnits; k += kConsumers) {
-              const uint4 y = *v_row(t, lo + k / kVUnits, k % kVUnits);
-              bool bad = false;
-              for (const uint32_t w : {y.x, y.y, y.z, y.w})
-                bad |= (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-              if (bad) atomicOr(&sm->bad_rows[t % 3], 1u << (d.len - 1 - d.key0 - lo - k / kVUnits));
-            }
-          }
-        }
-      }
-    }
-    ok = ok && healthy;
-    if (!ok) *reinterpret_cast<volatile int *>(&sm->failed) = 1;
-
-    // One barrier and vote of all eight warps: has a logit outgrown its reference (or did a wait
-    // run out)?
-    if (named_barrier_or(1, kConsumers, grew || !ok)) {
-      if (*reinterpret_cast<volatile int *>(&sm->failed)) break;
-      if (!stop) {
-#pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-          if (kW * k >= real) break;
-          if (!kKeep) load(k);
-#pragma unroll
-          for (int e = 0; e < kW; ++e) {
-            const float y = warp_max(logit(k, e));
-            if (lane == 0) sm->wmax[map][quarter][r0 + kW * k + e] = y;
-          }
-        }
-        // O moves with the reference, so the product before must be done.
-        if (!fresh)
-          ok = mbar_wait_warp(&sm->pv_done[(t - 1) & 1], phase<2>(t - 1), &sm->abort, kWaitNs);
-      }
-      if (named_barrier_or(2, kConsumers, !ok)) break;
-      if (!stop) {
-        const auto new_m = [&](int q) {
-          const float(*w)[kNR] = sm->wmax[map];
-          const float y = fmaxf(fmaxf(w[0][r0 + q], w[1][r0 + q]), fmaxf(w[2][r0 + q], w[3][r0 + q]));
-          return fresh ? y : fmaxf(m[q], y);
-        };
-        // Rows that are not there never grow.
-        if (quarter == 0 && lane < kMine)
-          sm->m[m_turn ^ 1][map][r0 + lane] = lane < real ? new_m(lane) : INFINITY;
-        if (!fresh) {
-          const uint32_t o_at =
-              tmem + G::kTmemO + (seg % G::kOBufs) * G::kOCols + map * 2 * kNQ + r0;
-          tc_fence_after_sync();
-#pragma unroll
-          for (int k = 0; k < kChunks; ++k) {
-            if (kW * k >= real) break;
-            float f[kW];
-            bool moved = false;
-#pragma unroll
-            for (int e = 0; e < kW; ++e) {
-              const int q = kW * k + e;
-              const float old = m[q], y = new_m(q);
-              f[e] = q < real && y != old ? ex2_approx(old - y) : 1.f;
-              moved |= q < real && y != old;
-              l[q] *= f[e];
-            }
-            if (moved) {  // the same decision in every thread of the map
-#pragma unroll 1
-              for (int part = 0; part < 2 * G::kValSlots; ++part) {
-                const uint32_t at = o_at + (part / 2) * G::kPCols + (part % 2) * kNQ + kW * k;
-                uint32_t y[kW];
-                tmem_load(at, y);
-                tmem_loaded(y);
-#pragma unroll
-                for (int e = 0; e < kW; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f[e]);
-                tmem_store(at, y);
-              }
-            }
-          }
-          tmem_st_wait();
-        }
-      }
-      named_barrier_sync(2, kConsumers);
-      m_turn ^= 1;
-    }
-    if (!stop) {
-    // Rows of v to keep out of the product (rare): zero them in the buffer as well, and keep
-    // their logits.
-    const uint32_t bad_rows = mixed ? sm->bad_rows[t % 3] : 0u;
-    const int back = d.len - 1 - d.key0 - key;
-    const bool kept_out = bad_rows && back >= 0 && back < kMaxBad && ((bad_rows >> back) & 1);
-    if (bad_rows) {
-      late |= bad_rows;
-#pragma unroll 1
-      for (int k = tid; k < kTile * kVUnits; k += kConsumers) {
-        const int x_back = d.len - 1 - d.key0 - k / kVUnits;
-        if (x_back >= 0 && x_back < kMaxBad && ((bad_rows >> x_back) & 1))
-          *v_row(t, k / kVUnits, k % kVUnits) = make_uint4(0, 0, 0, 0);
-      }
-    }
-
-    // P = 2^(x - m) as bf16 hi + lo.
-    uint8_t *p_buf = smem + L::kP + (t % G::kPBufs) * G::kPBytes;
-#pragma unroll
-    for (int k = 0; k < kChunks; ++k) {
-      if (kW * k >= real) break;
-      if (!kKeep) load(k);
-      uint32_t hi[kW > 1 ? kW / 2 : 1], lo[kW > 1 ? kW / 2 : 1];
-      float y[kW > 1 ? kW : 2];
-      y[1] = 0.f;
-#pragma unroll
-      for (int e = 0; e < kW; ++e) {
-        const int q = kW * k + e;
-        const float ref = sm->m[m_turn][map][r0 + q];
-        if (masked) {
-          const float x = logit(k, e);
-          if (kept_out) sm->late[seg & 1][map][back][r0 + q] = x;
-          y[e] = x == -INFINITY ? 0.f : ex2_approx(x - ref);  // also where no key has been seen yet
-        } else {
-          y[e] = ex2_approx(fmaf(__uint_as_float(raw[e]), p.scale_log2, -ref));
-        }
-        l[kW * k + e] += y[e];
-      }
-#pragma unroll
-      for (int e = 0; e < (kW > 1 ? kW / 2 : 1); ++e) {
-        hi[e] = pack_bf16x2(y[2 * e], y[2 * e + 1]);
-        lo[e] = pack_bf16x2(y[2 * e] - __uint_as_float(hi[e] << 16),
-                            y[2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u));
-      }
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        const int unit = (map * 2 + part) * (kNQ / 8) + r0 / 8 + k;  // of eight columns
-        const uint32_t *src = part ? lo : hi;
-        uint8_t *at = p_buf + (unit / 8) * (kTile * 128) + key * G::kPRow +
-                      (((unit % 8) ^ (G::kPRow == 64 ? (key >> 1) & 3 : key & 7)) << 4) +
-                      2 * (r0 % 8);
-        if constexpr (kW == 1)
-          *reinterpret_cast<uint16_t *>(at) = static_cast<uint16_t>(src[0]);
-        else if constexpr (kW == 2)
-          *reinterpret_cast<uint32_t *>(at) = src[0];
-        else if constexpr (kW == 4)
-          *reinterpret_cast<uint2 *>(at) = make_uint2(src[0], src[1]);
-        else
-          *reinterpret_cast<uint4 *>(at) = make_uint4(src[0], src[1], src[2], src[3]);
-      }
-    }
-    fence_async_proxy();
-    tc_fence_before_sync();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm->p_full[t & 1]);
-    }
-
-    // ---- the end of the segment before ----
-    if (pending) {
-      pending = false;
-      const RowInfo *done_rows = sm->rows[(seg - 1) % kRing];
-      const int parity = (seg - 1) & 1;
-      const TileDesc &done = sm->done[parity];
-      const int done_real = kNR == 1 ? 1 : done.real;
-      const bool direct = (done.flags & kDirect) != 0;
-      // A thread has one value column.  The groups of four warps share the rows, kTake at a turn;
-      // for d = 128 every other group has the second 128 columns.
-      constexpr int kShares = kD == 128 ? G::kSets : 2 * G::kSets;
-      constexpr int kTake = kNR / kShares < 1 ? 1 : kNR / kShares < 8 ? kNR / kShares : 8;
-      constexpr int kTurns = (kNR + kShares * kTake - 1) / (kShares * kTake);
-      constexpr int kHas = kTake * kTurns;
-      const int block = kD == 128 ? group & 1 : 0;
-      const int share = kD == 128 ? group >> 1 : group;
-      const int col = 128 * block + key;
-      const auto row_at = [&](int k) { return kTake * (kShares * k + share); };  // of turn k
-      const uint32_t o_at =
-          tmem + G::kTmemO + ((seg - 1) % G::kOBufs) * G::kOCols + block * G::kPCols;
-      // What the output needs from global memory, on its way during the wait.
-      constexpr bool kEarly = kHas <= 4;
-      float lam[kEarly ? kHas : 1], gain[kEarly ? kHas : 1];
-      if (kEarly && direct) {
-#pragma unroll
-        for (int e = 0; e < kHas; ++e) {
-          const int q = row_at(e / kTake) + e % kTake;
-          if (q >= done_real) break;
-          lam[e] = __ldg(p.lambda + done_rows[q].head);
-          gain[e] = p.headnorm && p.norm_w != nullptr
-                        ? __ldg(p.norm_w + done_rows[q].head * (2 * kD) + col)
-                        : 1.f;
-        }
-      }
-      const uint32_t td = t - 1;
-      if (!mbar_wait_warp(&sm->pv_done[td & 1], phase<2>(td), &sm->abort, kWaitNs)) {
-        healthy = false;  // the next vote ends the loop
-        *reinterpret_cast<volatile int *>(&sm->failed) = 1;
-      }
-      tc_fence_after_sync();
-      const auto l_of = [&](int mp, int q) {
-        const float(*x)[kNR] = sm->lsum[parity][mp];
-        return (x[0][q] + x[1][q]) + (x[2][q] + x[3][q]);
-      };
-      float o[kHas];
-#pragma unroll
-      for (int k = 0; k < kTurns; ++k) {
-        const int q0 = row_at(k);
-        if (q0 >= done_real) break;
-        uint32_t part[4][kTake];  // map 1 hi, lo, map 2 hi, lo
-#pragma unroll
-        for (int e = 0; e < 4; ++e) tmem_load(o_at + e * kNQ + q0, part[e]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) tmem_loaded(part[e]);
-#pragma unroll
-        for (int e = 0; e < kTake; ++e) {
-          const int q = q0 + e;
-          if (q >= done_real) break;
-          float y1 = __uint_as_float(part[0][e]) + __uint_as_float(part[1][e]);
-          float y2 = __uint_as_float(part[2][e]) + __uint_as_float(part[3][e]);
-          if (done_late) {
-            const float2 more = late_sums(q, col);
-            y1 += more.x;
-            y2 += more.y;
-          }
-          if (direct) {
-            const float lm = kEarly ? lam[kTake * k + e] : __ldg(p.lambda + done_rows[q].head);
-            float y = y1 / l_of(0, q) - lm * (y2 / l_of(1, q));
-            if (done_rows[q].last < 0 && !done_poisoned) y = 0.f;  // a row that sees no key
-            o[kTake * k + e] = y;
-          } else if (dbg_ok(done.slot >= 0 && done.slot < 2 * static_cast<int>(gridDim.x),
-                            p.status, 42)) {
-            float *dst = p.part + (static_cast<int64_t>(done.slot) * 2 * kNR + q) * (2 * kD) + col;
-            dst[0] = y1;
-            dst[kNR * (2 * kD)] = y2;
-          }
-        }
-      }
-      // The row's (m, l): per slot for the join, per item for the weights.
-      if (quarter == 0 && r0 == 0 && (!direct || p.item_ml != nullptr)) {
-        float2 *ml = (direct ? p.item_ml + static_cast<int64_t>(done.item) * 2 * kNR
-                             : p.part_ml + static_cast<int64_t>(done.slot) * 2 * kNR) +
-                     map * kNR;
-        if (lane < done_real)
-          ml[lane] = make_float2(sm->ref[parity][map][lane], done_poisoned ? -1.f : l_of(map, lane));
-      }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->o_empty[(seg - 1) % G::kOBufs]);
-      if (direct) {
-        // Head norm: row sums over the lanes, the four quarters and (d = 128) both halves.
-        const auto row_sum = [&](int q) {
-          float y =
-              (sm->rsum[0][0][q] + sm->rsum[0][1][q]) + (sm->rsum[0][2][q] + sm->rsum[0][3][q]);
-          if (kD == 128)
-            y += (sm->rsum[1][0][q] + sm->rsum[1][1][q]) + (sm->rsum[1][2][q] + sm->rsum[1][3][q]);
-          return y;
-        };
-#pragma unroll 1
-        for (int pass = p.headnorm == 2 ? 0 : 1; pass < 2 && p.headnorm; ++pass) {  // mean, square
-#pragma unroll
-          for (int k = 0; k < kTurns; ++k) {
-            const int q0 = row_at(k);
-            if (q0 >= done_real) break;
-#pragma unroll
-            for (int e = 0; e < kTake; ++e) {
-              if (q0 + e >= done_real) break;
-              const float y = o[kTake * k + e];
-              const float z = warp_sum(pass ? y * y : y);
-              if (lane == 0) sm->rsum[block][quarter][q0 + e] = z;
-            }
-          }
-          named_barrier_sync(2, kConsumers);
-          if (pass == 0) {
-#pragma unroll
-            for (int k = 0; k < kTurns; ++k) {
-              const int q0 = row_at(k);
-              if (q0 >= done_real) break;
-#pragma unroll
-              for (int e = 0; e < kTake; ++e)
-                if (q0 + e < done_real) o[kTake * k + e] -= row_sum(q0 + e) * (0.5f / kD);
-            }
-            named_barrier_sync(2, kConsumers);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < kTurns; ++k) {
-          const int q0 = row_at(k);
-          if (q0 >= done_real) break;
-#pragma unroll
-          for (int e = 0; e < kTake; ++e) {
-            const int q = q0 + e;
-            if (q >= done_real) break;
-            float y = o[kTake * k + e];
-            if (p.headnorm && (done_rows[q].last >= 0 || done_poisoned)) {
-              y *= rsqrtf(row_sum(q) * (0.5f / kD) + p.eps) * p.out_scale;
-              if (kEarly)
-                y *= gain[kTake * k + e];
-              else if (p.norm_w != nullptr)
-                y *= __ldg(p.norm_w + done_rows[q].head * (2 * kD) + col);
-            }
-            p.out[done_rows[q].out + col] = __float2bfloat16_rn(y);
-          }
-        }
-      }
-    }
-    if (stop) break;
-    if (d.flags & kLast) {  // this segment's sums and references, read after the next vote
-#pragma unroll
-      for (int q = 0; q < kMine; ++q) {
-        if (q >= real) break;
-        const float y = warp_sum(l[q]);
-        if (lane == 0) sm->lsum[seg & 1][map][quarter][r0 + q] = poisoned ? NAN : y;
-      }
-      if (quarter == 0 && lane < real)
-        sm->ref[seg & 1][map][r0 + lane] = sm->m[m_turn][map][r0 + lane];
-      if (tid == 0) sm->done[seg & 1] = d;
-      done_poisoned = poisoned;
-      done_late = late;
-      pending = true;
-      ++seg;
-    }
-  }
-}
-
-template <int kD, bool kFp8, int kNR>
-__global__ void __launch_bounds__(Geo<kD, kFp8, kNR>::kThreads, 1)
-    diffpaged_fwd_kernel(const __grid_constant__ CUtensorMap mk1,
-                         const __grid_constant__ CUtensorMap mk2,
-                         const __grid_constant__ CUtensorMap mv,
-                         const __grid_constant__ FwdParams p) {
-  using G = Geo<kD, kFp8, kNR>;
-  using L = Layout<kD, kFp8, kNR>;
-  extern __shared__ uint8_t raw[];
-  uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  auto *sm = reinterpret_cast<Ctrl<kNR> *>(smem + L::kCtrl);
-  const int warp = threadIdx.x / 32;
-  Share share;
-  if (warp == kKeyWarp || warp == kValueWarp) {
-    if (threadIdx.x % 32 == 0) {
-      if (warp == kKeyWarp) {
-        tma_prefetch_desc(&mk1);
-        tma_prefetch_desc(&mk2);
-      } else {
-        tma_prefetch_desc(&mv);
-      }
-    }
-    // The setup up to here overlaps the kernel before; the kernel after may start its own from
-    // here on, so that what it reads before it waits for this one is what this one reads.
-    grid_dependency_wait();
-    share = find_share(p, blockIdx.x, gridDim.x);
-    grid_dependents_launch();
-  } else if (warp == kMmaWarp) {
-    tmem_alloc(&sm->tmem, G::kTmemCols);
-    tmem_relinquish();
-  } else if (threadIdx.x == 32 * kSoftmaxWarp) {
-    for (int s = 0; s < L::kKeyRing; ++s) {
-      mbar_init(&sm->k_full[s], 1);
-      mbar_init(&sm->k_empty[s], 1);
-    }
-    for (int s = 0; s < L::kValRing; ++s) {
-      mbar_init(&sm->v_full[s], 1);
-      mbar_init(&sm->v_empty[s], 1);
-    }
-    for (int k = 0; k < 2; ++k) {
-      mbar_init(&sm->q_full[k], 32);
-      mbar_init(&sm->q_empty[k], 1);
-      mbar_init(&sm->s_full[k], 1);
-      mbar_init(&sm->p_full[k], G::kConsumers / 32);
-      mbar_init(&sm->pv_done[k], 1);
-      mbar_init(&sm->o_empty[k], G::kConsumers / 32);
-    }
-    mbar_init(&sm->drain, 1);
-    sm->abort = sm->failed = 0;
-    for (int k = 0; k < 3; ++k) sm->bad_rows[k] = 0;
-    fence_barrier_init();
-  }
-  tc_fence_before_sync();
-  __syncthreads();
-  tc_fence_after_sync();
-  if (warp == kKeyWarp)
-    load_warp<kD, kFp8, kNR, true>(p, &mk1, &mk2, &mv, smem, sm, share);
-  else if (warp == kValueWarp)
-    load_warp<kD, kFp8, kNR, false>(p, &mk1, &mk2, &mv, smem, sm, share);
-  else if (warp == kMmaWarp)
-    mma_warp<kD, kFp8, kNR>(p, smem, sm);
-  else if (warp >= kSoftmaxWarp)
-    softmax_warps<kD, kFp8, kNR>(p, smem, sm);
-  __syncwarp();
-  tc_fence_before_sync();
-  __syncthreads();
-  if (warp == kMmaWarp) tmem_dealloc(sm->tmem, G::kTmemCols);
-  if (threadIdx.x == 0 && *reinterpret_cast<volatile int *>(&sm->abort) && p.status != nullptr)
-    atomicExch(p.status, static_cast<int32_t>(DIFFATTN_ERR_TIMEOUT));
 }
 
 // ---------------------------------------------------------------------------
@@ -1282,7 +108,8 @@ __device__ void join_row(const JoinParams &jp) {
       if (s.off > kItemCost) {
         parts = parts_of(s.all, s.begin - s.off, s.units);
         if (parts.first / 2 == static_cast<int>(which))
-          x = make_int4((s.b * p.kv_heads + s.hk) * p.row_blocks + s.rb, parts.first, parts.n, s.len);
+          x = make_int4((s.b * p.kv_heads + s.hk) * p.row_blocks + s.rb, parts.first, parts.n,
+                        s.len);
       }
     }
     if (lane == 0) cut = x;
@@ -1415,9 +242,9 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
   const auto load_pass = [&] {
     load_rows(group);
     if (key < len && group == 0)
-      dst = p.weights +
-            (static_cast<int64_t>(__ldg(table + p.by_page.div(key))) * p.kv_heads + hk) * p.page_size +
-            p.by_page.mod(key);
+      dst = p.weights + p.by_page.mod(key) +
+            (static_cast<int64_t>(__ldg(table + p.by_page.div(key))) * p.kv_heads + hk) *
+                p.page_size;
   };
   load_pass();
 
@@ -1434,9 +261,9 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
                            (hk * p.row_blocks + rb) * (kItemCost + units),
                        units);
     const auto state = [&](int s) {
-      return parts.n == 1
-                 ? p.item_ml[((static_cast<int64_t>(bh) * p.row_blocks + rb) * 2 + map) * jp.row_tile + row]
-                 : p.part_ml[(parts.slot(s) * 2ll + map) * jp.row_tile + row];
+      const int64_t at =
+          parts.n == 1 ? static_cast<int64_t>(bh) * p.row_blocks + rb : parts.slot(s);
+      return (parts.n == 1 ? p.item_ml : p.part_ml)[(at * 2 + map) * jp.row_tile + row];
     };
     float2 ml = make_float2(-INFINITY, 0.f);
     if (lane < parts.n) ml = state(lane);
@@ -1552,53 +379,10 @@ bool encode_pool(CUtensorMap *map, const void *base, int64_t width, const diffpa
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kD, bool kFp8, int kNR>
-diffattn_status launch_main(const FwdParams &p, const CUtensorMap (&maps)[3], int ctas,
-                            cudaStream_t stream) {
-  constexpr size_t kBytes = Layout<kD, kFp8, kNR>::kBytes;
-  static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
-  static std::atomic<bool> attr_set[64];  // per device (concurrent callers may both set)
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DIFFATTN_ERR_CUDA;
-  if (!attr_set[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(diffpaged_fwd_kernel<kD, kFp8, kNR>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kBytes)) != cudaSuccess)
-      return DIFFATTN_ERR_CUDA;
-    attr_set[dev].store(true, std::memory_order_release);
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(Geo<kD, kFp8, kNR>::kThreads);
-  cfg.dynamicSmemBytes = kBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, diffpaged_fwd_kernel<kD, kFp8, kNR>, maps[0], maps[1], maps[2],
-                            p) == cudaSuccess
-             ? DIFFATTN_OK
-             : DIFFATTN_ERR_CUDA;
-}
-
-template <int kD, bool kFp8>
-diffattn_status launch_rows(const FwdParams &p, const CUtensorMap (&maps)[3],
-                            const PagedFwdPlan &plan, cudaStream_t stream) {
-  switch (plan.row_tile) {
-    case 1: return launch_main<kD, kFp8, 1>(p, maps, plan.ctas, stream);
-    case 2: return launch_main<kD, kFp8, 2>(p, maps, plan.ctas, stream);
-    case 4: return launch_main<kD, kFp8, 4>(p, maps, plan.ctas, stream);
-    case 8: return launch_main<kD, kFp8, 8>(p, maps, plan.ctas, stream);
-    case 16: return launch_main<kD, kFp8, 16>(p, maps, plan.ctas, stream);
-    default: return launch_main<kD, kFp8, 32>(p, maps, plan.ctas, stream);
-  }
-}
-
 template <int kD>
 diffattn_status launch_join(const JoinParams &jp, cudaStream_t stream) {
-  const int64_t blocks = static_cast<int64_t>(jp.joins) + static_cast<int64_t>(jp.f.B) * jp.f.kv_heads * jp.weight_blocks;
+  const int64_t blocks = static_cast<int64_t>(jp.joins) +
+                         static_cast<int64_t>(jp.f.B) * jp.f.kv_heads * jp.weight_blocks;
   if (blocks == 0) return DIFFATTN_OK;
   if (blocks > INT32_MAX) return DIFFATTN_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
@@ -1628,7 +412,8 @@ bool plan_paged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache, boo
   while (q.row_tile < rows && q.row_tile < 32) q.row_tile *= 2;
   const int64_t row_tile = q.row_tile;
   q.row_blocks = static_cast<int>((rows + row_tile - 1) / row_tile);
-  const double items = static_cast<double>(desc.B) * static_cast<double>(cache.kv_heads) * q.row_blocks;
+  const double items =
+      static_cast<double>(desc.B) * static_cast<double>(cache.kv_heads) * q.row_blocks;
   if (items > INT32_MAX) return false;
   q.items = desc.B * cache.kv_heads * q.row_blocks;
   const int64_t most = cache.max_pages * cache.page_size;
@@ -1657,7 +442,8 @@ bool plan_paged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache, boo
                           static_cast<double>(rows) * static_cast<double>(q.padded) * 4.0;
     if (logits > 1.0e18) return false;
     q.item_stats = take(q.items * 2 * row_tile * sizeof(float2));
-    q.logits = take(static_cast<size_t>(desc.B * cache.kv_heads * 2 * rows * q.padded) * sizeof(float));
+    const int64_t floats = desc.B * cache.kv_heads * 2 * rows * q.padded;
+    q.logits = take(static_cast<size_t>(floats) * sizeof(float));
   }
   q.bytes = at;
   return true;
@@ -1721,11 +507,8 @@ diffattn_status launch_paged_fwd(const diffattn_desc &desc, const diffpaged_cach
       !encode_pool(&maps[2], cache.v, 2 * d, cache, cache.v_strides, false, p.piece_rows))
     return DIFFATTN_ERR_CUDA;
 
-  const diffattn_status st =
-      d == 64 ? (fp8 ? launch_rows<64, true>(p, maps, plan, stream)
-                     : launch_rows<64, false>(p, maps, plan, stream))
-              : (fp8 ? launch_rows<128, true>(p, maps, plan, stream)
-                     : launch_rows<128, false>(p, maps, plan, stream));
+  const diffattn_status st = d == 64 ? launch_paged_main_d64(p, maps, plan, fp8, stream)
+                                     : launch_paged_main_d128(p, maps, plan, fp8, stream);
   if (st != DIFFATTN_OK) return st;
   JoinParams jp = {};
   jp.f = p;

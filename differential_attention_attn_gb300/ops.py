@@ -878,7 +878,8 @@ def paged_evict(cache, *, keep: int, recent: int = 0, workspace=None, status=Non
             _check(st)
     ws, ws_bytes, _keep = _workspace(workspace, need, cache, stream)
     ref = cache._desc(cache.kv_heads, 0, True, 0, 0.0, 0.0, status)
-    st = (_lib or load()).diffpaged_evict(ref, cache._ref, int(keep), int(recent), ws, ws_bytes, handle)
+    st = (_lib or load()).diffpaged_evict(ref, cache._ref, int(keep), int(recent), ws, ws_bytes,
+                                          handle)
     if raw_status:
         return st
     _check(st)

@@ -25,9 +25,17 @@
  * is touched, DIFFATTN_ERR_PAGE is stored in desc->status_dev (when given),
  * and that sequence's output rows are NaN (fwd), its rows on valid pages are
  * written (append), it is left as it is (evict; the weights of fwd).  Entries
- * of the table past a sequence's length are not read.  A page may stand in
- * the table once only; with duplicates among the pages a call writes, their
- * contents are undefined.
+ * of the table past a sequence's length are not read.
+ *
+ * Sequences may share pages (a common prefix) in a call that only reads them:
+ * diffpaged_fwd without accumulate.  A page that a call writes (append: those
+ * of the new tokens; fwd with accumulate and evict: all) stands once only in
+ * the table, else its contents afterwards are undefined.  Calls that write a
+ * cache are ordered with all others on it (same stream, or synchronised).
+ *
+ * The kernels are launched with programmatic stream serialisation: they may
+ * start while the kernel before them on the stream drains, and wait for its
+ * end before they touch memory.
  */
 #ifndef DIFFATTN_PAGED_H
 #define DIFFATTN_PAGED_H

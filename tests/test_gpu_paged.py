@@ -500,3 +500,179 @@ def test_empty_calls():
     ops.paged_append(cache, k, k, torch.empty(1, 2, 0, 128, dtype=torch.bfloat16, device="cuda"))
     ops.paged_evict(cache, keep=16)
     assert c.kv_len.tolist() == [5]
+
+
+def test_many_sequences():
+    """More sequences than one warp scans at a time, most of them short, some idle."""
+    g = torch.Generator().manual_seed(1)
+    lens = torch.randint(0, 260, (300,), generator=g).tolist()
+    c = R.Cache(101, lens=lens, kv=1, d=64, page=16)
+    _parity(c, 2, 1)
+
+
+@pytest.mark.parametrize("lens", [[5, 300, 0], [0, 0, 0], [129]])
+@pytest.mark.parametrize("kv,H", [(2, 4), (1, 40)])
+def test_capacity_far_beyond_the_lengths(lens, kv, H):
+    c = R.Cache(102, lens=lens, kv=kv, d=64, page=32, extra_pages=500, weights=True)
+    out = _parity(c, H, 1)
+    if not any(lens):
+        assert not bool(out.any())
+    before = c.weights.clone()
+    q1, q2, lam, w = R.queries(3, c.B, H, 1, 64)
+    _, _, add, add_tol = R.attend(c, q1, q2, lam, norm_w=w)
+    _fwd(c, q1, q2, lam, w, accumulate=True)
+    after = c.weights
+    for b, n in enumerate(lens):
+        c.weights = before
+        old = c.rows("weights", b).double()
+        c.weights = after
+        R.check(c.rows("weights", b), old + add[b],
+                add_tol[b] + (old + add[b]) * (H // kv + 2) * 2.0 ** -23, "weights")
+
+
+def test_two_row_blocks_share_a_head():
+    """40 and 64 rows a key/value head, joined, with weights over all of them."""
+    for H, N in ((40, 1), (16, 4)):
+        c = R.Cache(103, lens=[3000, 700], kv=1, d=64, page=64, weights=True)
+        before = c.weights.clone()
+        q1, q2, lam, w = R.queries(104, 2, H, N, 64)
+        out = _fwd(c, q1, q2, lam, w, accumulate=True)
+        ref, tol, add, add_tol = R.attend(c, q1, q2, lam, norm_w=w, lambda_init=LI)
+        R.check(out, ref, tol, "out")
+        after = c.weights
+        for b in range(2):
+            c.weights = before
+            old = c.rows("weights", b).double()
+            c.weights = after
+            want = old + add[b]
+            R.check(c.rows("weights", b), want,
+                    add_tol[b] + want * (H * N + 2) * 2.0 ** -23, "weights")
+
+
+def test_sequences_that_share_a_prefix():
+    """A page may stand in several sequences' tables where a call only reads it."""
+    c = R.Cache(105, lens=[200, 150, 70], kv=2, d=64, page=16)
+    c.table[1, :4] = c.table[0, :4]
+    c.table[2, :2] = c.table[0, :2]
+    _parity(c, 4, 2)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_problems(seed):
+    g = torch.Generator().manual_seed(200 + seed)
+    pick = lambda *x: x[int(torch.randint(len(x), (1,), generator=g))]
+    kv, group, N = pick(1, 2, 3), pick(1, 2, 3, 5, 8), pick(1, 1, 2, 4, 7)
+    B, hi = pick(1, 2, 5), pick(40, 400, 1500)
+    lens = torch.randint(0, hi + 1, (B,), generator=g).tolist()
+    c = R.Cache(300 + seed, lens=lens, kv=kv, d=pick(64, 128), page=pick(16, 32, 48, 80, 128),
+                dtype=pick(torch.bfloat16, E4M3), layout=pick("head", "token"),
+                extra_pages=pick(0, 3))
+    _parity(c, kv * group, N, seed=seed, causal=pick(True, False), headnorm=pick(0, 1, 2))
+
+
+def test_workspace_contents_do_not_matter():
+    c = R.Cache(106, lens=[900, 20, 2000], kv=2, d=64, page=16, weights=True)
+    cache = c.ops_cache()
+    q1, q2, lam, w = R.queries(107, 3, 8, 2, 64)
+    kw = dict(norm_w=w, lambda_init=LI, accumulate=True)
+    before = c.weights.clone()
+    need = ops.paged_fwd_plan(cache, 8, 2, accumulate=True)
+    got = []
+    for fill in (0, 255, 127):
+        c.weights.copy_(before)
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        got.append((ops.paged_fwd(cache, q1, q2, lam, workspace=ws, **kw), c.weights.clone()))
+    for out, weights in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(weights, got[0][1])
+    pools = {t: getattr(c, t).clone() for t in ("k1", "k2", "v", "weights", "kv_len")}
+    got = []
+    for fill in (0, 255, 127):
+        for t, x in pools.items():
+            getattr(c, t).copy_(x)
+        ws = torch.full((ops.paged_evict_plan(cache, keep=500),), fill, dtype=torch.uint8,
+                        device="cuda")
+        ops.paged_evict(cache, keep=500, recent=20, workspace=ws)
+        got.append([getattr(c, t).clone() for t in pools])
+    for other in got[1:]:
+        for x, y in zip(other, got[0]):
+            bits = torch.int16 if x.dtype == torch.bfloat16 else torch.int32
+            assert torch.equal(x.view(bits), y.view(bits))
+
+
+def test_steps_without_waiting_are_those_with():
+    """Lengths raised, rows appended, attention, eviction, back to back on the stream: kernels that
+    start before the ones ahead of them end see what those wrote."""
+    outs = []
+    for wait in (True, False):
+        c = R.Cache(108, lens=[700, 700, 700], kv=2, d=64, page=16, weights=True, fill=0.0)
+        c.kv_len.copy_(torch.tensor([3, 600, 250], dtype=torch.int32))
+        cache = c.ops_cache()
+        g = torch.Generator(device="cuda").manual_seed(109)
+        q1, q2, lam, w = R.queries(110, 3, 4, 1, 64)
+        torch.cuda.synchronize()
+        got = []
+        for step in range(60):
+            new = [torch.randn(3, 2, 1, x, generator=g, device="cuda").to(torch.bfloat16)
+                   for x in (64, 64, 128)]
+            c.kv_len.add_(1)
+            ops.paged_append(cache, *new)
+            got.append(ops.paged_fwd(cache, q1, q2, lam, norm_w=w, accumulate=True))
+            ops.paged_evict(cache, keep=610, recent=30)
+            if wait:
+                torch.cuda.synchronize()
+        outs.append(got + [c.weights, c.kv_len])
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
+
+
+def test_two_graphs_with_a_workspace_each_replay_at_once():
+    c = R.Cache(111, lens=[3000, 500], kv=2, d=64, page=16)
+    cache = c.ops_cache()
+    graphs, outs, want = [], [], []
+    for k in range(2):
+        q1, q2, lam, w = R.queries(112 + k, 2, 4, 1, 64)
+        want.append(_fwd(c, q1, q2, lam, w))
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            ops.paged_fwd(cache, q1, q2, lam, norm_w=w, lambda_init=LI)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(ops.paged_fwd(cache, q1, q2, lam, norm_w=w, lambda_init=LI))
+        graphs.append((graph, side, (q1, q2, lam, w)))
+    for _ in range(20):
+        for graph, side, _ in graphs:
+            with torch.cuda.stream(side):
+                graph.replay()
+    torch.cuda.synchronize()
+    for out, ref in zip(outs, want):
+        assert torch.equal(out, ref)
+
+
+def test_bounds_checked_build_agrees():
+    """The debug build's checks find nothing, and its results are the release build's."""
+    import ctypes
+
+    from differential_attention_attn_gb300 import build as libbuild
+    debug = ops.bind(ctypes.CDLL(libbuild.build(debug=True)))
+    for d, dtype, N, H in ((64, torch.bfloat16, 3, 8), (128, E4M3, 1, 2), (64, E4M3, 1, 24),
+                           (128, torch.bfloat16, 5, 8)):
+        both = []
+        for lib in (ops.load(), debug):
+            with ops.using(lib):
+                c = R.Cache(113, lens=[1500, 0, 70, 129], kv=2, d=d, page=48, dtype=dtype,
+                            weights=True, fill=0.0)
+                cache = c.ops_cache()
+                q1, q2, lam, w = R.queries(114, 4, H, N, d, dtype)
+                g = torch.Generator().manual_seed(115)
+                new = [torch.randn(4, 2, N, x, generator=g).to(torch.bfloat16).cuda()
+                       for x in (d, d, 2 * d)]
+                status = torch.zeros(1, dtype=torch.int32, device="cuda")
+                ops.paged_append(cache, *new, status=status)
+                out = ops.paged_fwd(cache, q1, q2, lam, norm_w=w, accumulate=True, status=status)
+                ops.paged_evict(cache, keep=100, recent=9, status=status)
+                torch.cuda.synchronize()
+                assert int(status) == 0
+                both.append([out, c.weights, c.v, c.kv_len])
+        for x, y in zip(*both):
+            assert torch.equal(x, y)
