@@ -289,6 +289,14 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[kN
         : "memory");
 }
 
+// Named barriers beside the softmax warps' 1 and 2.  The load warps find the share while the other
+// warps set up: they wait only for the barriers in shared memory, and the others, whose bounded
+// waits are for this kernel's own work, until the kernel before has ended.
+constexpr uint32_t kLoadBarrier = 3, kStartBarrier = 4;
+__device__ __forceinline__ void named_barrier_arrive(uint32_t id, uint32_t count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 // Phase parity of the n-th use (from 0) of buffer n % kBufs.
 template <int kBufs>
 __device__ __forceinline__ uint32_t phase(uint32_t n) {
@@ -394,15 +402,35 @@ __device__ __forceinline__ Share find_share(const FwdParams &p, uint32_t cta, ui
 
 // ---------------------------------------------------------------------------
 // The load warps, one for the keys (with the tiles' descriptions and the q rows) and one for the
-// values: a copy takes one thread 80 to 130 cycles to issue, and a tile in pages of 16 rows has 32
-// of them, which one warp issues more slowly than HBM delivers.
+// values: a copy takes one thread 80 to 180 cycles to issue, and a tile in pages of 16 rows has 32
+// of them, which one warp issues more slowly than HBM delivers.  (Two for the keys alone were no
+// faster: 33 us where one takes 30 for 64 x 16 heads of 200 keys.)
 // ---------------------------------------------------------------------------
 template <int kD, bool kFp8, int kNR, bool kKeys>
 __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap *mk1,
                                           const CUtensorMap *mk2, const CUtensorMap *mv,
-                                          uint8_t *smem, Ctrl<kNR> *sm, const Share &share) {
+                                          uint8_t *smem, Ctrl<kNR> *sm) {
   using G = Geo<kD, kFp8, kNR>;
   using L = Layout<kD, kFp8, kNR>;
+  constexpr int kPerTile = kKeys ? G::kKeySlots : G::kValSlots;
+  constexpr int kSlots = kKeys ? L::kKeyRing : L::kValRing;
+  uint64_t *full = kKeys ? sm->k_full : sm->v_full;
+  uint64_t *empty = kKeys ? sm->k_empty : sm->v_empty;
+  if (threadIdx.x % 32 == 0) {
+    if (kKeys) {
+      tma_prefetch_desc(mk1);
+      tma_prefetch_desc(mk2);
+    } else {
+      tma_prefetch_desc(mv);
+    }
+  }
+  // The setup up to here overlaps the kernel before; the kernel after may start its own from here
+  // on, so that what it reads before it waits for this one is what this one reads.
+  grid_dependency_wait();
+  named_barrier_arrive(kStartBarrier, 96 + G::kConsumers);
+  const Share share = find_share(p, blockIdx.x, gridDim.x);
+  grid_dependents_launch();
+  named_barrier_sync(kLoadBarrier, 64 + G::kConsumers);
   const int lane = threadIdx.x % 32;
   const int32_t most = p.max_pages * p.page_size;
   int32_t b = share.b, hk = share.hk, rb = share.rb, len = share.len, units = share.units;
@@ -442,10 +470,6 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
   int32_t id = tile < end ? page_of(tile) : 0;
   // Read once (by one row block), the pages leave L2 before anything else does.
   const uint64_t policy = p.row_blocks == 1 ? l2_evict_first() : l2_evict_normal();
-  constexpr int kPerTile = kKeys ? G::kKeySlots : G::kValSlots;
-  constexpr int kSlots = kKeys ? L::kKeyRing : L::kValRing;
-  uint64_t *full = kKeys ? sm->k_full : sm->v_full;
-  uint64_t *empty = kKeys ? sm->k_empty : sm->v_empty;
   uint8_t *ring = smem + (kKeys ? L::kKeyAt : L::kValAt) + box * kBoxBytes;
   const auto freed = [&](uint32_t c) {  // the slot of use c is free again
     return c < kSlots ||
@@ -1143,6 +1167,33 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
   }
 }
 
+// The barriers in shared memory (one thread).
+template <int kD, bool kFp8, int kNR>
+__device__ __forceinline__ void prepare(Ctrl<kNR> *sm) {
+  using G = Geo<kD, kFp8, kNR>;
+  using L = Layout<kD, kFp8, kNR>;
+  for (int s = 0; s < L::kKeyRing; ++s) {
+    mbar_init(&sm->k_full[s], 1);
+    mbar_init(&sm->k_empty[s], 1);
+  }
+  for (int s = 0; s < L::kValRing; ++s) {
+    mbar_init(&sm->v_full[s], 1);
+    mbar_init(&sm->v_empty[s], 1);
+  }
+  for (int k = 0; k < 2; ++k) {
+    mbar_init(&sm->q_full[k], 32);
+    mbar_init(&sm->q_empty[k], 1);
+    mbar_init(&sm->s_full[k], 1);
+    mbar_init(&sm->p_full[k], G::kConsumers / 32);
+    mbar_init(&sm->pv_done[k], 1);
+    mbar_init(&sm->o_empty[k], G::kConsumers / 32);
+  }
+  mbar_init(&sm->drain, 1);
+  sm->abort = sm->failed = 0;
+  for (int k = 0; k < 3; ++k) sm->bad_rows[k] = 0;
+  fence_barrier_init();
+}
+
 template <int kD, bool kFp8, int kNR>
 __global__ void __launch_bounds__(Geo<kD, kFp8, kNR>::kThreads, 1)
     diffpaged_fwd_kernel(const __grid_constant__ CUtensorMap mk1,
@@ -1155,57 +1206,25 @@ __global__ void __launch_bounds__(Geo<kD, kFp8, kNR>::kThreads, 1)
   uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   auto *sm = reinterpret_cast<Ctrl<kNR> *>(smem + L::kCtrl);
   const int warp = threadIdx.x / 32;
-  Share share;
-  if (warp == kKeyWarp || warp == kValueWarp) {
-    if (threadIdx.x % 32 == 0) {
-      if (warp == kKeyWarp) {
-        tma_prefetch_desc(&mk1);
-        tma_prefetch_desc(&mk2);
-      } else {
-        tma_prefetch_desc(&mv);
-      }
-    }
-    // The setup up to here overlaps the kernel before; the kernel after may start its own from
-    // here on, so that what it reads before it waits for this one is what this one reads.
-    grid_dependency_wait();
-    share = find_share(p, blockIdx.x, gridDim.x);
-    grid_dependents_launch();
+  if (warp == kKeyWarp) {
+    load_warp<kD, kFp8, kNR, true>(p, &mk1, &mk2, &mv, smem, sm);
+  } else if (warp == kValueWarp) {
+    load_warp<kD, kFp8, kNR, false>(p, &mk1, &mk2, &mv, smem, sm);
   } else if (warp == kMmaWarp) {
     tmem_alloc(&sm->tmem, G::kTmemCols);
     tmem_relinquish();
-  } else if (threadIdx.x == 32 * kSoftmaxWarp) {
-    for (int s = 0; s < L::kKeyRing; ++s) {
-      mbar_init(&sm->k_full[s], 1);
-      mbar_init(&sm->k_empty[s], 1);
-    }
-    for (int s = 0; s < L::kValRing; ++s) {
-      mbar_init(&sm->v_full[s], 1);
-      mbar_init(&sm->v_empty[s], 1);
-    }
-    for (int k = 0; k < 2; ++k) {
-      mbar_init(&sm->q_full[k], 32);
-      mbar_init(&sm->q_empty[k], 1);
-      mbar_init(&sm->s_full[k], 1);
-      mbar_init(&sm->p_full[k], G::kConsumers / 32);
-      mbar_init(&sm->pv_done[k], 1);
-      mbar_init(&sm->o_empty[k], G::kConsumers / 32);
-    }
-    mbar_init(&sm->drain, 1);
-    sm->abort = sm->failed = 0;
-    for (int k = 0; k < 3; ++k) sm->bad_rows[k] = 0;
-    fence_barrier_init();
-  }
-  tc_fence_before_sync();
-  __syncthreads();
-  tc_fence_after_sync();
-  if (warp == kKeyWarp)
-    load_warp<kD, kFp8, kNR, true>(p, &mk1, &mk2, &mv, smem, sm, share);
-  else if (warp == kValueWarp)
-    load_warp<kD, kFp8, kNR, false>(p, &mk1, &mk2, &mv, smem, sm, share);
-  else if (warp == kMmaWarp)
+    tc_fence_before_sync();
+    named_barrier_sync(kStartBarrier, 96 + G::kConsumers);
+    tc_fence_after_sync();
     mma_warp<kD, kFp8, kNR>(p, smem, sm);
-  else if (warp >= kSoftmaxWarp)
+  } else if (warp >= kSoftmaxWarp) {
+    if (threadIdx.x == 32 * kSoftmaxWarp) prepare<kD, kFp8, kNR>(sm);
+    __syncwarp();
+    named_barrier_arrive(kLoadBarrier, 64 + G::kConsumers);
+    named_barrier_sync(kStartBarrier, 96 + G::kConsumers);
+    tc_fence_after_sync();
     softmax_warps<kD, kFp8, kNR>(p, smem, sm);
+  }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
