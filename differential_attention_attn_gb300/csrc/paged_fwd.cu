@@ -341,6 +341,9 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
     join_row<kD>(jp);
   else
     add_weights(jp, blockIdx.x - jp.joins);
+  // Blocks with nothing to do wait as well: were there no others (no item cut), this kernel would
+  // end, and the one behind it on the stream begin, before the main kernel has.
+  grid_dependency_wait();
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,

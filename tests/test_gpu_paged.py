@@ -625,6 +625,26 @@ def test_steps_without_waiting_are_those_with():
         assert torch.equal(x, y)
 
 
+def test_next_kernel_waits_where_no_item_is_cut():
+    """Items that fill the CTAs' shares exactly, so that the second kernel has nothing to join: what
+    follows on the stream still sees the outputs."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    c = R.Cache(116, lens=[1024] * (2 * sms), kv=1, d=64, page=64)
+    cache = c.ops_cache()
+    q1, q2, lam, w = R.queries(117, 2 * sms, 1, 1, 64)
+    want = _fwd(c, q1, q2, lam, w)
+    out = torch.empty_like(want)
+    ws = torch.empty(ops.paged_fwd_plan(cache, 1), dtype=torch.uint8, device="cuda")
+    got = []
+    for _ in range(50):
+        out.fill_(float("nan"))
+        ops.paged_fwd(cache, q1, q2, lam, norm_w=w, lambda_init=LI, workspace=ws, out=out)
+        got.append(out.clone())
+    torch.cuda.synchronize()
+    for x in got:
+        assert torch.equal(x, want)
+
+
 def test_two_graphs_with_a_workspace_each_replay_at_once():
     c = R.Cache(111, lens=[3000, 500], kv=2, d=64, page=16)
     cache = c.ops_cache()
