@@ -44,7 +44,9 @@ diffattn_status launch_paged_append(const diffattn_desc &desc, const diffpaged_c
                                     const void *k1, const void *k2, const void *v,
                                     const diffattn_strides *strides, cudaStream_t stream);
 
-size_t paged_evict_bytes(const diffattn_desc &desc, const diffpaged_cache &cache, int64_t keep);
+// False when a size does not fit.
+bool paged_evict_bytes(const diffattn_desc &desc, const diffpaged_cache &cache, int64_t keep,
+                       size_t *bytes);
 diffattn_status launch_paged_evict(const diffattn_desc &desc, const diffpaged_cache &cache,
                                    int64_t keep, int64_t recent, void *workspace,
                                    cudaStream_t stream);

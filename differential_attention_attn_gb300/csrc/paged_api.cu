@@ -127,8 +127,8 @@ diffattn_status diffpaged_evict_plan(const diffattn_desc *desc, const diffpaged_
   if (st != DIFFATTN_OK) return st;
   if (workspace_bytes == nullptr || keep < 0 || cache->weights == nullptr)
     return DIFFATTN_ERR_INVALID_ARG;
-  *workspace_bytes = paged_evict_bytes(*desc, *cache, keep);
-  return DIFFATTN_OK;
+  return paged_evict_bytes(*desc, *cache, keep, workspace_bytes) ? DIFFATTN_OK
+                                                                 : DIFFATTN_ERR_UNSUPPORTED;
 }
 
 diffattn_status diffpaged_evict(const diffattn_desc *desc, const diffpaged_cache *cache,

@@ -38,6 +38,7 @@ constexpr int kMoveThreads = 256;
 constexpr int kBatch = 4;   // 16-byte units of a thread in a block of rows
 constexpr int kAhead = 3;   // blocks of rows in flight
 constexpr int kHeld = 16384;  // weights that the selection holds in shared memory
+constexpr int kMostSlices = 8;  // 128-byte columns of k1, k2 and v rows: 8 d bytes, d <= 128
 
 struct EvictParams {
   uint8_t *pool[3];
@@ -320,10 +321,16 @@ EvictLayout layout(const diffattn_desc &desc, const diffpaged_cache &cache, int6
 
 }  // namespace
 
-size_t paged_evict_bytes(const diffattn_desc &desc, const diffpaged_cache &cache, int64_t keep) {
+bool paged_evict_bytes(const diffattn_desc &desc, const diffpaged_cache &cache, int64_t keep,
+                       size_t *bytes) {
+  *bytes = 0;
+  const int64_t most = cache.max_pages * cache.page_size;
   // A budget that no sequence can pass needs nothing.
-  if (keep >= cache.max_pages * cache.page_size || desc.B == 0) return 0;
-  return layout(desc, cache, keep).bytes;
+  if (keep >= most || desc.B == 0) return true;
+  const double items = static_cast<double>(desc.B) * static_cast<double>(cache.kv_heads);
+  if (items * kMostSlices > INT32_MAX || items * static_cast<double>(most) > 1.0e17) return false;
+  *bytes = layout(desc, cache, keep).bytes;
+  return true;
 }
 
 diffattn_status launch_paged_evict(const diffattn_desc &desc, const diffpaged_cache &cache,
@@ -362,8 +369,7 @@ diffattn_status launch_paged_evict(const diffattn_desc &desc, const diffpaged_ca
   p.copy = reinterpret_cast<float *>(ws + l.copy);
   p.list = reinterpret_cast<int2 *>(ws + l.list);
   p.plan = reinterpret_cast<int2 *>(ws + l.plan);
-  const double items = static_cast<double>(desc.B) * static_cast<double>(cache.kv_heads);
-  if (items * slices > INT32_MAX) return DIFFATTN_ERR_UNSUPPORTED;
+  const int64_t items = desc.B * cache.kv_heads;  // items * kMostSlices fits (paged_evict_bytes)
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

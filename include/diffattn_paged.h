@@ -50,7 +50,8 @@ extern "C" {
  * head * s.h + row * s.n + c of its tensor, s its strides: the pages may be
  * stored head by head ([pages, kv_heads, page_size, width]) or token by token
  * ([pages, page_size, kv_heads, width]).  Strides are positive multiples of 16
- * bytes and below 2^39 elements, and the tensors 16-byte aligned. */
+ * bytes and below 2^39 elements, and the tensors 16-byte aligned.  The rows
+ * of k1, k2 and v do not overlap (one buffer may hold them side by side). */
 typedef struct diffpaged_cache {
     void *k1;                  /* bf16, or e4m3 with DIFFATTN_E4M3_QK; width d */
     void *k2;                  /* as k1 */

@@ -148,6 +148,19 @@ def test_evict_plan(lib):
     assert plan(-1) == ops.ERR_INVALID_ARG
 
 
+def test_sizes_that_do_not_fit(lib):
+    """Workspaces past 64 bits and grids past 31 are refused, not wrapped."""
+    n = ctypes.c_size_t(0)
+    st = ops.Strides(1 << 38, 1 << 20, 128)  # (those of a contiguous pool would be past the limit)
+    big = _cache(heads=1 << 14, page=1 << 29, max_pages=1, k1_strides=st, k2_strides=st,
+                 v_strides=st)
+    for B in (1 << 20, 1 << 16):
+        desc = _desc(B=B, H=1 << 14)
+        assert lib.diffpaged_evict_plan(ctypes.byref(desc), ctypes.byref(big), 1 << 28,
+                                        ctypes.byref(n)) == ops.ERR_UNSUPPORTED
+        assert _evict(lib, desc, big, keep=1 << 28) == ops.ERR_UNSUPPORTED
+
+
 def test_nothing_to_do(lib):
     assert _append(lib, _desc(N=0), _cache()) == ops.OK
     assert _append(lib, _desc(B=0), _cache()) == ops.OK
