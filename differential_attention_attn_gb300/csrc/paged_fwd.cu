@@ -248,27 +248,38 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
   };
   load_pass();
 
-  // The rows' statistics, a warp per row and map: the first 32 parts' in one load.
+  // The rows' statistics: a power of two of lanes, at least as many as parts (up to 32), per row
+  // and map.
   bool bad = false;
-#pragma unroll 4
-  for (int k = warp; k < 2 * p.rows; k += kJoinThreads / 32) {
-    const int map = k & 1, r = k >> 1;
+  const auto parts_at = [&](int rb) {
+    if (p.whole) return Parts{0, 1};
+    return parts_of(shared_all,
+                    shared_before * p.kv_heads * p.row_blocks +
+                        (hk * p.row_blocks + rb) * (kItemCost + units),
+                    units);
+  };
+  int wide = 1;
+  for (int rb = 0; rb < p.row_blocks; ++rb)
+    while (wide < 32 && wide < parts_at(rb).n) wide *= 2;
+  const int own = lane & (wide - 1);
+#pragma unroll 1
+  for (int k0 = 0; k0 < 2 * p.rows; k0 += kJoinThreads / wide) {
+    const int k = k0 + threadIdx.x / wide;
+    const bool real = k < 2 * p.rows;
+    const int map = k & 1, r = real ? k >> 1 : 0;
     const int rb = r / jp.row_tile, row = r - rb * jp.row_tile;
-    Parts parts = {0, 1};
-    if (!p.whole)
-      parts = parts_of(shared_all,
-                       shared_before * p.kv_heads * p.row_blocks +
-                           (hk * p.row_blocks + rb) * (kItemCost + units),
-                       units);
+    const Parts parts = parts_at(rb);
     const auto state = [&](int s) {
       const int64_t at =
           parts.n == 1 ? static_cast<int64_t>(bh) * p.row_blocks + rb : parts.slot(s);
       return (parts.n == 1 ? p.item_ml : p.part_ml)[(at * 2 + map) * jp.row_tile + row];
     };
+    const int i = p.by_group.div(r);
+    const float scale = map ? __ldg(p.lambda + hk * p.group + r - i * p.group) : 1.f;
     float2 ml = make_float2(-INFINITY, 0.f);
-    if (lane < parts.n) ml = state(lane);
+    if (real && own < parts.n) ml = state(own);
     bad |= ml.y < 0.f;
-    for (int s = lane + 32; s < parts.n; s += 32) {
+    for (int s = own + wide; s < parts.n && real; s += wide) {
       const float2 more = state(s);
       bad |= more.y < 0.f;
       const float y = fmaxf(ml.x, more.x);
@@ -276,15 +287,15 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
              (more.x == y ? more.y : exp2f(more.x - y) * more.y);
       ml.x = y;
     }
-    const float y = warp_max(ml.x);
-    const float sum = warp_sum(ml.x == y ? ml.y : ml.y * exp2f(ml.x - y));
-    const int i = p.by_group.div(r);
+    float y = ml.x;
+    for (int o = wide / 2; o > 0; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+    float sum = ml.x == y ? ml.y : ml.y * exp2f(ml.x - y);
+    for (int o = wide / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const bool none = len - p.N + i < 0;  // the row sees no key: it adds nothing
-    if (lane == 0) {
+    if (real && own == 0) {
       float *out = reinterpret_cast<float *>(row_stat + r) + 2 * map;
       out[0] = none ? 0.f : y;
-      out[1] = none ? 0.f
-                    : (map ? __ldg(p.lambda + hk * p.group + r - i * p.group) : 1.f) / sum;
+      out[1] = none ? 0.f : scale / sum;
     }
   }
   if (__syncthreads_or(bad)) return;  // a bad page: the sequence's weights stay as they are

@@ -92,7 +92,7 @@ namespace {
 constexpr int kTile = kPagedTile;
 // Warps 0-2 issue, those from 4 on (a multiple of four, for their quarters of tensor memory) do the
 // softmax.
-constexpr int kMmaWarp = 0, kKeyWarp = 1, kValueWarp = 2, kSoftmaxWarp = 4;
+constexpr int kMmaWarp = 0, kKeyWarp = 1, kValueWarp = 2, kQueryWarp = 3, kSoftmaxWarp = 4;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kGrowth = 8.f;  // log2 units a logit may pass the reference maximum by
@@ -197,10 +197,28 @@ __device__ __forceinline__ float warp_sum(float x) {
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
+// (A NaN counts only where all are.)
 __device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The sums of kN values (a power of two) over the warp; lane l returns that of value
+// l / (32 / kN).  Half of the values change hands at each step.
+template <int kN>
+__device__ __forceinline__ float warp_sums(float (&x)[kN]) {
+  const int lane = threadIdx.x % 32;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
+  for (int o = 16, n = kN / 2; o > 0; o >>= 1, n >>= 1) {
+    if (n == 0) x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const bool upper = lane & o;
+      const float mine = upper ? x[j + n] : x[j], other = upper ? x[j] : x[j + n];
+      x[j] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+    }
+  }
+  return x[0];
 }
 
 // One arrival on the barrier when this thread's cp.async copies so far have landed.
@@ -400,6 +418,31 @@ __device__ __forceinline__ Share find_share(const FwdParams &p, uint32_t cta, ui
   return s;
 }
 
+// A load warp's place in its share.
+struct Walk {
+  int32_t b, hk, rb, len, units;
+  int32_t tile, end;  // the tile, and the share's end, in tiles of the current item
+  __device__ __forceinline__ explicit Walk(const Share &s)
+      : b(s.b), hk(s.hk), rb(s.rb), len(s.len), units(s.units), tile(max(0, s.off - kItemCost)),
+        end(s.end - kItemCost) {}
+  // To the next item with a tile in the share (the first may be cut before its tiles).
+  __device__ __forceinline__ void next_item(const FwdParams &p) {
+    end -= units + kItemCost;
+    tile = 0;
+    if (++rb == p.row_blocks) {
+      rb = 0;
+      if (++hk == p.kv_heads) {
+        hk = 0;
+        ++b;
+        if (end > 0) {
+          len = __ldg(p.kv_len + b);
+          units = units_of(len, p.max_pages * p.page_size);
+        }
+      }
+    }
+  }
+};
+
 // ---------------------------------------------------------------------------
 // The load warps, one for the keys (with the tiles' descriptions and the q rows) and one for the
 // values: a copy takes one thread 80 to 180 cycles to issue, and a tile in pages of 16 rows has 32
@@ -428,14 +471,13 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
   // on, so that what it reads before it waits for this one is what this one reads.
   grid_dependency_wait();
   named_barrier_arrive(kStartBarrier, 96 + G::kConsumers);
-  const Share share = find_share(p, blockIdx.x, gridDim.x);
+  Walk w(find_share(p, blockIdx.x, gridDim.x));
+  int32_t &b = w.b, &hk = w.hk, &rb = w.rb, &len = w.len, &units = w.units, &tile = w.tile,
+          &end = w.end;
   grid_dependents_launch();
-  named_barrier_sync(kLoadBarrier, 64 + G::kConsumers);
+  named_barrier_sync(kLoadBarrier, 96 + G::kConsumers);
   const int lane = threadIdx.x % 32;
   const int32_t most = p.max_pages * p.page_size;
-  int32_t b = share.b, hk = share.hk, rb = share.rb, len = share.len, units = share.units;
-  int32_t tile = max(0, share.off - kItemCost);  // of the current item
-  int32_t end = share.end - kItemCost;           // the share's end, in tiles of that item
   // Each slot is two boxes wide and up to eight page pieces high: a lane each.
   const int piece = lane / 2, box = lane % 2;
   const int first_row = piece * p.piece_rows;
@@ -451,22 +493,6 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
   uint32_t seg = 0;    // segments (the share's parts of items)
   int32_t seg_start = tile;
   int32_t slot = 2 * blockIdx.x;
-  // To the next item with a tile in the share (the first may be cut before its tiles).
-  const auto next_item = [&] {
-    end -= units + kItemCost;
-    tile = 0;
-    if (++rb == p.row_blocks) {
-      rb = 0;
-      if (++hk == p.kv_heads) {
-        hk = 0;
-        ++b;
-        if (end > 0) {
-          len = __ldg(p.kv_len + b);
-          units = units_of(len, most);
-        }
-      }
-    }
-  };
   int32_t id = tile < end ? page_of(tile) : 0;
   // Read once (by one row block), the pages leave L2 before anything else does.
   const uint64_t policy = p.row_blocks == 1 ? l2_evict_first() : l2_evict_normal();
@@ -510,7 +536,7 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
       seg_start = 0;
       slot = 2 * blockIdx.x + 1;
     }
-    if (++tile == units) next_item();
+    if (++tile == units) w.next_item(p);
     if (tile < end) id = page_of(tile);
 #pragma unroll 1
     for (int k = 0; k < kPerTile; ++k) {
@@ -545,33 +571,7 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
           mbar_arrive(&full[s]);
       }
     }
-    // The segment's q rows: 16-byte units into the swizzled operand layout.
-    if (kKeys && ok && seg_first) {
-      const uint32_t qb = seg & 1;
-      if (seg >= 2 &&
-          !(ok = mbar_wait_warp(&sm->q_empty[qb], phase<2>(seg - 2), &sm->abort, kWaitNs)))
-        break;
-      constexpr int kUnits = G::kKeyRow / 16;
-#pragma unroll 1
-      for (int x = lane; x < 2 * d.real * kUnits; x += 32) {
-        const int map = x >= d.real * kUnits, y = x - map * d.real * kUnits;
-        const int q = y / kUnits, u = y % kUnits;
-        const int r = q_row + q;
-        const int i = p.by_group.div(r), h = d.hk * p.group + r - i * p.group;
-        const diffattn_strides &qs = map ? p.q2s : p.q1s;
-        const int64_t at = d.b * qs.b + h * qs.h + i * qs.n;
-        const uint8_t *src =
-            static_cast<const uint8_t *>(map ? p.q2 : p.q1) + at * (kFp8 ? 1 : 2) + 16 * u;
-        uint32_t off;
-        if (G::kKeyRow == 64)
-          off = q * 64 + ((u ^ ((q >> 1) & 3)) << 4);
-        else
-          off = (u / 8) * (G::kNS * 128) + q * 128 + (((u % 8) ^ (q & 7)) << 4);
-        cp_async16(smem_u32(smem + L::kQ + (2 * qb + map) * G::kQBytes) + off, src);
-      }
-      cp_async_arrive(&sm->q_full[qb]);
-      ++seg;
-    }
+    if (kKeys && seg_first) ++seg;
   }
   // The end mark takes the next slot's turn; then the copies still in flight
   // are awaited (bounded), so that none lands after the CTA is gone.
@@ -583,12 +583,52 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
     }
     ++uses;
   }
-  if (kKeys) asm volatile("cp.async.wait_all;" ::: "memory");
   if (lane == 0) {
     volatile int never = 0;
     for (uint32_t c = uses > kSlots ? uses - kSlots : 0; c < uses; ++c)
       mbar_wait(&full[c % kSlots], phase<kSlots>(c), &never, kDrainNs);
   }
+}
+
+// ---------------------------------------------------------------------------
+// The query warp: each segment's q rows, 16-byte units into the swizzled operand layout.
+// ---------------------------------------------------------------------------
+template <int kD, bool kFp8, int kNR>
+__device__ __forceinline__ void query_warp(const FwdParams &p, uint8_t *smem, Ctrl<kNR> *sm) {
+  using G = Geo<kD, kFp8, kNR>;
+  using L = Layout<kD, kFp8, kNR>;
+  constexpr int kUnits = G::kKeyRow / 16;
+  const int lane = threadIdx.x % 32;
+  grid_dependency_wait();
+  Walk w(find_share(p, blockIdx.x, gridDim.x));
+  named_barrier_sync(kLoadBarrier, 96 + G::kConsumers);
+#pragma unroll 1
+  for (uint32_t seg = 0; w.tile < w.end; ++seg) {
+    const uint32_t qb = seg & 1;
+    if (seg >= 2 && !mbar_wait_warp(&sm->q_empty[qb], phase<2>(seg - 2), &sm->abort, kWaitNs))
+      break;
+    const int32_t real = min(kNR, p.rows - w.rb * kNR);
+#pragma unroll 1
+    for (int x = lane; x < 2 * real * kUnits; x += 32) {
+      const int map = x >= real * kUnits, y = x - map * real * kUnits;
+      const int q = y / kUnits, u = y % kUnits;
+      const int r = w.rb * kNR + q;
+      const int i = p.by_group.div(r), h = w.hk * p.group + r - i * p.group;
+      const diffattn_strides &qs = map ? p.q2s : p.q1s;
+      const int64_t at = w.b * qs.b + h * qs.h + i * qs.n;
+      const uint8_t *src =
+          static_cast<const uint8_t *>(map ? p.q2 : p.q1) + at * (kFp8 ? 1 : 2) + 16 * u;
+      uint32_t off;
+      if (G::kKeyRow == 64)
+        off = q * 64 + ((u ^ ((q >> 1) & 3)) << 4);
+      else
+        off = (u / 8) * (G::kNS * 128) + q * 128 + (((u % 8) ^ (q & 7)) << 4);
+      cp_async16(smem_u32(smem + L::kQ + (2 * qb + map) * G::kQBytes) + off, src);
+    }
+    cp_async_arrive(&sm->q_full[qb]);
+    w.next_item(p);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -743,27 +783,6 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
   // A segment's end waits for its last product, so it is done after the next tile's P.
   bool pending = false, done_poisoned = false;
   uint32_t done_late = 0;
-  // What the keys kept out of the product add to column `col` of row q of both maps.
-  const auto late_sums = [&](int q, int col) {
-    float2 y = make_float2(0.f, 0.f);
-    const int parity = (seg - 1) & 1;
-    const TileDesc &done = sm->done[parity];
-#pragma unroll 1
-    for (uint32_t rest = done_late; rest; rest &= rest - 1) {
-      const int back = __ffs(rest) - 1;
-      const int32_t pos = done.len - 1 - back;
-      const int32_t page =
-          p.page_table[static_cast<int64_t>(done.b) * p.max_pages + p.by_page.div(pos)];
-      if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) continue;
-      const float v = __bfloat162float(
-          static_cast<const __nv_bfloat16 *>(p.v_pages)[page * p.vs.b + done.hk * p.vs.h +
-                                                        p.by_page.mod(pos) * p.vs.n + col]);
-      const float x1 = sm->late[parity][0][back][q], x2 = sm->late[parity][1][back][q];
-      if (x1 != -INFINITY) y.x += ex2_approx(x1 - sm->ref[parity][0][q]) * v;
-      if (x2 != -INFINITY) y.y += ex2_approx(x2 - sm->ref[parity][1][q]) * v;
-    }
-    return y;
-  };
 #pragma unroll 1
   for (uint32_t t = 0;; ++t) {
     bool ok = mbar_wait_warp(&sm->s_full[t & 1], phase<2>(t), &sm->abort, kWaitNs);
@@ -793,6 +812,16 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
       const float x = __uint_as_float(raw[e]) * p.scale_log2;
       return masked && d.key0 + key > rows[kW * k + e].last ? -INFINITY : x;
     };
+    // The logits of the loaded rows, for the keys' weights.
+    const auto keep_logits = [&](int k) {
+      const int64_t bh = static_cast<int64_t>(d.b) * p.kv_heads + d.hk;
+      const int row = d.item % p.row_blocks * kNR + r0 + kW * k;
+      float *dst = p.logits + ((bh * 2 + map) * p.rows + row) * p.padded + d.key0 + key;
+#pragma unroll
+      for (int e = 0; e < kW; ++e)
+        if (kW * k + e < real && dbg_ok(d.key0 + key < p.padded, p.status, 41))
+          dst[e * p.padded] = logit(k, e);
+    };
     bool grew = false;
     if (tid == 0) sm->bad_rows[(t + 1) % 3] = 0;
     if (!stop) {
@@ -819,15 +848,7 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
               top = fmaxf(top, fmaf(__uint_as_float(raw[e]), p.scale_log2, -m[kW * k + e]));
           }
         }
-        if (p.logits != nullptr && key < keys) {
-          const int64_t bh = static_cast<int64_t>(d.b) * p.kv_heads + d.hk;
-          const int row = d.item % p.row_blocks * kNR + r0 + kW * k;
-          float *dst = p.logits + ((bh * 2 + map) * p.rows + row) * p.padded + d.key0 + key;
-#pragma unroll
-          for (int e = 0; e < kW; ++e)
-            if (kW * k + e < real && dbg_ok(d.key0 + key < p.padded, p.status, 41))
-              dst[e * p.padded] = logit(k, e);
-        }
+        if (!kKeep && p.logits != nullptr && key < keys) keep_logits(k);
       }
       grew = fresh || top > kGrowth;  // the first tile sets the references
       // P's buffer: the product that read it last is done.
@@ -999,6 +1020,7 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->p_full[t & 1]);
+      if (kKeep && p.logits != nullptr && key < keys && real > 0) keep_logits(0);
     }
 
     // ---- the end of the segment before ----
@@ -1022,7 +1044,7 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
       const uint32_t o_at =
           tmem + G::kTmemO + ((seg - 1) % G::kOBufs) * G::kOCols + block * G::kPCols;
       // What the output needs from global memory, on its way during the wait.
-      constexpr bool kEarly = kHas <= 4;
+      constexpr bool kEarly = kHas <= 8;
       float lam[kEarly ? kHas : 1], gain[kEarly ? kHas : 1];
       if (kEarly && direct) {
 #pragma unroll
@@ -1055,22 +1077,40 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
         for (int e = 0; e < 4; ++e) tmem_load(o_at + e * kNQ + q0, part[e]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) tmem_loaded(part[e]);
+        float y[2][kTake];
+#pragma unroll
+        for (int e = 0; e < kTake; ++e) {
+          y[0][e] = __uint_as_float(part[0][e]) + __uint_as_float(part[1][e]);
+          y[1][e] = __uint_as_float(part[2][e]) + __uint_as_float(part[3][e]);
+        }
+        // What the keys kept out of the product add.
+#pragma unroll 1
+        for (uint32_t rest = done_late; rest; rest &= rest - 1) {
+          const int back = __ffs(rest) - 1;
+          const int32_t pos = done.len - 1 - back;
+          const int32_t page =
+              p.page_table[static_cast<int64_t>(done.b) * p.max_pages + p.by_page.div(pos)];
+          if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) continue;
+          const float v = __bfloat162float(static_cast<const __nv_bfloat16 *>(
+              p.v_pages)[page * p.vs.b + done.hk * p.vs.h + p.by_page.mod(pos) * p.vs.n + col]);
+#pragma unroll
+          for (int e = 0; e < kTake; ++e)
+#pragma unroll
+            for (int mp = 0; mp < 2; ++mp) {
+              const float x = sm->late[parity][mp][back][q0 + e];
+              if (x != -INFINITY) y[mp][e] += ex2_approx(x - sm->ref[parity][mp][q0 + e]) * v;
+            }
+        }
 #pragma unroll
         for (int e = 0; e < kTake; ++e) {
           const int q = q0 + e;
           if (q >= done_real) break;
-          float y1 = __uint_as_float(part[0][e]) + __uint_as_float(part[1][e]);
-          float y2 = __uint_as_float(part[2][e]) + __uint_as_float(part[3][e]);
-          if (done_late) {
-            const float2 more = late_sums(q, col);
-            y1 += more.x;
-            y2 += more.y;
-          }
+          const float y1 = y[0][e], y2 = y[1][e];
           if (direct) {
             const float lm = kEarly ? lam[kTake * k + e] : __ldg(p.lambda + done_rows[q].head);
-            float y = y1 / l_of(0, q) - lm * (y2 / l_of(1, q));
-            if (done_rows[q].last < 0 && !done_poisoned) y = 0.f;  // a row that sees no key
-            o[kTake * k + e] = y;
+            const float z = __fdividef(y1, l_of(0, q)) - lm * __fdividef(y2, l_of(1, q));
+            o[kTake * k + e] =
+                done_rows[q].last < 0 && !done_poisoned ? 0.f : z;  // 0: the row sees no key
           } else if (dbg_ok(done.slot >= 0 && done.slot < 2 * static_cast<int>(gridDim.x),
                             p.status, 42)) {
             float *dst = p.part + (static_cast<int64_t>(done.slot) * 2 * kNR + q) * (2 * kD) + col;
@@ -1106,13 +1146,16 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
           for (int k = 0; k < kTurns; ++k) {
             const int q0 = row_at(k);
             if (q0 >= done_real) break;
+            float z[kTake];
 #pragma unroll
             for (int e = 0; e < kTake; ++e) {
-              if (q0 + e >= done_real) break;
-              const float y = o[kTake * k + e];
-              const float z = warp_sum(pass ? y * y : y);
-              if (lane == 0) sm->rsum[block][quarter][q0 + e] = z;
+              const float y = q0 + e < done_real ? o[kTake * k + e] : 0.f;
+              z[e] = pass ? y * y : y;
             }
+            constexpr int kLanes = 32 / kTake;
+            const float y = warp_sums(z);
+            if (lane % kLanes == 0 && q0 + lane / kLanes < done_real)
+              sm->rsum[block][quarter][q0 + lane / kLanes] = y;
           }
           named_barrier_sync(2, kConsumers);
           if (pass == 0) {
@@ -1150,12 +1193,10 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
     }
     if (stop) break;
     if (d.flags & kLast) {  // this segment's sums and references, read after the next vote
-#pragma unroll
-      for (int q = 0; q < kMine; ++q) {
-        if (q >= real) break;
-        const float y = warp_sum(l[q]);
-        if (lane == 0) sm->lsum[seg & 1][map][quarter][r0 + q] = poisoned ? NAN : y;
-      }
+      constexpr int kLanes = 32 / kMine;
+      const float y = warp_sums(l);
+      if (lane % kLanes == 0 && lane / kLanes < real)
+        sm->lsum[seg & 1][map][quarter][r0 + lane / kLanes] = poisoned ? NAN : y;
       if (quarter == 0 && lane < real)
         sm->ref[seg & 1][map][r0 + lane] = sm->m[m_turn][map][r0 + lane];
       if (tid == 0) sm->done[seg & 1] = d;
@@ -1210,6 +1251,8 @@ __global__ void __launch_bounds__(Geo<kD, kFp8, kNR>::kThreads, 1)
     load_warp<kD, kFp8, kNR, true>(p, &mk1, &mk2, &mv, smem, sm);
   } else if (warp == kValueWarp) {
     load_warp<kD, kFp8, kNR, false>(p, &mk1, &mk2, &mv, smem, sm);
+  } else if (warp == kQueryWarp) {
+    query_warp<kD, kFp8, kNR>(p, smem, sm);
   } else if (warp == kMmaWarp) {
     tmem_alloc(&sm->tmem, G::kTmemCols);
     tmem_relinquish();
@@ -1220,7 +1263,7 @@ __global__ void __launch_bounds__(Geo<kD, kFp8, kNR>::kThreads, 1)
   } else if (warp >= kSoftmaxWarp) {
     if (threadIdx.x == 32 * kSoftmaxWarp) prepare<kD, kFp8, kNR>(sm);
     __syncwarp();
-    named_barrier_arrive(kLoadBarrier, 64 + G::kConsumers);
+    named_barrier_arrive(kLoadBarrier, 96 + G::kConsumers);
     named_barrier_sync(kStartBarrier, 96 + G::kConsumers);
     tc_fence_after_sync();
     softmax_warps<kD, kFp8, kNR>(p, smem, sm);
