@@ -38,14 +38,26 @@ constexpr int kJoinThreads = 256;
 constexpr int kMaxParts = 256;       // more than SMs
 constexpr int kWeightBlocks = 1216;  // in all, about: two rounds of four per SM
 
+constexpr size_t kDiscardBytes = size_t{16} << 20;
+
+// Rows of a plane of the logits, by the rows of a block of the main kernel.
+int plane_rows(int row_tile) { return row_tile < 4 ? row_tile : 4; }
+
 struct JoinParams {
   FwdParams f;
   int32_t ctas, join_rows, row_tile;  // row_tile: rows of a block of the main kernel
   int32_t by_item;                    // joins are numbered by item, else by boundary
   uint32_t joins;                     // blocks that join
   int32_t weight_blocks;              // per (sequence, key/value head); 0 without weights
-  int32_t row_groups;                 // warps that share a key's rows (1, 2, 4 or 8)
+  int32_t row_groups;                 // warps that share a key's planes (1, 2, 4 or 8)
+  // The logits are so many that L2 would write most of them out (8 x 8 x 32768 keys of four rows,
+  // 67 MB: discarded once read, a call takes 200 us instead of 207); below, it costs 0.3 us.
+  int32_t discard;
 };
+
+__device__ __forceinline__ void discard_line(void *line) {
+  asm volatile("discard.global.L2 [%0], 128;" ::"l"(line) : "memory");
+}
 
 __device__ __forceinline__ bool timed_out(const FwdParams &p) {
   return p.status != nullptr &&
@@ -192,9 +204,23 @@ __device__ void join_row(const JoinParams &jp) {
         __float2bfloat16_rn(timed_out(p) ? NAN : o);
 }
 
+template <int kN>
+__device__ __forceinline__ void load_row(const float *src, float (&x)[kN]) {
+  if constexpr (kN == 1) {
+    x[0] = *src;
+  } else if constexpr (kN == 2) {
+    const float2 y = *reinterpret_cast<const float2 *>(src);
+    x[0] = y.x, x[1] = y.y;
+  } else {
+    const float4 y = *reinterpret_cast<const float4 *>(src);
+    x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+  }
+}
+
 // Block (sequence, key/value head, k): weights[j] += sum_r |map1 - lambda map2| of every
-// weight_blocks-th run of keys.  A thread takes four keys of every row_groups-th row, at most four
-// rows of both maps in flight; the groups' sums are added in their order.
+// weight_blocks-th run of keys.  A thread takes four keys of every row_groups-th plane of kPlane
+// rows, both maps of a plane in flight; the groups' sums are added in their order.
+template <int kPlane>
 __device__ void add_weights(const JoinParams &jp, uint32_t block) {
   const FwdParams &p = jp.f;
   extern __shared__ float4 row_stat[];  // per row: M1, 1 / l1, M2, lambda / l2
@@ -223,28 +249,32 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
   grid_dependency_wait();
   if (timed_out(p)) return;
 
-  // A pass's first loads: its logits of this warp's first four rows, and the weights they go to.
+  // A pass's first loads: the logits of this warp's first plane, and where the weights are.
   const int32_t *table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-  const float *logits = p.logits + static_cast<int64_t>(bh) * 2 * p.rows * p.padded;
-  int32_t key = first + (warp / groups) * 128 + 4 * lane;
-  float4 x1[4], x2[4];
-  float *dst = nullptr;
-  const auto load_rows = [&](int r0) {
+  float *logits = p.logits + static_cast<int64_t>(bh) * 2 * p.planes * p.padded * kPlane;
+  const int64_t map_step = p.planes * p.padded * kPlane;
+  int32_t key0 = first + (warp / groups) * 128;  // this warp's 128 keys
+  float x1[4][kPlane], x2[4][kPlane];
+  int32_t pages[4] = {0, 0, 0, 0};
+  const auto load_plane = [&](int plane) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = r0 + k * groups;
-      if (r < p.rows && key < len) {
-        x1[k] = *reinterpret_cast<const float4 *>(logits + r * p.padded + key);
-        x2[k] = *reinterpret_cast<const float4 *>(logits + (p.rows + r) * p.padded + key);
+    for (int j = 0; j < 4; ++j) {
+      const int32_t key = key0 + 32 * j + lane;
+      if (key < len && plane < p.planes) {
+        const float *src = logits + (plane * p.padded + key) * kPlane;
+        load_row(src, x1[j]);
+        load_row(src + map_step, x2[j]);
       }
     }
   };
   const auto load_pass = [&] {
-    load_rows(group);
-    if (key < len && group == 0)
-      dst = p.weights + p.by_page.mod(key) +
-            (static_cast<int64_t>(__ldg(table + p.by_page.div(key))) * p.kv_heads + hk) *
-                p.page_size;
+    load_plane(group);
+    if (group == 0)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int32_t key = key0 + 32 * j + lane;
+        if (key < len) pages[j] = __ldg(table + p.by_page.div(key));
+      }
   };
   load_pass();
 
@@ -301,29 +331,40 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
   if (__syncthreads_or(bad)) return;  // a bad page: the sequence's weights stay as they are
 #pragma unroll 1
   for (int32_t at = first; at < len; at += run * jp.weight_blocks) {
-    float w[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int r0 = group; r0 < p.rows; r0 += 4 * groups) {
-      if (r0 != group) load_rows(r0);
+    float *to[4];
+    float old[4], w[4] = {0.f, 0.f, 0.f, 0.f};
+    if (group == 0)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = r0 + k * groups;
+      for (int j = 0; j < 4; ++j) {
+        const int32_t key = key0 + 32 * j + lane;
+        to[j] = p.weights + p.by_page.mod(key) +
+                (static_cast<int64_t>(pages[j]) * p.kv_heads + hk) * p.page_size;
+        if (key < len) old[j] = *to[j];
+      }
+#pragma unroll 1
+    for (int plane = group; plane < p.planes; plane += groups) {
+      if (plane != group) load_plane(plane);
+#pragma unroll
+      for (int e = 0; e < kPlane; ++e) {
+        const int r = plane * kPlane + e;
         if (r >= p.rows) break;
         const float4 st = row_stat[r];
         if (st.y == 0.f) continue;
-        w[0] += fabsf(ex2_approx(x1[k].x - st.x) * st.y - ex2_approx(x2[k].x - st.z) * st.w);
-        w[1] += fabsf(ex2_approx(x1[k].y - st.x) * st.y - ex2_approx(x2[k].y - st.z) * st.w);
-        w[2] += fabsf(ex2_approx(x1[k].z - st.x) * st.y - ex2_approx(x2[k].z - st.z) * st.w);
-        w[3] += fabsf(ex2_approx(x1[k].w - st.x) * st.y - ex2_approx(x2[k].w - st.z) * st.w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] += fabsf(ex2_approx(x1[j][e] - st.x) * st.y - ex2_approx(x2[j][e] - st.z) * st.w);
+      }
+      // The logits are not needed any more: many of them are dropped before L2 writes them out.
+      if (jp.discard) {
+        __syncwarp();
+        constexpr int kLines = 4 * kPlane;  // of 128 keys of a plane and map
+        if (lane < 2 * kLines && key0 < len)
+          discard_line(logits + (plane * p.padded + key0) * kPlane + (lane / kLines) * map_step +
+                       lane % kLines * 32);
       }
     }
-    const int32_t here = key;
-    float *to = dst;
-    float old[4] = {0.f, 0.f, 0.f, 0.f};
-    if (group == 0)
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (here + k < len) old[k] = to[k];
-    key += run * jp.weight_blocks;
+    const int32_t here = key0 + lane;
+    key0 += run * jp.weight_blocks;
     if (at + run * jp.weight_blocks < len) load_pass();
     if (groups > 1) {
       sums[threadIdx.x] = make_float4(w[0], w[1], w[2], w[3]);
@@ -340,18 +381,18 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
     }
     if (group == 0)
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (here + k < len) to[k] = old[k] + w[k];
+      for (int j = 0; j < 4; ++j)
+        if (here + 32 * j < len) *to[j] = old[j] + w[j];
   }
 }
 
-template <int kD>
+template <int kD, int kPlane>
 __global__ void __launch_bounds__(kJoinThreads, 4)
     diffpaged_join_kernel(const __grid_constant__ JoinParams jp) {
   if (blockIdx.x < jp.joins)
     join_row<kD>(jp);
   else
-    add_weights(jp, blockIdx.x - jp.joins);
+    add_weights<kPlane>(jp, blockIdx.x - jp.joins);
   // Blocks with nothing to do wait as well: were there no others (no item cut), this kernel would
   // end, and the one behind it on the stream begin, before the main kernel has.
   grid_dependency_wait();
@@ -393,8 +434,8 @@ bool encode_pool(CUtensorMap *map, const void *base, int64_t width, const diffpa
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kD>
-diffattn_status launch_join(const JoinParams &jp, cudaStream_t stream) {
+template <int kD, int kPlane>
+diffattn_status launch_join_of(const JoinParams &jp, cudaStream_t stream) {
   const int64_t blocks = static_cast<int64_t>(jp.joins) +
                          static_cast<int64_t>(jp.f.B) * jp.f.kv_heads * jp.weight_blocks;
   if (blocks == 0) return DIFFATTN_OK;
@@ -409,8 +450,17 @@ diffattn_status launch_join(const JoinParams &jp, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, diffpaged_join_kernel<kD>, jp) == cudaSuccess ? DIFFATTN_OK
-                                                                               : DIFFATTN_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, diffpaged_join_kernel<kD, kPlane>, jp) == cudaSuccess
+             ? DIFFATTN_OK
+             : DIFFATTN_ERR_CUDA;
+}
+
+template <int kD>
+diffattn_status launch_join(const JoinParams &jp, cudaStream_t stream) {
+  const int plane = plane_rows(jp.row_tile);
+  return plane == 1   ? launch_join_of<kD, 1>(jp, stream)
+         : plane == 2 ? launch_join_of<kD, 2>(jp, stream)
+                      : launch_join_of<kD, 4>(jp, stream);
 }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
@@ -452,12 +502,13 @@ bool plan_paged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache, boo
   q.part = take(slots * 2 * row_tile * 2 * desc.d * sizeof(float));
   q.stats = take(slots * 2 * row_tile * sizeof(float2));
   if (accumulate) {
+    const int64_t plane = plane_rows(q.row_tile), kept = (rows + plane - 1) / plane * plane;
     const double logits = static_cast<double>(desc.B) * static_cast<double>(cache.kv_heads) * 2.0 *
-                          static_cast<double>(rows) * static_cast<double>(q.padded) * 4.0;
+                          static_cast<double>(kept) * static_cast<double>(q.padded) * 4.0;
     if (logits > 1.0e18) return false;
     q.item_stats = take(q.items * 2 * row_tile * sizeof(float2));
-    const int64_t floats = desc.B * cache.kv_heads * 2 * rows * q.padded;
-    q.logits = take(static_cast<size_t>(floats) * sizeof(float));
+    q.logits = take(static_cast<size_t>(desc.B * cache.kv_heads * 2 * kept * q.padded) *
+                    sizeof(float));
   }
   q.bytes = at;
   return true;
@@ -512,6 +563,7 @@ diffattn_status launch_paged_fwd(const diffattn_desc &desc, const diffpaged_cach
     p.item_ml = reinterpret_cast<float2 *>(ws + plan.item_stats);
     p.logits = reinterpret_cast<float *>(ws + plan.logits);
     p.weights = cache.weights;
+    p.planes = (p.rows + plane_rows(plan.row_tile) - 1) / plane_rows(plan.row_tile);
   }
   p.padded = plan.padded;
 
@@ -533,7 +585,8 @@ diffattn_status launch_paged_fwd(const diffattn_desc &desc, const diffpaged_cach
   const int64_t cuts = plan.whole ? 0 : plan.ctas - 1;
   jp.by_item = plan.items < cuts ? 1 : 0;
   jp.joins = static_cast<uint32_t>((jp.by_item ? plan.items : cuts) * jp.join_rows);
-  jp.row_groups = p.rows <= 4 ? 1 : p.rows <= 8 ? 2 : p.rows <= 16 ? 4 : 8;
+  jp.row_groups = p.planes <= 1 ? 1 : p.planes <= 2 ? 2 : p.planes <= 4 ? 4 : 8;
+  jp.discard = plan.bytes - plan.logits >= kDiscardBytes ? 1 : 0;
   if (accumulate) {
     // As many blocks as find work, but not more than a few per SM: each forms the rows' statistics.
     const int64_t run = 4 * kJoinThreads / jp.row_groups, heads = desc.B * cache.kv_heads;

@@ -82,8 +82,11 @@ struct FwdParams {
   float *part;
   float2 *part_ml;
   float2 *item_ml;
-  float *logits;  // [B * kv_heads][2][rows][padded], log2 units, or null
+  // [B * kv_heads][2][planes][padded][rows of a plane], log2 units, or null: the rows in planes of
+  // (up to) four, so that a thread stores those of its key at once and a warp whole lines.
+  float *logits;
   int64_t padded;
+  int32_t planes;
   float *weights;
 };
 
@@ -108,7 +111,8 @@ enum : int32_t { kFirst = 1, kLast = 2, kStop = 4, kBad = 8, kDirect = 16 };
 struct TileDesc {
   int32_t b, hk, real, key0;  // real: rows of the block
   int32_t len, flags, slot, item;
-  int32_t steps, pad[3];  // 16-key steps of the second product (one for an idle sequence)
+  int32_t steps;  // 16-key steps of the second product (one for an idle sequence)
+  int32_t rb, pad[2];
 };
 
 
@@ -528,6 +532,7 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
                 (seg_start == 0 && tile + 1 == units ? kDirect : 0);
       d.item = (b * p.kv_heads + hk) * p.row_blocks + rb;
       d.steps = max(1, (keys + 15) / 16);
+      d.rb = rb;
       q_row = rb * kNR;
       if (bad && lane == 0) report_bad_page(p.status);
     }
@@ -814,13 +819,22 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
     };
     // The logits of the loaded rows, for the keys' weights.
     const auto keep_logits = [&](int k) {
+      constexpr int kPlane = kNR < 4 ? kNR : 4;
       const int64_t bh = static_cast<int64_t>(d.b) * p.kv_heads + d.hk;
-      const int row = d.item % p.row_blocks * kNR + r0 + kW * k;
-      float *dst = p.logits + ((bh * 2 + map) * p.rows + row) * p.padded + d.key0 + key;
+      const int plane = (d.rb * kNR + r0 + kW * k) / kPlane;
+      float *dst =
+          p.logits + (((bh * 2 + map) * p.planes + plane) * p.padded + d.key0 + key) * kPlane;
 #pragma unroll
-      for (int e = 0; e < kW; ++e)
-        if (kW * k + e < real && dbg_ok(d.key0 + key < p.padded, p.status, 41))
-          dst[e * p.padded] = logit(k, e);
+      for (int e = 0; e < kW; e += kPlane, dst += p.padded * kPlane) {
+        if (kW * k + e >= real || !dbg_ok(d.key0 + key < p.padded, p.status, 41)) break;
+        if constexpr (kPlane == 1)
+          *dst = logit(k, e);
+        else if constexpr (kPlane == 2)
+          *reinterpret_cast<float2 *>(dst) = make_float2(logit(k, e), logit(k, e + 1));
+        else
+          *reinterpret_cast<float4 *>(dst) =
+              make_float4(logit(k, e), logit(k, e + 1), logit(k, e + 2), logit(k, e + 3));
+      }
     };
     bool grew = false;
     if (tid == 0) sm->bad_rows[(t + 1) % 3] = 0;
