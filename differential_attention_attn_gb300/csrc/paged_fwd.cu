@@ -36,7 +36,9 @@ __device__ __forceinline__ Parts parts_of(const Shares &all, uint32_t start, uin
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 constexpr int kMaxParts = 256;       // more than SMs
-constexpr int kWeightBlocks = 1216;  // in all, about: two rounds of four per SM
+constexpr int kMaxRowBlocks = kPagedMaxTokens * kPagedMaxGroup / 32;
+static_assert(kMaxRowBlocks <= 32, "a lane each");
+constexpr int kWeightBlocks = 912;  // in all, about: two rounds of three per SM
 
 constexpr size_t kDiscardBytes = size_t{16} << 20;
 
@@ -225,8 +227,8 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
   const FwdParams &p = jp.f;
   extern __shared__ float4 row_stat[];  // per row: M1, 1 / l1, M2, lambda / l2
   __shared__ float4 sums[kJoinThreads];
-  __shared__ Shares shared_all;
-  __shared__ uint32_t shared_before;
+  __shared__ Parts item_parts[kMaxRowBlocks];
+  __shared__ int shared_parts;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int groups = jp.row_groups, group = warp & (groups - 1);
   const int run = kJoinThreads * 4 / groups;  // keys of a pass
@@ -236,16 +238,34 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
   const int32_t most = p.max_pages * p.page_size;
   const int32_t first = static_cast<int32_t>(block - bh * jp.weight_blocks) * run;
   if (len < 0 || len > most || first >= len) return;
-  if (warp == 0 && !p.whole) {
-    uint32_t before;
-    const Shares all = all_shares(p, jp.ctas, b, &before);
-    if (lane == 0) {
-      shared_all = all;
-      shared_before = before;
+  // While the main kernel runs: the parts of the item's row blocks, and the factors of the rows'
+  // maps, 1 (0 for a row that sees no key and adds nothing) and lambda.
+  if (warp == 0) {
+    Parts parts = {0, 1};
+    if (!p.whole) {
+      uint32_t before;
+      const Shares all = all_shares(p, jp.ctas, b, &before);
+      const uint32_t units = units_of(len, most);
+      if (lane < p.row_blocks)
+        parts = parts_of(all,
+                         before * p.kv_heads * p.row_blocks +
+                             (hk * p.row_blocks + lane) * (kItemCost + units),
+                         units);
     }
+    if (lane < p.row_blocks) item_parts[lane] = parts;
+    const int most_parts = __reduce_max_sync(0xffffffffu, parts.n);
+    if (lane == 0) shared_parts = most_parts;
+  }
+  for (int r = threadIdx.x; r < p.rows; r += kJoinThreads) {
+    const int i = p.by_group.div(r);
+    const bool none = len - p.N + i < 0;
+    row_stat[r] = make_float4(0.f, none ? 0.f : 1.f, 0.f,
+                              __ldg(p.lambda + hk * p.group + r - i * p.group));
   }
   __syncthreads();
-  const uint32_t units = units_of(len, most);
+  int wide = 1;
+  while (wide < 32 && wide < shared_parts) wide *= 2;
+  const int own = lane & (wide - 1), per_round = kJoinThreads / wide;
   grid_dependency_wait();
   if (timed_out(p)) return;
 
@@ -278,54 +298,54 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
   };
   load_pass();
 
-  // The rows' statistics: a power of two of lanes, at least as many as parts (up to 32), per row
-  // and map.
-  bool bad = false;
-  const auto parts_at = [&](int rb) {
-    if (p.whole) return Parts{0, 1};
-    return parts_of(shared_all,
-                    shared_before * p.kv_heads * p.row_blocks +
-                        (hk * p.row_blocks + rb) * (kItemCost + units),
-                    units);
+  // The rows' statistics: `wide` lanes per row and map, up to four of them in flight.
+  const auto part_state = [&](int k, int part) {  // row k / 2, map k % 2
+    const int r = k >> 1, rb = r / jp.row_tile;
+    const Parts parts = item_parts[rb];
+    if (part >= parts.n) return make_float2(-INFINITY, 0.f);
+    const int64_t at =
+        parts.n == 1 ? static_cast<int64_t>(bh) * p.row_blocks + rb : parts.slot(part);
+    return (parts.n == 1 ? p.item_ml
+                         : p.part_ml)[(at * 2 + (k & 1)) * jp.row_tile + r - rb * jp.row_tile];
   };
-  int wide = 1;
-  for (int rb = 0; rb < p.row_blocks; ++rb)
-    while (wide < 32 && wide < parts_at(rb).n) wide *= 2;
-  const int own = lane & (wide - 1);
+  bool bad = false;
 #pragma unroll 1
-  for (int k0 = 0; k0 < 2 * p.rows; k0 += kJoinThreads / wide) {
-    const int k = k0 + threadIdx.x / wide;
-    const bool real = k < 2 * p.rows;
-    const int map = k & 1, r = real ? k >> 1 : 0;
-    const int rb = r / jp.row_tile, row = r - rb * jp.row_tile;
-    const Parts parts = parts_at(rb);
-    const auto state = [&](int s) {
-      const int64_t at =
-          parts.n == 1 ? static_cast<int64_t>(bh) * p.row_blocks + rb : parts.slot(s);
-      return (parts.n == 1 ? p.item_ml : p.part_ml)[(at * 2 + map) * jp.row_tile + row];
-    };
-    const int i = p.by_group.div(r);
-    const float scale = map ? __ldg(p.lambda + hk * p.group + r - i * p.group) : 1.f;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (real && own < parts.n) ml = state(own);
-    bad |= ml.y < 0.f;
-    for (int s = own + wide; s < parts.n && real; s += wide) {
-      const float2 more = state(s);
-      bad |= more.y < 0.f;
-      const float y = fmaxf(ml.x, more.x);
-      ml.y = (ml.x == y ? ml.y : ml.y * exp2f(ml.x - y)) +
-             (more.x == y ? more.y : exp2f(more.x - y) * more.y);
-      ml.x = y;
+  for (int k0 = 0; k0 < 2 * p.rows; k0 += 4 * per_round) {
+    float2 ml[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = k0 + j * per_round + threadIdx.x / wide;
+      ml[j] = k < 2 * p.rows ? part_state(k, own) : make_float2(-INFINITY, 0.f);
+      bad |= ml[j].y < 0.f;
     }
-    float y = ml.x;
-    for (int o = wide / 2; o > 0; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
-    float sum = ml.x == y ? ml.y : ml.y * exp2f(ml.x - y);
-    for (int o = wide / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const bool none = len - p.N + i < 0;  // the row sees no key: it adds nothing
-    if (real && own == 0) {
-      float *out = reinterpret_cast<float *>(row_stat + r) + 2 * map;
-      out[0] = none ? 0.f : y;
-      out[1] = none ? 0.f : scale / sum;
+    if (shared_parts > 32)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = k0 + j * per_round + threadIdx.x / wide;
+        if (k < 2 * p.rows)
+#pragma unroll 1
+          for (int s = own + 32; s < shared_parts; s += 32) {
+            const float2 more = part_state(k, s);
+            bad |= more.y < 0.f;
+            const float y = fmaxf(ml[j].x, more.x);
+            ml[j].y = (ml[j].x == y ? ml[j].y : ml[j].y * ex2_approx(ml[j].x - y)) +
+                      (more.x == y ? more.y : ex2_approx(more.x - y) * more.y);
+            ml[j].x = y;
+          }
+      }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (k0 + j * per_round >= 2 * p.rows) break;
+      const int k = k0 + j * per_round + threadIdx.x / wide;
+      float y = ml[j].x;
+      for (int o = wide / 2; o > 0; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+      float sum = ml[j].x == y ? ml[j].y : ml[j].y * ex2_approx(ml[j].x - y);
+      for (int o = wide / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (own == 0 && k < 2 * p.rows) {
+        float *out = reinterpret_cast<float *>(row_stat + (k >> 1)) + 2 * (k & 1);
+        out[0] = y;
+        out[1] = (k & 1) == 0 && out[1] == 0.f ? 0.f : __fdividef(out[1], sum);
+      }
     }
   }
   if (__syncthreads_or(bad)) return;  // a bad page: the sequence's weights stay as they are
@@ -387,7 +407,7 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
 }
 
 template <int kD, int kPlane>
-__global__ void __launch_bounds__(kJoinThreads, 4)
+__global__ void __launch_bounds__(kJoinThreads, 3)
     diffpaged_join_kernel(const __grid_constant__ JoinParams jp) {
   if (blockIdx.x < jp.joins)
     join_row<kD>(jp);
@@ -585,14 +605,19 @@ diffattn_status launch_paged_fwd(const diffattn_desc &desc, const diffpaged_cach
   const int64_t cuts = plan.whole ? 0 : plan.ctas - 1;
   jp.by_item = plan.items < cuts ? 1 : 0;
   jp.joins = static_cast<uint32_t>((jp.by_item ? plan.items : cuts) * jp.join_rows);
-  jp.row_groups = p.planes <= 1 ? 1 : p.planes <= 2 ? 2 : p.planes <= 4 ? 4 : 8;
   jp.discard = plan.bytes - plan.logits >= kDiscardBytes ? 1 : 0;
   if (accumulate) {
-    // As many blocks as find work, but not more than a few per SM: each forms the rows' statistics.
-    const int64_t run = 4 * kJoinThreads / jp.row_groups, heads = desc.B * cache.kv_heads;
-    const int64_t runs = (plan.padded + run - 1) / run;
+    // As many blocks as find work, but not more than a few per SM, as each forms the rows'
+    // statistics.  Planes go to warps of their own while that makes more blocks than would wait.
+    const int64_t heads = desc.B * cache.kv_heads;
     const int64_t share = (int64_t{kWeightBlocks} + heads - 1) / heads;
-    jp.weight_blocks = static_cast<int32_t>(runs < share ? runs : share);
+    const auto runs = [&] {
+      const int64_t run = 4 * kJoinThreads / jp.row_groups;
+      return (plan.padded + run - 1) / run;
+    };
+    jp.row_groups = 1;
+    while (jp.row_groups < 8 && jp.row_groups < p.planes && runs() < share) jp.row_groups *= 2;
+    jp.weight_blocks = static_cast<int32_t>(runs() < share ? runs() : share);
   }
   return d == 64 ? launch_join<64>(jp, stream) : launch_join<128>(jp, stream);
 }
