@@ -36,7 +36,7 @@ struct AppendParams {
   const int32_t *page_table;
   const int32_t *kv_len;
   int32_t *status;
-  uint32_t rows;  // B * kv_heads * N
+  uint32_t rows, groups;  // B * kv_heads * N; the warps that take them
   uint32_t N, kv_heads, page_size, max_pages, num_pages;
   FastDiv by_n, by_heads, by_page;
 };
@@ -59,26 +59,30 @@ __device__ __forceinline__ uint4 to_e4m3(const uint4 &a, const uint4 &b) {
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// A warp per row.  kEager: the row is loaded while its place is looked up, the shortest chain for a
-// few new tokens; otherwise only once it is known to be no padding, which costs a prompt without
-// padding less (27.2 us for 131072 rows at d = 64, eager 23.6) than eager loads cost one of which
-// half is padding (14.2 us for 65568 rows of e4m3 keys at d = 128, eager 21.4).
-template <int kD, bool kFp8, bool kEager>
-__global__ void __launch_bounds__(kWarps * 32, 8) diffpaged_append_kernel(const AppendParams p) {
+// A warp per kRows consecutive rows of a head.  kEager: loaded while their place is looked up, the
+// shortest chain for a few new tokens; otherwise only once they are known to be no padding, which
+// costs a prompt without padding less than eager loads cost one of which half is padding (65568
+// rows of e4m3 keys at d = 128: 14.2 us, eager 21.4).  Two rows a warp suit bf16 (131072 rows at
+// d = 64: 26.1 us, one 27.2), where a lane holds one or two units of each; with e4m3 it holds up to
+// four, and one row is faster (the case above with two rows: 14.4 us and, at d = 64, 29.7 us for 30.8: close).
+template <int kD, bool kFp8, int kRows, bool kEager>
+__global__ void __launch_bounds__(kWarps * 32, kRows == 1 ? 8 : 6)
+    diffpaged_append_kernel(const AppendParams p) {
   constexpr int kKeyUnits = kFp8 ? kD / 16 : kD / 8;  // 16-byte units stored per key row
   constexpr int kUnits = 2 * kKeyUnits + kD / 4;
   constexpr int kPerLane = (kUnits + 31) / 32;
   const int lane = threadIdx.x % 32;
-  const uint32_t row = blockIdx.x * kWarps + threadIdx.x / 32;
-  if (row >= p.rows) return;
-  const uint32_t bh = p.by_n.div(row), i = row - bh * p.N;
+  const uint32_t group = blockIdx.x * kWarps + threadIdx.x / 32;
+  if (group >= p.groups) return;
+  const uint32_t bh = p.by_n.div(group), i0 = (group - bh * p.by_n.d) * kRows;
   const uint32_t b = p.by_heads.div(bh), h = bh - b * p.kv_heads;
   grid_dependency_wait();
   grid_dependents_launch();
   const int32_t len = __ldg(p.kv_len + b);
 
-  uint4 x[kPerLane], y[kPerLane];
-  const auto load = [&] {
+  uint4 x[kRows][kPerLane], y[kRows][kPerLane];
+  int32_t page[kRows];
+  const auto load = [&](int r) {
 #pragma unroll
     for (int u = 0; u < kPerLane; ++u) {
       const int unit = lane + 32 * u;
@@ -86,46 +90,61 @@ __global__ void __launch_bounds__(kWarps * 32, 8) diffpaged_append_kernel(const 
         const int t = unit < kKeyUnits ? 0 : unit < 2 * kKeyUnits ? 1 : 2;
         const int off = unit - t * kKeyUnits;
         const bool wide = kFp8 && t < 2;  // sixteen bf16 in, sixteen bytes out
-        const uint8_t *s = p.src[t] + b * p.src_b[t] + h * p.src_h[t] + i * p.src_n[t] +
+        const uint8_t *s = p.src[t] + b * p.src_b[t] + h * p.src_h[t] + (i0 + r) * p.src_n[t] +
                            off * (wide ? 32 : 16);
-        x[u] = __ldg(reinterpret_cast<const uint4 *>(s));
-        if (wide) y[u] = __ldg(reinterpret_cast<const uint4 *>(s) + 1);
+        x[r][u] = __ldg(reinterpret_cast<const uint4 *>(s));
+        if (wide) y[r][u] = __ldg(reinterpret_cast<const uint4 *>(s) + 1);
       }
     }
   };
-  if (kEager) load();
-  const int32_t t = len - static_cast<int32_t>(p.N) + static_cast<int32_t>(i);
+  if (kEager)
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+      if (i0 + r < p.N) load(r);
   if (len < 0 || static_cast<uint32_t>(len) > p.max_pages * p.page_size) {
     report_bad_page(p.status);
     return;
   }
-  if (t < 0) return;
-  const int32_t n = p.by_page.div(t), slot = t - n * static_cast<int32_t>(p.page_size);
-  const int32_t page = __ldg(p.page_table + static_cast<int64_t>(b) * p.max_pages + n);
-  if (!kEager) load();
-  if (static_cast<uint32_t>(page) >= p.num_pages) {
-    report_bad_page(p.status);
-    return;
-  }
-  if (!dbg_ok(slot >= 0 && static_cast<uint32_t>(slot) < p.page_size, p.status, 40)) return;
+  const int32_t t0 = len - static_cast<int32_t>(p.N) + static_cast<int32_t>(i0);
+  const auto wanted = [&](int r) { return i0 + r < p.N && t0 + r >= 0; };
 #pragma unroll
-  for (int u = 0; u < kPerLane; ++u) {
-    const int unit = lane + 32 * u;
-    if (unit < kUnits) {
-      const int k = unit < kKeyUnits ? 0 : unit < 2 * kKeyUnits ? 1 : 2;
-      const int off = unit - k * kKeyUnits;
-      uint8_t *d = p.dst[k] + page * p.dst_p[k] + h * p.dst_h[k] + slot * p.dst_n[k] + off * 16;
-      *reinterpret_cast<uint4 *>(d) = (kFp8 && k < 2) ? to_e4m3(x[u], y[u]) : x[u];
+  for (int r = 0; r < kRows; ++r)
+    if (wanted(r)) {
+      page[r] = __ldg(p.page_table + static_cast<int64_t>(b) * p.max_pages + p.by_page.div(t0 + r));
+      if (!kEager) load(r);
     }
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    if (!wanted(r)) continue;
+    if (static_cast<uint32_t>(page[r]) >= p.num_pages) {
+      report_bad_page(p.status);
+      continue;
+    }
+    const int32_t slot = p.by_page.mod(t0 + r);
+    if (!dbg_ok(slot >= 0 && static_cast<uint32_t>(slot) < p.page_size, p.status, 40)) continue;
+#pragma unroll
+    for (int u = 0; u < kPerLane; ++u) {
+      const int unit = lane + 32 * u;
+      if (unit < kUnits) {
+        const int k = unit < kKeyUnits ? 0 : unit < 2 * kKeyUnits ? 1 : 2;
+        const int off = unit - k * kKeyUnits;
+        uint8_t *d = p.dst[k] + page[r] * p.dst_p[k] + h * p.dst_h[k] + slot * p.dst_n[k] +
+                     off * 16;
+        *reinterpret_cast<uint4 *>(d) = (kFp8 && k < 2) ? to_e4m3(x[r][u], y[r][u]) : x[r][u];
+      }
+    }
+    if (lane == 0 && p.weights != nullptr)
+      p.weights[(static_cast<int64_t>(page[r]) * p.kv_heads + h) * p.page_size + slot] = 0.f;
   }
-  if (lane == 0 && p.weights != nullptr)
-    p.weights[(static_cast<int64_t>(page) * p.kv_heads + h) * p.page_size + slot] = 0.f;
 }
 
-template <int kD, bool kFp8>
-cudaError_t launch(const AppendParams &p, cudaStream_t stream) {
+template <int kD, bool kFp8, int kRows, bool kEager>
+cudaError_t launch_rows(AppendParams p, cudaStream_t stream) {
+  const uint32_t per_head = (p.N + kRows - 1) / kRows;
+  p.by_n = fast_div(per_head);
+  p.groups = p.rows / p.N * per_head;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.rows + kWarps - 1) / kWarps);
+  cfg.gridDim = dim3((p.groups + kWarps - 1) / kWarps);
   cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -133,8 +152,13 @@ cudaError_t launch(const AppendParams &p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return p.rows <= kFewRows ? cudaLaunchKernelEx(&cfg, diffpaged_append_kernel<kD, kFp8, true>, p)
-                            : cudaLaunchKernelEx(&cfg, diffpaged_append_kernel<kD, kFp8, false>, p);
+  return cudaLaunchKernelEx(&cfg, diffpaged_append_kernel<kD, kFp8, kRows, kEager>, p);
+}
+
+template <int kD, bool kFp8>
+cudaError_t launch(const AppendParams &p, cudaStream_t stream) {
+  return p.rows <= kFewRows ? launch_rows<kD, kFp8, 1, true>(p, stream)
+                            : launch_rows<kD, kFp8, kFp8 ? 1 : 2, false>(p, stream);
 }
 
 }  // namespace
@@ -175,7 +199,6 @@ diffattn_status launch_paged_append(const diffattn_desc &desc, const diffpaged_c
   p.page_size = static_cast<uint32_t>(cache.page_size);
   p.max_pages = static_cast<uint32_t>(cache.max_pages);
   p.num_pages = static_cast<uint32_t>(cache.num_pages);
-  p.by_n = fast_div(p.N);
   p.by_heads = fast_div(p.kv_heads);
   p.by_page = fast_div(p.page_size);
   cudaError_t e;
