@@ -63,8 +63,8 @@ __device__ __forceinline__ uint4 to_e4m3(const uint4 &a, const uint4 &b) {
 // shortest chain for a few new tokens; otherwise only once they are known to be no padding, which
 // costs a prompt without padding less than eager loads cost one of which half is padding (65568
 // rows of e4m3 keys at d = 128: 14.2 us, eager 21.4).  Two rows a warp suit bf16 (131072 rows at
-// d = 64: 26.1 us, one 27.2), where a lane holds one or two units of each; with e4m3 it holds up to
-// four, and one row is faster (the case above with two rows: 14.4 us and, at d = 64, 29.7 us for 30.8: close).
+// d = 64: 26.2 us, one 27.2), where a lane holds one or two units of each.  With e4m3 it holds up to
+// four, and one row is as good (the case above with two: 14.4 us).
 template <int kD, bool kFp8, int kRows, bool kEager>
 __global__ void __launch_bounds__(kWarps * 32, kRows == 1 ? 8 : 6)
     diffpaged_append_kernel(const AppendParams p) {

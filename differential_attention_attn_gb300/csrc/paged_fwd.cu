@@ -406,13 +406,15 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
   }
 }
 
+// kPlane: rows of a plane of the logits; 0 where no weights are added.
 template <int kD, int kPlane>
-__global__ void __launch_bounds__(kJoinThreads, 3)
+__global__ void __launch_bounds__(kJoinThreads, kPlane ? 3 : 6)
     diffpaged_join_kernel(const __grid_constant__ JoinParams jp) {
-  if (blockIdx.x < jp.joins)
+  if (kPlane == 0 || blockIdx.x < jp.joins) {
     join_row<kD>(jp);
-  else
-    add_weights<kPlane>(jp, blockIdx.x - jp.joins);
+  } else {
+    if constexpr (kPlane > 0) add_weights<kPlane>(jp, blockIdx.x - jp.joins);
+  }
   // Blocks with nothing to do wait as well: were there no others (no item cut), this kernel would
   // end, and the one behind it on the stream begin, before the main kernel has.
   grid_dependency_wait();
@@ -477,8 +479,9 @@ diffattn_status launch_join_of(const JoinParams &jp, cudaStream_t stream) {
 
 template <int kD>
 diffattn_status launch_join(const JoinParams &jp, cudaStream_t stream) {
-  const int plane = plane_rows(jp.row_tile);
-  return plane == 1   ? launch_join_of<kD, 1>(jp, stream)
+  const int plane = jp.weight_blocks ? plane_rows(jp.row_tile) : 0;
+  return plane == 0   ? launch_join_of<kD, 0>(jp, stream)
+         : plane == 1   ? launch_join_of<kD, 1>(jp, stream)
          : plane == 2 ? launch_join_of<kD, 2>(jp, stream)
                       : launch_join_of<kD, 4>(jp, stream);
 }
