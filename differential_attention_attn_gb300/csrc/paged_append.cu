@@ -11,6 +11,8 @@
 // and written) and the chain length -> page number -> store for a few tokens.
 // A row of k1 | k2 | v is 32 (d = 64) or 64 sixteen-byte units, so each lane of
 // a warp moves one or two of them and every access is a full 128-byte line.
+// Measured on GB300: 131072 rows at d = 64 (135 MB) 26.2 us, 76 % of the copy
+// rate; 65536 rows at d = 128 22 us, 90 %; one token of 64 x 16 heads 1.9 us.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -63,8 +65,8 @@ __device__ __forceinline__ uint4 to_e4m3(const uint4 &a, const uint4 &b) {
 // shortest chain for a few new tokens; otherwise only once they are known to be no padding, which
 // costs a prompt without padding less than eager loads cost one of which half is padding (65568
 // rows of e4m3 keys at d = 128: 14.2 us, eager 21.4).  Two rows a warp suit bf16 (131072 rows at
-// d = 64: 26.2 us, one 27.2), where a lane holds one or two units of each.  With e4m3 it holds up to
-// four, and one row is as good (the case above with two: 14.4 us).
+// d = 64: 26.2 us, one 27.2), where a lane holds one or two units of each.  With e4m3 it holds up
+// to four, and one row is as good (the case above with two: 14.4 us).
 template <int kD, bool kFp8, int kRows, bool kEager>
 __global__ void __launch_bounds__(kWarps * 32, kRows == 1 ? 8 : 6)
     diffpaged_append_kernel(const AppendParams p) {

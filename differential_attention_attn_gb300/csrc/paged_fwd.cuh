@@ -25,7 +25,7 @@
 //     192 KB in all: the keys of both maps (d = 64 or e4m3), one map's keys or
 //     128 value columns.  The copies leave L2 first (evict_first): a cache is
 //     read once a step, and without the hint it pushes out even the kernel's
-//     code (8 x 8K keys: 55 -> 51 us).
+//     code (8 x 8K keys: 55 -> 51 us).  A third warp fetches the q rows.
 //   - One warp issues the products, keys and value columns on the 128-row side
 //     of tcgen05.mma, where the tile fills it, and the few rows r on the other:
 //       S_m^T = K_m Q_m^T            (128 keys x rows)
@@ -35,7 +35,11 @@
 //     The reference maximum moves only when some logit passes it by 2^8: one
 //     barrier with a vote per tile instead of a reduction over the keys.
 //   - The end of a segment (a CTA's part of an item) is done after the next
-//     tile's softmax, so that its last product runs meanwhile.
+//     tile's softmax, so that its last product runs meanwhile.  Its code and
+//     that of the first tile run once or a few times a call, so they are kept
+//     short: fetching them costs more than executing them (three tiles of 20
+//     rows, with each row's sums reduced in turn and inlined: 18.9 us, with
+//     all rows in one exchange: 14.4 us).
 //   - P enters the second product as bf16 hi + lo side by side (relative
 //     error 2^-17): o1 - lambda o2 cancels and the head norm scales the
 //     difference back up, so a plain bf16 P would show; the wider product is
@@ -43,12 +47,13 @@
 //
 // Measured on GB300 (device time of a call, join included; the copy rate is
 // 6.78 TB/s): 32 heads x 16384 keys in pages of 64, 268 MB: 47 us, 84 % of it;
-// 8 sequences x 8 heads x 8192 keys at d = 128, 537 MB: 86 us, 92 %; 24
+// 8 sequences x 8 heads x 8192 keys at d = 128, 537 MB: 84 us, 94 %; 24
 // sequences of 100 to 9001 keys in pages of 16, four query heads to a key/value
-// head, 448 MB: 75 us, 87 %; one sequence of 200 keys, 16 heads: 6.5 us, of
-// which 2.5 us pass before the first copy lands.  Of a large call's time beyond
-// the copy rate about 3 us go to the first lookups and copies and 3 us to the
-// join; with 32 rows the softmax bounds it (8 x 8K keys, 86 us).
+// head, 448 MB: 76 us, 87 %; 8 x 8 x 32768 keys, 1.07 GB: 163 to 167 us, 95 to
+// 97 %; one sequence of 200 keys, 16 heads: 6.0 us, of which 2.5 us pass before
+// the first copy lands.  Of a large call's time beyond the copy rate about 3 us
+// go to the first lookups and copies and 3 us to the join; with 32 rows the
+// softmax bounds it (8 x 8K keys: 16 rows 53 us, 32 rows 83 us).
 #pragma once
 
 #include <cuda_bf16.h>
