@@ -19,9 +19,9 @@
 //      rows' places are fetched while a block of rows is on its way.
 //
 // Bound: HBM, each kept row read and written once.  16 x 8 heads of 8000 to 8192
-// keys at d = 64 cut to 4096 (543 MB): 109 us, the selection 14 us of it and the
-// move 92 us, 87 % of the copy rate; 4 x 16 heads of e4m3 keys cut from 1088 to
-// 1024: 18 us, 5.5 us the selection.
+// keys at d = 64 cut to 4096 (543 MB): 103 us, the selection 14 us of it and the
+// move 86 us, 93 % of the copy rate; 4 x 16 heads of e4m3 keys cut from 1088 to
+// 1024: 16 us, 5.5 us the selection.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -37,9 +37,13 @@ namespace {
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048 / kSelectThreads;  // of a histogram, per thread
-constexpr int kMoveThreads = 256;
-constexpr int kBatch = 4;   // 16-byte units of a thread in a block of rows
-constexpr int kAhead = 3;   // blocks of rows in flight
+// 256 rows of a slice a block, two blocks in flight: 103 us for 16 x 8 heads of 8192 keys halved;
+// with 256 threads (128 rows, three in flight) 110 us, with slices of 64 bytes 109 us (but 25 us for
+// 30 where there are only eight heads), of 256 bytes 129 us.
+constexpr int kMoveThreads = 1024;
+constexpr int kBatch = 2;   // 16-byte units of a thread in a block of rows
+constexpr int kAhead = 2;   // blocks of rows in flight
+constexpr size_t kRingBytes = size_t{16} * kAhead * kBatch * kMoveThreads;
 constexpr int kHeld = 16384;  // weights that the selection holds in shared memory
 constexpr int kMostSlices = 8;  // 128-byte columns of k1, k2 and v rows: 8 d bytes, d <= 128
 
@@ -253,7 +257,8 @@ __global__ void __launch_bounds__(kMoveThreads) diffpaged_move_kernel(const Evic
   // A ring of row blocks in shared memory.  A thread stores what it loaded itself; the barrier
   // makes every source of a block be read before any of its places is written, and the sources of
   // the blocks after lie behind those places.
-  __shared__ uint4 ring[kAhead][kBatch][kMoveThreads];
+  extern __shared__ uint4 ring_raw[];
+  auto *ring = reinterpret_cast<uint4(*)[kBatch][kMoveThreads]>(ring_raw);
   int2 from[kBatch];  // places of the next block's rows
   const auto look_up = [&](int32_t first) {
 #pragma unroll
@@ -386,7 +391,9 @@ diffattn_status launch_paged_evict(const diffattn_desc &desc, const diffpaged_ca
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DIFFATTN_ERR_CUDA;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(diffpaged_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(sizeof(float) * kHeld)) != cudaSuccess)
+                             static_cast<int>(sizeof(float) * kHeld)) != cudaSuccess ||
+        cudaFuncSetAttribute(diffpaged_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kRingBytes)) != cudaSuccess)
       return DIFFATTN_ERR_CUDA;
     attr_set[dev].store(true, std::memory_order_release);
   }
@@ -396,7 +403,7 @@ diffattn_status launch_paged_evict(const diffattn_desc &desc, const diffpaged_ca
   if (cudaLaunchKernelEx(&cfg, diffpaged_select_kernel, p) != cudaSuccess) return DIFFATTN_ERR_CUDA;
   cfg.gridDim = dim3(static_cast<unsigned>(items) * slices);
   cfg.blockDim = dim3(kMoveThreads);
-  cfg.dynamicSmemBytes = 0;
+  cfg.dynamicSmemBytes = kRingBytes;
   return cudaLaunchKernelEx(&cfg, diffpaged_move_kernel, p, slices) == cudaSuccess
              ? DIFFATTN_OK
              : DIFFATTN_ERR_CUDA;
