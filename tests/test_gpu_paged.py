@@ -257,6 +257,36 @@ def test_accumulated_weights(lens, H, kv, N, d, page, dtype):
     assert torch.equal(c.weights, after)
 
 
+@pytest.mark.parametrize("lens,H,kv,N,d,page,causal", [
+    ([20001], 1, 1, 1, 64, 64, True),          # an item cut over every CTA
+    ([9000, 0, 300], 3, 1, 1, 64, 64, True),   # a plane of three rows
+    ([700, 3, 260], 10, 2, 1, 64, 16, True),   # five rows
+    ([700, 1, 500], 7, 1, 2, 128, 16, False),  # fourteen rows, some see no key
+    ([1300, 30], 40, 1, 1, 64, 16, True),      # two row blocks
+    ([90, 10], 64, 1, 16, 64, 16, True),       # 32 row blocks
+    ([70000, 100], 16, 2, 1, 64, 64, True),    # logits past what L2 holds back
+])
+def test_accumulated_weights_by_rows_and_parts(lens, H, kv, N, d, page, causal):
+    c = R.Cache(33, lens=lens, kv=kv, d=d, page=page, weights=True)
+    before = c.weights.clone()
+    old = [c.rows("weights", b).double() for b in range(c.B)]
+    q1, q2, lam, w = R.queries(34, c.B, H, N, d)
+    lam[0] = 0.0
+    out = _fwd(c, q1, q2, lam, w, accumulate=True, causal=causal)
+    ref, tol, add, add_tol = R.attend(c, q1, q2, lam, norm_w=w, lambda_init=LI, causal=causal)
+    R.check(out, ref, tol, "out")
+    for b, n in enumerate(lens):
+        if n:
+            want = old[b] + add[b]
+            tol_w = add_tol[b] + want.abs() * (H // kv * N + 2) * 2.0 ** -23
+            R.check(c.rows("weights", b), want, tol_w, f"weights of sequence {b}")
+    after = c.weights.clone()
+    for _ in range(3):  # the same bits again, in memory that the call before has used
+        c.weights.copy_(before)
+        assert torch.equal(_fwd(c, q1, q2, lam, w, accumulate=True, causal=causal), out)
+        assert torch.equal(c.weights, after)
+
+
 # ---- bad pages and lengths ------------------------------------------------------------------
 
 @pytest.mark.parametrize("lens", [[100, 90, 33], [1000, 900, 33]])
