@@ -690,7 +690,7 @@ class PagedCache:
         self.device, self.dtype = k1.device, k1.dtype
         self.index = k1.get_device()
         self.code = E4M3_QK if k1.dtype == torch.float8_e4m3fn else BF16
-        self._descs = {}
+        self._calls = {}
         self._struct = PagedCacheStruct(
             k1.data_ptr(), k2.data_ptr(), v.data_ptr(),
             0 if weights is None else weights.data_ptr(), page_table.data_ptr(),
@@ -698,19 +698,46 @@ class PagedCache:
             page, 0)
         self._ref = ctypes.byref(self._struct)
 
-    def _desc(self, H, N, causal, headnorm, eps, lambda_init, status):
-        """The descriptor of a call; without a status word made once per set of values."""
-        if status is not None:
-            return ctypes.byref(make_desc(self.B, H, N, self.d, self.code, causal, headnorm, eps,
-                                          lambda_init, status))
-        key = (H, N, causal, headnorm, eps, lambda_init)
-        ref = self._descs.get(key)
-        if ref is None:
-            if len(self._descs) >= 256:
-                self._descs.clear()
-            ref = self._descs[key] = ctypes.byref(
-                make_desc(self.B, H, N, self.d, self.code, causal, headnorm, eps, lambda_init))
-        return ref
+    # What a call's shapes and numbers come to (its descriptor, the shapes of its other tensors, its
+    # workspace) is worked out and checked once, and kept under them; with a status word, each time.
+
+    def _keep(self, key, status, call):
+        if status is None:
+            if len(self._calls) >= 256:
+                self._calls.clear()
+            self._calls[key] = call
+        return call
+
+    def _new_append(self, shape, status):
+        if len(shape) != 4 or shape[0] != self.B or shape[1] != self.kv_heads or \
+                shape[3] != self.d:
+            raise ValueError(f"k1 and k2 must be [{self.B}, {self.kv_heads}, N, {self.d}], "
+                             f"v [{self.B}, {self.kv_heads}, N, {2 * self.d}]")
+        desc = make_desc(self.B, self.kv_heads, shape[2], self.d, self.code, True, 0, 0.0, 0.0,
+                         status)
+        return self._keep(shape, status, (ctypes.byref(desc), (*shape[:3], 2 * self.d)))
+
+    def _new_fwd(self, key, status):
+        shape, causal, headnorm, eps, lambda_init, accumulate = key
+        if len(shape) != 4 or shape[0] != self.B or shape[3] != self.d:
+            raise ValueError(f"q1 and q2 must be [{self.B}, H, N, {self.d}]")
+        H, N = shape[1], shape[2]
+        ref = ctypes.byref(make_desc(self.B, H, N, self.d, self.code, causal, headnorm, eps,
+                                     lambda_init, status))
+        need = ctypes.c_size_t(0)
+        st = load().diffpaged_fwd_plan(ref, self._ref, int(accumulate), ctypes.byref(need))
+        if st != OK:
+            return st, None
+        return OK, self._keep(key, status, (ref, (self.B, H, N, 2 * self.d), H, need.value))
+
+    def _new_evict(self, keep, status):
+        ref = ctypes.byref(make_desc(self.B, self.kv_heads, 0, self.d, self.code, True, 0, 0.0,
+                                     0.0, status))
+        need = ctypes.c_size_t(0)
+        st = load().diffpaged_evict_plan(ref, self._ref, keep, ctypes.byref(need))
+        if st != OK:
+            return st, None
+        return OK, self._keep(keep, status, (ref, need.value))
 
 
 def _strides4(t):
@@ -771,10 +798,10 @@ def paged_append(cache, k1, k2, v, *, status=None, stream=None, raw_status: bool
     [B, kv_heads, N, 2d]; views of any layout with contiguous rows.
     """
     shape = k1.shape
-    B, H, d = cache.B, cache.kv_heads, cache.d
-    if len(shape) != 4 or shape[0] != B or shape[1] != H or shape[3] != d or \
-            k2.shape != shape or v.shape != (B, H, shape[2], 2 * d):
-        raise ValueError(f"k1 and k2 must be [{B}, {H}, N, {d}], v [{B}, {H}, N, {2 * d}]")
+    call = cache._calls.get(shape) if status is None else None
+    ref, v_shape = call or cache._new_append(shape, status)
+    if k2.shape != shape or v.shape != v_shape:
+        raise ValueError(f"k2 must be {tuple(shape)}, as k1, and v {v_shape}")
     dtype, index = torch.bfloat16, cache.index
     if k1.dtype != dtype or k2.dtype != dtype or v.dtype != dtype:
         raise ValueError("k1, k2 and v must be bfloat16")
@@ -782,9 +809,8 @@ def paged_append(cache, k1, k2, v, *, status=None, stream=None, raw_status: bool
         raise ValueError("all tensors must be on the cache's device")
     strides = _strides_or_null(k1, k2, v)
     handle = _stream_on(cache, stream)
-    st = (_lib or load()).diffpaged_append(
-        cache._desc(H, shape[2], True, 0, 0.0, 0.0, status), cache._ref, k1.data_ptr(),
-        k2.data_ptr(), v.data_ptr(), strides, handle)
+    st = (_lib or load()).diffpaged_append(ref, cache._ref, k1.data_ptr(), k2.data_ptr(),
+                                           v.data_ptr(), strides, handle)
     if raw_status:
         return st
     _check(st)
@@ -814,40 +840,38 @@ def paged_fwd(cache, q1, q2, lam, *, causal: bool = True, headnorm: int = 1, nor
     workspace: a CUDA tensor of at least paged_fwd_plan bytes (a torch buffer when None).
     Returns bf16 out [B, H, N, 2d] (of `stream`'s memory when allocated here).
     """
-    shape, d, index, f32 = q1.shape, cache.d, cache.index, torch.float32
-    if len(shape) != 4 or shape[0] != cache.B or shape[3] != d or q2.shape != shape:
-        raise ValueError(f"q1 and q2 must be [{cache.B}, H, N, {d}]")
-    H, N = shape[1], shape[2]
-    if q1.dtype != cache.dtype or q2.dtype != cache.dtype:
-        raise ValueError(f"q1 and q2 must be {cache.dtype}, as the cache's keys")
-    if q1.get_device() != index or q2.get_device() != index or lam.get_device() != index:
-        raise ValueError("all tensors must be on the cache's device")
-    if lam.dtype != f32 or lam.numel() != H or not lam.is_contiguous():
-        raise ValueError("lam must be contiguous float32 [H]")
-    if norm_w is not None and (norm_w.dtype != f32 or norm_w.numel() != H * 2 * d or
-                               not norm_w.is_contiguous() or norm_w.get_device() != index):
-        raise ValueError("norm_w must be contiguous float32 [H, 2d] on the cache's device")
-    handle = _stream_on(cache, stream)
-    if out is None:
-        out = _new_on(stream, (shape[0], H, N, 2 * d), torch.bfloat16, cache.device)
-    elif out.shape != (shape[0], H, N, 2 * d) or out.dtype != torch.bfloat16 or \
-            out.get_device() != index:
-        raise ValueError("out must be bfloat16 [B, H, N, 2d] on the cache's device")
-    strides = _strides_or_null(q1, q2, out)
-    ref = cache._desc(H, N, causal, headnorm, eps, lambda_init, status)
-    lib, need = _lib or load(), 0
-    if workspace is None:
-        n = ctypes.c_size_t(0)
-        st = lib.diffpaged_fwd_plan(ref, cache._ref, int(accumulate), ctypes.byref(n))
+    key = (q1.shape, causal, headnorm, eps, lambda_init, accumulate)
+    call = cache._calls.get(key) if status is None else None
+    if call is None:
+        st, call = cache._new_fwd(key, status)
         if st != OK:
             if raw_status:
                 return st
             _check(st)
-        need = n.value
-    ws, ws_bytes, _keep = _workspace(workspace, need, cache, stream)
-    st = lib.diffpaged_fwd(ref, cache._ref, q1.data_ptr(), q2.data_ptr(), lam.data_ptr(),
-                           None if norm_w is None else norm_w.data_ptr(), out.data_ptr(),
-                           strides, int(accumulate), ws, ws_bytes, handle)
+    ref, out_shape, H, need = call
+    index, dtype, f32 = cache.index, cache.dtype, torch.float32
+    if q2.shape != q1.shape:
+        raise ValueError(f"q2 must be {tuple(q1.shape)}, as q1")
+    if q1.dtype != dtype or q2.dtype != dtype:
+        raise ValueError(f"q1 and q2 must be {dtype}, as the cache's keys")
+    if q1.get_device() != index or q2.get_device() != index or lam.get_device() != index:
+        raise ValueError("all tensors must be on the cache's device")
+    if lam.dtype != f32 or lam.numel() != H or not lam.is_contiguous():
+        raise ValueError("lam must be contiguous float32 [H]")
+    if norm_w is not None and (norm_w.dtype != f32 or norm_w.numel() != H * out_shape[3] or
+                               not norm_w.is_contiguous() or norm_w.get_device() != index):
+        raise ValueError("norm_w must be contiguous float32 [H, 2d] on the cache's device")
+    handle = _stream_on(cache, stream)
+    if out is None:
+        out = _new_on(stream, out_shape, torch.bfloat16, cache.device)
+    elif out.shape != out_shape or out.dtype != torch.bfloat16 or out.get_device() != index:
+        raise ValueError("out must be bfloat16 [B, H, N, 2d] on the cache's device")
+    strides = _strides_or_null(q1, q2, out)
+    ws, ws_bytes, _hold = _workspace(workspace, need, cache, stream)
+    st = (_lib or load()).diffpaged_fwd(
+        ref, cache._ref, q1.data_ptr(), q2.data_ptr(), lam.data_ptr(),
+        None if norm_w is None else norm_w.data_ptr(), out.data_ptr(), strides, int(accumulate),
+        ws, ws_bytes, handle)
     if raw_status:
         return st
     _check(st)
@@ -869,16 +893,17 @@ def paged_evict(cache, *, keep: int, recent: int = 0, workspace=None, status=Non
                 raw_status: bool = False):
     """`diffpaged_evict`: cut every sequence longer than `keep` to its last `recent` keys and
     the keep - recent of the largest weights, in place; updates cache.kv_len."""
-    handle, need = _stream_on(cache, stream), 0
-    if workspace is None:
-        st, need = paged_evict_plan(cache, keep=keep, raw_status=True)
+    handle, keep = _stream_on(cache, stream), int(keep)
+    call = cache._calls.get(keep) if status is None else None
+    if call is None:
+        st, call = cache._new_evict(keep, status)
         if st != OK:
             if raw_status:
                 return st
             _check(st)
-    ws, ws_bytes, _keep = _workspace(workspace, need, cache, stream)
-    ref = cache._desc(cache.kv_heads, 0, True, 0, 0.0, 0.0, status)
-    st = (_lib or load()).diffpaged_evict(ref, cache._ref, int(keep), int(recent), ws, ws_bytes,
+    ref, need = call
+    ws, ws_bytes, _hold = _workspace(workspace, need, cache, stream)
+    st = (_lib or load()).diffpaged_evict(ref, cache._ref, keep, int(recent), ws, ws_bytes,
                                           handle)
     if raw_status:
         return st
