@@ -21,7 +21,8 @@ constexpr int kPagedMaxGroup = 64;
 
 struct PagedFwdPlan {
   int ctas;        // CTAs of the main kernel
-  bool whole;      // one CTA per item (nothing to join); else equal shares of all tiles
+  bool whole;      // one CTA per item; else equal shares of all tiles,
+  bool cut;        // which may cut items (the second kernel joins those) or not
   int row_tile;    // rows of a block
   int row_blocks;  // row blocks per key/value head
   int64_t items;   // B * kv_heads * row_blocks

@@ -36,6 +36,7 @@ __device__ __forceinline__ Parts parts_of(const Shares &all, uint32_t start, uin
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 constexpr int kMaxParts = 256;       // more than SMs
+constexpr int64_t kUneven = 5;       // steps, see plan_paged_fwd
 constexpr int kMaxRowBlocks = kPagedMaxTokens * kPagedMaxGroup / 32;
 static_assert(kMaxRowBlocks <= 32, "a lane each");
 constexpr int kWeightBlocks = 912;  // in all, about: two rounds of three per SM
@@ -247,7 +248,7 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
   // maps, 1 (0 for a row that sees no key and adds nothing) and lambda.
   if (warp == 0) {
     Parts parts = {0, 1};
-    if (!p.whole) {
+    if (p.cut) {
       uint32_t before;
       const Shares all = all_shares(p, jp.ctas, b, &before);
       const uint32_t units = units_of(len, most);
@@ -520,7 +521,14 @@ bool plan_paged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache, boo
   q.ctas = q.whole ? static_cast<int>(q.items) : sm_count;
   if (!q.whole && q.items * (units + kItemCost) < sm_count)
     q.ctas = static_cast<int>(q.items * (units + kItemCost));
-  const size_t slots = q.whole ? 0 : 2 * static_cast<size_t>(q.ctas);
+  // Nor are items cut where they are so many, or so short, that taking them whole makes the longest
+  // share at most kUneven steps longer, which costs less than the join.  408 items of two tiles (8
+  // rows): 19.8 us, cut 24.7; 1024 of two: 25.5 and 28.2; 228 of six (32 rows, d = 128): 58 and 69;
+  // 240 of ten, where it would be 5.05 steps: 26.8 and 25.1 us.
+  const int64_t per = (q.items + sm_count - 1) / sm_count;
+  q.cut = !q.whole && !(q.items > sm_count &&
+                        (units + kItemCost) * (per * sm_count - q.items) <= kUneven * sm_count);
+  const size_t slots = q.cut ? 2 * static_cast<size_t>(q.ctas) : 0;
   size_t at = 0;
   const auto take = [&at](size_t bytes) {
     const size_t here = at;
@@ -579,11 +587,12 @@ diffattn_status launch_paged_fwd(const diffattn_desc &desc, const diffpaged_cach
   p.causal = desc.causal ? 1 : 0;
   p.headnorm = desc.headnorm;
   p.whole = plan.whole ? 1 : 0;
+  p.cut = plan.cut ? 1 : 0;
   p.eps = desc.eps;
   p.out_scale = 1.0f - desc.lambda_init;
   p.scale_log2 = kLog2e / std::sqrt(static_cast<float>(d));
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  if (!plan.whole) {
+  if (plan.cut) {
     p.part = reinterpret_cast<float *>(ws + plan.part);
     p.part_ml = reinterpret_cast<float2 *>(ws + plan.stats);
   }
@@ -610,7 +619,7 @@ diffattn_status launch_paged_fwd(const diffattn_desc &desc, const diffpaged_cach
   jp.row_tile = plan.row_tile;
   jp.join_rows = p.rows < jp.row_tile ? p.rows : jp.row_tile;
   // Cut items are at most one per boundary.
-  const int64_t cuts = plan.whole ? 0 : plan.ctas - 1;
+  const int64_t cuts = plan.cut ? plan.ctas - 1 : 0;
   jp.by_item = plan.items < cuts ? 1 : 0;
   jp.joins = static_cast<uint32_t>((jp.by_item ? plan.items : cuts) * jp.join_rows);
   jp.discard = plan.bytes - plan.logits >= kDiscardBytes ? 1 : 0;

@@ -19,7 +19,8 @@
 //     from kv_len on the device; a ragged batch is balanced and a graph
 //     replays with new lengths.  Items cut by a CTA boundary leave partial
 //     states, which a second kernel (launched dependent on the first) joins.
-//     With few tiles in all, one CTA takes each item and nothing is joined.
+//     With few tiles in all one CTA takes each item, and many short items are
+//     not cut either: nothing is joined then.
 //   - Two warps issue TMA copies of page pieces (16 to 64 rows, by the page
 //     size), one of keys and one of values, into rings of 32 KB buffers, 128 to
 //     192 KB in all: the keys of both maps (d = 64 or e4m3), one map's keys or
@@ -79,7 +80,8 @@ struct FwdParams {
   diffattn_strides q1s, q2s, outs, vs;
   int32_t B, H, N, kv_heads, group, rows;  // rows = N * group
   int32_t num_pages, max_pages, page_size, piece_rows;
-  int32_t row_blocks, causal, headnorm, whole;
+  int32_t row_blocks, causal, headnorm;
+  int32_t whole, cut;  // one CTA per item; items may be cut by shares (else neither or whole)
   FastDiv by_page, by_group;  // page_size, group
   float eps, out_scale, scale_log2;
   // Workspace (see PagedFwdPlan): partial O [2 C][2][NR][2 d] and their (m, l), and for accumulate
@@ -427,13 +429,23 @@ __device__ __forceinline__ Share find_share(const FwdParams &p, uint32_t cta, ui
   return s;
 }
 
-// A load warp's place in its share.
+// A load warp's place in its share.  Where items are not cut, a share has those that begin in it.
 struct Walk {
   int32_t b, hk, rb, len, units;
   int32_t tile, end;  // the tile, and the share's end, in tiles of the current item
-  __device__ __forceinline__ explicit Walk(const Share &s)
+  __device__ __forceinline__ Walk(const FwdParams &p, const Share &s)
       : b(s.b), hk(s.hk), rb(s.rb), len(s.len), units(s.units), tile(max(0, s.off - kItemCost)),
-        end(s.end - kItemCost) {}
+        end(s.end - kItemCost) {
+    if (!p.cut) {
+      if (s.off > 0)
+        next_item(p);
+      else
+        take_whole(p);
+    }
+  }
+  __device__ __forceinline__ void take_whole(const FwdParams &p) {
+    if (!p.cut && end > -kItemCost) end = max(end, units);
+  }
   // To the next item with a tile in the share (the first may be cut before its tiles).
   __device__ __forceinline__ void next_item(const FwdParams &p) {
     end -= units + kItemCost;
@@ -443,12 +455,13 @@ struct Walk {
       if (++hk == p.kv_heads) {
         hk = 0;
         ++b;
-        if (end > 0) {
+        if (end > (p.cut ? 0 : -kItemCost)) {
           len = __ldg(p.kv_len + b);
           units = units_of(len, p.max_pages * p.page_size);
         }
       }
     }
+    take_whole(p);
   }
 };
 
@@ -480,7 +493,7 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
   // on, so that what it reads before it waits for this one is what this one reads.
   grid_dependency_wait();
   named_barrier_arrive(kStartBarrier, 96 + G::kConsumers);
-  Walk w(find_share(p, blockIdx.x, gridDim.x));
+  Walk w(p, find_share(p, blockIdx.x, gridDim.x));
   int32_t &b = w.b, &hk = w.hk, &rb = w.rb, &len = w.len, &units = w.units, &tile = w.tile,
           &end = w.end;
   grid_dependents_launch();
@@ -610,7 +623,7 @@ __device__ __forceinline__ void query_warp(const FwdParams &p, uint8_t *smem, Ct
   constexpr int kUnits = G::kKeyRow / 16;
   const int lane = threadIdx.x % 32;
   grid_dependency_wait();
-  Walk w(find_share(p, blockIdx.x, gridDim.x));
+  Walk w(p, find_share(p, blockIdx.x, gridDim.x));
   named_barrier_sync(kLoadBarrier, 96 + G::kConsumers);
 #pragma unroll 1
   for (uint32_t seg = 0; w.tile < w.end; ++seg) {

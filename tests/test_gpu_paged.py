@@ -560,6 +560,40 @@ def test_capacity_far_beyond_the_lengths(lens, kv, H):
                 add_tol[b] + (old + add[b]) * (H // kv + 2) * 2.0 ** -23, "weights")
 
 
+@pytest.mark.parametrize("d,dtype,H,N,top", [
+    (64, torch.bfloat16, 2, 1, 130), (128, E4M3, 4, 3, 40), (64, E4M3, 40, 1, 130),
+    (128, torch.bfloat16, 2, 1, 700)])
+def test_many_short_items(d, dtype, H, N, top):
+    """More items than SMs, taken whole (or cut, the longest): idle sequences and bad ones among
+    them, with weights and without."""
+    g = torch.Generator().manual_seed(118)
+    lens = torch.randint(0, top + 1, (190,), generator=g).tolist()
+    lens[:5] = [0, 1, top, 0, top - 1]
+    lens[-2:] = [top, 0]
+    c = R.Cache(119, lens=lens, kv=2, d=d, page=16, dtype=dtype, weights=True)
+    out = _parity(c, H, N)
+    before = c.weights.clone()
+    q1, q2, lam, w = R.queries(3, c.B, H, N, d, dtype)
+    assert torch.equal(_fwd(c, q1, q2, lam, w, accumulate=True), out)
+    _, _, add, add_tol = R.attend(c, q1, q2, lam, norm_w=w, lambda_init=LI)
+    after = c.weights
+    for b in (1, 2, 4, 90, 188):
+        if lens[b]:
+            c.weights = before
+            want = c.rows("weights", b).double() + add[b]
+            c.weights = after
+            R.check(c.rows("weights", b), want,
+                    add_tol[b] + want.abs() * (H // 2 * N + 2) * 2.0 ** -23, f"weights of {b}")
+    page = c.table[2, 0].item()
+    c.table[2, 0] = -7
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = ops.paged_fwd(c.ops_cache(), q1, q2, lam, norm_w=w, lambda_init=LI, status=status)
+    assert int(status) == ops.ERR_PAGE and bool(torch.isnan(got[2]).all())
+    got[2] = out[2]
+    assert torch.equal(got, out)
+    c.table[2, 0] = page
+
+
 def test_two_row_blocks_share_a_head():
     """40 and 64 rows a key/value head, joined, with weights over all of them."""
     for H, N in ((40, 1), (16, 4)):
