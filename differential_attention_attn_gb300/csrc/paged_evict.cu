@@ -12,7 +12,7 @@
 //      value T and how many equal to T still fit; a scan in position order
 //      then writes the list of kept places and moves the weights.  Up to
 //      16384 weights are held in shared memory, more in the workspace.
-//   2. Move (one block per item and 128-byte column slice of k1, k2, v).  A
+//   2. Move (one block per item and column slice of k1, k2, v).  A
 //      kept row's place is at or before its source, and sources ascend, so
 //      blocks of rows taken in order only need all loads of a block before
 //      its stores; the slices are independent of one another.  The next
@@ -38,8 +38,8 @@ constexpr int kSelectThreads = 1024;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048 / kSelectThreads;  // of a histogram, per thread
 // 256 rows of a slice a block, two blocks in flight: 103 us for 16 x 8 heads of 8192 keys halved;
-// with 256 threads (128 rows, three in flight) 110 us, with slices of 64 bytes 109 us (but 25 us for
-// 30 where there are only eight heads), of 256 bytes 129 us.
+// with 256 threads (128 rows, three in flight) 110 us, with slices of 64 bytes 109 us, of 256 bytes
+// 129 us.
 constexpr int kMoveThreads = 1024;
 constexpr int kBatch = 2;   // 16-byte units of a thread in a block of rows
 constexpr int kAhead = 2;   // blocks of rows in flight
@@ -51,6 +51,7 @@ struct EvictParams {
   uint8_t *pool[3];
   int64_t page_b[3], head_b[3], row_b[3];  // strides in bytes
   int32_t width_b[3];                      // bytes of a row
+  int32_t slice_b;                         // of them a block of the move takes
   float *weights;
   const int32_t *page_table;
   int32_t *kv_len;
@@ -235,17 +236,21 @@ __global__ void __launch_bounds__(kSelectThreads) diffpaged_select_kernel(const 
   }
 }
 
+__host__ __device__ __forceinline__ int32_t slices_of(int32_t width, int32_t slice) {
+  return (width + slice - 1) / slice;
+}
+
 __global__ void __launch_bounds__(kMoveThreads) diffpaged_move_kernel(const EvictParams p,
                                                                       int slices) {
   const int item = blockIdx.x / slices;
   int slice = blockIdx.x - item * slices;
   const int b = item / p.kv_heads, hk = item - b * p.kv_heads;
   int t = 0;
-  while (slice >= (p.width_b[t] + 127) / 128) slice -= (p.width_b[t++] + 127) / 128;
-  const int units = p.width_b[t] < 128 ? p.width_b[t] / 16 : 8;  // 16-byte units of the slice
+  while (slice >= slices_of(p.width_b[t], p.slice_b)) slice -= slices_of(p.width_b[t++], p.slice_b);
+  const int units = min(p.width_b[t], p.slice_b) / 16;  // 16-byte units of the slice
   const int unit = threadIdx.x & (units - 1), line = threadIdx.x / units;
   const int lines = kMoveThreads / units;  // rows taken side by side
-  uint8_t *base = p.pool[t] + hk * p.head_b[t] + slice * 128 + unit * 16;
+  uint8_t *base = p.pool[t] + hk * p.head_b[t] + slice * p.slice_b + unit * 16;
   const int64_t page_b = p.page_b[t], row_b = p.row_b[t];
   const int32_t *table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
   const int2 *list = p.list + static_cast<int64_t>(item) * p.keep;
@@ -358,7 +363,15 @@ diffattn_status launch_paged_evict(const diffattn_desc &desc, const diffpaged_ca
     p.head_b[t] = es * st[t]->h;
     p.row_b[t] = es * st[t]->n;
     p.width_b[t] = static_cast<int32_t>(es * (t == 2 ? 2 * desc.d : desc.d));
-    slices += (p.width_b[t] + 127) / 128;
+  }
+  // Slices of 128 bytes, narrower ones (down to a sector) while some SMs would have none: 8192 keys
+  // halved, 8 heads 30.5 -> 23.5 us, 32 heads 46.7 -> 41 us.
+  const int sms = device_sm_count();
+  if (sms <= 0) return DIFFATTN_ERR_CUDA;
+  for (p.slice_b = 128;; p.slice_b /= 2) {
+    slices = 0;
+    for (int t = 0; t < 3; ++t) slices += slices_of(p.width_b[t], p.slice_b);
+    if (p.slice_b == 32 || desc.B * cache.kv_heads * slices > sms) break;
   }
   p.weights = cache.weights;
   p.page_table = cache.page_table;
