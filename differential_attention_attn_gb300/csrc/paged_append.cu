@@ -10,8 +10,9 @@
 // Bound: a copy, so HBM bandwidth for prompts (B Hkv N rows of 8 d bytes read
 // and written) and the chain length -> page number -> store for a few tokens.
 // A row of k1 | k2 | v is 32 (d = 64) or 64 sixteen-byte units, so each lane of
-// a warp moves one or two of them and every access is a full 128-byte line.
-// Measured on GB300: 131072 rows at d = 64 (135 MB) 26.2 us, 76 % of the copy
+// a warp moves one or two of them (e4m3 keys leave as eight bytes each) and
+// every access fills its sectors.
+// Measured on GB300: 131072 rows at d = 64 (135 MB) 26.1 us, 76 % of the copy
 // rate; 65536 rows at d = 128 22 us, 90 %; one token of 64 x 16 heads 1.9 us.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -43,36 +44,29 @@ struct AppendParams {
   FastDiv by_n, by_heads, by_page;
 };
 
-// Eight bf16 values of each of two 16-byte units as sixteen e4m3 values.
-__device__ __forceinline__ uint4 to_e4m3(const uint4 &a, const uint4 &b) {
-  uint32_t out[4];
-  const uint32_t in[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+// Eight bf16 values as eight e4m3 values.
+__device__ __forceinline__ uint2 to_e4m3(const uint4 &a) {
+  const uint32_t in[4] = {a.x, a.y, a.z, a.w};
+  uint32_t half[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint16_t half[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t w = in[2 * i + j];
-      const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xFFFF0000u);
-      half[j] = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-    }
-    out[i] = static_cast<uint32_t>(half[0]) | (static_cast<uint32_t>(half[1]) << 16);
+    const float lo = __uint_as_float(in[i] << 16), hi = __uint_as_float(in[i] & 0xFFFF0000u);
+    half[i] = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
   }
-  return make_uint4(out[0], out[1], out[2], out[3]);
+  return make_uint2(half[0] | (half[1] << 16), half[2] | (half[3] << 16));
 }
 
 // A warp per kRows consecutive rows of a head.  kEager: loaded while their place is looked up, the
 // shortest chain for a few new tokens; otherwise only once they are known to be no padding, which
 // costs a prompt without padding less than eager loads cost one of which half is padding (65568
-// rows of e4m3 keys at d = 128: 14.2 us, eager 21.4).  Two rows a warp suit bf16 (131072 rows at
-// d = 64: 26.2 us, one 27.2), where a lane holds one or two units of each.  With e4m3 it holds up
-// to four, and one row is as good (the case above with two: 14.4 us).
+// rows of e4m3 keys at d = 128: 13.3 us, eager 21.4).  Two rows a warp: 131072 rows at d = 64 26.1
+// us, one 27.2; e4m3 keys 26.6 and 28.5 us, four rows 25.2 (but 13.5 us in the case above).
 template <int kD, bool kFp8, int kRows, bool kEager>
 __global__ void __launch_bounds__(kWarps * 32, kRows == 1 ? 8 : 6)
     diffpaged_append_kernel(const AppendParams p) {
-  constexpr int kKeyUnits = kFp8 ? kD / 16 : kD / 8;  // 16-byte units stored per key row
-  constexpr int kUnits = 2 * kKeyUnits + kD / 4;
-  constexpr int kPerLane = (kUnits + 31) / 32;
+  constexpr int kKeyUnits = kD / 8;  // 16-byte units of a key row
+  constexpr int kPerLane = (2 * kKeyUnits + kD / 4) / 32;
+  static_assert(kPerLane * 32 == 2 * kKeyUnits + kD / 4, "no idle lanes");
   const int lane = threadIdx.x % 32;
   const uint32_t group = blockIdx.x * kWarps + threadIdx.x / 32;
   if (group >= p.groups) return;
@@ -82,21 +76,16 @@ __global__ void __launch_bounds__(kWarps * 32, kRows == 1 ? 8 : 6)
   grid_dependents_launch();
   const int32_t len = __ldg(p.kv_len + b);
 
-  uint4 x[kRows][kPerLane], y[kRows][kPerLane];
+  uint4 x[kRows][kPerLane];
   int32_t page[kRows];
   const auto load = [&](int r) {
 #pragma unroll
     for (int u = 0; u < kPerLane; ++u) {
       const int unit = lane + 32 * u;
-      if (unit < kUnits) {
-        const int t = unit < kKeyUnits ? 0 : unit < 2 * kKeyUnits ? 1 : 2;
-        const int off = unit - t * kKeyUnits;
-        const bool wide = kFp8 && t < 2;  // sixteen bf16 in, sixteen bytes out
-        const uint8_t *s = p.src[t] + b * p.src_b[t] + h * p.src_h[t] + (i0 + r) * p.src_n[t] +
-                           off * (wide ? 32 : 16);
-        x[r][u] = __ldg(reinterpret_cast<const uint4 *>(s));
-        if (wide) y[r][u] = __ldg(reinterpret_cast<const uint4 *>(s) + 1);
-      }
+      const int t = unit < kKeyUnits ? 0 : unit < 2 * kKeyUnits ? 1 : 2;
+      const uint8_t *s = p.src[t] + b * p.src_b[t] + h * p.src_h[t] + (i0 + r) * p.src_n[t] +
+                         (unit - t * kKeyUnits) * 16;
+      x[r][u] = __ldg(reinterpret_cast<const uint4 *>(s));
     }
   };
   if (kEager)
@@ -127,13 +116,13 @@ __global__ void __launch_bounds__(kWarps * 32, kRows == 1 ? 8 : 6)
 #pragma unroll
     for (int u = 0; u < kPerLane; ++u) {
       const int unit = lane + 32 * u;
-      if (unit < kUnits) {
-        const int k = unit < kKeyUnits ? 0 : unit < 2 * kKeyUnits ? 1 : 2;
-        const int off = unit - k * kKeyUnits;
-        uint8_t *d = p.dst[k] + page[r] * p.dst_p[k] + h * p.dst_h[k] + slot * p.dst_n[k] +
-                     off * 16;
-        *reinterpret_cast<uint4 *>(d) = (kFp8 && k < 2) ? to_e4m3(x[r][u], y[r][u]) : x[r][u];
-      }
+      const int t = unit < kKeyUnits ? 0 : unit < 2 * kKeyUnits ? 1 : 2;
+      uint8_t *row = p.dst[t] + page[r] * p.dst_p[t] + h * p.dst_h[t] + slot * p.dst_n[t];
+      const int off = unit - t * kKeyUnits;
+      if (kFp8 && t < 2)
+        reinterpret_cast<uint2 *>(row)[off] = to_e4m3(x[r][u]);
+      else
+        reinterpret_cast<uint4 *>(row)[off] = x[r][u];
     }
     if (lane == 0 && p.weights != nullptr)
       p.weights[(static_cast<int64_t>(page[r]) * p.kv_heads + h) * p.page_size + slot] = 0.f;
@@ -160,7 +149,7 @@ cudaError_t launch_rows(AppendParams p, cudaStream_t stream) {
 template <int kD, bool kFp8>
 cudaError_t launch(const AppendParams &p, cudaStream_t stream) {
   return p.rows <= kFewRows ? launch_rows<kD, kFp8, 1, true>(p, stream)
-                            : launch_rows<kD, kFp8, kFp8 ? 1 : 2, false>(p, stream);
+                            : launch_rows<kD, kFp8, 2, false>(p, stream);
 }
 
 }  // namespace
