@@ -466,8 +466,8 @@ def test_captured_step_replays_with_new_lengths():
         c.kv_len.copy_(torch.tensor([100, 260], dtype=torch.int32))
     q1, q2, lam, w = R.queries(72, B, H, 1, d)
     g = torch.Generator().manual_seed(73)
-    steps = [[torch.randn(B, kv, 1, x, generator=g).to(torch.bfloat16).cuda() for x in (d, d, 2 * d)]
-             for _ in range(6)]
+    steps = [[torch.randn(B, kv, 1, x, generator=g).to(torch.bfloat16).cuda()
+              for x in (d, d, 2 * d)] for _ in range(6)]
     buf = [t.clone() for t in steps[0]]
 
     def step(cache, kv_len, new):
@@ -530,6 +530,48 @@ def test_empty_calls():
     ops.paged_append(cache, k, k, torch.empty(1, 2, 0, 128, dtype=torch.bfloat16, device="cuda"))
     ops.paged_evict(cache, keep=16)
     assert c.kv_len.tolist() == [5]
+
+
+def test_calls_that_do_not_fit_are_refused():
+    """Wrong shapes, types, devices, layouts and workspaces, also right after a good call of the
+    same numbers; nothing is launched."""
+    c = R.Cache(92, lens=[40, 7], kv=2, d=64, page=16, weights=True)
+    cache = c.ops_cache()
+    q1, q2, lam, w = R.queries(93, 2, 4, 1, 64)
+    new = [torch.ones(2, 2, 1, x, dtype=torch.bfloat16, device="cuda") for x in (64, 64, 128)]
+    pools = [getattr(c, t).clone() for t in ("k1", "k2", "v", "weights")]
+    good = ops.paged_fwd(cache, q1, q2, lam)
+    for bad in ((q1[:1], q2, lam), (q1, q2[:, :2], lam), (q1[..., :32], q2[..., :32], lam),
+                (q1.float(), q2, lam), (q1, q2.half(), lam), (q1.cpu(), q2, lam),
+                (q1, q2, lam[:3]), (q1, q2, lam.double()), (q1, q2, lam.cpu()),
+                (q1[0], q2[0], lam),
+                (q1, torch.zeros(2, 4, 1, 128, dtype=torch.bfloat16, device="cuda")[..., ::2],
+                 lam)):
+        with pytest.raises(ValueError):
+            ops.paged_fwd(cache, *bad)
+    for kw in (dict(norm_w=w[:, :64]), dict(norm_w=w.half()), dict(out=good[:1]),
+               dict(out=good.float()), dict(out=good.cpu()),
+               dict(workspace=torch.empty(64, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            ops.paged_fwd(cache, q1, q2, lam, **kw)
+    with pytest.raises(ops.DiffAttnError):  # N past 16 tokens
+        ops.paged_fwd(cache, *(torch.zeros(2, 4, 17, 64, dtype=torch.bfloat16, device="cuda"),) * 2,
+                      lam)
+    assert ops.paged_fwd(cache, q1, q2, lam, eps=-1.0, raw_status=True) == ops.ERR_INVALID_ARG
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    assert ops.paged_fwd(cache, q1, q2, lam, accumulate=True, workspace=small,
+                         raw_status=True) == ops.ERR_INVALID_ARG
+    for bad in ((new[0][:1], new[1], new[2]), (new[0], new[1][:, :1], new[2]),
+                (new[0], new[1], new[0]), (new[0].float(), new[1], new[2]),
+                (new[0], new[1], new[2].cpu())):
+        with pytest.raises(ValueError):
+            ops.paged_append(cache, *bad)
+    assert ops.paged_evict(cache, keep=4, recent=5, raw_status=True) == ops.ERR_INVALID_ARG
+    assert ops.paged_evict(cache, keep=-1, raw_status=True) == ops.ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    for t, before in zip(("k1", "k2", "v", "weights"), pools):
+        assert torch.equal(getattr(c, t).view(torch.uint8), before.view(torch.uint8))
+    assert c.kv_len.tolist() == [40, 7]
 
 
 def test_many_sequences():
