@@ -287,6 +287,35 @@ def test_accumulated_weights_by_rows_and_parts(lens, H, kv, N, d, page, causal):
         assert torch.equal(c.weights, after)
 
 
+def test_weights_of_calls_in_a_row_on_one_workspace():
+    """Logits past what L2 holds back, written, read and dropped by call after call without a wait
+    between them: the weights are those of the same calls one at a time."""
+    d, kv, H, n = 64, 4, 16, 80000
+    caches = [R.Cache(120 + k, lens=[n - k, 3000], kv=kv, d=d, page=64, weights=True, fill=0.0)
+              for k in range(2)]
+    ops_caches = [c.ops_cache() for c in caches]
+    queries = [R.queries(122 + k, 2, H, 1, d) for k in range(2)]
+    start = [c.weights.clone() for c in caches]
+    need = max(ops.paged_fwd_plan(c, H, accumulate=True) for c in ops_caches)
+    assert need > 16 << 20
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    results = []
+    for wait in (True, False):
+        for c, w0 in zip(caches, start):
+            c.weights.copy_(w0)
+        torch.cuda.synchronize()
+        for step in range(24):
+            q1, q2, lam, w = queries[step % 2]
+            ops.paged_fwd(ops_caches[step % 2], q1, q2, lam, norm_w=w, accumulate=True,
+                          workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        results.append([c.weights.clone() for c in caches])
+    for x, y in zip(*results):
+        assert torch.equal(x, y)
+
+
 # ---- bad pages and lengths ------------------------------------------------------------------
 
 @pytest.mark.parametrize("lens", [[100, 90, 33], [1000, 900, 33]])
