@@ -700,6 +700,7 @@ class PagedCache:
 
     # What a call's shapes and numbers come to (its descriptor, the shapes of its other tensors, its
     # workspace) is worked out and checked once, and kept under them; with a status word, each time.
+    # Keys hold plain numbers: a tensor would stand for whatever value it had the first time.
 
     def _keep(self, key, status, call):
         if status is None:
@@ -840,7 +841,7 @@ def paged_fwd(cache, q1, q2, lam, *, causal: bool = True, headnorm: int = 1, nor
     workspace: a CUDA tensor of at least paged_fwd_plan bytes (a torch buffer when None).
     Returns bf16 out [B, H, N, 2d] (of `stream`'s memory when allocated here).
     """
-    key = (q1.shape, causal, headnorm, eps, lambda_init, accumulate)
+    key = (q1.shape, bool(causal), int(headnorm), float(eps), float(lambda_init), bool(accumulate))
     call = cache._calls.get(key) if status is None else None
     if call is None:
         st, call = cache._new_fwd(key, status)

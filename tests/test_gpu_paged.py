@@ -831,3 +831,17 @@ def test_bounds_checked_build_agrees():
                 both.append([out, c.weights, c.v, c.kv_len])
         for x, y in zip(*both):
             assert torch.equal(x, y)
+
+
+def test_numbers_given_as_tensors_are_read_at_every_call():
+    """eps and lambda_init as tensors of one element that change in place between calls."""
+    c = R.Cache(125, lens=[40, 7], kv=2, d=64, page=16)
+    cache = c.ops_cache()
+    q1, q2, lam, w = R.queries(126, 2, 4, 1, 64)
+    li, eps = torch.tensor(0.25), torch.tensor(1e-5)
+    for a, b in ((0.25, 1e-5), (0.75, 1e-5), (0.75, 0.5)):
+        li.fill_(a)
+        eps.fill_(b)
+        got = ops.paged_fwd(cache, q1, q2, lam, norm_w=w, lambda_init=li, eps=eps)
+        ref, tol, _, _ = R.attend(c, q1, q2, lam, norm_w=w, lambda_init=a, eps=b)
+        R.check(got, ref, tol, f"lambda_init {a}, eps {b}")
