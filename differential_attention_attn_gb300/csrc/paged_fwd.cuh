@@ -61,6 +61,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -106,6 +107,8 @@ constexpr int kMmaWarp = 0, kKeyWarp = 1, kValueWarp = 2, kQueryWarp = 3, kSoftm
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kGrowth = 8.f;  // log2 units a logit may pass the reference maximum by
+// A reference before any key above -infinity is seen: finite, so that such a key's 2^(x - m) is 0.
+constexpr float kLeast = -FLT_MAX;
 constexpr int kMaxBad = 16;     // as many as new tokens: more than keys that only some of them see
 constexpr int kRing = 8;        // tile descriptors; fewer tiles are between load and epilogue
 constexpr int kBoxBytes = kTile * 128;   // 64 bf16 columns of a tile
@@ -943,7 +946,7 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
       if (named_barrier_or(2, kConsumers, !ok)) break;
       if (!stop) {
         const auto new_m = [&](int q) {
-          float y = fresh ? -INFINITY : m[q];
+          float y = fresh ? kLeast : m[q];
 #pragma unroll
           for (int w = 0; w < 4; ++w) y = fmaxf(y, sm->wmax[map][w][r0 + q]);
           return y;

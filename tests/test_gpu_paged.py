@@ -845,3 +845,30 @@ def test_numbers_given_as_tensors_are_read_at_every_call():
         got = ops.paged_fwd(cache, q1, q2, lam, norm_w=w, lambda_init=li, eps=eps)
         ref, tol, _, _ = R.attend(c, q1, q2, lam, norm_w=w, lambda_init=a, eps=b)
         R.check(got, ref, tol, f"lambda_init {a}, eps {b}")
+
+
+@pytest.mark.parametrize("lens,upto,kv,H", [
+    ([600, 300], 128, 2, 4),    # the whole first tile
+    ([600, 300], 290, 1, 1),    # two tiles and a part of the third
+    ([9000, 40], 7000, 1, 8),   # whole parts of a joined item
+    ([3000, 200], 2999, 1, 40),  # one key is left; two row blocks
+])
+def test_keys_with_logits_of_minus_infinity_weigh_nothing(lens, upto, kv, H):
+    """Visible keys whose logits are -infinity, over whole tiles: the softmax of the others."""
+    c = R.Cache(127, lens=lens, kv=kv, d=64, page=16, weights=True)
+    for b, n in enumerate(lens):
+        t = torch.arange(min(upto, n - 1), device="cuda")
+        for pool in (c.k1, c.k2):
+            pool[c.table[b].long()[t // 16], :, t % 16, 3] = -float("inf")
+    q1, q2, lam, w = R.queries(128, 2, H, 1, 64)
+    for q in (q1, q2):
+        q[..., 3] = 0.5
+    old = [c.rows("weights", b).double() for b in range(2)]
+    out = _fwd(c, q1, q2, lam, w, accumulate=True)
+    ref, tol, add, add_tol = R.attend(c, q1, q2, lam, norm_w=w, lambda_init=LI)
+    assert bool(torch.isfinite(ref).all())
+    R.check(out, ref, tol, "out")
+    for b in range(2):
+        want = old[b] + add[b]
+        R.check(c.rows("weights", b), want,
+                add_tol[b] + want * (H // kv + 2) * 2.0 ** -23, "weights")
