@@ -68,6 +68,10 @@ inline FastDiv fast_div(uint32_t d) {  // 2^(s - 1) < d <= 2^s, mul = ceil(2^(31
   return {static_cast<uint32_t>(((uint64_t{1} << (31 + s)) + d - 1) / d), 31 + s, d};
 }
 
+// kv_len is read by plain loads and only behind the dependency wait of a kernel or of the one before
+// it: diffpaged_evict writes it, and the kernels behind may be resident by then (dependent launch),
+// where the read-only path (__ldg) must not be used.
+
 // Stores DIFFATTN_ERR_PAGE in the call's status word unless another code is there.
 __device__ __forceinline__ void report_bad_page(int32_t *status) {
   if (status != nullptr) atomicCAS(status, 0, static_cast<int32_t>(DIFFATTN_ERR_PAGE));

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRows == 1 ? 8 : 6)
   const uint32_t b = p.by_heads.div(bh), h = bh - b * p.kv_heads;
   grid_dependency_wait();
   grid_dependents_launch();
-  const int32_t len = __ldg(p.kv_len + b);
+  const int32_t len = p.kv_len[b];
 
   uint4 x[kRows][kPerLane];
   int32_t page[kRows];
@@ -85,7 +85,8 @@ __global__ void __launch_bounds__(kWarps * 32, kRows == 1 ? 8 : 6)
       const int t = unit < kKeyUnits ? 0 : unit < 2 * kKeyUnits ? 1 : 2;
       const uint8_t *s = p.src[t] + b * p.src_b[t] + h * p.src_h[t] + (i0 + r) * p.src_n[t] +
                          (unit - t * kKeyUnits) * 16;
-      x[r][u] = __ldg(reinterpret_cast<const uint4 *>(s));
+      // (A plain load: the rows may be the output of a kernel that this one has started under.)
+      x[r][u] = *reinterpret_cast<const uint4 *>(s);
     }
   };
   if (kEager)

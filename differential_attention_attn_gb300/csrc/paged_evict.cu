@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kSelectThreads) diffpaged_select_kernel(const 
   for (int i = tid; i < 2048; i += kSelectThreads) hist[i] = 0;
   grid_dependency_wait();
   grid_dependents_launch();
-  const int32_t len = __ldg(p.kv_len + b);
+  const int32_t len = p.kv_len[b];
   const bool bad_len = len < 0 || len > p.max_pages * p.page_size;
   if (bad_len || len <= p.keep) {
     if (tid == 0) {

@@ -84,7 +84,7 @@ __device__ __forceinline__ Shares all_shares(const FwdParams &p, uint32_t ctas, 
   const int32_t most = p.max_pages * p.page_size;
   uint32_t total = 0, mine = 0;
   for (int32_t x = threadIdx.x % 32; x < p.B; x += 32) {
-    const uint32_t u = kItemCost + units_of(__ldg(p.kv_len + x), most);
+    const uint32_t u = kItemCost + units_of(p.kv_len[x], most);
     total += u;
     mine += x < b ? u : 0;
   }
@@ -113,7 +113,7 @@ __device__ void join_row(const JoinParams &jp) {
       const int32_t b = static_cast<int32_t>(bh / p.kv_heads);
       uint32_t before;
       const Shares all = all_shares(p, jp.ctas, b, &before);
-      const int32_t len = __ldg(p.kv_len + b);
+      const int32_t len = p.kv_len[b];
       const uint32_t units = units_of(len, p.max_pages * p.page_size);
       const uint32_t heads = p.kv_heads * p.row_blocks;
       parts = parts_of(all, before * heads + (which - b * heads) * (kItemCost + units), units);
@@ -240,7 +240,7 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
   const int run = kJoinThreads * 4 / groups;  // keys of a pass
   const uint32_t bh = block / jp.weight_blocks;
   const int b = static_cast<int>(bh / p.kv_heads), hk = static_cast<int>(bh - b * p.kv_heads);
-  const int32_t len = __ldg(p.kv_len + b);
+  const int32_t len = p.kv_len[b];
   const int32_t most = p.max_pages * p.page_size;
   const int32_t first = static_cast<int32_t>(block - bh * jp.weight_blocks) * run;
   if (len < 0 || len > most || first >= len) return;

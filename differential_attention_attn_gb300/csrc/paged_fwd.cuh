@@ -377,7 +377,7 @@ __device__ __forceinline__ Share find_share(const FwdParams &p, uint32_t cta, ui
     const uint32_t item = cta - s.b * heads;
     s.hk = item / p.row_blocks;
     s.rb = item - s.hk * p.row_blocks;
-    s.len = __ldg(p.kv_len + s.b);
+    s.len = p.kv_len[s.b];
     s.units = units_of(s.len, most);
     s.end = kItemCost + s.units;
     return s;
@@ -390,7 +390,7 @@ __device__ __forceinline__ Share find_share(const FwdParams &p, uint32_t cta, ui
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int32_t x = b0 + 32 * k + lane;
-      last[k] = x < p.B ? __ldg(p.kv_len + x) : 0;
+      last[k] = x < p.B ? p.kv_len[x] : 0;
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -404,7 +404,7 @@ __device__ __forceinline__ Share find_share(const FwdParams &p, uint32_t cta, ui
 #pragma unroll 1
     for (int32_t b0 = 0; b0 < p.B; b0 += 32) {
       const int32_t x = b0 + lane;
-      const int32_t len = p.B <= 32 ? last[0] : x < p.B ? __ldg(p.kv_len + x) : 0;
+      const int32_t len = p.B <= 32 ? last[0] : x < p.B ? p.kv_len[x] : 0;
       const uint32_t u = x < p.B ? (kItemCost + units_of(len, most)) * heads : 0;
       uint32_t incl = u;
 #pragma unroll
@@ -459,7 +459,7 @@ struct Walk {
         hk = 0;
         ++b;
         if (end > (p.cut ? 0 : -kItemCost)) {
-          len = __ldg(p.kv_len + b);
+          len = p.kv_len[b];
           units = units_of(len, p.max_pages * p.page_size);
         }
       }

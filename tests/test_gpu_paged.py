@@ -872,3 +872,40 @@ def test_keys_with_logits_of_minus_infinity_weigh_nothing(lens, upto, kv, H):
         want = old[b] + add[b]
         R.check(c.rows("weights", b), want,
                 add_tol[b] + want * (H // kv + 2) * 2.0 ** -23, "weights")
+
+
+@pytest.mark.parametrize("B,kv", [(3, 2), (40, 8)])
+def test_evict_then_append_and_attend_with_nothing_between(B, kv):
+    """The next kernels start while the eviction runs, and see the lengths that it writes: with keys
+    replaced at the end of what stays."""
+    lens = [700 - 3 * b for b in range(B)]
+    results = []
+    for wait in (True, False):
+        c = R.Cache(129, lens=lens, kv=kv, d=64, page=16, weights=True, fill=0.0)
+        cache = c.ops_cache()
+        pools = {t: getattr(c, t).clone() for t in ("k1", "k2", "v", "weights", "kv_len")}
+        q1, q2, lam, w = R.queries(130, B, 2 * kv, 2, 64)
+        g = torch.Generator().manual_seed(131)
+        new = [torch.randn(B, kv, 2, x, generator=g).to(torch.bfloat16).cuda()
+               for x in (64, 64, 128)]
+        got = []
+        for step in range(20):
+            for t, x in pools.items():
+                getattr(c, t).copy_(x)
+            torch.cuda.synchronize()
+            ops.paged_evict(cache, keep=300 + step, recent=30)
+            if wait:
+                torch.cuda.synchronize()
+            ops.paged_append(cache, *new)
+            if wait:
+                torch.cuda.synchronize()
+            got.append(ops.paged_fwd(cache, q1, q2, lam, norm_w=w, accumulate=True))
+            torch.cuda.synchronize()
+            got.append(c.weights.clone())
+            assert c.kv_len.tolist() == [300 + step] * B
+        results.append(got)
+        c.lens = c.kv_len.tolist()
+        for b in (0, B - 1):
+            assert torch.equal(c.rows("v", b)[:, -2:], new[2][b])
+    for x, y in zip(*results):
+        assert torch.equal(x, y)

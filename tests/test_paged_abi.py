@@ -189,3 +189,20 @@ def test_python_checks():
         ops.PagedCache(pool, pool, v, table, torch.zeros(2, dtype=torch.int32))
     with pytest.raises(ValueError, match="CUDA"):
         ops.PagedCache(pool, pool, v, table, lens)
+
+
+def test_lengths_are_not_read_through_the_read_only_path():
+    """kv_len is written by diffpaged_evict while the kernels behind it may be resident already
+    (dependent launch): ld.global.nc, which __ldg is, must not read it."""
+    import glob
+    import os
+    files = glob.glob(os.path.join(libbuild.CSRC, "paged*"))
+    assert len(files) >= 6
+    uses = 0
+    for path in files:
+        text = open(path).read()
+        uses += text.count("kv_len[")
+        for part in text.split("__ldg(")[1:]:
+            assert "kv_len" not in part[:part.index(")")], path
+            assert "uint4" not in part[:part.index(")")], path  # rows: another kernel's output
+    assert uses > 0
