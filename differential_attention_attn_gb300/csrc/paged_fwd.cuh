@@ -895,6 +895,11 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
       // see different keys, a non-finite v row that only some of them see is noted, to be kept out
       // of the product.
       if (ok && (keys < kTile || mixed)) {
+        // A wait for a slot's use c is for the right phase only once its use before, c - kValRing,
+        // has landed: sure for tiles up to t - kPBufs, whose products are done.  Where a slot may
+        // still be tile t - 1's (d = 128, bf16, up to 16 rows), that tile's product is awaited.
+        if (L::kValRing < G::kPBufs * G::kValSlots && t > 0)
+          ok = mbar_wait_warp(&sm->pv_done[(t - 1) & 1], phase<2>(t - 1), &sm->abort, kWaitNs);
 #pragma unroll 1
         for (int k = 0; k < G::kValSlots; ++k) {
           const uint32_t c = t * G::kValSlots + k;

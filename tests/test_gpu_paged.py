@@ -909,3 +909,26 @@ def test_evict_then_append_and_attend_with_nothing_between(B, kv):
             assert torch.equal(c.rows("v", b)[:, -2:], new[2][b])
     for x, y in zip(*results):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("H,kv,N", [(2, 2, 1), (4, 1, 1), (1, 1, 8), (8, 1, 2)])
+@pytest.mark.parametrize("top", [40, 700])
+def test_ends_of_items_behind_values_in_flight(H, kv, N, top):
+    """d = 128 with bf16 keys has three value buffers for two a tile: the garbage behind a sequence's
+    end is cleared in the tile's own values, not in those of the tile before, which may still be on
+    their way.  Call after call on many short items, with other traffic beside them."""
+    g = torch.Generator().manual_seed(132)
+    lens = torch.randint(0, top + 1, (200,), generator=g).tolist()
+    c = R.Cache(133, lens=lens, kv=kv, d=128, page=16)
+    out = _parity(c, H, N)
+    cache = c.ops_cache()
+    q1, q2, lam, w = R.queries(3, c.B, H, N, 128)
+    noise = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(100):
+            noise.add_(1)
+    got = [ops.paged_fwd(cache, q1, q2, lam, norm_w=w, lambda_init=LI) for _ in range(60)]
+    torch.cuda.synchronize()
+    for x in got:
+        assert torch.equal(x, out)
