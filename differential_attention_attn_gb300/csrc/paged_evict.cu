@@ -311,6 +311,14 @@ __global__ void __launch_bounds__(kMoveThreads) diffpaged_move_kernel(const Evic
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+// For a budget that no sequence can pass: the lengths are looked at all the same.
+__global__ void __launch_bounds__(256)
+    diffpaged_lengths_kernel(const int32_t *kv_len, int32_t B, int32_t most, int32_t *status) {
+  grid_dependency_wait();
+  const uint32_t b = blockIdx.x * 256 + threadIdx.x;
+  if (b < static_cast<uint32_t>(B) && (kv_len[b] < 0 || kv_len[b] > most)) report_bad_page(status);
+}
+
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct EvictLayout {
@@ -349,7 +357,25 @@ bool paged_evict_bytes(const diffattn_desc &desc, const diffpaged_cache &cache, 
 diffattn_status launch_paged_evict(const diffattn_desc &desc, const diffpaged_cache &cache,
                                    int64_t keep, int64_t recent, void *workspace,
                                    cudaStream_t stream) {
-  if (keep >= cache.max_pages * cache.page_size) return DIFFATTN_OK;
+  const int64_t most = cache.max_pages * cache.page_size;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (keep >= most) {
+    if (desc.status_dev == nullptr) return DIFFATTN_OK;
+    cfg.gridDim = dim3(static_cast<unsigned>((desc.B + 255) / 256));
+    cfg.blockDim = dim3(256);
+    return cudaLaunchKernelEx(&cfg, diffpaged_lengths_kernel,
+                              static_cast<const int32_t *>(cache.kv_len),
+                              static_cast<int32_t>(desc.B), static_cast<int32_t>(most),
+                              desc.status_dev) == cudaSuccess
+               ? DIFFATTN_OK
+               : DIFFATTN_ERR_CUDA;
+  }
   const bool fp8 = desc.dtype == DIFFATTN_E4M3_QK;
   const EvictLayout l = layout(desc, cache, keep);
   EvictParams p = {};
@@ -391,13 +417,8 @@ diffattn_status launch_paged_evict(const diffattn_desc &desc, const diffpaged_ca
   p.list = reinterpret_cast<int2 *>(ws + l.list);
   p.plan = reinterpret_cast<int2 *>(ws + l.plan);
   const int64_t items = desc.B * cache.kv_heads;  // items * kMostSlices fits (paged_evict_bytes)
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(items));
   cfg.blockDim = dim3(kSelectThreads);
-  const int64_t most = cache.max_pages * cache.page_size;
   cfg.dynamicSmemBytes = sizeof(float) * static_cast<size_t>(most < kHeld ? most : kHeld);
   static std::atomic<bool> attr_set[64];  // per device (concurrent callers may both set)
   int dev = 0;
@@ -410,9 +431,6 @@ diffattn_status launch_paged_evict(const diffattn_desc &desc, const diffpaged_ca
       return DIFFATTN_ERR_CUDA;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, diffpaged_select_kernel, p) != cudaSuccess) return DIFFATTN_ERR_CUDA;
   cfg.gridDim = dim3(static_cast<unsigned>(items) * slices);
   cfg.blockDim = dim3(kMoveThreads);

@@ -932,3 +932,24 @@ def test_ends_of_items_behind_values_in_flight(H, kv, N, top):
     torch.cuda.synchronize()
     for x in got:
         assert torch.equal(x, out)
+
+
+@pytest.mark.parametrize("keep", [119, 160, 161, 1 << 40])
+@pytest.mark.parametrize("bad", [-1, 161, 2 ** 31 - 1, -2 ** 31])
+def test_evict_reports_a_bad_length_whatever_the_budget(keep, bad):
+    """Budgets below, at and past the 160 keys that the table has room for, among 300 sequences."""
+    c = R.Cache(134, lens=[100] + [30] * 299, kv=1, d=64, page=16, weights=True, extra_pages=3)
+    cache = c.ops_cache()
+    assert c.max_pages * 16 == 160
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pools = [getattr(c, t).clone() for t in ("k1", "k2", "v", "weights")]
+    ops.paged_evict(cache, keep=keep, recent=3, status=status)
+    assert int(status) == 0
+    c.kv_len[299] = bad
+    ops.paged_evict(cache, keep=keep, recent=3, status=status)
+    assert int(status) == ops.ERR_PAGE
+    ops.paged_evict(cache, keep=keep, recent=3)  # no status word: nothing to report to
+    torch.cuda.synchronize()
+    assert c.kv_len.tolist() == [100] + [30] * 298 + [bad]
+    for t, x in zip(("k1", "k2", "v", "weights"), pools):
+        assert torch.equal(getattr(c, t).view(torch.uint8), x.view(torch.uint8)), t
