@@ -19,10 +19,14 @@ constexpr int kPagedTile = 128;
 constexpr int kPagedMaxTokens = 16;
 constexpr int kPagedMaxGroup = 64;
 
+// How items (sequence, key/value head, row block) go to CTAs: one each; in equal shares of all
+// tiles, each item whole in the share that it begins in; in equal shares that cut items, which the
+// second kernel joins; or one of these, as the lengths found on the device have it.
+enum PagedMode : int32_t { kPagedWhole, kPagedUncut, kPagedCut, kPagedByLengths };
+
 struct PagedFwdPlan {
   int ctas;        // CTAs of the main kernel
-  bool whole;      // one CTA per item; else equal shares of all tiles,
-  bool cut;        // which may cut items (the second kernel joins those) or not
+  PagedMode mode;  // not kPagedCut: no capacity says that the lengths are long
   int row_tile;    // rows of a block
   int row_blocks;  // row blocks per key/value head
   int64_t items;   // B * kv_heads * row_blocks

@@ -36,7 +36,6 @@ __device__ __forceinline__ Parts parts_of(const Shares &all, uint32_t start, uin
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 constexpr int kMaxParts = 256;       // more than SMs
-constexpr int64_t kUneven = 5;       // steps, see plan_paged_fwd
 constexpr int kMaxRowBlocks = kPagedMaxTokens * kPagedMaxGroup / 32;
 static_assert(kMaxRowBlocks <= 32, "a lane each");
 constexpr int kWeightBlocks = 912;  // in all, about: two rounds of three per SM
@@ -82,15 +81,18 @@ __device__ __forceinline__ float block_sum(float x, float *scratch) {
 __device__ __forceinline__ Shares all_shares(const FwdParams &p, uint32_t ctas, int32_t b,
                                              uint32_t *before) {
   const int32_t most = p.max_pages * p.page_size;
-  uint32_t total = 0, mine = 0;
+  uint32_t total = 0, mine = 0, longest = 0, shortest = 0xFFFFFFFFu;
   for (int32_t x = threadIdx.x % 32; x < p.B; x += 32) {
     const uint32_t u = kItemCost + units_of(p.kv_len[x], most);
     total += u;
     mine += x < b ? u : 0;
+    longest = max(longest, u);
+    shortest = min(shortest, u);
   }
-  total = __reduce_add_sync(0xffffffffu, total);
   *before = __reduce_add_sync(0xffffffffu, mine);
-  return cut_line(total * p.kv_heads * p.row_blocks, ctas);
+  return cut_line(p, __reduce_add_sync(0xffffffffu, total),
+                  __reduce_max_sync(0xffffffffu, longest),
+                  __reduce_min_sync(0xffffffffu, shortest), ctas);
 }
 
 // Block (cut item, row): joins one row.  The cut items are found from the boundaries between
@@ -116,11 +118,12 @@ __device__ void join_row(const JoinParams &jp) {
       const int32_t len = p.kv_len[b];
       const uint32_t units = units_of(len, p.max_pages * p.page_size);
       const uint32_t heads = p.kv_heads * p.row_blocks;
-      parts = parts_of(all, before * heads + (which - b * heads) * (kItemCost + units), units);
+      if (all.mode == kPagedCut)
+        parts = parts_of(all, before * heads + (which - b * heads) * (kItemCost + units), units);
       if (parts.n > 1) x = make_int4(static_cast<int>(which), parts.first, parts.n, len);
     } else {
       const Share s = find_share(p, which + 1, jp.ctas);
-      if (s.off > kItemCost) {
+      if (s.all.mode == kPagedCut && s.off > kItemCost) {
         parts = parts_of(s.all, s.begin - s.off, s.units);
         if (parts.first / 2 == static_cast<int>(which))
           x = make_int4((s.b * p.kv_heads + s.hk) * p.row_blocks + s.rb, parts.first, parts.n,
@@ -248,11 +251,11 @@ __device__ void add_weights(const JoinParams &jp, uint32_t block) {
   // maps, 1 (0 for a row that sees no key and adds nothing) and lambda.
   if (warp == 0) {
     Parts parts = {0, 1};
-    if (p.cut) {
+    if (p.mode == kPagedByLengths) {
       uint32_t before;
       const Shares all = all_shares(p, jp.ctas, b, &before);
       const uint32_t units = units_of(len, most);
-      if (lane < p.row_blocks)
+      if (all.mode == kPagedCut && lane < p.row_blocks)
         parts = parts_of(all,
                          before * p.kv_heads * p.row_blocks +
                              (hk * p.row_blocks + lane) * (kItemCost + units),
@@ -421,9 +424,9 @@ __global__ void __launch_bounds__(kJoinThreads, kPlane ? 3 : 6)
   } else {
     if constexpr (kPlane > 0) add_weights<kPlane>(jp, blockIdx.x - jp.joins);
   }
-  // Blocks with nothing to do wait as well: were there no others (no item cut), this kernel would
-  // end, and the one behind it on the stream begin, before the main kernel has.
-  grid_dependency_wait();
+  // Blocks with nothing to do leave, but for the first: were there no others (no item cut), this
+  // kernel would end, and the one behind it on the stream begin, before the main kernel has.
+  if (blockIdx.x == 0) grid_dependency_wait();
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -512,23 +515,29 @@ bool plan_paged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache, boo
   const int64_t most = cache.max_pages * cache.page_size;
   const int64_t units = (most + kTile - 1) / kTile;
   q.padded = units * kTile;
-  // One CTA per item, and nothing to join, where equal shares would save less time than the join
-  // and the second segment of most CTAs take (6 us, of 1 us a tile).  64 items of 8 tiles on 152
-  // SMs: 12.6 us, in shares 14.6 us; of 16 tiles 20.2 us and 18.3 us.  16 items of 4 tiles: 8.1
-  // and 9.1 us, of 8 tiles 11.7 and 9.5 us.
   if (items * static_cast<double>(units + kItemCost) >= 2147483648.0) return false;
-  q.whole = q.items <= sm_count && units * (sm_count - q.items) <= int64_t{6} * sm_count;
-  q.ctas = q.whole ? static_cast<int>(q.items) : sm_count;
-  if (!q.whole && q.items * (units + kItemCost) < sm_count)
-    q.ctas = static_cast<int>(q.items * (units + kItemCost));
-  // Nor are items cut where they are so many, or so short, that taking them whole makes the longest
-  // share at most kUneven steps longer, which costs less than the join.  408 items of two tiles (8
-  // rows): 19.8 us, cut 24.7; 1024 of two: 25.5 and 28.2; 228 of six (32 rows, d = 128): 58 and 69;
-  // 240 of ten, where it would be 5.05 steps: 26.8 and 25.1 us.
+  // The kernels choose from the lengths how items are taken (cut_line).  Where the choice is the
+  // same for all lengths up to the capacity, it is made here, and the second kernel and its
+  // workspace are left out: one CTA per item where that is right for full sequences and, as the
+  // launch is saved too, costs at most kSecondKernel tiles more where only one sequence is full; an
+  // uncut share is longest - 1 steps longer at most, and where all items are equally long, as those
+  // of a single sequence are, `per` of them long.
+  const int64_t heads = cache.kv_heads * q.row_blocks;
   const int64_t per = (q.items + sm_count - 1) / sm_count;
-  q.cut = !q.whole && !(q.items > sm_count &&
-                        (units + kItemCost) * (per * sm_count - q.items) <= kUneven * sm_count);
-  const size_t slots = q.cut ? 2 * static_cast<size_t>(q.ctas) : 0;
+  const int64_t alone = int64_t{kMostAlone} * sm_count, uneven = int64_t{kUneven} * sm_count;
+  q.mode = kPagedByLengths;
+  if (q.items <= sm_count) {
+    if (units * (sm_count - q.items) <= alone &&
+        units * (sm_count - heads) - (q.items - heads) <= alone + kSecondKernel * sm_count)
+      q.mode = kPagedWhole;
+  } else if (units + kItemCost <= kUneven ||
+             (desc.B == 1 && (units + kItemCost) * (per * sm_count - q.items) <= uneven)) {
+    q.mode = kPagedUncut;
+  }
+  q.ctas = q.mode == kPagedWhole ? static_cast<int>(q.items) : sm_count;
+  if (q.items * (units + kItemCost) < q.ctas)
+    q.ctas = static_cast<int>(q.items * (units + kItemCost));
+  const size_t slots = q.mode == kPagedByLengths ? 2 * static_cast<size_t>(q.ctas) : 0;
   size_t at = 0;
   const auto take = [&at](size_t bytes) {
     const size_t here = at;
@@ -586,13 +595,12 @@ diffattn_status launch_paged_fwd(const diffattn_desc &desc, const diffpaged_cach
   p.by_group = fast_div(static_cast<uint32_t>(p.group));
   p.causal = desc.causal ? 1 : 0;
   p.headnorm = desc.headnorm;
-  p.whole = plan.whole ? 1 : 0;
-  p.cut = plan.cut ? 1 : 0;
+  p.mode = plan.mode;
   p.eps = desc.eps;
   p.out_scale = 1.0f - desc.lambda_init;
   p.scale_log2 = kLog2e / std::sqrt(static_cast<float>(d));
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  if (plan.cut) {
+  if (plan.mode == kPagedByLengths) {
     p.part = reinterpret_cast<float *>(ws + plan.part);
     p.part_ml = reinterpret_cast<float2 *>(ws + plan.stats);
   }
@@ -615,11 +623,11 @@ diffattn_status launch_paged_fwd(const diffattn_desc &desc, const diffpaged_cach
   if (st != DIFFATTN_OK) return st;
   JoinParams jp = {};
   jp.f = p;
-  jp.ctas = plan.whole ? 1 : plan.ctas;
+  jp.ctas = plan.ctas;
   jp.row_tile = plan.row_tile;
   jp.join_rows = p.rows < jp.row_tile ? p.rows : jp.row_tile;
   // Cut items are at most one per boundary.
-  const int64_t cuts = plan.cut ? plan.ctas - 1 : 0;
+  const int64_t cuts = plan.mode == kPagedByLengths ? plan.ctas - 1 : 0;
   jp.by_item = plan.items < cuts ? 1 : 0;
   jp.joins = static_cast<uint32_t>((jp.by_item ? plan.items : cuts) * jp.join_rows);
   jp.discard = plan.bytes - plan.logits >= kDiscardBytes ? 1 : 0;

@@ -19,8 +19,12 @@
 //     from kv_len on the device; a ragged batch is balanced and a graph
 //     replays with new lengths.  Items cut by a CTA boundary leave partial
 //     states, which a second kernel (launched dependent on the first) joins.
-//     With few tiles in all one CTA takes each item, and many short items are
-//     not cut either: nothing is joined then.
+//     Where the lengths make that longer by a few tiles only (few tiles in all,
+//     many short items), one CTA takes each item, or each the items that begin
+//     in its share, and nothing is joined.  Both kernels choose alike from the
+//     lengths (18 x 8 heads of 100 to 9001 keys, 144 items for 152 SMs: chosen
+//     from the capacity of the page table 74 us, from the lengths 60 us; 19 x 8
+//     with one sequence of 32768 keys beside others of 200: 236 and 33 us).
 //   - Two warps issue TMA copies of page pieces (16 to 64 rows, by the page
 //     size), one of keys and one of values, into rings of 32 KB buffers, 128 to
 //     192 KB in all: the keys of both maps (d = 64 or e4m3), one map's keys or
@@ -82,7 +86,7 @@ struct FwdParams {
   int32_t B, H, N, kv_heads, group, rows;  // rows = N * group
   int32_t num_pages, max_pages, page_size, piece_rows;
   int32_t row_blocks, causal, headnorm;
-  int32_t whole, cut;  // one CTA per item; items may be cut by shares (else neither or whole)
+  int32_t mode;  // PagedMode
   FastDiv by_page, by_group;  // page_size, group
   float eps, out_scale, scale_log2;
   // Workspace (see PagedFwdPlan): partial O [2 C][2][NR][2 d] and their (m, l), and for accumulate
@@ -114,6 +118,18 @@ constexpr int kRing = 8;        // tile descriptors; fewer tiles are between loa
 constexpr int kBoxBytes = kTile * 128;   // 64 bf16 columns of a tile
 constexpr int kSlotBytes = 2 * kBoxBytes;
 constexpr int kItemCost = 2;    // steps, see Shares
+// One CTA per item, and nothing to join, where equal shares would not save this many tiles of the
+// longest, what the join and the second segment of most CTAs take (6 us, of 1 us a tile).  64 items
+// of 8 tiles on 152 SMs: 12.6 us, in shares 14.6 us; of 16 tiles 20.2 us and 18.3 us.  16 items of 4
+// tiles: 8.1 and 9.1 us, of 8 tiles 11.7 and 9.5 us.
+constexpr int kMostAlone = 6;
+// What a second kernel takes that finds nothing to do (64 of 8 tiles: 12.0 us, with one 14.5 us).
+constexpr int kSecondKernel = 2;
+// Nor are items cut where they are so many, or so short, that no share gets this many steps longer
+// by taking them whole, which costs less than the join.  408 items of two tiles (8 rows): 19.8 us,
+// cut 24.7; 1024 of two: 25.5 and 28.2; 228 of six (32 rows, d = 128): 58 and 69; 240 of ten, where
+// it would be 5.05 steps: 26.8 and 25.1 us.
+constexpr int kUneven = 5;
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum : int32_t { kFirst = 1, kLast = 2, kStop = 4, kBad = 8, kDirect = 16 };
@@ -165,6 +181,30 @@ struct Geo {
   static_assert(kTmemUsed <= 512, "tensor memory");
 };
 
+// Work is laid out on a line: kItemCost steps that hold nothing for each item, then its tiles, a
+// step each.  (A segment costs its CTA about as much as two tiles beside its tiles: a CTA with ten
+// short items took 91 us where the others took 65.)  `ctas` shares cut the line into `each` or (the
+// first `more`) each + 1 steps.  Fewer than 2^31 steps (checked at launch).
+struct Shares {
+  uint32_t ctas, each, more;
+  int32_t mode;  // kPagedWhole, kPagedUncut or kPagedCut
+  __device__ __forceinline__ uint32_t begin(uint32_t cta) const {
+    return cta * each + min(cta, more);
+  }
+  __device__ __forceinline__ uint32_t cta_of(uint32_t step) const {
+    const uint32_t border = more * (each + 1);
+    return step < border ? step / (each + 1) : more + (step - border) / each;
+  }
+};
+// The CTA's share: the item (b, hk, rb) that it begins in, the steps from that item's first one to
+// the share's begin and end, and the item's tiles.
+struct Share {
+  Shares all;
+  uint32_t begin;     // of the share
+  int32_t off, end;   // from the item's first step; end = off: nothing
+  int32_t b, hk, rb, len, units;
+};
+
 template <int kNR>
 struct Ctrl {
   float m[2][2][kNR];  // reference maxima of both maps' rows, two copies in turn
@@ -178,6 +218,7 @@ struct Ctrl {
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_empty[2], drain;
   uint32_t bad_rows[3];
+  Share share;
   uint32_t tmem;
   int abort, failed;
 };
@@ -321,8 +362,8 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[kN
         : "memory");
 }
 
-// Named barriers beside the softmax warps' 1 and 2.  The load warps find the share while the other
-// warps set up: they wait only for the barriers in shared memory, and the others, whose bounded
+// Named barriers beside the softmax warps' 1 and 2.  The key warp finds the share while the other
+// warps set up: the load warps wait only for the barriers in shared memory, and the others, whose bounded
 // waits are for this kernel's own work, until the kernel before has ended.
 constexpr uint32_t kLoadBarrier = 3, kStartBarrier = 4;
 __device__ __forceinline__ void named_barrier_arrive(uint32_t id, uint32_t count) {
@@ -335,70 +376,74 @@ __device__ __forceinline__ uint32_t phase(uint32_t n) {
   return (n / kBufs) & 1;
 }
 
-// Work is laid out on a line: kItemCost steps that hold nothing for each item, then its tiles, a
-// step each.  (A segment costs its CTA about as much as two tiles beside its tiles: a CTA with ten
-// short items took 91 us where the others took 65.)  `ctas` shares cut the line into `each` or (the
-// first `more`) each + 1 steps.  Fewer than 2^31 steps (checked at launch).
-struct Shares {
-  uint32_t ctas, each, more;
-  __device__ __forceinline__ uint32_t begin(uint32_t cta) const {
-    return cta * each + min(cta, more);
-  }
-  __device__ __forceinline__ uint32_t cta_of(uint32_t step) const {
-    const uint32_t border = more * (each + 1);
-    return step < border ? step / (each + 1) : more + (step - border) / each;
-  }
-};
-__device__ __forceinline__ Shares cut_line(uint32_t steps, uint32_t ctas) {
+// The shares of `ctas` CTAs from the sequences' steps: their sum, the most and the least of one
+// (per head and row block).
+__device__ __forceinline__ Shares cut_line(const FwdParams &p, uint32_t total, uint32_t longest,
+                                           uint32_t shortest, uint32_t ctas) {
+  const uint32_t heads = p.kv_heads * p.row_blocks, items = p.B * heads, steps = total * heads;
   Shares s;
+  s.mode = p.mode;
   s.ctas = min(ctas, steps);
   s.each = steps / s.ctas;
   s.more = steps - s.each * s.ctas;
+  if (s.mode != kPagedByLengths) return s;
+  if (items <= ctas) {
+    const uint64_t tiles = steps - kItemCost * items;
+    s.mode = static_cast<uint64_t>(longest - kItemCost) * ctas <= tiles + kMostAlone * ctas
+                 ? kPagedWhole
+                 : kPagedCut;
+  } else {
+    // In a share of `most` steps begin at most most / shortest items, rounded up, and what begins
+    // last ends at most longest - 1 steps behind it.
+    const uint32_t most = s.each + (s.more > 0 ? 1 : 0);
+    const uint64_t uncut = min(static_cast<uint64_t>(most - 1 + longest),
+                               static_cast<uint64_t>((most - 1) / shortest + 1) * longest);
+    s.mode = uncut * ctas <= steps + static_cast<uint64_t>(kUneven) * ctas ? kPagedUncut
+                                                                             : kPagedCut;
+  }
   return s;
 }
-
-// The CTA's share: the item (b, hk, rb) that it begins in, the steps from that item's first one to
-// the share's begin and end, and the item's tiles.
-struct Share {
-  Shares all;
-  uint32_t begin;     // of the share
-  int32_t off, end;   // from the item's first step; end = off: nothing
-  int32_t b, hk, rb, len, units;
-};
 
 // CTA `cta`'s share of `ctas` CTAs (one warp, uniform).
 __device__ __forceinline__ Share find_share(const FwdParams &p, uint32_t cta, uint32_t ctas) {
   const int lane = threadIdx.x % 32;
   const int32_t most = p.max_pages * p.page_size;
-  Share s = {{1, 1, 0}, 0, 0, 0, 0, 0, 0, 0, 1};
+  Share s = {{1, 1, 0, p.mode}, 0, 0, 0, 0, 0, 0, 0, 1};
   const uint32_t heads = p.kv_heads * p.row_blocks;  // items of a sequence
-  if (p.whole) {
-    s.b = cta / heads;
-    const uint32_t item = cta - s.b * heads;
-    s.hk = item / p.row_blocks;
-    s.rb = item - s.hk * p.row_blocks;
-    s.len = p.kv_len[s.b];
-    s.units = units_of(s.len, most);
-    s.end = kItemCost + s.units;
-    return s;
-  }
-  uint32_t total = 0;
   int32_t last[4];  // lengths of the last 128 sequences, four a lane
+  if (p.mode != kPagedWhole) {
+    uint32_t total = 0, longest = 0, shortest = 0xFFFFFFFFu;
 #pragma unroll 1
-  for (int32_t b0 = 0; b0 < p.B; b0 += 128) {
-    uint32_t u = 0;
+    for (int32_t b0 = 0; b0 < p.B; b0 += 128) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int32_t x = b0 + 32 * k + lane;
-      last[k] = x < p.B ? p.kv_len[x] : 0;
+      for (int k = 0; k < 4; ++k) {
+        const int32_t x = b0 + 32 * k + lane;
+        last[k] = x < p.B ? p.kv_len[x] : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (b0 + 32 * k + lane < p.B) {
+          const uint32_t u = kItemCost + units_of(last[k], most);
+          total += u;
+          longest = max(longest, u);
+          shortest = min(shortest, u);
+        }
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (b0 + 32 * k + lane < p.B) u += kItemCost + units_of(last[k], most);
-    total += __reduce_add_sync(0xffffffffu, u);
+    s.all = cut_line(p, __reduce_add_sync(0xffffffffu, total),
+                     __reduce_max_sync(0xffffffffu, longest),
+                     __reduce_min_sync(0xffffffffu, shortest), ctas);
   }
-  s.all = cut_line(total * heads, ctas);
-  if (cta < s.all.ctas) {
+  if (s.all.mode == kPagedWhole) {
+    if (cta < p.B * heads) {
+      s.b = cta / heads;
+      const uint32_t item = cta - s.b * heads;
+      s.hk = item / p.row_blocks;
+      s.rb = item - s.hk * p.row_blocks;
+      s.len = p.kv_len[s.b];
+      s.units = units_of(s.len, most);
+      s.end = kItemCost + s.units;
+    }
+  } else if (cta < s.all.ctas) {
     s.begin = s.all.begin(cta);
     uint32_t left = s.begin;  // steps before the share, counted down sequence by sequence
 #pragma unroll 1
@@ -436,18 +481,19 @@ __device__ __forceinline__ Share find_share(const FwdParams &p, uint32_t cta, ui
 struct Walk {
   int32_t b, hk, rb, len, units;
   int32_t tile, end;  // the tile, and the share's end, in tiles of the current item
+  bool cut;           // items are
   __device__ __forceinline__ Walk(const FwdParams &p, const Share &s)
       : b(s.b), hk(s.hk), rb(s.rb), len(s.len), units(s.units), tile(max(0, s.off - kItemCost)),
-        end(s.end - kItemCost) {
-    if (!p.cut) {
+        end(s.end - kItemCost), cut(s.all.mode == kPagedCut) {
+    if (!cut) {
       if (s.off > 0)
         next_item(p);
       else
-        take_whole(p);
+        take_whole();
     }
   }
-  __device__ __forceinline__ void take_whole(const FwdParams &p) {
-    if (!p.cut && end > -kItemCost) end = max(end, units);
+  __device__ __forceinline__ void take_whole() {
+    if (!cut && end > -kItemCost) end = max(end, units);
   }
   // To the next item with a tile in the share (the first may be cut before its tiles).
   __device__ __forceinline__ void next_item(const FwdParams &p) {
@@ -458,18 +504,18 @@ struct Walk {
       if (++hk == p.kv_heads) {
         hk = 0;
         ++b;
-        if (end > (p.cut ? 0 : -kItemCost)) {
+        if (end > (cut ? 0 : -kItemCost)) {
           len = p.kv_len[b];
           units = units_of(len, p.max_pages * p.page_size);
         }
       }
     }
-    take_whole(p);
+    take_whole();
   }
 };
 
 // ---------------------------------------------------------------------------
-// The load warps, one for the keys (with the tiles' descriptions and the q rows) and one for the
+// The load warps, one for the keys (with the share and the tiles' descriptions) and one for the
 // values: a copy takes one thread 80 to 180 cycles to issue, and a tile in pages of 16 rows has 32
 // of them, which one warp issues more slowly than HBM delivers.  (Two for the keys alone were no
 // faster: 33 us where one takes 30 for 64 x 16 heads of 200 keys.)
@@ -496,11 +542,18 @@ __device__ __forceinline__ void load_warp(const FwdParams &p, const CUtensorMap 
   // on, so that what it reads before it waits for this one is what this one reads.
   grid_dependency_wait();
   named_barrier_arrive(kStartBarrier, 96 + G::kConsumers);
-  Walk w(p, find_share(p, blockIdx.x, gridDim.x));
+  // One warp finds the share for the three that walk it, whose copies of the code would have to be
+  // fetched too (18 x 8 heads of 100 to 9001 keys 59.9 -> 59.3 us, 152 items of 20 tiles 34.6 ->
+  // 33.8).
+  if (kKeys) {
+    const Share s = find_share(p, blockIdx.x, gridDim.x);
+    if (threadIdx.x % 32 == 0) sm->share = s;
+    grid_dependents_launch();
+  }
+  named_barrier_sync(kLoadBarrier, 96 + G::kConsumers);
+  Walk w(p, sm->share);
   int32_t &b = w.b, &hk = w.hk, &rb = w.rb, &len = w.len, &units = w.units, &tile = w.tile,
           &end = w.end;
-  grid_dependents_launch();
-  named_barrier_sync(kLoadBarrier, 96 + G::kConsumers);
   const int lane = threadIdx.x % 32;
   const int32_t most = p.max_pages * p.page_size;
   // Each slot is two boxes wide and up to eight page pieces high: a lane each.
@@ -626,8 +679,8 @@ __device__ __forceinline__ void query_warp(const FwdParams &p, uint8_t *smem, Ct
   constexpr int kUnits = G::kKeyRow / 16;
   const int lane = threadIdx.x % 32;
   grid_dependency_wait();
-  Walk w(p, find_share(p, blockIdx.x, gridDim.x));
   named_barrier_sync(kLoadBarrier, 96 + G::kConsumers);
+  Walk w(p, sm->share);
 #pragma unroll 1
   for (uint32_t seg = 0; w.tile < w.end; ++seg) {
     const uint32_t qb = seg & 1;

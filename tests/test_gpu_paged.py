@@ -953,3 +953,153 @@ def test_evict_reports_a_bad_length_whatever_the_budget(keep, bad):
     assert c.kv_len.tolist() == [100] + [30] * 298 + [bad]
     for t, x in zip(("k1", "k2", "v", "weights"), pools):
         assert torch.equal(getattr(c, t).view(torch.uint8), x.view(torch.uint8)), t
+
+
+def _longest_share(lens, heads, ctas):
+    """Steps (a tile each, two more an item) of the longest share and of an equal one, for items
+    taken whole by one CTA each, whole in the equal shares that they begin in, and cut."""
+    item = [2 + max(1, -(-n // 128)) for n in lens for _ in range(heads)]
+    total = sum(item)
+    alone = max(item) if len(item) <= ctas else None
+    each, more = divmod(total, ctas)
+    begins = [c * each + min(c, more) for c in range(ctas + 1)]
+    at, c, uncut = 0, 0, [0] * ctas
+    for x in item:
+        while c + 1 < ctas and begins[c + 1] <= at:
+            c += 1
+        uncut[c] += x
+        at += x
+    return alone, max(uncut), total / ctas
+
+
+@pytest.mark.parametrize("B,kv,lo,hi,big", [
+    (18, 8, 100, 9001, 0), (19, 8, 100, 9001, 0), (38, 8, 100, 9001, 0), (19, 8, 200, 200, 32768),
+    (38, 8, 200, 200, 32768), (16, 8, 200, 200, 4800), (57, 8, 500, 900, 0), (64, 16, 100, 700, 0),
+    (8, 8, 1024, 1024, 0), (1, 16, 200, 200, 0)])
+def test_ragged_batches_are_balanced(B, kv, lo, hi, big):
+    """The kernels take items whole only where no CTA has many steps more than in equal shares: told
+    from the parts that a call leaves in its workspace, as the second kernel would read them."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    lens = [hi - (hi - lo) * b // max(1, B - 1) for b in range(B)]
+    if big:
+        lens[B // 2] = big
+    page, d = 64, 64
+    max_pages = -(-max(lens) // page) + 600  # far more room than any sequence takes
+    need = [-(-n // page) for n in lens]
+    P = sum(need)
+    table = torch.full((B, max_pages), -1, dtype=torch.int32)
+    ids = iter(torch.randperm(P, generator=torch.Generator().manual_seed(135)).tolist())
+    for b in range(B):
+        for k in range(need[b]):
+            table[b, k] = next(ids)
+    g = torch.Generator(device="cuda").manual_seed(136)
+    pool = lambda w: torch.randn(P, kv, page, w, generator=g, device="cuda").to(torch.bfloat16)
+    cache = ops.PagedCache(pool(d), pool(d), pool(2 * d), table.cuda(),
+                           torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    q1, q2, lam, w = R.queries(137, B, kv, 1, d)
+    need_ws = ops.paged_fwd_plan(cache, kv)
+    slots = 2 * sms * 2  # partial states: [2 CTAs][2 maps], a row of 2 d each; then their (m, l)
+    part_bytes = -(-slots * 2 * d * 4 // 256) * 256
+    assert need_ws == part_bytes + -(-slots * 8 // 256) * 256
+    mark = 12345.0
+    ws = torch.full((need_ws // 4,), mark, device="cuda")
+    out = ops.paged_fwd(cache, q1, q2, lam, norm_w=w, workspace=ws)
+    parts = ws[part_bytes // 4:][:slots * 2].view(2 * sms, 2, 2)
+    cut = bool((parts != mark).any())
+    alone, uncut, equal = _longest_share(lens, kv, sms)
+    if not cut:  # at most as far from equal shares as the rules have it
+        assert (alone is not None and alone - 2 <= equal + 6) or uncut <= equal + 5
+    elif alone is not None:
+        assert alone - 2 > equal - 2 * B * kv / sms + 6 - 1e-9
+    # the same values as one sequence after another
+    for b in sorted({0, B // 2, B - 1}):
+        one = ops.PagedCache(cache.k1, cache.k2, cache.v, table[b:b + 1].cuda(),
+                             cache.kv_len[b:b + 1].clone())
+        ref = ops.paged_fwd(one, q1[b:b + 1], q2[b:b + 1], lam, norm_w=w).float()
+        # each within a bf16 rounding and its fp32 sums of the value: 2^-8 and 2^-12 apart at most
+        err = (out[b:b + 1].float() - ref).abs()
+        assert bool((err <= ref.abs() * 2.0 ** -7 + 2.0 ** -12 * ref.abs().amax(-1, True)).all())
+
+
+def test_modes_follow_the_lengths_under_one_graph():
+    """One captured call, replayed with lengths that have its items taken one to a CTA, whole in
+    shares, and cut: the values are the definition's, and those of a call with these lengths."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for B, kv, sets in (
+            (20, 2, ([100] * 20, [1500] + [90] * 19, [1500] * 20, [0] * 20, [7, 1200] * 10)),
+            (sms, 2, ([150] * sms, [1500] + [90] * (sms - 1), [0, 300] * (sms // 2) + [1] * (sms % 2)))):
+        c = R.Cache(138, lens=[1500] * B, kv=kv, d=64, page=64, weights=True)
+        cache = c.ops_cache()
+        q1, q2, lam, w = R.queries(139, B, kv, 1, 64)
+        call = lambda: ops.paged_fwd(cache, q1, q2, lam, norm_w=w, lambda_init=LI, accumulate=True)
+        start = c.weights.clone()
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = call()
+        for lens in sets:
+            c.lens = lens
+            c.kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+            c.weights.copy_(start)
+            graph.replay()
+            got, weights = out.clone(), c.weights.clone()
+            c.weights.copy_(start)
+            assert torch.equal(call(), got) and torch.equal(c.weights, weights)
+            some = sorted({0, 1, B // 2, B - 1})
+            sub = R.Cache.__new__(R.Cache)
+            sub.__dict__.update(c.__dict__)
+            sub.lens, sub.table = [lens[b] for b in some], c.table[some]
+            ref, tol, add, add_tol = R.attend(sub, q1[some], q2[some], lam, norm_w=w,
+                                              lambda_init=LI)
+            R.check(got[some], ref, tol, f"lengths {lens[:3]}")
+            for k, b in enumerate(some):
+                if not lens[b]:
+                    continue
+                sub.weights = start
+                want = sub.rows("weights", k).double() + add[k]
+                sub.weights = weights
+                R.check(sub.rows("weights", k), want, add_tol[k] + want.abs() * 3 * 2.0 ** -23,
+                        f"weights of {b}")
+
+
+@pytest.mark.parametrize("lens,kv,H", [([200], 16, 16), ([90, 0, 33], 2, 8), ([130] * 100, 3, 3)])
+def test_room_beyond_the_lengths_changes_nothing(lens, kv, H):
+    """Items taken whole because of the lengths give the bits of those that no length would cut."""
+    outs = []
+    for extra in (0, 600):
+        c = R.Cache(140, lens=lens, kv=kv, d=64, page=16, extra_pages=extra)
+        outs.append(_fwd(c, *R.queries(141, len(lens), H, 1, 64)))
+        assert (ops.paged_fwd_plan(c.ops_cache(), H) > 0) == (extra > 0)
+    assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("kind", ["one to a CTA", "between items"])
+def test_next_kernel_waits_where_the_second_finds_nothing_to_join(kind):
+    """The second kernel is launched, because other lengths would have items cut, and has nothing to
+    do: what follows on the stream still sees the outputs."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    extra = 0
+    if kind == "one to a CTA":  # 64 items of eight tiles, with room for more
+        lens, kv, extra = [1024] * 8, 8, 20
+    else:  # steps of 20, 10 and 10: the bounds of equal shares fall between items
+        lens, kv = [18 * 128, 8 * 128, 8 * 128] * (sms // 2), 1
+    c = R.Cache(142, lens=lens, kv=kv, d=64, page=128, extra_pages=extra)
+    cache = c.ops_cache()
+    q1, q2, lam, w = R.queries(143, len(lens), kv, 1, 64)
+    need = ops.paged_fwd_plan(cache, kv)
+    assert need > 0
+    want = _fwd(c, q1, q2, lam, w)
+    out = torch.empty_like(want)
+    ws = torch.full((need,), 1, dtype=torch.uint8, device="cuda")
+    got = []
+    for _ in range(50):
+        out.fill_(float("nan"))
+        ops.paged_fwd(cache, q1, q2, lam, norm_w=w, lambda_init=LI, workspace=ws, out=out)
+        got.append(out.clone())
+    torch.cuda.synchronize()
+    for x in got:
+        assert torch.equal(x, want)
+    assert bool((ws == 1).all())  # no partial state was left: nothing was cut
