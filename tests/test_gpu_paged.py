@@ -1103,3 +1103,104 @@ def test_next_kernel_waits_where_the_second_finds_nothing_to_join(kind):
     for x in got:
         assert torch.equal(x, want)
     assert bool((ws == 1).all())  # no partial state was left: nothing was cut
+
+
+@pytest.mark.parametrize("B,kv,d,dtype,layout,page", [
+    (5, 8, 64, torch.bfloat16, "head", 16),    # 40 heads: slices of 128 bytes
+    (13, 3, 128, torch.bfloat16, "token", 48),  # 39
+    (10, 8, 64, E4M3, "token", 64), (4, 10, 128, E4M3, "head", 16),
+    (6, 4, 64, torch.bfloat16, "head", 32),    # 24: slices of 64 bytes
+    (5, 3, 128, torch.bfloat16, "head", 16), (7, 3, 64, E4M3, "head", 16)])  # the last: of 32
+def test_evict_of_many_heads(B, kv, d, dtype, layout, page):
+    """As many heads as a served batch has: the move takes wider slices of the rows then."""
+    lens = [800 - 61 * b for b in range(B)]
+    c = R.Cache(144, lens=lens, kv=kv, d=d, page=page, dtype=dtype, layout=layout, weights=True)
+    _check_evict(c, 300, 32)
+    _check_evict(c, 299, 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, E4M3])
+@pytest.mark.parametrize("layout,page", [("head", 48), ("token", 64)])
+def test_append_many_rows_of_every_type(d, dtype, layout, page):
+    """More than 16384 rows, an odd number a head, with padding in front and strided sources."""
+    N, kv = 1639, 5
+    lens = [1700, 1639, 3, 0]
+    c = R.Cache(145, lens=lens, kv=kv, d=d, page=page, dtype=dtype, layout=layout, weights=True,
+                fill=7.0)
+    assert 4 * kv * N > 16384
+    want = {t: R.f64(getattr(c, t)).clone() for t in ("k1", "k2", "v", "weights")}
+    g = torch.Generator().manual_seed(146)
+    new = {t: (torch.randn(4, N, kv, w, generator=g) * 200).to(torch.bfloat16).cuda()
+           .permute(0, 2, 1, 3) for t, w in (("k1", d), ("k2", d), ("v", 2 * d))}
+    for b, n in enumerate(lens):
+        at = torch.arange(max(0, n - N), n, device="cuda")
+        pages, slots = c.table[b].long()[at // page], at % page
+        for t in ("k1", "k2", "v"):
+            rows = R.f64(new[t][b, :, N - len(at):]).transpose(0, 1)
+            want[t][pages, :, slots] = R.to_e4m3(rows) if dtype == E4M3 and t != "v" else rows
+        want["weights"][pages, :, slots] = 0
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ops.paged_append(c.ops_cache(), new["k1"], new["k2"], new["v"], status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    for t in want:
+        assert torch.equal(R.f64(getattr(c, t)), want[t]), t
+
+
+def test_many_items_that_are_cut():
+    """More items than SMs, long enough to be cut, with idle sequences and a bad one among them."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    lens = torch.randint(0, 1101, (sms,), generator=torch.Generator().manual_seed(147)).tolist()
+    lens[:5] = [0, 1, 1100, 0, 1099]
+    lens[-2:] = [1100, 0]
+    _, uncut, equal = _longest_share(lens, 2, sms)
+    assert uncut > equal + 5
+    c = R.Cache(148, lens=lens, kv=2, d=64, page=16, weights=True)
+    before = c.weights.clone()
+    out = _parity(c, 4, 2)
+    q1, q2, lam, w = R.queries(3, c.B, 4, 2, 64)
+    assert torch.equal(_fwd(c, q1, q2, lam, w, accumulate=True), out)
+    _, _, add, add_tol = R.attend(c, q1, q2, lam, norm_w=w, lambda_init=LI)
+    after = c.weights
+    for b in range(sms):
+        if lens[b]:
+            c.weights = before
+            want = c.rows("weights", b).double() + add[b]
+            c.weights = after
+            R.check(c.rows("weights", b), want, add_tol[b] + want.abs() * 6 * 2.0 ** -23,
+                    f"weights of {b}")
+    c.table[4, 60] = -7
+    kept = c.weights.clone()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = ops.paged_fwd(c.ops_cache(), q1, q2, lam, norm_w=w, lambda_init=LI, status=status,
+                        accumulate=True)
+    assert int(status) == ops.ERR_PAGE and bool(torch.isnan(got[4]).all())
+    got[4] = out[4]
+    assert torch.equal(got, out)
+    mine = [int(x) for x in c.table[4] if x >= 0]
+    assert torch.equal(c.weights[mine], kept[mine])
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("d", [64, 128])
+def test_non_finite_newest_values_of_a_joined_item(bad, d):
+    """Values kept out of the product reach the rows that see them through the partial states."""
+    lens = [9003, 5000, 130]
+    c = R.Cache(149, lens=lens, kv=1, d=d, page=16)
+    for b, n in enumerate(lens):
+        for back in (1, 2):
+            c.v[int(c.table[b, (n - back) // 16]), 0, (n - back) % 16, 5] = bad
+    q1, q2, lam, w = R.queries(150, 3, 2, 4, d)
+    out = _fwd(c, q1, q2, lam, w, headnorm=0).double()
+    ref, tol, _, _ = R.attend(c, q1, q2, lam, headnorm=0)
+    R.check(out[:, :, :2], ref[:, :, :2], tol[:, :, :2], "rows before them")
+    others = [x for x in range(2 * d) if x != 5]
+    assert not bool(torch.isfinite(out[:, :, 2:, 5]).any())
+    clean = R.Cache.__new__(R.Cache)
+    clean.__dict__.update(c.__dict__)
+    clean.v = c.v.clone()
+    clean.v[..., 5] = 0
+    ref, tol, _, _ = R.attend(clean, q1, q2, lam, headnorm=0)
+    R.check(out[:, :, 2:][..., others], ref[:, :, 2:][..., others], tol[:, :, 2:][..., others],
+            "the other columns")
