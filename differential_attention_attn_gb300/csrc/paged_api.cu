@@ -21,8 +21,8 @@ bool strides_ok(const diffattn_strides &s, int64_t multiple) {
   return true;
 }
 
-// Everything that the desc and the cache say on their own.  group: the query
-// heads per key/value head (1 for append and evict, where H = kv_heads).
+// Everything that the desc and the cache say on their own.  query_heads: H
+// counts query heads, a multiple of kv_heads (fwd), else H = kv_heads.
 diffattn_status check_cache(const diffattn_desc *desc, const diffpaged_cache *c, bool query_heads) {
   diffattn_status st = check_common_desc(desc);
   if (st != DIFFATTN_OK) return st;

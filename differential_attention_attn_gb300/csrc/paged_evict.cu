@@ -18,10 +18,10 @@
 //      its stores; the slices are independent of one another.  The next
 //      rows' places are fetched while a block of rows is on its way.
 //
-// Bound: HBM, each kept row read and written once.  16 x 8 heads of 8000 to 8192
+// Bound: HBM, each kept row behind the first one dropped read and written once.  16 x 8 heads of 8000 to 8192
 // keys at d = 64 cut to 4096 (543 MB): 103 us, the selection 14 us of it and the
 // move 86 us, 93 % of the copy rate; 4 x 16 heads of e4m3 keys cut from 1088 to
-// 1024: 16 us, 5.5 us the selection.
+// 1024: 16 to 17 us, 5.5 us the selection.
 #include <cuda_runtime.h>
 
 #include <atomic>

@@ -55,10 +55,10 @@
 // 8 sequences x 8 heads x 8192 keys at d = 128, 537 MB: 84 us, 94 %; 24
 // sequences of 100 to 9001 keys in pages of 16, four query heads to a key/value
 // head, 448 MB: 76 us, 87 %; 8 x 8 x 32768 keys, 1.07 GB: 163 to 167 us, 95 to
-// 97 %; one sequence of 200 keys, 16 heads: 6.0 us, of which 2.5 us pass before
+// 97 %; one sequence of 200 keys, 16 heads: 6.3 us, of which 2.5 us pass before
 // the first copy lands.  Of a large call's time beyond the copy rate about 3 us
 // go to the first lookups and copies and 3 us to the join; with 32 rows the
-// softmax bounds it (8 x 8K keys: 16 rows 53 us, 32 rows 83 us).
+// softmax bounds it (8 x 8K keys: 16 rows 53 us, 32 rows 78 to 83 us).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -120,15 +120,18 @@ constexpr int kSlotBytes = 2 * kBoxBytes;
 constexpr int kItemCost = 2;    // steps, see Shares
 // One CTA per item, and nothing to join, where equal shares would not save this many tiles of the
 // longest, what the join and the second segment of most CTAs take (6 us, of 1 us a tile).  64 items
-// of 8 tiles on 152 SMs: 12.6 us, in shares 14.6 us; of 16 tiles 20.2 us and 18.3 us.  16 items of 4
-// tiles: 8.1 and 9.1 us, of 8 tiles 11.7 and 9.5 us.
+// of 8 tiles on 152 SMs: 12.0 us, cut 14.1; of 16 tiles 18.6 and 18.4; 16 items of 4 tiles 7.7 and
+// 8.3, of 8 tiles 10.8 and 9.6; 128 items of 500 to 1500 keys 18.0 and 19.3; 64 of 100 to 1500 keys
+// (cut: it would be 9.2 tiles) 15.0 and 13.8.
 constexpr int kMostAlone = 6;
-// What a second kernel takes that finds nothing to do (64 of 8 tiles: 12.0 us, with one 14.5 us).
+// What a second kernel takes that finds nothing to do (64 x 16 heads of 200 keys: 24.8 us, and 26.3
+// under a table of 4096 keys, which other lengths could have cut).
 constexpr int kSecondKernel = 2;
 // Nor are items cut where they are so many, or so short, that no share gets this many steps longer
-// by taking them whole, which costs less than the join.  408 items of two tiles (8 rows): 19.8 us,
-// cut 24.7; 1024 of two: 25.5 and 28.2; 228 of six (32 rows, d = 128): 58 and 69; 240 of ten, where
-// it would be 5.05 steps: 26.8 and 25.1 us.
+// by taking them whole, which costs less than the join.  408 items of two tiles (8 rows): 18.5 us,
+// cut 22.4; 1024 of two: 24.8 and 27.8; 228 of six (32 rows, d = 128): 54 and 63; 240 of ten, where
+// it would be 5.05 steps: 30.5 and 31.5; 456 of 500 to 900 keys, where it could be more: 33.2 and
+// 33.6.
 constexpr int kUneven = 5;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -363,8 +366,8 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[kN
 }
 
 // Named barriers beside the softmax warps' 1 and 2.  The key warp finds the share while the other
-// warps set up: the load warps wait only for the barriers in shared memory, and the others, whose bounded
-// waits are for this kernel's own work, until the kernel before has ended.
+// warps set up.  The load and query warps wait for that and for the barriers in shared memory, and
+// the others, whose bounded waits are for this kernel's own work, until the kernel before has ended.
 constexpr uint32_t kLoadBarrier = 3, kStartBarrier = 4;
 __device__ __forceinline__ void named_barrier_arrive(uint32_t id, uint32_t count) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
@@ -834,7 +837,7 @@ __device__ __forceinline__ void mma_warp(const FwdParams &p, uint8_t *smem, Ctrl
 }
 
 // ---------------------------------------------------------------------------
-// The softmax warps.  Warp w: map w / 4; its lanes are keys (then value
+// The softmax warps.  Warp w: map (w / 4) % 2, rows by w / 8; its lanes are keys (then value
 // columns) 32 (w % 4) + lane of a tile, as tensor memory gives them to it.
 // ---------------------------------------------------------------------------
 template <int kD, bool kFp8, int kNR>
@@ -982,7 +985,7 @@ __device__ __forceinline__ void softmax_warps(const FwdParams &p, uint8_t *smem,
     ok = ok && healthy;
     if (!ok) *reinterpret_cast<volatile int *>(&sm->failed) = 1;
 
-    // One barrier and vote of all eight warps: has a logit outgrown its reference (or did a wait
+    // One barrier and vote of all softmax warps: has a logit outgrown its reference (or did a wait
     // run out)?
     if (named_barrier_or(1, kConsumers, grew || !ok)) {
       if (*reinterpret_cast<volatile int *>(&sm->failed)) break;

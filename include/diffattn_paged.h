@@ -24,8 +24,10 @@
  * 0 .. max_pages * page_size is found on the device: nothing outside the pool
  * is touched, DIFFATTN_ERR_PAGE is stored in desc->status_dev (when given),
  * and that sequence's output rows are NaN (fwd), its rows on valid pages are
- * written (append), it is left as it is (evict; the weights of fwd).  Entries
- * of the table past a sequence's length are not read.
+ * written (append; nothing of it where its length is bad), it is left as it is
+ * (evict; the weights of fwd).  Entries of the table past a sequence's length
+ * are not read, and by append only those of the new tokens, by evict only those
+ * of the sequences that it cuts.
  *
  * Sequences may share pages (a common prefix) in a call that only reads them:
  * diffpaged_fwd without accumulate.  A page that a call writes (append: those
@@ -96,7 +98,11 @@ diffattn_status diffpaged_append(const diffattn_desc *desc, const diffpaged_cach
  * kv_heads: query head h reads key/value head h / (H / kv_heads).  causal = 1:
  * token i sees the keys up to its own position; 0: all kv_len[b] keys.  A row
  * that sees no key is zero.  What masked or unused places of the pages hold
- * (NaN and infinities too) has no influence.
+ * (NaN and infinities too) has no influence.  A key whose logit is -infinity
+ * has no weight beside others.  A NaN or infinite value (v) that a row sees
+ * makes its column of the row NaN or infinite, an infinite one NaN as well
+ * (inf - inf in the two maps' difference and in the products that make it up),
+ * and with a head norm the whole row NaN.
  *
  * accumulate != 0 also adds, for every key j of a sequence and each key/value
  * head, sum |map1[j] - lambda_h map2[j]| over the N tokens and the query heads
@@ -106,11 +112,17 @@ diffattn_status diffpaged_append(const diffattn_desc *desc, const diffpaged_cach
  * workspace: caller-owned scratch of at least the bytes diffpaged_fwd_plan
  * gives for the same desc and cache sizes, 256-byte aligned; its contents on
  * entry do not matter; calls (and captured graphs) that share one must be
- * ordered.  NULL is fine when the plan gives 0.
+ * ordered.  NULL is fine when the plan gives 0.  It goes by the table's
+ * capacity, not by the lengths: with accumulate about 8 bytes per query head,
+ * new token and place (B * H * N * max_pages * page_size), beside partial
+ * states of at most 128 KB per SM.
  *
  * Domain (else DIFFATTN_ERR_UNSUPPORTED): d 64 or 128, DIFFATTN_BF16 or
  * DIFFATTN_E4M3_QK, N <= 16, H / kv_heads <= 64, page_size a multiple of 16,
- * an sm_103 device.  Longer runs of new tokens go through diffattn_fwd_kv.
+ * an sm_103 device.  A longer run of new tokens (a chunk of a prompt) has no
+ * form over pages: diffattn_fwd_kv takes contiguous keys and values of equal
+ * lengths with as many heads as the queries (for e4m3 keys d = 64 and head
+ * norms 0 and 1 only), so its rows have to be gathered and repeated first.
  */
 diffattn_status diffpaged_fwd(const diffattn_desc *desc, const diffpaged_cache *cache,
                               const void *q1, const void *q2, const float *lambda,
@@ -131,6 +143,9 @@ diffattn_status diffpaged_fwd_plan(const diffattn_desc *desc, const diffpaged_ca
  * keys' rows and weights move to positions 0 .. keep - 1 in their order, in
  * place; rows at positions >= keep stay as they were; kv_len[b] becomes keep,
  * and the sequence's pages past ceil(keep / page_size) are free for the caller.
+ * (So each cache that is evicted from, a layer's for instance, needs a kv_len
+ * of its own: with a shared one the second cache's sequences would be short
+ * already.)
  * Sequences of at most `keep` keys are left as they are.  0 <= recent <= keep.
  * (Positions count from the front of the cache: rotary or other position
  * information is already in the stored keys.)
