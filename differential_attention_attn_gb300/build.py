@@ -26,7 +26,8 @@ LIB_DEBUG = os.path.join(HERE, "libdiffattn_debug.so")
 SOURCES = ["api.cu", "fwd_bf16_sm103.cu", "fwd_f32.cu", "headnorm.cu", "splitkv.cu",
            "noalloc.cu", "bwd_bf16_sm103.cu", "fwd_d128_sm103.cu", "bwd_d128_sm103.cu",
            "selftest.cu", "paged_api.cu", "paged_append.cu", "paged_fwd.cu",
-           "paged_fwd_d64.cu", "paged_fwd_d128.cu", "paged_evict.cu"]
+           "paged_fwd_d64.cu", "paged_fwd_d128.cu", "paged_evict.cu", "rotary.cu",
+           "ragged_api.cu", "ragged_step.cu", "ragged_append.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -61,7 +62,8 @@ def _stale(lib: str = LIB) -> bool:
         return True
     t = os.path.getmtime(lib)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps += [os.path.join(HERE, "..", "include", f) for f in ("diffattn.h", "diffattn_paged.h")]
+    include = os.path.join(HERE, "..", "include")
+    deps += [os.path.join(include, f) for f in os.listdir(include)]
     return any(os.path.getmtime(p) > t for p in deps if os.path.exists(p))
 
 

@@ -11,6 +11,13 @@
 
 namespace diffattn {
 
+// Checks shared by the C-ABI files over paged caches (paged_api.cu): strides (positive multiples
+// below 2^39), and everything that the desc and the cache say on their own.  query_heads: H
+// counts query heads, a multiple of kv_heads, else H = kv_heads.
+bool paged_strides_ok(const diffattn_strides &s, int64_t multiple);
+diffattn_status check_paged_cache(const diffattn_desc *desc, const diffpaged_cache *c,
+                                  bool query_heads);
+
 constexpr int kPageGrain = 16;  // page sizes are multiples of this many rows
 
 // Forward: keys are taken in tiles of kPagedTile; the rows (new token, query

@@ -7,23 +7,24 @@
 
 #include "paged.h"
 
-namespace {
-
 using namespace diffattn;
 
+namespace {
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+}  // namespace
+
+namespace diffattn {
 
 constexpr int64_t kStrideLimit = int64_t{1} << 39;
 
-bool strides_ok(const diffattn_strides &s, int64_t multiple) {
+bool paged_strides_ok(const diffattn_strides &s, int64_t multiple) {
   for (const int64_t x : {s.b, s.h, s.n})
     if (x <= 0 || x % multiple != 0 || x >= kStrideLimit) return false;
   return true;
 }
 
-// Everything that the desc and the cache say on their own.  query_heads: H
-// counts query heads, a multiple of kv_heads (fwd), else H = kv_heads.
-diffattn_status check_cache(const diffattn_desc *desc, const diffpaged_cache *c, bool query_heads) {
+diffattn_status check_paged_cache(const diffattn_desc *desc, const diffpaged_cache *c,
+                                  bool query_heads) {
   diffattn_status st = check_common_desc(desc);
   if (st != DIFFATTN_OK) return st;
   if (c == nullptr) return DIFFATTN_ERR_INVALID_ARG;
@@ -45,15 +46,19 @@ diffattn_status check_cache(const diffattn_desc *desc, const diffpaged_cache *c,
       !aligned(c->weights, 4) || !aligned(c->page_table, 4) || !aligned(c->kv_len, 4))
     return DIFFATTN_ERR_INVALID_ARG;
   const int64_t k_multiple = desc->dtype == DIFFATTN_E4M3_QK ? 16 : 8;
-  if (!strides_ok(c->k1_strides, k_multiple) || !strides_ok(c->k2_strides, k_multiple) ||
-      !strides_ok(c->v_strides, 8))
+  if (!paged_strides_ok(c->k1_strides, k_multiple) || !paged_strides_ok(c->k2_strides, k_multiple) ||
+      !paged_strides_ok(c->v_strides, 8))
     return DIFFATTN_ERR_INVALID_ARG;
   return DIFFATTN_OK;
 }
 
+}  // namespace diffattn
+
+namespace {
+
 diffattn_status plan_fwd(const diffattn_desc *desc, const diffpaged_cache *cache, int accumulate,
                          PagedFwdPlan *plan) {
-  diffattn_status st = check_cache(desc, cache, true);
+  diffattn_status st = check_paged_cache(desc, cache, true);
   if (st != DIFFATTN_OK) return st;
   if (accumulate && cache->weights == nullptr) return DIFFATTN_ERR_INVALID_ARG;
   if (desc->N > kPagedMaxTokens || desc->H / cache->kv_heads > kPagedMaxGroup)
@@ -73,14 +78,14 @@ extern "C" {
 diffattn_status diffpaged_append(const diffattn_desc *desc, const diffpaged_cache *cache,
                                  const void *k1, const void *k2, const void *v,
                                  const diffattn_strides *strides, void *stream) {
-  diffattn_status st = check_cache(desc, cache, false);
+  diffattn_status st = check_paged_cache(desc, cache, false);
   if (st != DIFFATTN_OK) return st;
   if (desc->B * desc->H * desc->N == 0) return DIFFATTN_OK;
   if (!k1 || !k2 || !v || !aligned(k1, 16) || !aligned(k2, 16) || !aligned(v, 16))
     return DIFFATTN_ERR_INVALID_ARG;
   if (strides != nullptr)
     for (int i = 0; i < 3; ++i)
-      if (!strides_ok(strides[i], 8)) return DIFFATTN_ERR_INVALID_ARG;
+      if (!paged_strides_ok(strides[i], 8)) return DIFFATTN_ERR_INVALID_ARG;
   if (desc->N >= (int64_t{1} << 30)) return DIFFATTN_ERR_UNSUPPORTED;
   if ((st = require_sm103()) != DIFFATTN_OK) return st;
   return launch_paged_append(*desc, *cache, k1, k2, v, strides, static_cast<cudaStream_t>(stream));
@@ -109,8 +114,8 @@ diffattn_status diffpaged_fwd(const diffattn_desc *desc, const diffpaged_cache *
     return DIFFATTN_ERR_INVALID_ARG;
   if (strides != nullptr) {
     const int64_t q_multiple = desc->dtype == DIFFATTN_E4M3_QK ? 16 : 8;
-    if (!strides_ok(strides[0], q_multiple) || !strides_ok(strides[1], q_multiple) ||
-        !strides_ok(strides[2], 8))
+    if (!paged_strides_ok(strides[0], q_multiple) || !paged_strides_ok(strides[1], q_multiple) ||
+        !paged_strides_ok(strides[2], 8))
       return DIFFATTN_ERR_INVALID_ARG;
   }
   if (plan.bytes > 0 &&
@@ -123,7 +128,7 @@ diffattn_status diffpaged_fwd(const diffattn_desc *desc, const diffpaged_cache *
 
 diffattn_status diffpaged_evict_plan(const diffattn_desc *desc, const diffpaged_cache *cache,
                                      int64_t keep, size_t *workspace_bytes) {
-  diffattn_status st = check_cache(desc, cache, false);
+  diffattn_status st = check_paged_cache(desc, cache, false);
   if (st != DIFFATTN_OK) return st;
   if (workspace_bytes == nullptr || keep < 0 || cache->weights == nullptr)
     return DIFFATTN_ERR_INVALID_ARG;

@@ -19,6 +19,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdiffattn.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "diffattn.h")
 PAGED_HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "diffattn_paged.h")
+ROTARY_HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "diffattn_rotary.h")
+RAGGED_HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "diffattn_ragged.h")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_BOUNDS = 0, 1, 2, 3, 4, 5
 ERR_PAGE = 6
@@ -57,6 +59,22 @@ class PagedCacheStruct(ctypes.Structure):
         ("num_pages", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
         ("max_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
+    ]
+
+
+class RotaryTableStruct(ctypes.Structure):
+    """Mirror of `diffrotary_table` in include/diffattn_rotary.h."""
+    _fields_ = [("freq", ctypes.c_void_p), ("rot", ctypes.c_int32), ("neighbours", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class PageBookStruct(ctypes.Structure):
+    """Mirror of `diffragged_book` in include/diffattn_ragged.h."""
+    _fields_ = [
+        ("kv_len", ctypes.c_void_p), ("held", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+        ("free_pages", ctypes.c_void_p), ("free_count", ctypes.c_void_p), ("B", ctypes.c_int64),
+        ("max_pages", ctypes.c_int64), ("capacity", ctypes.c_int64),
+        ("page_size", ctypes.c_int32), ("reserved", ctypes.c_int32),
     ]
 
 
@@ -144,6 +162,16 @@ def bind(lib):
             ("evict_plan", [dp, cp, i64, szp]),
             ("evict", [dp, cp, i64, i64, vp, ctypes.c_size_t, vp])):
         fn = getattr(lib, "diffpaged_" + name)
+        fn.restype, fn.argtypes = ctypes.c_int, args
+    i32, f64, sp = ctypes.c_int32, ctypes.c_double, ctypes.POINTER(Strides)
+    tp, bp = ctypes.POINTER(RotaryTableStruct), ctypes.POINTER(PageBookStruct)
+    for name, args in (
+            ("diffrotary_frequencies", [i32, f64, i32, f64, f64, f64, f64, vp,
+                                        ctypes.POINTER(ctypes.c_float)]),
+            ("diffrotary_apply", [dp, tp, i32, vp, vp, vp, sp, vp, i64, i64, i32, vp]),
+            ("diffragged_step", [bp, vp, i64, vp, vp, vp, vp, vp]),
+            ("diffragged_append", [dp, cp, vp, vp, vp, vp, vp, vp, vp, sp, vp, tp, vp, vp])):
+        fn = getattr(lib, name)
         fn.restype, fn.argtypes = ctypes.c_int, args
     lib.diffattn_selftest_wait.restype = ctypes.c_int
     lib.diffattn_selftest_wait.argtypes = [vp, ctypes.c_int64, vp]
@@ -741,13 +769,17 @@ class PagedCache:
         return OK, self._keep(keep, status, (ref, need.value))
 
 
-def _strides4(t):
-    """(outer, head, row) element strides of a 4-D tensor with contiguous rows.  An axis of one
-    element is never stepped along: it gets the stride it would have in contiguous storage."""
-    s, n = t.stride(), t.shape
+def _strides_of(n, s):
+    """(outer, head, row) element strides of a 4-D tensor of shape n and strides s with contiguous
+    rows.  An axis of one element is never stepped along: it gets the stride it would have in
+    contiguous storage."""
     row = s[2] if n[2] > 1 else n[3]
     head = s[1] if n[1] > 1 else row * n[2]
     return Strides(s[0] if n[0] > 1 else head * n[1], head, row)
+
+
+def _strides4(t):
+    return _strides_of(t.shape, t.stride())
 
 
 def _strides_or_null(a, b, c):
@@ -909,6 +941,262 @@ def paged_evict(cache, *, keep: int, recent: int = 0, workspace=None, status=Non
     if raw_status:
         return st
     _check(st)
+
+
+# ---- rotary positions ------------------------------------------------------------------------
+
+_SCALING = {None: 0, "linear": 1, "ntk": 2, "parts": 3}
+
+
+class RotaryTable:
+    """The frequencies of a rotary position encoding (`diffrotary_table` of
+    include/diffattn_rotary.h): the first `rot` channels of a row are turned, in pairs
+    (i, i + rot / 2) or, with neighbours, (2i, 2i + 1).
+
+    scaling stretches it for longer contexts by `factor`: "linear" (all frequencies / factor),
+    "ntk" (a larger base) or "parts" (pairs that turn at least `fast` times within the
+    `original` positions stay, those of at most `slow` turns are stretched, and the turned
+    channels grow by 0.1 ln(factor) + 1).  `freq` (int64, the bits of 64-bit fractions of a
+    turn) and `scale` are made once; the frequencies in radians are freq * 2 pi / 2^64.
+    """
+
+    def __init__(self, rot: int, *, base: float = 10000.0, neighbours: bool = False, scaling=None,
+                 factor: float = 1.0, original: float = 0.0, fast: float = 32.0, slow: float = 1.0,
+                 device="cuda"):
+        if scaling not in _SCALING:
+            raise ValueError(f"scaling must be one of {list(_SCALING)}")
+        freq = torch.empty(max(0, int(rot)) // 2, dtype=torch.int64)
+        scale = ctypes.c_float(0)
+        _check(load().diffrotary_frequencies(int(rot), float(base), _SCALING[scaling],
+                                             float(factor), float(original), float(fast),
+                                             float(slow), freq.data_ptr(), ctypes.byref(scale)))
+        self.rot, self.neighbours, self.scale = int(rot), bool(neighbours), scale.value
+        self.freq = freq.to(device)
+        if not self.freq.is_cuda:
+            raise ValueError("the table must be on a CUDA device")
+        self.device, self.index = self.freq.device, self.freq.get_device()
+        self._struct = RotaryTableStruct(self.freq.data_ptr(), self.rot, int(self.neighbours),
+                                         self.scale, 0)
+        self._ref = ctypes.byref(self._struct)
+        self._calls = {}
+
+    # What the shapes and strides of a call's tensors come to is checked once and kept under them
+    # (plain numbers; a status word's address makes a key of its own kind, so those are not kept).
+
+    def _new_call(self, key, status):
+        dtype, shapes, x_strides, y_strides = key
+        if not 1 <= len(shapes) <= 4:
+            raise ValueError("one to four tensors, [B, heads, N, d] each")
+        if dtype not in _DTYPE_CODE:
+            raise ValueError(f"unsupported dtype {dtype}")
+        if any(len(s) != 4 for s in shapes):
+            raise ValueError("tensors must be [B, heads, N, d]")
+        B, _, N, d = shapes[0]
+        if any((s[0], s[2], s[3]) != (B, N, d) for s in shapes):
+            raise ValueError("the tensors must agree in B, N and d")
+        for strides in (x_strides, y_strides):
+            if any(s[3] != 1 for s in strides):
+                raise ValueError("rows must be contiguous (last stride 1)")
+        n = len(shapes)
+        both = [_strides_of(shapes[i // 2], (x_strides, y_strides)[i % 2][i // 2])
+                for i in range(2 * n)]
+        desc = make_desc(B, shapes[0][1], N, d, _DTYPE_CODE[dtype], True, 0, 0.0, 0.0, status)
+        call = (ctypes.byref(desc), n, ctypes.c_void_p * n,
+                (ctypes.c_int64 * n)(*(s[1] for s in shapes)), (Strides * (2 * n))(*both), B, N)
+        if status is None:
+            if len(self._calls) >= 256:
+                self._calls.clear()
+            self._calls[key] = call
+        return call
+
+
+def _rotary(table, tensors, positions, start, outs, status, stream, raw_status, inverse):
+    x = list(tensors)
+    if not x:
+        raise ValueError("one to four tensors, [B, heads, N, d] each")
+    index, dtype = table.index, x[0].dtype
+    if outs is None:
+        with (contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)):
+            outs = [torch.empty_like(t) for t in x]
+    shapes = tuple([t.shape for t in x])
+    key = (dtype, shapes, tuple([t.stride() for t in x]), tuple([t.stride() for t in outs]))
+    call = table._calls.get(key) if status is None else None
+    ref, n, pointers, heads, strides, B, N = call or table._new_call(key, status)
+    if len(outs) != n or tuple([t.shape for t in outs]) != shapes:
+        raise ValueError("outs must be as many tensors of the inputs' shapes")
+    for t in (*x, *outs):
+        if t.dtype != dtype:
+            raise ValueError("all tensors must be of one dtype")
+        if t.get_device() != index:
+            raise ValueError("all tensors must be on the table's device")
+    at, step = None, 0
+    if positions is not None:
+        if positions.dtype != torch.int32 or positions.shape not in ((N,), (B, N)) or \
+                not positions.is_contiguous() or positions.get_device() != index:
+            raise ValueError("positions must be contiguous int32 [N] or [B, N] on the table's "
+                             "device")
+        at, step = positions.data_ptr(), N if positions.dim() == 2 else 0
+    handle = _stream_on(table, stream)
+    st = (_lib or load()).diffrotary_apply(
+        ref, table._ref, n, pointers(*[t.data_ptr() for t in x]),
+        pointers(*[t.data_ptr() for t in outs]), heads, strides, at, step, int(start),
+        inverse, handle)
+    if raw_status:
+        return st
+    _check(st)
+    return outs
+
+
+def rotary(table, tensors, positions=None, *, start: int = 0, outs=None, status=None, stream=None,
+           raw_status: bool = False):
+    """`diffrotary_apply`: rows turned by their positions, one launch for up to four tensors.
+
+    tensors: [B, heads, N, d] each (q1, q2, k1, k2 with their own numbers of heads; d 64 or 128),
+    all bf16 or all fp32, views of any layout with contiguous rows.  positions: int32 [N] or
+    [B, N], any values; without them row i is at start + i.  outs: tensors of the same shapes (the
+    inputs themselves: in place; new ones when None).  Returns the list of outputs.
+    """
+    return _rotary(table, tensors, positions, start, outs, status, stream, raw_status, 0)
+
+
+def rotary_bwd(table, grads, positions=None, *, start: int = 0, outs=None, status=None,
+               stream=None, raw_status: bool = False):
+    """Gradients of `rotary`'s inputs from those of its outputs: the rows turned back."""
+    return _rotary(table, grads, positions, start, outs, status, stream, raw_status, 1)
+
+
+# ---- packed ("ragged") batches ---------------------------------------------------------------
+
+class PageBook:
+    """Who has which pages (`diffragged_book` of include/diffattn_ragged.h), for a cache or several
+    of one geometry: page_table [B, max_pages] and kv_len [B] as in PagedCache (the same tensors),
+    held [B] (the pages of each sequence: the first entries of its table), free_pages [capacity]
+    (a stack) and free_count [1].  All int32 CUDA tensors of one device, contiguous, checked here
+    once and then changed in place."""
+
+    def __init__(self, page_table, kv_len, held, free_pages, free_count, page_size: int):
+        if page_table.dim() != 2 or free_pages.dim() != 1:
+            raise ValueError("page_table must be [B, max_pages] and free_pages [capacity]")
+        B, max_pages = page_table.shape
+        for name, t, shape in (("page_table", page_table, (B, max_pages)), ("kv_len", kv_len, (B,)),
+                               ("held", held, (B,)), ("free_pages", free_pages, free_pages.shape),
+                               ("free_count", free_count, (1,))):
+            if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous int32 {tuple(shape)}")
+            if not t.is_cuda or t.device != page_table.device:
+                raise ValueError("all tensors must be CUDA tensors of one device")
+        self.page_table, self.kv_len, self.held = page_table, kv_len, held
+        self.free_pages, self.free_count = free_pages, free_count
+        self.B, self.page_size = B, int(page_size)
+        self.device, self.index = page_table.device, page_table.get_device()
+        self._struct = PageBookStruct(kv_len.data_ptr(), held.data_ptr(), page_table.data_ptr(),
+                                      free_pages.data_ptr(), free_count.data_ptr(), B, max_pages,
+                                      free_pages.numel(), self.page_size, 0)
+        self._ref = ctypes.byref(self._struct)
+
+
+def _whole(name, t, dtype, n, index):
+    if t.dtype != dtype or t.numel() != n or t.dim() != 1 or not t.is_contiguous() or \
+            t.get_device() != index:
+        raise ValueError(f"{name} must be contiguous {dtype} [{n}] on the cache's device")
+    return t.data_ptr()
+
+
+def ragged_step(book, new_len, *, q_start, positions=None, slots=None, status=None, stream=None,
+                raw_status: bool = False):
+    """`diffragged_step`: a step's lengths, pages, q_start, positions and slots, on the device.
+
+    new_len: int32 [B], the sequences' new tokens (-1: it has ended).  Written: q_start int32
+    [B + 1]; positions int32 [T] and slots int64 [T] of the packed rows (either may be None), -1
+    behind the last token; and the book's tensors.  A step that does not fit changes none of these,
+    gives all-zero q_start and stores ERR_PAGE in `status` (int32 [1]).
+    """
+    index, T = book.index, 0
+    if positions is not None:
+        T = positions.numel()
+    elif slots is not None:
+        T = slots.numel()
+    new = _whole("new_len", new_len, torch.int32, book.B, index)
+    start = _whole("q_start", q_start, torch.int32, book.B + 1, index)
+    at = None if positions is None else _whole("positions", positions, torch.int32, T, index)
+    to = None if slots is None else _whole("slots", slots, torch.int64, T, index)
+    word = None if status is None else _whole("status", status, torch.int32, 1, index)
+    handle = _stream_on(book, stream)
+    if positions is None and slots is None:
+        T = 2 ** 31 - 1  # no rows to write, and any number of them
+    st = (_lib or load()).diffragged_step(book._ref, new, T, start, at, to, word, handle)
+    if raw_status:
+        return st
+    _check(st)
+
+
+def _packed_call(cache, key, status):
+    """The descriptor, strides and output shapes of a diffragged_append call."""
+    H, shapes, strides = key
+    k_shape, v_shape = shapes[0], shapes[2]
+    if len(k_shape) != 3 or k_shape[1:] != (cache.kv_heads, cache.d):
+        raise ValueError(f"k1 and k2 must be [T, {cache.kv_heads}, {cache.d}]")
+    T = k_shape[0]
+    want = [k_shape, k_shape, (T, cache.kv_heads, 2 * cache.d)] + [(T, H, cache.d)] * 4
+    for name, s, w in zip(("k1", "k2", "v", "q1", "q2", "q1's output", "q2's output"), shapes,
+                          want):
+        if tuple(s) != tuple(w):
+            raise ValueError(f"{name} must be {tuple(w)}")
+    if any(s[2] != 1 for s in strides):
+        raise ValueError("rows must be contiguous (last stride 1)")
+    st = [_strides_of((1, *n), (1, *s)) for n, s in zip(shapes, strides)]
+    # _strides_of takes [outer, head, row]: here the second axis is the token's, the third the head's
+    st = [Strides(0, s.n, s.h) for s in st]
+    order = [3, 4, 0, 1, 2, 5, 6] if len(st) == 7 else [0, 0, 0, 1, 2, 0, 0]
+    desc = make_desc(1, H, T, cache.d, cache.code, True, 0, 0.0, 0.0, status)
+    return cache._keep(key, status, (ctypes.byref(desc), (Strides * 7)(*(st[i] for i in order)), T))
+
+
+def ragged_append(cache, k1, k2, v, slots, *, rotary=None, positions=None, q=None, q_out=None,
+                  status=None, stream=None, raw_status: bool = False):
+    """`diffragged_append`: the packed tokens' keys and values into the cache, and their queries,
+    turned by `rotary` (a RotaryTable; None: as they are) at `positions` (int32 [T]).
+
+    k1, k2: bf16 [T, kv_heads, d], v: bf16 [T, kv_heads, 2d], slots: int64 [T] as ragged_step gives
+    them (-1: the token is left out).  q: (q1, q2), bf16 [T, H, d], or None; q_out: two tensors of
+    that shape and the cache's key dtype (new ones when None; bf16 ones may be the inputs).
+    Views of any layout with contiguous rows.  Returns q_out.
+    """
+    index, bf16 = cache.index, torch.bfloat16
+    ts = [k1, k2, v]
+    H = cache.kv_heads
+    if q is not None:
+        H = q[0].shape[1] if q[0].dim() == 3 else -1
+        if q_out is None:
+            q_out = [_new_on(stream, q[0].shape, cache.dtype, cache.device) for _ in range(2)]
+        ts += [q[0], q[1], q_out[0], q_out[1]]
+    key = (H, tuple([t.shape for t in ts]), tuple([t.stride() for t in ts]))
+    call = cache._calls.get(key) if status is None else None
+    ref, strides, T = call or _packed_call(cache, key, status)
+    for t in ts[:5]:
+        if t.dtype != bf16:
+            raise ValueError("k1, k2, v and q must be bfloat16")
+    for t in ts[5:]:
+        if t.dtype != cache.dtype:
+            raise ValueError(f"q_out must be {cache.dtype}, as the cache's keys")
+    for t in ts:
+        if t.get_device() != index:
+            raise ValueError("all tensors must be on the cache's device")
+    to = _whole("slots", slots, torch.int64, T, index)
+    at = None
+    if rotary is not None:
+        if rotary.index != index or positions is None:
+            raise ValueError("rotary must be on the cache's device, and goes with positions")
+        at = _whole("positions", positions, torch.int32, T, index)
+    handle = _stream_on(cache, stream)
+    ptrs = [t.data_ptr() for t in ts]
+    qs, outs = (ptrs[3:5], ptrs[5:7]) if q is not None else ((None, None), (None, None))
+    st = (_lib or load()).diffragged_append(ref, cache._ref, *qs, *ptrs[:3], *outs, strides, to,
+                                            None if rotary is None else rotary._ref, at, handle)
+    if raw_status:
+        return st
+    _check(st)
+    return q_out
 
 
 def headnorm(x, *, H: int, norm_w=None, eps: float = 1e-5, lambda_init: float = 0.0,

@@ -1,0 +1,99 @@
+/*
+ * A serving step over a packed ("ragged") batch on the paged cache of
+ * diffattn_paged.h: prompts, chunks of prompts and single tokens together (part
+ * of libdiffattn; types, status codes and conventions as there).
+ *
+ * The new tokens of B sequences stand behind one another in tensors of N rows:
+ * those of sequence b are rows q_start[b] .. q_start[b + 1] - 1 (q_start: device
+ * int32 [B + 1], not falling, q_start[0] >= 0); rows outside q_start[0] ..
+ * q_start[B] - 1 belong to none and are neither read nor written.  A sequence's
+ * n tokens are its newest: token i sits at position kv_len[b] - n + i of its
+ * cache (kv_len counts them; a negative position is padding).
+ *
+ * A step: diffragged_step grows the sequences, gives them pages and works out
+ * where each token goes; per layer, diffragged_append turns the queries and
+ * keys and writes the cache's rows.  All sizes but the tensors' capacities are
+ * read on the device, so a captured step replays with new ones.
+ */
+#ifndef DIFFATTN_RAGGED_H
+#define DIFFATTN_RAGGED_H
+
+#include "diffattn_paged.h"
+#include "diffattn_rotary.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* The pages of a cache (or of several of one geometry, such as the layers' of a
+ * model) and who has them; all device int32. */
+typedef struct diffragged_book {
+    int32_t *kv_len;     /* [B] lengths */
+    int32_t *held;       /* [B] pages that each sequence has: the first entries of its table */
+    int32_t *page_table; /* [B, max_pages] */
+    int32_t *free_pages; /* [capacity] a stack of the pages that nobody has */
+    int32_t *free_count; /* [1] how many */
+    int64_t B;
+    int64_t max_pages;   /* >= 1 */
+    int64_t capacity;    /* >= 0 */
+    int32_t page_size;   /* >= 1; max_pages * page_size < 2^30 */
+    int32_t reserved;    /* 0 */
+} diffragged_book;
+
+/*
+ * diffragged_step — the batch's bookkeeping for one step.
+ *
+ * new_len: device int32 [B], each sequence's new tokens; -1 ends a sequence (its
+ * length becomes 0).  Lengths grow; a sequence then holds ceil(length /
+ * page_size) pages: what it has beyond that (it has ended, or diffpaged_evict
+ * has cut it) goes back on the stack, by sequence and place in its table, and
+ * what it lacks is then taken from the top of the stack, in the same order.
+ * Entries of the table that no longer hold a page keep their values, and so do
+ * those of free_pages above the new count.
+ *
+ * Outputs: q_start [B + 1]; for each packed row positions [N] (int32) and slots
+ * [N] (int64, page * page_size + row in it), either NULL when not wanted, -1 in
+ * rows behind the last token.
+ *
+ * A step that does not fit (too few free pages, more than N tokens, a sequence
+ * longer than its table, a stack that would outgrow its capacity) or whose
+ * numbers are wrong (new_len < -1; a negative length or count; held outside
+ * ceil(length / page_size) .. max_pages) changes nothing: q_start is all 0,
+ * positions and slots all -1, and DIFFATTN_ERR_PAGE is stored in status (when
+ * given).
+ */
+diffattn_status diffragged_step(const diffragged_book *book, const int32_t *new_len, int64_t N,
+                                int32_t *q_start, int32_t *positions, int64_t *slots,
+                                int32_t *status, void *stream);
+
+/*
+ * diffragged_append — the packed tokens' rows into the cache, turned by their
+ * positions.
+ *
+ * q1, q2: device bf16 [N, H, d]; k1, k2: [N, kv_heads, d]; v: [N, kv_heads, 2d];
+ * q1_out, q2_out: [N, H, d], bf16 or, with DIFFATTN_E4M3_QK, e4m3.  q1, q2 and
+ * their outputs are all NULL where only the cache is written; a bf16 output may
+ * be its input (same strides).  strides[0..6]: those of q1, q2, k1, k2, v,
+ * q1_out, q2_out in elements (n: of a token, h: of a head, b not used; positive
+ * multiples of 16 bytes below 2^39), or NULL when all are contiguous.
+ * slots: device int64 [N]; a token of slot -1 is left out, its query rows too;
+ * one outside -1 .. num_pages * page_size - 1 as well, and DIFFATTN_ERR_PAGE is
+ * stored.  No slot but -1 stands twice.  table NULL: nothing is turned, else
+ * positions (device int32 [N]) has each token's.  Values are rounded once, to
+ * bf16 or (saturating at +-448, NaN stays NaN) to e4m3; v is copied.  Weights of
+ * the written places become zero where the cache has any.
+ * desc: N, H (a multiple of kv_heads; with q1 NULL only checked), d, dtype;
+ * B and the rest are checked but not used.
+ */
+diffattn_status diffragged_append(const diffattn_desc *desc, const diffpaged_cache *cache,
+                                  const void *q1, const void *q2, const void *k1, const void *k2,
+                                  const void *v, void *q1_out, void *q2_out,
+                                  const diffattn_strides *strides, const int64_t *slots,
+                                  const diffrotary_table *table, const int32_t *positions,
+                                  void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* DIFFATTN_RAGGED_H */
