@@ -27,7 +27,8 @@ SOURCES = ["api.cu", "fwd_bf16_sm103.cu", "fwd_f32.cu", "headnorm.cu", "splitkv.
            "noalloc.cu", "bwd_bf16_sm103.cu", "fwd_d128_sm103.cu", "bwd_d128_sm103.cu",
            "selftest.cu", "paged_api.cu", "paged_append.cu", "paged_fwd.cu",
            "paged_fwd_d64.cu", "paged_fwd_d128.cu", "paged_evict.cu", "rotary.cu",
-           "ragged_api.cu", "ragged_step.cu", "ragged_append.cu"]
+           "ragged_api.cu", "ragged_step.cu", "ragged_append.cu", "ragged_fwd.cu",
+           "ragged_fwd_d64.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -23,4 +23,19 @@ diffattn_status launch_ragged_append(const diffattn_desc &desc, const diffpaged_
                                      const diffrotary_table *table, const int32_t *positions,
                                      cudaStream_t stream);
 
+// Forward: shares of the work (a CTA at d = 64, a pair of them at d = 128) and workspace offsets.
+struct RaggedFwdPlan {
+  int32_t shares;
+  bool joins;  // a second kernel may have something to do
+  size_t part, join, swap;
+  size_t bytes;
+};
+RaggedFwdPlan plan_ragged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache,
+                              int sm_count);
+diffattn_status launch_ragged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache,
+                                  const RaggedFwdPlan &plan, const int32_t *q_start, const void *q1,
+                                  const void *q2, const float *lambda, const float *norm_w,
+                                  void *out, const diffattn_strides strides[3], void *workspace,
+                                  cudaStream_t stream);
+
 }  // namespace diffattn

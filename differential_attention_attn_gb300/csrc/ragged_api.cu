@@ -18,6 +18,23 @@ bool packed_strides_ok(const diffattn_strides &s, int64_t multiple) {
   return paged_strides_ok({multiple, s.h, s.n}, multiple);
 }
 
+// Everything about a forward but its tensors; the plan.
+diffattn_status plan_fwd(const diffattn_desc *desc, const diffpaged_cache *cache,
+                         RaggedFwdPlan *plan) {
+  diffattn_status st = check_paged_cache(desc, cache, true);
+  if (st != DIFFATTN_OK) return st;
+  if (desc->d != 64) return DIFFATTN_ERR_UNSUPPORTED;
+  if (desc->H / cache->kv_heads > kRaggedMaxGroup || desc->N > (int64_t{1} << 30) ||
+      desc->B >= (int64_t{1} << 24) || desc->H > 65535)
+    return DIFFATTN_ERR_UNSUPPORTED;
+  *plan = RaggedFwdPlan{};
+  if (desc->B == 0 || desc->H == 0 || desc->N == 0) return DIFFATTN_OK;
+  const int sms = device_sm_count();
+  if (sms <= 1) return DIFFATTN_ERR_CUDA;
+  *plan = plan_ragged_fwd(*desc, *cache, sms);
+  return DIFFATTN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -94,6 +111,42 @@ diffattn_status diffragged_append(const diffattn_desc *desc, const diffpaged_cac
   void *const out[2] = {q1_out, q2_out};
   return launch_ragged_append(*desc, *cache, src, out, st7, slots, table, positions,
                               static_cast<cudaStream_t>(stream));
+}
+
+diffattn_status diffragged_fwd_plan(const diffattn_desc *desc, const diffpaged_cache *cache,
+                                    size_t *workspace_bytes) {
+  if (workspace_bytes == nullptr) return DIFFATTN_ERR_INVALID_ARG;
+  RaggedFwdPlan plan;
+  const diffattn_status st = plan_fwd(desc, cache, &plan);
+  if (st == DIFFATTN_OK) *workspace_bytes = plan.bytes;
+  return st;
+}
+
+diffattn_status diffragged_fwd(const diffattn_desc *desc, const diffpaged_cache *cache,
+                               const int32_t *q_start, const void *q1, const void *q2,
+                               const float *lambda, const float *norm_w, void *out,
+                               const diffattn_strides *strides, void *workspace,
+                               size_t workspace_bytes, void *stream) {
+  RaggedFwdPlan plan;
+  diffattn_status st = plan_fwd(desc, cache, &plan);
+  if (st != DIFFATTN_OK) return st;
+  if (desc->B == 0 || desc->H == 0 || desc->N == 0) return DIFFATTN_OK;
+  if (!q_start || !q1 || !q2 || !lambda || !out || !aligned(q_start, 4) || !aligned(q1, 16) ||
+      !aligned(q2, 16) || !aligned(out, 16) || !aligned(lambda, 4) || !aligned(norm_w, 16))
+    return DIFFATTN_ERR_INVALID_ARG;
+  const bool fp8 = desc->dtype == DIFFATTN_E4M3_QK;
+  diffattn_strides st3[3];
+  for (int i = 0; i < 3; ++i) {
+    const int64_t width = i == 2 ? 2 * desc->d : desc->d;
+    st3[i] = strides ? strides[i] : diffattn_strides{0, width, desc->H * width};
+    if (!packed_strides_ok(st3[i], fp8 && i < 2 ? 16 : 8)) return DIFFATTN_ERR_INVALID_ARG;
+  }
+  if (plan.bytes > 0 &&
+      (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < plan.bytes))
+    return DIFFATTN_ERR_INVALID_ARG;
+  if ((st = require_sm103()) != DIFFATTN_OK) return st;
+  return launch_ragged_fwd(*desc, *cache, plan, q_start, q1, q2, lambda, norm_w, out, st3, workspace,
+                           static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,486 @@
+// diffragged_fwd: what its two kernels (d = 64 and d = 128) have in common: how
+// the work is cut, how a share of it is walked, and the load warps.
+//
+// The mathematics.  Rows are r = (token, query head of the group) of one
+// key/value head, 128 to a tile, so that a tile's rows share every key and value
+// that it reads:
+//   x_m[r, j] = q_m[r] . k_m[j] / sqrt(d),  map_m = softmax_j(x_m),  m = 1, 2
+//   o[r] = sum_j (map1[r, j] - lambda_h map2[r, j]) v[j], then the head norm,
+// keys j up to the row's position.  An item is a (sequence, key/value head, tile
+// of rows) with its keys in tiles of 128; each map is an ordinary softmax with a
+// running reference and sum, so that ranges of an item's keys done by different
+// CTAs join exactly: with M = max m_s, O = sum_s 2^(m_s - M) O_s, l alike.
+//
+// How the work is cut.  All items lie on a line, each kItemCost steps that stand
+// for its epilogue, then a step for each key tile, and every share (a CTA, or a
+// pair of them) takes an equal piece of it, found from q_start and kv_len on the
+// device: a batch of prompts, chunks and single tokens is balanced, and a
+// captured graph replays with others.  Items that a border cuts leave partial
+// states that a second kernel joins.  Where cutting gains less than that costs,
+// shares take whole items (see cut_line).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "debug_check.cuh"
+#include "ptx.cuh"
+#include "ragged.h"
+
+namespace diffattn {
+
+// An item that a border cuts, as the share with its first tile leaves it for the second kernel.
+struct RaggedJoin {
+  int32_t parts;  // 0: none
+  int32_t slot;   // of the first part; the k-th is in slot 2 (slot / 2 + k)
+  int32_t hk, row, tokens, first;  // key/value head, first row and its position, tokens
+  int32_t pad[2];
+};
+
+struct RaggedParams {
+  const int32_t *q_start, *kv_len, *page_table;
+  const float *lambda, *norm_w;
+  __nv_bfloat16 *out;
+  int32_t *status;
+  float *part;        // [2 * shares][2 maps][part_floats(2 d)]
+  RaggedJoin *joins;  // [shares]
+  float *swap;        // d = 128: what the CTAs of a pair hand one another
+  int64_t out_n, out_h;  // element strides of a token and a head
+  int32_t B, N, kv_heads, group, tokens;  // N: packed rows; tokens: of a tile, 128 / group
+  int32_t num_pages, max_pages, page_size, piece_rows;
+  int32_t causal, headnorm, shares;
+  FastDiv by_page, by_group, by_tokens;
+  float eps, out_scale, scale_log2;
+};
+
+diffattn_status launch_ragged_main_d64(const RaggedParams &p, const CUtensorMap (&maps)[5], bool fp8,
+                                       cudaStream_t stream);
+diffattn_status launch_ragged_main_d128(const RaggedParams &p, const CUtensorMap (&maps)[5],
+                                        bool fp8, cudaStream_t stream);
+
+using RaggedKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                              const CUtensorMap, const CUtensorMap, const RaggedParams);
+// One launch of a main kernel, `cluster` CTAs a share, behind the kernel before (dependent launch).
+// ready: which devices have the kernel's shared memory size set.
+inline diffattn_status launch_ragged_kernel(RaggedKernel kernel, std::atomic<bool> (&ready)[64],
+                                            const RaggedParams &p, const CUtensorMap (&maps)[5],
+                                            int threads, uint32_t smem, int cluster,
+                                            cudaStream_t stream) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DIFFATTN_ERR_CUDA;
+  if (dev < 0 || dev >= 64) return DIFFATTN_ERR_UNSUPPORTED;
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem)) != cudaSuccess)
+      return DIFFATTN_ERR_CUDA;
+    ready[dev].store(true, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.shares * cluster));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], maps[4], p) ==
+                 cudaSuccess
+             ? DIFFATTN_OK
+             : DIFFATTN_ERR_CUDA;
+}
+
+// A part: O [2 d columns][128 rows] as accumulated, references (log2 units), sums.
+__host__ __device__ constexpr int64_t part_floats(int dv) { return (dv + 2) * 128ll; }
+
+namespace {
+
+constexpr int kTile = 128;  // keys of a tile, and rows
+constexpr int kItemCost = 2;
+// Steps that leaving parts and joining them costs a call, about.
+constexpr int kJoinSteps = 8;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kDrainNs = 200000000ull;
+constexpr int kSegRing = 4;
+
+enum : int32_t { kWhole, kUncut, kCut };  // how shares take items
+enum : int32_t { kStop = 1, kDirect = 2, kEmpty = 4, kBadLen = 8 };
+
+// A share's part of an item.
+struct Segment {
+  int32_t row, tokens;    // first packed row, tokens of this tile of rows
+  int32_t first, len;     // position of its first token, keys of the sequence
+  int32_t b, hk;
+  int32_t tile0, tiles;   // key tiles
+  int32_t flags, slot;
+};
+
+__device__ __forceinline__ bool drain_wait(uint64_t *bar, uint32_t parity) {
+  volatile int never = 0;
+  return mbar_wait(bar, parity, &never, kDrainNs);
+}
+__device__ __forceinline__ void fence_async_proxy() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// sum_{i < n} floor((a i + b) / m), a, b >= 0, by exchanging the two axes of the lattice below the
+// line (Euclid's steps on a and m).
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int32_t m, int32_t a, int64_t b) {
+  int64_t sum = 0;
+  while (true) {
+    if (a >= m) {
+      sum += n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      sum += n * (b / m);
+      b %= m;
+    }
+    const int64_t y = a * n + b;
+    if (y < m) return sum;
+    n = y / m;
+    b = y % m;
+    const int32_t t = m;
+    m = a;
+    a = t;
+  }
+}
+
+// A sequence's new tokens, in tiles of rows, and the steps of these.
+struct Seq {
+  int32_t row, n, len, first, tiles;  // first: position of its first new token; tiles of rows
+  bool bad_len, bad_rows;
+  __device__ __forceinline__ Seq() {}
+  __device__ __forceinline__ Seq(const RaggedParams &p, int32_t b) {
+    row = p.q_start[b];
+    const int32_t end = p.q_start[b + 1];
+    len = p.kv_len[b];
+    bad_rows = row < 0 || end < row || end > p.N;
+    n = bad_rows ? 0 : end - row;
+    bad_len = len < 0 || len > p.max_pages * p.page_size;
+    if (bad_len) len = 0;
+    first = len - n;
+    tiles = p.by_tokens.div(n + p.tokens - 1);
+  }
+  // Keys that tile q of rows sees, and key tiles (one for a tile that only has rows to write).
+  __device__ __forceinline__ int32_t keys(const RaggedParams &p, int32_t q) const {
+    const int32_t last = first + min((q + 1) * p.tokens, n) - 1;
+    return last < 0 ? 0 : p.causal ? last + 1 : len;
+  }
+  __device__ __forceinline__ int32_t units(const RaggedParams &p, int32_t q) const {
+    return max(1, (keys(p, q) + kTile - 1) / kTile);
+  }
+  // Steps of tiles 0 .. q - 1 of rows.
+  __device__ __forceinline__ int64_t steps(const RaggedParams &p, int32_t q) const {
+    const int32_t whole = min(q, tiles - 1);  // tiles with all their tokens
+    int64_t s = static_cast<int64_t>(q) * kItemCost;
+    if (whole > 0) {
+      const int32_t idle = first < 0 ? min(whole, -first / p.tokens) : 0;
+      s += idle;
+      if (p.causal) {
+        const int64_t b = first + static_cast<int64_t>(idle + 1) * p.tokens - 1;
+        s += whole - idle;
+        if (whole > idle) s += floor_sum(whole - idle, kTile, p.tokens, b);
+      } else {
+        s += static_cast<int64_t>(whole - idle) * ((len + kTile - 1) / kTile);
+      }
+    }
+    if (q > whole) s += units(p, tiles - 1);
+    return s;
+  }
+};
+
+// Every share's piece of the line: `each` steps, and one more for the first `more`.
+struct Line {
+  int64_t each, more;
+  int32_t mode, shares;
+  __device__ __forceinline__ int64_t begin(int64_t share) const {
+    return share * each + min(share, more);
+  }
+  __device__ __forceinline__ int64_t share_of(int64_t step) const {
+    const int64_t border = more * (each + 1);
+    return step < border ? step / (each + 1) : more + (step - border) / each;
+  }
+};
+
+struct ShareState {
+  unsigned long long total, items, sums[32];
+  unsigned long long left;  // steps (whole items: items) of the sequence before the share
+  int32_t longest, b;       // b: the sequence that it begins in, B for none
+};
+
+// How a line of `total` steps in `items` items, the longest of `longest` steps, is shared.
+__device__ __forceinline__ Line cut_line(int32_t shares, int64_t total, int64_t items,
+                                         int32_t longest) {
+  Line line;
+  line.shares = static_cast<int32_t>(min(static_cast<int64_t>(shares), max(total, int64_t{1})));
+  line.each = total / line.shares;
+  line.more = total - line.each * line.shares;
+  // Whole items, one a share, where the longest is not kJoinSteps longer than equal pieces; where
+  // there are more of them than shares, equal pieces with the items that begin in each, at most
+  // one longer than equal.
+  const int64_t equal = (total + line.shares - 1) / line.shares;
+  line.mode = items <= shares ? (longest <= equal + kJoinSteps ? kWhole : kCut)
+                              : (longest <= kJoinSteps ? kUncut : kCut);
+  return line;
+}
+
+// Finds the sequence that share `index` begins in (all kThreads threads; ends with a barrier).
+template <int kThreads>
+__device__ __forceinline__ Line find_share(const RaggedParams &p, int32_t index, ShareState *st) {
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  if (tid == 0) {
+    st->total = st->items = 0;
+    st->longest = 0;
+    st->b = p.B;
+  }
+  __syncthreads();
+  const auto steps_of = [&](const Seq &s) {
+    return s.n > 0 ? s.steps(p, s.tiles) * p.kv_heads : int64_t{0};
+  };
+  int64_t total = 0, items = 0, mine = 0, mine_items = 0;
+  int32_t longest = 0;
+  for (int32_t b = tid; b < p.B; b += kThreads) {
+    const Seq s(p, b);
+    const int64_t t = steps_of(s);
+    const int64_t n = static_cast<int64_t>(s.tiles) * p.kv_heads;
+    if (b == tid) {
+      mine = t;
+      mine_items = n;
+    }
+    total += t;
+    items += n;
+    if (s.n > 0) longest = max(longest, kItemCost + s.units(p, s.tiles - 1));
+    if (s.bad_rows && index == 0) report_bad_page(p.status);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    items += __shfl_xor_sync(0xffffffffu, items, o);
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 0 && total > 0) {
+    atomicAdd(&st->total, static_cast<unsigned long long>(total));
+    atomicAdd(&st->items, static_cast<unsigned long long>(items));
+    atomicMax(&st->longest, longest);
+  }
+  __syncthreads();
+  const Line line = cut_line(p.shares, st->total, st->items, st->longest);
+  const int64_t target = line.mode == kWhole ? index : line.begin(index);
+  const int64_t all = line.mode == kWhole ? st->items : st->total;
+  if (index < line.shares && target < all) {  // uniform
+    int64_t base = 0;
+    for (int32_t b0 = 0; b0 < p.B && base <= target; b0 += kThreads) {
+      int64_t x = 0;
+      if (b0 == 0) {
+        x = line.mode == kWhole ? mine_items : mine;
+      } else if (b0 + tid < p.B) {
+        const Seq s(p, b0 + tid);
+        x = line.mode == kWhole ? static_cast<int64_t>(s.tiles) * p.kv_heads : steps_of(s);
+      }
+      int64_t incl = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) st->sums[warp] = incl;
+      __syncthreads();
+      int64_t before = base, chunk = 0;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        const int64_t y = st->sums[w];
+        chunk += y;
+        if (w < warp) before += y;
+      }
+      before += incl - x;
+      if (before <= target && target < before + x) {
+        st->b = b0 + tid;
+        st->left = target - before;
+      }
+      base += chunk;
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+  return line;
+}
+
+// A share's walk along its items (one warp, uniform).
+struct Walk {
+  Seq s;
+  int32_t b, hk, q, units;
+  int32_t tile;   // the next key tile of the item
+  int64_t end;    // the share's end, in tiles of the item
+  bool cut;
+  __device__ __forceinline__ Walk(const RaggedParams &p, const Line &line, int32_t index,
+                                  const ShareState &st)
+      : b(st.b), hk(0), q(0), units(1), tile(0), end(-kItemCost), cut(line.mode == kCut) {
+    if (b >= p.B) return;
+    s = Seq(p, b);
+    const int64_t left = st.left;
+    if (line.mode == kWhole) {
+      hk = static_cast<int32_t>(left / s.tiles);
+      q = static_cast<int32_t>(left - static_cast<int64_t>(hk) * s.tiles);
+      units = s.units(p, q);
+      end = units;
+      return;
+    }
+    const int64_t head = s.steps(p, s.tiles);
+    hk = static_cast<int32_t>(left / head);
+    const int64_t rest = left - hk * head;
+    // The last tile of rows whose steps begin at or before `rest`, 32 candidates at a time.
+    int32_t lo = 0, hi = s.tiles;
+    while (hi - lo > 1) {
+      const int32_t step = (hi - lo + 31) / 32;
+      const int64_t x = lo + static_cast<int64_t>(threadIdx.x % 32) * step;
+      const bool before = x < hi && s.steps(p, static_cast<int32_t>(x)) <= rest;
+      const int top = 31 - __clz(__ballot_sync(0xffffffffu, before));
+      lo += top * step;
+      hi = min(hi, lo + step);
+    }
+    q = lo;
+    units = s.units(p, q);
+    const int64_t off = rest - s.steps(p, q);  // of the share's begin in the item
+    tile = static_cast<int32_t>(max(int64_t{0}, off - kItemCost));
+    end = off + line.each + (index < line.more ? 1 : 0) - kItemCost;
+    if (!cut) {
+      if (off > 0)
+        next(p);
+      else
+        take_whole();
+    }
+  }
+  __device__ __forceinline__ bool more(const RaggedParams &p) const { return b < p.B && tile < end; }
+  // Uncut: the items that begin in the share are all its own.
+  __device__ __forceinline__ void take_whole() {
+    if (!cut && end > -kItemCost) end = max(end, static_cast<int64_t>(units));
+  }
+  __device__ __forceinline__ void next(const RaggedParams &p) {
+    end -= units + kItemCost;
+    tile = 0;
+    if (++q == s.tiles) {
+      q = 0;
+      if (++hk == p.kv_heads) {
+        hk = 0;
+        // (In cut lines an item whose first tile is past the end has no part here.)
+        do {
+          if (++b == p.B || end <= (cut ? 0 : -kItemCost)) return;
+          s = Seq(p, b);
+        } while (s.n == 0);
+      }
+    }
+    units = s.units(p, q);
+    take_whole();
+  }
+};
+
+// Where a key warp or a value warp is in its ring.
+template <int kSlots>
+struct Ring {
+  uint32_t n = 0;  // uses so far
+  __device__ __forceinline__ int slot() const { return n % kSlots; }
+  __device__ __forceinline__ bool wait_empty(uint64_t *empty, volatile int *abort) const {
+    return n < kSlots ||
+           mbar_wait_warp(&empty[slot()], ((n - kSlots) / kSlots) & 1, abort, kWaitNs);
+  }
+  __device__ __forceinline__ void drain(uint64_t *full) const {  // of the copies still in flight
+    for (uint32_t c = n > kSlots ? n - kSlots : 0; c < n; ++c)
+      drain_wait(&full[c % kSlots], (c / kSlots) & 1);
+  }
+};
+
+// The key of a tile from which on some row of the segment does not see it, or there is none.
+__device__ __forceinline__ int32_t seen_by_all(const RaggedParams &p, const Segment &g) {
+  return p.causal ? min(max(g.first, 0), g.len - 1) : g.len - 1;
+}
+
+// Values that not all rows see must not reach the others through a zero weight (0 * inf is not
+// zero): of the tile's keys past `seen` those behind the sequence's end become zero, and values of
+// the others that are not finite as well, in shared memory; a column's first such key (its distance
+// from `seen`, at most 254) is kept in `first`, two columns a word, eight of each block of 64 a
+// lane, by the four lanes that agree in lane % 8: rows at least that far from `seen` see it.  One
+// warp.
+template <int kBlocks>
+__device__ __forceinline__ void fix_values(uint8_t *tile, int32_t key0, int32_t seen, int32_t len,
+                                           uint32_t (&first)[kBlocks][4]) {
+  const int lane = threadIdx.x % 32;
+  const int chunk = lane & 7, half = lane >> 3;  // four rows at a time
+#pragma unroll 1
+  for (int row = max(0, seen + 1 - key0) / 4 * 4 + half; row < kTile; row += 4) {
+    const int32_t key = key0 + row;
+    if (key <= seen) continue;
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k) {
+      uint4 *at = reinterpret_cast<uint4 *>(tile + k * (kTile * 128) + row * 128 +
+                                            ((chunk ^ (row & 7)) << 4));
+      if (key >= len) {
+        *at = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      uint4 x = *at;
+      uint32_t *w = reinterpret_cast<uint32_t *>(&x);
+      bool any = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool lo = (w[i] & 0x7F80u) == 0x7F80u, hi = (w[i] & 0x7F800000u) == 0x7F800000u;
+        if (lo || hi) {
+          const uint32_t d = min(254, key - seen);
+          uint32_t f = first[k][i];
+          if (lo) f = (f & 0xFFFF0000u) | min(f & 0xFFFFu, d);
+          if (hi) f = (f & 0xFFFFu) | (min(f >> 16, d) << 16);
+          first[k][i] = f;
+          w[i] &= (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0xFFFFu : 0xFFFFFFFFu);
+          any = true;
+        }
+      }
+      if (any) *at = x;
+    }
+  }
+}
+
+// The four lanes' results as one byte a column (255: none); whether there is any.
+template <int kBlocks>
+__device__ __forceinline__ bool store_first(uint32_t (&first)[kBlocks][4], uint8_t *columns) {
+  const int lane = threadIdx.x % 32;
+  bool any = false;
+#pragma unroll
+  for (int k = 0; k < kBlocks; ++k) {
+    uint32_t out[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t f = first[k][i];
+#pragma unroll
+      for (int o = 8; o <= 16; o *= 2) {
+        const uint32_t g = __shfl_xor_sync(0xffffffffu, f, o);
+        f = min(f & 0xFFFFu, g & 0xFFFFu) | (min(f >> 16, g >> 16) << 16);
+      }
+      any |= f != 0xFFFFFFFFu;
+      out[i / 2] |= ((f & 0xFFu) | ((f >> 8) & 0xFF00u)) << (16 * (i % 2));
+    }
+    if (lane < 8) *reinterpret_cast<uint2 *>(columns + 64 * k + 8 * lane) = make_uint2(out[0], out[1]);
+  }
+  return __any_sync(0xffffffffu, any);
+}
+
+// The load warps, one for the keys (with the walk along the share and the segments' descriptions)
+// and one for the values.  A tile in pages of 16 rows is 16 copies for each of them, a lane each.
+// Copies of a tile land in kBoxes boxes of kTile rows; box k of piece i at k * box bytes + its rows.
+
+// This lane's page of tile t of sequence b: lane = piece * kBoxes + box.
+__device__ __forceinline__ int32_t page_of(const RaggedParams &p, int32_t b, int32_t len, int32_t key,
+                                           bool piece_ok) {
+  return piece_ok && key < len
+             ? p.page_table[static_cast<int64_t>(b) * p.max_pages + p.by_page.div(key)]
+             : 0;
+}
+
+}  // namespace
+}  // namespace diffattn

@@ -170,7 +170,9 @@ def bind(lib):
                                         ctypes.POINTER(ctypes.c_float)]),
             ("diffrotary_apply", [dp, tp, i32, vp, vp, vp, sp, vp, i64, i64, i32, vp]),
             ("diffragged_step", [bp, vp, i64, vp, vp, vp, vp, vp]),
-            ("diffragged_append", [dp, cp, vp, vp, vp, vp, vp, vp, vp, sp, vp, tp, vp, vp])):
+            ("diffragged_append", [dp, cp, vp, vp, vp, vp, vp, vp, vp, sp, vp, tp, vp, vp]),
+            ("diffragged_fwd", [dp, cp, vp, vp, vp, fp, fp, vp, sp, vp, ctypes.c_size_t, vp]),
+            ("diffragged_fwd_plan", [dp, cp, szp])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = ctypes.c_int, args
     lib.diffattn_selftest_wait.restype = ctypes.c_int
@@ -1197,6 +1199,89 @@ def ragged_append(cache, k1, k2, v, slots, *, rotary=None, positions=None, q=Non
         return st
     _check(st)
     return q_out
+
+
+def ragged_fwd_plan(cache, H: int, T: int, *, raw_status: bool = False):
+    """`diffragged_fwd_plan`: workspace bytes of ragged_fwd with H query heads and T packed rows."""
+    desc = make_desc(cache.B, H, T, cache.d, cache.code, True, 1, 1e-5, 0.0)
+    n = ctypes.c_size_t(0)
+    st = load().diffragged_fwd_plan(ctypes.byref(desc), cache._ref, ctypes.byref(n))
+    if raw_status:
+        return st, n.value
+    _check(st)
+    return n.value
+
+
+def _new_ragged_fwd(cache, key, status):
+    shape, strides, causal, headnorm, eps, lambda_init = key
+    if len(shape) != 3 or shape[2] != cache.d:
+        raise ValueError(f"q1 and q2 must be [T, H, {cache.d}]")
+    if any(s[2] != 1 for s in strides):
+        raise ValueError("rows must be contiguous (last stride 1)")
+    T, H, d = shape
+    ref = ctypes.byref(make_desc(cache.B, H, T, d, cache.code, causal, headnorm, eps, lambda_init,
+                                 status))
+    need = ctypes.c_size_t(0)
+    st = load().diffragged_fwd_plan(ref, cache._ref, ctypes.byref(need))
+    if st != OK:
+        return st, None
+    out_shape = (T, H, 2 * d)
+    st3 = [_strides_of((1, *n), (1, *s)) for n, s in zip((shape, shape, out_shape), strides)]
+    arr = (Strides * 3)(*(Strides(0, s.n, s.h) for s in st3))
+    return OK, cache._keep(key, status, (ref, out_shape, H, need.value, arr))
+
+
+def ragged_fwd(cache, q1, q2, lam, q_start, *, causal: bool = True, headnorm: int = 1, norm_w=None,
+               eps: float = 1e-5, lambda_init: float = 0.0, workspace=None, out=None, status=None,
+               stream=None, raw_status: bool = False):
+    """`diffragged_fwd`: all new tokens of a packed batch against the paged cache, any number of
+    them a sequence.
+
+    q1, q2: [T, H, d] of the cache's key dtype, H a multiple of its kv_heads; sequence b's tokens
+    are rows q_start[b] .. q_start[b + 1] - 1 (int32 [B + 1]) and its newest kv_len[b] - n + i.
+    lam: float32 [H]; norm_w: float32 [H, 2d] (16-byte aligned) or None.  Views of any layout with
+    contiguous rows (`out` too).  workspace: a CUDA tensor of at least ragged_fwd_plan bytes (a
+    torch buffer when None).  Returns bf16 out [T, H, 2d]; rows of no sequence are not written.
+    """
+    index, dtype, f32 = cache.index, cache.dtype, torch.float32
+    shape = q1.shape
+    if q2.shape != shape:
+        raise ValueError(f"q2 must be {tuple(shape)}, as q1")
+    if out is None:
+        if len(shape) != 3:
+            raise ValueError(f"q1 and q2 must be [T, H, {cache.d}]")
+        out = _new_on(stream, (shape[0], shape[1], 2 * shape[2]), torch.bfloat16, cache.device)
+    key = (shape, (q1.stride(), q2.stride(), out.stride()), bool(causal), int(headnorm), float(eps),
+           float(lambda_init))
+    call = cache._calls.get(key) if status is None else None
+    if call is None:
+        st, call = _new_ragged_fwd(cache, key, status)
+        if st != OK:
+            if raw_status:
+                return st
+            _check(st)
+    ref, out_shape, H, need, strides = call
+    if q1.dtype != dtype or q2.dtype != dtype:
+        raise ValueError(f"q1 and q2 must be {dtype}, as the cache's keys")
+    if q1.get_device() != index or q2.get_device() != index or lam.get_device() != index:
+        raise ValueError("all tensors must be on the cache's device")
+    if lam.dtype != f32 or lam.numel() != H or not lam.is_contiguous():
+        raise ValueError("lam must be contiguous float32 [H]")
+    if norm_w is not None and (norm_w.dtype != f32 or norm_w.numel() != H * out_shape[2] or
+                               not norm_w.is_contiguous() or norm_w.get_device() != index):
+        raise ValueError("norm_w must be contiguous float32 [H, 2d] on the cache's device")
+    if out.shape != out_shape or out.dtype != torch.bfloat16 or out.get_device() != index:
+        raise ValueError("out must be bfloat16 [T, H, 2d] on the cache's device")
+    start = _whole("q_start", q_start, torch.int32, cache.B + 1, index)
+    handle = _stream_on(cache, stream)
+    ws, ws_bytes, _hold = _workspace(workspace, need, cache, stream)
+    st = (_lib or load()).diffragged_fwd(
+        ref, cache._ref, start, q1.data_ptr(), q2.data_ptr(), lam.data_ptr(),
+        None if norm_w is None else norm_w.data_ptr(), out.data_ptr(), strides, ws, ws_bytes, handle)
+    if raw_status:
+        return st
+    _check(st)
+    return out
 
 
 def headnorm(x, *, H: int, norm_w=None, eps: float = 1e-5, lambda_init: float = 0.0,

@@ -12,8 +12,9 @@
  *
  * A step: diffragged_step grows the sequences, gives them pages and works out
  * where each token goes; per layer, diffragged_append turns the queries and
- * keys and writes the cache's rows.  All sizes but the tensors' capacities are
- * read on the device, so a captured step replays with new ones.
+ * keys and writes the cache's rows, and diffragged_fwd attends.  All sizes but
+ * the tensors' capacities are read on the device, so a captured step replays
+ * with new ones.
  */
 #ifndef DIFFATTN_RAGGED_H
 #define DIFFATTN_RAGGED_H
@@ -91,6 +92,37 @@ diffattn_status diffragged_append(const diffattn_desc *desc, const diffpaged_cac
                                   const diffattn_strides *strides, const int64_t *slots,
                                   const diffrotary_table *table, const int32_t *positions,
                                   void *stream);
+
+/*
+ * diffragged_fwd — the differential head's forward of all new tokens against
+ * their sequences' pages: any numbers of them, from none and one to a whole
+ * prompt.
+ *
+ * q1, q2: device [N, H, d], bf16 or (DIFFATTN_E4M3_QK) e4m3; out: bf16 [N, H, 2d];
+ * strides[0..2] those of q1, q2, out (as above) or NULL; lambda fp32 [H], norm_w
+ * fp32 [H, 2d], 16-byte aligned, or NULL.  The formula, norms,
+ * heads, causal (token i sees the keys up to its own position; 0: all kv_len[b])
+ * and what masked and unused places hold are as in diffpaged_fwd: a row that
+ * sees no key is zero, a value that is not finite reaches those rows only that
+ * see it, and makes its column (with a head norm the row) of them NaN.
+ * A page number outside the pool, a length outside the table or rows outside
+ * 0 .. N store DIFFATTN_ERR_PAGE: rows that would have read such a page are NaN
+ * (others of the sequence may be), so are all of a bad length, and those of a
+ * sequence whose q_start is wrong are not written.
+ *
+ * workspace: as for diffpaged_fwd; its size does not depend on the lengths.
+ * desc: B sequences, N rows, H, d (64 or 128), dtype, causal, headnorm, eps,
+ * lambda_init.  Domain: H / kv_heads <= 64, page_size a multiple of 16.
+ */
+diffattn_status diffragged_fwd(const diffattn_desc *desc, const diffpaged_cache *cache,
+                               const int32_t *q_start, const void *q1, const void *q2,
+                               const float *lambda, const float *norm_w, void *out,
+                               const diffattn_strides *strides, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of diffragged_fwd (host-only apart from the SM count). */
+diffattn_status diffragged_fwd_plan(const diffattn_desc *desc, const diffpaged_cache *cache,
+                                    size_t *workspace_bytes);
 
 #ifdef __cplusplus
 }

@@ -93,7 +93,9 @@ def attend(c, q_start, q1, q2, lam, *, causal=True, headnorm=1, norm_w=None, eps
     """(out [T, H, 2d], tolerance) in float64; rows of no sequence are left at zero.
 
     The tolerance is paged_ref.attend's with probabilities in the second product as one bf16
-    number (2^-9 relative: half a step of bf16's 2^-8, the sums being of the unrounded ones).
+    number (bf16 has 8 significant bits, so a step is 2^-7 of the binade's least value and half of
+    one at most 2^-8 of a value, torch.finfo(torch.bfloat16).eps / 2; the sums are of the
+    unrounded ones).
     """
     T, H, d = q1.shape
     G = H // c.kv
@@ -124,7 +126,7 @@ def attend(c, q_start, q1, q2, lam, *, causal=True, headnorm=1, norm_w=None, eps
             o = w @ vs
             both = maps[0] + abs(lh) * maps[1]
             rel = 2 * (math.log(2) * dx + 2.0 ** -22) + 2 * (n / 16 + 8) * 2.0 ** -23
-            a = (both @ vs.abs()) * (rel[:, None] + 2.0 ** -9 + 2.0 ** -17)
+            a = (both @ vs.abs()) * (rel[:, None] + 2.0 ** -8 + 2.0 ** -16)
             bad = (see[:, :, None] & ~torch.isfinite(v)[None]).any(1) if not \
                 torch.isfinite(v).all() else torch.zeros_like(o, dtype=torch.bool)
             o = torch.where(bad, math.nan, o)

@@ -9,6 +9,7 @@ from tests import paged_ref as R
 from tests import ragged_ref as G
 
 pytestmark = pytest.mark.gpu
+INF = float("inf")
 BF16, E4M3 = torch.bfloat16, torch.float8_e4m3fn
 BOOK = ("kv_len", "held", "page_table", "free_pages", "free_count")
 
@@ -250,3 +251,248 @@ def test_append_refusals():
         call(k1, k2, v, slots, q=[x[:, :3].contiguous() for x in q])  # 3 heads over 2
     with pytest.raises(ops.DiffAttnError):
         call(k1, k2, v, slots, q=q, q_out=[q[0], q[0].transpose(0, 0).as_strided((3, 4, 64), (256, 63, 1))])
+
+
+# ---- attention --------------------------------------------------------------------------------
+
+LI = 0.5
+
+
+def _queries(seed, T, H, d, dtype, scale=1.5):
+    g = torch.Generator().manual_seed(seed)
+    q = [(torch.randn(T, H, d, generator=g) * scale).to(dtype).cuda() for _ in range(2)]
+    lam = (torch.rand(H, generator=g) * 0.8 + 0.1).cuda()
+    w = (1.0 + 0.1 * torch.randn(H, 2 * d, generator=g)).cuda()
+    return q[0], q[1], lam, w
+
+
+def _starts(new, before=0):
+    at = [before]
+    for n in new:
+        at.append(at[-1] + n)
+    return at
+
+
+def _parity(c, H, new, seed=3, before=0, behind=0, causal=True, headnorm=1, scale=1.5, q=None, **kw):
+    starts = _starts(new, before)
+    T = starts[-1] + behind
+    q1, q2, lam, w = _queries(seed, T, H, c.d, c.dtype, scale) if q is None else q
+    out = torch.full((T, H, 2 * c.d), 7.0, dtype=BF16, device="cuda")
+    word = _int([0])
+    got = ops.ragged_fwd(c.ops_cache(), q1, q2, lam, _int(starts), norm_w=w, lambda_init=LI,
+                         causal=causal, headnorm=headnorm, out=out, status=word, **kw)
+    torch.cuda.synchronize()
+    assert int(word) == 0 and got is out
+    ref, tol = G.attend(c, starts, q1, q2, lam, causal=causal, headnorm=headnorm, norm_w=w,
+                        lambda_init=LI)
+    R.check(out[starts[0]: starts[-1]], ref[starts[0]: starts[-1]], tol[starts[0]: starts[-1]], "out")
+    assert torch.all(out[: starts[0]] == 7.0) and torch.all(out[starts[-1]:] == 7.0)
+    return out
+
+
+KINDS = [(64, BF16), (64, E4M3)]
+
+
+@pytest.mark.parametrize("d,dtype", KINDS)
+@pytest.mark.parametrize("H,kv", [(2, 2), (4, 1), (6, 2), (7, 1), (64, 1)])
+def test_short_ragged_batch(d, dtype, H, kv):
+    """Whole items; groups that do not divide 128; rows outside the batch."""
+    lens, new = [1, 0, 16, 17, 63, 64, 65, 128, 200, 5], [1, 0, 3, 17, 1, 64, 40, 1, 130, 2]
+    c = R.Cache(11, lens=lens, kv=kv, d=d, page=16, dtype=dtype)
+    _parity(c, H, new, before=2, behind=3)
+
+
+@pytest.mark.parametrize("d,dtype", KINDS)
+@pytest.mark.parametrize("page,layout", [(16, "token"), (48, "head"), (64, "head"), (128, "token"),
+                                         (256, "head")])
+def test_long_ragged_batch(d, dtype, page, layout):
+    """Items cut by borders between shares and joined."""
+    c = R.Cache(12, lens=[1500, 1, 3, 700, 65, 2049], kv=2, d=d, page=page, dtype=dtype,
+                layout=layout)
+    _parity(c, 4, [900, 1, 0, 1, 60, 130])
+
+
+@pytest.mark.parametrize("d", [64])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("headnorm", [0, 1, 2])
+def test_norms_and_masks(d, causal, headnorm):
+    c = R.Cache(13, lens=[3, 400, 0, 61, 1, 66, 2100], kv=2, d=d, page=16)
+    _parity(c, 4, [3, 200, 0, 1, 1, 66, 300], causal=causal, headnorm=headnorm)
+
+
+@pytest.mark.parametrize("d", [64])
+@pytest.mark.parametrize("causal", [True, False])
+def test_padding_positions(d, causal):
+    """More tokens than the sequence is long: rows that see no key are zero, whole tiles of them
+    too."""
+    c = R.Cache(14, lens=[2, 0, 40, 130], kv=1, d=d, page=16)
+    out = _parity(c, 1, [5, 300, 200, 131], causal=causal)
+    assert torch.all(out[:3] == 0) and torch.all(out[5:305] == 0)
+
+
+@pytest.mark.parametrize("d", [64])
+@pytest.mark.parametrize("kv,H,n,new", [(1, 1, 20001, 1), (1, 8, 12000, 33), (2, 2, 9000, 300),
+                                        (8, 8, 3000, 3000)])
+def test_one_sequence(d, kv, H, n, new):
+    c = R.Cache(15, lens=[n], kv=kv, d=d, page=64)
+    _parity(c, H, [new])
+
+
+def test_many_sequences():
+    """More sequences than threads that look for a share, most of them idle or single tokens."""
+    rng = random.Random(2)
+    lens = [rng.choice([0, 1, 20, 33]) for _ in range(1500)]
+    new = [min(n, rng.choice([0, 1, 1, 5])) for n in lens]
+    c = R.Cache(16, lens=lens, kv=1, d=64, page=16)
+    _parity(c, 1, new)
+
+
+@pytest.mark.parametrize("d", [64])
+def test_large_and_climbing_logits(d):
+    c = R.Cache(17, lens=[1900, 130], kv=2, d=d, page=16, fill=0.0)
+    for t in ("k1", "k2"):
+        for b, n in enumerate(c.lens):
+            pages = c.table[b].long()[torch.arange(n, device="cuda") // 16]
+            x = getattr(c, t)
+            ramp = torch.linspace(0.1, 6.0, n, device="cuda")[:, None, None]
+            x[pages, :, torch.arange(n, device="cuda") % 16] = (
+                x[pages, :, torch.arange(n, device="cuda") % 16].float() * ramp).to(BF16)
+    _parity(c, 4, [700, 130], scale=4.0)
+
+
+@pytest.mark.parametrize("d", [64])
+@pytest.mark.parametrize("headnorm", [0, 1])
+@pytest.mark.parametrize("n", [130, 2500])
+def test_values_that_are_not_finite_reach_only_rows_that_see_them(d, headnorm, n):
+    """Also through the join, and whatever lies behind the sequences (R.Cache fills NaN)."""
+    c = R.Cache(18, lens=[n, 40], kv=2, d=d, page=16)
+    new = min(n, 600)
+    for k, (back, col, x) in enumerate([(1, 0, INF), (new // 2, 5, float("nan")),
+                                        (new - 2, 2 * d - 1, -INF), (17, 64, float("nan"))]):
+        t = n - back
+        c.v[int(c.table[0, t // 16]), k % 2, t % 16, col] = x
+    _parity(c, 4, [new, 40], headnorm=headnorm)
+
+
+@pytest.mark.parametrize("d", [64])
+def test_keys_and_queries_that_are_not_finite(d):
+    """A NaN in a masked key has no influence; a NaN query row is its own row's."""
+    c = R.Cache(19, lens=[300], kv=1, d=d, page=16)
+    t = 290
+    c.k1[int(c.table[0, t // 16]), 0, t % 16, 3] = float("nan")
+    q = _queries(5, 40, 2, d, BF16)
+    q[0][7, 1, 0] = float("nan")
+    out = _parity(c, 2, [40], q=q)
+    bad = torch.isnan(out.float()).any(-1)
+    assert bad[30:].all() and bad[7, 1] and int(bad[:30].sum()) == 1
+
+
+@pytest.mark.parametrize("d", [64])
+def test_strided_queries_and_output(d):
+    c = R.Cache(20, lens=[500, 90], kv=2, d=d, page=32)  # NaN behind the sequences
+    starts = [0, 70, 90]
+    q1, q2, lam, w = _queries(6, 90, 4, d, BF16)
+    want = ops.ragged_fwd(c.ops_cache(), q1, q2, lam, _int(starts), norm_w=w, lambda_init=LI)
+    wide = torch.zeros(90, 4, 3 * d, dtype=BF16, device="cuda")
+    wide[:, :, d: 2 * d] = q1
+    heads_first = q2.transpose(0, 1).contiguous().transpose(0, 1)
+    out = torch.zeros(4, 90, 2 * d, dtype=BF16, device="cuda").transpose(0, 1)
+    ops.ragged_fwd(c.ops_cache(), wide[:, :, d: 2 * d], heads_first, lam, _int(starts), norm_w=w,
+                   lambda_init=LI, out=out)
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("d", [64])
+def test_bad_pages_lengths_and_rows(d):
+    """Reported, and nothing outside the pool or the batch is touched."""
+    c = R.Cache(21, lens=[200, 300, 100, 50, 2000], kv=2, d=d, page=16, fill=0.0)
+    new = [30, 40, 10, 5, 200]
+    starts = _starts(new)
+    q1, q2, lam, w = _queries(7, starts[-1] + 2, 4, d, BF16)
+    good, tol = G.attend(c, starts, q1, q2, lam, norm_w=w, lambda_init=LI)
+    for what, seq in (("page", 0), ("page", 4), ("length", 1), ("rows", 2)):
+        table, kv_len, q_start = c.table.clone(), c.kv_len.clone(), _int(starts)
+        if what == "page":
+            table[seq, 1] = c.k1.shape[0] if seq else -5
+        elif what == "length":
+            kv_len[seq] = c.max_pages * 16 + 1
+        else:
+            q_start[3] = starts[-1] + 3  # sequence 2 ends behind the rows, sequence 3 falls
+        cache = ops.PagedCache(c.k1, c.k2, c.v, table, kv_len)
+        word, out = _int([0]), torch.full(good.shape, 7.0, dtype=BF16, device="cuda")
+        ops.ragged_fwd(cache, q1, q2, lam, q_start, norm_w=w, lambda_init=LI, status=word, out=out)
+        torch.cuda.synchronize()
+        assert int(word) == ops.ERR_PAGE, what
+        for b in range(5):
+            mine = slice(starts[b], starts[b + 1])
+            if what == "rows" and b in (2, 3):
+                assert torch.all(out[mine] == 7.0)
+            elif b == seq:
+                assert torch.isnan(out[mine].float()).all(), (what, b)
+            else:
+                R.check(out[mine], good[mine], tol[mine], f"{what} {b}")
+        assert torch.all(out[starts[-1]:] == 7.0)
+
+
+@pytest.mark.parametrize("d", [64])
+def test_repeated_runs_graphs_and_stale_workspaces(d):
+    c = R.Cache(22, lens=[3000, 700, 1], kv=2, d=d, page=16)
+    q1, q2, lam, w = _queries(8, 400, 4, d, BF16)
+    cache = c.ops_cache()
+    q_start = _int([0, 390, 398, 399])
+    kw = dict(norm_w=w, lambda_init=LI)
+    need = ops.ragged_fwd_plan(cache, 4, 400)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")  # NaN bits
+    out = torch.zeros(400, 4, 2 * d, dtype=BF16, device="cuda")
+    want = ops.ragged_fwd(cache, q1, q2, lam, q_start, workspace=ws, out=out, **kw).clone()
+    for _ in range(3):
+        assert torch.equal(ops.ragged_fwd(cache, q1, q2, lam, q_start, workspace=ws, out=out, **kw),
+                           want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ops.ragged_fwd(cache, q1, q2, lam, q_start, workspace=ws, out=out, **kw)
+    for x in (c.k1, c.k2, c.v):  # finite places behind the sequences, to compare whole tensors
+        x.nan_to_num_(nan=0.0)
+    for lens, starts in (([3000, 700, 1], [0, 390, 398, 399]), ([128, 700, 1], [0, 3, 399, 400]),
+                         ([2999, 0, 0], [0, 1, 1, 1]), ([3000, 600, 1], [5, 5, 400, 400])):
+        cache.kv_len.copy_(_int(lens))
+        q_start.copy_(_int(starts))
+        out.zero_()
+        graph.replay()
+        fresh = torch.zeros_like(out)
+        ops.ragged_fwd(cache, q1, q2, lam, q_start, out=fresh, **kw)
+        assert torch.equal(out, fresh)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = ops.ragged_fwd(cache, q1, q2, lam, q_start, stream=side, **kw)
+    side.synchronize()
+    assert torch.equal(got[5:], out[5:])
+
+
+def test_fwd_refusals():
+    c = R.Cache(23, lens=[400], kv=2, d=64, page=16, fill=0.0)
+    cache = c.ops_cache()
+    q1, q2, lam, w = _queries(9, 6, 4, 64, BF16)
+    qs = _int([0, 6])
+    call = lambda *a, **k: ops.ragged_fwd(cache, *a, **k)
+    for a, k in (((q1, q2[:5], lam, qs), {}), ((q1.float(), q2.float(), lam, qs), {}),
+                 ((q1, q2, lam[:3], qs), {}), ((q1, q2, lam, qs.long()), {}),
+                 ((q1, q2, lam, _int([0, 3, 6])), {}), ((q1, q2, lam, qs), dict(norm_w=w[:, :64])),
+                 ((q1, q2, lam, qs), dict(out=torch.zeros(6, 4, 64, dtype=BF16, device="cuda"))),
+                 ((q1[:, :, :32], q2[:, :, :32], lam, qs), {}), ((q1[0], q2[0], lam, qs), {}),
+                 ((q1, q2, lam.cpu(), qs), {}),
+                 ((q1.transpose(1, 2).contiguous().transpose(1, 2), q2, lam, qs), {})):
+        with pytest.raises(ValueError):
+            call(*a, **k)
+    with pytest.raises(ops.DiffAttnError):
+        call(q1[:, :3].contiguous(), q2[:, :3].contiguous(), lam[:3].contiguous(), qs)
+    with pytest.raises(ops.DiffAttnError):
+        call(q1, q2, lam, qs, norm_w=torch.ones(4 * 128 + 1, device="cuda")[1:].view(4, 128))
+    big = R.Cache(23, lens=[4000], kv=2, d=64, page=16, fill=0.0).ops_cache()
+    need = ops.ragged_fwd_plan(big, 4, 6)
+    assert need > 0
+    with pytest.raises(ops.DiffAttnError):
+        ops.ragged_fwd(big, q1, q2, lam, qs,
+                       workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    out = ops.ragged_fwd(cache, q1[:0], q2[:0], lam, _int([0, 0]))
+    assert out.shape == (0, 4, 128)
