@@ -28,7 +28,7 @@ SOURCES = ["api.cu", "fwd_bf16_sm103.cu", "fwd_f32.cu", "headnorm.cu", "splitkv.
            "selftest.cu", "paged_api.cu", "paged_append.cu", "paged_fwd.cu",
            "paged_fwd_d64.cu", "paged_fwd_d128.cu", "paged_evict.cu", "rotary.cu",
            "ragged_api.cu", "ragged_step.cu", "ragged_append.cu", "ragged_fwd.cu",
-           "ragged_fwd_d64.cu"]
+           "ragged_fwd_d64.cu", "ragged_fwd_d128.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -23,7 +23,6 @@ diffattn_status plan_fwd(const diffattn_desc *desc, const diffpaged_cache *cache
                          RaggedFwdPlan *plan) {
   diffattn_status st = check_paged_cache(desc, cache, true);
   if (st != DIFFATTN_OK) return st;
-  if (desc->d != 64) return DIFFATTN_ERR_UNSUPPORTED;
   if (desc->H / cache->kv_heads > kRaggedMaxGroup || desc->N > (int64_t{1} << 30) ||
       desc->B >= (int64_t{1} << 24) || desc->H > 65535)
     return DIFFATTN_ERR_UNSUPPORTED;

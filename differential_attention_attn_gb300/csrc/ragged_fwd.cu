@@ -196,6 +196,7 @@ RaggedFwdPlan plan_ragged_fwd(const diffattn_desc &desc, const diffpaged_cache &
     q.part = take(size_t{2} * q.shares * 2 * part_floats(2 * desc.d) * sizeof(float));
     q.join = take(q.shares * sizeof(RaggedJoin));
   }
+  if (desc.d == 128) q.swap = take(ragged_swap_bytes(q.shares));
   q.bytes = at;
   return q;
 }
@@ -220,6 +221,7 @@ diffattn_status launch_ragged_fwd(const diffattn_desc &desc, const diffpaged_cac
     p.part = reinterpret_cast<float *>(ws + plan.part);
     p.joins = reinterpret_cast<RaggedJoin *>(ws + plan.join);
   }
+  if (d == 128) p.swap = reinterpret_cast<float *>(ws + plan.swap);
   p.out_n = strides[2].n;
   p.out_h = strides[2].h;
   p.B = static_cast<int32_t>(desc.B);
@@ -249,9 +251,11 @@ diffattn_status launch_ragged_fwd(const diffattn_desc &desc, const diffpaged_cac
       !encode_pool(&maps[3], cache.k2, d, cache, cache.k2_strides, fp8, p.piece_rows) ||
       !encode_pool(&maps[4], cache.v, 2 * d, cache, cache.v_strides, false, p.piece_rows))
     return DIFFATTN_ERR_CUDA;
-  diffattn_status st = launch_ragged_main_d64(p, maps, fp8, stream);
+  const diffattn_status st = d == 64 ? launch_ragged_main_d64(p, maps, fp8, stream)
+                                     : launch_ragged_main_d128(p, maps, fp8, stream);
   if (st != DIFFATTN_OK || !plan.joins) return st;
-  return launch_join<128>(p, stream) == cudaSuccess ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
+  const cudaError_t e = d == 64 ? launch_join<128>(p, stream) : launch_join<256>(p, stream);
+  return e == cudaSuccess ? DIFFATTN_OK : DIFFATTN_ERR_CUDA;
 }
 
 }  // namespace diffattn

@@ -62,6 +62,8 @@ diffattn_status launch_ragged_main_d64(const RaggedParams &p, const CUtensorMap 
 diffattn_status launch_ragged_main_d128(const RaggedParams &p, const CUtensorMap (&maps)[5],
                                         bool fp8, cudaStream_t stream);
 
+size_t ragged_swap_bytes(int shares);  // of d = 128
+
 using RaggedKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
                               const CUtensorMap, const CUtensorMap, const RaggedParams);
 // One launch of a main kernel, `cluster` CTAs a share, behind the kernel before (dependent launch).
@@ -359,6 +361,29 @@ struct Walk {
     }
   }
   __device__ __forceinline__ bool more(const RaggedParams &p) const { return b < p.B && tile < end; }
+  // The share's part of the item.
+  __device__ __forceinline__ Segment segment(const RaggedParams &p, int32_t share) const {
+    const int32_t t0 = q * p.tokens;
+    Segment g;
+    g.row = s.row + t0;
+    g.tokens = min(p.tokens, s.n - t0);
+    g.first = s.first + t0;
+    g.len = s.len;
+    g.b = b;
+    g.hk = hk;
+    g.tile0 = tile;
+    g.tiles = static_cast<int32_t>(min(static_cast<int64_t>(units), end)) - tile;
+    g.flags = (g.tiles == units ? kDirect : 0) | (s.keys(p, q) == 0 ? kEmpty : 0) |
+              (s.bad_len ? kBadLen : 0);
+    g.slot = 2 * share + (tile == 0 ? 1 : 0);
+    return g;
+  }
+  // Of a cut item that begins in the share.
+  __device__ __forceinline__ RaggedJoin join(const Line &line, int32_t share, const Segment &g) const {
+    const int64_t last = line.begin(share + 1) - end + units - 1;  // its last step on the line
+    return {static_cast<int32_t>(line.share_of(last)) - share + 1, g.slot, g.hk, g.row, g.tokens,
+            g.first, {0, 0}};
+  }
   // Uncut: the items that begin in the share are all its own.
   __device__ __forceinline__ void take_whole() {
     if (!cut && end > -kItemCost) end = max(end, static_cast<int64_t>(units));
@@ -446,14 +471,12 @@ __device__ __forceinline__ void fix_values(uint8_t *tile, int32_t key0, int32_t 
   }
 }
 
-// The four lanes' results as one byte a column (255: none); whether there is any.
+// The smallest over the four lanes that agree in lane % 8; whether any lane has one.
 template <int kBlocks>
-__device__ __forceinline__ bool store_first(uint32_t (&first)[kBlocks][4], uint8_t *columns) {
-  const int lane = threadIdx.x % 32;
+__device__ __forceinline__ bool merge_first(uint32_t (&first)[kBlocks][4]) {
   bool any = false;
 #pragma unroll
-  for (int k = 0; k < kBlocks; ++k) {
-    uint32_t out[2] = {0, 0};
+  for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t f = first[k][i];
@@ -462,12 +485,22 @@ __device__ __forceinline__ bool store_first(uint32_t (&first)[kBlocks][4], uint8
         const uint32_t g = __shfl_xor_sync(0xffffffffu, f, o);
         f = min(f & 0xFFFFu, g & 0xFFFFu) | (min(f >> 16, g >> 16) << 16);
       }
+      first[k][i] = f;
       any |= f != 0xFFFFFFFFu;
-      out[i / 2] |= ((f & 0xFFu) | ((f >> 8) & 0xFF00u)) << (16 * (i % 2));
     }
-    if (lane < 8) *reinterpret_cast<uint2 *>(columns + 64 * k + 8 * lane) = make_uint2(out[0], out[1]);
-  }
   return __any_sync(0xffffffffu, any);
+}
+// One byte a column, 255 for none.
+template <int kBlocks>
+__device__ __forceinline__ void store_first(const uint32_t (&first)[kBlocks][4], uint8_t *columns) {
+  const int lane = threadIdx.x % 32;
+  if (lane < 8)
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint16_t *>(columns + 64 * k + 8 * lane + 2 * i) =
+            static_cast<uint16_t>((first[k][i] & 0xFFu) | ((first[k][i] >> 8) & 0xFF00u));
 }
 
 // The load warps, one for the keys (with the walk along the share and the segments' descriptions)

@@ -50,7 +50,7 @@ struct Ctrl {
   int32_t unclean[kSegRing];  // `column` counts
   uint32_t tmem;
   int abort;
-  alignas(8) uint8_t column[kSegRing][DV];  // fix_values
+  alignas(8) uint8_t column[2][DV];  // fix_values, by segment
   float xch[2 * kTile];
 };
 static_assert(sizeof(ShareState) <= 2 * kTile * sizeof(float), "the set-up's state lies in xch");
@@ -150,25 +150,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n;
       };
       while (ok && w.more(p)) {
-        Segment g;
-        const int32_t t0 = w.q * p.tokens;
-        g.row = w.s.row + t0;
-        g.tokens = min(p.tokens, w.s.n - t0);
-        g.first = w.s.first + t0;
-        g.len = w.s.len;
-        g.b = w.b;
-        g.hk = w.hk;
-        g.tile0 = w.tile;
-        g.tiles = static_cast<int32_t>(min(static_cast<int64_t>(w.units), w.end)) - w.tile;
-        const bool whole = g.tiles == w.units;
-        g.flags = (whole ? kDirect : 0) | (w.s.keys(p, w.q) == 0 ? kEmpty : 0) |
-                  (w.s.bad_len ? kBadLen : 0);
-        g.slot = 2 * share + (g.tile0 == 0 ? 1 : 0);
-        if (g.tile0 == 0 && !whole) {
-          const int64_t last = line.begin(share + 1) - w.end + w.units - 1;
-          join = {static_cast<int32_t>(line.share_of(last)) - share + 1, g.slot, g.hk, g.row,
-                  g.tokens, g.first, {0, 0}};
-        }
+        const Segment g = w.segment(p, share);
+        if (g.tile0 == 0 && !(g.flags & kDirect)) join = w.join(line, share, g);
         const int r = n % kSegRing;
         publish(g);
         if (!ok) break;
@@ -285,8 +268,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t * kTile + kTile - 1 > seen) {
             fix_values<2>(smem + kValues + s * 2 * kBox, t * kTile, seen, g.len, first);
             if (t == g.tile0 + g.tiles - 1) {
-              const bool any = store_first<2>(first, ctrl->column[r]);
-              if (lane == 0) ctrl->unclean[r] = any;
+              if (merge_first<2>(first)) {
+                // (Two segments back the columns have been read.)
+                if (n >= 2 && !(ok = mbar_wait_warp(&ctrl->seg_empty[(n - 2) % kSegRing],
+                                                    ((n - 2) / kSegRing) & 1, abort_flag, kWaitNs)))
+                  break;
+                store_first<2>(first, ctrl->column[n & 1]);
+                if (lane == 0) ctrl->unclean[r] = 1;
+              }
             }
             fence_async_proxy();
           }
@@ -504,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 float x = __uint_as_float(v[i]);
-                if (unclean && ctrl->column[ring][key0 + c0 + i] <= far) x = NAN;
+                if (unclean && ctrl->column[n & 1][key0 + c0 + i] <= far) x = NAN;
                 part[(key0 + c0 + i) * kTile + r] = x;
               }
             }
@@ -553,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int32_t far = pos - seen_by_all(p, *g);
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (ctrl->column[ring][col0 + i] <= far) o[i] = ss = NAN;
+            if (ctrl->column[n & 1][col0 + i] <= far) o[i] = ss = NAN;
         }
         if (p.headnorm) {
           named_barrier_sync(1, kSoftmax);  // every thread has read the 1 / l exchange

@@ -290,7 +290,7 @@ def _parity(c, H, new, seed=3, before=0, behind=0, causal=True, headnorm=1, scal
     return out
 
 
-KINDS = [(64, BF16), (64, E4M3)]
+KINDS = [(64, BF16), (64, E4M3), (128, BF16), (128, E4M3)]
 
 
 @pytest.mark.parametrize("d,dtype", KINDS)
@@ -312,7 +312,7 @@ def test_long_ragged_batch(d, dtype, page, layout):
     _parity(c, 4, [900, 1, 0, 1, 60, 130])
 
 
-@pytest.mark.parametrize("d", [64])
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("headnorm", [0, 1, 2])
 def test_norms_and_masks(d, causal, headnorm):
@@ -320,7 +320,7 @@ def test_norms_and_masks(d, causal, headnorm):
     _parity(c, 4, [3, 200, 0, 1, 1, 66, 300], causal=causal, headnorm=headnorm)
 
 
-@pytest.mark.parametrize("d", [64])
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("causal", [True, False])
 def test_padding_positions(d, causal):
     """More tokens than the sequence is long: rows that see no key are zero, whole tiles of them
@@ -330,7 +330,7 @@ def test_padding_positions(d, causal):
     assert torch.all(out[:3] == 0) and torch.all(out[5:305] == 0)
 
 
-@pytest.mark.parametrize("d", [64])
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("kv,H,n,new", [(1, 1, 20001, 1), (1, 8, 12000, 33), (2, 2, 9000, 300),
                                         (8, 8, 3000, 3000)])
 def test_one_sequence(d, kv, H, n, new):
@@ -347,7 +347,7 @@ def test_many_sequences():
     _parity(c, 1, new)
 
 
-@pytest.mark.parametrize("d", [64])
+@pytest.mark.parametrize("d", [64, 128])
 def test_large_and_climbing_logits(d):
     c = R.Cache(17, lens=[1900, 130], kv=2, d=d, page=16, fill=0.0)
     for t in ("k1", "k2"):
@@ -360,7 +360,7 @@ def test_large_and_climbing_logits(d):
     _parity(c, 4, [700, 130], scale=4.0)
 
 
-@pytest.mark.parametrize("d", [64])
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("headnorm", [0, 1])
 @pytest.mark.parametrize("n", [130, 2500])
 def test_values_that_are_not_finite_reach_only_rows_that_see_them(d, headnorm, n):
@@ -374,7 +374,7 @@ def test_values_that_are_not_finite_reach_only_rows_that_see_them(d, headnorm, n
     _parity(c, 4, [new, 40], headnorm=headnorm)
 
 
-@pytest.mark.parametrize("d", [64])
+@pytest.mark.parametrize("d", [64, 128])
 def test_keys_and_queries_that_are_not_finite(d):
     """A NaN in a masked key has no influence; a NaN query row is its own row's."""
     c = R.Cache(19, lens=[300], kv=1, d=d, page=16)
@@ -387,7 +387,7 @@ def test_keys_and_queries_that_are_not_finite(d):
     assert bad[30:].all() and bad[7, 1] and int(bad[:30].sum()) == 1
 
 
-@pytest.mark.parametrize("d", [64])
+@pytest.mark.parametrize("d", [64, 128])
 def test_strided_queries_and_output(d):
     c = R.Cache(20, lens=[500, 90], kv=2, d=d, page=32)  # NaN behind the sequences
     starts = [0, 70, 90]
@@ -402,7 +402,7 @@ def test_strided_queries_and_output(d):
     assert torch.equal(out, want)
 
 
-@pytest.mark.parametrize("d", [64])
+@pytest.mark.parametrize("d", [64, 128])
 def test_bad_pages_lengths_and_rows(d):
     """Reported, and nothing outside the pool or the batch is touched."""
     c = R.Cache(21, lens=[200, 300, 100, 50, 2000], kv=2, d=d, page=16, fill=0.0)
@@ -434,7 +434,7 @@ def test_bad_pages_lengths_and_rows(d):
         assert torch.all(out[starts[-1]:] == 7.0)
 
 
-@pytest.mark.parametrize("d", [64])
+@pytest.mark.parametrize("d", [64, 128])
 def test_repeated_runs_graphs_and_stale_workspaces(d):
     c = R.Cache(22, lens=[3000, 700, 1], kv=2, d=d, page=16)
     q1, q2, lam, w = _queries(8, 400, 4, d, BF16)
