@@ -16,11 +16,14 @@
 namespace diffattn {
 namespace {
 
-// Block (share, 32 rows) joins the item that share begins and others go on with: a row a lane, 16
-// columns a warp, so that every read of a part is a whole line.
+// Block (share, 32 rows) joins the item that share begins and others go on with: a row a lane, 8
+// or 16 columns a warp, so that every read of a part is a whole line.  Latency bounds it (a few
+// parts of each item): all values of two parts are on their way at a time.
+constexpr int kJoinWarps = 16;
 template <int DV>
-__global__ void __launch_bounds__(2 * DV) diffragged_join_kernel(const __grid_constant__ RaggedParams p) {
-  constexpr int kWarps = DV / 16;
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    diffragged_join_kernel(const __grid_constant__ RaggedParams p) {
+  constexpr int kWarps = kJoinWarps, kCols = DV / kWarps;
   __shared__ float sums[kWarps][33];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   grid_dependency_wait();
@@ -32,33 +35,43 @@ __global__ void __launch_bounds__(2 * DV) diffragged_join_kernel(const __grid_co
   const auto part = [&](int k) {
     return p.part + (k == 0 ? j.slot : 2ll * (j.slot / 2 + k)) * 2 * kMap + r;
   };
-  float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll 4
-  for (int k = 0; k < j.parts; ++k)
-#pragma unroll
-    for (int m = 0; m < 2; ++m) top[m] = fmaxf(top[m], part(k)[m * kMap + DV * kTile]);
-  float o[2][16], l[2] = {0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 16; ++i) o[0][i] = o[1][i] = 0.f;
-#pragma unroll 1
-  for (int k = 0; k < j.parts; ++k) {
-    const float *src = part(k);
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const float ref = src[m * kMap + DV * kTile];
-      const float f = ref == top[m] ? 1.f : exp2f(ref - top[m]);
-      l[m] = fmaf(f, src[m * kMap + (DV + 1) * kTile], l[m]);
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        o[m][i] = fmaf(f, src[m * kMap + (16 * warp + i) * kTile], o[m][i]);
-    }
-  }
   const int32_t token = p.by_group.div(r), h = j.hk * p.group + r - token * p.group;
   const bool mine = r < rows;
-  const float c1 = 1.f / l[0], c2 = mine ? p.lambda[h] / l[1] : 0.f;
+  const float lam = mine ? p.lambda[h] : 0.f;
+  float gain[kCols];
+#pragma unroll
+  for (int i = 0; i < kCols; ++i)
+    gain[i] = p.headnorm && p.norm_w != nullptr && mine ? p.norm_w[h * DV + kCols * warp + i] : 1.f;
+  // Against the largest reference so far, as the parts were against theirs.
+  float top[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[2][kCols];
+#pragma unroll
+  for (int i = 0; i < kCols; ++i) o[0][i] = o[1][i] = 0.f;
+#pragma unroll 2
+  for (int k = 0; k < j.parts; ++k) {
+    const float *src = part(k);
+    float x[2][kCols], ref[2], sum[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      ref[m] = src[m * kMap + DV * kTile];
+      sum[m] = src[m * kMap + (DV + 1) * kTile];
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) x[m][i] = src[m * kMap + (kCols * warp + i) * kTile];
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const float now = fmaxf(top[m], ref[m]);
+      const float old = top[m] == now ? 1.f : exp2f(top[m] - now);
+      const float f = ref[m] == now ? 1.f : exp2f(ref[m] - now);
+      top[m] = now;
+      l[m] = l[m] * old + f * sum[m];
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) o[m][i] = o[m][i] * old + f * x[m][i];
+    }
+  }
+  const float c1 = 1.f / l[0], c2 = lam / l[1];
   float ss = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < kCols; ++i) {
     o[0][i] = o[0][i] * c1 - o[1][i] * c2;
     ss = fmaf(o[0][i], o[0][i], ss);
   }
@@ -75,40 +88,39 @@ __global__ void __launch_bounds__(2 * DV) diffragged_join_kernel(const __grid_co
     if (p.headnorm == 2) {
       float sm = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sm += o[0][i];
+      for (int i = 0; i < kCols; ++i) sm += o[0][i];
       const float mu = over_row(sm) * (1.f / DV);
       ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < kCols; ++i) {
         o[0][i] -= mu;
         ss = fmaf(o[0][i], o[0][i], ss);
       }
     }
     const float rr = rsqrtf(over_row(ss) * (1.f / DV) + p.eps) * p.out_scale;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      o[0][i] *= p.norm_w != nullptr && mine ? rr * p.norm_w[h * DV + 16 * warp + i] : rr;
+    for (int i = 0; i < kCols; ++i) o[0][i] *= rr * gain[i];
   }
   if (!mine) return;
   if (j.first + token < 0) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[0][i] = 0.f;
+    for (int i = 0; i < kCols; ++i) o[0][i] = 0.f;
   }
   if (!dbg_ok(j.row + token < p.N, p.status, 110)) return;
-  uint4 *out = reinterpret_cast<uint4 *>(p.out + (j.row + token) * p.out_n + h * p.out_h + 16 * warp);
+  uint4 *out =
+      reinterpret_cast<uint4 *>(p.out + (j.row + token) * p.out_n + h * p.out_h + kCols * warp);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    out[i] = make_uint4(pack_bf16x2(o[0][8 * i], o[0][8 * i + 1]),
-                        pack_bf16x2(o[0][8 * i + 2], o[0][8 * i + 3]),
-                        pack_bf16x2(o[0][8 * i + 4], o[0][8 * i + 5]),
-                        pack_bf16x2(o[0][8 * i + 6], o[0][8 * i + 7]));
+  for (int i = 0; i < kCols; i += 8)
+    out[i / 8] = make_uint4(pack_bf16x2(o[0][i], o[0][i + 1]), pack_bf16x2(o[0][i + 2], o[0][i + 3]),
+                            pack_bf16x2(o[0][i + 4], o[0][i + 5]),
+                            pack_bf16x2(o[0][i + 6], o[0][i + 7]));
 }
 
 template <int DV>
 cudaError_t launch_join(const RaggedParams &p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.shares), 4);
-  cfg.blockDim = dim3(2 * DV);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -133,24 +133,25 @@ __device__ __forceinline__ void fence_async_proxy() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// sum_{i < n} floor((a i + b) / m), a, b >= 0, by exchanging the two axes of the lattice below the
-// line (Euclid's steps on a and m).
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int32_t m, int32_t a, int64_t b) {
+// sum_{i < n} floor((a i + b) / m), a n + b below 2^32, by exchanging the two axes of the lattice
+// below the line (Euclid's steps on a and m).
+__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   int64_t sum = 0;
+#pragma unroll 1
   while (true) {
     if (a >= m) {
-      sum += n * (n - 1) / 2 * (a / m);
+      sum += static_cast<int64_t>(n) * (n - 1) / 2 * (a / m);
       a %= m;
     }
     if (b >= m) {
-      sum += n * (b / m);
+      sum += static_cast<int64_t>(n) * (b / m);
       b %= m;
     }
-    const int64_t y = a * n + b;
+    const uint32_t y = a * n + b;
     if (y < m) return sum;
     n = y / m;
     b = y % m;
-    const int32_t t = m;
+    const uint32_t t = m;
     m = a;
     a = t;
   }
@@ -185,12 +186,12 @@ struct Seq {
     const int32_t whole = min(q, tiles - 1);  // tiles with all their tokens
     int64_t s = static_cast<int64_t>(q) * kItemCost;
     if (whole > 0) {
-      const int32_t idle = first < 0 ? min(whole, -first / p.tokens) : 0;
+      const int32_t idle = first < 0 ? min(whole, p.by_tokens.div(-first)) : 0;
       s += idle;
       if (p.causal) {
-        const int64_t b = first + static_cast<int64_t>(idle + 1) * p.tokens - 1;
         s += whole - idle;
-        if (whole > idle) s += floor_sum(whole - idle, kTile, p.tokens, b);
+        if (whole > idle)
+          s += floor_sum(whole - idle, kTile, p.tokens, first + (idle + 1) * p.tokens - 1);
       } else {
         s += static_cast<int64_t>(whole - idle) * ((len + kTile - 1) / kTile);
       }
@@ -213,10 +214,11 @@ struct Line {
   }
 };
 
+// Where a share begins: in sequence b (p.B for nowhere), `left` steps (whole items: items) into it.
 struct ShareState {
   unsigned long long total, items, sums[32];
-  unsigned long long left;  // steps (whole items: items) of the sequence before the share
-  int32_t longest, b;       // b: the sequence that it begins in, B for none
+  unsigned long long left;
+  int32_t longest, b;
 };
 
 // How a line of `total` steps in `items` items, the longest of `longest` steps, is shared.
@@ -235,7 +237,67 @@ __device__ __forceinline__ Line cut_line(int32_t shares, int64_t total, int64_t 
   return line;
 }
 
-// Finds the sequence that share `index` begins in (all kThreads threads; ends with a barrier).
+__device__ __forceinline__ int64_t steps_of(const RaggedParams &p, const Seq &s) {
+  return s.n > 0 ? s.steps(p, s.tiles) * p.kv_heads : int64_t{0};
+}
+__device__ __forceinline__ int64_t warp_scan(int64_t x) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (static_cast<int>(threadIdx.x % 32) >= o) x += y;
+  }
+  return x;
+}
+
+// As many sequences as one warp looks through by itself, two a lane.  More take all of the block's
+// threads and some barriers.
+constexpr int kFewSequences = 64;
+
+// Finds where share `index` begins, among few sequences (one warp, the result in registers of it
+// all).
+__device__ __forceinline__ Line find_share_few(const RaggedParams &p, int32_t index, ShareState *st) {
+  const int lane = threadIdx.x % 32;
+  int64_t steps[2], items[2];
+  int32_t longest = 0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    steps[k] = items[k] = 0;
+    if (lane + 32 * k < p.B) {
+      const Seq s(p, lane + 32 * k);
+      if (s.n > 0) {
+        steps[k] = steps_of(p, s);
+        items[k] = static_cast<int64_t>(s.tiles) * p.kv_heads;
+        longest = max(longest, kItemCost + s.units(p, s.tiles - 1));
+      }
+      if (s.bad_rows && index == 0) report_bad_page(p.status);
+    }
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  const int64_t s0 = warp_scan(steps[0]), all0 = __shfl_sync(0xffffffffu, s0, 31);
+  const int64_t i0 = warp_scan(items[0]), items0 = __shfl_sync(0xffffffffu, i0, 31);
+  const int64_t s1 = warp_scan(steps[1]) + all0, total = __shfl_sync(0xffffffffu, s1, 31);
+  const int64_t i1 = warp_scan(items[1]) + items0, all_items = __shfl_sync(0xffffffffu, i1, 31);
+  const Line line = cut_line(p.shares, total, all_items, longest);
+  const bool whole = line.mode == kWhole;
+  const int64_t target = whole ? index : line.begin(index);
+  st->b = p.B;
+  if (index < line.shares && target < (whole ? all_items : total)) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int64_t end = whole ? (k ? i1 : i0) : (k ? s1 : s0);
+      const int64_t begin = end - (whole ? items[k] : steps[k]);
+      const uint32_t at = __ballot_sync(0xffffffffu, begin <= target && target < end);
+      if (at != 0) {
+        st->b = 32 * k + __ffs(at) - 1;
+        st->left = target - __shfl_sync(0xffffffffu, begin, __ffs(at) - 1);
+      }
+    }
+  }
+  return line;
+}
+
+// The same among any number, by all kThreads threads (ends with a barrier; the result in shared
+// memory).
 template <int kThreads>
 __device__ __forceinline__ Line find_share(const RaggedParams &p, int32_t index, ShareState *st) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -245,14 +307,11 @@ __device__ __forceinline__ Line find_share(const RaggedParams &p, int32_t index,
     st->b = p.B;
   }
   __syncthreads();
-  const auto steps_of = [&](const Seq &s) {
-    return s.n > 0 ? s.steps(p, s.tiles) * p.kv_heads : int64_t{0};
-  };
   int64_t total = 0, items = 0, mine = 0, mine_items = 0;
   int32_t longest = 0;
   for (int32_t b = tid; b < p.B; b += kThreads) {
     const Seq s(p, b);
-    const int64_t t = steps_of(s);
+    const int64_t t = steps_of(p, s);
     const int64_t n = static_cast<int64_t>(s.tiles) * p.kv_heads;
     if (b == tid) {
       mine = t;
@@ -276,24 +335,20 @@ __device__ __forceinline__ Line find_share(const RaggedParams &p, int32_t index,
   }
   __syncthreads();
   const Line line = cut_line(p.shares, st->total, st->items, st->longest);
-  const int64_t target = line.mode == kWhole ? index : line.begin(index);
-  const int64_t all = line.mode == kWhole ? st->items : st->total;
+  const bool whole = line.mode == kWhole;
+  const int64_t target = whole ? index : line.begin(index);
+  const int64_t all = whole ? st->items : st->total;
   if (index < line.shares && target < all) {  // uniform
     int64_t base = 0;
     for (int32_t b0 = 0; b0 < p.B && base <= target; b0 += kThreads) {
       int64_t x = 0;
       if (b0 == 0) {
-        x = line.mode == kWhole ? mine_items : mine;
+        x = whole ? mine_items : mine;
       } else if (b0 + tid < p.B) {
         const Seq s(p, b0 + tid);
-        x = line.mode == kWhole ? static_cast<int64_t>(s.tiles) * p.kv_heads : steps_of(s);
+        x = whole ? static_cast<int64_t>(s.tiles) * p.kv_heads : steps_of(p, s);
       }
-      int64_t incl = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
+      const int64_t incl = warp_scan(x);
       if (lane == 31) st->sums[warp] = incl;
       __syncthreads();
       int64_t before = base, chunk = 0;
@@ -432,43 +487,71 @@ __device__ __forceinline__ int32_t seen_by_all(const RaggedParams &p, const Segm
 // the others that are not finite as well, in shared memory; a column's first such key (its distance
 // from `seen`, at most 254) is kept in `first`, two columns a word, eight of each block of 64 a
 // lane, by the four lanes that agree in lane % 8: rows at least that far from `seen` see it.  One
-// warp.
+// warp; a first look over all of them costs a tenth of the look at each (d = 64, 127 keys: 0.9 and
+// 9.7 us), and all but broken models' values need no other.
+template <int kBlocks>
+__device__ __forceinline__ void fix_each(uint8_t *tile, int32_t key0, int32_t seen, int32_t len,
+                                         uint32_t (&first)[kBlocks][4]) {
+  const int lane = threadIdx.x % 32;
+  const int chunk = lane & 7;  // four rows at a time
+#pragma unroll 1
+  for (int row = (lane >> 3); row < kTile && key0 + row < len; row += 4) {
+    if (key0 + row <= seen) continue;
+    const uint32_t d = min(254, key0 + row - seen);
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k) {
+      uint32_t *at = reinterpret_cast<uint32_t *>(tile + k * (kTile * 128) + row * 128 +
+                                                  ((chunk ^ (row & 7)) << 4));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = at[i];
+        const bool lo = (w & 0x7F80u) == 0x7F80u, hi = (w & 0x7F800000u) == 0x7F800000u;
+        const uint32_t f = first[k][i];
+        first[k][i] = (lo ? min(f & 0xFFFFu, d) : f & 0xFFFFu) |
+                      ((hi ? min(f >> 16, d) : f >> 16) << 16);
+        if (lo || hi) at[i] = w & ((lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0xFFFFu : 0xFFFFFFFFu));
+      }
+    }
+  }
+}
 template <int kBlocks>
 __device__ __forceinline__ void fix_values(uint8_t *tile, int32_t key0, int32_t seen, int32_t len,
                                            uint32_t (&first)[kBlocks][4]) {
   const int lane = threadIdx.x % 32;
-  const int chunk = lane & 7, half = lane >> 3;  // four rows at a time
-#pragma unroll 1
-  for (int row = max(0, seen + 1 - key0) / 4 * 4 + half; row < kTile; row += 4) {
-    const int32_t key = key0 + row;
-    if (key <= seen) continue;
+  const int half = lane >> 3;
+  uint8_t *mine = tile + half * 128;
+  // Rows 8 j + half and 8 j + half + 4 of this lane: its chunk sits at one of two places of a row.
+  const int c0 = ((lane & 7) ^ half) << 4, c1 = c0 ^ 64;
+  uint32_t odd = 0;
+  const int end = min(kTile, len - key0);  // keys of the sequence
+  // (Loads alone, so that many are on their way.  An exponent of ones carries into the sign's place.
+  // Keys that all rows see may count here too: fix_each tells them apart.)
+#pragma unroll(kBlocks == 2 ? 2 : 1)
+  for (int row = max(0, seen + 1 - key0) & ~7; row < end; row += 8) {
+    uint4 x[2][kBlocks];
 #pragma unroll
-    for (int k = 0; k < kBlocks; ++k) {
-      uint4 *at = reinterpret_cast<uint4 *>(tile + k * (kTile * 128) + row * 128 +
-                                            ((chunk ^ (row & 7)) << 4));
-      if (key >= len) {
-        *at = make_uint4(0, 0, 0, 0);
-        continue;
-      }
-      uint4 x = *at;
-      uint32_t *w = reinterpret_cast<uint32_t *>(&x);
-      bool any = false;
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool lo = (w[i] & 0x7F80u) == 0x7F80u, hi = (w[i] & 0x7F800000u) == 0x7F800000u;
-        if (lo || hi) {
-          const uint32_t d = min(254, key - seen);
-          uint32_t f = first[k][i];
-          if (lo) f = (f & 0xFFFF0000u) | min(f & 0xFFFFu, d);
-          if (hi) f = (f & 0xFFFFu) | (min(f >> 16, d) << 16);
-          first[k][i] = f;
-          w[i] &= (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0xFFFFu : 0xFFFFFFFFu);
-          any = true;
-        }
-      }
-      if (any) *at = x;
+      for (int k = 0; k < kBlocks; ++k)
+        x[h][k] = *reinterpret_cast<const uint4 *>(mine + (row + 4 * h) * 128 + k * (kTile * 128) +
+                                                   (h ? c1 : c0));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t any = 0;
+#pragma unroll
+      for (int k = 0; k < kBlocks; ++k)
+        any |= ((x[h][k].x & 0x7F807F80u) + 0x00800080u) | ((x[h][k].y & 0x7F807F80u) + 0x00800080u) |
+               ((x[h][k].z & 0x7F807F80u) + 0x00800080u) | ((x[h][k].w & 0x7F807F80u) + 0x00800080u);
+      odd |= row + half + 4 * h < end ? any : 0;
     }
   }
+  for (int row = end + half; row < kTile; row += 4)
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k)  // (the lanes of a row cover its chunks in any order)
+      *reinterpret_cast<uint4 *>(tile + row * 128 + k * (kTile * 128) + ((lane & 7) << 4)) =
+          make_uint4(0, 0, 0, 0);
+  if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0))
+    fix_each<kBlocks>(tile, key0, seen, len, first);
 }
 
 // The smallest over the four lanes that agree in lane % 8; whether any lane has one.

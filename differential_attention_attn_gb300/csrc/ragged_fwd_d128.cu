@@ -14,7 +14,8 @@
 // At an item's end CTA m has o_m = (1 or -lambda) O_m / l_m.  Each hands the other
 // half of its columns (128 of 256, fp32, through L2: shared memory is full),
 // adds what it gets, and finishes those 128 columns; the norm's row sums cross
-// through distributed shared memory.
+// through distributed shared memory.  Eight warps of their own do this while the
+// softmax warps are at the next item.
 //
 // Tensor memory: S / P at 0 and 128 in turn, O at 256; shared memory: Q 32 KB, two
 // tiles of K (32 KB each) and two of V (64 KB each).
@@ -32,8 +33,13 @@ namespace {
 
 constexpr int HD = 128, DV = 256;
 constexpr int kSlots = 2;
-constexpr int kThreads = 384, kSoftmax = 256, kSoftmaxWarps = kSoftmax / 32;
-constexpr int kKeyWarp = 0, kMmaWarp = 1, kValueWarp = 2, kQueryWarp = 3;
+constexpr int kThreads = 640, kSoftmax = 256, kSoftmaxWarps = kSoftmax / 32;
+constexpr int kFinish = 256, kFinishWarps = kFinish / 32;
+constexpr int kKeyWarp = 0, kMmaWarp = 1, kValueWarp = 2, kQueryWarp = 3, kSoftmaxWarp = 4,
+              kFinishWarp = 12;
+constexpr uint32_t kRegsLaunch = 96, kRegsCtrl = 64, kRegsRest = 104;
+static_assert(128 * kRegsCtrl + (kSoftmax + kFinish) * kRegsRest <= kThreads * kRegsLaunch,
+              "register split");
 
 constexpr uint32_t kBox = kTile * 128;  // 64 bf16 or 128 e4m3 columns of a tile
 constexpr uint32_t kQ = 0, kKeys = 2 * kBox, kValues = kKeys + kSlots * 2 * kBox;
@@ -43,6 +49,7 @@ constexpr uint32_t kTmO = 256;
 struct Ctrl {
   uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots], v_fixed[kSlots];
   uint64_t q_full, q_empty, s_full[2], p_ready[2], pv_done, o_done, o_free, drain;
+  uint64_t l_full[2];  // by segment with keys: the softmax may be done with the next one's as well
   uint64_t peer[2];  // the other CTA's hand-overs, in turn
   uint64_t seg_full[kSegRing], seg_empty[kSegRing];
   Segment seg[kSegRing];
@@ -51,9 +58,10 @@ struct Ctrl {
   int abort;
   alignas(8) uint8_t column[2][DV];
   alignas(8) float xch[2][kTile];  // the other CTA's row sums, in turn
+  float inv[2][kTile];             // 1 / l of the rows, by segment with keys
 };
 static_assert(sizeof(ShareState) <= 2 * kTile * sizeof(float), "the set-up's state lies in xch");
-constexpr uint32_t kSmem = kCtrlAt + sizeof(Ctrl) + 1024;
+constexpr uint32_t kSmem = kCtrlAt + sizeof(Ctrl);
 static_assert(kSmem <= 232448, "shared memory");
 
 __device__ __forceinline__ uint32_t peer_address(const void *p, uint32_t rank) {
@@ -106,9 +114,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                const __grid_constant__ CUtensorMap tm_k2,
                                const __grid_constant__ CUtensorMap tm_v,
                                const __grid_constant__ RaggedParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                              ~static_cast<uintptr_t>(1023));
+  // (No room for slack: the declared alignment is what the swizzled tiles need.)
+  extern __shared__ __align__(1024) uint8_t smem[];
   Ctrl *ctrl = reinterpret_cast<Ctrl *>(smem + kCtrlAt);
   volatile int *abort_flag = &ctrl->abort;
   constexpr int kKeyBoxes = kFp8 ? 1 : 2;  // of 128 bytes a row
@@ -131,14 +138,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctrl->s_full[k], 1);
       mbar_init(&ctrl->p_ready[k], kSoftmaxWarps);
       mbar_init(&ctrl->peer[k], 1);
+      mbar_init(&ctrl->l_full[k], kSoftmaxWarps);
     }
     mbar_init(&ctrl->pv_done, 1);
     mbar_init(&ctrl->o_done, 1);
-    mbar_init(&ctrl->o_free, kSoftmaxWarps);
+    mbar_init(&ctrl->o_free, kFinishWarps);
     mbar_init(&ctrl->drain, 1);
     for (int s = 0; s < kSegRing; ++s) {
       mbar_init(&ctrl->seg_full[s], 1);
-      mbar_init(&ctrl->seg_empty[s], 3 + kSoftmaxWarps);
+      mbar_init(&ctrl->seg_empty[s], 3 + kSoftmaxWarps + kFinishWarps);
     }
     ctrl->abort = 0;
     fence_barrier_init();
@@ -161,499 +169,552 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
   ShareState *state = reinterpret_cast<ShareState *>(ctrl->xch);
   tc_fence_before_sync();
-  const Line line = find_share<kThreads>(p, share, state);
+  Line line;
+  if (p.B > kFewSequences)
+    line = find_share<kThreads>(p, share, state);
+  else
+    __syncthreads();
   tc_fence_after_sync();
   grid_dependents_launch();
   const uint32_t tmem = ctrl->tmem;
 
-  if (warp == kKeyWarp) {
-    // --------------------------------------------------------------- keys, and the segments
-    const int box = lane % kKeyBoxes, piece = lane / kKeyBoxes, row0 = piece * p.piece_rows;
-    const bool piece_ok = row0 < kTile;
-    Walk w(p, line, share, *state);
-    Ring<kSlots> ring;
-    RaggedJoin join = {};
-    uint32_t n = 0;
-    bool ok = true;
-    const auto publish = [&](const Segment &g) {
-      const int r = n % kSegRing;
-      if (n >= kSegRing)
-        ok = mbar_wait_warp(&ctrl->seg_empty[r], (n / kSegRing - 1) & 1, abort_flag, kWaitNs);
-      if (ok && lane == 0) {
-        ctrl->seg[r] = g;
-        ctrl->bad[r] = 0;
-        mbar_arrive(&ctrl->seg_full[r]);
+  // (The register budget of each side's code goes by the branch that it stands in.)
+  if (warp < kSoftmaxWarp) {
+    setmaxnreg_dec<kRegsCtrl>();
+    if (warp == kKeyWarp) {
+      // --------------------------------------------------------------- keys, and the segments
+      const int box = lane % kKeyBoxes, piece = lane / kKeyBoxes, row0 = piece * p.piece_rows;
+      const bool piece_ok = row0 < kTile;
+      ShareState few;
+      if (p.B <= kFewSequences) line = find_share_few(p, share, &few);
+      Walk w(p, line, share, p.B <= kFewSequences ? few : *state);
+      Ring<kSlots> ring;
+      RaggedJoin join = {};
+      uint32_t n = 0;
+      bool ok = true;
+      const auto publish = [&](const Segment &g) {
+        const int r = n % kSegRing;
+        if (n >= kSegRing)
+          ok = mbar_wait_warp(&ctrl->seg_empty[r], (n / kSegRing - 1) & 1, abort_flag, kWaitNs);
+        if (ok && lane == 0) {
+          ctrl->seg[r] = g;
+          ctrl->bad[r] = 0;
+          mbar_arrive(&ctrl->seg_full[r]);
+        }
+        ++n;
+      };
+      while (ok && w.more(p)) {
+        const Segment g = w.segment(p, share);
+        if (g.tile0 == 0 && !(g.flags & kDirect)) join = w.join(line, share, g);
+        const int r = n % kSegRing;
+        publish(g);
+        if (!ok) break;
+        if (w.s.bad_len && lane == 0) report_bad_page(p.status);
+        if (!(g.flags & kEmpty)) {
+          int32_t key = g.tile0 * kTile + row0;
+          int32_t id = page_of(p, g.b, g.len, key, piece_ok);
+          for (int32_t t = 0; t < g.tiles; ++t, key += kTile) {
+            const int32_t page = id;
+            const bool have = piece_ok && key < g.len;
+            const bool bad = have && static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages);
+            if (t + 1 < g.tiles) id = page_of(p, g.b, g.len, key + kTile, piece_ok);
+            if (!(ok = ring.wait_empty(ctrl->k_empty, abort_flag))) break;
+            const int s = ring.slot();
+            if (__any_sync(0xffffffffu, bad) && lane == 0) {
+              ctrl->bad[r] = 1;
+              report_bad_page(p.status);
+            }
+            if (have && dbg_ok(row0 + p.piece_rows <= kTile, p.status, 120))
+              tma_load_4d(smem + kKeys + s * 2 * kBox + box * kBox + row0 * 128, tm_k,
+                          &ctrl->k_full[s], 64 * box, p.by_page.mod(key), g.hk, bad ? 0 : page);
+            const int pieces = __popc(__ballot_sync(0xffffffffu, have));
+            if (lane == 0) mbar_arrive_expect_tx(&ctrl->k_full[s], pieces * p.piece_rows * 128);
+            ++ring.n;
+          }
+          if (!ok) break;
+        }
+        w.next(p);
       }
-      ++n;
-    };
-    while (ok && w.more(p)) {
-      const Segment g = w.segment(p, share);
-      if (g.tile0 == 0 && !(g.flags & kDirect)) join = w.join(line, share, g);
-      const int r = n % kSegRing;
-      publish(g);
-      if (!ok) break;
-      if (w.s.bad_len && lane == 0) report_bad_page(p.status);
-      if (!(g.flags & kEmpty)) {
+      if (ok) {
+        Segment g = {};
+        g.flags = kStop;
+        publish(g);
+      }
+      if (lane == 0) {
+        if (p.joins != nullptr && map == 0) p.joins[share] = join;
+        ring.drain(ctrl->k_full);
+      }
+      __syncwarp();
+    } else if (warp == kValueWarp) {
+      // --------------------------------------------------------------- values
+      const int box = lane & 3, piece = lane >> 2, row0 = piece * p.piece_rows;
+      const bool piece_ok = row0 < kTile;
+      Ring<kSlots> ring;
+      bool ok = true;
+      for (uint32_t n = 0; ok; ++n) {
+        const int r = n % kSegRing;
+        if (!mbar_wait_warp(&ctrl->seg_full[r], (n / kSegRing) & 1, abort_flag, kWaitNs)) break;
+        const Segment g = ctrl->seg[r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->seg_empty[r]);
+        if (g.flags & kStop) break;
+        if (g.flags & kEmpty) continue;
         int32_t key = g.tile0 * kTile + row0;
         int32_t id = page_of(p, g.b, g.len, key, piece_ok);
         for (int32_t t = 0; t < g.tiles; ++t, key += kTile) {
           const int32_t page = id;
           const bool have = piece_ok && key < g.len;
-          const bool bad = have && static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages);
+          const bool bad = static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages);
           if (t + 1 < g.tiles) id = page_of(p, g.b, g.len, key + kTile, piece_ok);
-          if (!(ok = ring.wait_empty(ctrl->k_empty, abort_flag))) break;
+          if (!(ok = ring.wait_empty(ctrl->v_empty, abort_flag))) break;
           const int s = ring.slot();
-          if (__any_sync(0xffffffffu, bad) && lane == 0) {
-            ctrl->bad[r] = 1;
-            report_bad_page(p.status);
-          }
-          if (have && dbg_ok(row0 + p.piece_rows <= kTile, p.status, 120))
-            tma_load_4d(smem + kKeys + s * 2 * kBox + box * kBox + row0 * 128, tm_k,
-                        &ctrl->k_full[s], 64 * box, p.by_page.mod(key), g.hk, bad ? 0 : page);
+          if (have && dbg_ok(row0 + p.piece_rows <= kTile, p.status, 121))
+            tma_load_4d(smem + kValues + s * 4 * kBox + box * kBox + row0 * 128, &tm_v,
+                        &ctrl->v_full[s], 64 * box, p.by_page.mod(key), g.hk, bad ? 0 : page);
           const int pieces = __popc(__ballot_sync(0xffffffffu, have));
-          if (lane == 0) mbar_arrive_expect_tx(&ctrl->k_full[s], pieces * p.piece_rows * 128);
+          if (lane == 0) mbar_arrive_expect_tx(&ctrl->v_full[s], pieces * p.piece_rows * 128);
           ++ring.n;
         }
-        if (!ok) break;
       }
-      w.next(p);
-    }
-    if (ok) {
-      Segment g = {};
-      g.flags = kStop;
-      publish(g);
-    }
-    if (lane == 0) {
-      if (p.joins != nullptr && map == 0) p.joins[share] = join;
-      ring.drain(ctrl->k_full);
-    }
-    __syncwarp();
-  } else if (warp == kValueWarp) {
-    // --------------------------------------------------------------- values
-    const int box = lane & 3, piece = lane >> 2, row0 = piece * p.piece_rows;
-    const bool piece_ok = row0 < kTile;
-    Ring<kSlots> ring;
-    bool ok = true;
-    for (uint32_t n = 0; ok; ++n) {
-      const int r = n % kSegRing;
-      if (!mbar_wait_warp(&ctrl->seg_full[r], (n / kSegRing) & 1, abort_flag, kWaitNs)) break;
-      const Segment g = ctrl->seg[r];
+      if (lane == 0) ring.drain(ctrl->v_full);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctrl->seg_empty[r]);
-      if (g.flags & kStop) break;
-      if (g.flags & kEmpty) continue;
-      int32_t key = g.tile0 * kTile + row0;
-      int32_t id = page_of(p, g.b, g.len, key, piece_ok);
-      for (int32_t t = 0; t < g.tiles; ++t, key += kTile) {
-        const int32_t page = id;
-        const bool have = piece_ok && key < g.len;
-        const bool bad = static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages);
-        if (t + 1 < g.tiles) id = page_of(p, g.b, g.len, key + kTile, piece_ok);
-        if (!(ok = ring.wait_empty(ctrl->v_empty, abort_flag))) break;
-        const int s = ring.slot();
-        if (have && dbg_ok(row0 + p.piece_rows <= kTile, p.status, 121))
-          tma_load_4d(smem + kValues + s * 4 * kBox + box * kBox + row0 * 128, &tm_v,
-                      &ctrl->v_full[s], 64 * box, p.by_page.mod(key), g.hk, bad ? 0 : page);
-        const int pieces = __popc(__ballot_sync(0xffffffffu, have));
-        if (lane == 0) mbar_arrive_expect_tx(&ctrl->v_full[s], pieces * p.piece_rows * 128);
-        ++ring.n;
-      }
-    }
-    if (lane == 0) ring.drain(ctrl->v_full);
-    __syncwarp();
-  } else if (warp == kQueryWarp) {
-    // --------------------------------------------------------------- queries, and clean values
-    uint32_t filled = 0, tiles = 0;
-    for (uint32_t n = 0;; ++n) {
-      const int r = n % kSegRing;
-      if (!mbar_wait_warp(&ctrl->seg_full[r], (n / kSegRing) & 1, abort_flag, kWaitNs)) break;
-      const Segment g = ctrl->seg[r];
-      if (g.flags & (kStop | kEmpty)) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctrl->seg_empty[r]);
-        if (g.flags & kStop) break;
-        continue;
-      }
-      if (filled > 0 && !mbar_wait_warp(&ctrl->q_empty, (filled - 1) & 1, abort_flag, kWaitNs))
-        break;
-      if (lane == 0) {
-        dbg_ok(g.row >= 0 && g.row + g.tokens <= p.N, p.status, 122);
-        ctrl->unclean[r] = 0;
-        mbar_arrive_expect_tx(&ctrl->q_full, kKeyBoxes * p.tokens * p.group * 128);
-        for (int k = 0; k < kKeyBoxes; ++k)
-          tma_load_3d(smem + kQ + k * kBox, tm_q, &ctrl->q_full, 64 * k, g.hk * p.group, g.row);
-      }
-      ++filled;
-      const int32_t seen = seen_by_all(p, g);
-      uint32_t first[4][4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) first[k][i] = 0xFFFFFFFFu;
-      bool ok = true;
-      // (Every value tile passes here, so that neither this warp nor the products can get a whole
-      // turn of the ring ahead of the other.)
-      for (int32_t t = g.tile0; t < g.tile0 + g.tiles; ++t, ++tiles) {
-        const int s = tiles % kSlots;
-        if (!(ok = mbar_wait_warp(&ctrl->v_full[s], (tiles / kSlots) & 1, abort_flag, kWaitNs)))
+    } else if (warp == kQueryWarp) {
+      // --------------------------------------------------------------- queries, and clean values
+      uint32_t filled = 0, tiles = 0;
+      for (uint32_t n = 0;; ++n) {
+        const int r = n % kSegRing;
+        if (!mbar_wait_warp(&ctrl->seg_full[r], (n / kSegRing) & 1, abort_flag, kWaitNs)) break;
+        const Segment g = ctrl->seg[r];
+        if (g.flags & (kStop | kEmpty)) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctrl->seg_empty[r]);
+          if (g.flags & kStop) break;
+          continue;
+        }
+        if (filled > 0 && !mbar_wait_warp(&ctrl->q_empty, (filled - 1) & 1, abort_flag, kWaitNs))
           break;
-        if (t * kTile + kTile - 1 > seen) {
-          fix_values<4>(smem + kValues + s * 4 * kBox, t * kTile, seen, g.len, first);
-          if (t == g.tile0 + g.tiles - 1) {
-            if (merge_first<4>(first)) {
-              // (Two segments back the columns have been read.)
-              if (n >= 2 && !(ok = mbar_wait_warp(&ctrl->seg_empty[(n - 2) % kSegRing],
-                                                  ((n - 2) / kSegRing) & 1, abort_flag, kWaitNs)))
-                break;
-              store_first<4>(first, ctrl->column[n & 1]);
-              if (lane == 0) ctrl->unclean[r] = 1;
-            }
-          }
-          fence_async_proxy();
+        if (lane == 0) {
+          dbg_ok(g.row >= 0 && g.row + g.tokens <= p.N, p.status, 122);
+          ctrl->unclean[r] = 0;
+          mbar_arrive_expect_tx(&ctrl->q_full, kKeyBoxes * p.tokens * p.group * 128);
+          for (int k = 0; k < kKeyBoxes; ++k)
+            tma_load_3d(smem + kQ + k * kBox, tm_q, &ctrl->q_full, 64 * k, g.hk * p.group, g.row);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctrl->v_fixed[s]);
-      }
-      if (!ok) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctrl->seg_empty[r]);
-    }
-    if (lane == 0 && filled > 0) drain_wait(&ctrl->q_full, (filled - 1) & 1);
-    __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // --------------------------------------------------------------- products
-    constexpr uint32_t kIdescQK = idesc_bf16_f32(kTile, kTile, false);
-    constexpr uint32_t kIdescQK8 = idesc_e4m3_f32(kTile, kTile);
-    constexpr uint32_t kIdescPV = idesc_bf16_f32(kTile, DV, true);
-    const uint64_t q64 = smem_desc_sw128(smem_u32(smem + kQ), 16, 1024);
-    const uint64_t k64 = smem_desc_sw128(smem_u32(smem + kKeys), 16, 1024);
-    const uint32_t dhi = static_cast<uint32_t>(q64 >> 32);
-    const uint32_t dq = static_cast<uint32_t>(q64), dk = static_cast<uint32_t>(k64);
-    const uint32_t dv =
-        static_cast<uint32_t>(smem_desc_sw128(smem_u32(smem + kValues), kBox, 1024));
-    auto qk = [&](uint32_t c) {  // S of key tile c
-      const uint32_t s = c % kSlots, to = tmem + 128 * (c & 1);
-      if (!dbg_ok(tmem_cols_ok(to, kTile, tmem, 512), p.status, 123)) return;
-      if (kFp8) {
-        const uint64_t b = k64 + (s * 2 * kBox >> 4);
+        ++filled;
+        const int32_t seen = seen_by_all(p, g);
+        uint32_t first[4][4];
 #pragma unroll
-        for (int kk = 0; kk < HD / 32; ++kk)
-          umma_e4m3_ss_warp(to, q64 + 2 * kk, b + 2 * kk, kIdescQK8, kk > 0);
-      } else {
-        const uint32_t b = dk + (s * 2 * kBox >> 4);
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * kBox + 32 * (kk & 3)) >> 4;
-          umma_bf16_ss_lo_warp(to, dq + off, b + off, dhi, kIdescQK, kk > 0);
-        }
-      }
-    };
-    auto pv = [&](uint32_t c, bool accumulate) {
-      const uint32_t b = dv + ((c % kSlots) * 4 * kBox >> 4), from = tmem + 128 * (c & 1);
-      if (!dbg_ok(tmem_cols_ok(tmem + kTmO, DV, tmem, 512), p.status, 124)) return;
-#pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk)
-        umma_bf16_ts_lo_warp(tmem + kTmO, from + kk * 8 + (kk >= 4 ? 32 : 0), b + 128 * kk, dhi,
-                             kIdescPV, (accumulate || kk > 0) ? 1u : 0u);
-    };
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-      return mbar_wait_warp(bar, parity, abort_flag, kWaitNs);
-    };
-    bool ok = true;
-    uint32_t c = 0, filled = 0;
-    for (uint32_t n = 0; ok; ++n) {
-      const int r = n % kSegRing;
-      if (!(ok = wait(&ctrl->seg_full[r], (n / kSegRing) & 1))) break;
-      const int32_t flags = ctrl->seg[r].flags, tiles = ctrl->seg[r].tiles;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctrl->seg_empty[r]);
-      if (flags & kStop) break;
-      if (flags & kEmpty) continue;
-      if (!(ok = wait(&ctrl->q_full, filled & 1))) break;
-      // S one tile ahead of P V, into the S that P V before last has read.
-      const auto next_s = [&](int32_t t) {
-        const uint32_t cc = c + t;
-        if (!wait(&ctrl->k_full[cc % kSlots], (cc / kSlots) & 1)) return false;
-        tc_fence_after_sync();
-        qk(cc);
-        umma_commit_warp(&ctrl->s_full[cc & 1]);
-        umma_commit_warp(&ctrl->k_empty[cc % kSlots]);
-        if (t == tiles - 1) umma_commit_warp(&ctrl->q_empty);
-        return true;
-      };
-      if (!(ok = next_s(0))) break;
-      for (int32_t t = 0; t < tiles; ++t) {
-        const uint32_t cc = c + t;
-        if (t + 1 < tiles && !(ok = next_s(t + 1))) break;
-        if (!(ok = wait(&ctrl->v_fixed[cc % kSlots], (cc / kSlots) & 1))) break;
-        if (!(ok = wait(&ctrl->p_ready[cc & 1], (cc >> 1) & 1))) break;
-        if (t == 0 && filled > 0 && !(ok = wait(&ctrl->o_free, (filled - 1) & 1))) break;
-        tc_fence_after_sync();
-        pv(cc, t > 0);
-        umma_commit_warp(&ctrl->v_empty[cc % kSlots]);
-        umma_commit_warp(&ctrl->pv_done);
-      }
-      if (!ok) break;
-      umma_commit_warp(&ctrl->o_done);
-      c += tiles;
-      ++filled;
-    }
-    umma_commit_warp(&ctrl->drain);
-    drain_wait(&ctrl->drain, 0);
-    __syncwarp();
-  } else {
-    // --------------------------------------------------------------- softmax
-    const int sw = warp - 4;
-    const int quarter = warp & 3;
-    const int hl = lane & 15, hc = lane >> 4;
-    const int warp_row = quarter * 32 + (sw >> 2) * 16, r = warp_row + hl;
-    const int key0 = 64 * hc;
-    const uint32_t lane_addr = static_cast<uint32_t>(warp_row) << 16;
-    const uint32_t t_o = tmem + lane_addr + kTmO;
-    const float sl2 = p.scale_log2;
-    const int32_t token = p.by_group.div(r), head = r - token * p.group;
-    const uint32_t peer_xch = peer_address(&ctrl->xch[0][0], map ^ 1);
-    const uint32_t peer_bar = peer_address(&ctrl->peer[0], map ^ 1);
-    uint32_t c = 0, filled = 0, direct = 0, handed = 0;
-    // Hands over what this CTA's threads have written for the other, and takes what that one has.
-    const auto exchange = [&]() {
-      named_barrier_sync(1, kSoftmax);
-      if (threadIdx.x == 128) peer_arrive(peer_bar + 8 * (handed & 1));
-      const bool ok = peer_wait(&ctrl->peer[handed & 1], (handed >> 1) & 1, abort_flag);
-      ++handed;
-      return ok;
-    };
-    for (uint32_t n = 0;; ++n) {
-      const int ring = n % kSegRing;
-      if (!mbar_wait_warp(&ctrl->seg_full[ring], (n / kSegRing) & 1, abort_flag, kWaitNs)) break;
-      const Segment *g = &ctrl->seg[ring];
-      const int32_t flags = g->flags;
-      if (flags & kStop) break;
-      const int32_t tiles = g->tiles, rows = g->tokens * p.group;
-      const int32_t pos = g->first + token;
-      const int32_t h = g->hk * p.group + head;
-      const bool live = warp_row < rows;
-      const int32_t lim0 =
-          (p.causal ? min(max(pos, 0), g->len - 1) : g->len - 1) - g->tile0 * kTile;
-      float coef = r < rows ? (map ? -p.lambda[h] : 1.f) : 0.f;
-      float m_run = -INFINITY, l_run = 0.f;
-      bool ok = true;
-      if (!(flags & kEmpty)) {
-        for (int32_t t = 0; t < tiles; ++t, ++c) {
-          const uint32_t t_s = tmem + lane_addr + 128 * (c & 1);
-          ok = mbar_wait_warp(&ctrl->s_full[c & 1], (c >> 1) & 1, abort_flag, kWaitNs);
-          if (!ok) break;
-          if (live) {
-            tc_fence_after_sync();
-            const int lim = lim0 - t * kTile;
-            const bool masked = __any_sync(0xffffffffu, lim < kTile - 1);
-            if (!dbg_ok_warp(tmem_range_ok(t_s, kTile, tmem, 512, warp, 16) &&
-                                 tmem_range_ok(t_o, DV, tmem, 512, warp, 16),
-                             p.status, 125)) {
-              ok = false;
-              break;
-            }
-            uint32_t pk[kTile / 4];
-            float tile_sum = 0.f;
-            bool exact = t == 0;
-            if (!exact) {
-              tile_sum = masked ? softmax_half_exp<true>(t_s, key0, m_run, sl2, lim, pk)
-                                : softmax_half_exp<false>(t_s, key0, m_run, sl2, lim, pk);
-              exact = __any_sync(0xffffffffu, !(tile_sum <= CERT_SUM));
-            }
-            if (exact) {
-              float mt = masked ? softmax_half_max<true>(t_s, key0, lim)
-                                : softmax_half_max<false>(t_s, key0, lim);
-              mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-              const float m_new = fmaxf(m_run, mt * sl2 + M_HEADROOM);
-              float alpha = 1.f;
-              if (t == 0) {
-                m_run = m_new;
-              } else if (m_new > m_run) {
-                alpha = ex2_approx(m_run - m_new);
-                m_run = m_new;
+          for (int i = 0; i < 4; ++i) first[k][i] = 0xFFFFFFFFu;
+        bool ok = true;
+        // (Every value tile passes here, so that neither this warp nor the products can get a whole
+        // turn of the ring ahead of the other.)
+        for (int32_t t = g.tile0; t < g.tile0 + g.tiles; ++t, ++tiles) {
+          const int s = tiles % kSlots;
+          if (!(ok = mbar_wait_warp(&ctrl->v_full[s], (tiles / kSlots) & 1, abort_flag, kWaitNs)))
+            break;
+          if (t * kTile + kTile - 1 > seen) {
+            fix_values<4>(smem + kValues + s * 4 * kBox, t * kTile, seen, g.len, first);
+            if (t == g.tile0 + g.tiles - 1) {
+              if (merge_first<4>(first)) {
+                // (Two segments back the columns have been read.)
+                if (n >= 2 && !(ok = mbar_wait_warp(&ctrl->seg_empty[(n - 2) % kSegRing],
+                                                    ((n - 2) / kSegRing) & 1, abort_flag, kWaitNs)))
+                  break;
+                store_first<4>(first, ctrl->column[n & 1]);
+                if (lane == 0) ctrl->unclean[r] = 1;
               }
-              if (__any_sync(0xffffffffu, alpha != 1.f)) {
-                // (S of this tile was made behind the product before last; the last one's end is
-                // awaited here.)
-                if (!(ok = mbar_wait_warp(&ctrl->pv_done, (c - 1) & 1, abort_flag, kWaitNs))) break;
-                tc_fence_after_sync();
-#pragma unroll 1
-                for (int c0 = 0; c0 < 4; ++c0) {
-                  const uint32_t at = t_o + 128 * (c0 >> 1) + 32 * (c0 & 1);
-                  uint32_t o[32];
-                  tmem_ld16_x32(at, o);
-#pragma unroll
-                  for (int i = 0; i < 32; i += 2) {
-                    const float2 v = __fmul2_rn(
-                        make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
-                        make_float2(alpha, alpha));
-                    o[i] = __float_as_uint(v.x);
-                    o[i + 1] = __float_as_uint(v.y);
-                  }
-                  tmem_st16_x32(at, o);
-                }
-              }
-              l_run *= alpha;
-              const float m_use = m_run == -INFINITY ? 0.f : m_run;
-              tile_sum = masked ? softmax_half_exp<true>(t_s, key0, m_use, sl2, lim, pk)
-                                : softmax_half_exp<false>(t_s, key0, m_use, sl2, lim, pk);
             }
-            l_run += tile_sum;
-            tmem_st16_x32(t_s, pk);
-            tmem_st_wait();
-            tc_fence_before_sync();
+            fence_async_proxy();
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ctrl->p_ready[c & 1]);
+          if (lane == 0) mbar_arrive(&ctrl->v_fixed[s]);
         }
-        if (ok) ok = mbar_wait_warp(&ctrl->o_done, filled & 1, abort_flag, kWaitNs);
-        const float l_row = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
-        if (named_barrier_or(1, kSoftmax, !ok || *abort_flag != 0)) break;
-        tc_fence_after_sync();
-        ++filled;
-        if (!(flags & kDirect)) {
-          // A part: O column by column, the reference and the sum.
-          float *part = p.part + (g->slot * 2ll + map) * part_floats(DV);
-          const bool unclean = ctrl->unclean[ring] != 0;
-          const int32_t far = pos - seen_by_all(p, *g);
-          const bool mine = r < rows;
-#pragma unroll 1
-          for (int c0 = 0; c0 < 4; ++c0) {
-            const int col = 128 * (c0 >> 1) + 32 * (c0 & 1);
-            uint32_t v[32];
-            tmem_ld16_x32(t_o + col, v);
-            if (mine) {
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->seg_empty[r]);
+      }
+      if (lane == 0 && filled > 0) drain_wait(&ctrl->q_full, (filled - 1) & 1);
+      __syncwarp();
+    } else {
+      // --------------------------------------------------------------- products
+      constexpr uint32_t kIdescQK = idesc_bf16_f32(kTile, kTile, false);
+      constexpr uint32_t kIdescQK8 = idesc_e4m3_f32(kTile, kTile);
+      constexpr uint32_t kIdescPV = idesc_bf16_f32(kTile, DV, true);
+      const uint64_t q64 = smem_desc_sw128(smem_u32(smem + kQ), 16, 1024);
+      const uint64_t k64 = smem_desc_sw128(smem_u32(smem + kKeys), 16, 1024);
+      const uint32_t dhi = static_cast<uint32_t>(q64 >> 32);
+      const uint32_t dq = static_cast<uint32_t>(q64), dk = static_cast<uint32_t>(k64);
+      const uint32_t dv =
+          static_cast<uint32_t>(smem_desc_sw128(smem_u32(smem + kValues), kBox, 1024));
+      auto qk = [&](uint32_t c) {  // S of key tile c
+        const uint32_t s = c % kSlots, to = tmem + 128 * (c & 1);
+        if (!dbg_ok(tmem_cols_ok(to, kTile, tmem, 512), p.status, 123)) return;
+        if (kFp8) {
+          const uint64_t b = k64 + (s * 2 * kBox >> 4);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                float x = __uint_as_float(v[i]);
-                if (unclean && ctrl->column[n & 1][key0 + col + i] <= far) x = NAN;
-                part[(key0 + col + i) * kTile + r] = x;
+          for (int kk = 0; kk < HD / 32; ++kk)
+            umma_e4m3_ss_warp(to, q64 + 2 * kk, b + 2 * kk, kIdescQK8, kk > 0);
+        } else {
+          const uint32_t b = dk + (s * 2 * kBox >> 4);
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * kBox + 32 * (kk & 3)) >> 4;
+            umma_bf16_ss_lo_warp(to, dq + off, b + off, dhi, kIdescQK, kk > 0);
+          }
+        }
+      };
+      auto pv = [&](uint32_t c, bool accumulate) {
+        const uint32_t b = dv + ((c % kSlots) * 4 * kBox >> 4), from = tmem + 128 * (c & 1);
+        if (!dbg_ok(tmem_cols_ok(tmem + kTmO, DV, tmem, 512), p.status, 124)) return;
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          umma_bf16_ts_lo_warp(tmem + kTmO, from + kk * 8 + (kk >= 4 ? 32 : 0), b + 128 * kk, dhi,
+                               kIdescPV, (accumulate || kk > 0) ? 1u : 0u);
+      };
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        return mbar_wait_warp(bar, parity, abort_flag, kWaitNs);
+      };
+      bool ok = true;
+      uint32_t c = 0, filled = 0;
+      for (uint32_t n = 0; ok; ++n) {
+        const int r = n % kSegRing;
+        if (!(ok = wait(&ctrl->seg_full[r], (n / kSegRing) & 1))) break;
+        const int32_t flags = ctrl->seg[r].flags, tiles = ctrl->seg[r].tiles;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->seg_empty[r]);
+        if (flags & kStop) break;
+        if (flags & kEmpty) continue;
+        if (!(ok = wait(&ctrl->q_full, filled & 1))) break;
+        // S one tile ahead of P V, into the S that P V before last has read.
+        const auto next_s = [&](int32_t t) {
+          const uint32_t cc = c + t;
+          if (!wait(&ctrl->k_full[cc % kSlots], (cc / kSlots) & 1)) return false;
+          tc_fence_after_sync();
+          qk(cc);
+          umma_commit_warp(&ctrl->s_full[cc & 1]);
+          umma_commit_warp(&ctrl->k_empty[cc % kSlots]);
+          if (t == tiles - 1) umma_commit_warp(&ctrl->q_empty);
+          return true;
+        };
+        if (!(ok = next_s(0))) break;
+        for (int32_t t = 0; t < tiles; ++t) {
+          const uint32_t cc = c + t;
+          if (t + 1 < tiles && !(ok = next_s(t + 1))) break;
+          if (!(ok = wait(&ctrl->v_fixed[cc % kSlots], (cc / kSlots) & 1))) break;
+          if (!(ok = wait(&ctrl->p_ready[cc & 1], (cc >> 1) & 1))) break;
+          if (t == 0 && filled > 0 && !(ok = wait(&ctrl->o_free, (filled - 1) & 1))) break;
+          tc_fence_after_sync();
+          pv(cc, t > 0);
+          umma_commit_warp(&ctrl->v_empty[cc % kSlots]);
+          umma_commit_warp(&ctrl->pv_done);
+        }
+        if (!ok) break;
+        umma_commit_warp(&ctrl->o_done);
+        c += tiles;
+        ++filled;
+      }
+      umma_commit_warp(&ctrl->drain);
+      drain_wait(&ctrl->drain, 0);
+      __syncwarp();
+    }
+  } else {
+    setmaxnreg_inc<kRegsRest>();
+    if (warp < kFinishWarp) {
+      // --------------------------------------------------------------- softmax
+      const int sw = warp - kSoftmaxWarp;
+      const int hl = lane & 15, hc = lane >> 4;
+      const int warp_row = (warp & 3) * 32 + (sw >> 2) * 16, r = warp_row + hl;
+      const int key0 = 64 * hc;
+      const uint32_t lane_addr = static_cast<uint32_t>(warp_row) << 16;
+      const uint32_t t_o = tmem + lane_addr + kTmO;
+      const float sl2 = p.scale_log2;
+      const int32_t token = p.by_group.div(r);
+      uint32_t c = 0, filled = 0;
+      for (uint32_t n = 0;; ++n) {
+        const int ring = n % kSegRing;
+        if (!mbar_wait_warp(&ctrl->seg_full[ring], (n / kSegRing) & 1, abort_flag, kWaitNs)) break;
+        const Segment *g = &ctrl->seg[ring];
+        const int32_t flags = g->flags;
+        if (flags & kStop) break;
+        if (!(flags & kEmpty)) {
+          const int32_t tiles = g->tiles, rows = g->tokens * p.group;
+          const bool live = warp_row < rows;
+          const int32_t lim0 =
+              (p.causal ? min(max(g->first + token, 0), g->len - 1) : g->len - 1) - g->tile0 * kTile;
+          float m_run = -INFINITY, l_run = 0.f;
+          bool ok = true;
+          for (int32_t t = 0; t < tiles; ++t, ++c) {
+            const uint32_t t_s = tmem + lane_addr + 128 * (c & 1);
+            ok = mbar_wait_warp(&ctrl->s_full[c & 1], (c >> 1) & 1, abort_flag, kWaitNs);
+            if (!ok) break;
+            if (live) {
+              tc_fence_after_sync();
+              const int lim = lim0 - t * kTile;
+              const bool masked = __any_sync(0xffffffffu, lim < kTile - 1);
+              if (!dbg_ok_warp(tmem_range_ok(t_s, kTile, tmem, 512, warp, 16) &&
+                                   tmem_range_ok(t_o, DV, tmem, 512, warp, 16),
+                               p.status, 125)) {
+                ok = false;
+                break;
               }
+              uint32_t pk[kTile / 4];
+              float tile_sum = 0.f;
+              bool exact = t == 0;
+              if (!exact) {
+                tile_sum = masked ? softmax_half_exp<true>(t_s, key0, m_run, sl2, lim, pk)
+                                  : softmax_half_exp<false>(t_s, key0, m_run, sl2, lim, pk);
+                exact = __any_sync(0xffffffffu, !(tile_sum <= CERT_SUM));
+              }
+              if (exact) {
+                float mt = masked ? softmax_half_max<true>(t_s, key0, lim)
+                                  : softmax_half_max<false>(t_s, key0, lim);
+                mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+                const float m_new = fmaxf(m_run, mt * sl2 + M_HEADROOM);
+                float alpha = 1.f;
+                if (t == 0) {
+                  m_run = m_new;
+                } else if (m_new > m_run) {
+                  alpha = ex2_approx(m_run - m_new);
+                  m_run = m_new;
+                }
+                if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                  // (S of this tile was made behind the product before last; the last one's end is
+                  // awaited here.)
+                  if (!(ok = mbar_wait_warp(&ctrl->pv_done, (c - 1) & 1, abort_flag, kWaitNs))) break;
+                  tc_fence_after_sync();
+#pragma unroll 1
+                  for (int c0 = 0; c0 < 4; ++c0) {
+                    const uint32_t at = t_o + 128 * (c0 >> 1) + 32 * (c0 & 1);
+                    uint32_t o[32];
+                    tmem_ld16_x32(at, o);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                      const float2 v = __fmul2_rn(
+                          make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
+                          make_float2(alpha, alpha));
+                      o[i] = __float_as_uint(v.x);
+                      o[i + 1] = __float_as_uint(v.y);
+                    }
+                    tmem_st16_x32(at, o);
+                  }
+                }
+                l_run *= alpha;
+                const float m_use = m_run == -INFINITY ? 0.f : m_run;
+                tile_sum = masked ? softmax_half_exp<true>(t_s, key0, m_use, sl2, lim, pk)
+                                  : softmax_half_exp<false>(t_s, key0, m_use, sl2, lim, pk);
+              }
+              l_run += tile_sum;
+              tmem_st16_x32(t_s, pk);
+              tmem_st_wait();
+              tc_fence_before_sync();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctrl->p_ready[c & 1]);
+          }
+          if (!ok) break;
+          const float l_row = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
+          if (hc == 0) {
+            // (The row's last sum but one has been read: the first product behind it awaited that.)
+            ctrl->inv[filled & 1][r] = 1.f / l_row;
+            if (!(flags & kDirect) && r < rows) {
+              float *part = p.part + (g->slot * 2ll + map) * part_floats(DV) + r;
+              part[DV * kTile] = m_run;
+              part[(DV + 1) * kTile] = ctrl->bad[ring] ? NAN : l_row;
             }
           }
-          if (mine && hc == 0) {
-            part[DV * kTile + r] = m_run;
-            part[(DV + 1) * kTile + r] = ctrl->bad[ring] ? NAN : l_row;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctrl->l_full[filled & 1]);
+          ++filled;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->seg_empty[ring]);
+      }
+    } else {
+      // --------------------------------------------------------------- finished items
+      const int fw = warp - kFinishWarp;
+      const int hl = lane & 15, hc = lane >> 4;
+      const int warp_row = (warp & 3) * 32 + (fw >> 2) * 16, r = warp_row + hl;
+      const int key0 = 64 * hc;
+      const uint32_t t_o = tmem + (static_cast<uint32_t>(warp_row) << 16) + kTmO;
+      const int32_t token = p.by_group.div(r), head = r - token * p.group;
+      const uint32_t peer_xch = peer_address(&ctrl->xch[0][0], map ^ 1);
+      const uint32_t peer_bar = peer_address(&ctrl->peer[0], map ^ 1);
+      uint32_t filled = 0, direct = 0, handed = 0;
+      // Hands over what this CTA's threads have written for the other, and takes what that one has.
+      const auto exchange = [&]() {
+        named_barrier_sync(1, kFinish);
+        if (threadIdx.x == 32 * kFinishWarp) peer_arrive(peer_bar + 8 * (handed & 1));
+        const bool ok = peer_wait(&ctrl->peer[handed & 1], (handed >> 1) & 1, abort_flag);
+        ++handed;
+        return ok;
+      };
+      for (uint32_t n = 0;; ++n) {
+        const int ring = n % kSegRing;
+        if (!mbar_wait_warp(&ctrl->seg_full[ring], (n / kSegRing) & 1, abort_flag, kWaitNs)) break;
+        const Segment *g = &ctrl->seg[ring];
+        const int32_t flags = g->flags;
+        if (flags & kStop) break;
+        const int32_t rows = g->tokens * p.group;
+        const int32_t pos = g->first + token;
+        const int32_t h = g->hk * p.group + head;
+        const bool live = warp_row < rows;
+        float coef = r < rows ? (map ? -p.lambda[h] : 1.f) : 0.f;
+        if (!(flags & kEmpty)) {
+          bool ok = mbar_wait_warp(&ctrl->l_full[filled & 1], (filled >> 1) & 1, abort_flag, kWaitNs);
+          if (ok) ok = mbar_wait_warp(&ctrl->o_done, filled & 1, abort_flag, kWaitNs);
+          if (named_barrier_or(1, kFinish, !ok || *abort_flag != 0)) break;
+          tc_fence_after_sync();
+          coef *= ctrl->bad[ring] ? NAN : ctrl->inv[filled & 1][r];
+          ++filled;
+          if (!(flags & kDirect)) {
+            // A part: O column by column.
+            float *part = p.part + (g->slot * 2ll + map) * part_floats(DV);
+            const bool unclean = ctrl->unclean[ring] != 0;
+            const int32_t far = pos - seen_by_all(p, *g);
+            const bool mine = r < rows;
+#pragma unroll 1
+            for (int c0 = 0; c0 < 4; ++c0) {
+              const int col = 128 * (c0 >> 1) + 32 * (c0 & 1);
+              uint32_t v[32];
+              tmem_ld16_x32(t_o + col, v);
+              if (mine) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  float x = __uint_as_float(v[i]);
+                  if (unclean && ctrl->column[n & 1][key0 + col + i] <= far) x = NAN;
+                  part[(key0 + col + i) * kTile + r] = x;
+                }
+              }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&ctrl->o_free);
+              mbar_arrive(&ctrl->seg_empty[ring]);
+            }
+            continue;
+          }
+        }
+
+        // This thread's columns: 128 map + 64 hc .., of its row.
+        const int col0 = 128 * map + key0;
+        float o[64];
+        if (flags & kEmpty) {
+          const float x = flags & kBadLen ? NAN : 0.f;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) o[i] = x;
+        } else {
+          // [CTA][turn][column of the other's half][row]
+          float *give = p.swap + ((blockIdx.x * 2ll + (direct & 1)) * 128 + key0) * kTile + r;
+          const float *take =
+              p.swap + (((blockIdx.x ^ 1) * 2ll + (direct & 1)) * 128 + key0) * kTile + r;
+          ++direct;
+#pragma unroll
+          for (int c0 = 0; c0 < 64; c0 += 32) {
+            uint32_t v[32];
+            tmem_ld16_x32(t_o + 128 * (map ^ 1) + c0, v);
+            if (live)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) give[(c0 + i) * kTile] = __uint_as_float(v[i]) * coef;
+          }
+#pragma unroll
+          for (int c0 = 0; c0 < 64; c0 += 32) {
+            uint32_t v[32];
+            tmem_ld16_x32(t_o + 128 * map + c0, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[c0 + i] = __uint_as_float(v[i]) * coef;
           }
           tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&ctrl->o_free);
-            mbar_arrive(&ctrl->seg_empty[ring]);
-          }
-          continue;
-        }
-        coef = ctrl->bad[ring] ? NAN : coef / l_row;
-      }
-
-      // ------------------------------------------------------------- the rows of a whole item
-      // This thread's columns: 128 map + 64 hc .., of its row.
-      const int col0 = 128 * map + key0;
-      float o[64];
-      if (flags & kEmpty) {
-        const float x = flags & kBadLen ? NAN : 0.f;
+          if (lane == 0) mbar_arrive(&ctrl->o_free);
+          bool fine = exchange();
+          if (live) {
+            // Sixteen on their way at a time: there are no registers for more beside o.
 #pragma unroll
-        for (int i = 0; i < 64; ++i) o[i] = x;
-      } else {
-        // [CTA][turn][column of the other's half][row]
-        float *give = p.swap + ((blockIdx.x * 2ll + (direct & 1)) * 128 + key0) * kTile + r;
-        const float *take =
-            p.swap + (((blockIdx.x ^ 1) * 2ll + (direct & 1)) * 128 + key0) * kTile + r;
-        ++direct;
+            for (int i0 = 0; i0 < 64; i0 += 16) {
+              float x[16];
 #pragma unroll
-        for (int c0 = 0; c0 < 64; c0 += 32) {
-          uint32_t v[32];
-          tmem_ld16_x32(t_o + 128 * (map ^ 1) + c0, v);
-          if (live)
+              for (int i = 0; i < 16; ++i) x[i] = __ldcg(take + (i0 + i) * kTile);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) give[(c0 + i) * kTile] = __uint_as_float(v[i]) * coef;
-        }
-#pragma unroll
-        for (int c0 = 0; c0 < 64; c0 += 32) {
-          uint32_t v[32];
-          tmem_ld16_x32(t_o + 128 * map + c0, v);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[c0 + i] = __uint_as_float(v[i]) * coef;
-        }
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctrl->o_free);
-        bool fine = exchange();
-        if (live)
-#pragma unroll
-          for (int i = 0; i < 64; ++i) o[i] += __ldcg(take + i * kTile);
-        if (ctrl->unclean[ring]) {
-          const int32_t far = pos - seen_by_all(p, *g);
-#pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (ctrl->column[n & 1][col0 + i] <= far) o[i] = NAN;
-        }
-        if (p.headnorm) {
-          // The sum over the row of both CTAs' threads.
-          const auto row_sum = [&](float x) {
-            x += __shfl_xor_sync(0xffffffffu, x, 16);
-            const uint32_t turn = handed & 1;
-            if (hc == 0) peer_store(peer_xch + 4 * (turn * kTile + r), x);
-            fine &= exchange();
-            return x + ctrl->xch[turn][r];
-          };
-          if (p.headnorm == 2) {
-            float sm = 0.f;
-#pragma unroll
-            for (int i = 0; i < 64; ++i) sm += o[i];
-            const float mu = row_sum(sm) * (1.f / DV);
-#pragma unroll
-            for (int i = 0; i < 64; ++i) o[i] -= mu;
-          }
-          float ss = 0.f;
-#pragma unroll
-          for (int i = 0; i < 64; ++i) ss = fmaf(o[i], o[i], ss);
-          const float rr = rsqrtf(row_sum(ss) * (1.f / DV) + p.eps) * p.out_scale;
-          if (p.norm_w != nullptr && r < rows) {
-            const float4 *w4 = reinterpret_cast<const float4 *>(p.norm_w + h * DV + col0);
-#pragma unroll
-            for (int i = 0; i < 64; i += 4) {
-              const float4 w = w4[i / 4];
-              o[i] *= rr * w.x;
-              o[i + 1] *= rr * w.y;
-              o[i + 2] *= rr * w.z;
-              o[i + 3] *= rr * w.w;
+              for (int i = 0; i < 16; ++i) o[i0 + i] += x[i];
+              asm volatile("" ::: "memory");
             }
-          } else {
+          }
+          if (ctrl->unclean[ring]) {
+            const int32_t far = pos - seen_by_all(p, *g);
 #pragma unroll
-            for (int i = 0; i < 64; ++i) o[i] *= rr;
+            for (int i = 0; i < 64; ++i)
+              if (ctrl->column[n & 1][col0 + i] <= far) o[i] = NAN;
+          }
+          if (p.headnorm) {
+            // The sum over the row of both CTAs' threads.
+            const auto row_sum = [&](float x) {
+              x += __shfl_xor_sync(0xffffffffu, x, 16);
+              const uint32_t turn = handed & 1;
+              if (hc == 0) peer_store(peer_xch + 4 * (turn * kTile + r), x);
+              fine &= exchange();
+              return x + ctrl->xch[turn][r];
+            };
+            if (p.headnorm == 2) {
+              float sm = 0.f;
+#pragma unroll
+              for (int i = 0; i < 64; ++i) sm += o[i];
+              const float mu = row_sum(sm) * (1.f / DV);
+#pragma unroll
+              for (int i = 0; i < 64; ++i) o[i] -= mu;
+            }
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < 64; ++i) ss = fmaf(o[i], o[i], ss);
+            const float rr = rsqrtf(row_sum(ss) * (1.f / DV) + p.eps) * p.out_scale;
+            if (p.norm_w != nullptr && r < rows) {
+              const float4 *w4 = reinterpret_cast<const float4 *>(p.norm_w + h * DV + col0);
+#pragma unroll
+              for (int i = 0; i < 64; i += 4) {
+                const float4 w = w4[i / 4];
+                o[i] *= rr * w.x;
+                o[i + 1] *= rr * w.y;
+                o[i + 2] *= rr * w.z;
+                o[i + 3] *= rr * w.w;
+                if (i % 16 == 12) asm volatile("" ::: "memory");
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) o[i] *= rr;
+            }
+          }
+          if (pos < 0) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) o[i] = 0.f;
+          }
+          if (named_barrier_or(1, kFinish, !fine)) break;
+        }
+        if (live) {
+          uint4 pkt[8];
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            pkt[v] = make_uint4(
+                pack_bf16x2(o[8 * v], o[8 * v + 1]), pack_bf16x2(o[8 * v + 2], o[8 * v + 3]),
+                pack_bf16x2(o[8 * v + 4], o[8 * v + 5]), pack_bf16x2(o[8 * v + 6], o[8 * v + 7]));
+          transpose8_chunks(pkt, lane);
+          const int32_t r0 = r - (lane & 7);
+          __nv_bfloat16 *out =
+              p.out + g->row * p.out_n + g->hk * p.group * p.out_h + col0 + 8 * (lane & 7);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int32_t i = p.by_group.div(r0 + j);
+            if (r0 + j < rows && dbg_ok(g->row + i < p.N, p.status, 126))
+              *reinterpret_cast<uint4 *>(out + i * p.out_n + (r0 + j - i * p.group) * p.out_h) = pkt[j];
           }
         }
-        if (pos < 0) {
-#pragma unroll
-          for (int i = 0; i < 64; ++i) o[i] = 0.f;
-        }
-        if (named_barrier_or(1, kSoftmax, !fine)) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->seg_empty[ring]);
       }
-      if (live) {
-        uint4 pkt[8];
-#pragma unroll
-        for (int v = 0; v < 8; ++v)
-          pkt[v] = make_uint4(
-              pack_bf16x2(o[8 * v], o[8 * v + 1]), pack_bf16x2(o[8 * v + 2], o[8 * v + 3]),
-              pack_bf16x2(o[8 * v + 4], o[8 * v + 5]), pack_bf16x2(o[8 * v + 6], o[8 * v + 7]));
-        transpose8_chunks(pkt, lane);
-        const int32_t r0 = r - (lane & 7);
-        __nv_bfloat16 *out =
-            p.out + g->row * p.out_n + g->hk * p.group * p.out_h + col0 + 8 * (lane & 7);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int32_t i = p.by_group.div(r0 + j);
-          if (r0 + j < rows && dbg_ok(g->row + i < p.N, p.status, 126))
-            *reinterpret_cast<uint4 *>(out + i * p.out_n + (r0 + j - i * p.group) * p.out_h) = pkt[j];
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctrl->seg_empty[ring]);
     }
-  }
 
+  }
   tc_fence_before_sync();
   __syncthreads();
   if (warp == kMmaWarp) {

@@ -121,7 +121,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
   ShareState *state = reinterpret_cast<ShareState *>(ctrl->xch);
   tc_fence_before_sync();
-  const Line line = find_share<kThreads>(p, share, state);
+  Line line;
+  if (p.B > kFewSequences)
+    line = find_share<kThreads>(p, share, state);
+  else
+    __syncthreads();
   tc_fence_after_sync();
   grid_dependents_launch();
   const uint32_t tmem = ctrl->tmem;
@@ -133,7 +137,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------- keys, and the segments
       const int box = lane & 1, piece = lane >> 1, row0 = piece * p.piece_rows;
       const bool piece_ok = row0 < kTile;
-      Walk w(p, line, share, *state);
+      ShareState few;
+      if (p.B <= kFewSequences) line = find_share_few(p, share, &few);
+      Walk w(p, line, share, p.B <= kFewSequences ? few : *state);
       Ring<kSlots> ring;
       RaggedJoin join = {};
       uint32_t n = 0;
