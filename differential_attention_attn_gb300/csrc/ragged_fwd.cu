@@ -197,7 +197,7 @@ RaggedFwdPlan plan_ragged_fwd(const diffattn_desc &desc, const diffpaged_cache &
   q.shares = desc.d == 64 ? sm_count : sm_count / 2;
   // Items this short are never cut (cut_line).
   const int64_t units = (cache.max_pages * cache.page_size + kTile - 1) / kTile;
-  q.joins = units + kItemCost > kJoinSteps;
+  q.joins = kItemSteps + units * kTileSteps > kJoinSteps;
   size_t at = 0;
   const auto take = [&at](size_t bytes) {
     const size_t here = at;
@@ -241,6 +241,9 @@ diffattn_status launch_ragged_fwd(const diffattn_desc &desc, const diffpaged_cac
   p.kv_heads = static_cast<int32_t>(cache.kv_heads);
   p.group = static_cast<int32_t>(desc.H / cache.kv_heads);
   p.tokens = kTile / p.group;
+  p.group_bits = -1;
+  for (int k = 0; k <= 6; ++k)
+    if (p.group == 1 << k) p.group_bits = k;
   p.num_pages = static_cast<int32_t>(cache.num_pages);
   p.max_pages = static_cast<int32_t>(cache.max_pages);
   p.page_size = cache.page_size;

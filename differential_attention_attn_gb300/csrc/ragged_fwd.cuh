@@ -11,13 +11,15 @@
 // running reference and sum, so that ranges of an item's keys done by different
 // CTAs join exactly: with M = max m_s, O = sum_s 2^(m_s - M) O_s, l alike.
 //
-// How the work is cut.  All items lie on a line, each kItemCost steps that stand
-// for its epilogue, then a step for each key tile, and every share (a CTA, or a
-// pair of them) takes an equal piece of it, found from q_start and kv_len on the
+// How the work is cut.  All items lie on a line, each some steps that stand for
+// its end, then some for each key tile (a step is about 0.27 us; a tile of a few
+// rows leaves most softmax warps idle and takes less), and every share (a CTA, or
+// a pair of them) takes an equal piece of it, found from q_start and kv_len on the
 // device: a batch of prompts, chunks and single tokens is balanced, and a
-// captured graph replays with others.  Items that a border cuts leave partial
-// states that a second kernel joins.  Where cutting gains less than that costs,
-// shares take whole items (see cut_line).
+// captured graph replays with others.  A tile belongs to the share with its first
+// step.  Items that a border cuts leave partial states that a second kernel
+// joins.  Where cutting gains less than that costs, shares take whole items (see
+// cut_line).
 #pragma once
 
 #include <cuda.h>
@@ -53,6 +55,7 @@ struct RaggedParams {
   int32_t B, N, kv_heads, group, tokens;  // N: packed rows; tokens: of a tile, 128 / group
   int32_t num_pages, max_pages, page_size, piece_rows;
   int32_t causal, headnorm, shares;
+  int32_t group_bits;  // group = 2^group_bits, or -1
   FastDiv by_page, by_group, by_tokens;
   float eps, out_scale, scale_log2;
 };
@@ -106,9 +109,11 @@ __host__ __device__ constexpr int64_t part_floats(int dv) { return (dv + 2) * 12
 namespace {
 
 constexpr int kTile = 128;  // keys of a tile, and rows
-constexpr int kItemCost = 2;
-// Steps that leaving parts and joining them costs a call, about.
-constexpr int kJoinSteps = 8;
+// Steps, measured at d = 64: a tile takes 1.37 us with 128 rows and 1.08 us with up to 16 (one warp
+// of eight has rows), an item 4 us beside its tiles.
+constexpr int kTileSteps = 5, kFewSteps = 4, kFewRows = 16, kItemSteps = 15;
+// What leaving parts and joining them costs a call, about, and the least that a share is cut to.
+constexpr int kJoinSteps = 40, kLeastSteps = 3 * kTileSteps;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr int kSegRing = 4;
@@ -157,6 +162,12 @@ __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a,
   }
 }
 
+// sum_{i < x} floor(i / 2^k)
+__device__ __forceinline__ int64_t step_sum(uint32_t x, uint32_t k) {
+  const uint32_t q = x >> k, r = x & ((1u << k) - 1);
+  return ((static_cast<int64_t>(q) * q - q) >> 1 << k) + static_cast<int64_t>(q) * r;
+}
+
 // A sequence's new tokens, in tiles of rows, and the steps of these.
 struct Seq {
   int32_t row, n, len, first, tiles;  // first: position of its first new token; tiles of rows
@@ -173,7 +184,8 @@ struct Seq {
     first = len - n;
     tiles = p.by_tokens.div(n + p.tokens - 1);
   }
-  // Keys that tile q of rows sees, and key tiles (one for a tile that only has rows to write).
+  // Keys that tile q of rows sees, key tiles (one for a tile that only has rows to write), and the
+  // steps of each.
   __device__ __forceinline__ int32_t keys(const RaggedParams &p, int32_t q) const {
     const int32_t last = first + min((q + 1) * p.tokens, n) - 1;
     return last < 0 ? 0 : p.causal ? last + 1 : len;
@@ -181,22 +193,35 @@ struct Seq {
   __device__ __forceinline__ int32_t units(const RaggedParams &p, int32_t q) const {
     return max(1, (keys(p, q) + kTile - 1) / kTile);
   }
+  __device__ __forceinline__ int32_t weight(const RaggedParams &p, int32_t q) const {
+    return (n - q * p.tokens) * p.group > kFewRows ? kTileSteps : kFewSteps;
+  }
+  __device__ __forceinline__ int32_t longest(const RaggedParams &p) const {
+    return n > 0 ? kItemSteps + units(p, tiles - 1) * kTileSteps : 0;
+  }
   // Steps of tiles 0 .. q - 1 of rows.
   __device__ __forceinline__ int64_t steps(const RaggedParams &p, int32_t q) const {
     const int32_t whole = min(q, tiles - 1);  // tiles with all their tokens
-    int64_t s = static_cast<int64_t>(q) * kItemCost;
+    int64_t s = 0;
     if (whole > 0) {
       const int32_t idle = first < 0 ? min(whole, p.by_tokens.div(-first)) : 0;
-      s += idle;
-      if (p.causal) {
-        s += whole - idle;
-        if (whole > idle)
-          s += floor_sum(whole - idle, kTile, p.tokens, first + (idle + 1) * p.tokens - 1);
+      s = whole;
+      if (p.causal) {  // tile i of the others: (first + (i + 1) tokens - 1) / 128 + 1
+        if (whole > idle) {
+          const uint32_t b = first + (idle + 1) * p.tokens - 1;
+          if (p.group_bits >= 0) {  // tokens = 128 / 2^group_bits
+            const uint32_t c = b >> (7 - p.group_bits);
+            s += step_sum(c + (whole - idle), p.group_bits) - step_sum(c, p.group_bits);
+          } else {
+            s += floor_sum(whole - idle, kTile, p.tokens, b);
+          }
+        }
       } else {
-        s += static_cast<int64_t>(whole - idle) * ((len + kTile - 1) / kTile);
+        s += static_cast<int64_t>(whole - idle) * ((len + kTile - 1) / kTile - 1);
       }
     }
-    if (q > whole) s += units(p, tiles - 1);
+    s = s * kTileSteps + static_cast<int64_t>(q) * kItemSteps;
+    if (q > whole) s += units(p, tiles - 1) * weight(p, tiles - 1);
     return s;
   }
 };
@@ -210,7 +235,11 @@ struct Line {
   }
   __device__ __forceinline__ int64_t share_of(int64_t step) const {
     const int64_t border = more * (each + 1);
-    return step < border ? step / (each + 1) : more + (step - border) / each;
+    const int64_t a = step < border ? step : step - border, b = step < border ? each + 1 : each;
+    const int64_t q = ((a | b) >> 32) == 0
+                          ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
+                          : a / b;
+    return step < border ? q : more + q;
   }
 };
 
@@ -224,16 +253,24 @@ struct ShareState {
 // How a line of `total` steps in `items` items, the longest of `longest` steps, is shared.
 __device__ __forceinline__ Line cut_line(int32_t shares, int64_t total, int64_t items,
                                          int32_t longest) {
+  // (A division of 64 bits is a long way: most lines are short enough for one of 32.)
+  const auto divide = [](int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
+                                : a / b;
+  };
   Line line;
-  line.shares = static_cast<int32_t>(min(static_cast<int64_t>(shares), max(total, int64_t{1})));
-  line.each = total / line.shares;
-  line.more = total - line.each * line.shares;
   // Whole items, one a share, where the longest is not kJoinSteps longer than equal pieces; where
   // there are more of them than shares, equal pieces with the items that begin in each, at most
   // one longer than equal.
-  const int64_t equal = (total + line.shares - 1) / line.shares;
-  line.mode = items <= shares ? (longest <= equal + kJoinSteps ? kWhole : kCut)
+  line.each = divide(total, shares);
+  line.mode = items <= shares ? (longest <= line.each + kJoinSteps ? kWhole : kCut)
                               : (longest <= kJoinSteps ? kUncut : kCut);
+  line.shares = shares;
+  if (line.mode == kCut && line.each < kLeastSteps) {  // a piece holds a tile at least
+    line.shares = max(1, static_cast<int32_t>(total) / kLeastSteps);
+    line.each = divide(total, line.shares);
+  }
+  line.more = total - line.each * line.shares;
   return line;
 }
 
@@ -267,7 +304,7 @@ __device__ __forceinline__ Line find_share_few(const RaggedParams &p, int32_t in
       if (s.n > 0) {
         steps[k] = steps_of(p, s);
         items[k] = static_cast<int64_t>(s.tiles) * p.kv_heads;
-        longest = max(longest, kItemCost + s.units(p, s.tiles - 1));
+        longest = max(longest, s.longest(p));
       }
       if (s.bad_rows && index == 0) report_bad_page(p.status);
     }
@@ -319,7 +356,7 @@ __device__ __forceinline__ Line find_share(const RaggedParams &p, int32_t index,
     }
     total += t;
     items += n;
-    if (s.n > 0) longest = max(longest, kItemCost + s.units(p, s.tiles - 1));
+    longest = max(longest, s.longest(p));
     if (s.bad_rows && index == 0) report_bad_page(p.status);
   }
 #pragma unroll
@@ -373,26 +410,27 @@ __device__ __forceinline__ Line find_share(const RaggedParams &p, int32_t index,
 // A share's walk along its items (one warp, uniform).
 struct Walk {
   Seq s;
-  int32_t b, hk, q, units;
+  int32_t b, hk, q, units, weight;
   int32_t tile;   // the next key tile of the item
-  int64_t end;    // the share's end, in tiles of the item
+  int64_t end;    // the share's end, in steps from the item's first tile
   bool cut;
   __device__ __forceinline__ Walk(const RaggedParams &p, const Line &line, int32_t index,
                                   const ShareState &st)
-      : b(st.b), hk(0), q(0), units(1), tile(0), end(-kItemCost), cut(line.mode == kCut) {
+      : b(st.b), hk(0), q(0), units(1), weight(1), tile(0), end(-kItemSteps),
+        cut(line.mode == kCut) {
     if (b >= p.B) return;
     s = Seq(p, b);
-    const int64_t left = st.left;
+    int64_t rest = st.left;
     if (line.mode == kWhole) {
-      hk = static_cast<int32_t>(left / s.tiles);
-      q = static_cast<int32_t>(left - static_cast<int64_t>(hk) * s.tiles);
-      units = s.units(p, q);
-      end = units;
+      hk = static_cast<int32_t>(rest) / s.tiles;
+      q = static_cast<int32_t>(rest) - hk * s.tiles;
+      item(p);
+      end = static_cast<int64_t>(units) * weight;
       return;
     }
     const int64_t head = s.steps(p, s.tiles);
-    hk = static_cast<int32_t>(left / head);
-    const int64_t rest = left - hk * head;
+    hk = static_cast<int32_t>((rest >> 32) == 0 ? static_cast<uint32_t>(rest) / head : rest / head);
+    rest -= hk * head;
     // The last tile of rows whose steps begin at or before `rest`, 32 candidates at a time.
     int32_t lo = 0, hi = s.tiles;
     while (hi - lo > 1) {
@@ -404,18 +442,22 @@ struct Walk {
       hi = min(hi, lo + step);
     }
     q = lo;
-    units = s.units(p, q);
-    const int64_t off = rest - s.steps(p, q);  // of the share's begin in the item
-    tile = static_cast<int32_t>(max(int64_t{0}, off - kItemCost));
-    end = off + line.each + (index < line.more ? 1 : 0) - kItemCost;
-    if (!cut) {
-      if (off > 0)
-        next(p);
-      else
-        take_whole();
+    item(p);
+    const int64_t off = rest - s.steps(p, q) - kItemSteps;  // of the share's begin from the tiles
+    end = off + line.each + (index < line.more ? 1 : 0);
+    if (cut) {
+      // (`off` is below an item's steps.)
+      tile = off > 0 ? (static_cast<int32_t>(off) + weight - 1) / weight : 0;
+      if (tile == units) next(p);
+    } else if (off > -kItemSteps) {
+      next(p);
+    } else {
+      take_whole();
     }
   }
-  __device__ __forceinline__ bool more(const RaggedParams &p) const { return b < p.B && tile < end; }
+  __device__ __forceinline__ bool more(const RaggedParams &p) const {
+    return b < p.B && static_cast<int64_t>(tile) * weight < end;
+  }
   // The share's part of the item.
   __device__ __forceinline__ Segment segment(const RaggedParams &p, int32_t share) const {
     const int32_t t0 = q * p.tokens;
@@ -427,7 +469,8 @@ struct Walk {
     g.b = b;
     g.hk = hk;
     g.tile0 = tile;
-    g.tiles = static_cast<int32_t>(min(static_cast<int64_t>(units), end)) - tile;
+    const bool all = end > static_cast<int64_t>(units - 1) * weight;
+    g.tiles = (all ? units : (static_cast<int32_t>(end) + weight - 1) / weight) - tile;
     g.flags = (g.tiles == units ? kDirect : 0) | (s.keys(p, q) == 0 ? kEmpty : 0) |
               (s.bad_len ? kBadLen : 0);
     g.slot = 2 * share + (tile == 0 ? 1 : 0);
@@ -435,16 +478,21 @@ struct Walk {
   }
   // Of a cut item that begins in the share.
   __device__ __forceinline__ RaggedJoin join(const Line &line, int32_t share, const Segment &g) const {
-    const int64_t last = line.begin(share + 1) - end + units - 1;  // its last step on the line
+    // The last tile's place on the line.
+    const int64_t last = line.begin(share + 1) - end + static_cast<int64_t>(units - 1) * weight;
     return {static_cast<int32_t>(line.share_of(last)) - share + 1, g.slot, g.hk, g.row, g.tokens,
             g.first, {0, 0}};
   }
+  __device__ __forceinline__ void item(const RaggedParams &p) {
+    units = s.units(p, q);
+    weight = s.weight(p, q);
+  }
   // Uncut: the items that begin in the share are all its own.
   __device__ __forceinline__ void take_whole() {
-    if (!cut && end > -kItemCost) end = max(end, static_cast<int64_t>(units));
+    if (!cut && end > -kItemSteps) end = max(end, static_cast<int64_t>(units) * weight);
   }
   __device__ __forceinline__ void next(const RaggedParams &p) {
-    end -= units + kItemCost;
+    end -= static_cast<int64_t>(units) * weight + kItemSteps;
     tile = 0;
     if (++q == s.tiles) {
       q = 0;
@@ -452,12 +500,12 @@ struct Walk {
         hk = 0;
         // (In cut lines an item whose first tile is past the end has no part here.)
         do {
-          if (++b == p.B || end <= (cut ? 0 : -kItemCost)) return;
+          if (++b == p.B || end <= (cut ? 0 : -kItemSteps)) return;
           s = Seq(p, b);
         } while (s.n == 0);
       }
     }
-    units = s.units(p, q);
+    item(p);
     take_whole();
   }
 };
@@ -522,10 +570,12 @@ __device__ __forceinline__ void fix_values(uint8_t *tile, int32_t key0, int32_t 
   uint8_t *mine = tile + half * 128;
   // Rows 8 j + half and 8 j + half + 4 of this lane: its chunk sits at one of two places of a row.
   const int c0 = ((lane & 7) ^ half) << 4, c1 = c0 ^ 64;
-  uint32_t odd = 0;
   const int end = min(kTile, len - key0);  // keys of the sequence
-  // (Loads alone, so that many are on their way.  An exponent of ones carries into the sign's place.
-  // Keys that all rows see may count here too: fix_each tells them apart.)
+  // Zero times a value is zero, or NaN where the value is not finite, and so is a sum of such: one
+  // instruction for two values.  (Keys that all rows see may count here too: fix_each tells them
+  // apart.)
+  const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+  __nv_bfloat162 odd[4] = {zero, zero, zero, zero};
 #pragma unroll(kBlocks == 2 ? 2 : 1)
   for (int row = max(0, seen + 1 - key0) & ~7; row < end; row += 8) {
     uint4 x[2][kBlocks];
@@ -533,24 +583,26 @@ __device__ __forceinline__ void fix_values(uint8_t *tile, int32_t key0, int32_t 
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int k = 0; k < kBlocks; ++k)
-        x[h][k] = *reinterpret_cast<const uint4 *>(mine + (row + 4 * h) * 128 + k * (kTile * 128) +
-                                                   (h ? c1 : c0));
+        x[h][k] = row + half + 4 * h < end
+                      ? *reinterpret_cast<const uint4 *>(mine + (row + 4 * h) * 128 +
+                                                         k * (kTile * 128) + (h ? c1 : c0))
+                      : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t any = 0;
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int k = 0; k < kBlocks; ++k)
-        any |= ((x[h][k].x & 0x7F807F80u) + 0x00800080u) | ((x[h][k].y & 0x7F807F80u) + 0x00800080u) |
-               ((x[h][k].z & 0x7F807F80u) + 0x00800080u) | ((x[h][k].w & 0x7F807F80u) + 0x00800080u);
-      odd |= row + half + 4 * h < end ? any : 0;
-    }
+      for (int k = 0; k < kBlocks; ++k) {
+        const __nv_bfloat162 *v = reinterpret_cast<const __nv_bfloat162 *>(&x[h][k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) odd[i] = __hfma2(v[i], zero, odd[i]);
+      }
   }
   for (int row = end + half; row < kTile; row += 4)
 #pragma unroll
     for (int k = 0; k < kBlocks; ++k)  // (the lanes of a row cover its chunks in any order)
       *reinterpret_cast<uint4 *>(tile + row * 128 + k * (kTile * 128) + ((lane & 7) << 4)) =
           make_uint4(0, 0, 0, 0);
-  if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0))
+  const __nv_bfloat162 any = __hadd2(__hadd2(odd[0], odd[1]), __hadd2(odd[2], odd[3]));
+  if (__any_sync(0xffffffffu, __hisnan(any.x) || __hisnan(any.y)))
     fix_each<kBlocks>(tile, key0, seen, len, first);
 }
 

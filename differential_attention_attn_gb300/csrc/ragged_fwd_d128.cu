@@ -280,28 +280,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == kQueryWarp) {
       // --------------------------------------------------------------- queries, and clean values
-      uint32_t filled = 0, tiles = 0;
-      for (uint32_t n = 0;; ++n) {
-        const int r = n % kSegRing;
-        if (!mbar_wait_warp(&ctrl->seg_full[r], (n / kSegRing) & 1, abort_flag, kWaitNs)) break;
-        const Segment g = ctrl->seg[r];
-        if (g.flags & (kStop | kEmpty)) {
+      uint32_t filled = 0, tiles = 0, n = 0;  // segments with keys, key tiles, segments
+      // The next segment with keys, its queries on their way (once the last one's have been read);
+      // none at the end of the share.
+      const auto next_queries = [&](Segment &g) {
+        for (;; ++n) {
+          const int r = n % kSegRing;
+          if (!mbar_wait_warp(&ctrl->seg_full[r], (n / kSegRing) & 1, abort_flag, kWaitNs))
+            return false;
+          g = ctrl->seg[r];
+          if (g.flags & kStop) return false;
+          if (!(g.flags & kEmpty)) break;
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctrl->seg_empty[r]);
-          if (g.flags & kStop) break;
-          continue;
         }
         if (filled > 0 && !mbar_wait_warp(&ctrl->q_empty, (filled - 1) & 1, abort_flag, kWaitNs))
-          break;
+          return false;
         if (lane == 0) {
           dbg_ok(g.row >= 0 && g.row + g.tokens <= p.N, p.status, 122);
-          ctrl->unclean[r] = 0;
+          ctrl->unclean[n % kSegRing] = 0;
           mbar_arrive_expect_tx(&ctrl->q_full, kKeyBoxes * p.tokens * p.group * 128);
           for (int k = 0; k < kKeyBoxes; ++k)
             tma_load_3d(smem + kQ + k * kBox, tm_q, &ctrl->q_full, 64 * k, g.hk * p.group, g.row);
         }
         ++filled;
-        const int32_t seen = seen_by_all(p, g);
+        return true;
+      };
+      Segment g;
+      bool more = next_queries(g);
+      while (more) {
+        const uint32_t here = n++;
+        const int r = here % kSegRing;
+        const int32_t seen = seen_by_all(p, g), last = g.tile0 + g.tiles - 1, len = g.len;
         uint32_t first[4][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -310,21 +320,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         // (Every value tile passes here, so that neither this warp nor the products can get a whole
         // turn of the ring ahead of the other.)
-        for (int32_t t = g.tile0; t < g.tile0 + g.tiles; ++t, ++tiles) {
+        for (int32_t t = g.tile0; t <= last; ++t, ++tiles) {
           const int s = tiles % kSlots;
+          // The next queries' place is free before the last values are here.
+          if (t == last) more = next_queries(g);
           if (!(ok = mbar_wait_warp(&ctrl->v_full[s], (tiles / kSlots) & 1, abort_flag, kWaitNs)))
             break;
           if (t * kTile + kTile - 1 > seen) {
-            fix_values<4>(smem + kValues + s * 4 * kBox, t * kTile, seen, g.len, first);
-            if (t == g.tile0 + g.tiles - 1) {
-              if (merge_first<4>(first)) {
-                // (Two segments back the columns have been read.)
-                if (n >= 2 && !(ok = mbar_wait_warp(&ctrl->seg_empty[(n - 2) % kSegRing],
-                                                    ((n - 2) / kSegRing) & 1, abort_flag, kWaitNs)))
-                  break;
-                store_first<4>(first, ctrl->column[n & 1]);
-                if (lane == 0) ctrl->unclean[r] = 1;
-              }
+            fix_values<4>(smem + kValues + s * 4 * kBox, t * kTile, seen, len, first);
+            if (t == last && merge_first<4>(first)) {
+              // (Two segments back the columns have been read.)
+              if (here >= 2 &&
+                  !(ok = mbar_wait_warp(&ctrl->seg_empty[(here - 2) % kSegRing],
+                                        ((here - 2) / kSegRing) & 1, abort_flag, kWaitNs)))
+                break;
+              store_first<4>(first, ctrl->column[here & 1]);
+              if (lane == 0) ctrl->unclean[r] = 1;
             }
             fence_async_proxy();
           }
