@@ -30,8 +30,9 @@ struct RaggedFwdPlan {
   size_t part, join, swap;
   size_t bytes;
 };
-RaggedFwdPlan plan_ragged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache,
-                              int sm_count);
+// False when a size does not fit.
+bool plan_ragged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache, int sm_count,
+                     RaggedFwdPlan *plan);
 diffattn_status launch_ragged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache,
                                   const RaggedFwdPlan &plan, const int32_t *q_start, const void *q1,
                                   const void *q2, const float *lambda, const float *norm_w,

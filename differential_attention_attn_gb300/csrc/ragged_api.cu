@@ -30,8 +30,7 @@ diffattn_status plan_fwd(const diffattn_desc *desc, const diffpaged_cache *cache
   if (desc->B == 0 || desc->H == 0 || desc->N == 0) return DIFFATTN_OK;
   const int sms = device_sm_count();
   if (sms <= 1) return DIFFATTN_ERR_CUDA;
-  *plan = plan_ragged_fwd(*desc, *cache, sms);
-  return DIFFATTN_OK;
+  return plan_ragged_fwd(*desc, *cache, sms, plan) ? DIFFATTN_OK : DIFFATTN_ERR_UNSUPPORTED;
 }
 
 }  // namespace

@@ -191,12 +191,19 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-RaggedFwdPlan plan_ragged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache,
-                              int sm_count) {
-  RaggedFwdPlan q = {};
+bool plan_ragged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache, int sm_count,
+                     RaggedFwdPlan *plan) {
+  RaggedFwdPlan &q = *plan;
+  q = RaggedFwdPlan{};
   q.shares = desc.d == 64 ? sm_count : sm_count / 2;
   // Items this short are never cut (cut_line).
   const int64_t units = (cache.max_pages * cache.page_size + kTile - 1) / kTile;
+  // A line has fewer than 2^31 steps, however full the batch and the table.
+  const int64_t tokens = kTile / (desc.H / cache.kv_heads);
+  if (static_cast<double>(cache.kv_heads) * static_cast<double>(desc.N / tokens + desc.B) *
+          static_cast<double>(kItemSteps + units * kTileSteps) >=
+      2147483648.0)
+    return false;
   q.joins = kItemSteps + units * kTileSteps > kJoinSteps;
   size_t at = 0;
   const auto take = [&at](size_t bytes) {
@@ -210,7 +217,7 @@ RaggedFwdPlan plan_ragged_fwd(const diffattn_desc &desc, const diffpaged_cache &
   }
   if (desc.d == 128) q.swap = take(ragged_swap_bytes(q.shares));
   q.bytes = at;
-  return q;
+  return true;
 }
 
 diffattn_status launch_ragged_fwd(const diffattn_desc &desc, const diffpaged_cache &cache,

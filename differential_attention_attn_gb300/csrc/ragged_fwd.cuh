@@ -140,7 +140,7 @@ __device__ __forceinline__ void fence_async_proxy() {
 
 // sum_{i < n} floor((a i + b) / m), a n + b below 2^32, by exchanging the two axes of the lattice
 // below the line (Euclid's steps on a and m).
-__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+__device__ __forceinline__ int32_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   int64_t sum = 0;
 #pragma unroll 1
   while (true) {
@@ -153,7 +153,7 @@ __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a,
       b %= m;
     }
     const uint32_t y = a * n + b;
-    if (y < m) return sum;
+    if (y < m) return static_cast<int32_t>(sum);
     n = y / m;
     b = y % m;
     const uint32_t t = m;
@@ -163,9 +163,9 @@ __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a,
 }
 
 // sum_{i < x} floor(i / 2^k)
-__device__ __forceinline__ int64_t step_sum(uint32_t x, uint32_t k) {
+__device__ __forceinline__ int32_t step_sum(uint32_t x, uint32_t k) {
   const uint32_t q = x >> k, r = x & ((1u << k) - 1);
-  return ((static_cast<int64_t>(q) * q - q) >> 1 << k) + static_cast<int64_t>(q) * r;
+  return static_cast<int32_t>(((static_cast<uint64_t>(q) * q - q) >> 1 << k) + q * r);
 }
 
 // A sequence's new tokens, in tiles of rows, and the steps of these.
@@ -199,10 +199,10 @@ struct Seq {
   __device__ __forceinline__ int32_t longest(const RaggedParams &p) const {
     return n > 0 ? kItemSteps + units(p, tiles - 1) * kTileSteps : 0;
   }
-  // Steps of tiles 0 .. q - 1 of rows.
-  __device__ __forceinline__ int64_t steps(const RaggedParams &p, int32_t q) const {
+  // Steps of tiles 0 .. q - 1 of rows (of all heads: below 2^31, the plan saw to it).
+  __device__ __forceinline__ int32_t steps(const RaggedParams &p, int32_t q) const {
     const int32_t whole = min(q, tiles - 1);  // tiles with all their tokens
-    int64_t s = 0;
+    int32_t s = 0;
     if (whole > 0) {
       const int32_t idle = first < 0 ? min(whole, p.by_tokens.div(-first)) : 0;
       s = whole;
@@ -217,10 +217,10 @@ struct Seq {
           }
         }
       } else {
-        s += static_cast<int64_t>(whole - idle) * ((len + kTile - 1) / kTile - 1);
+        s += (whole - idle) * ((len + kTile - 1) / kTile - 1);
       }
     }
-    s = s * kTileSteps + static_cast<int64_t>(q) * kItemSteps;
+    s = s * kTileSteps + q * kItemSteps;
     if (q > whole) s += units(p, tiles - 1) * weight(p, tiles - 1);
     return s;
   }
@@ -228,59 +228,49 @@ struct Seq {
 
 // Every share's piece of the line: `each` steps, and one more for the first `more`.
 struct Line {
-  int64_t each, more;
+  int32_t each, more;
   int32_t mode, shares;
-  __device__ __forceinline__ int64_t begin(int64_t share) const {
+  __device__ __forceinline__ int32_t begin(int32_t share) const {
     return share * each + min(share, more);
   }
-  __device__ __forceinline__ int64_t share_of(int64_t step) const {
-    const int64_t border = more * (each + 1);
-    const int64_t a = step < border ? step : step - border, b = step < border ? each + 1 : each;
-    const int64_t q = ((a | b) >> 32) == 0
-                          ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
-                          : a / b;
-    return step < border ? q : more + q;
+  __device__ __forceinline__ int32_t share_of(int32_t step) const {
+    const int32_t border = more * (each + 1);
+    return step < border ? step / (each + 1) : more + (step - border) / each;
   }
 };
 
 // Where a share begins: in sequence b (p.B for nowhere), `left` steps (whole items: items) into it.
 struct ShareState {
-  unsigned long long total, items, sums[32];
-  unsigned long long left;
-  int32_t longest, b;
+  int32_t total, items, longest, b, left;
+  int32_t sums[32];
 };
 
 // How a line of `total` steps in `items` items, the longest of `longest` steps, is shared.
-__device__ __forceinline__ Line cut_line(int32_t shares, int64_t total, int64_t items,
+__device__ __forceinline__ Line cut_line(int32_t shares, int32_t total, int32_t items,
                                          int32_t longest) {
-  // (A division of 64 bits is a long way: most lines are short enough for one of 32.)
-  const auto divide = [](int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
-                                : a / b;
-  };
   Line line;
   // Whole items, one a share, where the longest is not kJoinSteps longer than equal pieces; where
   // there are more of them than shares, equal pieces with the items that begin in each, at most
   // one longer than equal.
-  line.each = divide(total, shares);
+  line.each = total / shares;
   line.mode = items <= shares ? (longest <= line.each + kJoinSteps ? kWhole : kCut)
                               : (longest <= kJoinSteps ? kUncut : kCut);
   line.shares = shares;
   if (line.mode == kCut && line.each < kLeastSteps) {  // a piece holds a tile at least
-    line.shares = max(1, static_cast<int32_t>(total) / kLeastSteps);
-    line.each = divide(total, line.shares);
+    line.shares = max(1, total / kLeastSteps);
+    line.each = total / line.shares;
   }
   line.more = total - line.each * line.shares;
   return line;
 }
 
-__device__ __forceinline__ int64_t steps_of(const RaggedParams &p, const Seq &s) {
-  return s.n > 0 ? s.steps(p, s.tiles) * p.kv_heads : int64_t{0};
+__device__ __forceinline__ int32_t steps_of(const RaggedParams &p, const Seq &s) {
+  return s.n > 0 ? s.steps(p, s.tiles) * p.kv_heads : 0;
 }
-__device__ __forceinline__ int64_t warp_scan(int64_t x) {  // inclusive
+__device__ __forceinline__ int32_t warp_scan(int32_t x) {  // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (static_cast<int>(threadIdx.x % 32) >= o) x += y;
   }
   return x;
@@ -293,42 +283,31 @@ constexpr int kFewSequences = 64;
 // Finds where share `index` begins, among few sequences (one warp, the result in registers of it
 // all).
 __device__ __forceinline__ Line find_share_few(const RaggedParams &p, int32_t index, ShareState *st) {
-  const int lane = threadIdx.x % 32;
-  int64_t steps[2], items[2];
-  int32_t longest = 0;
+  const int b0 = 2 * (threadIdx.x % 32);
+  int32_t steps[2] = {0, 0}, items[2] = {0, 0}, longest = 0;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    steps[k] = items[k] = 0;
-    if (lane + 32 * k < p.B) {
-      const Seq s(p, lane + 32 * k);
-      if (s.n > 0) {
-        steps[k] = steps_of(p, s);
-        items[k] = static_cast<int64_t>(s.tiles) * p.kv_heads;
-        longest = max(longest, s.longest(p));
-      }
+  for (int k = 0; k < 2; ++k)
+    if (b0 + k < p.B) {
+      const Seq s(p, b0 + k);
+      steps[k] = steps_of(p, s);
+      items[k] = s.tiles * p.kv_heads;
+      longest = max(longest, s.longest(p));
       if (s.bad_rows && index == 0) report_bad_page(p.status);
     }
-  }
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  const int64_t s0 = warp_scan(steps[0]), all0 = __shfl_sync(0xffffffffu, s0, 31);
-  const int64_t i0 = warp_scan(items[0]), items0 = __shfl_sync(0xffffffffu, i0, 31);
-  const int64_t s1 = warp_scan(steps[1]) + all0, total = __shfl_sync(0xffffffffu, s1, 31);
-  const int64_t i1 = warp_scan(items[1]) + items0, all_items = __shfl_sync(0xffffffffu, i1, 31);
-  const Line line = cut_line(p.shares, total, all_items, longest);
+  const Line line = cut_line(p.shares, __reduce_add_sync(0xffffffffu, steps[0] + steps[1]),
+                             __reduce_add_sync(0xffffffffu, items[0] + items[1]),
+                             __reduce_max_sync(0xffffffffu, longest));
   const bool whole = line.mode == kWhole;
-  const int64_t target = whole ? index : line.begin(index);
+  const int32_t x0 = whole ? items[0] : steps[0], x1 = whole ? items[1] : steps[1];
+  const int32_t end = warp_scan(x0 + x1), target = whole ? index : line.begin(index);
+  const uint32_t at = __ballot_sync(0xffffffffu, target < end);
   st->b = p.B;
-  if (index < line.shares && target < (whole ? all_items : total)) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int64_t end = whole ? (k ? i1 : i0) : (k ? s1 : s0);
-      const int64_t begin = end - (whole ? items[k] : steps[k]);
-      const uint32_t at = __ballot_sync(0xffffffffu, begin <= target && target < end);
-      if (at != 0) {
-        st->b = 32 * k + __ffs(at) - 1;
-        st->left = target - __shfl_sync(0xffffffffu, begin, __ffs(at) - 1);
-      }
-    }
+  if (index < line.shares && at != 0) {
+    const int lane = __ffs(at) - 1;
+    const int32_t left = target - __shfl_sync(0xffffffffu, end - x0 - x1, lane);
+    const int32_t first = __shfl_sync(0xffffffffu, x0, lane);
+    st->b = 2 * lane + (left >= first);
+    st->left = left >= first ? left - first : left;
   }
   return line;
 }
@@ -339,17 +318,14 @@ template <int kThreads>
 __device__ __forceinline__ Line find_share(const RaggedParams &p, int32_t index, ShareState *st) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   if (tid == 0) {
-    st->total = st->items = 0;
-    st->longest = 0;
+    st->total = st->items = st->longest = 0;
     st->b = p.B;
   }
   __syncthreads();
-  int64_t total = 0, items = 0, mine = 0, mine_items = 0;
-  int32_t longest = 0;
+  int32_t total = 0, items = 0, mine = 0, mine_items = 0, longest = 0;
   for (int32_t b = tid; b < p.B; b += kThreads) {
     const Seq s(p, b);
-    const int64_t t = steps_of(p, s);
-    const int64_t n = static_cast<int64_t>(s.tiles) * p.kv_heads;
+    const int32_t t = steps_of(p, s), n = s.tiles * p.kv_heads;
     if (b == tid) {
       mine = t;
       mine_items = n;
@@ -359,38 +335,35 @@ __device__ __forceinline__ Line find_share(const RaggedParams &p, int32_t index,
     longest = max(longest, s.longest(p));
     if (s.bad_rows && index == 0) report_bad_page(p.status);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    items += __shfl_xor_sync(0xffffffffu, items, o);
-  }
+  total = __reduce_add_sync(0xffffffffu, total);
+  items = __reduce_add_sync(0xffffffffu, items);
   longest = __reduce_max_sync(0xffffffffu, longest);
   if (lane == 0 && total > 0) {
-    atomicAdd(&st->total, static_cast<unsigned long long>(total));
-    atomicAdd(&st->items, static_cast<unsigned long long>(items));
+    atomicAdd(&st->total, total);
+    atomicAdd(&st->items, items);
     atomicMax(&st->longest, longest);
   }
   __syncthreads();
   const Line line = cut_line(p.shares, st->total, st->items, st->longest);
   const bool whole = line.mode == kWhole;
-  const int64_t target = whole ? index : line.begin(index);
-  const int64_t all = whole ? st->items : st->total;
+  const int32_t target = whole ? index : line.begin(index);
+  const int32_t all = whole ? st->items : st->total;
   if (index < line.shares && target < all) {  // uniform
-    int64_t base = 0;
+    int32_t base = 0;
     for (int32_t b0 = 0; b0 < p.B && base <= target; b0 += kThreads) {
-      int64_t x = 0;
+      int32_t x = 0;
       if (b0 == 0) {
         x = whole ? mine_items : mine;
       } else if (b0 + tid < p.B) {
         const Seq s(p, b0 + tid);
-        x = whole ? static_cast<int64_t>(s.tiles) * p.kv_heads : steps_of(p, s);
+        x = whole ? s.tiles * p.kv_heads : steps_of(p, s);
       }
-      const int64_t incl = warp_scan(x);
+      const int32_t incl = warp_scan(x);
       if (lane == 31) st->sums[warp] = incl;
       __syncthreads();
-      int64_t before = base, chunk = 0;
+      int32_t before = base, chunk = 0;
       for (int w = 0; w < kThreads / 32; ++w) {
-        const int64_t y = st->sums[w];
+        const int32_t y = st->sums[w];
         chunk += y;
         if (w < warp) before += y;
       }
@@ -411,8 +384,8 @@ __device__ __forceinline__ Line find_share(const RaggedParams &p, int32_t index,
 struct Walk {
   Seq s;
   int32_t b, hk, q, units, weight;
-  int32_t tile;   // the next key tile of the item
-  int64_t end;    // the share's end, in steps from the item's first tile
+  int32_t tile;  // the next key tile of the item
+  int32_t end;   // the share's end, in steps from the item's first tile
   bool cut;
   __device__ __forceinline__ Walk(const RaggedParams &p, const Line &line, int32_t index,
                                   const ShareState &st)
@@ -420,34 +393,32 @@ struct Walk {
         cut(line.mode == kCut) {
     if (b >= p.B) return;
     s = Seq(p, b);
-    int64_t rest = st.left;
+    int32_t rest = st.left;
     if (line.mode == kWhole) {
-      hk = static_cast<int32_t>(rest) / s.tiles;
-      q = static_cast<int32_t>(rest) - hk * s.tiles;
+      hk = rest / s.tiles;
+      q = rest - hk * s.tiles;
       item(p);
-      end = static_cast<int64_t>(units) * weight;
+      end = units * weight;
       return;
     }
-    const int64_t head = s.steps(p, s.tiles);
-    hk = static_cast<int32_t>((rest >> 32) == 0 ? static_cast<uint32_t>(rest) / head : rest / head);
+    const int32_t head = s.steps(p, s.tiles);
+    hk = rest / head;
     rest -= hk * head;
     // The last tile of rows whose steps begin at or before `rest`, 32 candidates at a time.
     int32_t lo = 0, hi = s.tiles;
     while (hi - lo > 1) {
-      const int32_t step = (hi - lo + 31) / 32;
-      const int64_t x = lo + static_cast<int64_t>(threadIdx.x % 32) * step;
-      const bool before = x < hi && s.steps(p, static_cast<int32_t>(x)) <= rest;
+      const int32_t step = (hi - lo + 31) / 32, x = lo + static_cast<int32_t>(threadIdx.x % 32) * step;
+      const bool before = x < hi && s.steps(p, x) <= rest;
       const int top = 31 - __clz(__ballot_sync(0xffffffffu, before));
       lo += top * step;
       hi = min(hi, lo + step);
     }
     q = lo;
     item(p);
-    const int64_t off = rest - s.steps(p, q) - kItemSteps;  // of the share's begin from the tiles
+    const int32_t off = rest - s.steps(p, q) - kItemSteps;  // of the share's begin from the tiles
     end = off + line.each + (index < line.more ? 1 : 0);
     if (cut) {
-      // (`off` is below an item's steps.)
-      tile = off > 0 ? (static_cast<int32_t>(off) + weight - 1) / weight : 0;
+      tile = off > 0 ? (off + weight - 1) / weight : 0;
       if (tile == units) next(p);
     } else if (off > -kItemSteps) {
       next(p);
@@ -456,7 +427,7 @@ struct Walk {
     }
   }
   __device__ __forceinline__ bool more(const RaggedParams &p) const {
-    return b < p.B && static_cast<int64_t>(tile) * weight < end;
+    return b < p.B && tile * weight < end;
   }
   // The share's part of the item.
   __device__ __forceinline__ Segment segment(const RaggedParams &p, int32_t share) const {
@@ -469,8 +440,7 @@ struct Walk {
     g.b = b;
     g.hk = hk;
     g.tile0 = tile;
-    const bool all = end > static_cast<int64_t>(units - 1) * weight;
-    g.tiles = (all ? units : (static_cast<int32_t>(end) + weight - 1) / weight) - tile;
+    g.tiles = (end > (units - 1) * weight ? units : (end + weight - 1) / weight) - tile;
     g.flags = (g.tiles == units ? kDirect : 0) | (s.keys(p, q) == 0 ? kEmpty : 0) |
               (s.bad_len ? kBadLen : 0);
     g.slot = 2 * share + (tile == 0 ? 1 : 0);
@@ -478,10 +448,8 @@ struct Walk {
   }
   // Of a cut item that begins in the share.
   __device__ __forceinline__ RaggedJoin join(const Line &line, int32_t share, const Segment &g) const {
-    // The last tile's place on the line.
-    const int64_t last = line.begin(share + 1) - end + static_cast<int64_t>(units - 1) * weight;
-    return {static_cast<int32_t>(line.share_of(last)) - share + 1, g.slot, g.hk, g.row, g.tokens,
-            g.first, {0, 0}};
+    const int32_t last = line.begin(share + 1) - end + (units - 1) * weight;  // its last tile's place
+    return {line.share_of(last) - share + 1, g.slot, g.hk, g.row, g.tokens, g.first, {0, 0}};
   }
   __device__ __forceinline__ void item(const RaggedParams &p) {
     units = s.units(p, q);
@@ -489,10 +457,10 @@ struct Walk {
   }
   // Uncut: the items that begin in the share are all its own.
   __device__ __forceinline__ void take_whole() {
-    if (!cut && end > -kItemSteps) end = max(end, static_cast<int64_t>(units) * weight);
+    if (!cut && end > -kItemSteps) end = max(end, units * weight);
   }
   __device__ __forceinline__ void next(const RaggedParams &p) {
-    end -= static_cast<int64_t>(units) * weight + kItemSteps;
+    end -= units * weight + kItemSteps;
     tile = 0;
     if (++q == s.tiles) {
       q = 0;

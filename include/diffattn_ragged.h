@@ -112,7 +112,10 @@ diffattn_status diffragged_append(const diffattn_desc *desc, const diffpaged_cac
  *
  * workspace: as for diffpaged_fwd; its size does not depend on the lengths.
  * desc: B sequences, N rows, H, d (64 or 128), dtype, causal, headnorm, eps,
- * lambda_init.  Domain: H / kv_heads <= 64, page_size a multiple of 16.
+ * lambda_init.  Domain: H / kv_heads <= 64, page_size a multiple of 16, and
+ * kv_heads (N / floor(128 kv_heads / H) + B) (5 max_pages page_size / 128 + 20) <
+ * 2^31 (a call of 65536 rows of 32 heads over 8 key/value heads in tables of a
+ * million keys comes to a third of that).
  */
 diffattn_status diffragged_fwd(const diffattn_desc *desc, const diffpaged_cache *cache,
                                const int32_t *q_start, const void *q1, const void *q2,
