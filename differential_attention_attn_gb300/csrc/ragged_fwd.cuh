@@ -499,111 +499,107 @@ __device__ __forceinline__ int32_t seen_by_all(const RaggedParams &p, const Segm
 }
 
 // Values that not all rows see must not reach the others through a zero weight (0 * inf is not
-// zero): of the tile's keys past `seen` those behind the sequence's end become zero, and values of
-// the others that are not finite as well, in shared memory; a column's first such key (its distance
-// from `seen`, at most 254) is kept in `first`, two columns a word, eight of each block of 64 a
-// lane, by the four lanes that agree in lane % 8: rows at least that far from `seen` see it.  One
-// warp; a first look over all of them costs a tenth of the look at each (d = 64, 127 keys: 0.9 and
-// 9.7 us), and all but broken models' values need no other.
+// zero): of a tile's keys past `seen` those behind the sequence's end become zero, and values of the
+// others that are not finite as well, in shared memory, before the tile's product.  The softmax
+// warps do this, 16 rows each, once they have the tile's weights: one warp beside them took 2.2 us
+// (d = 64) and 3 us for a tile, in which the tensor cores waited at each item's end.
+//
+// Zero times a value is zero, or NaN where the value is not finite, and so is a sum of such: one
+// instruction looks at two values.  (Keys that all rows see may count too; fix_each tells them
+// apart.)  True where the warp's rows hold one.
 template <int kBlocks>
-__device__ __forceinline__ void fix_each(uint8_t *tile, int32_t key0, int32_t seen, int32_t len,
-                                         uint32_t (&first)[kBlocks][4]) {
+__device__ __forceinline__ bool fix_rows(uint8_t *tile, int32_t row0, int32_t key0, int32_t seen,
+                                         int32_t len) {
+  if (key0 + row0 + 15 <= seen) return false;
   const int lane = threadIdx.x % 32;
-  const int chunk = lane & 7;  // four rows at a time
-#pragma unroll 1
-  for (int row = (lane >> 3); row < kTile && key0 + row < len; row += 4) {
-    if (key0 + row <= seen) continue;
-    const uint32_t d = min(254, key0 + row - seen);
-#pragma unroll
-    for (int k = 0; k < kBlocks; ++k) {
-      uint32_t *at = reinterpret_cast<uint32_t *>(tile + k * (kTile * 128) + row * 128 +
-                                                  ((chunk ^ (row & 7)) << 4));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t w = at[i];
-        const bool lo = (w & 0x7F80u) == 0x7F80u, hi = (w & 0x7F800000u) == 0x7F800000u;
-        const uint32_t f = first[k][i];
-        first[k][i] = (lo ? min(f & 0xFFFFu, d) : f & 0xFFFFu) |
-                      ((hi ? min(f >> 16, d) : f >> 16) << 16);
-        if (lo || hi) at[i] = w & ((lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0xFFFFu : 0xFFFFFFFFu));
-      }
-    }
-  }
-}
-template <int kBlocks>
-__device__ __forceinline__ void fix_values(uint8_t *tile, int32_t key0, int32_t seen, int32_t len,
-                                           uint32_t (&first)[kBlocks][4]) {
-  const int lane = threadIdx.x % 32;
-  const int half = lane >> 3;
-  uint8_t *mine = tile + half * 128;
-  // Rows 8 j + half and 8 j + half + 4 of this lane: its chunk sits at one of two places of a row.
-  const int c0 = ((lane & 7) ^ half) << 4, c1 = c0 ^ 64;
-  const int end = min(kTile, len - key0);  // keys of the sequence
-  // Zero times a value is zero, or NaN where the value is not finite, and so is a sum of such: one
-  // instruction for two values.  (Keys that all rows see may count here too: fix_each tells them
-  // apart.)
+  const int end = len - key0;  // rows of the sequence
   const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
   __nv_bfloat162 odd[4] = {zero, zero, zero, zero};
-#pragma unroll(kBlocks == 2 ? 2 : 1)
-  for (int row = max(0, seen + 1 - key0) & ~7; row < end; row += 8) {
-    uint4 x[2][kBlocks];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+  for (int k0 = 0; k0 < kBlocks; k0 += 2) {
+    uint4 x[4][2];
 #pragma unroll
-      for (int k = 0; k < kBlocks; ++k)
-        x[h][k] = row + half + 4 * h < end
-                      ? *reinterpret_cast<const uint4 *>(mine + (row + 4 * h) * 128 +
-                                                         k * (kTile * 128) + (h ? c1 : c0))
-                      : make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+      for (int k = 0; k < 2; ++k) {
+        const int row = row0 + 4 * j + (lane >> 3);
+        uint4 *at = reinterpret_cast<uint4 *>(tile + (k0 + k) * (kTile * 128) + row * 128 +
+                                              ((lane & 7) << 4));
+        x[j][k] = make_uint4(0, 0, 0, 0);
+        if (row < end)
+          x[j][k] = *at;
+        else
+          *at = x[j][k];
+      }
 #pragma unroll
-      for (int k = 0; k < kBlocks; ++k) {
-        const __nv_bfloat162 *v = reinterpret_cast<const __nv_bfloat162 *>(&x[h][k]);
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const __nv_bfloat162 *v = reinterpret_cast<const __nv_bfloat162 *>(&x[j][k]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) odd[i] = __hfma2(v[i], zero, odd[i]);
       }
   }
-  for (int row = end + half; row < kTile; row += 4)
-#pragma unroll
-    for (int k = 0; k < kBlocks; ++k)  // (the lanes of a row cover its chunks in any order)
-      *reinterpret_cast<uint4 *>(tile + row * 128 + k * (kTile * 128) + ((lane & 7) << 4)) =
-          make_uint4(0, 0, 0, 0);
   const __nv_bfloat162 any = __hadd2(__hadd2(odd[0], odd[1]), __hadd2(odd[2], odd[3]));
-  if (__any_sync(0xffffffffu, __hisnan(any.x) || __hisnan(any.y)))
-    fix_each<kBlocks>(tile, key0, seen, len, first);
+  return __any_sync(0xffffffffu, __hisnan(any.x) || __hisnan(any.y));
 }
 
-// The smallest over the four lanes that agree in lane % 8; whether any lane has one.
+// Such rows: each value past `seen` that is not finite becomes zero, and its column's byte the
+// least distance from `seen` of such a key (at most 254; 255 where there is none): rows at least
+// that far from `seen` see it.  Broken models' values only, so short rather than fast.
 template <int kBlocks>
-__device__ __forceinline__ bool merge_first(uint32_t (&first)[kBlocks][4]) {
-  bool any = false;
-#pragma unroll
-  for (int k = 0; k < kBlocks; ++k)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t f = first[k][i];
-#pragma unroll
-      for (int o = 8; o <= 16; o *= 2) {
-        const uint32_t g = __shfl_xor_sync(0xffffffffu, f, o);
-        f = min(f & 0xFFFFu, g & 0xFFFFu) | (min(f >> 16, g >> 16) << 16);
-      }
-      first[k][i] = f;
-      any |= f != 0xFFFFFFFFu;
-    }
-  return __any_sync(0xffffffffu, any);
-}
-// One byte a column, 255 for none.
-template <int kBlocks>
-__device__ __forceinline__ void store_first(const uint32_t (&first)[kBlocks][4], uint8_t *columns) {
+__device__ __noinline__ void fix_each(uint8_t *tile, int32_t row0, int32_t key0, int32_t seen,
+                                      int32_t len, uint32_t *columns) {
   const int lane = threadIdx.x % 32;
-  if (lane < 8)
-#pragma unroll
-    for (int k = 0; k < kBlocks; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint16_t *>(columns + 64 * k + 8 * lane + 2 * i) =
-            static_cast<uint16_t>((first[k][i] & 0xFFu) | ((first[k][i] >> 8) & 0xFF00u));
+  for (int x = lane; x < 16 * kBlocks * 32; x += 32) {  // words of two columns
+    const int row = row0 + x / (kBlocks * 32), word = x % (kBlocks * 32);
+    const int32_t far = key0 + row - seen;
+    if (far <= 0 || key0 + row >= len) continue;
+    const int chunk = word % 32 / 4;
+    uint32_t *at = reinterpret_cast<uint32_t *>(tile + word / 32 * (kTile * 128) + row * 128 +
+                                                ((chunk ^ (row & 7)) << 4)) + word % 4;
+    const uint32_t w = *at;
+    const bool lo = (w & 0x7F80u) == 0x7F80u, hi = (w & 0x7F800000u) == 0x7F800000u;
+    if (!lo && !hi) continue;
+    *at = w & ((lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0xFFFFu : 0xFFFFFFFFu));
+    const uint32_t d = min(254, far);
+    const uint32_t two = (lo ? d : 255u) | ((hi ? d : 255u) << 8);
+    const uint32_t mine = word % 2 ? (two << 16) | 0xFFFFu : two | 0xFFFF0000u;
+    uint32_t old = columns[word / 2], now;
+    while ((now = __vminu4(old, mine)) != old) {
+      const uint32_t was = atomicCAS(&columns[word / 2], old, now);
+      if (was == old) break;
+      old = was;
+    }
+  }
+  __syncwarp();
+}
+
+// The first warp that needs a segment's column bytes (there are two sets, in turn) sets them to 255
+// once the segment before last has been read; `state` goes from 0 over 1 to 2.  False where a wait
+// ran out.
+__device__ __noinline__ bool open_columns(int32_t *state, uint32_t *columns, int words,
+                                          uint64_t *before_last, uint32_t parity, bool any_before,
+                                          volatile int *abort) {
+  const int lane = threadIdx.x % 32;
+  int32_t was = 0;
+  if (lane == 0) was = atomicCAS(state, 0, 1);
+  was = __shfl_sync(0xffffffffu, was, 0);
+  if (was == 0) {
+    if (any_before && !mbar_wait_warp(before_last, parity, abort, kWaitNs)) return false;
+    for (int x = lane; x < words; x += 32) columns[x] = 0xFFFFFFFFu;
+    __threadfence_block();
+    __syncwarp();
+    if (lane == 0) atomicExch(state, 2);
+    return true;
+  }
+  const uint64_t t0 = globaltimer_ns();
+  while (*reinterpret_cast<volatile int32_t *>(state) != 2) {
+    if (globaltimer_ns() - t0 > kWaitNs) *abort = 1;
+    if (*abort) return false;
+  }
+  __threadfence_block();
+  return true;
 }
 
 // The load warps, one for the keys (with the walk along the share and the segments' descriptions)

@@ -47,7 +47,7 @@ constexpr uint32_t kCtrlAt = kValues + kSlots * 4 * kBox;
 constexpr uint32_t kTmO = 256;
 
 struct Ctrl {
-  uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots], v_fixed[kSlots];
+  uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots];
   uint64_t q_full, q_empty, s_full[2], p_ready[2], pv_done, o_done, o_free, drain;
   uint64_t l_full[2];  // by segment with keys: the softmax may be done with the next one's as well
   uint64_t peer[2];  // the other CTA's hand-overs, in turn
@@ -130,7 +130,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctrl->k_empty[s], 1);
       mbar_init(&ctrl->v_full[s], 1);
       mbar_init(&ctrl->v_empty[s], 1);
-      mbar_init(&ctrl->v_fixed[s], 1);
     }
     mbar_init(&ctrl->q_full, 1);
     mbar_init(&ctrl->q_empty, 1);
@@ -198,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait_warp(&ctrl->seg_empty[r], (n / kSegRing - 1) & 1, abort_flag, kWaitNs);
         if (ok && lane == 0) {
           ctrl->seg[r] = g;
-          ctrl->bad[r] = 0;
+          ctrl->bad[r] = ctrl->unclean[r] = 0;
           mbar_arrive(&ctrl->seg_full[r]);
         }
         ++n;
@@ -279,70 +278,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) ring.drain(ctrl->v_full);
       __syncwarp();
     } else if (warp == kQueryWarp) {
-      // --------------------------------------------------------------- queries, and clean values
-      uint32_t filled = 0, tiles = 0, n = 0;  // segments with keys, key tiles, segments
-      // The next segment with keys, its queries on their way (once the last one's have been read);
-      // none at the end of the share.
-      const auto next_queries = [&](Segment &g) {
-        for (;; ++n) {
-          const int r = n % kSegRing;
-          if (!mbar_wait_warp(&ctrl->seg_full[r], (n / kSegRing) & 1, abort_flag, kWaitNs))
-            return false;
-          g = ctrl->seg[r];
-          if (g.flags & kStop) return false;
-          if (!(g.flags & kEmpty)) break;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctrl->seg_empty[r]);
-        }
-        if (filled > 0 && !mbar_wait_warp(&ctrl->q_empty, (filled - 1) & 1, abort_flag, kWaitNs))
-          return false;
-        if (lane == 0) {
-          dbg_ok(g.row >= 0 && g.row + g.tokens <= p.N, p.status, 122);
-          ctrl->unclean[n % kSegRing] = 0;
-          mbar_arrive_expect_tx(&ctrl->q_full, kKeyBoxes * p.tokens * p.group * 128);
-          for (int k = 0; k < kKeyBoxes; ++k)
-            tma_load_3d(smem + kQ + k * kBox, tm_q, &ctrl->q_full, 64 * k, g.hk * p.group, g.row);
-        }
-        ++filled;
-        return true;
-      };
-      Segment g;
-      bool more = next_queries(g);
-      while (more) {
-        const uint32_t here = n++;
-        const int r = here % kSegRing;
-        const int32_t seen = seen_by_all(p, g), last = g.tile0 + g.tiles - 1, len = g.len;
-        uint32_t first[4][4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) first[k][i] = 0xFFFFFFFFu;
-        bool ok = true;
-        // (Every value tile passes here, so that neither this warp nor the products can get a whole
-        // turn of the ring ahead of the other.)
-        for (int32_t t = g.tile0; t <= last; ++t, ++tiles) {
-          const int s = tiles % kSlots;
-          // The next queries' place is free before the last values are here.
-          if (t == last) more = next_queries(g);
-          if (!(ok = mbar_wait_warp(&ctrl->v_full[s], (tiles / kSlots) & 1, abort_flag, kWaitNs)))
+      // --------------------------------------------------------------- queries
+      uint32_t filled = 0;  // segments with keys
+      for (uint32_t n = 0;; ++n) {
+        const int r = n % kSegRing;
+        if (!mbar_wait_warp(&ctrl->seg_full[r], (n / kSegRing) & 1, abort_flag, kWaitNs)) break;
+        const Segment *g = &ctrl->seg[r];
+        const int32_t flags = g->flags;
+        if (flags & kStop) break;
+        if (!(flags & kEmpty)) {
+          if (filled > 0 && !mbar_wait_warp(&ctrl->q_empty, (filled - 1) & 1, abort_flag, kWaitNs))
             break;
-          if (t * kTile + kTile - 1 > seen) {
-            fix_values<4>(smem + kValues + s * 4 * kBox, t * kTile, seen, len, first);
-            if (t == last && merge_first<4>(first)) {
-              // (Two segments back the columns have been read.)
-              if (here >= 2 &&
-                  !(ok = mbar_wait_warp(&ctrl->seg_empty[(here - 2) % kSegRing],
-                                        ((here - 2) / kSegRing) & 1, abort_flag, kWaitNs)))
-                break;
-              store_first<4>(first, ctrl->column[here & 1]);
-              if (lane == 0) ctrl->unclean[r] = 1;
-            }
-            fence_async_proxy();
+          if (lane == 0) {
+            dbg_ok(g->row >= 0 && g->row + g->tokens <= p.N, p.status, 122);
+            mbar_arrive_expect_tx(&ctrl->q_full, kKeyBoxes * p.tokens * p.group * 128);
+            for (int k = 0; k < kKeyBoxes; ++k)
+              tma_load_3d(smem + kQ + k * kBox, tm_q, &ctrl->q_full, 64 * k, g->hk * p.group,
+                          g->row);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctrl->v_fixed[s]);
+          ++filled;
         }
-        if (!ok) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctrl->seg_empty[r]);
       }
@@ -413,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int32_t t = 0; t < tiles; ++t) {
           const uint32_t cc = c + t;
           if (t + 1 < tiles && !(ok = next_s(t + 1))) break;
-          if (!(ok = wait(&ctrl->v_fixed[cc % kSlots], (cc / kSlots) & 1))) break;
+          if (!(ok = wait(&ctrl->v_full[cc % kSlots], (cc / kSlots) & 1))) break;
           if (!(ok = wait(&ctrl->p_ready[cc & 1], (cc >> 1) & 1))) break;
           if (t == 0 && filled > 0 && !(ok = wait(&ctrl->o_free, (filled - 1) & 1))) break;
           tc_fence_after_sync();
@@ -452,6 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(flags & kEmpty)) {
           const int32_t tiles = g->tiles, rows = g->tokens * p.group;
           const bool live = warp_row < rows;
+          const int32_t seen = seen_by_all(p, *g), len = g->len;
+          const int32_t first_key = g->tile0 * kTile;
           const int32_t lim0 =
               (p.causal ? min(max(g->first + token, 0), g->len - 1) : g->len - 1) - g->tile0 * kTile;
           float m_run = -INFINITY, l_run = 0.f;
@@ -521,6 +478,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st_wait();
               tc_fence_before_sync();
             }
+            if (first_key + (t + 1) * kTile - 1 > seen) {
+              uint8_t *values = smem + kValues + (c % kSlots) * 4 * kBox;
+              const int32_t key = first_key + t * kTile;
+              if (!(ok = mbar_wait_warp(&ctrl->v_full[c % kSlots], (c / kSlots) & 1, abort_flag, kWaitNs)))
+                break;
+              if (fix_rows<4>(values, 16 * sw, key, seen, len)) {
+                uint32_t *columns = reinterpret_cast<uint32_t *>(ctrl->column[n & 1]);
+                if (!(ok = open_columns(&ctrl->unclean[ring], columns, DV / 4,
+                                        &ctrl->seg_empty[(n - 2) % kSegRing], ((n - 2) / kSegRing) & 1,
+                                        n >= 2, abort_flag)))
+                  break;
+                fix_each<4>(values, 16 * sw, key, seen, len, columns);
+              }
+              fence_async_proxy();
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctrl->p_ready[c & 1]);
           }
@@ -582,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(flags & kDirect)) {
             // A part: O column by column.
             float *part = p.part + (g->slot * 2ll + map) * part_floats(DV);
-            const bool unclean = ctrl->unclean[ring] != 0;
+            const bool unclean = ctrl->unclean[ring] == 2;
             const int32_t far = pos - seen_by_all(p, *g);
             const bool mine = r < rows;
 #pragma unroll 1
@@ -653,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               asm volatile("" ::: "memory");
             }
           }
-          if (ctrl->unclean[ring]) {
+          if (ctrl->unclean[ring] == 2) {
             const int32_t far = pos - seen_by_all(p, *g);
 #pragma unroll
             for (int i = 0; i < 64; ++i)

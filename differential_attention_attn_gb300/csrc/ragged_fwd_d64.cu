@@ -43,14 +43,14 @@ constexpr uint32_t kCtrlAt = kValues + kSlots * 2 * kBox;
 
 struct Ctrl {
   uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots];
-  uint64_t v_fixed[kSlots], q_full, q_empty, s_full[2], p_ready[2], o_done, o_free, drain;
+  uint64_t q_full, q_empty, s_full[2], p_ready[2], o_done, o_free, drain;
   uint64_t seg_full[kSegRing], seg_empty[kSegRing];
   Segment seg[kSegRing];
   int32_t bad[kSegRing];      // the segment met a page number outside the pool
   int32_t unclean[kSegRing];  // `column` counts
   uint32_t tmem;
   int abort;
-  alignas(8) uint8_t column[2][DV];  // fix_values, by segment
+  alignas(8) uint8_t column[2][DV];  // fix_each, by segment
   float xch[2 * kTile];
 };
 static_assert(sizeof(ShareState) <= 2 * kTile * sizeof(float), "the set-up's state lies in xch");
@@ -83,7 +83,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctrl->k_empty[s], 1);
       mbar_init(&ctrl->v_full[s], 1);
       mbar_init(&ctrl->v_empty[s], 1);
-      mbar_init(&ctrl->v_fixed[s], 1);
     }
     mbar_init(&ctrl->q_full, 1);
     mbar_init(&ctrl->q_empty, 1);
@@ -150,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait_warp(&ctrl->seg_empty[r], (n / kSegRing - 1) & 1, abort_flag, kWaitNs);
         if (ok && lane == 0) {
           ctrl->seg[r] = g;
-          ctrl->bad[r] = 0;
+          ctrl->bad[r] = ctrl->unclean[r] = 0;
           mbar_arrive(&ctrl->seg_full[r]);
         }
         ++n;
@@ -235,70 +234,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) ring.drain(ctrl->v_full);
       __syncwarp();
     } else if (warp == kQueryWarp) {
-      // ------------------------------------------------------------- queries, and clean values
-      uint32_t filled = 0, tiles = 0, n = 0;  // segments with keys, key tiles, segments
-      // The next segment with keys, its queries on their way (once the last one's have been read);
-      // none at the end of the share.
-      const auto next_queries = [&](Segment &g) {
-        for (;; ++n) {
-          const int r = n % kSegRing;
-          if (!mbar_wait_warp(&ctrl->seg_full[r], (n / kSegRing) & 1, abort_flag, kWaitNs))
-            return false;
-          g = ctrl->seg[r];
-          if (g.flags & kStop) return false;
-          if (!(g.flags & kEmpty)) break;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctrl->seg_empty[r]);
-        }
-        if (filled > 0 && !mbar_wait_warp(&ctrl->q_empty, (filled - 1) & 1, abort_flag, kWaitNs))
-          return false;
-        if (lane == 0) {
-          dbg_ok(g.row >= 0 && g.row + g.tokens <= p.N, p.status, 102);
-          ctrl->unclean[n % kSegRing] = 0;
-          mbar_arrive_expect_tx(&ctrl->q_full, 2 * p.tokens * p.group * kRowBytes);
-          tma_load_3d(smem + kQ, &tm_q1, &ctrl->q_full, 0, g.hk * p.group, g.row);
-          tma_load_3d(smem + kQ + kBox, &tm_q2, &ctrl->q_full, 0, g.hk * p.group, g.row);
-        }
-        ++filled;
-        return true;
-      };
-      Segment g;
-      bool more = next_queries(g);
-      while (more) {
-        const uint32_t here = n++;
-        const int r = here % kSegRing;
-        const int32_t seen = seen_by_all(p, g), last = g.tile0 + g.tiles - 1, len = g.len;
-        uint32_t first[2][4];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) first[k][i] = 0xFFFFFFFFu;
-        bool ok = true;
-        // (Every value tile passes here, so that neither this warp nor the products can get a whole
-        // turn of the ring ahead of the other.)
-        for (int32_t t = g.tile0; t <= last; ++t, ++tiles) {
-          const int s = tiles % kSlots;
-          // The next queries' place is free before the last values are here.
-          if (t == last) more = next_queries(g);
-          if (!(ok = mbar_wait_warp(&ctrl->v_full[s], (tiles / kSlots) & 1, abort_flag, kWaitNs)))
+      // ------------------------------------------------------------- queries
+      uint32_t filled = 0;  // segments with keys
+      for (uint32_t n = 0;; ++n) {
+        const int r = n % kSegRing;
+        if (!mbar_wait_warp(&ctrl->seg_full[r], (n / kSegRing) & 1, abort_flag, kWaitNs)) break;
+        const Segment *g = &ctrl->seg[r];
+        const int32_t flags = g->flags;
+        if (flags & kStop) break;
+        if (!(flags & kEmpty)) {
+          if (filled > 0 && !mbar_wait_warp(&ctrl->q_empty, (filled - 1) & 1, abort_flag, kWaitNs))
             break;
-          if (t * kTile + kTile - 1 > seen) {
-            fix_values<2>(smem + kValues + s * 2 * kBox, t * kTile, seen, len, first);
-            if (t == last && merge_first<2>(first)) {
-              // (Two segments back the columns have been read.)
-              if (here >= 2 &&
-                  !(ok = mbar_wait_warp(&ctrl->seg_empty[(here - 2) % kSegRing],
-                                        ((here - 2) / kSegRing) & 1, abort_flag, kWaitNs)))
-                break;
-              store_first<2>(first, ctrl->column[here & 1]);
-              if (lane == 0) ctrl->unclean[r] = 1;
-            }
-            fence_async_proxy();
+          if (lane == 0) {
+            dbg_ok(g->row >= 0 && g->row + g->tokens <= p.N, p.status, 102);
+            mbar_arrive_expect_tx(&ctrl->q_full, 2 * p.tokens * p.group * kRowBytes);
+            tma_load_3d(smem + kQ, &tm_q1, &ctrl->q_full, 0, g->hk * p.group, g->row);
+              tma_load_3d(smem + kQ + kBox, &tm_q2, &ctrl->q_full, 0, g->hk * p.group, g->row);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctrl->v_fixed[s]);
+          ++filled;
         }
-        if (!ok) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctrl->seg_empty[r]);
       }
@@ -373,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit_warp(&ctrl->s_full[1]);
           umma_commit_warp(&ctrl->k_empty[s]);
           if (t == tiles - 1) umma_commit_warp(&ctrl->q_empty);
-          if (!(ok = wait(&ctrl->v_fixed[s], ph))) break;
+          if (!(ok = wait(&ctrl->v_full[s], ph))) break;
           if (!(ok = wait(&ctrl->p_ready[0], c & 1))) break;
           if (t == 0 && filled > 0 && !(ok = wait(&ctrl->o_free, (filled - 1) & 1))) break;
           tc_fence_after_sync();
@@ -416,6 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t h = g->hk * p.group + head;
       const float lam = r < rows ? p.lambda[h] : 0.f;
       const bool live = warp_row < rows;  // some row of the warp counts
+      // The first tile that not all rows see whole (map 2's warps have nothing to do with it).
+      const int32_t t_fix = k == 0 ? (seen_by_all(p, *g) + 1) / kTile - g->tile0 : INT32_MAX;
       // Key column x of the segment's tile t is visible to this row iff x <= lim0 - 128 t.  (A row
       // that sees no key, or is none, is computed as one that sees some, and not written.)
       const int32_t lim0 =
@@ -484,6 +440,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_wait();
             tc_fence_before_sync();
           }
+          // The first product with the tile's values waits for map 1's warps.
+          if (t >= t_fix) {
+            uint8_t *values = smem + kValues + (c % kSlots) * 2 * kBox;
+            const int32_t key = (g->tile0 + t) * kTile, seen = seen_by_all(p, *g), len = g->len;
+            if (!(ok = mbar_wait_warp(&ctrl->v_full[c % kSlots], (c / kSlots) & 1, abort_flag,
+                                      kWaitNs)))
+              break;
+            if (fix_rows<2>(values, 16 * sw, key, seen, len)) {
+              uint32_t *columns = reinterpret_cast<uint32_t *>(ctrl->column[n & 1]);
+              if (!(ok = open_columns(&ctrl->unclean[ring], columns, DV / 4,
+                                      &ctrl->seg_empty[(n - 2) % kSegRing],
+                                      ((n - 2) / kSegRing) & 1, n >= 2, abort_flag)))
+                break;
+              fix_each<2>(values, 16 * sw, key, seen, len, columns);
+            }
+            fence_async_proxy();
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctrl->p_ready[k]);
         }
@@ -498,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(flags & kDirect)) {
           // A part: O_k column by column, the reference and the sum.
           float *part = p.part + (g->slot * 2ll + k) * part_floats(DV);
-          const bool unclean = ctrl->unclean[ring] != 0;
+          const bool unclean = ctrl->unclean[ring] == 2;
           const int32_t far = pos - seen_by_all(p, *g);
           const bool mine = r < rows;
 #pragma unroll 1
@@ -554,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctrl->o_free);
-        if (ctrl->unclean[ring]) {
+        if (ctrl->unclean[ring] == 2) {
           const int32_t far = pos - seen_by_all(p, *g);
 #pragma unroll
           for (int i = 0; i < 32; ++i)
