@@ -996,9 +996,10 @@ class RotaryTable:
         B, _, N, d = shapes[0]
         if any((s[0], s[2], s[3]) != (B, N, d) for s in shapes):
             raise ValueError("the tensors must agree in B, N and d")
-        for strides in (x_strides, y_strides):
-            if any(s[3] != 1 for s in strides):
-                raise ValueError("rows must be contiguous (last stride 1)")
+        if y_strides is None:  # new outputs, contiguous
+            y_strides = [(s[1] * N * d, N * d, d, 1) for s in shapes]
+        if any(s[3] != 1 for s in (*x_strides, *y_strides)):
+            raise ValueError("rows must be contiguous (last stride 1)")
         n = len(shapes)
         both = [_strides_of(shapes[i // 2], (x_strides, y_strides)[i % 2][i // 2])
                 for i in range(2 * n)]
@@ -1013,24 +1014,28 @@ class RotaryTable:
 
 
 def _rotary(table, tensors, positions, start, outs, status, stream, raw_status, inverse):
-    x = list(tensors)
+    x = tensors if type(tensors) is list else list(tensors)
     if not x:
         raise ValueError("one to four tensors, [B, heads, N, d] each")
     index, dtype = table.index, x[0].dtype
-    if outs is None:
-        with (contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)):
-            outs = [torch.empty_like(t) for t in x]
     shapes = tuple([t.shape for t in x])
-    key = (dtype, shapes, tuple([t.stride() for t in x]), tuple([t.stride() for t in outs]))
+    key = (dtype, shapes, tuple([t.stride() for t in x]),
+           None if outs is None else tuple([t.stride() for t in outs]))
     call = table._calls.get(key) if status is None else None
     ref, n, pointers, heads, strides, B, N = call or table._new_call(key, status)
-    if len(outs) != n or tuple([t.shape for t in outs]) != shapes:
-        raise ValueError("outs must be as many tensors of the inputs' shapes")
-    for t in (*x, *outs):
+    for t in x:
         if t.dtype != dtype:
             raise ValueError("all tensors must be of one dtype")
         if t.get_device() != index:
             raise ValueError("all tensors must be on the table's device")
+    if outs is None:
+        outs = [_new_on(stream, s, dtype, table.device) for s in shapes]
+    else:
+        if len(outs) != n or tuple([t.shape for t in outs]) != shapes:
+            raise ValueError("outs must be as many tensors of the inputs' shapes")
+        for t in outs:
+            if t.dtype != dtype or t.get_device() != index:
+                raise ValueError("outs must be of the inputs' dtype, on the table's device")
     at, step = None, 0
     if positions is not None:
         if positions.dtype != torch.int32 or positions.shape not in ((N,), (B, N)) or \
@@ -1056,7 +1061,7 @@ def rotary(table, tensors, positions=None, *, start: int = 0, outs=None, status=
     tensors: [B, heads, N, d] each (q1, q2, k1, k2 with their own numbers of heads; d 64 or 128),
     all bf16 or all fp32, views of any layout with contiguous rows.  positions: int32 [N] or
     [B, N], any values; without them row i is at start + i.  outs: tensors of the same shapes (the
-    inputs themselves: in place; new ones when None).  Returns the list of outputs.
+    inputs themselves: in place), new contiguous ones when None.  Returns the list of outputs.
     """
     return _rotary(table, tensors, positions, start, outs, status, stream, raw_status, 0)
 
