@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThreads) diffrotary_kernel(const __grid_const
   Turn turn;
   if (turns) {
     int64_t pos = p.positions ? p.positions[b * p.position_stride + i] : p.start + i;
-    turn = make_turn(p.freq, u, p.inverse ? -pos : pos, p.scale);
+    turn = make_turn<kQuads == 1>(p.freq, u, p.inverse ? -pos : pos, p.scale);
   }
 #pragma unroll
   for (int r = 0; r < kRows; ++r)
