@@ -18,19 +18,25 @@ bool packed_strides_ok(const diffattn_strides &s, int64_t multiple) {
   return paged_strides_ok({multiple, s.h, s.n}, multiple);
 }
 
-// Everything about a forward but its tensors; the plan.
-diffattn_status plan_fwd(const diffattn_desc *desc, const diffpaged_cache *cache,
-                         RaggedFwdPlan *plan) {
-  diffattn_status st = check_paged_cache(desc, cache, true);
+// Everything about a forward but its tensors, without a device.
+diffattn_status check_fwd(const diffattn_desc *desc, const diffpaged_cache *cache) {
+  const diffattn_status st = check_paged_cache(desc, cache, true);
   if (st != DIFFATTN_OK) return st;
   if (desc->H / cache->kv_heads > kRaggedMaxGroup || desc->N > (int64_t{1} << 30) ||
       desc->B >= (int64_t{1} << 24) || desc->H > 65535)
     return DIFFATTN_ERR_UNSUPPORTED;
-  *plan = RaggedFwdPlan{};
   if (desc->B == 0 || desc->H == 0 || desc->N == 0) return DIFFATTN_OK;
+  RaggedFwdPlan plan;
+  return plan_ragged_fwd(*desc, *cache, 2, &plan) ? DIFFATTN_OK : DIFFATTN_ERR_UNSUPPORTED;
+}
+
+diffattn_status plan_fwd(const diffattn_desc &desc, const diffpaged_cache &cache,
+                         RaggedFwdPlan *plan) {
+  *plan = RaggedFwdPlan{};
+  if (desc.B == 0 || desc.H == 0 || desc.N == 0) return DIFFATTN_OK;
   const int sms = device_sm_count();
   if (sms <= 1) return DIFFATTN_ERR_CUDA;
-  return plan_ragged_fwd(*desc, *cache, sms, plan) ? DIFFATTN_OK : DIFFATTN_ERR_UNSUPPORTED;
+  return plan_ragged_fwd(desc, cache, sms, plan) ? DIFFATTN_OK : DIFFATTN_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -115,7 +121,8 @@ diffattn_status diffragged_fwd_plan(const diffattn_desc *desc, const diffpaged_c
                                     size_t *workspace_bytes) {
   if (workspace_bytes == nullptr) return DIFFATTN_ERR_INVALID_ARG;
   RaggedFwdPlan plan;
-  const diffattn_status st = plan_fwd(desc, cache, &plan);
+  diffattn_status st = check_fwd(desc, cache);
+  if (st == DIFFATTN_OK) st = plan_fwd(*desc, *cache, &plan);
   if (st == DIFFATTN_OK) *workspace_bytes = plan.bytes;
   return st;
 }
@@ -125,8 +132,7 @@ diffattn_status diffragged_fwd(const diffattn_desc *desc, const diffpaged_cache 
                                const float *lambda, const float *norm_w, void *out,
                                const diffattn_strides *strides, void *workspace,
                                size_t workspace_bytes, void *stream) {
-  RaggedFwdPlan plan;
-  diffattn_status st = plan_fwd(desc, cache, &plan);
+  diffattn_status st = check_fwd(desc, cache);
   if (st != DIFFATTN_OK) return st;
   if (desc->B == 0 || desc->H == 0 || desc->N == 0) return DIFFATTN_OK;
   if (!q_start || !q1 || !q2 || !lambda || !out || !aligned(q_start, 4) || !aligned(q1, 16) ||
@@ -139,6 +145,8 @@ diffattn_status diffragged_fwd(const diffattn_desc *desc, const diffpaged_cache 
     st3[i] = strides ? strides[i] : diffattn_strides{0, width, desc->H * width};
     if (!packed_strides_ok(st3[i], fp8 && i < 2 ? 16 : 8)) return DIFFATTN_ERR_INVALID_ARG;
   }
+  RaggedFwdPlan plan;
+  if ((st = plan_fwd(*desc, *cache, &plan)) != DIFFATTN_OK) return st;
   if (plan.bytes > 0 &&
       (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < plan.bytes))
     return DIFFATTN_ERR_INVALID_ARG;

@@ -496,3 +496,126 @@ def test_fwd_refusals():
                        workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
     out = ops.ragged_fwd(cache, q1[:0], q2[:0], lam, _int([0, 0]))
     assert out.shape == (0, 4, 128)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_batches(seed):
+    """Head groups, pages, lengths and counts by chance: whole, uncut and cut items."""
+    rng = random.Random(seed)
+    d, dtype = KINDS[seed % 4]
+    kv, group = rng.choice([1, 2, 3]), rng.choice([1, 2, 3, 4, 5, 8, 16, 40])
+    B = rng.choice([1, 2, 5, 20, 70, 130])
+    most = rng.choice([30, 200, 1500, 5000]) if B < 20 else rng.choice([30, 300])
+    lens = [rng.choice([0, 1, rng.randint(1, most), most]) for _ in range(B)]
+    new = [rng.choice([0, 1, 1, rng.randint(0, 150), n]) for n in lens]
+    while sum(new) * kv * group * most > 3e8:  # the reference's time
+        new = [n // 2 for n in new]
+    c = R.Cache(100 + seed, lens=lens, kv=kv, d=d, page=rng.choice([16, 32, 48, 80, 128]),
+                dtype=dtype, layout=rng.choice(["head", "token"]))
+    _parity(c, kv * group, new, before=rng.choice([0, 3]), behind=rng.choice([0, 7]),
+            causal=rng.random() < 0.8, headnorm=rng.choice([0, 1, 2]))
+
+
+def test_share_search_over_many_sequences():
+    """More sequences than one warp looks through, long ones among them, so that items are cut."""
+    lens = [1 + 37 * i % 400 for i in range(100)]
+    lens[7], lens[93] = 9000, 4000
+    new = [1] * 100
+    new[7], new[50], new[93] = 260, 100, 33
+    c = R.Cache(24, lens=lens, kv=2, d=64, page=16)
+    _parity(c, 8, [min(a, b) for a, b in zip(new, lens)])
+
+
+@pytest.mark.parametrize("d,dtype", KINDS)
+def test_steps_of_a_server_together(d, dtype):
+    """step, append and fwd over several steps of growing, idle and ending sequences, against
+    sequences kept on the side: prompts in chunks, single tokens, pages handed on, one graph."""
+    B, kv, H, page, T = 5, 2, 6, 16, 160
+    g = torch.Generator().manual_seed(3)
+    pages, max_pages = 60, 30
+    qk = dtype
+    pools = [torch.full((pages, kv, page, w), float("nan"), device="cuda").to(t)
+             for w, t in ((d, qk), (d, qk), (2 * d, BF16))]
+    table = torch.full((B, max_pages), -1, dtype=torch.int32, device="cuda")
+    kv_len, held = _int([0] * B), _int([0] * B)
+    free, count = _int(list(range(pages))), _int([pages])
+    cache = ops.PagedCache(*pools, table, kv_len)
+    book = ops.PageBook(table, kv_len, held, free, count, page)
+    rot = ops.RotaryTable(64 if d == 64 else 96, neighbours=d == 128)
+    freq, m = G.frequencies(rot.rot)
+    new_len, q_start = _int([0] * B), _int([0] * (B + 1))
+    positions, slots = _int([0] * T), _int([0] * T, torch.int64)
+    x = [torch.zeros(T, h, w, dtype=BF16, device="cuda")
+         for h, w in ((H, d), (H, d), (kv, d), (kv, d), (kv, 2 * d))]
+    q_out = [torch.zeros(T, H, d, device="cuda").to(qk) for _ in range(2)]
+    out = torch.zeros(T, H, 2 * d, dtype=BF16, device="cuda")
+    lam, w = torch.rand(H, generator=g).cuda(), (1 + 0.1 * torch.randn(H, 2 * d, generator=g)).cuda()
+    word = _int([0])
+    ws = torch.empty(ops.ragged_fwd_plan(cache, H, T), dtype=torch.uint8, device="cuda")
+
+    def step():
+        ops.ragged_step(book, new_len, q_start=q_start, positions=positions, slots=slots, status=word)
+        ops.ragged_append(cache, x[2], x[3], x[4], slots, rotary=rot, positions=positions,
+                          q=(x[0], x[1]), q_out=q_out, status=word)
+        ops.ragged_fwd(cache, q_out[0], q_out[1], lam, q_start, norm_w=w, lambda_init=LI, out=out,
+                       workspace=ws, status=word)
+
+    step()  # nothing new; loads the kernels
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    seqs = [[torch.zeros(kv, 0, w, dtype=torch.float64) for w in (d, d, 2 * d)] for _ in range(B)]
+    for new in ([100, 7, 0, 1, 33], [60, 1, 50, 1, 40], [1, 1, 1, 0, -1], [0, 90, -1, 16, 20],
+                [1, 1, 31, 1, 1], [-1, 1, 1, 1, 120]):
+        for t in x:
+            t.copy_(torch.randn(t.shape, generator=g))
+        new_len.copy_(_int(new))
+        if new[0] == 1:
+            graph.replay()
+        else:
+            step()
+        torch.cuda.synchronize()
+        assert int(word) == 0
+        starts = _starts([max(0, n) for n in new])
+        assert q_start.tolist() == starts
+        got, kc = out.clone(), []
+        for b, n in enumerate(new):
+            if n < 0:
+                seqs[b] = [torch.zeros(kv, 0, w, dtype=torch.float64) for w in (d, d, 2 * d)]
+                continue
+            old = seqs[b][0].shape[1]
+            pos = torch.arange(old, old + n)
+            for i, t in enumerate((2, 3, 4)):
+                rows = x[t][starts[b]: starts[b + 1]].double().cpu().transpose(0, 1)
+                if i < 2:  # what the cache holds of them: turned and rounded
+                    y, tol = G.turn(rows, pos, freq, m, rot.neighbours)
+                    held_rows = _cache_rows(pools[i], table[b], page, old, old + n)
+                    assert float(((held_rows - y).abs() - G.rounded(y, tol, qk)).max() if n else 0) <= 0
+                    rows = held_rows
+                seqs[b][i] = torch.cat((seqs[b][i], rows), 1)
+        # the attention against the rows that the cache holds and the queries that were written
+        lens = [s[0].shape[1] for s in seqs]
+        assert kv_len.tolist() == lens and held.tolist() == [-(-n // page) for n in lens]
+        c = _Held(pools, table, lens, kv, d, page, qk)
+        ref, tol = G.attend(c, starts, q_out[0], q_out[1], lam, norm_w=w, lambda_init=LI)
+        R.check(got[: starts[-1]], ref[: starts[-1]], tol[: starts[-1]], "out")
+    assert int(count) + int(held.sum()) == pages
+    ids = free[: int(count)].tolist() + [p for b in range(B) for p in
+                                         table[b, : int(held[b])].tolist()]
+    assert sorted(ids) == list(range(pages))
+
+
+def _cache_rows(pool, table, page, begin, end):
+    at = torch.arange(begin, end, device="cuda")
+    raw = pool.view(torch.uint8) if pool.dtype == E4M3 else pool
+    x = raw[table.long()[at // page], :, at % page].transpose(0, 1).contiguous()
+    return R.f64(x.view(E4M3) if pool.dtype == E4M3 else x).cpu()
+
+
+class _Held(R.Cache):
+    """What a paged cache holds, as paged_ref.Cache has it."""
+
+    def __init__(self, pools, table, lens, kv, d, page, dtype):
+        self.k1, self.k2, self.v = pools
+        self.table, self.lens, self.kv, self.d, self.page, self.dtype = table, lens, kv, d, page, dtype
+        self.B = len(lens)
