@@ -396,44 +396,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             float tile_sum = 0.f;
             // As in the dense forward: against the running reference, whose sums certify the tile,
             // or from the maximum.
-            bool exact = t == 0;
-            if (!exact) {
+            if (t == 0) {
+              tile_sum = softmax_half_first(t_s, key0, sl2, lim, masked, m_run, pk);
+            } else {
               tile_sum = masked ? softmax_half_exp<true>(t_s, key0, m_run, sl2, lim, pk)
                                 : softmax_half_exp<false>(t_s, key0, m_run, sl2, lim, pk);
-              exact = __any_sync(0xffffffffu, !(tile_sum <= CERT_SUM));
-            }
-            if (exact) {
-              float mt = masked ? softmax_half_max<true>(t_s, key0, lim)
-                                : softmax_half_max<false>(t_s, key0, lim);
-              mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-              const float m_new = fmaxf(m_run, mt * sl2 + M_HEADROOM);
-              float alpha = 1.f;
-              if (t == 0) {
-                m_run = m_new;
-              } else if (m_new > m_run) {
-                alpha = ex2_approx(m_run - m_new);
-                m_run = m_new;
-              }
-              if (__any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-                for (int c0 = 0; c0 < DV / 2; c0 += 32) {
-                  uint32_t o[32];
-                  tmem_ld16_x32(t_o + c0, o);
-#pragma unroll
-                  for (int i = 0; i < 32; i += 2) {
-                    const float2 v = __fmul2_rn(
-                        make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
-                        make_float2(alpha, alpha));
-                    o[i] = __float_as_uint(v.x);
-                    o[i + 1] = __float_as_uint(v.y);
-                  }
-                  tmem_st16_x32(t_o + c0, o);
+              if (__any_sync(0xffffffffu, !(tile_sum <= CERT_SUM))) {
+                float mt = masked ? softmax_half_max<true>(t_s, key0, lim)
+                                  : softmax_half_max<false>(t_s, key0, lim);
+                mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+                const float m_new = fmaxf(m_run, mt * sl2 + M_HEADROOM);
+                float alpha = 1.f;
+                if (m_new > m_run) {  // move m whenever the tile exceeds it
+                  alpha = ex2_approx(m_run - m_new);
+                  m_run = m_new;
                 }
+                if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+                  for (int c0 = 0; c0 < DV / 2; c0 += 32) {
+                    uint32_t o[32];
+                    tmem_ld16_x32(t_o + c0, o);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                      const float2 v = __fmul2_rn(
+                          make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
+                          make_float2(alpha, alpha));
+                      o[i] = __float_as_uint(v.x);
+                      o[i + 1] = __float_as_uint(v.y);
+                    }
+                    tmem_st16_x32(t_o + c0, o);
+                  }
+                }
+                l_run *= alpha;
+                const float m_use = m_run == -INFINITY ? 0.f : m_run;
+                tile_sum = masked ? softmax_half_exp<true>(t_s, key0, m_use, sl2, lim, pk)
+                                  : softmax_half_exp<false>(t_s, key0, m_use, sl2, lim, pk);
               }
-              l_run *= alpha;
-              const float m_use = m_run == -INFINITY ? 0.f : m_run;
-              tile_sum = masked ? softmax_half_exp<true>(t_s, key0, m_use, sl2, lim, pk)
-                                : softmax_half_exp<false>(t_s, key0, m_use, sl2, lim, pk);
             }
             l_run += tile_sum;
             tmem_st16_x32(t_s, pk);

@@ -114,5 +114,39 @@ __device__ __forceinline__ float softmax_half_max(uint32_t t_s, int key0, int li
   return v[0];
 }
 
+// A row's first tile, whose reference is not known yet: the maximum of its visible keys (both halves'
+// threads) from the registers that the exponentials are then taken from, so that S is read once.
+// Sets m (-infinity where no key is visible or all logits are) and returns the half row's sum.
+__device__ __forceinline__ float softmax_half_first(uint32_t t_s, int key0, float sl2, int lim,
+                                                    bool masked, float &m,
+                                                    uint32_t (&pk)[kTileColumns / 4]) {
+  float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                   make_float2(0.f, 0.f)};
+  uint32_t a[32], b[32];
+  tmem_ld16_x32_nowait(t_s, a);
+  tmem_ld16_x32_nowait(t_s + 32, b);
+  tmem_ld_wait_x32(a);
+  tmem_ld_wait_x32(b);
+  if (masked) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      a[i] = key0 + i <= lim ? a[i] : 0xFF800000u;  // -infinity
+      b[i] = key0 + 32 + i <= lim ? b[i] : 0xFF800000u;
+    }
+  }
+  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    top[i % 4] = fmaxf(top[i % 4], fmaxf(__uint_as_float(a[i]), __uint_as_float(b[i])));
+  float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+  m = mt * sl2 + M_HEADROOM;
+  const float m_use = m == -INFINITY ? 0.f : m;
+  softmax_chunk_exp<false>(a, key0, 0, m_use, sl2, lim, acc, pk);
+  softmax_chunk_exp<false>(b, key0 + 32, 16, m_use, sl2, lim, acc, pk);
+  const float2 s01 = __fadd2_rn(acc[0], acc[1]), s23 = __fadd2_rn(acc[2], acc[3]);
+  return (s01.x + s01.y) + (s23.x + s23.y);
+}
+
 }  // namespace
 }  // namespace diffattn
