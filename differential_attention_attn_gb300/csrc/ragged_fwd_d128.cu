@@ -447,7 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               } else {
                 tile_sum = masked ? softmax_half_exp<true>(t_s, key0, m_run, sl2, lim, pk)
                                   : softmax_half_exp<false>(t_s, key0, m_run, sl2, lim, pk);
-                if (__any_sync(0xffffffffu, !(tile_sum <= CERT_SUM))) {
+                // (Rows past the segment's last hold whatever lies there, and have no say.)
+                if (__any_sync(0xffffffffu, !(tile_sum <= CERT_SUM) && r < rows)) {
                   float mt = masked ? softmax_half_max<true>(t_s, key0, lim)
                                     : softmax_half_max<false>(t_s, key0, lim);
                   mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));

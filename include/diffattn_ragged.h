@@ -6,7 +6,8 @@
  * The new tokens of B sequences stand behind one another in tensors of N rows:
  * those of sequence b are rows q_start[b] .. q_start[b + 1] - 1 (q_start: device
  * int32 [B + 1], not falling, q_start[0] >= 0); rows outside q_start[0] ..
- * q_start[B] - 1 belong to none and are neither read nor written.  A sequence's
+ * q_start[B] - 1 belong to none: they are not written, and what they hold has no
+ * influence.  A sequence's
  * n tokens are its newest: token i sits at position kv_len[b] - n + i of its
  * cache (kv_len counts them; a negative position is padding).
  *

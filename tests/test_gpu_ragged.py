@@ -388,6 +388,25 @@ def test_keys_and_queries_that_are_not_finite(d):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,new", [([300, 40, 9], [40, 1, 3]), ([2500, 1300], [70, 5])])
+def test_rows_of_none_have_no_influence(d, lens, new):
+    """Not on a bit of the others: the rows of a tile behind a sequence's last are other sequences'
+    or nobody's."""
+    c = R.Cache(25, lens=lens, kv=1, d=d, page=16)
+    starts = _starts(new, 2)
+    T = starts[-1] + 60
+    q1, q2, lam, w = _queries(5, T, 2, d, BF16)
+    got = []
+    for x in (0.0, float("nan"), 3e4):
+        for q in (q1, q2):
+            q[:2], q[starts[-1]:] = x, x
+        out = torch.zeros(T, 2, 2 * d, dtype=BF16, device="cuda")
+        got.append(ops.ragged_fwd(c.ops_cache(), q1, q2, lam, _int(starts), norm_w=w, lambda_init=LI,
+                                  out=out))
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_strided_queries_and_output(d):
     c = R.Cache(20, lens=[500, 90], kv=2, d=d, page=32)  # NaN behind the sequences
     starts = [0, 70, 90]
