@@ -51,7 +51,7 @@ diffattn_status diffragged_step(const diffragged_book *book, const int32_t *new_
       book->reserved != 0)
     return DIFFATTN_ERR_INVALID_ARG;
   if (book->B >= (int64_t{1} << 24) || book->max_pages >= (int64_t{1} << 30) / book->page_size ||
-      book->capacity > INT32_MAX || N > INT32_MAX)
+      book->capacity > (int64_t{1} << 30) || N > (int64_t{1} << 30))
     return DIFFATTN_ERR_UNSUPPORTED;
   if (q_start == nullptr || !aligned(q_start, 4) || !aligned(positions, 4) || !aligned(slots, 8) ||
       !aligned(status, 4))
@@ -109,7 +109,10 @@ diffattn_status diffragged_append(const diffattn_desc *desc, const diffpaged_cac
     if (q && in == out && (fp8 || st7[i].h != st7[5 + i].h || st7[i].n != st7[5 + i].n))
       return DIFFATTN_ERR_INVALID_ARG;
   }
-  if (desc->N > (int64_t{1} << 30) || 2 * H + 4 * kv > 65535) return DIFFATTN_ERR_UNSUPPORTED;
+  // (The kernel's blocks: 16 tokens and a head each at least.)
+  if (desc->N > (int64_t{1} << 30) || 2 * H + 4 * kv > 65535 ||
+      (desc->N / 16 + 1) * (2 * H + 4 * kv) >= (int64_t{1} << 31))
+    return DIFFATTN_ERR_UNSUPPORTED;
   if ((st = require_sm103()) != DIFFATTN_OK) return st;
   const void *const src[5] = {q1, q2, k1, k2, v};
   void *const out[2] = {q1_out, q2_out};

@@ -137,10 +137,8 @@ cudaError_t launch_rows(RaggedAppendParams &p, cudaStream_t stream) {
   }
   constexpr uint32_t kTokens = kThreads / (kD / 16);
   cudaLaunchConfig_t cfg = {};
-  const uint64_t blocks = static_cast<uint64_t>((p.tokens + kTokens - 1) / kTokens) * slices;
-  if (blocks >= (uint64_t{1} << 31)) return cudaErrorInvalidConfiguration;
   p.by_slices = fast_div(slices);
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.gridDim = dim3((p.tokens + kTokens - 1) / kTokens * slices);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

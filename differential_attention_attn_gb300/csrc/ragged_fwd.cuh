@@ -241,9 +241,16 @@ struct Line {
 
 // Where a share begins: in sequence b (p.B for nowhere), `left` steps (whole items: items) into it.
 struct ShareState {
+  unsigned long long rows;
   int32_t total, items, longest, b, left;
   int32_t sums[32];
 };
+
+// The sum over the warp of counts whose sum may need more than 32 bits.
+__device__ __forceinline__ int64_t warp_count(uint32_t n) {
+  return static_cast<int64_t>(__reduce_add_sync(0xffffffffu, n & 0xFFFFu)) +
+         (static_cast<int64_t>(__reduce_add_sync(0xffffffffu, n >> 16)) << 16);
+}
 
 // How a line of `total` steps in `items` items, the longest of `longest` steps, is shared.
 __device__ __forceinline__ Line cut_line(int32_t shares, int32_t total, int32_t items,
@@ -252,7 +259,7 @@ __device__ __forceinline__ Line cut_line(int32_t shares, int32_t total, int32_t 
   // Whole items, one a share, where the longest is not kJoinSteps longer than equal pieces; where
   // there are more of them than shares, equal pieces with the items that begin in each, at most
   // one longer than equal.
-  line.each = total / shares;
+  line.each = total / shares;  // (any number where the rows are wrong: unused then)
   line.mode = items <= shares ? (longest <= line.each + kJoinSteps ? kWhole : kCut)
                               : (longest <= kJoinSteps ? kUncut : kCut);
   line.shares = shares;
@@ -285,15 +292,20 @@ constexpr int kFewSequences = 64;
 __device__ __forceinline__ Line find_share_few(const RaggedParams &p, int32_t index, ShareState *st) {
   const int b0 = 2 * (threadIdx.x % 32);
   int32_t steps[2] = {0, 0}, items[2] = {0, 0}, longest = 0;
+  int64_t rows = 0;
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
+  for (int k = 0; k < 2; ++k) {
+    uint32_t n = 0;
     if (b0 + k < p.B) {
       const Seq s(p, b0 + k);
+      n = s.n;
       steps[k] = steps_of(p, s);
       items[k] = s.tiles * p.kv_heads;
       longest = max(longest, s.longest(p));
       if (s.bad_rows && index == 0) report_bad_page(p.status);
     }
+    rows += warp_count(n);
+  }
   const Line line = cut_line(p.shares, __reduce_add_sync(0xffffffffu, steps[0] + steps[1]),
                              __reduce_add_sync(0xffffffffu, items[0] + items[1]),
                              __reduce_max_sync(0xffffffffu, longest));
@@ -302,6 +314,11 @@ __device__ __forceinline__ Line find_share_few(const RaggedParams &p, int32_t in
   const int32_t end = warp_scan(x0 + x1), target = whole ? index : line.begin(index);
   const uint32_t at = __ballot_sync(0xffffffffu, target < end);
   st->b = p.B;
+  // (Sequences on top of one another could come to any number of steps: none of them is taken.)
+  if (rows > p.N) {
+    if (index == 0) report_bad_page(p.status);
+    return line;
+  }
   if (index < line.shares && at != 0) {
     const int lane = __ffs(at) - 1;
     const int32_t left = target - __shfl_sync(0xffffffffu, end - x0 - x1, lane);
@@ -318,13 +335,16 @@ template <int kThreads>
 __device__ __forceinline__ Line find_share(const RaggedParams &p, int32_t index, ShareState *st) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   if (tid == 0) {
+    st->rows = 0;
     st->total = st->items = st->longest = 0;
     st->b = p.B;
   }
   __syncthreads();
   int32_t total = 0, items = 0, mine = 0, mine_items = 0, longest = 0;
+  int64_t rows = 0;
   for (int32_t b = tid; b < p.B; b += kThreads) {
     const Seq s(p, b);
+    rows += s.n;
     const int32_t t = steps_of(p, s), n = s.tiles * p.kv_heads;
     if (b == tid) {
       mine = t;
@@ -338,7 +358,10 @@ __device__ __forceinline__ Line find_share(const RaggedParams &p, int32_t index,
   total = __reduce_add_sync(0xffffffffu, total);
   items = __reduce_add_sync(0xffffffffu, items);
   longest = __reduce_max_sync(0xffffffffu, longest);
-  if (lane == 0 && total > 0) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) rows += __shfl_xor_sync(0xffffffffu, rows, o);
+  if (lane == 0 && rows > 0) {
+    atomicAdd(&st->rows, static_cast<unsigned long long>(rows));
     atomicAdd(&st->total, total);
     atomicAdd(&st->items, items);
     atomicMax(&st->longest, longest);
@@ -347,8 +370,11 @@ __device__ __forceinline__ Line find_share(const RaggedParams &p, int32_t index,
   const Line line = cut_line(p.shares, st->total, st->items, st->longest);
   const bool whole = line.mode == kWhole;
   const int32_t target = whole ? index : line.begin(index);
+  // (As above.)
+  const bool apart = st->rows <= static_cast<unsigned long long>(p.N);
+  if (!apart && tid == 0 && index == 0) report_bad_page(p.status);
   const int32_t all = whole ? st->items : st->total;
-  if (index < line.shares && target < all) {  // uniform
+  if (apart && index < line.shares && target < all) {  // uniform
     int32_t base = 0;
     for (int32_t b0 = 0; b0 < p.B && base <= target; b0 += kThreads) {
       int32_t x = 0;

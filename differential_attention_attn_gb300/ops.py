@@ -1130,7 +1130,7 @@ def ragged_step(book, new_len, *, q_start, positions=None, slots=None, status=No
     word = None if status is None else _whole("status", status, torch.int32, 1, index)
     handle = _stream_on(book, stream)
     if positions is None and slots is None:
-        T = 2 ** 31 - 1  # no rows to write, and any number of them
+        T = 1 << 30  # no rows to write, and any number of them
     st = (_lib or load()).diffragged_step(book._ref, new, T, start, at, to, word, handle)
     if raw_status:
         return st

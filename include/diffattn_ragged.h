@@ -57,6 +57,9 @@ typedef struct diffragged_book {
  * [N] (int64, page * page_size + row in it), either NULL when not wanted, -1 in
  * rows behind the last token.
  *
+ * Calls on a book are ordered with those that use its lengths and table (same
+ * stream, or synchronised).  N and capacity are at most 2^30.
+ *
  * A step that does not fit (too few free pages, more than N tokens, a sequence
  * longer than its table, a stack that would outgrow its capacity) or whose
  * numbers are wrong (new_len < -1; a negative length or count; held outside
@@ -109,7 +112,8 @@ diffattn_status diffragged_append(const diffattn_desc *desc, const diffpaged_cac
  * A page number outside the pool, a length outside the table or rows outside
  * 0 .. N store DIFFATTN_ERR_PAGE: rows that would have read such a page are NaN
  * (others of the sequence may be), so are all of a bad length, and those of a
- * sequence whose q_start is wrong are not written.
+ * sequence whose q_start is wrong are not written (of the whole batch where its
+ * sequences, wrong ones apart, have more than N rows together).
  *
  * workspace: as for diffpaged_fwd; its size does not depend on the lengths.
  * desc: B sequences, N rows, H, d (64 or 128), dtype, causal, headnorm, eps,

@@ -453,6 +453,20 @@ def test_bad_pages_lengths_and_rows(d):
         assert torch.all(out[starts[-1]:] == 7.0)
 
 
+@pytest.mark.parametrize("B", [40, 90])
+def test_sequences_on_top_of_one_another(B):
+    """Every other one of them is right by itself; together they have many times the rows there are
+    (and could have more steps than 31 bits): reported, and nothing is written."""
+    T = 200
+    c = R.Cache(26, lens=[300] * B, kv=2, d=64, page=16, fill=0.0)
+    q1, q2, lam, w = _queries(7, T, 4, 64, BF16)
+    out, word = torch.full((T, 4, 128), 7.0, dtype=BF16, device="cuda"), _int([0])
+    ops.ragged_fwd(c.ops_cache(), q1, q2, lam, _int([0, T] * (B // 2) + [0]), norm_w=w, out=out,
+                   status=word)
+    torch.cuda.synchronize()
+    assert int(word) == ops.ERR_PAGE and torch.all(out == 7.0)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_repeated_runs_graphs_and_stale_workspaces(d):
     c = R.Cache(22, lens=[3000, 700, 1], kv=2, d=d, page=16)

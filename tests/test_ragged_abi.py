@@ -142,9 +142,9 @@ def test_step_refused(lib):
     for bad in (dict(new=0), dict(q=0), dict(q=FAKE + 2), dict(pos=FAKE + 2), dict(slots=FAKE + 4),
                 dict(status=FAKE + 1), dict(n=-1)):
         assert _step(lib, _book(), **bad) == I, bad
-    for bad in (dict(B=1 << 24), dict(max_pages=1 << 26), dict(capacity=1 << 31)):
+    for bad in (dict(B=1 << 24), dict(max_pages=1 << 26), dict(capacity=(1 << 30) + 1)):
         assert _step(lib, _book(**bad)) == U, bad
-    assert _step(lib, _book(), n=1 << 31) == U
+    assert _step(lib, _book(), n=(1 << 30) + 1) == U
 
 
 def _cache(heads=2, d=64, page=16, pages=8, max_pages=64, **kw):
