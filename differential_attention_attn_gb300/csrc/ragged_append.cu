@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 8)
     return;
   }
   Turn turn;
-  if (turns) turn = make_turn<true>(p.freq, u, p.positions[token], p.scale);
+  if (turns) turn = make_turn<!kFp8>(p.freq, u, p.positions[token], p.scale);
   int64_t page = 0;
   int32_t place = 0;
   uint8_t *y = p.dst[k];

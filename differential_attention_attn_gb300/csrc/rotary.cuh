@@ -28,10 +28,12 @@ struct Turn {
 
 // The turn of pairs 8u .. 8u + 7 at position pos (negated: the turn back).  The product with the
 // 64-bit fraction wraps at whole turns; its upper 32 bits are the angle to 2^-32 of a turn.
-// kShort (outputs of 16 and fewer bits, which hide 2^-21): the sine and cosine by the approximate
+// kShort (bf16 outputs, whose rounding hides 2^-21): the sine and cosine by the approximate
 // instructions, within half a turn of zero off by at most 2^-21.41 and 2^-21.19; eight pairs by
 // sincospif take as long as the memory of four heads' units (221 MB of packed rows 35.3 us, so
-// 34.8; of e4m3 keys 120 MB 23.6 and 22.6).
+// 34.8).  Not where e4m3 is written, whose wide steps show it: a value next to the border between
+// two falls to either side by its last bits (of 12.7 million, 27 to 33 wrongly, so 4 to 14; 120 MB
+// 22.6 us, so 23.6).
 template <bool kShort>
 __device__ __forceinline__ Turn make_turn(const uint64_t *freq, int u, int64_t pos, float scale) {
   Turn t;
