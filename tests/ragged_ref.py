@@ -96,8 +96,13 @@ def attend(c, q_start, q1, q2, lam, *, causal=True, headnorm=1, norm_w=None, eps
 
     The tolerance is paged_ref.attend's with probabilities in the second product as one bf16
     number (bf16 has 8 significant bits, so a step is 2^-7 of the binade's least value and half of
-    one at most 2^-8 of a value, torch.finfo(torch.bfloat16).eps / 2; the sums are of the
-    unrounded ones).
+    one at most 2^-8 of a value, torch.finfo(torch.bfloat16).eps / 2).
+
+    The sum of a row's first tile is of the rounded numbers p (1 + e), |e| <= E = 2^-8, that of the
+    others of the unrounded ones.  With F the first tile's keys and S = sum_F p e <= E,
+        o' - o = (sum_all p v (1 + e)) / (1 + S) - o = (sum_all p e v - S o) / (1 + S),
+    at most (E sum p |v| + E |o|) / (1 - E) for each map: the maps' own |o| beside sum p |v|, and a
+    factor of 1 / (1 - 2^-8) that the last line's 1.01 holds.
     """
     T, H, d = q1.shape
     G = H // c.kv
@@ -127,8 +132,9 @@ def attend(c, q_start, q1, q2, lam, *, causal=True, headnorm=1, norm_w=None, eps
             vs = torch.where(torch.isfinite(v), v, 0.0)
             o = w @ vs
             both = maps[0] + abs(lh) * maps[1]
+            own = (maps[0] @ vs).abs() + abs(lh) * (maps[1] @ vs).abs()
             rel = 2 * (math.log(2) * dx + 2.0 ** -22) + 2 * (n / 16 + 8) * 2.0 ** -23
-            a = (both @ vs.abs()) * (rel[:, None] + 2.0 ** -8 + 2.0 ** -16)
+            a = (both @ vs.abs()) * (rel[:, None] + 2.0 ** -8 + 2.0 ** -16) + own * 2.0 ** -8
             bad = (see[:, :, None] & ~torch.isfinite(v)[None]).any(1) if not \
                 torch.isfinite(v).all() else torch.zeros_like(o, dtype=torch.bool)
             o = torch.where(bad, math.nan, o)

@@ -406,6 +406,24 @@ def test_rows_of_none_have_no_influence(d, lens, new):
     assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
 
 
+@pytest.mark.parametrize("d,dtype", KINDS)
+def test_a_row_of_one_key_gets_its_value(d, dtype):
+    """(1 - lambda) v in fp32, however near lambda is to one: a weight's rounding is in the sum too.
+    Both maps' quotients and products, lambda's and the difference are 2^-24 each of (1 + lambda) |v|
+    at most four in a row."""
+    c = R.Cache(31, lens=[90, 1, 1, 300], kv=2, d=d, page=16, dtype=dtype)
+    starts = _starts([90, 1, 1, 300])
+    q1, q2, lam, _ = _queries(9, starts[-1], 4, d, dtype)
+    lam = torch.tensor([0.99, 0.8, 1.003, 0.0], device="cuda")
+    out = ops.ragged_fwd(c.ops_cache(), q1, q2, lam, _int(starts), headnorm=0)
+    for b in range(4):
+        v = R.f64(c.rows("v", b, 1))[:, 0].repeat_interleave(2, 0)
+        x = lam.double()[:, None]
+        y = (1 - x) * v
+        tol = (1 + x) * v.abs() * 4 * 2.0 ** -24 * 1.01 + y.abs() * 2.0 ** -8
+        R.check(out[starts[b]], y, tol, f"sequence {b}")
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_strided_queries_and_output(d):
     c = R.Cache(20, lens=[500, 90], kv=2, d=d, page=32)  # NaN behind the sequences
