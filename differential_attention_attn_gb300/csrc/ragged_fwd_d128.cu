@@ -17,6 +17,11 @@
 // through distributed shared memory.  Eight warps of their own do this while the
 // softmax warps are at the next item.
 //
+// Bound: the tensor cores (busy 64 % of a call with seven items to a pair) and the
+// items' ends.  2048 tokens behind 16384, 16 heads over 4: 452 us, 1140 TFLOP/s of
+// the 8 d multiply-adds a pair, 1710 of the 12 d executed.  e4m3 keys, six sequences
+// of 2000 to 5003 of them with 513 to 1025 new tokens: 231 us.
+//
 // Tensor memory: S / P at 0 and 128 in turn, O at 256; shared memory: Q 32 KB, two
 // tiles of K (32 KB each) and two of V (64 KB each).
 #include <cuda.h>
@@ -547,10 +552,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (uint32_t n = 0;; ++n) {
         const int ring = n % kSegRing;
-        if (!mbar_wait_warp(&ctrl->seg_full[ring], (n / kSegRing) & 1, abort_flag, kWaitNs)) break;
+        // (Every way out of the loop is agreed on: a segment may come after one warp has given up.)
+        const bool got =
+            mbar_wait_warp(&ctrl->seg_full[ring], (n / kSegRing) & 1, abort_flag, kWaitNs);
         const Segment *g = &ctrl->seg[ring];
-        const int32_t flags = g->flags;
-        if (flags & kStop) break;
+        const int32_t flags = got ? g->flags : kStop;
+        if (flags & kStop) {
+          named_barrier_or(1, kFinish, true);
+          break;
+        }
         const int32_t rows = g->tokens * p.group;
         const int32_t pos = g->first + token;
         const int32_t h = g->hk * p.group + head;

@@ -11,10 +11,20 @@
 //     last one's rows are still being finished;
 //   - a warp of its own loads the queries, the heads of a group beside one
 //     another ({d, group, tokens} boxes, so that any group up to 64 fills the
-//     128 rows as far as whole tokens go), and clears what masked rows of a value
-//     tile must not spread;
+//     128 rows as far as whole tokens go); the softmax warps clear what masked
+//     rows of a value tile must not spread;
 //   - softmax warps whose 16 rows are all past the segment's last one (a single
 //     token of four heads fills one warp of eight) only pass the barriers on.
+//
+// Bound: from a few dozen rows on, the two softmaxes in turn with the products (a
+// tile 1.4 us; its products alone 0.75 us, its exponentials 0.5 us); the tensor
+// pipe is busy 59 % of the time, the issue slots 47 %.  2048 tokens behind 32768,
+// 32 heads over 8: 1151 us, 926 TFLOP/s of 8 d multiply-adds a pair, 1390 of the 12 d
+// executed.  A single token a sequence is bound by the keys' and values' bytes, a
+// start of 6 us and the join.  A CTA for each map (as at d = 128) took 1272 us, with
+// the next tile's logits read ahead into registers 1460; steps of 64 keys, whose
+// logits are made while the other half's softmax runs, 1268 (the fixed part of a
+// step, 80 of 310 instructions a warp, doubles).
 //
 // Tensor memory (512 columns): S1 / P1 at 0, S2 / P2 at 128, O1 at 256, O2 at 384;
 // shared memory: Q1, Q2 32 KB, three 32 KB tiles of K1, K2 and three of V.
@@ -374,10 +384,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t c = 0, filled = 0;
     for (uint32_t n = 0;; ++n) {
       const int ring = n % kSegRing;
-      if (!mbar_wait_warp(&ctrl->seg_full[ring], (n / kSegRing) & 1, abort_flag, kWaitNs)) break;
+      // (Every way out of the loop is agreed on: a segment may come after one warp has given up.)
+      const bool got =
+          mbar_wait_warp(&ctrl->seg_full[ring], (n / kSegRing) & 1, abort_flag, kWaitNs);
       const Segment *g = &ctrl->seg[ring];
-      const int32_t flags = g->flags;
-      if (flags & kStop) break;
+      const int32_t flags = got ? g->flags : kStop;
+      if (flags & kStop) {
+        named_barrier_or(1, kSoftmax, true);
+        break;
+      }
       const int32_t tiles = g->tiles, rows = g->tokens * p.group;
       const int32_t pos = g->first + token;
       const int32_t h = g->hk * p.group + head;
