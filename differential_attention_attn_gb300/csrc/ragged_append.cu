@@ -13,7 +13,7 @@
 // small blocks at full occupancy (256 threads at three blocks an SM: 38.0 us).
 // Measured on GB300: 9004 tokens of 32 heads over 8 key/value heads at d = 64,
 // 221 MB: 34.8 us, 94 % of the copy rate; 6165 tokens at d = 128 with e4m3 keys,
-// 120 MB: 23.6 us, 75 %; 64 single tokens 2.1 us.
+// 120 MB: 23.8 us, 74 %; 64 single tokens 2.1 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -31,22 +31,28 @@ struct Turn {
 // kShort (bf16 outputs, whose rounding hides 2^-21): the sine and cosine by the approximate
 // instructions, within half a turn of zero off by at most 2^-21.41 and 2^-21.19; eight pairs by
 // sincospif take as long as the memory of four heads' units (221 MB of packed rows 35.3 us, so
-// 34.8).  Not where e4m3 is written, whose wide steps show it: a value next to the border between
-// two falls to either side by its last bits (of 12.7 million, 27 to 33 wrongly, so 4 to 14; 120 MB
-// 22.6 us, so 23.6).
+// 34.8).  Not where fp32 or e4m3 is written: e4m3's wide steps show the last bits of a value next to
+// the border between two (of 12.7 million, 27 to 33 fell to the wrong side, so 3 to 11; 120 MB
+// 22.6 us, so 23.8).
 template <bool kShort>
 __device__ __forceinline__ Turn make_turn(const uint64_t *freq, int u, int64_t pos, float scale) {
   Turn t;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint64_t angle = static_cast<uint64_t>(pos) * freq[8 * u + i];
-    const float part = static_cast<float>(static_cast<int32_t>(angle >> 32));  // of 2^31: half a turn
+    const int32_t part = static_cast<int32_t>(angle >> 32);  // of 2^31: half a turn
+    constexpr float kStep = 1.4629180792671596e-9f;          // pi 2^-31
     if constexpr (kShort) {
-      const float x = part * 1.4629180792671596e-9f;  // pi 2^-31
+      const float x = static_cast<float>(part) * kStep;
       t.s[i] = __sinf(x);
       t.c[i] = __cosf(x);
     } else {
-      sincospif(part * 0x1p-31f, &t.s[i], &t.c[i]);
+      // fp32 has the upper 24 bits; the last eight are a turn of d <= 2^-21.3 more, to first order.
+      float s, c;
+      sincospif(static_cast<float>(part & ~0xFF) * 0x1p-31f, &s, &c);
+      const float d = static_cast<float>(part & 0xFF) * kStep;
+      t.s[i] = fmaf(c, d, s);
+      t.c[i] = fmaf(-s, d, c);
     }
     t.s[i] *= scale;
     t.c[i] *= scale;

@@ -26,14 +26,16 @@ def frequencies(rot, base=10000.0, scaling=None, factor=1.0, original=0.0, fast=
     return torch.tensor(f, dtype=torch.float64), m
 
 
-def turn(x, pos, freq, m, neighbours, inverse=False):
+def turn(x, pos, freq, m, neighbours, inverse=False, short=True):
     """(y, tolerance before y is rounded): x [..., N, d] float64 turned by pos [..., N].
 
-    An angle is off by 2^-24 of half a turn (its fp32 rounding; the 64-bit product's upper half
-    adds 2^-32 of a turn) and once more where it becomes radians, the sine and cosine by 2^-21.19
-    (the bound of CUDA's __cosf between -pi and pi; 2 ulp = 2^-22 where sincospif is used), the
-    scale and the two products and their sum by 2^-24 each: with |c|, |s| <= m, that is
-    (2 pi + 2^2.81 + 3) 2^-24 (|a| + |b|) m at most, below 16.4 * 2^-24.  The frequencies of both
+    Short (bf16 is written): an angle is off by 2^-24 of half a turn (its fp32 rounding; the 64-bit
+    product's upper half adds 2^-32 of a turn) and once more where it becomes radians, the sine and
+    cosine by 2^-21.19 (the bound of CUDA's __cosf between -pi and pi), the scale and the two
+    products and their sum by 2^-24 each: with |c|, |s| <= m, that is
+    (2 pi + 2^2.81 + 3) 2^-24 (|a| + |b|) m at most, below 16.4 * 2^-24.  Else the angle has its 32
+    bits (2^-29.3 radians), sine and cosine are off by 2 ulp, 4 * 2^-24, at most, and by 2^-24 where
+    the last eight bits are added: 4 + 1 + 3 and a little, 8.1 * 2^-24.  The frequencies of both
     sides carry 2^-51 of a far angle.
     """
     r = 2 * freq.numel()
@@ -46,7 +48,7 @@ def turn(x, pos, freq, m, neighbours, inverse=False):
                                                                    slice(r // 2, r))
     a, b = x[..., ia], x[..., ib]
     y[..., ia], y[..., ib] = a * c - b * s, a * s + b * c
-    t = (a.abs() + b.abs()) * m * (16.4 * 2.0 ** -24 + angle.abs() * 2.0 ** -51)
+    t = (a.abs() + b.abs()) * m * ((16.4 if short else 8.1) * 2.0 ** -24 + angle.abs() * 2.0 ** -51)
     tol[..., ia], tol[..., ib] = t, t
     return y, tol
 

@@ -172,7 +172,8 @@ def test_append(dtype, d, rot, layout, pool, neighbours, T):
     freq, m = G.frequencies(rot) if rot else (torch.zeros(0, dtype=torch.float64), 1.0)
 
     def turned(x, to):
-        y, t = G.turn(x.double().transpose(0, 1), pos, freq, m, neighbours)
+        y, t = G.turn(x.double().transpose(0, 1), pos, freq, m, neighbours,
+                      short=dtype == BF16)
         y, t = y.transpose(0, 1), t.transpose(0, 1)
         if to == E4M3:
             y = y.clamp(-448.0, 448.0)
@@ -639,7 +640,8 @@ def test_steps_of_a_server_together(d, dtype):
             for i, t in enumerate((2, 3, 4)):
                 rows = x[t][starts[b]: starts[b + 1]].double().cpu().transpose(0, 1)
                 if i < 2:  # what the cache holds of them: turned and rounded
-                    y, tol = G.turn(rows, pos, freq, m, rot.neighbours)
+                    y, tol = G.turn(rows, pos, freq, m, rot.neighbours,
+                                    short=qk == BF16)
                     held_rows = _cache_rows(pools[i], table[b], page, old, old + n)
                     assert float(((held_rows - y).abs() - G.rounded(y, tol, qk)).max() if n else 0) <= 0
                     rows = held_rows

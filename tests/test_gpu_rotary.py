@@ -26,7 +26,8 @@ def _rows(seed, B, heads, N, d, dtype, layout):
 def _check(table, kw, xs, ys, pos, inverse=False):
     freq, m = G.frequencies(**kw)
     for x, y in zip(xs, ys):
-        ref, tol = G.turn(x.double(), pos[:, None], freq, m, table.neighbours, inverse)
+        ref, tol = G.turn(x.double(), pos[:, None], freq, m, table.neighbours, inverse,
+                          short=x.dtype == BF16)
         tol = G.rounded(ref, tol, x.dtype)
         assert y.dtype == x.dtype and float(((y.double() - ref).abs() - tol).max()) <= 0
         r = kw["rot"]
