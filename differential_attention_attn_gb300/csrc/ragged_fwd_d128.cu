@@ -6,8 +6,8 @@
 // width, fwd_d128_sm103.cu) take every product of queries and keys and every
 // exponential twice.  One map to a CTA leaves 256 columns for two S in turn, so
 // that S of the next tile is made while this one's softmax and product run, and
-// is an ordinary softmax attention whose tensor work (12 d^2 multiply-adds a
-// row and key tile of both maps, 4 of them for S) hides its exponentials: half
+// is an ordinary softmax attention whose tensor work (6 d^2 multiply-adds a
+// row and key tile of both maps, 2 of them for S) hides its exponentials: half
 // as many per product as at d = 64.  Values are read by both CTAs of the pair,
 // from L2 the second time.
 //
@@ -19,7 +19,7 @@
 //
 // Bound: the tensor cores (busy 64 % of a call with seven items to a pair) and the
 // items' ends.  2048 tokens behind 16384, 16 heads over 4: 452 us, 1140 TFLOP/s of
-// the 8 d multiply-adds a pair, 1710 of the 12 d executed.  e4m3 keys, six sequences
+// the 8 d flop a pair, 1710 of the 12 d executed.  e4m3 keys, six sequences
 // of 2000 to 5003 of them with 513 to 1025 new tokens: 231 us.
 //
 // Tensor memory: S / P at 0 and 128 in turn, O at 256; shared memory: Q 32 KB, two

@@ -2,7 +2,7 @@
 // one CTA, on tcgen05.
 //
 // Per key tile S1 = Q1 K1^T, S2 = Q2 K2^T into tensor memory, P_k = 2^(x - m_k)
-// as bf16 over S_k, O1 += P1 V, O2 += P2 V: 12 d multiply-adds a pair, and two
+// as bf16 over S_k, O1 += P1 V, O2 += P2 V: 6 d multiply-adds a pair, and two
 // exponentials.  The products and the softmax are those of the dense forward
 // (fwd_bf16_sm103.cu): two threads a row and map, exponentials against a running
 // reference that sums certify, the exact path where they do not.  What differs:
@@ -19,7 +19,7 @@
 // Bound: from a few dozen rows on, the two softmaxes in turn with the products (a
 // tile 1.4 us; its products alone 0.75 us, its exponentials 0.5 us); the tensor
 // pipe is busy 59 % of the time, the issue slots 47 %.  2048 tokens behind 32768,
-// 32 heads over 8: 1151 us, 926 TFLOP/s of 8 d multiply-adds a pair, 1390 of the 12 d
+// 32 heads over 8: 1151 us, 926 TFLOP/s of the 8 d flop a pair, 1390 of the 12 d
 // executed.  A single token a sequence is bound by the keys' and values' bytes, a
 // start of 6 us and the join.  A CTA for each map (as at d = 128) took 1272 us, with
 // the next tile's logits read ahead into registers 1460; steps of 64 keys, whose
