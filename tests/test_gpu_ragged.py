@@ -440,6 +440,64 @@ def test_strided_queries_and_output(d):
     assert torch.equal(out, want)
 
 
+def _far_rows(T, heads, width, dtype=BF16):
+    """[T, heads, width] with 2^31 elements from token to token."""
+    x = torch.empty((T - 1) * 2 ** 31 + heads * width, dtype=dtype, device="cuda")
+    return x.as_strided((T, heads, width), (2 ** 31, width, 1))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_offsets_past_32_bits(d):
+    """Pages, packed rows and outputs whose byte and element offsets do not fit 32 bits."""
+    page, H, T, n = 64, 2, 3, 150
+    P = 2 ** 32 // (page * 2 * d)  # v: 2^32 elements
+    pools = [torch.empty(P, 1, page, w, dtype=BF16, device="cuda") for w in (d, d, 2 * d)]
+    far = [P - 1, P - 7, P // 2 + 3]
+    c = R.Cache(41, lens=[n], kv=1, d=d, page=page)
+    for k, f in enumerate(far):
+        for big, t in zip(pools, (c.k1, c.k2, c.v)):
+            big[f] = t[int(c.table[0, k])]
+    cache = ops.PagedCache(*pools, torch.tensor([far], dtype=torch.int32, device="cuda"), c.kv_len)
+    new = _packed(42, T, [(1, d), (1, d), (1, 2 * d)], "plain")
+    rows = [_far_rows(T, 1, w) for w in (d, d, 2 * d)]
+    slots = torch.empty(T, dtype=torch.int64, device="cuda")
+    for i in range(T):  # the last three tokens: in both caches
+        at = n - T + i
+        slots[i] = far[at // page] * page + at % page
+        for x, y, t in zip(rows, new, (c.k1, c.k2, c.v)):
+            x[i] = y[i]
+            t[int(c.table[0, at // page]), :, at % page] = y[i]
+    q1, q2, lam, w = _queries(43, T, H, d, BF16)
+    q_far, q_out = [_far_rows(T, H, d) for _ in range(2)], [_far_rows(T, H, d) for _ in range(2)]
+    for x, y in zip(q_far, (q1, q2)):
+        x.copy_(y)
+    ops.ragged_append(cache, *rows, slots, q=q_far, q_out=q_out)
+    assert torch.equal(q_out[0], q1) and torch.equal(q_out[1], q2)
+    out = ops.ragged_fwd(cache, *q_out, lam, _int([0, T]), norm_w=w, lambda_init=LI,
+                         out=_far_rows(T, H, 2 * d))
+    ref, tol = G.attend(c, [0, T], q1, q2, lam, norm_w=w, lambda_init=LI)
+    R.check(out, ref, tol, "out")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_two_streams_at_once(d):
+    """Calls that run side by side, each with a workspace of its own."""
+    calls = []
+    for seed, lens, new in ((44, [3000, 70, 900], [200, 1, 33]), (45, [500, 2500], [130, 7])):
+        c = R.Cache(seed, lens=lens, kv=2, d=d, page=16)
+        starts = _starts(new)
+        q1, q2, lam, w = _queries(seed, starts[-1], 4, d, BF16)
+        cache, at = c.ops_cache(), _int(starts)
+
+        def call(stream=None, cache=cache, q1=q1, q2=q2, lam=lam, w=w, at=at):
+            return ops.ragged_fwd(cache, q1, q2, lam, at, norm_w=w, lambda_init=LI, stream=stream)
+        calls.append((call, call(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [(call(stream), want) for _ in range(10) for call, want, stream in calls]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x, want in got)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_bad_pages_lengths_and_rows(d):
     """Reported, and nothing outside the pool or the batch is touched."""

@@ -92,6 +92,25 @@ def test_in_place_and_many_rows(heads):
     assert got[0] is same[0] and all(torch.equal(a, b) for a, b in zip(same, ys))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_offsets_past_32_bits(dtype):
+    """Rows 2^31 elements apart, from batch to batch, head to head or token to token, in place and
+    into another tensor."""
+    kw = dict(rot=64)
+    table = ops.RotaryTable(**kw)
+    for axis in range(3):
+        shape = [1, 1, 1, 64]
+        shape[axis] = 3
+        strides = [64 * shape[1] * shape[2], 64 * shape[2], 64, 1]
+        strides[axis] = 2 ** 31
+        x = torch.empty(2 ** 32 + 64, dtype=dtype, device="cuda").as_strided(shape, strides)
+        x.copy_(_rows(9 + axis, *shape, dtype, "head"))
+        pos = torch.arange(7, 7 + shape[2], device="cuda")
+        y = ops.rotary(table, [x], start=7)[0]
+        _check(table, kw, [x], [y], pos.expand(shape[0], shape[2]))
+        assert torch.equal(ops.rotary(table, [x], start=7, outs=[x])[0], y)
+
+
 def test_gradient_against_differences():
     """sum(dy * rotary(x)) changes by the gradient: the map is linear, so one difference is exact
     up to fp32 (64-bit sums; each of the 2 * 3 * 20 * 64 terms is off by at most 12 * 2^-24 of the
