@@ -385,10 +385,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t n = 0;; ++n) {
       const int ring = n % kSegRing;
       // (Every way out of the loop is agreed on: a segment may come after one warp has given up.)
-      const bool got =
-          mbar_wait_warp(&ctrl->seg_full[ring], (n / kSegRing) & 1, abort_flag, kWaitNs);
+      if (!mbar_wait_warp(&ctrl->seg_full[ring], (n / kSegRing) & 1, abort_flag, kWaitNs)) {
+        named_barrier_or(1, kSoftmax, true);
+        break;
+      }
       const Segment *g = &ctrl->seg[ring];
-      const int32_t flags = got ? g->flags : kStop;
+      const int32_t flags = g->flags;
       if (flags & kStop) {
         named_barrier_or(1, kSoftmax, true);
         break;
