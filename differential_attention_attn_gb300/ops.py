@@ -1019,6 +1019,8 @@ def _rotary(table, tensors, positions, start, outs, status, stream, raw_status, 
         raise ValueError("one to four tensors, [B, heads, N, d] each")
     index, dtype = table.index, x[0].dtype
     shapes = tuple([t.shape for t in x])
+    if outs is not None and tuple([t.shape for t in outs]) != shapes:
+        raise ValueError("outs must be as many tensors of the inputs' shapes")
     key = (dtype, shapes, tuple([t.stride() for t in x]),
            None if outs is None else tuple([t.stride() for t in outs]))
     call = table._calls.get(key) if status is None else None
@@ -1031,8 +1033,6 @@ def _rotary(table, tensors, positions, start, outs, status, stream, raw_status, 
     if outs is None:
         outs = [_new_on(stream, s, dtype, table.device) for s in shapes]
     else:
-        if len(outs) != n or tuple([t.shape for t in outs]) != shapes:
-            raise ValueError("outs must be as many tensors of the inputs' shapes")
         for t in outs:
             if t.dtype != dtype or t.get_device() != index:
                 raise ValueError("outs must be of the inputs' dtype, on the table's device")
@@ -1172,7 +1172,12 @@ def ragged_append(cache, k1, k2, v, slots, *, rotary=None, positions=None, q=Non
     index, bf16 = cache.index, torch.bfloat16
     ts = [k1, k2, v]
     H = cache.kv_heads
-    if q is not None:
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out goes with q")
+    else:
+        if len(q) != 2 or q_out is not None and len(q_out) != 2:
+            raise ValueError("q and q_out must be two tensors each")
         H = q[0].shape[1] if q[0].dim() == 3 else -1
         if q_out is None:
             q_out = [_new_on(stream, q[0].shape, cache.dtype, cache.device) for _ in range(2)]
@@ -1219,7 +1224,7 @@ def ragged_fwd_plan(cache, H: int, T: int, *, raw_status: bool = False):
 
 def _new_ragged_fwd(cache, key, status):
     shape, strides, causal, headnorm, eps, lambda_init = key
-    if len(shape) != 3 or shape[2] != cache.d:
+    if shape[2] != cache.d:
         raise ValueError(f"q1 and q2 must be [T, H, {cache.d}]")
     if any(s[2] != 1 for s in strides):
         raise ValueError("rows must be contiguous (last stride 1)")
@@ -1233,7 +1238,7 @@ def _new_ragged_fwd(cache, key, status):
     out_shape = (T, H, 2 * d)
     st3 = [_strides_of((1, *n), (1, *s)) for n, s in zip((shape, shape, out_shape), strides)]
     arr = (Strides * 3)(*(Strides(0, s.n, s.h) for s in st3))
-    return OK, cache._keep(key, status, (ref, out_shape, H, need.value, arr))
+    return OK, cache._keep(key, status, (ref, need.value, arr))
 
 
 def ragged_fwd(cache, q1, q2, lam, q_start, *, causal: bool = True, headnorm: int = 1, norm_w=None,
@@ -1252,10 +1257,13 @@ def ragged_fwd(cache, q1, q2, lam, q_start, *, causal: bool = True, headnorm: in
     shape = q1.shape
     if q2.shape != shape:
         raise ValueError(f"q2 must be {tuple(shape)}, as q1")
+    if len(shape) != 3:
+        raise ValueError(f"q1 and q2 must be [T, H, {cache.d}]")
+    out_shape = (shape[0], shape[1], 2 * shape[2])
     if out is None:
-        if len(shape) != 3:
-            raise ValueError(f"q1 and q2 must be [T, H, {cache.d}]")
-        out = _new_on(stream, (shape[0], shape[1], 2 * shape[2]), torch.bfloat16, cache.device)
+        out = _new_on(stream, out_shape, torch.bfloat16, cache.device)
+    elif out.shape != out_shape or out.dtype != torch.bfloat16 or out.get_device() != index:
+        raise ValueError("out must be bfloat16 [T, H, 2d] on the cache's device")
     key = (shape, (q1.stride(), q2.stride(), out.stride()), bool(causal), int(headnorm), float(eps),
            float(lambda_init))
     call = cache._calls.get(key) if status is None else None
@@ -1265,7 +1273,8 @@ def ragged_fwd(cache, q1, q2, lam, q_start, *, causal: bool = True, headnorm: in
             if raw_status:
                 return st
             _check(st)
-    ref, out_shape, H, need, strides = call
+    ref, need, strides = call
+    H = shape[1]
     if q1.dtype != dtype or q2.dtype != dtype:
         raise ValueError(f"q1 and q2 must be {dtype}, as the cache's keys")
     if q1.get_device() != index or q2.get_device() != index or lam.get_device() != index:
@@ -1275,8 +1284,6 @@ def ragged_fwd(cache, q1, q2, lam, q_start, *, causal: bool = True, headnorm: in
     if norm_w is not None and (norm_w.dtype != f32 or norm_w.numel() != H * out_shape[2] or
                                not norm_w.is_contiguous() or norm_w.get_device() != index):
         raise ValueError("norm_w must be contiguous float32 [H, 2d] on the cache's device")
-    if out.shape != out_shape or out.dtype != torch.bfloat16 or out.get_device() != index:
-        raise ValueError("out must be bfloat16 [T, H, 2d] on the cache's device")
     start = _whole("q_start", q_start, torch.int32, cache.B + 1, index)
     handle = _stream_on(cache, stream)
     ws, ws_bytes, _hold = _workspace(workspace, need, cache, stream)

@@ -8,6 +8,7 @@ import re
 import subprocess
 
 import pytest
+import torch
 
 from differential_attention_attn_gb300 import build as libbuild
 from differential_attention_attn_gb300 import ops
@@ -251,3 +252,48 @@ def test_what_other_kernels_write_is_not_read_through_the_read_only_path():
     assert len(files) >= 8
     for path in files:
         assert "__ldg(" not in open(path).read(), path
+
+
+# ---- the binding's own checks -----------------------------------------------------------------
+
+def _without_a_device(cls, **fields):
+    """An object of the binding as far as its checks of arguments go: they come before any launch,
+    and a tensor without a device has the index -1."""
+    x = cls.__new__(cls)
+    for name, value in dict(fields, index=-1, device=torch.device("cpu"), _calls={}, _ref=None).items():
+        setattr(x, name, value)
+    return x
+
+
+def test_first_rotary_call_with_wrong_outputs_names_them():
+    x = torch.zeros(2, 4, 8, 64, dtype=torch.bfloat16)
+    for outs in ([], [x], [x] * 3, [x[0], x[0]], [x[0, 0, 0], x], [x, x[..., None]]):
+        table = _without_a_device(ops.RotaryTable)
+        with pytest.raises(ValueError, match="outs must be as many tensors of the inputs' shapes"):
+            ops.rotary(table, [x, x], outs=outs)
+        assert not table._calls
+
+
+def _cache_without_a_device():
+    return _without_a_device(ops.PagedCache, dtype=torch.bfloat16, kv_heads=2, d=64, B=1,
+                             code=ops.BF16)
+
+
+def test_first_append_with_wrong_queries_or_outputs_names_them():
+    k, v, q = (torch.zeros(3, h, w, dtype=torch.bfloat16) for h, w in ((2, 64), (2, 128), (4, 64)))
+    slots = torch.zeros(3, dtype=torch.int64)
+    for kw in (dict(q=(q,)), dict(q=(q, q, q)), dict(q=(q, q), q_out=(q,)),
+               dict(q=(q, q), q_out=[q] * 3), dict(q=()), dict(q_out=(q, q))):
+        with pytest.raises(ValueError, match="q_out"):
+            ops.ragged_append(_cache_without_a_device(), k, k, v, slots, **kw)
+    for kw in (dict(q=(q, q), q_out=(q, q[0])), dict(q=(q, q[0])), dict(q=(q[0], q[0]))):
+        with pytest.raises(ValueError, match="must be"):
+            ops.ragged_append(_cache_without_a_device(), k, k, v, slots, **kw)
+
+
+def test_first_forward_with_an_output_of_other_axes_names_it():
+    q, lam = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(4)
+    for shape in ((3, 512), (1536,), (1, 3, 4, 128), (3, 4, 64), (4, 4, 128)):
+        with pytest.raises(ValueError, match="out must be"):
+            ops.ragged_fwd(_cache_without_a_device(), q, q, lam, torch.zeros(2, dtype=torch.int32),
+                           out=torch.zeros(shape, dtype=torch.bfloat16))
