@@ -177,7 +177,8 @@ __global__ void __launch_bounds__(kThreads, 1) diffragged_step_kernel(const Step
   if (any_bad || count0 < 0 || count0 + given > p.capacity || taken > count0 + given ||
       rows > p.N) {
     for (int32_t b = flat.first; b <= p.B; b += flat.step) p.q_start[b] = 0;
-    for (int64_t r = flat.first; r < p.N; r += flat.step) write_none(p, r);
+    if (p.rows)  // (N may be anything where no rows are wanted)
+      for (int64_t r = flat.first; r < p.N; r += flat.step) write_none(p, r);
     if (tid == 0 && rank == 0) report_bad_page(p.status);
     return;
   }

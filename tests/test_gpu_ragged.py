@@ -132,6 +132,46 @@ def test_step_outputs_left_out_graph_and_empty():
         assert q0.tolist() == [0] and set(pos.tolist()) == {-1}
 
 
+@pytest.mark.parametrize("N", [4096, 4097])
+@pytest.mark.parametrize("B", [256, 257, 1024, 1025])
+def test_step_at_the_borders_of_its_launch_shapes(B, N):
+    """One block or a cluster of eight, 1024 sequences at a time: from 4097 rows or 257 sequences on
+    the cluster, from 1025 sequences on a second round.  The pool has only the pages that others give
+    back in the same step; with one page less it does not fit."""
+    rng = random.Random(B + N)
+    lens = [rng.randint(1, 16) if b % 2 == 0 else rng.choice([0, 16]) for b in range(B)]
+    new = [-1 if b % 2 == 0 else 1 for b in range(B)]
+    taking = range(1, B, 2)
+    if B % 2:  # one ends more than take: two pages
+        new[1] = 17
+    left = N - sum(n for n in new if n > 0)
+    for b in taking:
+        more = min(left, -new[b] % 16, rng.randint(0, 30))
+        new[b], left = new[b] + more, left - more
+    want = _step(Book(B, lens, 16, 4, spare=0), new, N)
+    assert want["free_count"] == [0]
+    new[B - 2 if B % 2 else B - 1] += 16  # a page more than there is
+    assert "kv_len" not in _step(Book(B, lens, 16, 4, spare=0), new, N + 16)
+
+
+def test_step_without_rows_that_does_not_fit():
+    """Neither positions nor slots: any number of rows, but no more pages than there are."""
+    for B in (3, 300):
+        book = Book(8, [20] * B, 16, 6, spare=B - 1)
+        before = {t: getattr(book, t).clone() for t in BOOK}
+        q, word = torch.full((B + 1,), 77, dtype=torch.int32, device="cuda"), _int([0])
+        ops.ragged_step(book.ops, _int([13] * B), q_start=q, status=word)  # a page each
+        torch.cuda.synchronize()
+        assert int(word) == ops.ERR_PAGE and q.tolist() == [0] * (B + 1)
+        for t in BOOK:
+            assert torch.equal(getattr(book, t), before[t]), t
+        word.zero_()
+        ops.ragged_step(book.ops, _int([13] * (B - 1) + [12]), q_start=q, status=word)
+        torch.cuda.synchronize()
+        assert int(word) == 0 and book.kv_len.tolist() == [33] * (B - 1) + [32]
+        assert q.tolist() == [13 * b for b in range(B)] + [13 * B - 1] and int(book.free_count) == 0
+
+
 # ---- append -----------------------------------------------------------------------------------
 
 def _packed(seed, T, heads_widths, layout="packed", scale=1.0):
