@@ -111,6 +111,57 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
+// What a row's O of the pieces before counts times, then that of the piece itself ([2][row], behind
+// what the pairs hand over): from a softmax warp to a finishing one, in turn.
+__device__ __forceinline__ float *factors_at(const RaggedParams &p, uint32_t turn) {
+  return p.swap + (2ll * p.shares * 2 * 128 + (blockIdx.x * 2ll + turn) * 2) * kTile;
+}
+
+// A row's reference and sum of a piece with those of the pieces before, which are in the part; leaves
+// what either's O counts times.  (These three are functions of their own, so that the short items' code
+// keeps its registers.)
+__device__ __noinline__ float2 merge_sums(const RaggedParams &p, const Segment &g, int map, int r,
+                                          uint32_t turn, float m, float l) {
+  const float *part = p.part + (g.slot * 2ll + map) * part_floats(DV) + r;
+  const Merge x = merge_states(part[DV * kTile], part[(DV + 1) * kTile], m, l);
+  float *factors = factors_at(p, turn) + r;
+  factors[0] = x.before;
+  factors[kTile] = x.now;
+  return make_float2(x.m, x.l);
+}
+
+// A piece's O in tensor memory with that of the pieces before, which is in the part.  (Each thread
+// reads what it has written itself.)
+__device__ __noinline__ void merge_rows(const RaggedParams &p, const Segment &g, int map, int r, int key0,
+                                        uint32_t turn, uint32_t t_o) {
+  const float *part = p.part + (g.slot * 2ll + map) * part_floats(DV) + r;
+  const float *factors = factors_at(p, turn) + r;
+  const bool mine = r < g.tokens * p.group;
+  const float before = mine ? factors[0] : 0.f, now = mine ? factors[kTile] : 1.f;
+#pragma unroll 1
+  for (int c0 = 0; c0 < 4; ++c0) {
+    const int col = 128 * (c0 >> 1) + 32 * (c0 & 1);
+    uint32_t o[32];
+    tmem_ld16_x32(t_o + col, o);
+    if (mine) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        o[i] = __float_as_uint(__uint_as_float(o[i]) * now + part[(key0 + col + i) * kTile] * before);
+    }
+    __syncwarp();
+    tmem_st16_x32(t_o + col, o);
+  }
+  tmem_st_wait();
+}
+
+// Hands over what this CTA's finishing threads have written for the other, and takes what that one has:
+// the `handed`-th time.
+__device__ __noinline__ bool exchange_pair(Ctrl *ctrl, uint32_t peer_bar, uint32_t handed) {
+  named_barrier_sync(1, kFinish);
+  if (threadIdx.x == 32 * kFinishWarp) peer_arrive(peer_bar + 8 * (handed & 1));
+  return peer_wait(&ctrl->peer[handed & 1], (handed >> 1) & 1, &ctrl->abort);
+}
+
 template <bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1)
     diffragged_fwd_d128_kernel(const __grid_constant__ CUtensorMap tm_q1,
@@ -220,14 +271,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (bool left = ends_one; ok;) {
         const bool walk = w.more(p);
         if (!walk && !left) break;
-        const Segment g = walk ? w.segment(p, share) : end_of_one;
+        const Segment all = walk ? w.segment(p, share) : end_of_one;
         if (!walk) left = false;
-        if (g.tile0 == 0 && !(g.flags & kDirect)) join = w.join(line, share, g);
-        const int r = n % kSegRing;
-        publish(g);
-        if (!ok) break;
-        if ((g.flags & kBadLen) && lane == 0) report_bad_page(p.status);
-        if (!(g.flags & kEmpty)) {
+        if (all.tile0 == 0 && !(all.flags & kDirect)) join = w.join(line, share, all);
+        if ((all.flags & kBadLen) && lane == 0) report_bad_page(p.status);
+        int32_t rest = all.tiles;
+        while (true) {
+          const Segment g = piece_of(walk ? w.segment(p, share) : end_of_one, rest);
+          const int r = n % kSegRing;
+          publish(g);
+          if (!ok || (g.flags & kEmpty)) break;
           int32_t key = g.tile0 * kTile + row0;
           int32_t id = page_of(p, g.b, g.len, key, piece_ok);
           for (int32_t t = 0; t < g.tiles; ++t, key += kTile) {
@@ -248,8 +301,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive_expect_tx(&ctrl->k_full[s], pieces * p.piece_rows * 128);
             ++ring.n;
           }
-          if (!ok) break;
+          rest -= g.tiles;
+          if (!ok || rest == 0) break;
         }
+        if (!ok) break;
         if (walk) w.next(p);
       }
       if (ok) {
@@ -514,8 +569,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&ctrl->p_ready[c & 1]);
           }
           if (!ok) break;
-          const float l_row = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
+          float l_row = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
           if (hc == 0) {
+            if ((flags & kAgain) && r < rows) {
+              const float2 both = merge_sums(p, *g, map, r, filled & 1, m_run, l_row);
+              m_run = both.x;
+              l_row = both.y;
+            }
             // (The row's last sum but one has been read: the first product behind it awaited that.)
             ctrl->inv[filled & 1][r] = 1.f / l_row;
             if (!(flags & kDirect) && r < rows) {
@@ -572,6 +632,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (named_barrier_or(1, kFinish, !ok || *abort_flag != 0)) break;
           tc_fence_after_sync();
           coef *= ctrl->bad[ring] ? NAN : ctrl->inv[filled & 1][r];
+          if (flags & kAgain) {
+            if (live) merge_rows(p, *g, map, r, key0, filled & 1, t_o);
+            // (The CTAs of a pair meet at each piece at least: neither falls behind by more.)
+            if (named_barrier_or(1, kFinish, !exchange_pair(ctrl, peer_bar, handed++))) break;
+          }
           ++filled;
           if (!(flags & kDirect)) {
             // A part: O column by column.
@@ -734,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 size_t ragged_swap_bytes(int shares) {
-  return size_t{2} * shares * 2 * 128 * kTile * sizeof(float);
+  return size_t{2} * shares * 2 * (128 + 2) * kTile * sizeof(float);  // with factors_at
 }
 
 diffattn_status launch_ragged_main_d128(const RaggedParams &p, const CUtensorMap (&maps)[5],

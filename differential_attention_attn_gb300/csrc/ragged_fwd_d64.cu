@@ -70,6 +70,32 @@ static_assert(kSmem <= 232448, "shared memory");
 __host__ __device__ constexpr uint32_t tm_s(int k) { return 128u * k; }
 __host__ __device__ constexpr uint32_t tm_o(int k) { return 256u + 128u * k; }
 
+// A piece's O (of one map, in tensor memory), reference and sum with those of the pieces before, which
+// are in the part.  (Each thread reads what it has written itself, but for the reference and the sum,
+// which a lane of its warp has.)
+__device__ __noinline__ float2 merge_piece(const float *part, int key0, uint32_t t_o, bool mine,
+                                           float m, float l) {
+  tc_fence_after_sync();
+  Merge x = {m, l, 0.f, 1.f};
+  if (mine) x = merge_states(part[DV * kTile], part[(DV + 1) * kTile], m, l);
+#pragma unroll 1
+  for (int c0 = 0; c0 < DV / 2; c0 += 32) {
+    uint32_t o[32];
+    tmem_ld16_x32(t_o + c0, o);
+    if (mine) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        o[i] = __float_as_uint(__uint_as_float(o[i]) * x.now +
+                               part[(key0 + c0 + i) * kTile] * x.before);
+    }
+    __syncwarp();
+    tmem_st16_x32(t_o + c0, o);
+  }
+  tmem_st_wait();
+  tc_fence_before_sync();
+  return make_float2(x.m, x.l);
+}
+
 template <bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1)
     diffragged_fwd_d64_kernel(const __grid_constant__ CUtensorMap tm_q1,
@@ -177,14 +203,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (bool left = ends_one; ok;) {
         const bool walk = w.more(p);
         if (!walk && !left) break;
-        const Segment g = walk ? w.segment(p, share) : end_of_one;
+        const Segment all = walk ? w.segment(p, share) : end_of_one;
         if (!walk) left = false;
-        if (g.tile0 == 0 && !(g.flags & kDirect)) join = w.join(line, share, g);
-        const int r = n % kSegRing;
-        publish(g);
-        if (!ok) break;
-        if ((g.flags & kBadLen) && lane == 0) report_bad_page(p.status);
-        if (!(g.flags & kEmpty)) {
+        if (all.tile0 == 0 && !(all.flags & kDirect)) join = w.join(line, share, all);
+        if ((all.flags & kBadLen) && lane == 0) report_bad_page(p.status);
+        int32_t rest = all.tiles;
+        while (true) {
+          const Segment g = piece_of(walk ? w.segment(p, share) : end_of_one, rest);
+          const int r = n % kSegRing;
+          publish(g);
+          if (!ok || (g.flags & kEmpty)) break;
           int32_t key = g.tile0 * kTile + row0;
           int32_t id = page_of(p, g.b, g.len, key, piece_ok);
           for (int32_t t = 0; t < g.tiles; ++t, key += kTile) {
@@ -209,8 +237,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_arrive_expect_tx(&ctrl->k_full[s], pieces * p.piece_rows * kRowBytes);
             ++ring.n;
           }
-          if (!ok) break;
+          rest -= g.tiles;
+          if (!ok || rest == 0) break;
         }
+        if (!ok) break;
         if (walk) w.next(p);
       }
       if (ok) {
@@ -490,7 +520,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&ctrl->p_ready[k]);
         }
         if (ok) ok = mbar_wait_warp(&ctrl->o_done, filled & 1, abort_flag, kWaitNs);
-        const float l_row = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
+        float l_row = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
+        if ((flags & kAgain) && ok && live) {
+          const float2 both = merge_piece(p.part + (g->slot * 2ll + k) * part_floats(DV) + r, key0, t_o,
+                                          r < rows, m_run, l_row);
+          m_run = both.x;
+          l_row = both.y;
+        }
         const float inv = 1.f / l_row;
         // (Every thread has read the last segment's exchange: its P of this one came behind it.)
         if (hc == 0) xch[k * kTile + r] = inv;

@@ -1,4 +1,5 @@
 """The packed-batch operators on the GPU against float64 references."""
+import math
 import random
 
 import pytest
@@ -386,6 +387,116 @@ def test_many_sequences():
     new = [min(n, rng.choice([0, 1, 1, 5])) for n in lens]
     c = R.Cache(16, lens=lens, kv=1, d=64, page=16)
     _parity(c, 1, new)
+
+
+class _Shared(R.Cache):
+    """Sequences far longer than the pool: pages that are only read may stand in a table many times."""
+
+    def __init__(self, seed, pages, page, d, dtype, tables, lens, scales=None):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        k = [torch.randn(pages, 1, page, d, generator=g, device="cuda") for _ in range(2)]
+        if scales is not None:
+            k = [x * torch.tensor(scales, device="cuda")[:, None, None, None] for x in k]
+        self.k1, self.k2 = (x.to(dtype) for x in k)
+        self.v = (torch.randn(pages, 1, page, 2 * d, generator=g, device="cuda") + 1).to(BF16)
+        self.table, self.lens, self.kv_len = tables.to(torch.int32).cuda(), list(lens), _int(lens)
+        self.B, self.kv, self.d, self.page, self.dtype = len(lens), 1, d, page, dtype
+
+    def ops_cache(self):
+        return ops.PagedCache(self.k1, self.k2, self.v, self.table, self.kv_len)
+
+
+def _sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def _alike_rows(B, n, page, d, dtype):
+    """B rows of n keys each, all of whose weights and values are alike, so that what sums drop adds
+    up.
+
+    With every page as often in the table, each map is the softmax over the pool.  Beside a row's
+    E = 2^-8 of every p |v| (P as bf16) and of |out| (its own rounding), a product with V drops at
+    most two steps of O, 2 * 2^-23, per 16 keys of a piece of 2^17 keys, a sum one in each of its
+    2^17 / 128 tiles, and joining the pieces and parts of both rounds twice each, 2^-24."""
+    pages, H, pieces = 8, 2, n // 2 ** 17 + 6
+    table = torch.arange(n // page).remainder(pages).expand(B, -1).contiguous()
+    c = _Shared(51, pages, page, d, dtype, table, [n] * B)
+    q1, q2, _, _ = _queries(52, B, H, d, dtype, 0.7)
+    lam, word = torch.tensor([0.1, 0.4], device="cuda"), _int([0])
+    out = ops.ragged_fwd(c.ops_cache(), q1, q2, lam, _int(range(B + 1)), headnorm=0, status=word)
+    torch.cuda.synchronize()
+    assert int(word) == 0
+    v, o, tol = R.f64(c.v).reshape(-1, 2 * d), 0.0, 0.0
+    for q, k, w in ((q1, c.k1, torch.ones_like(lam)), (q2, c.k2, -lam)):
+        q, k = R.f64(q), R.f64(k).reshape(-1, d)
+        x = q @ k.T / math.sqrt(d)
+        p = torch.softmax(x, -1)
+        dx = (q.abs() @ k.abs().T).amax(-1) / math.sqrt(d) * 1.4427 * (d / 16 + 2) * 2.0 ** -22
+        rel = 2 * (math.log(2) * dx + 2.0 ** -21) + 2 * (2 ** 13 + 2 ** 10 + pieces) * 2.0 ** -23 + 2.0 ** -8
+        o = o + w.double()[:, None] * (p @ v)
+        tol = tol + w.double().abs()[:, None] * (p @ v.abs()) * rel[..., None]
+    R.check(out, o, tol * 1.01 + o.abs() * 2.0 ** -8, "out")
+
+
+@pytest.mark.parametrize("d,dtype", KINDS)
+@pytest.mark.parametrize("fewer", [0, 2])
+def test_rows_of_millions_of_keys(d, dtype, fewer):
+    """As many rows as SMs (each item whole) or a few less (all cut)."""
+    _alike_rows(_sms() - fewer, 2 ** 23, 4096, d, dtype)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_items_that_take_longer_than_a_wait(d):
+    """Some 2.6 million key tiles in each item, about three seconds: every wait is for a piece."""
+    _alike_rows(_sms() if d == 64 else _sms() // 2, 5 * 2 ** 26, 65536, d, BF16)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("alike", [True, False])
+@pytest.mark.parametrize("headnorm", [0, 2])
+def test_long_ranges_in_pieces(d, alike, headnorm):
+    """Ranges of keys that are walked in three pieces: logits that climb, fall or stay from piece to
+    piece, a value that is not finite in the first piece or seen by the last token alone, whole
+    items (alike) and cut ones."""
+    page, pages, H, kinds = 2048, 40, 2, 5
+    n = 2 * 2 ** 17 + 3 * page + 777
+    lens = [n - (0 if alike else 64 * b) for b in range(kinds)]
+    rng, cols = random.Random(53), -(-n // page)
+    ids = [[rng.randrange(3, pages - 1) for _ in range(cols)] for _ in range(kinds)]
+    ids[0].sort()
+    ids[1].sort(reverse=True)
+    ids[3][7] = 0    # NaN in a column that all rows see, in the first piece
+    ids[4][-1] = 1   # an infinite value at the last token's row
+    scales = [1.0] * 3 + [0.3 + 0.05 * i for i in range(pages - 4)] + [1.0]
+    few = _Shared(54, pages, page, d, BF16, torch.tensor(ids), lens, scales)
+    few.v[0, 0, 100, 9] = float("nan")
+    few.v[1, 0, (lens[4] - 1) % page, 2 * d - 1] = INF
+    B = _sms() + (0 if alike else 3)
+    kind = [b % kinds for b in range(B)]
+    c = _Shared(54, pages, page, d, BF16, torch.tensor([ids[k] for k in kind]),
+                [lens[k] for k in kind], scales)
+    c.v = few.v
+    new = 3
+    q1, q2, lam, w = _queries(55, new * kinds, H, d, BF16)
+    lam = lam * 0.5
+    rows = torch.tensor([new * k + i for k in kind for i in range(new)], device="cuda")
+    word = _int([0])
+    out = ops.ragged_fwd(c.ops_cache(), q1[rows], q2[rows], lam, _int(range(0, new * B + 1, new)),
+                         norm_w=w, lambda_init=LI, headnorm=headnorm, status=word)
+    torch.cuda.synchronize()
+    assert int(word) == 0
+    ref, tol = G.attend(few, list(range(0, new * kinds + 1, new)), q1, q2, lam, norm_w=w,
+                        lambda_init=LI, headnorm=headnorm)
+    R.check(out, ref[rows], tol[rows], "out")
+    # a page outside the pool in the first piece: all rows of its sequences are NaN, and no other's
+    c.table[::kinds, 3] = pages
+    bad = ops.ragged_fwd(c.ops_cache(), q1[rows], q2[rows], lam, _int(range(0, new * B + 1, new)),
+                         norm_w=w, lambda_init=LI, headnorm=headnorm, status=word)
+    torch.cuda.synchronize()
+    assert int(word) == ops.ERR_PAGE
+    hit = torch.tensor(kind, device="cuda").repeat_interleave(new) == 0
+    assert torch.isnan(bad[hit].float()).all()
+    R.check(bad[~hit], ref[rows][~hit], tol[rows][~hit], "others")
 
 
 @pytest.mark.parametrize("d", [64, 128])

@@ -59,6 +59,21 @@ def test_append_and_fwd(dbg, d, dtype, lens, new):
     _same(dbg, run)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_ranges_in_pieces(dbg, d):
+    """Two pieces of 2^17 keys or less in each item; the pool's pages many times in each table."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    B, page, n = torch.cuda.get_device_properties(0).multi_processor_count + 1, 1024, 2 ** 17 + 300
+    pools = [torch.randn(9, 1, page, w, generator=g, device="cuda").to(BF16) for w in (d, d, 2 * d)]
+    table = torch.randint(0, 9, (B, -(-n // page)), generator=g, device="cuda", dtype=torch.int32)
+    lens = n - torch.arange(B, dtype=torch.int32, device="cuda") % 250
+    cache = ops.PagedCache(*pools, table, lens)
+    q = [torch.randn(2 * B, 1, d, generator=g, device="cuda").to(BF16) for _ in range(2)]
+    q_start = torch.arange(0, 2 * B + 1, 2, dtype=torch.int32, device="cuda")
+    lam = torch.full((1,), 0.5, device="cuda")
+    _same(dbg, lambda word: [ops.ragged_fwd(cache, *q, lam, q_start, lambda_init=0.3, status=word)])
+
+
 @pytest.mark.parametrize("B,n", [(3, 40), (300, 30)])
 def test_step(dbg, B, n):
     def run(word):
