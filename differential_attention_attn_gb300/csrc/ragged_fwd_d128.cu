@@ -505,8 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (t == 0) {
                 tile_sum = softmax_half_first(t_s, key0, sl2, lim, masked, m_run, pk);
               } else {
-                tile_sum = masked ? softmax_half_exp<true>(t_s, key0, m_run, sl2, lim, pk)
-                                  : softmax_half_exp<false>(t_s, key0, m_run, sl2, lim, pk);
+                tile_sum = masked ? softmax_half_exp<true, true>(t_s, key0, m_run, sl2, lim, pk)
+                                  : softmax_half_exp<false, true>(t_s, key0, m_run, sl2, lim, pk);
                 // (Rows past the segment's last hold whatever lies there, and have no say.)
                 if (__any_sync(0xffffffffu, !(tile_sum <= CERT_SUM) && r < rows)) {
                   float mt = masked ? softmax_half_max<true>(t_s, key0, lim)
@@ -541,8 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
                   l_run *= alpha;
                   const float m_use = m_run == -INFINITY ? 0.f : m_run;
-                  tile_sum = masked ? softmax_half_exp<true>(t_s, key0, m_use, sl2, lim, pk)
-                                    : softmax_half_exp<false>(t_s, key0, m_use, sl2, lim, pk);
+                  tile_sum = masked ? softmax_half_exp<true, true>(t_s, key0, m_use, sl2, lim, pk)
+                                    : softmax_half_exp<false, true>(t_s, key0, m_use, sl2, lim, pk);
                 }
               }
               l_run += tile_sum;

@@ -83,8 +83,9 @@ __device__ __forceinline__ void softmax_chunk_exp(const uint32_t (&x)[32], int k
 
 // Exponentials of this thread's 64 keys of an S row (keys key0 .. key0 + 63,
 // read through the two-threads-per-lane shape) against reference maximum m.
-// Returns the half row's sum of the (unrounded) exponentials.
-template <bool kMasked>
+// Returns the half row's sum of the unrounded exponentials or, kRounded, of
+// the rounded ones.
+template <bool kMasked, bool kRounded = false>
 __device__ __forceinline__ float softmax_half_exp(uint32_t t_s, int key0, float m, float sl2,
                                                   int lim, uint32_t (&pk)[kTileColumns / 4]) {
   float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
@@ -94,8 +95,8 @@ __device__ __forceinline__ float softmax_half_exp(uint32_t t_s, int key0, float 
   tmem_ld16_x32_nowait(t_s + 32, b);
   tmem_ld_wait_x32(a);
   tmem_ld_wait_x32(b);
-  softmax_chunk_exp<kMasked>(a, key0, 0, m, sl2, lim, acc, pk);
-  softmax_chunk_exp<kMasked>(b, key0 + 32, 16, m, sl2, lim, acc, pk);
+  softmax_chunk_exp<kMasked, kRounded>(a, key0, 0, m, sl2, lim, acc, pk);
+  softmax_chunk_exp<kMasked, kRounded>(b, key0 + 32, 16, m, sl2, lim, acc, pk);
   const float2 s01 = __fadd2_rn(acc[0], acc[1]), s23 = __fadd2_rn(acc[2], acc[3]);
   return (s01.x + s01.y) + (s23.x + s23.y);
 }
@@ -131,9 +132,11 @@ __device__ __forceinline__ float softmax_half_max(uint32_t t_s, int key0, int li
 // Sets m (-infinity where no key is visible or all logits are) and returns the half row's sum, which
 // is of the rounded exponentials: weights that the products take then add up to one, so that a row of
 // one key gets the value itself and a row of few (the first of a prompt, where both maps nearly
-// cancel) keeps the precision of fp32 statistics.  Over many keys the roundings average out, and the
-// later tiles add the unrounded ones, two at once (all tiles rounded: 2048 tokens behind 32768 keys
-// 1215 us for 1157).
+// cancel) keeps the precision of fp32 statistics.  The d = 128 forward adds the rounded ones in all
+// tiles (it costs up to 1 %), so that rows whose maps both lean on one key keep it wherever the key is.
+// At d = 64 later tiles add the unrounded ones, two at once: over many keys the roundings average out,
+// and all tiles rounded took 1215 to 1238 us for 1146 to 1157 (2048 tokens behind 32768 keys), 259 for
+// 247 (a mixed batch); only tiles that hold much of a row's sum, by a vote, 1211 and 272.
 __device__ __forceinline__ float softmax_half_first(uint32_t t_s, int key0, float sl2, int lim,
                                                     bool masked, float &m,
                                                     uint32_t (&pk)[kTileColumns / 4]) {

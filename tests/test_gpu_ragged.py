@@ -576,6 +576,34 @@ def test_a_row_of_one_key_gets_its_value(d, dtype):
         R.check(out[starts[b]], y, tol, f"sequence {b}")
 
 
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("n", [90, 1000, 5000])
+def test_rows_that_lean_on_one_key_at_d_128(dtype, n):
+    """Both maps have nearly all weight on one key, anywhere, and lambda is near one: the weights that
+    the values are multiplied with add up to one, so their roundings cancel as the maps do.
+
+    With weights w_j (1 + e_j) over their sum, |e_j| <= E = 2^-8, a map's output changes by
+    sum_j w_j (e_j - sum_i w_i e_i) v_j to first order, and |e_j - sum_i w_i e_i| =
+    |sum_i w_i (e_j - e_i)| <= 2 E (1 - w_j).  The rest as in ragged_ref.attend."""
+    d, T = 128, 24
+    c = R.Cache(61, lens=[n], kv=1, d=d, page=16, dtype=dtype)
+    q1, q2, lam, _ = _queries(62, T, 1, d, dtype)
+    lam = torch.full((1,), 0.95, device="cuda")
+    at = torch.linspace(0, n - 1, T).round().long().cuda()
+    q1[:, 0], q2[:, 0] = (R.f64(c.rows(t, 0))[0][at].mul(1.2).to(dtype) for t in ("k1", "k2"))
+    out = ops.ragged_fwd(c.ops_cache(), q1, q2, lam, _int([0, T]), headnorm=0, causal=False)
+    v, o, tol = R.f64(c.rows("v", 0))[0], 0.0, 0.0
+    for q, t, x in ((q1, "k1", 1.0), (q2, "k2", -0.95)):
+        q, k = R.f64(q)[:, 0], R.f64(c.rows(t, 0))[0]
+        w = torch.softmax(q @ k.T / math.sqrt(d), -1)
+        assert float(w.gather(1, at[:, None]).min()) > 0.9
+        dx = (q.abs() @ k.abs().T).amax(-1, keepdim=True) / math.sqrt(d) * 1.4427 * (d / 16 + 2) * 2.0 ** -22
+        rel = 2 * (math.log(2) * dx + 2.0 ** -21) + 2 * (n / 16 + 8) * 2.0 ** -23
+        o = o + x * (w @ v)
+        tol = tol + abs(x) * ((w * (1 - w)) @ v.abs() * 2 * 2.0 ** -8 + (w @ v.abs()) * rel)
+    R.check(out[:, 0], o, tol * 1.02 + o.abs() * 2.0 ** -8, "out")
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_strided_queries_and_output(d):
     c = R.Cache(20, lens=[500, 90], kv=2, d=d, page=32)  # NaN behind the sequences
