@@ -1,5 +1,6 @@
 // diffragged_fwd: what its two kernels (d = 64 and d = 128) have in common: how
-// the work is cut, how a share of it is walked, and the load warps.
+// the work is cut, how a share of it is walked, the launch, and how a tile's values
+// are cleared of what not all rows see.
 //
 // The mathematics.  Rows are r = (token, query head of the group) of one
 // key/value head, 128 to a tile, so that a tile's rows share every key and value
@@ -661,11 +662,10 @@ __device__ __noinline__ bool open_columns(int32_t *state, uint32_t *columns, int
   return true;
 }
 
-// The load warps, one for the keys (with the walk along the share and the segments' descriptions)
-// and one for the values.  A tile in pages of 16 rows is 16 copies for each of them, a lane each.
-// Copies of a tile land in kBoxes boxes of kTile rows; box k of piece i at k * box bytes + its rows.
-
-// This lane's page of tile t of sequence b: lane = piece * kBoxes + box.
+// The page of the piece of a tile that begins at `key` of sequence b.  (Each kernel has a warp that
+// loads keys, walks along the share and describes its segments, and one that loads values.  A tile is
+// pieces of piece_rows rows, each in one page, in boxes 128 bytes wide, a copy and a lane each: lane =
+// piece * boxes + box.)
 __device__ __forceinline__ int32_t page_of(const RaggedParams &p, int32_t b, int32_t len, int32_t key,
                                            bool piece_ok) {
   return piece_ok && key < len

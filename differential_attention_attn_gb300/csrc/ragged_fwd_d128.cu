@@ -18,9 +18,9 @@
 // softmax warps are at the next item.
 //
 // Bound: the tensor cores (busy 64 % of a call with seven items to a pair) and the
-// items' ends.  2048 tokens behind 16384, 16 heads over 4: 452 us, 1140 TFLOP/s of
-// the 8 d flop a pair, 1710 of the 12 d executed.  e4m3 keys, six sequences
-// of 2000 to 5003 of them with 513 to 1025 new tokens: 231 us.
+// items' ends.  2048 tokens behind 16384, 16 heads over 4: 430 to 446 us, 1155 to
+// 1199 TFLOP/s of the 8 d flop a pair, 1730 to 1800 of the 12 d executed.  e4m3
+// keys, six sequences of 2000 to 5003 of them with 513 to 1025 new tokens: 237 us.
 //
 // Tensor memory: S / P at 0 and 128 in turn, O at 256; shared memory: Q 32 KB, two
 // tiles of K (32 KB each) and two of V (64 KB each).
@@ -259,9 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n;
       };
       // The end of an item that another share begins comes last where its head has other tiles of
-      // rows: their shares then begin at its first keys together, and read them from L2.  (d = 64,
-      // 2048 tokens behind 32768: 1194 -> 1151 us; eight times 256 tokens 1085 -> 995 us; a single
-      // token has no one to share with: 61 -> 63 us.)
+      // rows: their shares then begin at its first keys together, and read them from L2.  (Measured
+      // at d = 64, see ragged_fwd_d64.cu; here it only keeps the two alike.)
       const bool ends_one = w.more(p) && w.cut && w.tile > 0 && w.s.tiles > 1;
       Segment end_of_one;
       if (ends_one) {

@@ -19,8 +19,9 @@
 // Bound: from a few dozen rows on, the two softmaxes in turn with the products (a
 // tile 1.4 us; its products alone 0.75 us, its exponentials 0.5 us); the tensor
 // pipe is busy 59 % of the time, the issue slots 47 %.  2048 tokens behind 32768,
-// 32 heads over 8: 1151 us, 926 TFLOP/s of the 8 d flop a pair, 1390 of the 12 d
-// executed.  A single token a sequence is bound by the keys' and values' bytes, a
+// 32 heads over 8: 1146 to 1158 us, 920 to 930 TFLOP/s of the 8 d flop a pair, 1380 to
+// 1395 of the 12 d executed (called on end, 1218 us: the GPU then runs at its power
+// limit).  A single token a sequence is bound by the keys' and values' bytes, a
 // start of 6 us and the join.  A CTA for each map (as at d = 128) took 1272 us, with
 // the next tile's logits read ahead into registers 1460; steps of 64 keys, whose
 // logits are made while the other half's softmax runs, 1268 (the fixed part of a
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             dbg_ok(g->row >= 0 && g->row + g->tokens <= p.N, p.status, 102);
             mbar_arrive_expect_tx(&ctrl->q_full, 2 * p.tokens * p.group * kRowBytes);
             tma_load_3d(smem + kQ, &tm_q1, &ctrl->q_full, 0, g->hk * p.group, g->row);
-              tma_load_3d(smem + kQ + kBox, &tm_q2, &ctrl->q_full, 0, g->hk * p.group, g->row);
+            tma_load_3d(smem + kQ + kBox, &tm_q2, &ctrl->q_full, 0, g->hk * p.group, g->row);
           }
           ++filled;
         }

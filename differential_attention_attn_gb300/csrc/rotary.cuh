@@ -32,8 +32,8 @@ struct Turn {
 // instructions, within half a turn of zero off by at most 2^-21.41 and 2^-21.19; eight pairs by
 // sincospif take as long as the memory of four heads' units (221 MB of packed rows 35.3 us, so
 // 34.8).  Not where fp32 or e4m3 is written: e4m3's wide steps show the last bits of a value next to
-// the border between two (of 12.7 million, 27 to 33 fell to the wrong side, so 3 to 11; 120 MB
-// 22.6 us, so 23.8).
+// the border between two (of 12.7 million, 27 to 33 fell to the wrong side, so 3 to 6, as with sines
+// worked out in 64 bits and rounded once; 120 MB 22.6 us, so 23.9).
 template <bool kShort>
 __device__ __forceinline__ Turn make_turn(const uint64_t *freq, int u, int64_t pos, float scale) {
   Turn t;

@@ -1115,8 +1115,9 @@ def ragged_step(book, new_len, *, q_start, positions=None, slots=None, status=No
 
     new_len: int32 [B], the sequences' new tokens (-1: it has ended).  Written: q_start int32
     [B + 1]; positions int32 [T] and slots int64 [T] of the packed rows (either may be None), -1
-    behind the last token; and the book's tensors.  A step that does not fit changes none of these,
-    gives all-zero q_start and stores ERR_PAGE in `status` (int32 [1]).
+    behind the last token; and the book's tensors.  A step that does not fit changes none of the
+    book's, gives all-zero q_start, -1 in all rows, and stores ERR_PAGE in `status` (int32 [1]).
+    Positions are places in the cache: after paged_evict lower than those in the text.
     """
     index, T = book.index, 0
     if positions is not None:
@@ -1167,7 +1168,9 @@ def ragged_append(cache, k1, k2, v, slots, *, rotary=None, positions=None, q=Non
     k1, k2: bf16 [T, kv_heads, d], v: bf16 [T, kv_heads, 2d], slots: int64 [T] as ragged_step gives
     them (-1: the token is left out).  q: (q1, q2), bf16 [T, H, d], or None; q_out: two tensors of
     that shape and the cache's key dtype (new ones when None; bf16 ones may be the inputs).
-    Views of any layout with contiguous rows.  Returns q_out.
+    Views of any layout with contiguous rows.  Returns q_out.  (As in ragged_fwd, what a call's
+    shapes come to is kept under them: buffers of one T, padded with slots of -1, save the 10 to
+    20 us of host time that a new T takes.)
     """
     index, bf16 = cache.index, torch.bfloat16
     ts = [k1, k2, v]
@@ -1252,6 +1255,7 @@ def ragged_fwd(cache, q1, q2, lam, q_start, *, causal: bool = True, headnorm: in
     lam: float32 [H]; norm_w: float32 [H, 2d] (16-byte aligned) or None.  Views of any layout with
     contiguous rows (`out` too).  workspace: a CUDA tensor of at least ragged_fwd_plan bytes (a
     torch buffer when None).  Returns bf16 out [T, H, 2d]; rows of no sequence are not written.
+    Weights are rounded once more than in paged_fwd: see Precision in include/diffattn_ragged.h.
     """
     index, dtype, f32 = cache.index, cache.dtype, torch.float32
     shape = q1.shape

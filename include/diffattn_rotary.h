@@ -12,8 +12,10 @@
  * and the other channels are copied.  Its gradient is the turn by -p f_i.
  *
  * Frequencies are kept in turns per position as 64-bit fractions: p f_i is then
- * an integer product that wraps as angles do, exact for every 64-bit position,
- * so that far positions come out as precisely as near ones.
+ * an integer product that wraps as angles do, without rounding for any 64-bit
+ * position.  What a far position adds is the error of the fraction itself, below
+ * 2^-55 of a turn as diffrotary_frequencies works it out in fp64: the angle is off
+ * by |p| 2^-55 of a turn, 2^-24 at p = 2^31.
  */
 #ifndef DIFFATTN_ROTARY_H
 #define DIFFATTN_ROTARY_H
