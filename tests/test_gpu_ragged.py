@@ -499,6 +499,28 @@ def test_long_ranges_in_pieces(d, alike, headnorm):
     R.check(bad[~hit], ref[rows][~hit], tol[rows][~hit], "others")
 
 
+@pytest.mark.parametrize("d,causal", [(64, True), (64, False), (128, True), (128, False)])
+def test_long_ranges_of_several_row_tiles(d, causal):
+    """Heads with two tiles of rows, so that a share walks the end of an item that another one begins
+    last, after whole and cut items of its own: all of them in pieces."""
+    page, pages, H, kinds, new = 2048, 20, 32, 2, 5
+    lens = [2 ** 17 + 999, 2 ** 18 + 5000]
+    rng, cols = random.Random(56), -(-lens[1] // page)
+    few = _Shared(57, pages, page, d, BF16,
+                  torch.tensor([[rng.randrange(pages) for _ in range(cols)] for _ in range(kinds)]),
+                  lens)
+    B = _sms() + 11
+    kind = [rng.randrange(kinds) for _ in range(B)]
+    c = _Shared(57, pages, page, d, BF16, few.table[kind], [lens[k] for k in kind])
+    q1, q2, lam, w = _queries(58, new * kinds, H, d, BF16)
+    lam = lam * 0.5
+    rows = torch.tensor([new * k + i for k in kind for i in range(new)], device="cuda")
+    out = ops.ragged_fwd(c.ops_cache(), q1[rows], q2[rows], lam, _int(range(0, new * B + 1, new)),
+                         norm_w=w, lambda_init=LI, causal=causal)
+    ref, tol = G.attend(few, [0, new, 2 * new], q1, q2, lam, norm_w=w, lambda_init=LI, causal=causal)
+    R.check(out, ref[rows], tol[rows], "out")
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_large_and_climbing_logits(d):
     c = R.Cache(17, lens=[1900, 130], kv=2, d=d, page=16, fill=0.0)
